@@ -306,6 +306,166 @@ uzip_status uzip_decompress_batched_timed(uzip_dtype dtype, size_t num_buffers, 
                                           size_t workspace_bytes, hipStream_t stream, hipEvent_t main_start,
                                           hipEvent_t main_stop);
 
+/* ---- products with packed weights ---------------------------------------------
+ * Weights that arrived compressed can stay small in device memory and be
+ * multiplied from there.  A frame (above) is the form for the wire: its rANS
+ * chunks decode one after another at about 1.9 TB/s.  A packed weight is the
+ * resident form: the same split of each bf16 value into its exponent and its
+ * sign+mantissa byte, the exponent as a 4-bit code within the window of a
+ * 16 x 64 tile, so that a product can decode it while it reads it, at the
+ * speed of memory.  Near-Gaussian weights take about 12.1 bits a value; any
+ * bit pattern comes back as it was (values outside a tile's window are listed
+ * beside it, and a tile with more than 64 of them keeps its exponents as
+ * bytes, at most 24.1 bits a value).  Only bf16 weights are packed.
+ *
+ * A stack holds `matrices` matrices of `rows` x `cols`.  gated: each matrix is
+ * two of rows/2 rows, the gate's and then the up projection's, for
+ * UZIP_ACT_SWIGLU; without it that activation is refused, and with it every
+ * other one.
+ *
+ * All calls share the conventions above: argument errors return at once with
+ * nothing launched; workspaces and outputs are the caller's; nothing is
+ * allocated or synchronised, and a call keeps nothing between calls, so that
+ * calls may be captured into graphs and run side by side as long as each has
+ * its own workspace and outputs.  Sums are taken in fp32 in a fixed order: the
+ * same call gives the same bits.  Rows of a bf16 or fp32 matrix may be any
+ * stride apart (in values, at least the row's length); unaligned or odd ones
+ * cost a copy.  At most 2^31 - 1 rows, columns or tokens, 65,535 matrices and
+ * 2^25 tiles a stack.  No argument may overlap an output.
+ * UZIP_ERR_CAPACITY: packed capacity below uzip_weight_max_size. */
+typedef struct {
+    const void *data;   /* device, 16-byte aligned, as uzip_weight_pack wrote it */
+    size_t bytes;       /* bytes readable there: the packed size, or more */
+    size_t matrices;
+    size_t rows;
+    size_t cols;
+    uint32_t gated;     /* 0 or 1 */
+    uint32_t reserved;  /* 0 */
+} uzip_weight;
+
+typedef enum {
+    UZIP_ACT_NONE = 0,
+    UZIP_ACT_RELU = 1,
+    UZIP_ACT_GELU = 2,      /* z Phi(z), with the error function */
+    UZIP_ACT_GELU_TANH = 3, /* its tanh form */
+    UZIP_ACT_SILU = 4,      /* z / (1 + exp(-z)) */
+    UZIP_ACT_SWIGLU = 5     /* silu(gate rows) * up rows: half as many outputs as rows */
+} uzip_act;
+
+/* Upper bound of the packed size (the exact size is data-dependent), and the
+ * workspace of uzip_weight_pack.  0 for invalid arguments.  Host functions. */
+size_t uzip_weight_max_size(size_t matrices, size_t rows, size_t cols, uint32_t gated);
+size_t uzip_weight_workspace_size(size_t matrices, size_t rows, size_t cols, uint32_t gated);
+
+/* Packs bf16 matrices (2-byte aligned; strides in values).  The packed size
+ * goes to the device word *d_out_size: bytes from there on are not needed. */
+uzip_status uzip_weight_pack(const void *d_in, size_t matrices, size_t rows, size_t cols, size_t row_stride,
+                             size_t matrix_stride, uint32_t gated, void *d_out, size_t out_capacity,
+                             uint64_t *d_out_size, void *d_workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The matrices back, bit for bit.  Needs no workspace. */
+uzip_status uzip_weight_unpack(const uzip_weight *weight, void *d_out, size_t row_stride, size_t matrix_stride,
+                               hipStream_t stream);
+
+/* y = act(x W^T + bias) + residual.  x: [tokens, cols] bf16.  bias: [rows]
+ * (grouped: [matrices, rows]) bf16 or fp32, or null.  residual: y's shape and
+ * type, or null.  y: [tokens, rows] (gated: rows/2) bf16 or fp32.  preact: if
+ * not null, receives x W^T + bias, [tokens, rows] bf16 or fp32, for the
+ * backward call (rounded to bf16 it takes half the memory, and adds an error
+ * of the size of dz's own rounding to the gradients).
+ * offsets (grouped only): matrices + 1 ascending int32 row numbers in device
+ * memory; matrix g takes rows offsets[g] .. offsets[g+1] - 1 of x, y and
+ * preact, and rows of no group are left as they were.  Offsets outside
+ * [0, tokens] are clamped, a descending pair is an empty group; overlapping
+ * groups are not supported. */
+typedef struct {
+    const void *x;
+    size_t x_stride;
+    size_t tokens;
+    const int32_t *offsets;
+    const void *bias;
+    const void *residual;
+    size_t residual_stride;
+    void *y;
+    size_t y_stride;
+    void *preact;
+    size_t preact_stride;
+    uint32_t bias_dtype; /* UZIP_BF16 or UZIP_FP32 */
+    uint32_t y_dtype;
+    uint32_t act;        /* uzip_act */
+    uint32_t preact_dtype;
+} uzip_linear_args;
+
+/* The workspace depends on sizes, strides, pointers' alignment and types only. */
+size_t uzip_linear_workspace_size(const uzip_weight *weight, const uzip_linear_args *args);
+uzip_status uzip_linear(const uzip_weight *weight, const uzip_linear_args *args, void *d_workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+/* The same for a stack of matrices and rows grouped by matrix; no residual. */
+uzip_status uzip_grouped_linear(const uzip_weight *weight, const uzip_linear_args *args, void *d_workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* The gradients: with dz = dy act'(preact), dx = dz W, dw = dz^T x and
+ * dbias = the sum of dz's rows (the residual's gradient is dy).  dz is rounded
+ * to bf16 for the two products; dbias is summed from the unrounded values.
+ * preact may be null for UZIP_ACT_NONE.  dx: [tokens, cols] bf16; dw:
+ * [matrices, rows, cols] bf16, contiguous; dbias: [matrices, rows]; each may
+ * be null.  x may be null without dw.  A group without rows has zero dw and
+ * dbias; dx rows of no group are left as they were.  One matrix without
+ * offsets, or a stack with them. */
+typedef struct {
+    const void *dy;      /* [tokens, rows] (gated: rows/2) */
+    size_t dy_stride;
+    const void *x;
+    size_t x_stride;
+    const void *preact;
+    size_t preact_stride;
+    size_t tokens;
+    const int32_t *offsets;
+    void *dx;
+    size_t dx_stride;
+    void *dw;
+    void *dbias;
+    uint32_t dy_dtype;   /* UZIP_BF16 or UZIP_FP32 */
+    uint32_t dbias_dtype;
+    uint32_t act;
+    uint32_t preact_dtype;
+} uzip_linear_backward_args;
+
+size_t uzip_linear_backward_workspace_size(const uzip_weight *weight, const uzip_linear_backward_args *args);
+uzip_status uzip_linear_backward(const uzip_weight *weight, const uzip_linear_backward_args *args, void *d_workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+uzip_status uzip_grouped_linear_backward(const uzip_weight *weight, const uzip_linear_backward_args *args,
+                                         void *d_workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Softmax cross entropy of the logits x W^T, which are never stored: a token's
+ * loss is lse - logit[target] with lse = log(sum(exp(logits))).  target:
+ * int64 [tokens]; a token whose target is ignore_index has loss 0 and no
+ * gradient; one whose target is neither that nor a row of W has loss NaN and
+ * no gradient.  loss and lse: fp32 [tokens].  One matrix, not gated. */
+typedef struct {
+    const void *x;
+    size_t x_stride;
+    size_t tokens;
+    const int64_t *target;
+    int64_t ignore_index;
+    float *loss;
+    float *lse;          /* output; the backward call's input */
+    const float *dloss;  /* backward: the losses' gradients, [tokens] */
+    void *dx;            /* backward: [tokens, cols] bf16, or null */
+    size_t dx_stride;
+    void *dw;            /* backward: [rows, cols] bf16, contiguous, or null */
+} uzip_loss_args;
+
+size_t uzip_linear_cross_entropy_workspace_size(const uzip_weight *weight, const uzip_loss_args *args);
+uzip_status uzip_linear_cross_entropy(const uzip_weight *weight, const uzip_loss_args *args, void *d_workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+/* dx = dlogits W and dw = dlogits^T x with dlogits = dloss (softmax - onehot),
+ * rounded to bf16 for the products.  Works through the vocabulary in pieces:
+ * a piece's dlogits are the only ones that exist at a time. */
+size_t uzip_linear_cross_entropy_backward_workspace_size(const uzip_weight *weight, const uzip_loss_args *args);
+uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const uzip_loss_args *args,
+                                               void *d_workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Static English name of a status code. */
 const char *uzip_status_string(uzip_status s);
 

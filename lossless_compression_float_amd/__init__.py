@@ -70,6 +70,20 @@ EXPORTED = (
     "uzip_compress_batched_timed",
     "uzip_decompress_batched_timed",
     "uzip_status_string",
+    "uzip_weight_max_size",
+    "uzip_weight_workspace_size",
+    "uzip_weight_pack",
+    "uzip_weight_unpack",
+    "uzip_linear_workspace_size",
+    "uzip_linear",
+    "uzip_grouped_linear",
+    "uzip_linear_backward_workspace_size",
+    "uzip_linear_backward",
+    "uzip_grouped_linear_backward",
+    "uzip_linear_cross_entropy_workspace_size",
+    "uzip_linear_cross_entropy",
+    "uzip_linear_cross_entropy_backward_workspace_size",
+    "uzip_linear_cross_entropy_backward",
 )
 
 _lib = None
@@ -435,3 +449,14 @@ def compress_batched_arbitrated(tensors, pol: uzip_policy, chunk_bytes: int = 0,
     _check(st, "uzip_compress_batched_arbitrated")
     _keep_for(stream, outs, out_sizes, plans, ws)
     return outs, out_sizes, plans
+
+
+# ---- products with packed weights ---------------------------------------------
+from .weights import (ACTIVATIONS, PackedWeight, grouped_linear, grouped_linear_backward, linear,  # noqa: E402
+                      linear_backward, linear_cross_entropy, linear_cross_entropy_backward, pack_weight, unpack_weight,
+                      uzip_grouped_linear, uzip_grouped_linear_backward, uzip_linear, uzip_linear_args,
+                      uzip_linear_backward, uzip_linear_backward_args, uzip_linear_backward_workspace_size,
+                      uzip_linear_cross_entropy, uzip_linear_cross_entropy_backward,
+                      uzip_linear_cross_entropy_backward_workspace_size, uzip_linear_cross_entropy_workspace_size,
+                      uzip_linear_workspace_size, uzip_loss_args, uzip_weight, uzip_weight_max_size, uzip_weight_pack,
+                      uzip_weight_unpack, uzip_weight_workspace_size)
