@@ -8,9 +8,11 @@
 // gives eight consecutive contraction values of row (first operand) or column
 // (second operand) c, and holds rows 4 q .. 4 q + 3 of column c of the fp32
 // result.  Which contraction index a (q, j) slot stands for is free as long as
-// both operands agree; here, in half h of a block of 64, it is 16 q + 8 h + j,
+// both operands agree; here, in half h of a block of 64, it is 32 h + 8 q + j,
 // the order of a packed tile.
 #include <stdint.h>
+
+#include <type_traits>
 
 #include <hip/hip_runtime.h>
 
@@ -38,12 +40,6 @@ __device__ inline float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ inline float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 __device__ inline float from_bf16(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
 
-// Waits for this wave's LDS operations and for the workgroup's other waves.
-// Loads from memory that are still on their way into registers stay so.
-__device__ inline void lds_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 // ---- packed tiles -----------------------------------------------------------
 
 struct Tile {
@@ -70,60 +66,73 @@ __device__ inline void tile_load(Tile &t, const WeightView &w, uint64_t tile, ui
     t.code = *reinterpret_cast<const uint2 *>(p + kTileSm + lane * 8);
     t.h = uniform(head.x);
     t.off = uniform(head.y);
-    t.ent = 0;
-    const uint32_t cnt = (t.h >> 8) & 0xFF;
-    if (cnt != 0 && cnt != kTileRaw) {
-        const uint32_t *list = reinterpret_cast<const uint32_t *>(w.extra + (uint64_t)t.off * 16);
-        if (lane < cnt) t.ent = list[lane];
-    }
+    // (the entry load has no branch: a tile without a list reads one of its own words)
+    const uint32_t cnt = t.h >> 8 & 0xFF, n = cnt == kTileRaw ? 0 : cnt;
+    const uint32_t *list = reinterpret_cast<const uint32_t *>(n ? w.extra + (uint64_t)t.off * 16 : p);
+    t.ent = list[lane < n ? lane : 0];
 }
 
 // Eight pairs of bf16 values from a lane's tile registers: five operations a
-// pair.  The byte of sign and mantissa is spread over a half word and masked,
-// the code shifted to the exponent's place and taken from the base.
-__device__ inline void tile_decode(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
+// pair, no branches.  The byte of sign and mantissa is spread over a half word
+// and masked, the code shifted to the exponent's place and taken from the base.
+__device__ inline uint32_t tile_signs(const Tile &t, int p) {
     const uint32_t sm[4] = {t.sm.x, t.sm.y, t.sm.z, t.sm.w};
-    const uint32_t cnt = (t.h >> 8) & 0xFF;
-    if (cnt == kTileRaw) {
+    return __builtin_amdgcn_perm(0, sm[p >> 1], p & 1 ? 0x03030202u : 0x01010000u) & 0x807F807Fu;
+}
+__device__ inline uint32_t tile_codes(const Tile &t, int p) {
+    const uint32_t c = p < 4 ? t.code.x : t.code.y;
+    const int k = p & 3;
+    return (k == 0 ? c << 7 : k == 1 ? c << 3 : k == 2 ? c >> 1 : c >> 5) & 0x07800780u;
+}
+__device__ inline void tile_decode_plain(const Tile &t, uint32_t v[8]) {
+    const uint32_t base = (t.h & 0xFF) * 0x00800080u;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) v[p] = tile_signs(t, p) | (base - tile_codes(t, p));
+}
+
+// The two kinds of tile for which that is not enough: exponent bytes, and
+// code 15 for exponent 0.
+__device__ inline bool tile_special(uint32_t h) { return (h & kTileZero) || (h >> 8 & 0xFF) == kTileRaw; }
+__device__ inline void tile_decode_special(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
+    if ((t.h >> 8 & 0xFF) == kTileRaw) {
         const uint4 ex = *reinterpret_cast<const uint4 *>(w.extra + (uint64_t)t.off * 16 + lane * 16);
         const uint32_t e[4] = {ex.x, ex.y, ex.z, ex.w};
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-            const uint32_t s = __builtin_amdgcn_perm(0, sm[p >> 1], p & 1 ? 0x03030202u : 0x01010000u) & 0x807F807Fu;
             const uint32_t x = e[p >> 1] >> (p & 1 ? 16 : 0);
-            v[p] = s | ((x & 0xFF) << 7) | ((x & 0xFF00) << 15);
+            v[p] = tile_signs(t, p) | ((x & 0xFF) << 7) | ((x & 0xFF00) << 15);
         }
         return;
     }
     const uint32_t base = (t.h & 0xFF) * 0x00800080u;
-    const bool zero = (t.h & kTileZero) != 0;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        const uint32_t c = p < 4 ? t.code.x : t.code.y;
-        const int k = p & 3;
-        uint32_t x = (k == 0 ? c << 7 : k == 1 ? c << 3 : k == 2 ? c >> 1 : c >> 5) & 0x07800780u;
-        const uint32_t s = __builtin_amdgcn_perm(0, sm[p >> 1], p & 1 ? 0x03030202u : 0x01010000u);
-        if (zero) {
-            const uint32_t z = (x + 0x00800080u) & 0x08000800u;  // bit 11 of the halves whose code is 15
-            const uint32_t m = (z << 4) - (z >> 4);              // 0x7F80 there
-            x = (base - (x & ~m)) & ~m;
-        } else {
-            x = base - x;
-        }
-        v[p] = (s & 0x807F807Fu) | x;
+        const uint32_t x = tile_codes(t, p);
+        const uint32_t z = (x + 0x00800080u) & 0x08000800u;  // bit 11 of the halves whose code is 15
+        const uint32_t m = (z << 4) - (z >> 4);              // 0x7F80 there
+        v[p] = tile_signs(t, p) | ((base - (x & ~m)) & ~m);
     }
-    if (cnt != 0) {
-        const uint32_t n = cnt < kMaxListed ? cnt : kMaxListed;
-        for (uint32_t i = 0; i < n; ++i) {
-            const uint32_t e = __builtin_amdgcn_readlane(t.ent, i);
-            const uint32_t at = (e >> 4) & 63, idx = e & 15;
-            const bool mine = lane == at;
-            const uint32_t val = e >> 16;
+}
+
+__device__ inline uint32_t tile_listed(uint32_t h) {
+    const uint32_t cnt = h >> 8 & 0xFF;
+    return cnt == kTileRaw ? 0 : min(cnt, kMaxListed);
+}
+
+// All of it, in registers.
+__device__ inline void tile_decode(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
+    tile_decode_plain(t, v);
+    if (!(t.h & (0xFF00u | kTileZero))) return;
+    if (tile_special(t.h)) tile_decode_special(t, w, lane, v);
+    const uint32_t n = tile_listed(t.h);
+    for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t e = __builtin_amdgcn_readlane(t.ent, i);
+        const uint32_t idx = e & 15, val = e >> 16;
+        const bool mine = lane == (e >> 4 & 63);
 #pragma unroll
-            for (int p = 0; p < 8; ++p)
-                if ((idx >> 1) == (uint32_t)p)
-                    v[p] = !mine ? v[p] : idx & 1 ? (v[p] & 0xFFFFu) | (val << 16) : (v[p] & 0xFFFF0000u) | val;
-        }
+        for (int p = 0; p < 8; ++p)
+            if ((idx >> 1) == (uint32_t)p)
+                v[p] = !mine ? v[p] : idx & 1 ? (v[p] & 0xFFFFu) | (val << 16) : (v[p] & 0xFFFF0000u) | val;
     }
 }
 
@@ -135,10 +144,13 @@ __device__ inline void tile_gather(const PackParams &p, uint64_t tile, uint32_t 
     const uint64_t kb = tile % p.l.col_blocks, t = tile / p.l.col_blocks;
     const uint64_t rb = t % p.l.row_blocks, e = t / p.l.row_blocks;
     const uint64_t part = rb / p.l.part_blocks, row = (rb % p.l.part_blocks) * kTileRows + r;
-    const uint64_t c0 = kb * kTileCols + q * 16;
+    const uint64_t c0 = kb * kTileCols + q * 8;
     const uint16_t *src = p.in + e * p.matrix_stride + (part * p.l.part_rows + row) * p.row_stride + c0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = row < p.l.part_rows && c0 + i < p.cols ? src[i] : (uint16_t)0;
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t c = (i >> 3) * 32 + (i & 7);
+        v[i] = row < p.l.part_rows && c0 + c < p.cols ? src[c] : (uint16_t)0;
+    }
 }
 
 // A wave packs a tile: the histogram of its exponents picks the window that
@@ -321,16 +333,18 @@ __global__ __launch_bounds__(256) void k_unpack(UnpackParams p) {
     const uint64_t rb = u % p.w.row_blocks, e = u / p.w.row_blocks;
     const uint64_t part = rb / p.w.part_blocks, row = (rb % p.w.part_blocks) * kTileRows + r;
     if (row >= p.w.part_rows) return;
-    const uint64_t c0 = kb * kTileCols + q * 16;
+    const uint64_t c0 = kb * kTileCols + q * 8;
     uint16_t *dst = p.out + e * p.matrix_stride + (part * p.w.part_rows + row) * p.row_stride + c0;
-    if (c0 + 16 <= p.cols && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+    if (c0 + 40 <= p.cols && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
         reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        reinterpret_cast<uint4 *>(dst)[4] = make_uint4(v[4], v[5], v[6], v[7]);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (c0 + i < p.cols) dst[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t c = (i >> 3) * 32 + (i & 7);
+        if (c0 + c < p.cols) dst[c] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    }
 }
 
 // Rows copied to a stride of whole 16-byte units, zeros behind the last column.
@@ -507,13 +521,13 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
         uint2 hd[RB];
         uint4 x[MT][2];
         auto load_x = [&](uint32_t kb) {
-            const uint32_t k = kb * kTileCols + q * 16;
+            const uint32_t k = kb * kTileCols + q * 8;
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     x[j][h] = make_uint4(0, 0, 0, 0);
-                    const uint32_t kk = k + h * 8;
+                    const uint32_t kk = k + h * 32;
                     if (p.x_vec) {
                         if (xv[j] && kk < p.cols) x[j][h] = *reinterpret_cast<const uint4 *>(xr[j] + kk);
                     } else if (xv[j]) {
@@ -594,40 +608,82 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
 // dx:            r = column of x, c = token,     a = weight row
 // dw:            r = column of x, c = weight row, a = token
 //
-// The operands of each block of 64 contraction values are staged in LDS, two
-// blocks deep: while one is multiplied, the next is decoded or copied from
-// registers, and the one after it is on its way from memory.
+// Four waves, each a quarter of the tile.  The contraction goes in stages of
+// 32 through a ring of four LDS stages.  In step s a wave multiplies the
+// fragments it read in the step before, reads those of stage s + 1, starts the
+// copies of stage s + 3 from memory to LDS and decodes its share of the weights
+// of the stages after next; one barrier ends the step.
 
 enum Operand { kPacked, kPackedT, kRows, kCols };
 
-// Place of 16-byte unit `unit` of row `row` in a [TC][64] operand (128-byte
-// rows): the xor spreads the 16 rows that a read touches over the banks.
-__device__ inline uint32_t rows_at(uint32_t row, uint32_t unit) { return row * 128 + ((unit ^ (row & 7)) * 16); }
+// Place of 16-byte unit `unit` of row `row` in a stage of [T][32] values (64
+// bytes a row): the xor makes 16 rows cover the 256 bytes of the banks.
+__device__ inline uint32_t rows_at(uint32_t row, uint32_t unit) { return row * 64 + ((unit ^ (row >> 2 & 3)) * 16); }
 
-// Place of the 32-byte granule `g` of contraction row `a` in a [64][T]
-// operand that is read transposed.  A transposing read takes four consecutive
-// rows a of two quads 16 rows apart: these eight get eight different granules
-// of the 256 bytes that the banks span.
+// Granule (32 bytes, 16 columns) `g` of contraction row `a` in a stage of
+// [32][T] values that is read transposed.  A transposing read takes four
+// consecutive rows of two quads eight rows apart: these eight get eight
+// different granules of the 256 bytes that the banks span.
+__device__ inline uint32_t cols_swizzle(uint32_t a) { return (a & 3) | (a >> 3 & 1) << 2; }
 template <int T>
 __device__ inline uint32_t cols_at(uint32_t a, uint32_t g) {
-    const uint32_t s = (a & 3) | ((a >> 2 ^ a >> 4) & 1) << 2;
-    return a * (T * 2) + ((g ^ s) * 32);
+    return a * (T * 2) + ((g ^ cols_swizzle(a)) * 32);
 }
 
-// Eight contraction values of column c0 + (lane & 15): a = 16 q + 8 h + j.
+// Eight contraction values 8 q + j of column c0 + (lane & 15).
 template <int T>
-__device__ inline bf16x8 cols_frag(const uint8_t *lds, uint32_t c0, uint32_t h, uint32_t lane) {
+__device__ inline bf16x8 cols_frag(const uint8_t *lds, uint32_t c0, uint32_t lane) {
     const uint32_t q = lane >> 4, l = lane & 15;
     s16x4 v[2];
 #pragma unroll
     for (uint32_t t = 0; t < 2; ++t) {
-        const uint32_t a = q * 16 + h * 8 + t * 4 + (l >> 2);
+        const uint32_t a = q * 8 + t * 4 + (l >> 2);
         const uint8_t *p = lds + cols_at<T>(a, c0 >> 4) + (l & 3) * 8;
         v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
     }
     typedef short s16x8 __attribute__((ext_vector_type(8)));
     const s16x8 x = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(bf16x8, x);
+}
+
+// A run of memory of which `bytes` may be read; reads behind them give zeros.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr uint32_t kRsrcWord3 = 0x00020000u;  // raw 32-bit buffer access on the gfx9 family
+__device__ inline rsrc_t buffer(const uint8_t *p, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t u = (uint64_t)uniform((uint32_t)(a >> 32)) << 32 | uniform((uint32_t)a);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), (short)0, (int)uniform(bytes), (int)kRsrcWord3);
+}
+// 16 bytes a lane from memory straight to LDS, at `dst` + 16 lane.  In asm, so
+// that the compiler does not wait for it before the next read of LDS: the
+// kernel's own waits and barriers say when the bytes are there.  It has no
+// result registers, and the asm statements around it keep their order.
+__device__ inline void copy_to_lds(rsrc_t r, uint32_t off, const uint8_t *dst) {
+    const uint32_t at = uniform((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r) : "m0");
+}
+
+template <int N>
+__device__ inline void wait_copies() {  // all but the last N memory operations of this wave, and its LDS operations
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+__device__ inline void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// acc += a b, in place in accumulation registers.  In asm, because with all
+// 256 of them taken the compiler's own choice of registers moves accumulators
+// to and fro in the loop (and then spills); the statements keep their order.
+// Between them and other instructions on the same registers there have to be
+// 18 cycles that the compiler does not know of: settle().
+__device__ inline void mfma(f32x4 &acc, bf16x8 a, bf16x8 b) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+template <int F>
+__device__ inline void settle(f32x4 (&acc)[F][F]) {
+#pragma unroll
+    for (int i = 0; i < F * F; ++i) asm volatile("" : "+a"(acc[i / F][i % F]));
+    asm volatile("s_nop 15\n\ts_nop 15");
+#pragma unroll
+    for (int i = 0; i < F * F; ++i) asm volatile("" : "+a"(acc[i / F][i % F]));
 }
 
 // Expert and first row of token tile `ct`, or false behind the last one.
@@ -664,26 +720,17 @@ __device__ inline bool find_group(const GemmParams &p, uint32_t ct, uint32_t edg
     return false;
 }
 
-template <Operand RK, int TR, int WAVES>
-struct RSide {  // the operand whose index is contiguous in the output
-    static constexpr int TILES = TR * 64 / 1024 / WAVES;  // packed tiles a wave decodes
-    static constexpr int UNITS = TR * 64 / 8 / (WAVES * 64);
-    Tile t[RK == kCols ? 1 : TILES];
-    uint2 hd[RK == kCols ? 1 : TILES];
-    bool live[RK == kCols ? 1 : TILES];
-    uint4 u[RK == kCols ? UNITS : 1];
-};
-
-template <Operand RK, Operand CK, GemmKind KIND, bool GATED, int TR, int TC, int WR, int WC>
-__global__ __launch_bounds__(WR *WC * 64) void k_gemm(GemmParams p) {
-    constexpr int WAVES = WR * WC, THREADS = WAVES * 64;
-    constexpr int FR = TR / WR / 16, FC = TC / WC / 16;
-    constexpr int RBYTES = TR * 128, CBYTES = TC * 128;
-    constexpr int CUNITS = TC * 8 / THREADS;
-    __shared__ __align__(16) uint8_t lds[2 * (RBYTES + CBYTES)];
+template <Operand RK, Operand CK, GemmKind KIND, bool GATED, int T>
+__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm(GemmParams p) {
+    constexpr int F = T / 32;           // fragments of a wave in each direction
+    constexpr int STAGE = T * 64;       // bytes of one operand's stage
+    constexpr int COPIES = STAGE / 1024 / 4;  // copies a wave makes for one operand's stage
+    constexpr bool PACKED = RK == kPacked || RK == kPackedT;
+    constexpr int TILES = PACKED ? T / 128 : 1;  // packed tiles a wave decodes in a step
+    __shared__ __align__(16) uint8_t lds[8 * STAGE];  // four stages of R, four of C
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const uint32_t q = lane >> 4, l15 = lane & 15;
-    const uint32_t wr = wave % WR, wc = wave / WR;
+    const uint32_t wr = wave & 1, wc = wave >> 1;
 
     // Workgroups go to the 8 XCDs in turn: give each XCD a run of neighbouring
     // tiles, four column tiles wide, so that its L2 holds what they share.
@@ -705,219 +752,277 @@ __global__ __launch_bounds__(WR *WC * 64) void k_gemm(GemmParams p) {
     if (KIND == kGemmDw) {
         g = blockIdx.y;
         group_rows(p.offsets, g, p.tokens, a0, a_end);
-        c0 = ct * TC;
+        c0 = ct * T;
         c_end = p.c_limit;
     } else {
-        if (!find_group(p, ct, TC, lane, g, c0, c_end)) return;
+        if (!find_group(p, ct, T, lane, g, c0, c_end)) return;
         g = uniform(g);
         c0 = uniform(c0);
         c_end = uniform(c_end);
     }
-    const uint32_t steps = KIND == kGemmDw ? (a_end - a0 + 63) / 64 : p.steps;
-
-    RSide<RK, TR, WAVES> R;
-    uint4 cu[CUNITS];
+    // stages of 32 contraction values
+    const uint32_t S = KIND == kGemmDw ? (a_end - a0 + 31) / 32 : 2 * p.steps;
     const uint32_t KB = p.w.col_blocks;
 
-    // place of the wave's i-th packed tile: forward: 16-row block of the tile; dx: (row block, column block)
-    auto tile_index = [&](int i, uint32_t s, bool &live) -> uint64_t {
-        const uint32_t j = wave * R.TILES + i;
+    // ---- copies from memory ----
+    // Rows: a copy takes 16 rows.  Cols: 1 KiB of the stage's rows.  What lies behind the last row or column is read
+    // as zeros.
+    constexpr uint32_t kNowhere = 0xFFFFFF00u;
+    uint32_t c_off[COPIES], r_off[RK == kCols ? COPIES : 1];
+    auto cols_off = [&](int i, uint32_t x0, uint32_t limit, uint64_t stride) __attribute__((always_inline)) -> uint32_t {
+        const uint32_t j = (wave * COPIES + i) * 64 + lane, a = j / (T / 8), u = j % (T / 8);
+        const uint32_t c = x0 + (((u >> 1) ^ cols_swizzle(a)) * 2 + (u & 1)) * 8;
+        return c < limit ? (a * (uint32_t)stride + c) * 2 : kNowhere;
+    };
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+        if constexpr (CK == kRows) {
+            const uint32_t row = (wave * COPIES + i) * 16 + (lane >> 2), u = (lane & 3) ^ (row >> 2 & 3);
+            c_off[i] = (row * (uint32_t)p.cmat.stride + u * 8) * 2;
+        } else {
+            c_off[i] = cols_off(i, c0, p.c_limit, p.cmat.stride);
+        }
+        if constexpr (RK == kCols) r_off[i] = cols_off(i, rt * T, p.r_limit, p.rmat.stride);
+    }
+    uint8_t *const r_lds = lds, *const c_lds = lds + 4 * STAGE;
+    // Starts the copies of stage s; `between(i)` comes behind the i-th.  Stages behind the last are zeros.
+    constexpr int PARTS = COPIES * (RK == kCols ? 2 : 1);
+    auto copy_stage = [&](uint32_t s, auto between) __attribute__((always_inline)) {
+        uint8_t *cd = c_lds + (s & 3) * STAGE + wave * COPIES * 1024;
+        uint8_t *rd = r_lds + (s & 3) * STAGE + wave * COPIES * 1024;
+        const uint8_t *cp = static_cast<const uint8_t *>(p.cmat.p);
+        if constexpr (CK == kRows) {
+            const uint32_t rows = min((uint32_t)T, c_end - c0), bytes = ((rows - 1) * (uint32_t)p.cmat.stride + S * 32) * 2;
+            const rsrc_t c = buffer(cp + (uint64_t)c0 * p.cmat.stride * 2 + (uint64_t)s * 64, s < S ? bytes - s * 64 : 0);
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) {
+                copy_to_lds(c, c_off[i], cd + i * 1024);
+                between(i);
+            }
+        } else {
+            const uint32_t a = a0 + s * 32, rows = s < S ? min(32u, a_end - a) : 0;
+            const rsrc_t c = buffer(cp + (uint64_t)a * p.cmat.stride * 2, rows * (uint32_t)p.cmat.stride * 2);
+            const rsrc_t r = buffer(static_cast<const uint8_t *>(p.rmat.p) + (uint64_t)a * p.rmat.stride * 2,
+                                    rows * (uint32_t)p.rmat.stride * 2);
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) {
+                copy_to_lds(c, c_off[i], cd + i * 1024);
+                between(2 * i);
+                copy_to_lds(r, r_off[i], rd + i * 1024);
+                between(2 * i + 1);
+            }
+        }
+    };
+
+    // ---- packed weights ----
+    // Forward: a block of 64 contraction values is T / 16 tiles, which fill two stages: the wave decodes half of its
+    // tiles in each of two steps.  dx: a stage of 32 weight rows is 2 x T / 64 tiles.
+    Tile t[2][TILES];
+    uint2 hd[2][TILES];
+    auto tile_index = [&](uint32_t n, int i, bool &live) __attribute__((always_inline)) -> uint64_t {  // n: decode step
         uint32_t rb, kb;
+        n = min(n, S - 1);
         if (RK == kPacked) {
+            const uint32_t j = (wave * 2 + (n & 1)) * TILES + i;
+            kb = n >> 1;
             if (GATED) {
-                rb = rt * (TR / 32) + (j >> 1);
+                rb = rt * (T / 32) + (j >> 1);
                 live = rb < p.w.part_blocks;
                 rb = live ? rb + (j & 1 ? p.w.part_blocks : 0) : 0;
             } else {
-                rb = rt * (TR / 16) + j;
+                rb = rt * (T / 16) + j;
                 live = rb < p.row_blocks;
                 rb = live ? rb + p.row_block0 : 0;
             }
-            kb = s;
         } else {
-            rb = s * 4 + (j & 3);
-            kb = rt * (TR / 64) + (j >> 2);
+            const uint32_t j = wave * TILES + i;
+            rb = n * 2 + (j & 1);
+            kb = rt * (T / 64) + (j >> 1);
             live = rb < p.row_blocks && kb < KB;
             rb = live ? rb + p.row_block0 : 0;
             kb = live ? kb : 0;
         }
         return ((uint64_t)g * p.w.row_blocks + rb) * KB + kb;
     };
-    auto load_heads = [&](uint32_t s) {
-        if constexpr (RK != kCols) {
+    auto load_heads = [&](uint32_t n, int b) __attribute__((always_inline)) {
+        if constexpr (PACKED) {
 #pragma unroll
-            for (int i = 0; i < R.TILES; ++i) {
+            for (int i = 0; i < TILES; ++i) {
                 bool live;
-                R.hd[i] = tile_head(p.w, tile_index(i, s, live));
+                const uint64_t x = tile_index(n, i, live);
+                hd[b][i] = tile_head(p.w, x);
             }
         }
     };
-    auto load_cols = [&](const Mat &m, uint32_t s, uint32_t x0, uint32_t limit, uint4 *u, int units, int width) {
-        // [64 rows][width columns] of a matrix whose rows are the contraction
-        for (int i = 0; i < units; ++i) {
-            const uint32_t j = i * THREADS + tid, row = j / (width / 8), c = x0 + j % (width / 8) * 8;
-            const uint32_t a = a0 + s * 64 + row;
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (a < a_end && c < limit)
-                u[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(m.p) + (uint64_t)a * m.stride + c);
-        }
-    };
-    auto load = [&](uint32_t s) {
-        if constexpr (RK == kCols) {
-            load_cols(p.rmat, s, rt * TR, p.r_limit, R.u, R.UNITS, TR);
-        } else {
+    constexpr uint32_t kDead = 1u << 31;  // header flag here: the tile lies outside the weight
+    auto load_tiles = [&](uint32_t n, int b) __attribute__((always_inline)) {
+        if constexpr (PACKED) {
 #pragma unroll
-            for (int i = 0; i < R.TILES; ++i) {
+            for (int i = 0; i < TILES; ++i) {
                 bool live;
-                const uint64_t t = tile_index(i, s, live);
-                tile_load(R.t[i], p.w, t, R.hd[i], lane);
-                R.live[i] = live;
-            }
-        }
-        if constexpr (CK == kCols) {
-            load_cols(p.cmat, s, c0, p.c_limit, cu, CUNITS, TC);
-        } else {
-#pragma unroll
-            for (int i = 0; i < CUNITS; ++i) {
-                const uint32_t j = i * THREADS + tid, row = c0 + (j >> 3), a = s * 64 + (j & 7) * 8;
-                cu[i] = make_uint4(0, 0, 0, 0);
-                if (row < c_end && a < p.c_limit)
-                    cu[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.cmat.p) +
-                                                             (uint64_t)row * p.cmat.stride + a);
+                const uint64_t x = tile_index(n, i, live);
+                tile_load(t[b][i], p.w, x, hd[b][i], lane);
+                if (RK == kPackedT && !live) t[b][i].h |= kDead;
             }
         }
     };
-    auto stage = [&](uint8_t *rl, uint8_t *cl) {
-        if constexpr (RK == kCols) {
-#pragma unroll
-            for (int i = 0; i < R.UNITS; ++i) {
-                const uint32_t j = i * THREADS + tid, row = j / (TR / 8), c = j % (TR / 8);
-                *reinterpret_cast<uint4 *>(rl + cols_at<TR>(row, c >> 1) + (c & 1) * 16) = R.u[i];
-            }
+    // Places of the two halves of a lane's 16 values; dx: both in one stage.
+    auto tile_place = [&](uint32_t n, int i, uint32_t &s0, uint32_t &at0, uint32_t &s1, uint32_t &at1, uint32_t l) __attribute__((always_inline)) {
+        if (RK == kPacked) {
+            const uint32_t j = (wave * 2 + (n & 1)) * TILES + i;
+            s0 = n & ~1u;
+            s1 = s0 + 1;
+            at0 = at1 = j * 1024 + l * 16;
         } else {
+            const uint32_t j = wave * TILES + i, row = (j & 1) * 16 + (l & 15), lq = l >> 4;
+            s0 = s1 = n;
+            at0 = cols_at<T>(row, (j >> 1) * 4 + (lq >> 1)) + (lq & 1) * 16;
+            at1 = cols_at<T>(row, (j >> 1) * 4 + 2 + (lq >> 1)) + (lq & 1) * 16;
+        }
+    };
+    auto store_tile = [&](uint32_t n, int i, const uint32_t v[8]) __attribute__((always_inline)) {
+        uint32_t s0, s1, at0, at1;
+        tile_place(n, i, s0, at0, s1, at1, lane);
+        *reinterpret_cast<uint4 *>(r_lds + (s0 & 3) * STAGE + at0) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4 *>(r_lds + (s1 & 3) * STAGE + at1) = make_uint4(v[4], v[5], v[6], v[7]);
+    };
+    // What the plain decode does not cover is put right behind it, from the header and the list entry.
+    struct Mend {
+        uint32_t h, off, ent;
+    };
+    auto decode = [&](uint32_t n, int b, Mend *m) __attribute__((always_inline)) {
+        if constexpr (PACKED) {
 #pragma unroll
-            for (int i = 0; i < R.TILES; ++i) {
-                const uint32_t j = wave * R.TILES + i;
+            for (int i = 0; i < TILES; ++i) {
                 uint32_t v[8];
-                tile_decode(R.t[i], p.w, lane, v);
-                if (!R.live[i])
-                    for (int d = 0; d < 8; ++d) v[d] = 0;
-                const uint4 a = make_uint4(v[0], v[1], v[2], v[3]), b = make_uint4(v[4], v[5], v[6], v[7]);
-                if constexpr (RK == kPacked) {
-                    *reinterpret_cast<uint4 *>(rl + j * 2048 + lane * 16) = a;
-                    *reinterpret_cast<uint4 *>(rl + j * 2048 + 1024 + lane * 16) = b;
-                } else {
-                    const uint32_t row = (j & 3) * 16 + l15, flip = (lane >> 3 & 1) * 16;
-                    uint8_t *d = rl + cols_at<TR>(row, (j >> 2) * 4 + q);
-                    *reinterpret_cast<uint4 *>(d + flip) = flip ? b : a;
-                    *reinterpret_cast<uint4 *>(d + (16 - flip)) = flip ? a : b;
+                tile_decode_plain(t[b][i], v);
+                store_tile(n, i, v);
+                m[i] = Mend{t[b][i].h, t[b][i].off, t[b][i].ent};
+            }
+        }
+    };
+    auto mend = [&](uint32_t n, const Mend *m) __attribute__((always_inline)) {
+        if constexpr (PACKED) {
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                if ((m[i].h & (0xFF00u | kTileZero | kDead)) == 0) continue;
+                const bool dead = m[i].h & kDead;
+                if (dead || tile_special(m[i].h)) {
+                    uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (!dead) {
+                        bool live;
+                        Tile x;
+                        tile_load(x, p.w, tile_index(n, i, live), make_uint2(m[i].h, m[i].off), lane);
+                        tile_decode_special(x, p.w, lane, v);
+                    }
+                    store_tile(n, i, v);
+                }
+                if (!dead && lane < tile_listed(m[i].h)) {
+                    uint32_t s0, s1, at0, at1;
+                    tile_place(n, i, s0, at0, s1, at1, m[i].ent >> 4 & 63);
+                    const uint32_t at = m[i].ent & 8 ? (s1 & 3) * STAGE + at1 : (s0 & 3) * STAGE + at0;
+                    *reinterpret_cast<uint16_t *>(r_lds + at + (m[i].ent & 7) * 2) = (uint16_t)(m[i].ent >> 16);
                 }
             }
         }
-        if constexpr (CK == kCols) {
-#pragma unroll
-            for (int i = 0; i < CUNITS; ++i) {
-                const uint32_t j = i * THREADS + tid, row = j / (TC / 8), c = j % (TC / 8);
-                *reinterpret_cast<uint4 *>(cl + cols_at<TC>(row, c >> 1) + (c & 1) * 16) = cu[i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < CUNITS; ++i) {
-                const uint32_t j = i * THREADS + tid;
-                *reinterpret_cast<uint4 *>(cl + rows_at(j >> 3, j & 7)) = cu[i];
-            }
-        }
     };
 
-    f32x4 acc[FR][FC];
+    // ---- fragments and products ----
+    bf16x8 rf[2][F], cf[2][F];
+    auto read_frags = [&](uint32_t s, int b, int first, int end) __attribute__((always_inline)) {  // of F + F
+        const uint8_t *rl = r_lds + (s & 3) * STAGE, *cl = c_lds + (s & 3) * STAGE;
 #pragma unroll
-    for (int i = 0; i < FR; ++i)
-        for (int j = 0; j < FC; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    auto multiply = [&](const uint8_t *rl, const uint8_t *cl) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            bf16x8 cf[FC];
-#pragma unroll
-            for (int j = 0; j < FC; ++j) {
-                const uint32_t col = (wc * FC + j) * 16;
-                if constexpr (CK == kCols)
-                    cf[j] = cols_frag<TC>(cl, col, h, lane);
-                else
-                    cf[j] = *reinterpret_cast<const bf16x8 *>(cl + rows_at(col + l15, q * 2 + h));
-            }
-#pragma unroll
-            for (int i = 0; i < FR; ++i) {
-                bf16x8 rf;
+        for (int k = first; k < end; ++k) {
+            const int i = k >> 1;
+            if (k & 1) {
+                const uint32_t rr = (wr * F + i) * 16;
                 if constexpr (RK == kPacked)
-                    rf = *reinterpret_cast<const bf16x8 *>(rl + (wr * FR + i) * 2048 + h * 1024 + lane * 16);
+                    rf[b][i] = *reinterpret_cast<const bf16x8 *>(rl + rr * 64 + lane * 16);
                 else
-                    rf = cols_frag<TR>(rl, (wr * FR + i) * 16, h, lane);
-#pragma unroll
-                for (int j = 0; j < FC; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rf, cf[j], acc[i][j], 0, 0, 0);
+                    rf[b][i] = cols_frag<T>(rl, rr, lane);
+            } else {
+                const uint32_t cc = (wc * F + i) * 16;
+                if constexpr (CK == kCols)
+                    cf[b][i] = cols_frag<T>(cl, cc, lane);
+                else
+                    cf[b][i] = *reinterpret_cast<const bf16x8 *>(cl + rows_at(cc + l15, q));
             }
         }
     };
+    f32x4 acc[F][F];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+        for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    auto multiply = [&](int b, int first, int end) __attribute__((always_inline)) {  // of F F products
+#pragma unroll
+        for (int k = first; k < end; ++k) mfma(acc[k / F][k % F], rf[b][k / F], cf[b][k % F]);
+    };
 
-    if (steps > 0) {
-        load_heads(0);
-        load(0);
-        if (steps > 1) load_heads(1);
-        stage(lds, lds + 2 * RBYTES);
-        if (steps > 1) load(1);
-        if (steps > 2) load_heads(2);
-        lds_barrier();
-        for (uint32_t s = 0; s < steps; ++s) {
-            const uint32_t b = s & 1;
-            if (s + 1 < steps) stage(lds + (b ^ 1) * RBYTES, lds + 2 * RBYTES + (b ^ 1) * CBYTES);
-            if (s + 2 < steps) load(s + 2);
-            if (s + 3 < steps) load_heads(s + 3);
-            multiply(lds + b * RBYTES, lds + 2 * RBYTES + b * CBYTES);
-            lds_barrier();
+    // Decode step n fills, forward: half of stages n & ~1 and (n & ~1) + 1; dx: stage n.  In step s: n = s + 3
+    // forward (stage s + 2 is whole after step s, when s is odd with the one after it), n = s + 2 for dx.
+    constexpr uint32_t AHEAD = RK == kPacked ? 3 : 2;
+    constexpr int PER_STEP = COPIES * (RK == kCols ? 2 : 1) + (PACKED ? 3 * TILES : 0);
+    if (S > 0) {
+        Mend m[TILES];
+        for (uint32_t s = 0; s < 3; ++s) copy_stage(s, [](int) {});
+        if constexpr (PACKED) {
+            load_heads(0, 0);
+            load_heads(1, 1);
+            load_tiles(0, 0);
+            load_tiles(1, 1);
+            load_heads(2, 0);
+#pragma unroll
+            for (uint32_t n = 0; n < AHEAD; ++n) {
+                decode(n, n & 1, m);
+                if (n < S) mend(n, m);
+                load_tiles(n + 2, n & 1);
+                load_heads(n + 3, (n & 1) ^ 1);
+            }
         }
+        wait_copies<0>();
+        barrier();
+        read_frags(0, 0, 0, 2 * F);
+        settle(acc);  // the zeros
+        auto step = [&](uint32_t s, auto parity) __attribute__((always_inline)) {
+            constexpr int b = decltype(parity)::value;
+            constexpr int tb = (b + AHEAD) & 1;
+            const uint32_t n = s + AHEAD;
+            // copies, reads, the decoder and the loads between the matrix instructions, whose shadow hides them
+            copy_stage(s + 3, [&](int i) __attribute__((always_inline)) {
+                read_frags(s + 1, b ^ 1, i * 2 * F / PARTS, (i + 1) * 2 * F / PARTS);
+                if (i == 0) decode(n, tb, m);  // behind the last stage: into stages that nothing reads any more
+                if (i == PARTS - 1) load_tiles(n + 2, tb), load_heads(n + 3, tb ^ 1);
+                multiply(b, i * F * F / PARTS, (i + 1) * F * F / PARTS);
+            });
+            if (PACKED && n < S) mend(n, m);
+            wait_copies<PER_STEP>();  // stage s + 2 has arrived: only this step's copies and loads may be on their way
+            barrier();
+        };
+        for (uint32_t s = 0; s < S; s += 2) {  // (a step behind an odd number of stages adds zeros)
+            step(s, std::integral_constant<int, 0>{});
+            step(s + 1, std::integral_constant<int, 1>{});
+        }
+        wait_copies<0>();
+        barrier();
+        settle(acc);
     }
 
-    // ---- epilogues: acc[i][j][d] is row r0 + 16 i + 4 q + d, column cc0 + 16 j + l15 ----
-    const uint32_t cc0 = c0 + wc * FC * 16 + l15;
-    if constexpr (KIND == kGemmForward) {
-#pragma unroll
-        for (int j = 0; j < FC; ++j) {
-            const uint32_t m = cc0 + j * 16;
-            if (m >= c_end) continue;
-            const uint64_t bias_at = (uint64_t)g * p.rows;
-            if constexpr (GATED) {
-#pragma unroll
-                for (int i = 0; i < FR; i += 2) {
-                    const uint32_t n = (rt * (TR / 32) + (wr * FR + i) / 2) * 16 + q * 4;
-                    float z[2][4];
-                    for (int d = 0; d < 4; ++d) z[0][d] = acc[i][j][d], z[1][d] = acc[i + 1][j][d];
-                    linear_out<true>(p.lin, bias_at, p.w.part_rows, m, n, z);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < FR; ++i) {
-                    const uint32_t n = (rt * (TR / 16) + wr * FR + i) * 16 + q * 4;
-                    float z[1][4];
-                    for (int d = 0; d < 4; ++d) z[0][d] = acc[i][j][d];
-                    linear_out<false>(p.lin, bias_at, p.w.part_rows, m, n, z);
-                }
-            }
-        }
-    } else if constexpr (KIND == kGemmLossStat) {
+    // ---- epilogues: acc[i][j][d] is row 16 (wr F + i) + 4 q + d of the tile, column 16 (wc F + j) + l15 ----
+    if constexpr (KIND == kGemmLossStat) {
         // every token's largest logit in this tile, and the sum of exp(logit - that)
-        f32x2 *red = reinterpret_cast<f32x2 *>(lds);  // [WR][TC]
+        f32x2 *red = reinterpret_cast<f32x2 *>(lds);  // [2][T]
 #pragma unroll
-        for (int j = 0; j < FC; ++j) {
-            const uint32_t m = cc0 + j * 16;
+        for (int j = 0; j < F; ++j) {
+            const uint32_t m = c0 + (wc * F + j) * 16 + l15;
             const bool live = m < c_end;
             const int64_t want = live ? p.loss.target[m] : -1;
+            const uint32_t n0 = rt * T + wr * F * 16 + q * 4;
             float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < FR; ++i)
+            for (int i = 0; i < F; ++i)
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    const uint32_t n = rt * TR + (wr * FR + i) * 16 + q * 4 + d;
+                    const uint32_t n = n0 + i * 16 + d;
                     if (n >= p.rows) acc[i][j][d] = -INFINITY;
                     if (live && (int64_t)n == want && n < p.rows) p.loss.picked[m] = acc[i][j][d];
                     top = fmaxf(top, acc[i][j][d]);
@@ -928,77 +1033,86 @@ __global__ __launch_bounds__(WR *WC * 64) void k_gemm(GemmParams p) {
             const float ref = fminf(fmaxf(top, -3.0e38f), 3.0e38f);
             float sum = 0;
 #pragma unroll
-            for (int i = 0; i < FR; ++i)
+            for (int i = 0; i < F; ++i)
 #pragma unroll
                 for (int d = 0; d < 4; ++d) sum += __expf(acc[i][j][d] - ref);
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (q == 0) red[wr * TC + (wc * FC + j) * 16 + l15] = f32x2{ref, sum};
+            if (q == 0) red[wr * T + (wc * F + j) * 16 + l15] = f32x2{ref, sum};
         }
         __syncthreads();
-        for (uint32_t c = tid; c < TC; c += THREADS) {
+        for (uint32_t c = tid; c < T; c += 256) {
             if (c0 + c >= c_end) continue;
-            float ref = red[c][0];
-            for (int w = 1; w < WR; ++w) ref = fmaxf(ref, red[w * TC + c][0]);
-            float sum = 0;
-            for (int w = 0; w < WR; ++w) sum += red[w * TC + c][1] * __expf(red[w * TC + c][0] - ref);
+            const float ref = fmaxf(red[c][0], red[T + c][0]);
+            const float sum = red[c][1] * __expf(red[c][0] - ref) + red[T + c][1] * __expf(red[T + c][0] - ref);
             p.loss.part[(uint64_t)rt * p.tokens + c0 + c] = make_float2(ref, sum);
         }
-    } else if constexpr (KIND == kGemmLossDz) {
-        // g (softmax - one at the target), rounded to bf16 for the two products that follow; zero behind the last row
+        return;
+    }
+
+    // The others go through LDS, 64 columns at a time, so that a column's rows leave in one run: a wave's part is
+    // [columns][16 F] values in units of four, the unit's place xored with the column against bank conflicts.
+    constexpr int UNITS = F * 4;
+    f32x4 *out = reinterpret_cast<f32x4 *>(lds + wave * (2 * STAGE));
 #pragma unroll
-        for (int j = 0; j < FC; ++j) {
-            const uint32_t m = cc0 + j * 16;
-            if (m >= c_end) continue;
-            const int64_t want = p.loss.target[m];
-            const bool counts = want != p.loss.ignore && want >= 0 && want < (int64_t)p.rows;
-            const float gr = counts ? p.loss.dloss[m] : 0.0f, lse = p.loss.lse[m];
+    for (int ph = 0; ph < F; ph += 4) {
 #pragma unroll
-            for (int i = 0; i < FR; ++i) {
-                const uint32_t at = rt * TR + (wr * FR + i) * 16 + q * 4;
-                float z[4];
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < F; ++i) out[(j * 16 + l15) * UNITS + ((i * 4 + q) ^ l15)] = acc[i][ph + j];
+        constexpr int OUTS = GATED ? UNITS / 2 : UNITS;  // results of a column, in units of four
+#pragma unroll 1
+        for (uint32_t k = lane; k < 64 * OUTS; k += 64) {
+            const uint32_t cl = k / OUTS, u = k % OUTS;
+            const uint32_t c = c0 + (wc * F + ph) * 16 + cl;  // column
+            float v[GATED ? 2 : 1][4];
+#pragma unroll
+            for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+                const uint32_t from = GATED ? (u >> 2) * 8 + h * 4 + (u & 3) : u;
+                const f32x4 x = out[cl * UNITS + (from ^ (cl & 15))];
+                for (int d = 0; d < 4; ++d) v[h][d] = x[d];
+            }
+            const uint32_t r = rt * (T / (GATED ? 2 : 1)) + wr * OUTS * 4 + u * 4;  // first of four rows
+            if constexpr (KIND == kGemmForward) {
+                if (c < c_end) linear_out<GATED>(p.lin, (uint64_t)g * p.rows, p.w.part_rows, c, r, v);
+            } else if constexpr (KIND == kGemmLossDz) {
+                // g (softmax - one at the target), rounded to bf16 for the two products that follow; zeros behind the
+                // last row
+                if (c >= c_end) continue;
+                const int64_t want = p.loss.target[c];
+                const bool counts = want != p.loss.ignore && want >= 0 && want < (int64_t)p.rows;
+                const float gr = counts ? p.loss.dloss[c] : 0.0f, lse = p.loss.lse[c];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    const uint32_t n = p.row_block0 * 16 + at + d;
-                    float v = __expf(acc[i][j][d] - lse);
-                    if ((int64_t)n == want) v -= 1.0f;
-                    z[d] = n < p.rows && counts ? gr * v : 0.0f;
+                    const uint32_t n = p.row_block0 * 16 + r + d;
+                    float e = __expf(v[0][d] - lse);
+                    if ((int64_t)n == want) e -= 1.0f;
+                    v[0][d] = n < p.rows && counts ? gr * e : 0.0f;
                 }
-                store4(p.loss.dz, (uint64_t)m * p.loss.dz_stride + at, false, true, 4, z);
-            }
-        }
-    } else {
-        const StoreEpi &e = p.store;
-        const uint32_t r_end = p.cols;
-#pragma unroll
-        for (int j = 0; j < FC; ++j) {
-            const uint32_t c = cc0 + j * 16;
-            uint64_t row = c;
-            if constexpr (KIND == kGemmDw) {
-                // padded row of the stack's part -> row of the matrix; pieces start at row_block0
-                const uint32_t n = c + p.row_block0 * 16, pad = p.w.part_blocks * 16, part = n / pad, in = n - part * pad;
-                if (in >= p.w.part_rows || part >= p.w.parts || c >= p.row_blocks * 16) continue;
-                row = (uint64_t)g * p.rows + (uint64_t)part * p.w.part_rows + in;
+                store4(p.loss.dz, (uint64_t)c * p.loss.dz_stride + r, false, true, 4, v[0]);
             } else {
-                if (c >= c_end) continue;
-            }
-#pragma unroll
-            for (int i = 0; i < FR; ++i) {
-                const uint32_t r = rt * TR + (wr * FR + i) * 16 + q * 4;
-                if (r >= r_end) continue;
-                const uint32_t count = r_end - r < 4 ? r_end - r : 4;
-                float v[4];
-                for (int d = 0; d < 4; ++d) v[d] = acc[i][j][d];
+                const StoreEpi &e = p.store;
+                uint64_t row = c;
+                if constexpr (KIND == kGemmDw) {
+                    // padded row of the stack's part -> row of the matrix; pieces start at row_block0
+                    const uint32_t n = c + p.row_block0 * 16, pad = p.w.part_blocks * 16, part = n / pad, in = n - part * pad;
+                    if (in >= p.w.part_rows || part >= p.w.parts || c >= p.row_blocks * 16) continue;
+                    row = (uint64_t)g * p.rows + (uint64_t)part * p.w.part_rows + in;
+                } else {
+                    if (c >= c_end) continue;
+                }
+                if (r >= p.cols) continue;
+                const uint32_t count = p.cols - r < 4 ? p.cols - r : 4;
                 if (e.sum) {
                     const bool sv = count == 4;  // the sums' stride is a multiple of four
                     if (e.add) {
                         float o[4];
                         load4(e.sum, row * e.sum_stride + r, true, sv, count, o);
-                        for (int d = 0; d < 4; ++d) v[d] += o[d];
+                        for (int d = 0; d < 4; ++d) v[0][d] += o[d];
                     }
-                    if (!e.out) store4(e.sum, row * e.sum_stride + r, true, sv, count, v);
+                    if (!e.out) store4(e.sum, row * e.sum_stride + r, true, sv, count, v[0]);
                 }
-                if (e.out) store4(e.out, row * e.stride + r, false, e.vec && count == 4, count, v);
+                if (e.out) store4(e.out, row * e.stride + r, false, e.vec && count == 4, count, v[0]);
             }
         }
     }
@@ -1128,9 +1242,9 @@ template <Operand RK, Operand CK, GemmKind KIND, bool GATED>
 hipError_t gemm(uint32_t edge, const GemmParams &p, hipStream_t s) {
     const dim3 grid(p.r_tiles * p.c_tiles, KIND == kGemmDw ? p.groups : 1);
     if (edge == 256)
-        k_gemm<RK, CK, KIND, GATED, 256, 256, 2, 4><<<grid, 512, 0, s>>>(p);
+        k_gemm<RK, CK, KIND, GATED, 256><<<grid, 256, 0, s>>>(p);
     else
-        k_gemm<RK, CK, KIND, GATED, 128, 128, 2, 2><<<grid, 256, 0, s>>>(p);
+        k_gemm<RK, CK, KIND, GATED, 128><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
 }
 

@@ -4,7 +4,7 @@
 // A packed weight stack holds E matrices of N rows and K columns in bf16,
 // without loss.  Its unit is a tile of 16 rows by 64 columns, in the order in
 // which a wave's lanes feed the matrix instructions: lane l = 16 q + r holds
-// row r, columns 16 q .. 16 q + 15.  Every value keeps its sign and mantissa
+// of row r the columns 8 q + j and 32 + 8 q + j, j = 0 .. 7.  Every value keeps its sign and mantissa
 // byte; its exponent e is a 4-bit code base - e within the tile's window of 16
 // exponents (or of 15, code 15 then standing for exponent 0).  The few values
 // outside the window are listed; a tile with more than kMaxListed of them
@@ -137,7 +137,7 @@ struct GemmParams {
     uint32_t groups;        // matrices (1 without offsets)
     uint32_t tokens;        // rows of x
     uint32_t r_tiles, c_tiles;
-    uint32_t r_limit, c_limit;   // valid columns of rmat / cmat, multiples of 8
+    uint32_t r_limit, c_limit;   // columns of rmat / cmat that can be read, multiples of 8; of a contraction, of 64
     uint32_t steps;         // contraction blocks of 64
     uint32_t row_block0;    // first row block of a piece of the weight
     uint32_t row_blocks;    // row blocks of the piece

@@ -60,8 +60,12 @@ bool mat_ok(const void *p, uint64_t stride, uint64_t rows, uint64_t cols, uint32
 bool type_ok(uint32_t t) { return t == UZIP_BF16 || t == UZIP_FP32; }
 uint32_t type_size(uint32_t t) { return t == UZIP_FP32 ? 4 : 2; }
 
-// Whether a bf16 matrix can be read 16 bytes at a time.
+// Whether a bf16 matrix can be read 16 bytes at a time, and whether the tiled
+// product can: a tile's rows are addressed with 32 bits.
 bool by16(const void *p, uint64_t stride, uint64_t cols) { return aligned(p, 16) && stride % 8 == 0 && cols % 8 == 0; }
+bool tiled(const void *p, uint64_t stride, uint64_t cols) { return by16(p, stride, cols) && stride < (1u << 22); }
+// The same where its columns are the contraction, which goes in blocks of 64.
+bool tiled64(const void *p, uint64_t stride, uint64_t cols) { return tiled(p, stride, cols) && cols % 64 == 0; }
 
 // Carves a workspace; with a null base it only counts.
 struct Carver {
@@ -134,8 +138,8 @@ LinearPlan plan_linear(const uzip_weight *w, const uzip_linear_args *a, Carver &
     LinearPlan p{};
     const uint64_t groups = a->offsets ? w->matrices : 1;
     p.skinny = skinny_fits(a->tokens, groups);
-    p.stage = !p.skinny && !by16(a->x, a->x_stride, w->cols);
-    if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 8));
+    p.stage = !p.skinny && !tiled64(a->x, a->x_stride, w->cols);
+    if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 64));
     return p;
 }
 
@@ -161,7 +165,7 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
     }
     Mat x{a->x, a->x_stride};
     if (plan.stage) {
-        x = Mat{plan.x, up(w->cols, 8)};
+        x = Mat{plan.x, up(w->cols, 64)};
         const hipError_t e = launch_stage(static_cast<const uint16_t *>(a->x), a->x_stride, plan.x, x.stride, a->tokens,
                                           w->cols, stream);
         if (e != hipSuccess) return UZIP_ERR_DEVICE;
@@ -215,8 +219,8 @@ BackwardPlan plan_backward(const uzip_weight *w, const uzip_linear_backward_args
     BackwardPlan p{};
     p.width = up(l.row_blocks * kTileRows, 64);
     p.make_dz = (a->dx || a->dw) &&
-                (a->act != UZIP_ACT_NONE || a->dy_dtype == UZIP_FP32 || !by16(a->dy, a->dy_stride, w->rows));
-    p.stage_x = a->dw && !by16(a->x, a->x_stride, w->cols);
+                (a->act != UZIP_ACT_NONE || a->dy_dtype == UZIP_FP32 || !tiled64(a->dy, a->dy_stride, w->rows));
+    p.stage_x = a->dw && !tiled(a->x, a->x_stride, w->cols);
     // runs of rows whose column sums are taken apart: enough workgroups for the chip, at least 32 rows each
     p.chunks = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(1, blocks(a->tokens, 32 * groups) * (groups > 1 ? 2 : 1)),
                                             groups > 1 ? 64 : 256);
@@ -326,8 +330,8 @@ struct LossPlan {
 
 LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward, Carver &c) {
     LossPlan p{};
-    p.stage = !by16(a->x, a->x_stride, w->cols);
-    if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 8));
+    p.stage = !tiled64(a->x, a->x_stride, w->cols);
+    if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 64));
     if (!backward) {
         p.edge = gemm_edge(w->rows, a->tokens, 1);
         p.part = c.take<float2>(a->tokens * blocks(w->rows, p.edge));
@@ -345,7 +349,7 @@ LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward,
 uzip_status stage_loss_x(const uzip_weight *w, const uzip_loss_args *a, const LossPlan &plan, Mat &x, hipStream_t stream) {
     x = Mat{a->x, a->x_stride};
     if (!plan.stage) return UZIP_OK;
-    x = Mat{plan.x, up(w->cols, 8)};
+    x = Mat{plan.x, up(w->cols, 64)};
     return done(launch_stage(static_cast<const uint16_t *>(a->x), a->x_stride, plan.x, x.stride, a->tokens, w->cols, stream));
 }
 
