@@ -316,7 +316,7 @@ uzip_status uzip_decompress_batched_timed(uzip_dtype dtype, size_t num_buffers, 
  * speed of memory.  Near-Gaussian weights take about 12.1 bits a value; any
  * bit pattern comes back as it was (values outside a tile's window are listed
  * beside it, and a tile with more than 64 of them keeps its exponents as
- * bytes, at most 24.1 bits a value).  Only bf16 weights are packed.
+ * bytes, at most 20.2 bits a value).  Only bf16 weights are packed.
  *
  * A stack holds `matrices` matrices of `rows` x `cols`.  gated: each matrix is
  * two of rows/2 rows, the gate's and then the up projection's, for

@@ -42,34 +42,29 @@ __device__ inline float from_bf16(uint16_t u) { return __uint_as_float((uint32_t
 
 // ---- packed tiles -----------------------------------------------------------
 
+// A tile's header: base exponent, count << 8 and flags; offset of its list or
+// exponent bytes; the first kInline entries of the list.
 struct Tile {
-    uint4 sm;      // sign+mantissa bytes of this lane's 16 values
-    uint2 code;    // their 4-bit codes
-    uint32_t ent;  // this lane's list entry
-    uint32_t h;    // header word 0, uniform
-    uint32_t off;  // header word 1, uniform
+    uint4 sm;    // sign+mantissa bytes of this lane's 16 values
+    uint2 code;  // their 4-bit codes
+    uint4 h;     // header, uniform
 };
 
-// A tile's header.  A list that would reach behind the extra region is
-// dropped, so that damaged weights cannot make a kernel read out of range.
-__device__ inline uint2 tile_head(const WeightView &w, uint64_t tile) {
-    uint2 h = w.head[tile];
+// A list that would reach behind the extra region is dropped, so that damaged
+// weights cannot make a kernel read out of range.
+__device__ inline uint4 tile_head(const WeightView &w, uint64_t tile) {
+    uint4 h = w.head[tile];
     const uint32_t cnt = (h.x >> 8) & 0xFF;
-    const uint32_t units = cnt == kTileRaw ? 64 : (cnt + 3) / 4;
-    if (units > w.extra_units || h.y > w.extra_units - units) h.x &= ~0xFF00u;
+    const uint32_t units = cnt == kTileRaw ? 64 : cnt <= kInline ? 0 : (cnt + 3) / 4;
+    if (units > w.extra_units || (units && h.y > w.extra_units - units)) h.x &= ~0xFF00u;
     return h;
 }
 
-__device__ inline void tile_load(Tile &t, const WeightView &w, uint64_t tile, uint2 head, uint32_t lane) {
+__device__ inline void tile_load(Tile &t, const WeightView &w, uint64_t tile, uint4 head, uint32_t lane) {
     const uint8_t *p = w.tiles + tile * kTileBytes;
     t.sm = *reinterpret_cast<const uint4 *>(p + lane * 16);
     t.code = *reinterpret_cast<const uint2 *>(p + kTileSm + lane * 8);
-    t.h = uniform(head.x);
-    t.off = uniform(head.y);
-    // (the entry load has no branch: a tile without a list reads one of its own words)
-    const uint32_t cnt = t.h >> 8 & 0xFF, n = cnt == kTileRaw ? 0 : cnt;
-    const uint32_t *list = reinterpret_cast<const uint32_t *>(n ? w.extra + (uint64_t)t.off * 16 : p);
-    t.ent = list[lane < n ? lane : 0];
+    t.h = make_uint4(uniform(head.x), uniform(head.y), uniform(head.z), uniform(head.w));
 }
 
 // Eight pairs of bf16 values from a lane's tile registers: five operations a
@@ -85,7 +80,7 @@ __device__ inline uint32_t tile_codes(const Tile &t, int p) {
     return (k == 0 ? c << 7 : k == 1 ? c << 3 : k == 2 ? c >> 1 : c >> 5) & 0x07800780u;
 }
 __device__ inline void tile_decode_plain(const Tile &t, uint32_t v[8]) {
-    const uint32_t base = (t.h & 0xFF) * 0x00800080u;
+    const uint32_t base = (t.h.x & 0xFF) * 0x00800080u;
 #pragma unroll
     for (int p = 0; p < 8; ++p) v[p] = tile_signs(t, p) | (base - tile_codes(t, p));
 }
@@ -94,8 +89,8 @@ __device__ inline void tile_decode_plain(const Tile &t, uint32_t v[8]) {
 // code 15 for exponent 0.
 __device__ inline bool tile_special(uint32_t h) { return (h & kTileZero) || (h >> 8 & 0xFF) == kTileRaw; }
 __device__ inline void tile_decode_special(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
-    if ((t.h >> 8 & 0xFF) == kTileRaw) {
-        const uint4 ex = *reinterpret_cast<const uint4 *>(w.extra + (uint64_t)t.off * 16 + lane * 16);
+    if ((t.h.x >> 8 & 0xFF) == kTileRaw) {
+        const uint4 ex = *reinterpret_cast<const uint4 *>(w.extra + (uint64_t)t.h.y * 16 + lane * 16);
         const uint32_t e[4] = {ex.x, ex.y, ex.z, ex.w};
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
@@ -104,7 +99,7 @@ __device__ inline void tile_decode_special(const Tile &t, const WeightView &w, u
         }
         return;
     }
-    const uint32_t base = (t.h & 0xFF) * 0x00800080u;
+    const uint32_t base = (t.h.x & 0xFF) * 0x00800080u;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const uint32_t x = tile_codes(t, p);
@@ -118,15 +113,23 @@ __device__ inline uint32_t tile_listed(uint32_t h) {
     const uint32_t cnt = h >> 8 & 0xFF;
     return cnt == kTileRaw ? 0 : min(cnt, kMaxListed);
 }
+// This lane's entry of a tile's list (lanes below tile_listed).
+__device__ inline uint32_t tile_entry(const WeightView &w, uint4 h, uint32_t lane) {
+    const uint32_t n = tile_listed(h.x);
+    if (n <= kInline) return lane ? h.w : h.z;
+    return reinterpret_cast<const uint32_t *>(w.extra + (uint64_t)h.y * 16)[min(lane, n - 1)];
+}
 
 // All of it, in registers.
 __device__ inline void tile_decode(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
     tile_decode_plain(t, v);
-    if (!(t.h & (0xFF00u | kTileZero))) return;
-    if (tile_special(t.h)) tile_decode_special(t, w, lane, v);
-    const uint32_t n = tile_listed(t.h);
+    if (!(t.h.x & (0xFF00u | kTileZero))) return;
+    if (tile_special(t.h.x)) tile_decode_special(t, w, lane, v);
+    const uint32_t n = tile_listed(t.h.x);
+    if (n == 0) return;
+    const uint32_t ent = tile_entry(w, t.h, lane);
     for (uint32_t i = 0; i < n; ++i) {
-        const uint32_t e = __builtin_amdgcn_readlane(t.ent, i);
+        const uint32_t e = __builtin_amdgcn_readlane(ent, i);
         const uint32_t idx = e & 15, val = e >> 16;
         const bool mine = lane == (e >> 4 & 63);
 #pragma unroll
@@ -199,8 +202,8 @@ __global__ __launch_bounds__(256) void k_pack(PackParams p) {
     *reinterpret_cast<uint2 *>(out + kTileSm + lane * 8) = make_uint2(cd[0], cd[1]);
     if (lane == 0) {
         const uint32_t cnt = outside > kMaxListed ? kTileRaw : outside;
-        reinterpret_cast<uint2 *>(p.out + p.l.head_off)[tile] =
-            make_uint2(base | cnt << 8 | (zero ? kTileZero : 0u), cnt == kTileRaw ? 64 : (cnt + 3) / 4);
+        reinterpret_cast<uint4 *>(p.out + p.l.head_off)[tile] =
+            make_uint4(base | cnt << 8 | (zero ? kTileZero : 0u), cnt == kTileRaw ? 64 : cnt <= kInline ? 0 : (cnt + 3) / 4, 0, 0);
     }
 }
 
@@ -227,7 +230,7 @@ __device__ inline uint64_t block_scan(uint64_t v, uint64_t *lds, uint64_t &total
 // Extra units of each block of kScanTiles tiles.
 __global__ __launch_bounds__(256) void k_pack_sums(PackParams p) {
     __shared__ uint64_t lds[4];
-    const uint2 *head = reinterpret_cast<const uint2 *>(p.out + p.l.head_off);
+    const uint4 *head = reinterpret_cast<const uint4 *>(p.out + p.l.head_off);
     uint64_t s = 0, total;
     for (uint32_t i = threadIdx.x; i < kScanTiles; i += 256) {
         const uint64_t t = (uint64_t)blockIdx.x * kScanTiles + i;
@@ -260,14 +263,14 @@ __global__ __launch_bounds__(256) void k_pack_scan(PackParams p) {
         if (threadIdx.x == 0) *p.out_size = total;
     }
     // between the tile headers and the tiles
-    const uint64_t gap = p.l.head_off + 8 * p.l.tiles + 8 * threadIdx.x;
+    const uint64_t gap = p.l.head_off + 16 * p.l.tiles + 8 * threadIdx.x;
     if (gap < p.l.tile_off) *reinterpret_cast<uint64_t *>(p.out + gap) = 0;
 }
 
 // The tiles' offsets.
 __global__ __launch_bounds__(256) void k_pack_place(PackParams p) {
     __shared__ uint64_t lds[4];
-    uint2 *head = reinterpret_cast<uint2 *>(p.out + p.l.head_off);
+    uint4 *head = reinterpret_cast<uint4 *>(p.out + p.l.head_off);
     uint64_t at = p.sums[blockIdx.x];
     for (uint32_t i = 0; i < kScanTiles; i += 256) {
         const uint64_t t = (uint64_t)blockIdx.x * kScanTiles + i + threadIdx.x;
@@ -284,7 +287,7 @@ __global__ __launch_bounds__(256) void k_pack_extra(PackParams p) {
     const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint64_t tile = (uint64_t)blockIdx.x * 4 + wave;
     if (tile >= p.l.tiles) return;
-    const uint2 head = reinterpret_cast<const uint2 *>(p.out + p.l.head_off)[tile];
+    uint4 &head = reinterpret_cast<uint4 *>(p.out + p.l.head_off)[tile];
     const uint32_t cnt = (head.x >> 8) & 0xFF;
     if (cnt == 0) return;
     uint16_t v[16];
@@ -314,9 +317,15 @@ __global__ __launch_bounds__(256) void k_pack_extra(PackParams p) {
     uint32_t *list = reinterpret_cast<uint32_t *>(out);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        if (mine >> i & 1) list[slot++] = lane << 4 | i | (uint32_t)v[i] << 16;
+        if (mine >> i & 1) {
+            const uint32_t e = lane << 4 | i | (uint32_t)v[i] << 16;
+            if (slot == 0) head.z = e;
+            if (slot == 1) head.w = e;
+            if (cnt > kInline) list[slot] = e;
+            ++slot;
+        }
     // the last unit's unused entries
-    const uint32_t pad = (cnt + 3) / 4 * 4;
+    const uint32_t pad = cnt > kInline ? (cnt + 3) / 4 * 4 : 0;
     if (lane >= cnt && lane < pad) list[lane] = 0;
 }
 
@@ -518,7 +527,7 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
             xr[j] = static_cast<const uint16_t *>(p.x.p) + (uint64_t)(xv[j] ? m : begin) * p.x.stride;
         }
         Tile t[RB];
-        uint2 hd[RB];
+        uint4 hd[RB];
         uint4 x[MT][2];
         auto load_x = [&](uint32_t kb) {
             const uint32_t k = kb * kTileCols + q * 8;
@@ -608,11 +617,12 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
 // dx:            r = column of x, c = token,     a = weight row
 // dw:            r = column of x, c = weight row, a = token
 //
-// Four waves, each a quarter of the tile.  The contraction goes in stages of
-// 32 through a ring of four LDS stages.  In step s a wave multiplies the
-// fragments it read in the step before, reads those of stage s + 1, starts the
-// copies of stage s + 3 from memory to LDS and decodes its share of the weights
-// of the stages after next; one barrier ends the step.
+// The contraction goes in stages of 32 through a ring of four LDS stages.  In
+// step s a wave multiplies fragments of stage s and reads those of stage s + 1
+// behind them, starts the copies of stage s + 3 from memory to LDS, and decodes
+// its share of the weights of the stages after next; one barrier ends the step.
+// Two waves a SIMD: a wave alone issues an instruction every four cycles, and a
+// step has too many of them for the matrix instructions' time.
 
 enum Operand { kPacked, kPackedT, kRows, kCols };
 
@@ -658,10 +668,13 @@ __device__ inline rsrc_t buffer(const uint8_t *p, uint32_t bytes) {
 // that the compiler does not wait for it before the next read of LDS: the
 // kernel's own waits and barriers say when the bytes are there.  It has no
 // result registers, and the asm statements around it keep their order.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // (m0 is reserved; it is set here all the same)
 __device__ inline void copy_to_lds(rsrc_t r, uint32_t off, const uint8_t *dst) {
     const uint32_t at = uniform((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)dst);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r) : "m0");
 }
+#pragma clang diagnostic pop
 
 template <int N>
 __device__ inline void wait_copies() {  // all but the last N memory operations of this wave, and its LDS operations
@@ -669,21 +682,21 @@ __device__ inline void wait_copies() {  // all but the last N memory operations 
 }
 __device__ inline void barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-// acc += a b, in place in accumulation registers.  In asm, because with all
-// 256 of them taken the compiler's own choice of registers moves accumulators
+// acc += a b, in place in accumulation registers.  In asm, because with half
+// of the registers taken by them the compiler's own choice of registers moves accumulators
 // to and fro in the loop (and then spills); the statements keep their order.
 // Between them and other instructions on the same registers there have to be
 // 18 cycles that the compiler does not know of: settle().
 __device__ inline void mfma(f32x4 &acc, bf16x8 a, bf16x8 b) {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
-template <int F>
-__device__ inline void settle(f32x4 (&acc)[F][F]) {
+template <int FR, int FC>
+__device__ inline void settle(f32x4 (&acc)[FR][FC]) {
 #pragma unroll
-    for (int i = 0; i < F * F; ++i) asm volatile("" : "+a"(acc[i / F][i % F]));
+    for (int i = 0; i < FR * FC; ++i) asm volatile("" : "+a"(acc[i / FC][i % FC]));
     asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
-    for (int i = 0; i < F * F; ++i) asm volatile("" : "+a"(acc[i / F][i % F]));
+    for (int i = 0; i < FR * FC; ++i) asm volatile("" : "+a"(acc[i / FC][i % FC]));
 }
 
 // Expert and first row of token tile `ct`, or false behind the last one.
@@ -721,16 +734,18 @@ __device__ inline bool find_group(const GemmParams &p, uint32_t ct, uint32_t edg
 }
 
 template <Operand RK, Operand CK, GemmKind KIND, bool GATED, int T>
-__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm(GemmParams p) {
-    constexpr int F = T / 32;           // fragments of a wave in each direction
-    constexpr int STAGE = T * 64;       // bytes of one operand's stage
-    constexpr int COPIES = STAGE / 1024 / 4;  // copies a wave makes for one operand's stage
+__global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) {
+    constexpr int WAVES = T / 32, WR = 2, WC = WAVES / 2;
+    constexpr int FR = T / WR / 16, FC = T / WC / 16;  // fragments of a wave: 8 x 4 or 4 x 4
+    constexpr int STAGE = T * 64;                      // bytes of one operand's stage
+    constexpr int COPIES = STAGE / 1024 / WAVES;       // copies a wave makes for one operand's stage: 2
     constexpr bool PACKED = RK == kPacked || RK == kPackedT;
-    constexpr int TILES = PACKED ? T / 128 : 1;  // packed tiles a wave decodes in a step
-    __shared__ __align__(16) uint8_t lds[8 * STAGE];  // four stages of R, four of C
+    constexpr int SLOT = 2048;                         // a packed tile on its way to the decoder
+    // four stages of R, four of C, two packed tiles a wave
+    __shared__ __align__(16) uint8_t lds[8 * STAGE + (PACKED ? 2 * WAVES * SLOT : 0)];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const uint32_t q = lane >> 4, l15 = lane & 15;
-    const uint32_t wr = wave & 1, wc = wave >> 1;
+    const uint32_t wr = wave % WR, wc = wave / WR;
 
     // Workgroups go to the 8 XCDs in turn: give each XCD a run of neighbouring
     // tiles, four column tiles wide, so that its L2 holds what they share.
@@ -785,45 +800,35 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm(GemmParams p) {
         if constexpr (RK == kCols) r_off[i] = cols_off(i, rt * T, p.r_limit, p.rmat.stride);
     }
     uint8_t *const r_lds = lds, *const c_lds = lds + 4 * STAGE;
-    // Starts the copies of stage s; `between(i)` comes behind the i-th.  Stages behind the last are zeros.
     constexpr int PARTS = COPIES * (RK == kCols ? 2 : 1);
-    auto copy_stage = [&](uint32_t s, auto between) __attribute__((always_inline)) {
-        uint8_t *cd = c_lds + (s & 3) * STAGE + wave * COPIES * 1024;
-        uint8_t *rd = r_lds + (s & 3) * STAGE + wave * COPIES * 1024;
+    // The i-th of a wave's copies of stage s.  Stages behind the last are zeros.
+    auto copy_part = [&](uint32_t s, int i) __attribute__((always_inline)) {
         const uint8_t *cp = static_cast<const uint8_t *>(p.cmat.p);
         if constexpr (CK == kRows) {
             const uint32_t rows = min((uint32_t)T, c_end - c0), bytes = ((rows - 1) * (uint32_t)p.cmat.stride + S * 32) * 2;
             const rsrc_t c = buffer(cp + (uint64_t)c0 * p.cmat.stride * 2 + (uint64_t)s * 64, s < S ? bytes - s * 64 : 0);
-#pragma unroll
-            for (int i = 0; i < COPIES; ++i) {
-                copy_to_lds(c, c_off[i], cd + i * 1024);
-                between(i);
-            }
+            copy_to_lds(c, c_off[i], c_lds + (s & 3) * STAGE + (wave * COPIES + i) * 1024);
         } else {
             const uint32_t a = a0 + s * 32, rows = s < S ? min(32u, a_end - a) : 0;
-            const rsrc_t c = buffer(cp + (uint64_t)a * p.cmat.stride * 2, rows * (uint32_t)p.cmat.stride * 2);
-            const rsrc_t r = buffer(static_cast<const uint8_t *>(p.rmat.p) + (uint64_t)a * p.rmat.stride * 2,
-                                    rows * (uint32_t)p.rmat.stride * 2);
-#pragma unroll
-            for (int i = 0; i < COPIES; ++i) {
-                copy_to_lds(c, c_off[i], cd + i * 1024);
-                between(2 * i);
-                copy_to_lds(r, r_off[i], rd + i * 1024);
-                between(2 * i + 1);
-            }
+            const bool r = i & 1;
+            const Mat &m = r ? p.rmat : p.cmat;
+            const rsrc_t x = buffer(static_cast<const uint8_t *>(m.p) + (uint64_t)a * m.stride * 2, rows * (uint32_t)m.stride * 2);
+            copy_to_lds(x, r ? r_off[i >> 1] : c_off[i >> 1],
+                        (r ? r_lds : c_lds) + (s & 3) * STAGE + (wave * COPIES + (i >> 1)) * 1024);
         }
     };
 
     // ---- packed weights ----
-    // Forward: a block of 64 contraction values is T / 16 tiles, which fill two stages: the wave decodes half of its
-    // tiles in each of two steps.  dx: a stage of 32 weight rows is 2 x T / 64 tiles.
-    Tile t[2][TILES];
-    uint2 hd[2][TILES];
-    auto tile_index = [&](uint32_t n, int i, bool &live) __attribute__((always_inline)) -> uint64_t {  // n: decode step
+    // A wave decodes one tile in each step.  Forward: a block of 64 contraction values is T / 16 tiles, which fill two
+    // stages; decode step n fills half of stages n & ~1 and (n & ~1) + 1.  dx: a stage of 32 weight rows is
+    // 2 x T / 64 tiles; decode step n fills stage n.  In step s: n = s + 3 forward (stage s + 2 is whole after step s,
+    // when s is odd with the one after it), n = s + 2 for dx.  The tile was copied to LDS two steps before.
+    constexpr uint32_t AHEAD = RK == kPacked ? 3 : 2;
+    auto tile_index = [&](uint32_t n, bool &live) __attribute__((always_inline)) -> uint64_t {
         uint32_t rb, kb;
         n = min(n, S - 1);
         if (RK == kPacked) {
-            const uint32_t j = (wave * 2 + (n & 1)) * TILES + i;
+            const uint32_t j = wave * 2 + (n & 1);
             kb = n >> 1;
             if (GATED) {
                 rb = rt * (T / 32) + (j >> 1);
@@ -835,167 +840,177 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm(GemmParams p) {
                 rb = live ? rb + p.row_block0 : 0;
             }
         } else {
-            const uint32_t j = wave * TILES + i;
-            rb = n * 2 + (j & 1);
-            kb = rt * (T / 64) + (j >> 1);
+            rb = n * 2 + (wave & 1);
+            kb = rt * (T / 64) + (wave >> 1);
             live = rb < p.row_blocks && kb < KB;
             rb = live ? rb + p.row_block0 : 0;
             kb = live ? kb : 0;
         }
         return ((uint64_t)g * p.w.row_blocks + rb) * KB + kb;
     };
-    auto load_heads = [&](uint32_t n, int b) __attribute__((always_inline)) {
-        if constexpr (PACKED) {
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                bool live;
-                const uint64_t x = tile_index(n, i, live);
-                hd[b][i] = tile_head(p.w, x);
-            }
-        }
-    };
+    // Headers: lane l holds that of decode step 64 i + l; the next 64 are loaded meanwhile.
     constexpr uint32_t kDead = 1u << 31;  // header flag here: the tile lies outside the weight
-    auto load_tiles = [&](uint32_t n, int b) __attribute__((always_inline)) {
-        if constexpr (PACKED) {
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                bool live;
-                const uint64_t x = tile_index(n, i, live);
-                tile_load(t[b][i], p.w, x, hd[b][i], lane);
-                if (RK == kPackedT && !live) t[b][i].h |= kDead;
-            }
-        }
+    uint4 heads = make_uint4(0, 0, 0, 0), heads_next = heads;
+    auto load_heads = [&](uint32_t n0) __attribute__((always_inline)) -> uint4 {
+        bool live;
+        const uint64_t x = tile_index(n0 + lane, live);
+        uint4 h = tile_head(p.w, x);
+        if (RK == kPackedT && !live) h.x |= kDead;
+        return h;
     };
-    // Places of the two halves of a lane's 16 values; dx: both in one stage.
-    auto tile_place = [&](uint32_t n, int i, uint32_t &s0, uint32_t &at0, uint32_t &s1, uint32_t &at1, uint32_t l) __attribute__((always_inline)) {
+    uint8_t *const slots = lds + 8 * STAGE + wave * 2 * SLOT;
+    auto copy_tile = [&](uint32_t n) __attribute__((always_inline)) {
+        bool live;
+        const rsrc_t r = buffer(p.w.tiles + tile_index(n, live) * kTileBytes, kTileBytes);
+        copy_to_lds(r, lane * 16, slots + (n & 1) * SLOT);
+        copy_to_lds(r, kTileSm + (lane & 31) * 16, slots + (n & 1) * SLOT + kTileSm);  // (the codes twice)
+    };
+    auto read_tile = [&](uint32_t n, Tile &t) __attribute__((always_inline)) {
+        const uint8_t *d = slots + (n & 1) * SLOT;
+        t.sm = *reinterpret_cast<const uint4 *>(d + lane * 16);
+        t.code = *reinterpret_cast<const uint2 *>(d + kTileSm + lane * 8);
+        t.h.x = __builtin_amdgcn_readlane(heads.x, n & 63);
+    };
+    // Places in LDS of the two halves of a lane's 16 values; dx: both in one stage.
+    auto tile_place = [&](uint32_t n, uint32_t l, uint32_t &at0, uint32_t &at1) __attribute__((always_inline)) {
         if (RK == kPacked) {
-            const uint32_t j = (wave * 2 + (n & 1)) * TILES + i;
-            s0 = n & ~1u;
-            s1 = s0 + 1;
-            at0 = at1 = j * 1024 + l * 16;
+            const uint32_t at = (wave * 2 + (n & 1)) * 1024 + l * 16;
+            at0 = (n & 2) * STAGE + at;
+            at1 = at0 + STAGE;
         } else {
-            const uint32_t j = wave * TILES + i, row = (j & 1) * 16 + (l & 15), lq = l >> 4;
-            s0 = s1 = n;
-            at0 = cols_at<T>(row, (j >> 1) * 4 + (lq >> 1)) + (lq & 1) * 16;
-            at1 = cols_at<T>(row, (j >> 1) * 4 + 2 + (lq >> 1)) + (lq & 1) * 16;
+            const uint32_t row = (wave & 1) * 16 + (l & 15), lq = l >> 4;
+            at0 = (n & 3) * STAGE + cols_at<T>(row, (wave >> 1) * 4 + (lq >> 1)) + (lq & 1) * 16;
+            at1 = (n & 3) * STAGE + cols_at<T>(row, (wave >> 1) * 4 + 2 + (lq >> 1)) + (lq & 1) * 16;
         }
     };
-    auto store_tile = [&](uint32_t n, int i, const uint32_t v[8]) __attribute__((always_inline)) {
-        uint32_t s0, s1, at0, at1;
-        tile_place(n, i, s0, at0, s1, at1, lane);
-        *reinterpret_cast<uint4 *>(r_lds + (s0 & 3) * STAGE + at0) = make_uint4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<uint4 *>(r_lds + (s1 & 3) * STAGE + at1) = make_uint4(v[4], v[5], v[6], v[7]);
+    auto store_tile = [&](uint32_t n, const uint32_t v[8]) __attribute__((always_inline)) {
+        uint32_t at0, at1;
+        tile_place(n, lane, at0, at1);
+        *reinterpret_cast<uint4 *>(r_lds + at0) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4 *>(r_lds + at1) = make_uint4(v[4], v[5], v[6], v[7]);
     };
-    // What the plain decode does not cover is put right behind it, from the header and the list entry.
-    struct Mend {
-        uint32_t h, off, ent;
-    };
-    auto decode = [&](uint32_t n, int b, Mend *m) __attribute__((always_inline)) {
-        if constexpr (PACKED) {
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                uint32_t v[8];
-                tile_decode_plain(t[b][i], v);
-                store_tile(n, i, v);
-                m[i] = Mend{t[b][i].h, t[b][i].off, t[b][i].ent};
-            }
+    // What the plain decode does not cover is put right behind it.
+    auto mend = [&](uint32_t n, uint32_t h0) __attribute__((always_inline)) {
+        if ((h0 & (0xFF00u | kTileZero | kDead)) == 0 || n >= S) return;
+        uint32_t at0, at1;
+        if (h0 & kDead) {
+            const uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            store_tile(n, v);
+            return;
+        }
+        Tile t;
+        t.h = make_uint4(h0, __builtin_amdgcn_readlane(heads.y, n & 63), __builtin_amdgcn_readlane(heads.z, n & 63),
+                         __builtin_amdgcn_readlane(heads.w, n & 63));
+        if (tile_special(h0)) {
+            bool live;
+            uint32_t v[8];
+            tile_load(t, p.w, tile_index(n, live), t.h, lane);
+            tile_decode_special(t, p.w, lane, v);
+            store_tile(n, v);
+        }
+        if (lane < tile_listed(h0)) {
+            const uint32_t e = tile_entry(p.w, t.h, lane);
+            tile_place(n, e >> 4 & 63, at0, at1);
+            *reinterpret_cast<uint16_t *>(r_lds + (e & 8 ? at1 : at0) + (e & 7) * 2) = (uint16_t)(e >> 16);
         }
     };
-    auto mend = [&](uint32_t n, const Mend *m) __attribute__((always_inline)) {
-        if constexpr (PACKED) {
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                if ((m[i].h & (0xFF00u | kTileZero | kDead)) == 0) continue;
-                const bool dead = m[i].h & kDead;
-                if (dead || tile_special(m[i].h)) {
-                    uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (!dead) {
-                        bool live;
-                        Tile x;
-                        tile_load(x, p.w, tile_index(n, i, live), make_uint2(m[i].h, m[i].off), lane);
-                        tile_decode_special(x, p.w, lane, v);
-                    }
-                    store_tile(n, i, v);
-                }
-                if (!dead && lane < tile_listed(m[i].h)) {
-                    uint32_t s0, s1, at0, at1;
-                    tile_place(n, i, s0, at0, s1, at1, m[i].ent >> 4 & 63);
-                    const uint32_t at = m[i].ent & 8 ? (s1 & 3) * STAGE + at1 : (s0 & 3) * STAGE + at0;
-                    *reinterpret_cast<uint16_t *>(r_lds + at + (m[i].ent & 7) * 2) = (uint16_t)(m[i].ent >> 16);
-                }
-            }
+    auto next_heads = [&](uint32_t n) __attribute__((always_inline)) {  // before decode step n
+        if ((n & 63) == 0 && n) {
+            heads = heads_next;
+            heads_next = load_heads(n + 64);
         }
     };
 
     // ---- fragments and products ----
-    bf16x8 rf[2][F], cf[2][F];
-    auto read_frags = [&](uint32_t s, int b, int first, int end) __attribute__((always_inline)) {  // of F + F
-        const uint8_t *rl = r_lds + (s & 3) * STAGE, *cl = c_lds + (s & 3) * STAGE;
-#pragma unroll
-        for (int k = first; k < end; ++k) {
-            const int i = k >> 1;
-            if (k & 1) {
-                const uint32_t rr = (wr * F + i) * 16;
-                if constexpr (RK == kPacked)
-                    rf[b][i] = *reinterpret_cast<const bf16x8 *>(rl + rr * 64 + lane * 16);
-                else
-                    rf[b][i] = cols_frag<T>(rl, rr, lane);
-            } else {
-                const uint32_t cc = (wc * F + i) * 16;
-                if constexpr (CK == kCols)
-                    cf[b][i] = cols_frag<T>(cl, cc, lane);
-                else
-                    cf[b][i] = *reinterpret_cast<const bf16x8 *>(cl + rows_at(cc + l15, q));
-            }
-        }
+    bf16x8 rf[FR], cf[2][FC];
+    auto read_r = [&](uint32_t s, int i) __attribute__((always_inline)) {
+        const uint8_t *rl = r_lds + (s & 3) * STAGE;
+        const uint32_t rr = (wr * FR + i) * 16;
+        if constexpr (RK == kPacked)
+            rf[i] = *reinterpret_cast<const bf16x8 *>(rl + rr * 64 + lane * 16);
+        else
+            rf[i] = cols_frag<T>(rl, rr, lane);
     };
-    f32x4 acc[F][F];
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-        for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    auto multiply = [&](int b, int first, int end) __attribute__((always_inline)) {  // of F F products
-#pragma unroll
-        for (int k = first; k < end; ++k) mfma(acc[k / F][k % F], rf[b][k / F], cf[b][k % F]);
+    auto read_c = [&](uint32_t s, int b, int i) __attribute__((always_inline)) {
+        const uint8_t *cl = c_lds + (s & 3) * STAGE;
+        const uint32_t cc = (wc * FC + i) * 16;
+        if constexpr (CK == kCols)
+            cf[b][i] = cols_frag<T>(cl, cc, lane);
+        else
+            cf[b][i] = *reinterpret_cast<const bf16x8 *>(cl + rows_at(cc + l15, q));
     };
+    f32x4 acc[FR][FC];
+#pragma unroll
+    for (int i = 0; i < FR; ++i)
+        for (int j = 0; j < FC; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    // Decode step n fills, forward: half of stages n & ~1 and (n & ~1) + 1; dx: stage n.  In step s: n = s + 3
-    // forward (stage s + 2 is whole after step s, when s is odd with the one after it), n = s + 2 for dx.
-    constexpr uint32_t AHEAD = RK == kPacked ? 3 : 2;
-    constexpr int PER_STEP = COPIES * (RK == kCols ? 2 : 1) + (PACKED ? 3 * TILES : 0);
+    constexpr int PER_STEP = PARTS + (PACKED ? 2 : 0);
     if (S > 0) {
-        Mend m[TILES];
-        for (uint32_t s = 0; s < 3; ++s) copy_stage(s, [](int) {});
         if constexpr (PACKED) {
-            load_heads(0, 0);
-            load_heads(1, 1);
-            load_tiles(0, 0);
-            load_tiles(1, 1);
-            load_heads(2, 0);
+            heads = load_heads(0);
+            heads_next = load_heads(64);
+            copy_tile(0);
+            copy_tile(1);
+        }
+        for (uint32_t s = 0; s < 3; ++s)
 #pragma unroll
+            for (int i = 0; i < PARTS; ++i) copy_part(s, i);
+        if constexpr (PACKED) {
+#pragma unroll 1
             for (uint32_t n = 0; n < AHEAD; ++n) {
-                decode(n, n & 1, m);
-                if (n < S) mend(n, m);
-                load_tiles(n + 2, n & 1);
-                load_heads(n + 3, (n & 1) ^ 1);
+                if (n < 2) wait_copies<0>();
+                if (n == 2) wait_copies<2>();  // (tile 2, whose copy came before tile 3's)
+                Tile t;
+                uint32_t v[8];
+                read_tile(n, t);
+                tile_decode_plain(t, v);
+                store_tile(n, v);
+                mend(n, t.h.x);
+                wait_copies<0>();
+                copy_tile(n + 2);
             }
         }
         wait_copies<0>();
         barrier();
-        read_frags(0, 0, 0, 2 * F);
+#pragma unroll
+        for (int i = 0; i < FR; ++i) read_r(0, i);
+#pragma unroll
+        for (int i = 0; i < FC; ++i) read_c(0, 0, i);
         settle(acc);  // the zeros
         auto step = [&](uint32_t s, auto parity) __attribute__((always_inline)) {
             constexpr int b = decltype(parity)::value;
-            constexpr int tb = (b + AHEAD) & 1;
             const uint32_t n = s + AHEAD;
-            // copies, reads, the decoder and the loads between the matrix instructions, whose shadow hides them
-            copy_stage(s + 3, [&](int i) __attribute__((always_inline)) {
-                read_frags(s + 1, b ^ 1, i * 2 * F / PARTS, (i + 1) * 2 * F / PARTS);
-                if (i == 0) decode(n, tb, m);  // behind the last stage: into stages that nothing reads any more
-                if (i == PARTS - 1) load_tiles(n + 2, tb), load_heads(n + 3, tb ^ 1);
-                multiply(b, i * F * F / PARTS, (i + 1) * F * F / PARTS);
-            });
-            if (PACKED && n < S) mend(n, m);
-            wait_copies<PER_STEP>();  // stage s + 2 has arrived: only this step's copies and loads may be on their way
+            Tile t;
+            uint32_t v[8];
+            if constexpr (PACKED) {
+                next_heads(n);
+                read_tile(n, t);
+            }
+            const uint32_t base = PACKED ? (t.h.x & 0xFF) * 0x00800080u : 0;
+            // between the matrix instructions, whose shadow hides them: copies, reads and the decoder
+#pragma unroll
+            for (int i = 0; i < FR; ++i) {
+                if (i < PARTS) copy_part(s + 3, i);
+                if (i < FC) read_c(s + 1, b ^ 1, i);
+#pragma unroll
+                for (int j = 0; j < FC; ++j) mfma(acc[i][j], rf[i], cf[b][j]);
+                read_r(s + 1, i);
+                if constexpr (PACKED) {
+                    // eight pairs, from the second group of products on
+                    constexpr int GROUPS = FR - 1;
+                    if (i > 0)
+#pragma unroll
+                        for (int k = (i - 1) * 8 / GROUPS; k < i * 8 / GROUPS; ++k)
+                            v[k] = tile_signs(t, k) | (base - tile_codes(t, k));
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (PACKED) {
+                store_tile(n, v);  // behind the last stage: into stages that nothing reads any more
+                copy_tile(n + 2);
+                mend(n, t.h.x);
+            }
+            wait_copies<PER_STEP>();  // stage s + 2 has arrived: only this step's copies may be on their way
             barrier();
         };
         for (uint32_t s = 0; s < S; s += 2) {  // (a step behind an odd number of stages adds zeros)
@@ -1007,19 +1022,19 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm(GemmParams p) {
         settle(acc);
     }
 
-    // ---- epilogues: acc[i][j][d] is row 16 (wr F + i) + 4 q + d of the tile, column 16 (wc F + j) + l15 ----
+    // ---- epilogues: acc[i][j][d] is row 16 (wr FR + i) + 4 q + d of the tile, column 16 (wc FC + j) + l15 ----
     if constexpr (KIND == kGemmLossStat) {
         // every token's largest logit in this tile, and the sum of exp(logit - that)
         f32x2 *red = reinterpret_cast<f32x2 *>(lds);  // [2][T]
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const uint32_t m = c0 + (wc * F + j) * 16 + l15;
+        for (int j = 0; j < FC; ++j) {
+            const uint32_t m = c0 + (wc * FC + j) * 16 + l15;
             const bool live = m < c_end;
             const int64_t want = live ? p.loss.target[m] : -1;
-            const uint32_t n0 = rt * T + wr * F * 16 + q * 4;
+            const uint32_t n0 = rt * T + wr * FR * 16 + q * 4;
             float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < F; ++i)
+            for (int i = 0; i < FR; ++i)
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     const uint32_t n = n0 + i * 16 + d;
@@ -1033,15 +1048,15 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm(GemmParams p) {
             const float ref = fminf(fmaxf(top, -3.0e38f), 3.0e38f);
             float sum = 0;
 #pragma unroll
-            for (int i = 0; i < F; ++i)
+            for (int i = 0; i < FR; ++i)
 #pragma unroll
                 for (int d = 0; d < 4; ++d) sum += __expf(acc[i][j][d] - ref);
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (q == 0) red[wr * T + (wc * F + j) * 16 + l15] = f32x2{ref, sum};
+            if (q == 0) red[wr * T + (wc * FC + j) * 16 + l15] = f32x2{ref, sum};
         }
         __syncthreads();
-        for (uint32_t c = tid; c < T; c += 256) {
+        for (uint32_t c = tid; c < T; c += WAVES * 64) {
             if (c0 + c >= c_end) continue;
             const float ref = fmaxf(red[c][0], red[T + c][0]);
             const float sum = red[c][1] * __expf(red[c][0] - ref) + red[T + c][1] * __expf(red[T + c][0] - ref);
@@ -1050,21 +1065,21 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm(GemmParams p) {
         return;
     }
 
-    // The others go through LDS, 64 columns at a time, so that a column's rows leave in one run: a wave's part is
-    // [columns][16 F] values in units of four, the unit's place xored with the column against bank conflicts.
-    constexpr int UNITS = F * 4;
-    f32x4 *out = reinterpret_cast<f32x4 *>(lds + wave * (2 * STAGE));
+    // The others go through LDS, 16 KiB a wave at a time, so that a column's rows leave in one run: a wave's part is
+    // [columns][16 FR] values in units of four, the unit's place xored with the column against bank conflicts.
+    constexpr int UNITS = FR * 4, JP = 16 / FR;  // fragments of columns at a time
+    f32x4 *out = reinterpret_cast<f32x4 *>(lds + wave * 16384);
 #pragma unroll
-    for (int ph = 0; ph < F; ph += 4) {
+    for (int ph = 0; ph < FC; ph += JP) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < JP; ++j)
 #pragma unroll
-            for (int i = 0; i < F; ++i) out[(j * 16 + l15) * UNITS + ((i * 4 + q) ^ l15)] = acc[i][ph + j];
+            for (int i = 0; i < FR; ++i) out[(j * 16 + l15) * UNITS + ((i * 4 + q) ^ l15)] = acc[i][ph + j];
         constexpr int OUTS = GATED ? UNITS / 2 : UNITS;  // results of a column, in units of four
 #pragma unroll 1
-        for (uint32_t k = lane; k < 64 * OUTS; k += 64) {
+        for (uint32_t k = lane; k < JP * 16 * OUTS; k += 64) {
             const uint32_t cl = k / OUTS, u = k % OUTS;
-            const uint32_t c = c0 + (wc * F + ph) * 16 + cl;  // column
+            const uint32_t c = c0 + (wc * FC + ph) * 16 + cl;  // column
             float v[GATED ? 2 : 1][4];
 #pragma unroll
             for (int h = 0; h < (GATED ? 2 : 1); ++h) {
@@ -1242,7 +1257,7 @@ template <Operand RK, Operand CK, GemmKind KIND, bool GATED>
 hipError_t gemm(uint32_t edge, const GemmParams &p, hipStream_t s) {
     const dim3 grid(p.r_tiles * p.c_tiles, KIND == kGemmDw ? p.groups : 1);
     if (edge == 256)
-        k_gemm<RK, CK, KIND, GATED, 256><<<grid, 256, 0, s>>>(p);
+        k_gemm<RK, CK, KIND, GATED, 256><<<grid, 512, 0, s>>>(p);
     else
         k_gemm<RK, CK, KIND, GATED, 128><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();

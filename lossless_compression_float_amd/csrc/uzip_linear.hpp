@@ -24,15 +24,19 @@ constexpr uint32_t kTileCols = 64;
 constexpr uint32_t kTileBytes = 1536;  // 1024 sign+mantissa bytes, 512 bytes of codes
 constexpr uint32_t kTileSm = 1024;
 constexpr uint32_t kMaxListed = 64;    // one list entry a lane
+constexpr uint32_t kInline = 2;
 constexpr uint32_t kTileRaw = 255;     // count field of a tile that keeps exponent bytes
 constexpr uint32_t kTileZero = 1u << 16;  // code 15 stands for exponent 0
 constexpr uint32_t kWeightHeader = 256;
 constexpr uint32_t kWeightMagic = 0x31575A55u;  // "UZW1"
 constexpr uint32_t kScanTiles = 1024;  // tiles per block of the offset scan
 
-// Tile header word 0: base exponent, count << 8, flags; word 1: offset of the
+// Tile header: word 0: base exponent, count << 8, flags; word 1: offset of the
 // tile's list (u32 entries: position | bits << 16) or exponent bytes, in
-// 16-byte units from the start of the extra region.
+// 16-byte units from the start of the extra region; words 2 and 3: the list's
+// first entries.  A list of up to kInline entries is only there, so that a
+// product hardly ever waits for one: of 1024 normal values 0.05 are listed on
+// average.
 struct WeightLayout {
     uint64_t parts;      // 2 when gated: gate rows, then up rows, each padded to whole tiles
     uint64_t part_rows;  // rows of one part
@@ -40,7 +44,7 @@ struct WeightLayout {
     uint64_t row_blocks;  // of one matrix
     uint64_t col_blocks;
     uint64_t tiles;       // of the whole stack
-    uint64_t head_off;    // 8 bytes a tile
+    uint64_t head_off;    // 16 bytes a tile
     uint64_t tile_off;
     uint64_t extra_off;
     uint64_t max_bytes;
@@ -55,7 +59,7 @@ inline WeightLayout weight_layout(uint64_t matrices, uint64_t rows, uint64_t col
     l.col_blocks = (cols + kTileCols - 1) / kTileCols;
     l.tiles = matrices * l.row_blocks * l.col_blocks;
     l.head_off = kWeightHeader;
-    l.tile_off = (l.head_off + 8 * l.tiles + 255) / 256 * 256;
+    l.tile_off = (l.head_off + 16 * l.tiles + 255) / 256 * 256;
     l.extra_off = l.tile_off + kTileBytes * l.tiles;
     l.max_bytes = l.extra_off + 1024 * l.tiles;
     return l;
@@ -63,7 +67,7 @@ inline WeightLayout weight_layout(uint64_t matrices, uint64_t rows, uint64_t col
 
 // What kernels know of a packed stack.
 struct WeightView {
-    const uint2 *head;
+    const uint4 *head;
     const uint8_t *tiles;
     const uint8_t *extra;
     uint32_t extra_units;  // 16-byte units readable at `extra`

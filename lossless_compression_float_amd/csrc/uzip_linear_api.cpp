@@ -39,7 +39,7 @@ WeightView view(const uzip_weight *w) {
     const WeightLayout l = weight_layout(w->matrices, w->rows, w->cols, w->gated);
     const uint8_t *p = static_cast<const uint8_t *>(w->data);
     WeightView v{};
-    v.head = reinterpret_cast<const uint2 *>(p + l.head_off);
+    v.head = reinterpret_cast<const uint4 *>(p + l.head_off);
     v.tiles = p + l.tile_off;
     v.extra = p + l.extra_off;
     v.extra_units = (uint32_t)std::min<uint64_t>((w->bytes - l.extra_off) / 16, 0xFFFFFFFFu);

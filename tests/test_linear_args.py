@@ -43,7 +43,7 @@ def test_structs_have_the_headers_sizes():
 
 def test_packed_sizes():
     tiles = (4096 // 16) * (14336 // 64)
-    assert uz.uzip_weight_max_size(1, 4096, 14336) == 256 + 8 * tiles + 1536 * tiles + 1024 * tiles
+    assert uz.uzip_weight_max_size(1, 4096, 14336) == 256 + 16 * tiles + 1536 * tiles + 1024 * tiles
     assert uz.uzip_weight_max_size(1, 1, 1) == 512 + 2560
     # halves of 17 rows take two row blocks each, one matrix of 34 rows three
     assert uz.uzip_weight_max_size(3, 34, 65, 1) - 256 >= 3 * 4 * 2 * 2560 > uz.uzip_weight_max_size(3, 34, 65, 0)
