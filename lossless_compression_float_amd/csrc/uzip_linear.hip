@@ -52,13 +52,13 @@ struct Tile {
 
 // A list that would reach behind the extra region is dropped, so that damaged
 // weights cannot make a kernel read out of range.
-__device__ inline uint4 tile_head(const WeightView &w, uint64_t tile) {
-    uint4 h = w.head[tile];
+__device__ inline uint4 head_checked(const WeightView &w, uint4 h) {
     const uint32_t cnt = (h.x >> 8) & 0xFF;
     const uint32_t units = cnt == kTileRaw ? 64 : cnt <= kInline ? 0 : (cnt + 3) / 4;
     if (units > w.extra_units || (units && h.y > w.extra_units - units)) h.x &= ~0xFF00u;
     return h;
 }
+__device__ inline uint4 tile_head(const WeightView &w, uint64_t tile) { return head_checked(w, w.head[tile]); }
 
 __device__ inline void tile_load(Tile &t, const WeightView &w, uint64_t tile, uint4 head, uint32_t lane) {
     const uint8_t *p = w.tiles + tile * kTileBytes;
@@ -88,17 +88,17 @@ __device__ inline void tile_decode_plain(const Tile &t, uint32_t v[8]) {
 // The two kinds of tile for which that is not enough: exponent bytes, and
 // code 15 for exponent 0.
 __device__ inline bool tile_special(uint32_t h) { return (h & kTileZero) || (h >> 8 & 0xFF) == kTileRaw; }
-__device__ inline void tile_decode_special(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
-    if ((t.h.x >> 8 & 0xFF) == kTileRaw) {
-        const uint4 ex = *reinterpret_cast<const uint4 *>(w.extra + (uint64_t)t.h.y * 16 + lane * 16);
-        const uint32_t e[4] = {ex.x, ex.y, ex.z, ex.w};
+__device__ inline bool tile_raw(uint32_t h) { return (h >> 8 & 0xFF) == kTileRaw; }
+__device__ inline void tile_decode_raw(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
+    const uint4 ex = *reinterpret_cast<const uint4 *>(w.extra + (uint64_t)t.h.y * 16 + lane * 16);
+    const uint32_t e[4] = {ex.x, ex.y, ex.z, ex.w};
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const uint32_t x = e[p >> 1] >> (p & 1 ? 16 : 0);
-            v[p] = tile_signs(t, p) | ((x & 0xFF) << 7) | ((x & 0xFF00) << 15);
-        }
-        return;
+    for (int p = 0; p < 8; ++p) {
+        const uint32_t x = e[p >> 1] >> (p & 1 ? 16 : 0);
+        v[p] = tile_signs(t, p) | ((x & 0xFF) << 7) | ((x & 0xFF00) << 15);
     }
+}
+__device__ inline void tile_decode_zero(const Tile &t, uint32_t v[8]) {
     const uint32_t base = (t.h.x & 0xFF) * 0x00800080u;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
@@ -124,7 +124,8 @@ __device__ inline uint32_t tile_entry(const WeightView &w, uint4 h, uint32_t lan
 __device__ inline void tile_decode(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
     tile_decode_plain(t, v);
     if (!(t.h.x & (0xFF00u | kTileZero))) return;
-    if (tile_special(t.h.x)) tile_decode_special(t, w, lane, v);
+    if (tile_raw(t.h.x)) tile_decode_raw(t, w, lane, v);
+    else if (t.h.x & kTileZero) tile_decode_zero(t, v);
     const uint32_t n = tile_listed(t.h.x);
     if (n == 0) return;
     const uint32_t ent = tile_entry(w, t.h, lane);
@@ -627,8 +628,11 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
 enum Operand { kPacked, kPackedT, kRows, kCols };
 
 // Place of 16-byte unit `unit` of row `row` in a stage of [T][32] values (64
-// bytes a row): the xor makes 16 rows cover the 256 bytes of the banks.
-__device__ inline uint32_t rows_at(uint32_t row, uint32_t unit) { return row * 64 + ((unit ^ (row >> 2 & 3)) * 16); }
+// bytes a row): the xor makes 16 rows cover the 256 bytes of the banks, and
+// also rows 0-3 and 12-15 of one unit with rows 4-11 of the next, the lanes
+// that a read of 16 bytes takes together.
+__device__ inline uint32_t rows_swizzle(uint32_t row) { return (0u - (row >> 2)) & 3; }
+__device__ inline uint32_t rows_at(uint32_t row, uint32_t unit) { return row * 64 + ((unit ^ rows_swizzle(row)) * 16); }
 
 // Granule (32 bytes, 16 columns) `g` of contraction row `a` in a stage of
 // [32][T] values that is read transposed.  A transposing read takes four
@@ -670,8 +674,11 @@ __device__ inline rsrc_t buffer(const uint8_t *p, uint32_t bytes) {
 // result registers, and the asm statements around it keep their order.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // (m0 is reserved; it is set here all the same)
-__device__ inline void copy_to_lds(rsrc_t r, uint32_t off, const uint8_t *dst) {
-    const uint32_t at = uniform((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)dst);
+__device__ inline uint32_t lds_address(const uint8_t *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
+}
+__device__ inline void copy_to_lds(rsrc_t r, uint32_t off, uint32_t dst) {
+    const uint32_t at = uniform(dst);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r) : "m0");
 }
 #pragma clang diagnostic pop
@@ -792,7 +799,7 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
         if constexpr (CK == kRows) {
-            const uint32_t row = (wave * COPIES + i) * 16 + (lane >> 2), u = (lane & 3) ^ (row >> 2 & 3);
+            const uint32_t row = (wave * COPIES + i) * 16 + (lane >> 2), u = (lane & 3) ^ rows_swizzle(row);
             c_off[i] = (row * (uint32_t)p.cmat.stride + u * 8) * 2;
         } else {
             c_off[i] = cols_off(i, c0, p.c_limit, p.cmat.stride);
@@ -800,6 +807,7 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
         if constexpr (RK == kCols) r_off[i] = cols_off(i, rt * T, p.r_limit, p.rmat.stride);
     }
     uint8_t *const r_lds = lds, *const c_lds = lds + 4 * STAGE;
+    const uint32_t r_at = lds_address(lds), c_at = r_at + 4 * STAGE;
     constexpr int PARTS = COPIES * (RK == kCols ? 2 : 1);
     // The i-th of a wave's copies of stage s.  Stages behind the last are zeros.
     auto copy_part = [&](uint32_t s, int i) __attribute__((always_inline)) {
@@ -807,14 +815,14 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
         if constexpr (CK == kRows) {
             const uint32_t rows = min((uint32_t)T, c_end - c0), bytes = ((rows - 1) * (uint32_t)p.cmat.stride + S * 32) * 2;
             const rsrc_t c = buffer(cp + (uint64_t)c0 * p.cmat.stride * 2 + (uint64_t)s * 64, s < S ? bytes - s * 64 : 0);
-            copy_to_lds(c, c_off[i], c_lds + (s & 3) * STAGE + (wave * COPIES + i) * 1024);
+            copy_to_lds(c, c_off[i], c_at + (s & 3) * STAGE + (wave * COPIES + i) * 1024);
         } else {
             const uint32_t a = a0 + s * 32, rows = s < S ? min(32u, a_end - a) : 0;
             const bool r = i & 1;
             const Mat &m = r ? p.rmat : p.cmat;
             const rsrc_t x = buffer(static_cast<const uint8_t *>(m.p) + (uint64_t)a * m.stride * 2, rows * (uint32_t)m.stride * 2);
             copy_to_lds(x, r ? r_off[i >> 1] : c_off[i >> 1],
-                        (r ? r_lds : c_lds) + (s & 3) * STAGE + (wave * COPIES + (i >> 1)) * 1024);
+                        (r ? r_at : c_at) + (s & 3) * STAGE + (wave * COPIES + (i >> 1)) * 1024);
         }
     };
 
@@ -853,17 +861,21 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     uint4 heads = make_uint4(0, 0, 0, 0), heads_next = heads;
     auto load_heads = [&](uint32_t n0) __attribute__((always_inline)) -> uint4 {
         bool live;
-        const uint64_t x = tile_index(n0 + lane, live);
-        uint4 h = tile_head(p.w, x);
-        if (RK == kPackedT && !live) h.x |= kDead;
-        return h;
+        return p.w.head[tile_index(n0 + lane, live)];
+    };
+    auto use_heads = [&](uint32_t n0, uint4 h) __attribute__((always_inline)) {
+        bool live;
+        tile_index(n0 + lane, live);
+        heads = head_checked(p.w, h);
+        if (RK == kPackedT && !live) heads.x |= kDead;
     };
     uint8_t *const slots = lds + 8 * STAGE + wave * 2 * SLOT;
+    const uint32_t slots_at = r_at + 8 * STAGE + wave * 2 * SLOT;
     auto copy_tile = [&](uint32_t n) __attribute__((always_inline)) {
         bool live;
         const rsrc_t r = buffer(p.w.tiles + tile_index(n, live) * kTileBytes, kTileBytes);
-        copy_to_lds(r, lane * 16, slots + (n & 1) * SLOT);
-        copy_to_lds(r, kTileSm + (lane & 31) * 16, slots + (n & 1) * SLOT + kTileSm);  // (the codes twice)
+        copy_to_lds(r, lane * 16, slots_at + (n & 1) * SLOT);
+        copy_to_lds(r, kTileSm + (lane & 31) * 16, slots_at + (n & 1) * SLOT + kTileSm);  // (the codes twice)
     };
     auto read_tile = [&](uint32_t n, Tile &t) __attribute__((always_inline)) {
         const uint8_t *d = slots + (n & 1) * SLOT;
@@ -904,8 +916,15 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
         if (tile_special(h0)) {
             bool live;
             uint32_t v[8];
-            tile_load(t, p.w, tile_index(n, live), t.h, lane);
-            tile_decode_special(t, p.w, lane, v);
+            // (each branch uses all that it loads: a load left unused would be waited for in the next step)
+            const uint8_t *d = p.w.tiles + tile_index(n, live) * kTileBytes;
+            t.sm = *reinterpret_cast<const uint4 *>(d + lane * 16);
+            if (tile_raw(h0)) {
+                tile_decode_raw(t, p.w, lane, v);
+            } else {
+                t.code = *reinterpret_cast<const uint2 *>(d + kTileSm + lane * 8);
+                tile_decode_zero(t, v);
+            }
             store_tile(n, v);
         }
         if (lane < tile_listed(h0)) {
@@ -916,20 +935,22 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     };
     auto next_heads = [&](uint32_t n) __attribute__((always_inline)) {  // before decode step n
         if ((n & 63) == 0 && n) {
-            heads = heads_next;
+            use_heads(n, heads_next);
             heads_next = load_heads(n + 64);
         }
     };
 
     // ---- fragments and products ----
-    bf16x8 rf[FR], cf[2][FC];
-    auto read_r = [&](uint32_t s, int i) __attribute__((always_inline)) {
+    // rf[i] is read again behind its products; the last one has two places, so that no read is left for a step's end
+    bf16x8 rf[FR + 1], cf[2][FC];
+    auto place = [](int i, int b) __attribute__((always_inline)) { return i == FR - 1 && b ? FR : i; };
+    auto read_r = [&](uint32_t s, int i, int at) __attribute__((always_inline)) {
         const uint8_t *rl = r_lds + (s & 3) * STAGE;
         const uint32_t rr = (wr * FR + i) * 16;
         if constexpr (RK == kPacked)
-            rf[i] = *reinterpret_cast<const bf16x8 *>(rl + rr * 64 + lane * 16);
+            rf[at] = *reinterpret_cast<const bf16x8 *>(rl + rr * 64 + lane * 16);
         else
-            rf[i] = cols_frag<T>(rl, rr, lane);
+            rf[at] = cols_frag<T>(rl, rr, lane);
     };
     auto read_c = [&](uint32_t s, int b, int i) __attribute__((always_inline)) {
         const uint8_t *cl = c_lds + (s & 3) * STAGE;
@@ -947,7 +968,7 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     constexpr int PER_STEP = PARTS + (PACKED ? 2 : 0);
     if (S > 0) {
         if constexpr (PACKED) {
-            heads = load_heads(0);
+            use_heads(0, load_heads(0));
             heads_next = load_heads(64);
             copy_tile(0);
             copy_tile(1);
@@ -973,7 +994,7 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
         wait_copies<0>();
         barrier();
 #pragma unroll
-        for (int i = 0; i < FR; ++i) read_r(0, i);
+        for (int i = 0; i < FR; ++i) read_r(0, i, i);
 #pragma unroll
         for (int i = 0; i < FC; ++i) read_c(0, 0, i);
         settle(acc);  // the zeros
@@ -992,23 +1013,27 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
             for (int i = 0; i < FR; ++i) {
                 if (i < PARTS) copy_part(s + 3, i);
                 if (i < FC) read_c(s + 1, b ^ 1, i);
+                if (i == FR - 1) {
+                    read_r(s + 1, i, place(i, b ^ 1));
+                    if constexpr (PACKED) {
+                        store_tile(n, v);  // behind the last stage: into stages that nothing reads any more
+                        mend(n, t.h.x);
+                        copy_tile(n + 2);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
 #pragma unroll
-                for (int j = 0; j < FC; ++j) mfma(acc[i][j], rf[i], cf[b][j]);
-                read_r(s + 1, i);
+                for (int j = 0; j < FC; ++j) mfma(acc[i][j], rf[place(i, b)], cf[b][j]);
+                if (i < FR - 1) read_r(s + 1, i, i);
                 if constexpr (PACKED) {
-                    // eight pairs, from the second group of products on
-                    constexpr int GROUPS = FR - 1;
-                    if (i > 0)
+                    // eight pairs, between the first and the last group of products
+                    constexpr int GROUPS = FR - 2;
+                    if (i > 0 && i <= GROUPS)
 #pragma unroll
                         for (int k = (i - 1) * 8 / GROUPS; k < i * 8 / GROUPS; ++k)
                             v[k] = tile_signs(t, k) | (base - tile_codes(t, k));
                 }
                 __builtin_amdgcn_sched_barrier(0);
-            }
-            if constexpr (PACKED) {
-                store_tile(n, v);  // behind the last stage: into stages that nothing reads any more
-                copy_tile(n + 2);
-                mend(n, t.h.x);
             }
             wait_copies<PER_STEP>();  // stage s + 2 has arrived: only this step's copies may be on their way
             barrier();
