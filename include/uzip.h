@@ -396,7 +396,9 @@ typedef struct {
     uint32_t preact_dtype;
 } uzip_linear_args;
 
-/* The workspace depends on sizes, strides, pointers' alignment and types only. */
+/* The workspace depends on sizes, strides, pointers' alignment and types only.
+ * 0: the call needs none (d_workspace may be null), or its arguments are
+ * invalid, which the call itself reports. */
 size_t uzip_linear_workspace_size(const uzip_weight *weight, const uzip_linear_args *args);
 uzip_status uzip_linear(const uzip_weight *weight, const uzip_linear_args *args, void *d_workspace,
                         size_t workspace_bytes, hipStream_t stream);

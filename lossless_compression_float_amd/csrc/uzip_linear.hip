@@ -493,97 +493,119 @@ __device__ inline void group_rows(const int32_t *offsets, uint32_t g, uint32_t t
     if (end < begin) end = begin;
 }
 
+// A run of memory of which `bytes` may be read; reads behind them give zeros.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr uint32_t kRsrcWord3 = 0x00020000u;  // raw 32-bit buffer access on the gfx9 family
+__device__ inline rsrc_t buffer(const uint8_t *p, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t u = (uint64_t)uniform((uint32_t)(a >> 32)) << 32 | uniform((uint32_t)a);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), (short)0, (int)uniform(bytes), (int)kRsrcWord3);
+}
+__device__ inline uint4 read16(rsrc_t r, uint32_t off) {
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ inline uint2 read8(rsrc_t r, uint32_t off) {
+    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+    return make_uint2(v[0], v[1]);
+}
+constexpr uint32_t kNowhere = 0xFFFFFF00u;  // an offset that is behind every buffer
+
 // ---- few rows ---------------------------------------------------------------------
 
 // y = W x for up to 16 MT rows of x at a time.  A workgroup owns RB row blocks
-// of W; its waves split K and add their parts in LDS in a fixed order.  The
-// weights go from memory to the matrix instructions without touching LDS.
-template <int MT, int RB, bool GATED, int NW>
+// of W; its NW waves split K and add their parts in LDS in a fixed order.  The
+// weights go from memory to the matrix instructions without touching LDS, D
+// column blocks ahead.  Headers: lane l of `heads` holds that of the wave's
+// l-th block.  Blocks behind the last are read as zeros, so the loop has no
+// branch but the one for tiles with a list.
+template <int MT, int RB, bool GATED, int NW, int D>
 __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
     __shared__ f32x4 part[NW][RB * MT * 64];
     const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t q = lane >> 4, r = lane & 15;
     uint32_t begin, end;
     group_rows(p.offsets, blockIdx.y, p.tokens, begin, end);
-    const uint32_t KB = p.w.col_blocks;
+    if (begin == end) return;
+    const uint32_t KB = p.w.col_blocks, n = (KB + NW - 1 - wave) / NW;  // blocks of this wave
     uint64_t tile0[RB];
+    rsrc_t rows[RB];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
         uint32_t b = GATED ? blockIdx.x * (RB / 2) + i / 2 : blockIdx.x * RB + i;
         if (b >= p.w.part_blocks) b = p.w.part_blocks - 1;  // computed and dropped
         if (GATED && (i & 1)) b += p.w.part_blocks;
         tile0[i] = ((uint64_t)blockIdx.y * p.w.row_blocks + b) * KB;
+        rows[i] = buffer(p.w.tiles + tile0[i] * kTileBytes, KB * kTileBytes);
     }
     for (uint32_t m0 = begin; m0 < end; m0 += 16 * MT) {
         f32x4 acc[RB][MT];
 #pragma unroll
         for (int i = 0; i < RB; ++i)
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        const uint16_t *xr[MT];
-        bool xv[MT];
+        const uint32_t here = min(end - m0, 16u * MT);
+        const rsrc_t xb = buffer(static_cast<const uint8_t *>(p.x.p) + (uint64_t)m0 * p.x.stride * 2,
+                                 ((here - 1) * (uint32_t)p.x.stride + p.cols) * 2);
+        Tile t[D][RB];
+        uint4 x[D][MT][2];
+        uint4 heads[RB];
+        auto load = [&](uint32_t k, int d) __attribute__((always_inline)) {
+            const uint32_t kb = wave + k * NW;
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            const uint32_t m = m0 + j * 16 + r;
-            xv[j] = m < end;
-            xr[j] = static_cast<const uint16_t *>(p.x.p) + (uint64_t)(xv[j] ? m : begin) * p.x.stride;
-        }
-        Tile t[RB];
-        uint4 hd[RB];
-        uint4 x[MT][2];
-        auto load_x = [&](uint32_t kb) {
-            const uint32_t k = kb * kTileCols + q * 8;
+            for (int i = 0; i < RB; ++i) {
+                const uint32_t at = kb < KB ? kb * kTileBytes : KB * kTileBytes;
+                t[d][i].sm = read16(rows[i], at + lane * 16);
+                t[d][i].code = read8(rows[i], at + kTileSm + lane * 8);
+            }
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
+            for (int j = 0; j < MT; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    x[j][h] = make_uint4(0, 0, 0, 0);
-                    const uint32_t kk = k + h * 32;
-                    if (p.x_vec) {
-                        if (xv[j] && kk < p.cols) x[j][h] = *reinterpret_cast<const uint4 *>(xr[j] + kk);
-                    } else if (xv[j]) {
-                        uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (kk + i < p.cols) u[i >> 1] |= (uint32_t)xr[j][kk + i] << (16 * (i & 1));
-                        x[j][h] = make_uint4(u[0], u[1], u[2], u[3]);
-                    }
+                    const uint32_t c = kb * kTileCols + h * 32 + q * 8, m = j * 16 + r;
+                    x[d][j][h] = read16(xb, m < here && c < p.cols ? (m * (uint32_t)p.x.stride + c) * 2 : kNowhere);
                 }
-            }
         };
-        if (wave < KB) {
-#pragma unroll
-            for (int i = 0; i < RB; ++i) tile_load(t[i], p.w, tile0[i] + wave, tile_head(p.w, tile0[i] + wave), lane);
-            load_x(wave);
-            if (wave + NW < KB)
-#pragma unroll
-                for (int i = 0; i < RB; ++i) hd[i] = tile_head(p.w, tile0[i] + wave + NW);
-        }
-        for (uint32_t kb = wave; kb < KB; kb += NW) {
-            Tile c[RB];
-            uint4 xc[MT][2];
-#pragma unroll
-            for (int i = 0; i < RB; ++i) c[i] = t[i];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) xc[j][0] = x[j][0], xc[j][1] = x[j][1];
-            if (kb + NW < KB) {
-#pragma unroll
-                for (int i = 0; i < RB; ++i) tile_load(t[i], p.w, tile0[i] + kb + NW, hd[i], lane);
-                load_x(kb + NW);
-                if (kb + 2 * NW < KB)
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) hd[i] = tile_head(p.w, tile0[i] + kb + 2 * NW);
-            }
+        auto multiply = [&](uint32_t k, int d) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 uint32_t v[8];
-                tile_decode(c[i], p.w, lane, v);
+                t[d][i].h.x = __builtin_amdgcn_readlane(heads[i].x, k & 63);
+                tile_decode_plain(t[d][i], v);
+                if (t[d][i].h.x & (0xFF00u | kTileZero)) {
+                    t[d][i].h.y = __builtin_amdgcn_readlane(heads[i].y, k & 63);
+                    t[d][i].h.z = __builtin_amdgcn_readlane(heads[i].z, k & 63);
+                    t[d][i].h.w = __builtin_amdgcn_readlane(heads[i].w, k & 63);
+                    tile_decode(t[d][i], p.w, lane, v);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, xc[j][h]),
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, x[d][j][h]),
                                                                             acc[i][j], 0, 0, 0);
+                }
+            }
+        };
+        auto load_heads = [&](uint32_t k0) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i) heads[i] = p.w.head[tile0[i] + min(wave + (k0 + lane) * NW, KB - 1)];
+        };
+        load_heads(0);  // (first: loads come back in order)
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(d, d);
+        for (uint32_t k0 = 0; k0 < n; k0 += 64) {
+            if (k0) load_heads(k0);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                heads[i] = head_checked(p.w, heads[i]);
+                if (wave + (k0 + lane) * NW >= KB) heads[i].x = 0;
+            }
+            for (uint32_t k = k0; k < min(n, k0 + 64); k += D) {  // (64 is a multiple of D)
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    multiply(k + d, d);
+                    load(k + d + D, d);
                 }
             }
         }
@@ -660,14 +682,6 @@ __device__ inline bf16x8 cols_frag(const uint8_t *lds, uint32_t c0, uint32_t lan
     return __builtin_bit_cast(bf16x8, x);
 }
 
-// A run of memory of which `bytes` may be read; reads behind them give zeros.
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-constexpr uint32_t kRsrcWord3 = 0x00020000u;  // raw 32-bit buffer access on the gfx9 family
-__device__ inline rsrc_t buffer(const uint8_t *p, uint32_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const uint64_t u = (uint64_t)uniform((uint32_t)(a >> 32)) << 32 | uniform((uint32_t)a);
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), (short)0, (int)uniform(bytes), (int)kRsrcWord3);
-}
 // 16 bytes a lane from memory straight to LDS, at `dst` + 16 lane.  In asm, so
 // that the compiler does not wait for it before the next read of LDS: the
 // kernel's own waits and barriers say when the bytes are there.  It has no
@@ -789,7 +803,6 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     // ---- copies from memory ----
     // Rows: a copy takes 16 rows.  Cols: 1 KiB of the stage's rows.  What lies behind the last row or column is read
     // as zeros.
-    constexpr uint32_t kNowhere = 0xFFFFFF00u;
     uint32_t c_off[COPIES], r_off[RK == kCols ? COPIES : 1];
     auto cols_off = [&](int i, uint32_t x0, uint32_t limit, uint64_t stride) __attribute__((always_inline)) -> uint32_t {
         const uint32_t j = (wave * COPIES + i) * 64 + lane, a = j / (T / 8), u = j % (T / 8);
@@ -1270,11 +1283,11 @@ __global__ __launch_bounds__(256) void k_dbias(DzParams p) {
         static_cast<uint16_t *>(p.dbias)[o] = to_bf16(s);
 }
 
-template <int MT, int RB, bool GATED, int NW>
+template <int MT, int RB, bool GATED, int NW, int D>
 hipError_t skinny(const SkinnyParams &p, hipStream_t s) {
     const uint32_t per = GATED ? RB / 2 : RB;
     const dim3 grid((p.w.part_blocks + per - 1) / per, p.groups);
-    k_skinny<MT, RB, GATED, NW><<<grid, NW * 64, 0, s>>>(p);
+    k_skinny<MT, RB, GATED, NW, D><<<grid, NW * 64, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -1315,14 +1328,19 @@ hipError_t launch_stage(const uint16_t *in, uint64_t in_stride, uint16_t *out, u
 
 bool skinny_fits(uint64_t tokens, uint64_t groups) { return groups == 1 ? tokens <= 64 : tokens <= 16 * groups; }
 
+// Waves and row blocks of a workgroup: with rows enough to fill the chip, few
+// waves that share their reads of x (4096 x 4096 over 13 experts: 62 us, 5.3
+// TB/s, against 84 us with one row block and 16 waves); with fewer rows, many
+// waves, for the bytes in flight (one 4096 x 4096 matrix: 8.3 against 12.0 us).
 hipError_t launch_skinny(const SkinnyParams &p, hipStream_t s) {
     const bool one = p.groups > 1 || p.tokens <= 16;
+    const uint64_t blocks = (uint64_t)p.w.part_blocks * p.groups;
     if (p.lin.act == kActSwiglu) {
-        if (one) return skinny<1, 2, true, 8>(p, s);
-        return p.tokens <= 32 ? skinny<2, 2, true, 8>(p, s) : skinny<4, 2, true, 8>(p, s);
+        if (one) return blocks >= 512 ? skinny<1, 4, true, 4, 1>(p, s) : skinny<1, 2, true, 8, 1>(p, s);
+        return p.tokens <= 32 ? skinny<2, 2, true, 8, 2>(p, s) : skinny<4, 2, true, 8, 1>(p, s);
     }
-    if (one) return skinny<1, 1, false, 16>(p, s);
-    return p.tokens <= 32 ? skinny<2, 1, false, 16>(p, s) : skinny<4, 2, false, 8>(p, s);
+    if (one) return blocks >= 1024 ? skinny<1, 2, false, 8, 1>(p, s) : skinny<1, 1, false, 16, 1>(p, s);
+    return p.tokens <= 32 ? skinny<2, 1, false, 16, 2>(p, s) : skinny<4, 2, false, 8, 1>(p, s);
 }
 
 uint32_t gemm_edge(uint64_t r, uint64_t c, uint64_t groups) {

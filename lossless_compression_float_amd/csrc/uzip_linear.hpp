@@ -156,7 +156,6 @@ struct SkinnyParams {
     Mat x;
     const int32_t *offsets;
     uint32_t groups, tokens, rows, cols;
-    uint32_t x_vec;  // rows of x can be read 16 bytes at a time
     LinearEpi lin;
 };
 

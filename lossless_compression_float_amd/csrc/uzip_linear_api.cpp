@@ -81,10 +81,10 @@ struct Carver {
         used += up(n * sizeof(T), kAlign);
         return reinterpret_cast<T *>(p);
     }
-    uint64_t bytes() const { return used + kAlign; }  // slack: the caller's pointer need only be 16-byte aligned
+    uint64_t bytes() const { return used ? used + kAlign : 0; }  // slack: the caller's pointer need only be 16-byte aligned
 };
 
-bool workspace_ok(void *ws, uint64_t have, uint64_t need) { return ws && aligned(ws, 16) && have >= need; }
+bool workspace_ok(void *ws, uint64_t have, uint64_t need) { return need == 0 || (ws && aligned(ws, 16) && have >= need); }
 
 uzip_status done(hipError_t e) { return e == hipSuccess ? UZIP_OK : UZIP_ERR_DEVICE; }
 
@@ -138,7 +138,7 @@ LinearPlan plan_linear(const uzip_weight *w, const uzip_linear_args *a, Carver &
     LinearPlan p{};
     const uint64_t groups = a->offsets ? w->matrices : 1;
     p.skinny = skinny_fits(a->tokens, groups);
-    p.stage = !p.skinny && !tiled64(a->x, a->x_stride, w->cols);
+    p.stage = !(p.skinny ? tiled(a->x, a->x_stride, w->cols) : tiled64(a->x, a->x_stride, w->cols));
     if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 64));
     return p;
 }
@@ -150,25 +150,24 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
     if (a->tokens == 0) return UZIP_OK;
     const bool grouped = a->offsets != nullptr;
     const uint32_t groups = grouped ? (uint32_t)w->matrices : 1;
-    if (plan.skinny) {
-        SkinnyParams p{};
-        p.w = view(w);
-        p.x = Mat{a->x, a->x_stride};
-        p.offsets = a->offsets;
-        p.groups = groups;
-        p.tokens = (uint32_t)a->tokens;
-        p.rows = (uint32_t)w->rows;
-        p.cols = (uint32_t)w->cols;
-        p.x_vec = by16(a->x, a->x_stride, w->cols);
-        p.lin = linear_epi(w, a);
-        return done(launch_skinny(p, stream));
-    }
     Mat x{a->x, a->x_stride};
     if (plan.stage) {
         x = Mat{plan.x, up(w->cols, 64)};
         const hipError_t e = launch_stage(static_cast<const uint16_t *>(a->x), a->x_stride, plan.x, x.stride, a->tokens,
                                           w->cols, stream);
         if (e != hipSuccess) return UZIP_ERR_DEVICE;
+    }
+    if (plan.skinny) {
+        SkinnyParams p{};
+        p.w = view(w);
+        p.x = x;
+        p.offsets = a->offsets;
+        p.groups = groups;
+        p.tokens = (uint32_t)a->tokens;
+        p.rows = (uint32_t)w->rows;
+        p.cols = (uint32_t)up(w->cols, 8);
+        p.lin = linear_epi(w, a);
+        return done(launch_skinny(p, stream));
     }
     GemmParams p{};
     p.w = view(w);

@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from . import (UZIP_BF16, UZIP_FP32, _check, _keep_for, _stream, lib, workspace)
+from . import (UZIP_BF16, UZIP_FP32, UZIP_OK, _check, _keep_for, _stream, lib, workspace)
 
 _vp, _sz, _u32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int64
 
@@ -143,6 +143,8 @@ class PackedWeight:
     [matrices, rows, cols]."""
 
     def __init__(self, data: torch.Tensor, shape, gated: bool):
+        if not isinstance(data, torch.Tensor) or data.dtype is not torch.uint8 or not data.is_contiguous():
+            raise TypeError("a PackedWeight's data is a contiguous uint8 tensor")
         self.data = data
         self.shape = torch.Size(shape)
         self.gated = bool(gated)
@@ -160,13 +162,17 @@ class PackedWeight:
                                                                           self.device)
 
 
-def _no_guard():
-    return contextlib.nullcontext()
+_here = contextlib.nullcontext()
 
 
 def _on(device):
     """Makes `device` current for a launch when it is not already."""
-    return _no_guard() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _stream_of(stream, device) -> int:
+    """The stream's handle; without one that of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else int(stream.cuda_stream)
 
 
 def _code(t: torch.dtype, what: str) -> int:
@@ -228,19 +234,21 @@ def _tokens(x, what: str) -> int:
     return x.shape[0]
 
 
-def _ws(ws, need: int, device):
-    """The caller's workspace, or a new one: nothing is shared between calls."""
+def _call(name: str, fn, size, w, a, ws, stream, *outputs):
+    """Calls `fn` with the caller's workspace or a new one: nothing is shared
+    between calls."""
+    ref, device = ctypes.byref(a), w.device
     if ws is None:
-        return workspace(need, device)
-    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
+        need = size(w._ref, ref)
+        ws = workspace(need, device) if need else None
+    elif ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on %s" % device)
-    return ws
-
-
-def _size(n: int, what: str) -> int:
-    if n == 0:
-        raise ValueError("%s: arguments beyond the limits of one call" % what)
-    return n
+    st = fn(w._ref, ref, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+            _stream_of(stream, device))
+    if st != UZIP_OK:
+        _check(st, "uzip_" + name)
+    if stream is not None:
+        _keep_for(stream, *[t for t in (ws, *outputs) if t is not None])
 
 
 def pack_weight(w: torch.Tensor, gated: bool = False, trim: bool = True, stream=None) -> PackedWeight:
@@ -297,48 +305,40 @@ def _forward(what, w, x, offsets, bias, act, residual, out_dtype, return_preact,
     grouped = what == "grouped_linear"
     w = _weight(w, what, 3 if grouped else 2)
     L = _lib()
-    device, rows, cols = w.device, w.shape[-2], w.shape[-1]
+    device, (rows, cols) = w.device, w.shape[-2:]
     tokens = _tokens(x, "x")
-    a = uzip_linear_args()
-    a.x_stride = _matrix(x, "x", tokens, cols, device)
-    a.x, a.tokens, a.act = x.data_ptr(), tokens, _act(act, w)
-    if grouped:
-        a.offsets = _offsets(offsets, w)
+    x_stride = _matrix(x, "x", tokens, cols, device)
+    act = _act(act, w)
+    off = _offsets(offsets, w) if grouped else None
     width = rows // 2 if w.gated else rows
-    if out is not None:
-        out_dtype = out.dtype if out_dtype is None else out_dtype
-    elif out_dtype is None:
-        out_dtype = torch.bfloat16
-    a.y_dtype = _code(out_dtype, "out_dtype")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    y_code = _code(out_dtype, "out_dtype")
+    b = b_code = r = r_stride = 0
     if bias is not None:
-        shape = (w.shape[0], rows) if grouped else (rows,)
         if not isinstance(bias, torch.Tensor):
             raise TypeError("bias must be a tensor, not %s" % type(bias).__name__)
-        a.bias_dtype = _code(bias.dtype, "bias")
-        if bias.shape != shape or bias.device != device or not bias.is_contiguous():
-            raise ValueError("bias must be contiguous of shape %s on %s" % (list(shape), device))
-        a.bias = bias.data_ptr()
+        b_code = _code(bias.dtype, "bias")
+        if bias.shape != ((w.shape[0], rows) if grouped else (rows,)) or bias.device != device or not bias.is_contiguous():
+            raise ValueError("bias must be contiguous of shape %s on %s" % ([w.shape[0], rows] if grouped else [rows], device))
+        b = bias.data_ptr()
     if residual is not None:
-        a.residual_stride = _matrix(residual, "residual", tokens, width, device, out_dtype)
-        a.residual = residual.data_ptr()
+        r_stride = _matrix(residual, "residual", tokens, width, device, out_dtype)
+        r = residual.data_ptr()
+    z_code = _code(preact_dtype, "preact_dtype") if return_preact else 0
     with _on(device):
         if out is None:
             # rows of no group keep what the output holds: a new output starts with zeros there
             out = (torch.zeros if grouped else torch.empty)((tokens, width), dtype=out_dtype, device=device)
-        a.y_stride = _matrix(out, "out", tokens, width, device, out_dtype)
-        a.y = out.data_ptr()
-        z = None
-        if return_preact:
-            a.preact_dtype = _code(preact_dtype, "preact_dtype")
-            z = torch.empty((tokens, rows), dtype=preact_dtype, device=device)
-            a.preact, a.preact_stride = z.data_ptr(), rows
-        if tokens == 0:
-            return (out, z) if return_preact else out
-        ref = ctypes.byref(a)
-        ws = _ws(ws, _size(L.uzip_linear_workspace_size(w._ref, ref), what), device)
-        fn = L.uzip_grouped_linear if grouped else L.uzip_linear
-        _check(fn(w._ref, ref, ws.data_ptr(), ws.numel(), _stream(stream)), "uzip_" + what)
-        _keep_for(stream, out, ws, *([z] if z is not None else []))
+            y_stride = width
+        else:
+            y_stride = _matrix(out, "out", tokens, width, device, out_dtype)
+        z = torch.empty((tokens, rows), dtype=preact_dtype, device=device) if return_preact else None
+        if tokens:
+            a = uzip_linear_args(x.data_ptr(), x_stride, tokens, off, b, r, r_stride, out.data_ptr(), y_stride,
+                                 z.data_ptr() if return_preact else 0, rows, b_code, y_code, act, z_code)
+            _call(what, L.uzip_grouped_linear if grouped else L.uzip_linear, L.uzip_linear_workspace_size, w, a, ws, stream,
+                  out, z)
     return (out, z) if return_preact else out
 
 
@@ -369,12 +369,11 @@ def _backward(what, w, dy, x, offsets, preact, act, need_x, need_weight, need_bi
     grouped = what == "grouped_linear_backward"
     w = _weight(w, what, 3 if grouped else 2)
     L = _lib()
-    device, rows, cols = w.device, w.shape[-2], w.shape[-1]
+    device, (rows, cols) = w.device, w.shape[-2:]
     tokens = _tokens(dy, "dy")
-    width = rows // 2 if w.gated else rows
     a = uzip_linear_backward_args()
     a.act, a.tokens, a.dy_dtype = _act(act, w), tokens, _code(dy.dtype, "dy")
-    a.dy_stride, a.dy = _matrix(dy, "dy", tokens, width, device, dy.dtype), dy.data_ptr()
+    a.dy_stride, a.dy = _matrix(dy, "dy", tokens, rows // 2 if w.gated else rows, device, dy.dtype), dy.data_ptr()
     if act != "none":
         if preact is None:
             raise ValueError("%s needs the pre-activation for %s (return_preact=True)" % (what, act))
@@ -391,16 +390,13 @@ def _backward(what, w, dy, x, offsets, preact, act, need_x, need_weight, need_bi
             dx = (torch.zeros if grouped else torch.empty)((tokens, cols), dtype=torch.bfloat16, device=device)
             a.dx, a.dx_stride = dx.data_ptr(), cols
         if need_weight:
-            dw = torch.empty(tuple(w.shape), dtype=torch.bfloat16, device=device)
+            dw = torch.empty(w.shape, dtype=torch.bfloat16, device=device)
             a.dw = dw.data_ptr()
         if need_bias:
             db = torch.empty((w.shape[0], rows) if grouped else (rows,), dtype=bias_dtype, device=device)
             a.dbias, a.dbias_dtype = db.data_ptr(), code
-        ref = ctypes.byref(a)
-        ws = _ws(ws, _size(L.uzip_linear_backward_workspace_size(w._ref, ref), what), device)
-        fn = L.uzip_grouped_linear_backward if grouped else L.uzip_linear_backward
-        _check(fn(w._ref, ref, ws.data_ptr(), ws.numel(), _stream(stream)), "uzip_" + what)
-        _keep_for(stream, ws, *[t for t in (dx, dw, db) if t is not None])
+        _call(what, L.uzip_grouped_linear_backward if grouped else L.uzip_linear_backward,
+              L.uzip_linear_backward_workspace_size, w, a, ws, stream, dx, dw, db)
     return dx, dw, db
 
 
@@ -451,14 +447,10 @@ def linear_cross_entropy(x, weight: PackedWeight, target, ignore_index: int = -1
     with _on(device):
         loss = torch.empty(tokens, dtype=torch.float32, device=device)
         lse = torch.empty(tokens, dtype=torch.float32, device=device)
-        if tokens == 0:
-            return loss, lse
-        a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
-        ref = ctypes.byref(a)
-        ws = _ws(ws, _size(L.uzip_linear_cross_entropy_workspace_size(w._ref, ref), "linear_cross_entropy"), device)
-        _check(L.uzip_linear_cross_entropy(w._ref, ref, ws.data_ptr(), ws.numel(), _stream(stream)),
-               "uzip_linear_cross_entropy")
-        _keep_for(stream, loss, lse, ws)
+        if tokens:
+            a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
+            _call("linear_cross_entropy", L.uzip_linear_cross_entropy, L.uzip_linear_cross_entropy_workspace_size, w, a, ws,
+                  stream, loss, lse)
     return loss, lse
 
 
@@ -476,12 +468,8 @@ def linear_cross_entropy_backward(dloss, x, weight: PackedWeight, target, lse, i
             dx = torch.empty((tokens, w.shape[1]), dtype=torch.bfloat16, device=device)
             a.dx, a.dx_stride = dx.data_ptr(), w.shape[1]
         if need_weight:
-            dw = torch.empty(tuple(w.shape), dtype=torch.bfloat16, device=device)
+            dw = torch.empty(w.shape, dtype=torch.bfloat16, device=device)
             a.dw = dw.data_ptr()
-        ref = ctypes.byref(a)
-        ws = _ws(ws, _size(L.uzip_linear_cross_entropy_backward_workspace_size(w._ref, ref),
-                           "linear_cross_entropy_backward"), device)
-        _check(L.uzip_linear_cross_entropy_backward(w._ref, ref, ws.data_ptr(), ws.numel(), _stream(stream)),
-               "uzip_linear_cross_entropy_backward")
-        _keep_for(stream, ws, *[t for t in (dx, dw) if t is not None])
+        _call("linear_cross_entropy_backward", L.uzip_linear_cross_entropy_backward,
+              L.uzip_linear_cross_entropy_backward_workspace_size, w, a, ws, stream, dx, dw)
     return dx, dw

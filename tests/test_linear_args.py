@@ -78,11 +78,13 @@ def test_linear_argument_errors(grouped):
     fn = uz.uzip_grouped_linear if grouped else uz.uzip_linear
     w = weight(matrices=3) if grouped else weight()
     off = dict(offsets=FAKE) if grouped else {}
-    need = uz.uzip_linear_workspace_size(w, linear_args(**off))
+    assert uz.uzip_linear_workspace_size(w, linear_args(**off)) == 0  # few rows: no workspace
+    many = linear_args(tokens=5000, x_stride=65, **off)
+    need = uz.uzip_linear_workspace_size(w, many)
     assert need > 0
-    assert fn(w, linear_args(**off), FAKE, need - 1, None) == INVALID
-    assert fn(w, linear_args(**off), None, need, None) == INVALID
-    assert fn(w, linear_args(**off), FAKE + 4, need, None) == INVALID
+    assert fn(w, many, FAKE, need - 1, None) == INVALID
+    assert fn(w, many, None, need, None) == INVALID
+    assert fn(w, many, FAKE + 4, need, None) == INVALID
     for b in bad_weights():
         assert fn(b, linear_args(**off), FAKE, 1 << 30, None) == INVALID
         assert uz.uzip_linear_workspace_size(b, linear_args(**off)) == 0
