@@ -375,7 +375,7 @@ uzip_status uzip_weight_unpack(const uzip_weight *weight, void *d_out, size_t ro
  * of the size of dz's own rounding to the gradients).
  * offsets (grouped only): matrices + 1 ascending int32 row numbers in device
  * memory; matrix g takes rows offsets[g] .. offsets[g+1] - 1 of x, y and
- * preact, and rows of no group are left as they were.  Offsets outside
+ * preact, and rows of no group are left as they were (see clear_rest).  Offsets outside
  * [0, tokens] are clamped, a descending pair is an empty group; overlapping
  * groups are not supported. */
 typedef struct {
@@ -394,6 +394,8 @@ typedef struct {
     uint32_t y_dtype;
     uint32_t act;        /* uzip_act */
     uint32_t preact_dtype;
+    uint32_t clear_rest; /* grouped: 1 writes zeros to y in the rows of no group */
+    uint32_t reserved;   /* 0 */
 } uzip_linear_args;
 
 /* The workspace depends on sizes, strides, pointers' alignment and types only.
@@ -431,6 +433,8 @@ typedef struct {
     uint32_t dbias_dtype;
     uint32_t act;
     uint32_t preact_dtype;
+    uint32_t clear_rest; /* grouped: 1 writes zeros to dx in the rows of no group */
+    uint32_t reserved;   /* 0 */
 } uzip_linear_backward_args;
 
 size_t uzip_linear_backward_workspace_size(const uzip_weight *weight, const uzip_linear_backward_args *args);

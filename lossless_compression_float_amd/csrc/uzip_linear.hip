@@ -511,6 +511,25 @@ __device__ inline uint2 read8(rsrc_t r, uint32_t off) {
 }
 constexpr uint32_t kNowhere = 0xFFFFFF00u;  // an offset that is behind every buffer
 
+// Zeros in columns [c0, c1) of the rows before the first group and behind the
+// last (all of a workgroup's threads together).
+__device__ inline void clear_rest(const int32_t *offsets, uint32_t groups, uint32_t tokens, void *out, uint64_t stride,
+                                  uint32_t elem, uint32_t c0, uint32_t c1, uint32_t threads) {
+    uint32_t first, last, unused;
+    group_rows(offsets, 0, tokens, first, unused);
+    const int32_t e = offsets[groups];
+    last = max(first, e < 0 ? 0u : min((uint32_t)e, tokens));
+    const uint32_t rest = first + (tokens - last), wide = c1 - c0;
+    for (uint64_t i = threadIdx.x; i < (uint64_t)rest * wide; i += threads) {
+        const uint32_t r = (uint32_t)(i / wide), row = r < first ? r : last + (r - first);
+        const uint64_t at = (uint64_t)row * stride + c0 + (uint32_t)(i % wide);
+        if (elem == 4)
+            static_cast<uint32_t *>(out)[at] = 0;
+        else
+            static_cast<uint16_t *>(out)[at] = 0;
+    }
+}
+
 // ---- few rows ---------------------------------------------------------------------
 
 // y = W x for up to 16 MT rows of x at a time.  A workgroup owns RB row blocks
@@ -526,6 +545,12 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
     const uint32_t q = lane >> 4, r = lane & 15;
     uint32_t begin, end;
     group_rows(p.offsets, blockIdx.y, p.tokens, begin, end);
+    if (p.lin.clear && blockIdx.y == 0) {
+        constexpr uint32_t WIDE = (GATED ? RB / 2 : RB) * 16;
+        const uint32_t c = min(blockIdx.x * WIDE, p.w.part_rows);
+        clear_rest(p.offsets, p.groups, p.tokens, p.lin.y, p.lin.y_stride, p.lin.y_f32 ? 4 : 2, c,
+                   min(c + WIDE, p.w.part_rows), NW * 64);
+    }
     if (begin == end) return;
     const uint32_t KB = p.w.col_blocks, n = (KB + NW - 1 - wave) / NW;  // blocks of this wave
     uint64_t tile0[RB];
@@ -791,6 +816,14 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
         c0 = ct * T;
         c_end = p.c_limit;
     } else {
+        if ((KIND == kGemmForward || KIND == kGemmDx) && ct == 0) {
+            constexpr bool F = KIND == kGemmForward;
+            if (F ? p.lin.clear : p.store.clear) {
+                const uint32_t wide = GATED ? T / 2 : T, limit = F ? p.w.part_rows : p.cols, c = min(rt * wide, limit);
+                clear_rest(p.offsets, p.groups, p.tokens, F ? p.lin.y : p.store.out, F ? p.lin.y_stride : p.store.stride,
+                           F && p.lin.y_f32 ? 4 : 2, c, min(c + wide, limit), WAVES * 64);
+            }
+        }
         if (!find_group(p, ct, T, lane, g, c0, c_end)) return;
         g = uniform(g);
         c0 = uniform(c0);
@@ -1204,13 +1237,29 @@ __global__ __launch_bounds__(256) void k_loss_join(LossEpi e, float *loss, float
 
 // ---- the pre-activation's gradient --------------------------------------------------
 
-__device__ inline float read1(const void *p, uint64_t at, bool f32) {
-    return f32 ? static_cast<const float *>(p)[at] : from_bf16(static_cast<const uint16_t *>(p)[at]);
+// Eight consecutive values, those from `count` on as zeros.
+__device__ inline void read8v(const void *p, uint64_t at, bool f32, bool vec, uint32_t count, float v[8]) {
+    if (vec && count == 8) {
+        if (f32) {
+            const f32x4 *s = reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + at);
+            const f32x4 a = s[0], b = s[1];
+            for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
+            v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+            v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+        }
+        return;
+    }
+    for (uint32_t i = 0; i < 8; ++i)
+        v[i] = i >= count ? 0.0f
+               : f32      ? static_cast<const float *>(p)[at + i]
+                          : from_bf16(static_cast<const uint16_t *>(p)[at + i]);
 }
 
 // dz = dy act'(z) in the padded column order of the packed rows, and the sums
 // of its columns over a run of the group's rows, from the unrounded values.
-// A thread takes eight columns (of both halves when gated).
+// A thread takes eight columns (of both halves when gated).  Bound by memory.
 template <bool GATED>
 __global__ __launch_bounds__(256) void k_dz(DzParams p) {
     constexpr int H = GATED ? 2 : 1;
@@ -1224,28 +1273,28 @@ __global__ __launch_bounds__(256) void k_dz(DzParams p) {
     // columns behind the last part only hold zeros
     const bool tail = GATED && c >= p.part_pad;
     const uint32_t at = tail ? c + p.part_pad : c;
+    const uint32_t count = tail || c >= p.part_rows ? 0 : min(8u, p.part_rows - c);
     float sum[H][8];
 #pragma unroll
     for (int h = 0; h < H; ++h)
         for (int i = 0; i < 8; ++i) sum[h][i] = 0;
     if (at < p.width) {
+#pragma unroll 2
         for (uint32_t m = m0 + wave; m < m1; m += 4) {
-            float v[H][8];
+            float v[H][8], z[H][8], dy[8];
+            read8v(p.dy, m * p.dy_stride + c, p.dy_f32, p.vec, count, dy);
+            if (GATED || p.act != kActNone)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    read8v(p.z, m * p.z_stride + (uint64_t)h * p.part_rows + c, p.z_f32, p.vec, count, z[h]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool live = !tail && c + i < p.part_rows;
-                const float dy = live ? read1(p.dy, m * p.dy_stride + c + i, p.dy_f32) : 0.0f;
-                const uint64_t z = m * p.z_stride + c + i;
                 if (GATED) {
-                    const float a = live ? read1(p.z, z, p.z_f32) : 0.0f;
-                    const float b = live ? read1(p.z, z + p.part_rows, p.z_f32) : 0.0f;
-                    const float s = sigmoid(a);
-                    v[0][i] = live ? dy * b * s * (1.0f + a * (1.0f - s)) : 0.0f;
-                    v[H - 1][i] = live ? dy * a * s : 0.0f;
+                    const float a = z[0][i], b = z[H - 1][i], s = sigmoid(a);
+                    v[0][i] = dy[i] * b * s * (1.0f + a * (1.0f - s));
+                    v[H - 1][i] = dy[i] * a * s;
                 } else {
-                    v[0][i] = dy;
-                    if (p.act != kActNone && live)
-                        v[0][i] = dy * activate_grad(read1(p.z, z, p.z_f32), p.act);
+                    v[0][i] = p.act != kActNone ? dy[i] * activate_grad(z[0][i], p.act) : dy[i];
                 }
             }
 #pragma unroll
@@ -1270,12 +1319,22 @@ __global__ __launch_bounds__(256) void k_dz(DzParams p) {
             out[at + h * p.part_pad + i] = ((sum[h][i] + red[0][h][lane][i]) + red[1][h][lane][i]) + red[2][h][lane][i];
 }
 
+// The runs' sums, in a fixed order: a wave takes every fourth.
 __global__ __launch_bounds__(256) void k_dbias(DzParams p) {
-    const uint32_t n = blockIdx.x * 256 + threadIdx.x, g = blockIdx.y;
-    if (n >= p.part_rows * p.parts) return;
+    __shared__ float red[4][64];
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = blockIdx.y;
+    const uint32_t n = blockIdx.x * 64 + lane;
+    const bool live = n < p.part_rows * p.parts;
     const uint32_t part = n / p.part_rows, at = part * p.part_pad + n - part * p.part_rows;
+    const float *src = p.colsum + (uint64_t)g * p.chunks * p.width + at;
     float s = 0;
-    for (uint32_t i = 0; i < p.chunks; ++i) s += p.colsum[((uint64_t)g * p.chunks + i) * p.width + at];
+    if (live)
+#pragma unroll 4
+        for (uint32_t i = wave; i < p.chunks; i += 4) s += src[(uint64_t)i * p.width];
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave || !live) return;
+    s = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
     const uint64_t o = (uint64_t)g * p.part_rows * p.parts + n;
     if (p.dbias_f32)
         static_cast<float *>(p.dbias)[o] = s;
@@ -1374,7 +1433,7 @@ hipError_t launch_dz(const DzParams &p, hipStream_t s) {
         k_dz<true><<<grid, 256, 0, s>>>(p);
     else
         k_dz<false><<<grid, 256, 0, s>>>(p);
-    if (p.dbias) k_dbias<<<dim3((p.part_rows * p.parts + 255) / 256, p.groups), 256, 0, s>>>(p);
+    if (p.dbias) k_dbias<<<dim3((p.part_rows * p.parts + 63) / 64, p.groups), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 

@@ -111,6 +111,7 @@ struct LinearEpi {
     uint64_t residual_stride, y_stride, preact_stride;
     uint32_t bias_f32, y_f32, preact_f32, act;
     uint32_t vec;           // four consecutive values can be moved as one
+    uint32_t clear;         // zeros in the rows of no group
 };
 
 // The loss's epilogues.
@@ -132,6 +133,7 @@ struct StoreEpi {
     uint64_t stride, sum_stride, matrix_stride;
     uint32_t add;        // read the running sums first
     uint32_t vec;
+    uint32_t clear;      // zeros in the rows of no group
 };
 
 struct GemmParams {
@@ -171,6 +173,7 @@ struct DzParams {
     uint32_t groups, tokens;
     uint32_t part_rows, part_pad, parts, width;  // width: padded columns of dz
     uint32_t dy_f32, z_f32, act, chunks;
+    uint32_t vec;  // eight consecutive values can be read as one
     void *dbias;
     uint32_t dbias_f32;
 };

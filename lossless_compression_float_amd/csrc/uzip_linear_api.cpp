@@ -96,7 +96,7 @@ uint32_t token_tiles(uint64_t tokens, uint64_t groups, bool grouped, uint64_t ed
 // ---- forward ----------------------------------------------------------------
 
 bool linear_ok(const uzip_weight *w, const uzip_linear_args *a, bool grouped) {
-    if (!weight_ok(w) || !a) return false;
+    if (!weight_ok(w) || !a || a->clear_rest > 1 || a->reserved) return false;
     if (grouped ? !a->offsets || !aligned(a->offsets, 4) || a->residual : a->offsets || w->matrices != 1) return false;
     if (a->tokens > kMaxDim || !type_ok(a->y_dtype) || a->act > UZIP_ACT_SWIGLU) return false;
     if ((a->act == UZIP_ACT_SWIGLU) != (w->gated == 1)) return false;
@@ -121,6 +121,7 @@ LinearEpi linear_epi(const uzip_weight *w, const uzip_linear_args *a) {
     e.bias_f32 = a->bias_dtype == UZIP_FP32;
     e.y_f32 = a->y_dtype == UZIP_FP32;
     e.act = a->act;
+    e.clear = a->clear_rest && a->offsets;
     const uint32_t yb = 4 * type_size(a->y_dtype), bb = 4 * type_size(a->bias_dtype);
     const uint64_t part = w->rows / (w->gated + 1);
     e.vec = a->y_stride % 4 == 0 && aligned(a->y, yb) && (!a->bias || (part % 4 == 0 && aligned(a->bias, bb))) &&
@@ -190,7 +191,7 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
 // ---- backward ---------------------------------------------------------------
 
 bool backward_ok(const uzip_weight *w, const uzip_linear_backward_args *a, bool grouped) {
-    if (!weight_ok(w) || !a) return false;
+    if (!weight_ok(w) || !a || a->clear_rest > 1 || a->reserved) return false;
     if (grouped ? !a->offsets || !aligned(a->offsets, 4) : a->offsets || w->matrices != 1) return false;
     if (a->tokens > kMaxDim || !type_ok(a->dy_dtype) || a->act > UZIP_ACT_SWIGLU) return false;
     if ((a->act == UZIP_ACT_SWIGLU) != (w->gated == 1)) return false;
@@ -220,9 +221,9 @@ BackwardPlan plan_backward(const uzip_weight *w, const uzip_linear_backward_args
     p.make_dz = (a->dx || a->dw) &&
                 (a->act != UZIP_ACT_NONE || a->dy_dtype == UZIP_FP32 || !tiled64(a->dy, a->dy_stride, w->rows));
     p.stage_x = a->dw && !tiled(a->x, a->x_stride, w->cols);
-    // runs of rows whose column sums are taken apart: enough workgroups for the chip, at least 32 rows each
-    p.chunks = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(1, blocks(a->tokens, 32 * groups) * (groups > 1 ? 2 : 1)),
-                                            groups > 1 ? 64 : 256);
+    // runs of rows whose column sums are taken apart: about 2,048 workgroups (of 512 columns), of at least 8 rows
+    const uint64_t wide = blocks(w->gated ? l.part_blocks * kTileRows : p.width, 512) * groups;
+    p.chunks = (uint32_t)std::max<uint64_t>(1, std::min(blocks(2048, wide), blocks(a->tokens, 8)));
     if (p.make_dz) p.dz = c.take<uint16_t>(a->tokens * p.width);
     if (p.stage_x) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 8));
     if (a->dbias) p.colsum = c.take<float>(groups * p.chunks * p.width);
@@ -257,6 +258,8 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
         p.dy_f32 = a->dy_dtype == UZIP_FP32;
         p.act = a->act;
         p.chunks = plan.chunks;
+        p.vec = a->dy_stride % 8 == 0 && aligned(a->dy, 16) &&
+                (a->act == UZIP_ACT_NONE || (a->preact_stride % 8 == 0 && aligned(a->preact, 16) && v.part_rows % 8 == 0));
         p.dbias = a->dbias;
         p.dbias_f32 = a->dbias_dtype == UZIP_FP32;
         if (launch_dz(p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
@@ -280,6 +283,7 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
         p.store.out = static_cast<uint16_t *>(a->dx);
         p.store.stride = a->dx_stride;
         p.store.vec = a->dx_stride % 4 == 0 && aligned(a->dx, 8);
+        p.store.clear = a->clear_rest && a->offsets;
         if (launch_gemm(kGemmDx, edge, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     }
     if (a->dw) {

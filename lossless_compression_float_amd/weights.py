@@ -31,13 +31,15 @@ class uzip_weight(ctypes.Structure):
 class uzip_linear_args(ctypes.Structure):
     _fields_ = [("x", _vp), ("x_stride", _sz), ("tokens", _sz), ("offsets", _vp), ("bias", _vp), ("residual", _vp),
                 ("residual_stride", _sz), ("y", _vp), ("y_stride", _sz), ("preact", _vp), ("preact_stride", _sz),
-                ("bias_dtype", _u32), ("y_dtype", _u32), ("act", _u32), ("preact_dtype", _u32)]
+                ("bias_dtype", _u32), ("y_dtype", _u32), ("act", _u32), ("preact_dtype", _u32), ("clear_rest", _u32),
+                ("reserved", _u32)]
 
 
 class uzip_linear_backward_args(ctypes.Structure):
     _fields_ = [("dy", _vp), ("dy_stride", _sz), ("x", _vp), ("x_stride", _sz), ("preact", _vp), ("preact_stride", _sz),
                 ("tokens", _sz), ("offsets", _vp), ("dx", _vp), ("dx_stride", _sz), ("dw", _vp), ("dbias", _vp),
-                ("dy_dtype", _u32), ("dbias_dtype", _u32), ("act", _u32), ("preact_dtype", _u32)]
+                ("dy_dtype", _u32), ("dbias_dtype", _u32), ("act", _u32), ("preact_dtype", _u32), ("clear_rest", _u32),
+                ("reserved", _u32)]
 
 
 class uzip_loss_args(ctypes.Structure):
@@ -327,16 +329,16 @@ def _forward(what, w, x, offsets, bias, act, residual, out_dtype, return_preact,
         r = residual.data_ptr()
     z_code = _code(preact_dtype, "preact_dtype") if return_preact else 0
     with _on(device):
+        clear = int(grouped and out is None)
         if out is None:
-            # rows of no group keep what the output holds: a new output starts with zeros there
-            out = (torch.zeros if grouped else torch.empty)((tokens, width), dtype=out_dtype, device=device)
+            out = torch.empty((tokens, width), dtype=out_dtype, device=device)
             y_stride = width
         else:
             y_stride = _matrix(out, "out", tokens, width, device, out_dtype)
         z = torch.empty((tokens, rows), dtype=preact_dtype, device=device) if return_preact else None
         if tokens:
             a = uzip_linear_args(x.data_ptr(), x_stride, tokens, off, b, r, r_stride, out.data_ptr(), y_stride,
-                                 z.data_ptr() if return_preact else 0, rows, b_code, y_code, act, z_code)
+                                 z.data_ptr() if return_preact else 0, rows, b_code, y_code, act, z_code, clear)
             _call(what, L.uzip_grouped_linear if grouped else L.uzip_linear, L.uzip_linear_workspace_size, w, a, ws, stream,
                   out, z)
     return (out, z) if return_preact else out
@@ -387,8 +389,8 @@ def _backward(what, w, dy, x, offsets, preact, act, need_x, need_weight, need_bi
     with _on(device):
         dx = dw = db = None
         if need_x:
-            dx = (torch.zeros if grouped else torch.empty)((tokens, cols), dtype=torch.bfloat16, device=device)
-            a.dx, a.dx_stride = dx.data_ptr(), cols
+            dx = torch.empty((tokens, cols), dtype=torch.bfloat16, device=device)
+            a.dx, a.dx_stride, a.clear_rest = dx.data_ptr(), cols, int(grouped)
         if need_weight:
             dw = torch.empty(w.shape, dtype=torch.bfloat16, device=device)
             a.dw = dw.data_ptr()

@@ -20,13 +20,13 @@ def weight(rows=32, cols=64, matrices=1, gated=0, **kw):
 
 def linear_args(**kw):
     base = dict(x=FAKE, x_stride=64, tokens=5, offsets=None, bias=None, residual=None, residual_stride=0, y=FAKE,
-                y_stride=32, preact=None, preact_stride=0, bias_dtype=0, y_dtype=uz.UZIP_BF16, act=0, preact_dtype=uz.UZIP_BF16)
+                y_stride=32, preact=None, preact_stride=0, bias_dtype=0, y_dtype=uz.UZIP_BF16, act=0, preact_dtype=uz.UZIP_BF16, clear_rest=0, reserved=0)
     return uz.uzip_linear_args(**{**base, **kw})
 
 
 def backward_args(**kw):
     base = dict(dy=FAKE, dy_stride=32, x=FAKE, x_stride=64, preact=FAKE, preact_stride=32, tokens=5, offsets=None, dx=FAKE,
-                dx_stride=64, dw=FAKE, dbias=FAKE, dy_dtype=uz.UZIP_BF16, dbias_dtype=uz.UZIP_BF16, act=0, preact_dtype=uz.UZIP_BF16)
+                dx_stride=64, dw=FAKE, dbias=FAKE, dy_dtype=uz.UZIP_BF16, dbias_dtype=uz.UZIP_BF16, act=0, preact_dtype=uz.UZIP_BF16, clear_rest=0, reserved=0)
     return uz.uzip_linear_backward_args(**{**base, **kw})
 
 
@@ -38,7 +38,7 @@ def loss_args(**kw):
 
 def test_structs_have_the_headers_sizes():
     assert [ctypes.sizeof(t) for t in (uz.uzip_weight, uz.uzip_linear_args, uz.uzip_linear_backward_args,
-                                       uz.uzip_loss_args)] == [48, 104, 112, 88]
+                                       uz.uzip_loss_args)] == [48, 112, 120, 88]
 
 
 def test_packed_sizes():
@@ -90,7 +90,7 @@ def test_linear_argument_errors(grouped):
         assert uz.uzip_linear_workspace_size(b, linear_args(**off)) == 0
     assert fn(w, None, FAKE, 1 << 30, None) == INVALID
     for kw in [dict(x=None), dict(x=FAKE + 1), dict(x_stride=63), dict(y=None), dict(y_stride=31), dict(y_dtype=3),
-               dict(y_dtype=0), dict(act=6), dict(act=5), dict(preact=FAKE, preact_stride=32, preact_dtype=0),
+               dict(y_dtype=0), dict(act=6), dict(act=5), dict(reserved=1), dict(clear_rest=2), dict(preact=FAKE, preact_stride=32, preact_dtype=0),
                dict(preact=FAKE + 2, preact_stride=32, preact_dtype=2), dict(tokens=1 << 31), dict(bias=FAKE),
                dict(bias=FAKE + 1, bias_dtype=1), dict(bias=FAKE + 2, bias_dtype=2), dict(preact=FAKE, preact_stride=31),
                dict(residual=FAKE, residual_stride=31), dict(y=FAKE + 2, y_dtype=2),
@@ -126,7 +126,7 @@ def test_backward_argument_errors(grouped):
         assert fn(b, backward_args(**off), FAKE, 1 << 30, None) == INVALID
     for kw in [dict(dy=None), dict(dy_stride=31), dict(dy_dtype=5), dict(dx_stride=63), dict(x=None), dict(x_stride=1),
                dict(act=1, preact=None), dict(act=1, preact_stride=31), dict(act=5), dict(act=77), dict(dbias_dtype=0),
-               dict(dbias=FAKE + 1), dict(dw=FAKE + 1), dict(act=1, preact_dtype=3), dict(tokens=1 << 32),
+               dict(dbias=FAKE + 1), dict(dw=FAKE + 1), dict(act=1, preact_dtype=3), dict(reserved=1), dict(clear_rest=2), dict(tokens=1 << 32),
                dict(offsets=None if grouped else FAKE)]:
         assert fn(w, backward_args(**{**off, **kw}), FAKE, 1 << 30, None) == INVALID, kw
 
