@@ -779,16 +779,21 @@ __device__ inline bool find_group(const GemmParams &p, uint32_t ct, uint32_t edg
     return false;
 }
 
-template <Operand RK, Operand CK, GemmKind KIND, bool GATED, int T>
-__global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) {
-    constexpr int WAVES = T / 32, WR = 2, WC = WAVES / 2;
-    constexpr int FR = T / WR / 16, FC = T / WC / 16;  // fragments of a wave: 8 x 4 or 4 x 4
-    constexpr int STAGE = T * 64;                      // bytes of one operand's stage
-    constexpr int COPIES = STAGE / 1024 / WAVES;       // copies a wave makes for one operand's stage: 2
+template <Operand RK, Operand CK, GemmKind KIND, bool GATED, int TR, int TC, int WR, int WC>
+__global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
+    constexpr int WAVES = WR * WC;
+    static_assert(WAVES == 8, "eight waves");
+    constexpr int FR = TR / WR / 16, FC = TC / WC / 16;    // fragments of a wave
+    constexpr int RSTAGE = TR * 64, CSTAGE = TC * 64;      // bytes of an operand's stage
+    constexpr int C_ALL = CSTAGE / 1024, R_ALL = RSTAGE / 1024;      // copies that fill one
+    constexpr int C_COPIES = C_ALL > WAVES ? C_ALL / WAVES : 1;      // a wave's (with fewer than waves, some twice)
+    constexpr int R_COPIES = R_ALL > WAVES ? R_ALL / WAVES : 1;
     constexpr bool PACKED = RK == kPacked || RK == kPackedT;
-    constexpr int SLOT = 2048;                         // a packed tile on its way to the decoder
-    // four stages of R, four of C, two packed tiles a wave
-    __shared__ __align__(16) uint8_t lds[8 * STAGE + (PACKED ? 2 * WAVES * SLOT : 0)];
+    constexpr int TILES = TR / 16 / WAVES;  // packed tiles a wave decodes in two steps: 2 or 1
+    constexpr int SLOT = 2048;              // a packed tile on its way to the decoder
+    // four stages of R, four of C, the packed tiles
+    constexpr int RING = 4 * (RSTAGE + CSTAGE);
+    __shared__ __align__(16) uint8_t lds[RING + (PACKED ? TILES * WAVES * SLOT : 0)];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const uint32_t q = lane >> 4, l15 = lane & 15;
     const uint32_t wr = wave % WR, wc = wave / WR;
@@ -813,89 +818,102 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     if (KIND == kGemmDw) {
         g = blockIdx.y;
         group_rows(p.offsets, g, p.tokens, a0, a_end);
-        c0 = ct * T;
+        c0 = ct * TC;
         c_end = p.c_limit;
     } else {
         if ((KIND == kGemmForward || KIND == kGemmDx) && ct == 0) {
             constexpr bool F = KIND == kGemmForward;
             if (F ? p.lin.clear : p.store.clear) {
-                const uint32_t wide = GATED ? T / 2 : T, limit = F ? p.w.part_rows : p.cols, c = min(rt * wide, limit);
+                const uint32_t wide = GATED ? TR / 2 : TR, limit = F ? p.w.part_rows : p.cols, c = min(rt * wide, limit);
                 clear_rest(p.offsets, p.groups, p.tokens, F ? p.lin.y : p.store.out, F ? p.lin.y_stride : p.store.stride,
                            F && p.lin.y_f32 ? 4 : 2, c, min(c + wide, limit), WAVES * 64);
             }
         }
-        if (!find_group(p, ct, T, lane, g, c0, c_end)) return;
+        if (!find_group(p, ct, TC, lane, g, c0, c_end)) return;
         g = uniform(g);
         c0 = uniform(c0);
         c_end = uniform(c_end);
     }
     // stages of 32 contraction values
-    const uint32_t S = KIND == kGemmDw ? (a_end - a0 + 31) / 32 : 2 * p.steps;
+    const uint32_t S_ALL = KIND == kGemmDw ? (a_end - a0 + 31) / 32 : 2 * p.steps, s0 = 0, S = S_ALL;
     const uint32_t KB = p.w.col_blocks;
 
     // ---- copies from memory ----
     // Rows: a copy takes 16 rows.  Cols: 1 KiB of the stage's rows.  What lies behind the last row or column is read
     // as zeros.
-    uint32_t c_off[COPIES], r_off[RK == kCols ? COPIES : 1];
-    auto cols_off = [&](int i, uint32_t x0, uint32_t limit, uint64_t stride) __attribute__((always_inline)) -> uint32_t {
-        const uint32_t j = (wave * COPIES + i) * 64 + lane, a = j / (T / 8), u = j % (T / 8);
+    constexpr int PARTS = C_COPIES + (RK == kCols ? R_COPIES : 0);
+    uint32_t c_off[C_COPIES], r_off[RK == kCols ? R_COPIES : 1];
+    auto c_index = [&](int i) __attribute__((always_inline)) -> uint32_t { return (wave * C_COPIES + i) % C_ALL; };
+    auto r_index = [&](int i) __attribute__((always_inline)) -> uint32_t { return (wave * R_COPIES + i) % R_ALL; };
+    auto cols_off = [&](uint32_t index, uint32_t wide, uint32_t x0, uint32_t limit, uint64_t stride)
+                        __attribute__((always_inline)) -> uint32_t {
+        const uint32_t j = index * 64 + lane, a = j / (wide / 8), u = j % (wide / 8);
         const uint32_t c = x0 + (((u >> 1) ^ cols_swizzle(a)) * 2 + (u & 1)) * 8;
         return c < limit ? (a * (uint32_t)stride + c) * 2 : kNowhere;
     };
 #pragma unroll
-    for (int i = 0; i < COPIES; ++i) {
+    for (int i = 0; i < C_COPIES; ++i) {
         if constexpr (CK == kRows) {
-            const uint32_t row = (wave * COPIES + i) * 16 + (lane >> 2), u = (lane & 3) ^ rows_swizzle(row);
+            const uint32_t row = c_index(i) * 16 + (lane >> 2), u = (lane & 3) ^ rows_swizzle(row);
             c_off[i] = (row * (uint32_t)p.cmat.stride + u * 8) * 2;
         } else {
-            c_off[i] = cols_off(i, c0, p.c_limit, p.cmat.stride);
+            c_off[i] = cols_off(c_index(i), TC, c0, p.c_limit, p.cmat.stride);
         }
-        if constexpr (RK == kCols) r_off[i] = cols_off(i, rt * T, p.r_limit, p.rmat.stride);
     }
-    uint8_t *const r_lds = lds, *const c_lds = lds + 4 * STAGE;
-    const uint32_t r_at = lds_address(lds), c_at = r_at + 4 * STAGE;
-    constexpr int PARTS = COPIES * (RK == kCols ? 2 : 1);
+    if constexpr (RK == kCols)
+#pragma unroll
+        for (int i = 0; i < R_COPIES; ++i) r_off[i] = cols_off(r_index(i), TR, rt * TR, p.r_limit, p.rmat.stride);
+    uint8_t *const r_lds = lds, *const c_lds = lds + 4 * RSTAGE;
+    const uint32_t r_at = lds_address(lds), c_at = r_at + 4 * RSTAGE;
     // The i-th of a wave's copies of stage s.  Stages behind the last are zeros.
     auto copy_part = [&](uint32_t s, int i) __attribute__((always_inline)) {
         const uint8_t *cp = static_cast<const uint8_t *>(p.cmat.p);
         if constexpr (CK == kRows) {
-            const uint32_t rows = min((uint32_t)T, c_end - c0), bytes = ((rows - 1) * (uint32_t)p.cmat.stride + S * 32) * 2;
-            const rsrc_t c = buffer(cp + (uint64_t)c0 * p.cmat.stride * 2 + (uint64_t)s * 64, s < S ? bytes - s * 64 : 0);
-            copy_to_lds(c, c_off[i], c_at + (s & 3) * STAGE + (wave * COPIES + i) * 1024);
+            const uint32_t rows = min((uint32_t)TC, c_end - c0), bytes = ((rows - 1) * (uint32_t)p.cmat.stride + S_ALL * 32) * 2;
+            const rsrc_t c = buffer(cp + (uint64_t)c0 * p.cmat.stride * 2 + (uint64_t)(s0 + s) * 64,
+                                    s < S ? bytes - (s0 + s) * 64 : 0);
+            copy_to_lds(c, c_off[i], c_at + (s & 3) * CSTAGE + c_index(i) * 1024);
         } else {
             const uint32_t a = a0 + s * 32, rows = s < S ? min(32u, a_end - a) : 0;
-            const bool r = i & 1;
+            const bool r = i >= C_COPIES;
             const Mat &m = r ? p.rmat : p.cmat;
             const rsrc_t x = buffer(static_cast<const uint8_t *>(m.p) + (uint64_t)a * m.stride * 2, rows * (uint32_t)m.stride * 2);
-            copy_to_lds(x, r ? r_off[i >> 1] : c_off[i >> 1],
-                        (r ? r_at : c_at) + (s & 3) * STAGE + (wave * COPIES + (i >> 1)) * 1024);
+            if (r)
+                copy_to_lds(x, r_off[i - C_COPIES], r_at + (s & 3) * RSTAGE + r_index(i - C_COPIES) * 1024);
+            else
+                copy_to_lds(x, c_off[i], c_at + (s & 3) * CSTAGE + c_index(i) * 1024);
         }
     };
 
     // ---- packed weights ----
-    // A wave decodes one tile in each step.  Forward: a block of 64 contraction values is T / 16 tiles, which fill two
-    // stages; decode step n fills half of stages n & ~1 and (n & ~1) + 1.  dx: a stage of 32 weight rows is
-    // 2 x T / 64 tiles; decode step n fills stage n.  In step s: n = s + 3 forward (stage s + 2 is whole after step s,
-    // when s is odd with the one after it), n = s + 2 for dx.  The tile was copied to LDS two steps before.
-    constexpr uint32_t AHEAD = RK == kPacked ? 3 : 2;
-    auto tile_index = [&](uint32_t n, bool &live) __attribute__((always_inline)) -> uint64_t {
+    // A block of 64 contraction values (two stages) is TR / 16 tiles; a wave decodes TILES of them.
+    // TILES 2: one in each step.  Forward: decode step d fills half of stages d & ~1 and (d & ~1) + 1; in step s,
+    // d = s + 3 (stage s + 2 is whole after step s, when s is odd with the one after it).  dx: d fills stage d, d = s + 2.
+    // TILES 1: one in every other step, d = s / 2 + 1.  Forward: in even steps, into stages 2 d and 2 d + 1.  dx: half of
+    // the waves in even steps into stage 2 d, half in odd ones into 2 d + 1.
+    // A tile is copied to LDS two steps before.
+    constexpr bool FWD = RK == kPacked;
+    const uint32_t half = TILES == 2 || FWD ? 0 : wave / (WAVES / 2);
+    const uint32_t decodes = TILES == 2 ? S : (S + 1) / 2;
+    auto tile_index = [&](uint32_t d, bool &live) __attribute__((always_inline)) -> uint64_t {
         uint32_t rb, kb;
-        n = min(n, S - 1);
-        if (RK == kPacked) {
-            const uint32_t j = wave * 2 + (n & 1);
-            kb = n >> 1;
+        d = min(d, decodes - 1);
+        if (FWD) {
+            const uint32_t j = TILES == 2 ? wave * 2 + (d & 1) : wave;
+            kb = (s0 >> 1) + (TILES == 2 ? d >> 1 : d);
             if (GATED) {
-                rb = rt * (T / 32) + (j >> 1);
+                rb = rt * (TR / 32) + (j >> 1);
                 live = rb < p.w.part_blocks;
                 rb = live ? rb + (j & 1 ? p.w.part_blocks : 0) : 0;
             } else {
-                rb = rt * (T / 16) + j;
+                rb = rt * (TR / 16) + j;
                 live = rb < p.row_blocks;
                 rb = live ? rb + p.row_block0 : 0;
             }
         } else {
-            rb = n * 2 + (wave & 1);
-            kb = rt * (T / 64) + (wave >> 1);
+            const uint32_t j = TILES == 2 ? wave : wave % (WAVES / 2), stage = s0 + (TILES == 2 ? d : 2 * d + half);
+            rb = stage * 2 + (j & 1);
+            kb = rt * (TR / 64) + (j >> 1);
             live = rb < p.row_blocks && kb < KB;
             rb = live ? rb + p.row_block0 : 0;
             kb = live ? kb : 0;
@@ -905,84 +923,86 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     // Headers: lane l holds that of decode step 64 i + l; the next 64 are loaded meanwhile.
     constexpr uint32_t kDead = 1u << 31;  // header flag here: the tile lies outside the weight
     uint4 heads = make_uint4(0, 0, 0, 0), heads_next = heads;
-    auto load_heads = [&](uint32_t n0) __attribute__((always_inline)) -> uint4 {
+    auto load_heads = [&](uint32_t d0) __attribute__((always_inline)) -> uint4 {
         bool live;
-        return p.w.head[tile_index(n0 + lane, live)];
+        return p.w.head[tile_index(d0 + lane, live)];
     };
-    auto use_heads = [&](uint32_t n0, uint4 h) __attribute__((always_inline)) {
+    auto use_heads = [&](uint32_t d0, uint4 h) __attribute__((always_inline)) {
         bool live;
-        tile_index(n0 + lane, live);
+        tile_index(d0 + lane, live);
         heads = head_checked(p.w, h);
-        if (RK == kPackedT && !live) heads.x |= kDead;
+        if (!FWD && !live) heads.x |= kDead;
     };
-    uint8_t *const slots = lds + 8 * STAGE + wave * 2 * SLOT;
-    const uint32_t slots_at = r_at + 8 * STAGE + wave * 2 * SLOT;
-    auto copy_tile = [&](uint32_t n) __attribute__((always_inline)) {
+    constexpr int SLOTS = TILES;
+    uint8_t *const slots = lds + RING + wave * SLOTS * SLOT;
+    const uint32_t slots_at = r_at + RING + wave * SLOTS * SLOT;
+    auto copy_tile = [&](uint32_t d) __attribute__((always_inline)) {
         bool live;
-        const rsrc_t r = buffer(p.w.tiles + tile_index(n, live) * kTileBytes, kTileBytes);
-        copy_to_lds(r, lane * 16, slots_at + (n & 1) * SLOT);
-        copy_to_lds(r, kTileSm + (lane & 31) * 16, slots_at + (n & 1) * SLOT + kTileSm);  // (the codes twice)
+        const rsrc_t r = buffer(p.w.tiles + tile_index(d, live) * kTileBytes, kTileBytes);
+        copy_to_lds(r, lane * 16, slots_at + d % SLOTS * SLOT);
+        copy_to_lds(r, kTileSm + (lane & 31) * 16, slots_at + d % SLOTS * SLOT + kTileSm);  // (the codes twice)
     };
-    auto read_tile = [&](uint32_t n, Tile &t) __attribute__((always_inline)) {
-        const uint8_t *d = slots + (n & 1) * SLOT;
-        t.sm = *reinterpret_cast<const uint4 *>(d + lane * 16);
-        t.code = *reinterpret_cast<const uint2 *>(d + kTileSm + lane * 8);
-        t.h.x = __builtin_amdgcn_readlane(heads.x, n & 63);
+    auto read_tile = [&](uint32_t d, Tile &t) __attribute__((always_inline)) {
+        const uint8_t *at = slots + d % SLOTS * SLOT;
+        t.sm = *reinterpret_cast<const uint4 *>(at + lane * 16);
+        t.code = *reinterpret_cast<const uint2 *>(at + kTileSm + lane * 8);
+        t.h.x = __builtin_amdgcn_readlane(heads.x, d & 63);
     };
     // Places in LDS of the two halves of a lane's 16 values; dx: both in one stage.
-    auto tile_place = [&](uint32_t n, uint32_t l, uint32_t &at0, uint32_t &at1) __attribute__((always_inline)) {
-        if (RK == kPacked) {
-            const uint32_t at = (wave * 2 + (n & 1)) * 1024 + l * 16;
-            at0 = (n & 2) * STAGE + at;
-            at1 = at0 + STAGE;
+    auto tile_place = [&](uint32_t d, uint32_t l, uint32_t &at0, uint32_t &at1) __attribute__((always_inline)) {
+        if (FWD) {
+            const uint32_t j = TILES == 2 ? wave * 2 + (d & 1) : wave, at = j * 1024 + l * 16;
+            at0 = (TILES == 2 ? d & 2 : d * 2 & 2) * RSTAGE + at;
+            at1 = at0 + RSTAGE;
         } else {
-            const uint32_t row = (wave & 1) * 16 + (l & 15), lq = l >> 4;
-            at0 = (n & 3) * STAGE + cols_at<T>(row, (wave >> 1) * 4 + (lq >> 1)) + (lq & 1) * 16;
-            at1 = (n & 3) * STAGE + cols_at<T>(row, (wave >> 1) * 4 + 2 + (lq >> 1)) + (lq & 1) * 16;
+            const uint32_t j = TILES == 2 ? wave : wave % (WAVES / 2), row = (j & 1) * 16 + (l & 15), lq = l >> 4;
+            const uint32_t stage = (TILES == 2 ? d : 2 * d + half) & 3;
+            at0 = stage * RSTAGE + cols_at<TR>(row, (j >> 1) * 4 + (lq >> 1)) + (lq & 1) * 16;
+            at1 = stage * RSTAGE + cols_at<TR>(row, (j >> 1) * 4 + 2 + (lq >> 1)) + (lq & 1) * 16;
         }
     };
-    auto store_tile = [&](uint32_t n, const uint32_t v[8]) __attribute__((always_inline)) {
+    auto store_tile = [&](uint32_t d, const uint32_t v[8]) __attribute__((always_inline)) {
         uint32_t at0, at1;
-        tile_place(n, lane, at0, at1);
+        tile_place(d, lane, at0, at1);
         *reinterpret_cast<uint4 *>(r_lds + at0) = make_uint4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<uint4 *>(r_lds + at1) = make_uint4(v[4], v[5], v[6], v[7]);
     };
     // What the plain decode does not cover is put right behind it.
-    auto mend = [&](uint32_t n, uint32_t h0) __attribute__((always_inline)) {
-        if ((h0 & (0xFF00u | kTileZero | kDead)) == 0 || n >= S) return;
+    auto mend = [&](uint32_t d, uint32_t h0) __attribute__((always_inline)) {
+        if ((h0 & (0xFF00u | kTileZero | kDead)) == 0 || d >= decodes) return;
         uint32_t at0, at1;
         if (h0 & kDead) {
             const uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            store_tile(n, v);
+            store_tile(d, v);
             return;
         }
         Tile t;
-        t.h = make_uint4(h0, __builtin_amdgcn_readlane(heads.y, n & 63), __builtin_amdgcn_readlane(heads.z, n & 63),
-                         __builtin_amdgcn_readlane(heads.w, n & 63));
+        t.h = make_uint4(h0, __builtin_amdgcn_readlane(heads.y, d & 63), __builtin_amdgcn_readlane(heads.z, d & 63),
+                         __builtin_amdgcn_readlane(heads.w, d & 63));
         if (tile_special(h0)) {
             bool live;
             uint32_t v[8];
             // (each branch uses all that it loads: a load left unused would be waited for in the next step)
-            const uint8_t *d = p.w.tiles + tile_index(n, live) * kTileBytes;
-            t.sm = *reinterpret_cast<const uint4 *>(d + lane * 16);
+            const uint8_t *from = p.w.tiles + tile_index(d, live) * kTileBytes;
+            t.sm = *reinterpret_cast<const uint4 *>(from + lane * 16);
             if (tile_raw(h0)) {
                 tile_decode_raw(t, p.w, lane, v);
             } else {
-                t.code = *reinterpret_cast<const uint2 *>(d + kTileSm + lane * 8);
+                t.code = *reinterpret_cast<const uint2 *>(from + kTileSm + lane * 8);
                 tile_decode_zero(t, v);
             }
-            store_tile(n, v);
+            store_tile(d, v);
         }
         if (lane < tile_listed(h0)) {
             const uint32_t e = tile_entry(p.w, t.h, lane);
-            tile_place(n, e >> 4 & 63, at0, at1);
+            tile_place(d, e >> 4 & 63, at0, at1);
             *reinterpret_cast<uint16_t *>(r_lds + (e & 8 ? at1 : at0) + (e & 7) * 2) = (uint16_t)(e >> 16);
         }
     };
-    auto next_heads = [&](uint32_t n) __attribute__((always_inline)) {  // before decode step n
-        if ((n & 63) == 0 && n) {
-            use_heads(n, heads_next);
-            heads_next = load_heads(n + 64);
+    auto next_heads = [&](uint32_t d) __attribute__((always_inline)) {  // before decode step d
+        if ((d & 63) == 0 && d) {
+            use_heads(d, heads_next);
+            heads_next = load_heads(d + 64);
         }
     };
 
@@ -991,18 +1011,18 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     bf16x8 rf[FR + 1], cf[2][FC];
     auto place = [](int i, int b) __attribute__((always_inline)) { return i == FR - 1 && b ? FR : i; };
     auto read_r = [&](uint32_t s, int i, int at) __attribute__((always_inline)) {
-        const uint8_t *rl = r_lds + (s & 3) * STAGE;
+        const uint8_t *rl = r_lds + (s & 3) * RSTAGE;
         const uint32_t rr = (wr * FR + i) * 16;
-        if constexpr (RK == kPacked)
+        if constexpr (FWD)
             rf[at] = *reinterpret_cast<const bf16x8 *>(rl + rr * 64 + lane * 16);
         else
-            rf[at] = cols_frag<T>(rl, rr, lane);
+            rf[at] = cols_frag<TR>(rl, rr, lane);
     };
     auto read_c = [&](uint32_t s, int b, int i) __attribute__((always_inline)) {
-        const uint8_t *cl = c_lds + (s & 3) * STAGE;
+        const uint8_t *cl = c_lds + (s & 3) * CSTAGE;
         const uint32_t cc = (wc * FC + i) * 16;
         if constexpr (CK == kCols)
-            cf[b][i] = cols_frag<T>(cl, cc, lane);
+            cf[b][i] = cols_frag<TC>(cl, cc, lane);
         else
             cf[b][i] = *reinterpret_cast<const bf16x8 *>(cl + rows_at(cc + l15, q));
     };
@@ -1011,30 +1031,29 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     for (int i = 0; i < FR; ++i)
         for (int j = 0; j < FC; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    constexpr int PER_STEP = PARTS + (PACKED ? 2 : 0);
     if (S > 0) {
         if constexpr (PACKED) {
             use_heads(0, load_heads(0));
             heads_next = load_heads(64);
-            copy_tile(0);
-            copy_tile(1);
+            for (uint32_t d = 0; d < SLOTS; ++d) copy_tile(d);
         }
         for (uint32_t s = 0; s < 3; ++s)
 #pragma unroll
             for (int i = 0; i < PARTS; ++i) copy_part(s, i);
         if constexpr (PACKED) {
+            // the decode steps before those of step 0
+            constexpr uint32_t BEFORE = TILES == 1 ? 1 : FWD ? 3 : 2;
 #pragma unroll 1
-            for (uint32_t n = 0; n < AHEAD; ++n) {
-                if (n < 2) wait_copies<0>();
-                if (n == 2) wait_copies<2>();  // (tile 2, whose copy came before tile 3's)
+            for (uint32_t d = 0; d < BEFORE; ++d) {
+                wait_copies<0>();
                 Tile t;
                 uint32_t v[8];
-                read_tile(n, t);
+                read_tile(d, t);
                 tile_decode_plain(t, v);
-                store_tile(n, v);
-                mend(n, t.h.x);
+                store_tile(d, v);
+                mend(d, t.h.x);
                 wait_copies<0>();
-                copy_tile(n + 2);
+                copy_tile(d + SLOTS);
             }
         }
         wait_copies<0>();
@@ -1046,32 +1065,46 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
         settle(acc);  // the zeros
         auto step = [&](uint32_t s, auto parity) __attribute__((always_inline)) {
             constexpr int b = decltype(parity)::value;
-            const uint32_t n = s + AHEAD;
+            const uint32_t d = TILES == 1 ? s / 2 + 1 : FWD ? s + 3 : s + 2;
+            // whether this wave decodes in this step (TILES 1, dx: a uniform branch, else known)
+            const bool mine = PACKED && (TILES == 2 || (FWD ? b == 0 : half == b));
             Tile t;
             uint32_t v[8];
             if constexpr (PACKED) {
-                next_heads(n);
-                read_tile(n, t);
+                if (mine) {
+                    next_heads(d);
+                    read_tile(d, t);
+                }
             }
             const uint32_t base = PACKED ? (t.h.x & 0xFF) * 0x00800080u : 0;
             // between the matrix instructions, whose shadow hides them: copies, reads and the decoder
 #pragma unroll
             for (int i = 0; i < FR; ++i) {
                 if (i < PARTS) copy_part(s + 3, i);
-                if (i < FC) read_c(s + 1, b ^ 1, i);
+                if (i == FR - 1)
+#pragma unroll
+                    for (int k = FR; k < PARTS; ++k) copy_part(s + 3, k);
+#pragma unroll
+                for (int k = i * FC / FR; k < (i + 1) * FC / FR; ++k) read_c(s + 1, b ^ 1, k);
                 if (i == FR - 1) {
                     read_r(s + 1, i, place(i, b ^ 1));
                     if constexpr (PACKED) {
-                        store_tile(n, v);  // behind the last stage: into stages that nothing reads any more
-                        mend(n, t.h.x);
-                        copy_tile(n + 2);
+                        if (mine) {
+                            if constexpr (FR <= 2) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) v[k] = tile_signs(t, k) | (base - tile_codes(t, k));
+                            }
+                            store_tile(d, v);  // behind the last stage: into stages that nothing reads any more
+                            mend(d, t.h.x);
+                            copy_tile(d + SLOTS);
+                        }
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
                 for (int j = 0; j < FC; ++j) mfma(acc[i][j], rf[place(i, b)], cf[b][j]);
                 if (i < FR - 1) read_r(s + 1, i, i);
-                if constexpr (PACKED) {
+                if constexpr (PACKED && FR > 2) {
                     // eight pairs, between the first and the last group of products
                     constexpr int GROUPS = FR - 2;
                     if (i > 0 && i <= GROUPS)
@@ -1081,7 +1114,12 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            wait_copies<PER_STEP>();  // stage s + 2 has arrived: only this step's copies may be on their way
+            // stage s + 2 and the tile of the step after next but one have arrived: only this step's copies may be on
+            // their way
+            if (mine)
+                wait_copies<PARTS + 2>();
+            else
+                wait_copies<PARTS>();
             barrier();
         };
         for (uint32_t s = 0; s < S; s += 2) {  // (a step behind an odd number of stages adds zeros)
@@ -1096,13 +1134,13 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
     // ---- epilogues: acc[i][j][d] is row 16 (wr FR + i) + 4 q + d of the tile, column 16 (wc FC + j) + l15 ----
     if constexpr (KIND == kGemmLossStat) {
         // every token's largest logit in this tile, and the sum of exp(logit - that)
-        f32x2 *red = reinterpret_cast<f32x2 *>(lds);  // [2][T]
+        f32x2 *red = reinterpret_cast<f32x2 *>(lds);  // [WR][TC]
 #pragma unroll
         for (int j = 0; j < FC; ++j) {
             const uint32_t m = c0 + (wc * FC + j) * 16 + l15;
             const bool live = m < c_end;
             const int64_t want = live ? p.loss.target[m] : -1;
-            const uint32_t n0 = rt * T + wr * FR * 16 + q * 4;
+            const uint32_t n0 = rt * TR + wr * FR * 16 + q * 4;
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < FR; ++i)
@@ -1124,28 +1162,34 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
                 for (int d = 0; d < 4; ++d) sum += __expf(acc[i][j][d] - ref);
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (q == 0) red[wr * T + (wc * FC + j) * 16 + l15] = f32x2{ref, sum};
+            if (q == 0) red[wr * TC + (wc * FC + j) * 16 + l15] = f32x2{ref, sum};
         }
         __syncthreads();
-        for (uint32_t c = tid; c < T; c += WAVES * 64) {
+        for (uint32_t c = tid; c < TC; c += WAVES * 64) {
             if (c0 + c >= c_end) continue;
-            const float ref = fmaxf(red[c][0], red[T + c][0]);
-            const float sum = red[c][1] * __expf(red[c][0] - ref) + red[T + c][1] * __expf(red[T + c][0] - ref);
+            float ref = red[c][0], sum = 0;
+#pragma unroll
+            for (int w = 1; w < WR; ++w) ref = fmaxf(ref, red[w * TC + c][0]);
+#pragma unroll
+            for (int w = 0; w < WR; ++w) sum += red[w * TC + c][1] * __expf(red[w * TC + c][0] - ref);
             p.loss.part[(uint64_t)rt * p.tokens + c0 + c] = make_float2(ref, sum);
         }
         return;
     }
 
-    // The others go through LDS, 16 KiB a wave at a time, so that a column's rows leave in one run: a wave's part is
-    // [columns][16 FR] values in units of four, the unit's place xored with the column against bank conflicts.
-    constexpr int UNITS = FR * 4, JP = 16 / FR;  // fragments of columns at a time
-    f32x4 *out = reinterpret_cast<f32x4 *>(lds + wave * 16384);
+    // The others go through LDS, as many fragments of columns at a time as fit, so that a column's rows leave in one
+    // run: a wave's part is [columns][16 FR] values in units of four, the unit's place xored with the column against
+    // bank conflicts.
+    constexpr int UNITS = FR * 4, BYTES = RING / WAVES / 16 * 16, FIT = BYTES / (FR * 1024);
+    constexpr int JP = FIT >= FC ? FC : FIT >= 2 && FC % 2 == 0 ? 2 : 1, SWZ = UNITS < 16 ? UNITS - 1 : 15;
+    static_assert(FIT >= 1, "a fragment of columns fits");
+    f32x4 *out = reinterpret_cast<f32x4 *>(lds + wave * BYTES);
 #pragma unroll
     for (int ph = 0; ph < FC; ph += JP) {
 #pragma unroll
         for (int j = 0; j < JP; ++j)
 #pragma unroll
-            for (int i = 0; i < FR; ++i) out[(j * 16 + l15) * UNITS + ((i * 4 + q) ^ l15)] = acc[i][ph + j];
+            for (int i = 0; i < FR; ++i) out[(j * 16 + l15) * UNITS + ((i * 4 + q) ^ (l15 & SWZ))] = acc[i][ph + j];
         constexpr int OUTS = GATED ? UNITS / 2 : UNITS;  // results of a column, in units of four
 #pragma unroll 1
         for (uint32_t k = lane; k < JP * 16 * OUTS; k += 64) {
@@ -1155,10 +1199,10 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 2) void k_gemm(GemmParams p) 
 #pragma unroll
             for (int h = 0; h < (GATED ? 2 : 1); ++h) {
                 const uint32_t from = GATED ? (u >> 2) * 8 + h * 4 + (u & 3) : u;
-                const f32x4 x = out[cl * UNITS + (from ^ (cl & 15))];
+                const f32x4 x = out[cl * UNITS + (from ^ (cl & SWZ))];
                 for (int d = 0; d < 4; ++d) v[h][d] = x[d];
             }
-            const uint32_t r = rt * (T / (GATED ? 2 : 1)) + wr * OUTS * 4 + u * 4;  // first of four rows
+            const uint32_t r = rt * (TR / (GATED ? 2 : 1)) + wr * OUTS * 4 + u * 4;  // first of four rows
             if constexpr (KIND == kGemmForward) {
                 if (c < c_end) linear_out<GATED>(p.lin, (uint64_t)g * p.rows, p.w.part_rows, c, r, v);
             } else if constexpr (KIND == kGemmLossDz) {
@@ -1351,12 +1395,14 @@ hipError_t skinny(const SkinnyParams &p, hipStream_t s) {
 }
 
 template <Operand RK, Operand CK, GemmKind KIND, bool GATED>
-hipError_t gemm(uint32_t edge, const GemmParams &p, hipStream_t s) {
+hipError_t gemm(GemmTile tile, const GemmParams &p, hipStream_t s) {
     const dim3 grid(p.r_tiles * p.c_tiles, KIND == kGemmDw ? p.groups : 1);
-    if (edge == 256)
-        k_gemm<RK, CK, KIND, GATED, 256><<<grid, 512, 0, s>>>(p);
-    else
-        k_gemm<RK, CK, KIND, GATED, 128><<<grid, 256, 0, s>>>(p);
+    if (tile.r == 256 && tile.c == 256)
+        k_gemm<RK, CK, KIND, GATED, 256, 256, 2, 4><<<grid, 512, 0, s>>>(p);
+    else if (tile.r == 128 && tile.c == 128)
+        k_gemm<RK, CK, KIND, GATED, 128, 128, 2, 4><<<grid, 512, 0, s>>>(p);
+    else if constexpr (KIND != kGemmDw)
+        k_gemm<RK, CK, KIND, GATED, 256, 64, 4, 2><<<grid, 512, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -1402,20 +1448,22 @@ hipError_t launch_skinny(const SkinnyParams &p, hipStream_t s) {
     return p.tokens <= 32 ? skinny<2, 1, false, 16, 2>(p, s) : skinny<4, 2, false, 8, 1>(p, s);
 }
 
-uint32_t gemm_edge(uint64_t r, uint64_t c, uint64_t groups) {
-    return ((r + 255) / 256) * ((c + 255) / 256) * groups >= 256 ? 256 : 128;
+GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups) {
+    const uint64_t each = (c + groups - 1) / groups;
+    if (kind != kGemmDw && each <= 64) return GemmTile{256, 64};
+    return ((r + 255) / 256) * ((c + 255) / 256) >= 256 && each > 128 ? GemmTile{256, 256} : GemmTile{128, 128};
 }
 
-hipError_t launch_gemm(GemmKind kind, uint32_t edge, const GemmParams &p, hipStream_t s) {
+hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStream_t s) {
     if (p.r_tiles == 0 || p.c_tiles == 0) return hipSuccess;
     switch (kind) {
     case kGemmForward:
-        return p.lin.act == kActSwiglu ? gemm<kPacked, kRows, kGemmForward, true>(edge, p, s)
-                                       : gemm<kPacked, kRows, kGemmForward, false>(edge, p, s);
-    case kGemmLossStat: return gemm<kPacked, kRows, kGemmLossStat, false>(edge, p, s);
-    case kGemmLossDz: return gemm<kPacked, kRows, kGemmLossDz, false>(edge, p, s);
-    case kGemmDx: return gemm<kPackedT, kRows, kGemmDx, false>(edge, p, s);
-    case kGemmDw: return gemm<kCols, kCols, kGemmDw, false>(edge, p, s);
+        return p.lin.act == kActSwiglu ? gemm<kPacked, kRows, kGemmForward, true>(tile, p, s)
+                                       : gemm<kPacked, kRows, kGemmForward, false>(tile, p, s);
+    case kGemmLossStat: return gemm<kPacked, kRows, kGemmLossStat, false>(tile, p, s);
+    case kGemmLossDz: return gemm<kPacked, kRows, kGemmLossDz, false>(tile, p, s);
+    case kGemmDx: return gemm<kPackedT, kRows, kGemmDx, false>(tile, p, s);
+    case kGemmDw: return gemm<kCols, kCols, kGemmDw, false>(tile, p, s);
     }
     return hipErrorInvalidValue;
 }

@@ -185,10 +185,14 @@ hipError_t launch_stage(const uint16_t *in, uint64_t in_stride, uint16_t *out, u
 hipError_t launch_skinny(const SkinnyParams &p, hipStream_t s);
 // rows a call may have for the skinny kernel
 bool skinny_fits(uint64_t tokens, uint64_t groups);
-// tile edge (128 or 256) of a product with `r` by `c` outputs
-uint32_t gemm_edge(uint64_t r, uint64_t c, uint64_t groups);
 enum GemmKind { kGemmForward, kGemmLossStat, kGemmLossDz, kGemmDx, kGemmDw };
-hipError_t launch_gemm(GemmKind kind, uint32_t edge, const GemmParams &p, hipStream_t s);
+// Outputs of a workgroup: r by c.
+struct GemmTile {
+    uint32_t r, c;
+};
+// The tile of a product with `r` by `c` outputs, c in all of `groups` groups.
+GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups);
+hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStream_t s);
 hipError_t launch_loss_join(const LossEpi &e, float *loss, float *lse, uint32_t tokens, uint32_t parts, uint64_t vocab,
                             hipStream_t s);
 hipError_t launch_dz(const DzParams &p, hipStream_t s);

@@ -176,16 +176,16 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
     p.offsets = a->offsets;
     p.groups = groups;
     p.tokens = (uint32_t)a->tokens;
-    const uint32_t edge = gemm_edge(w->rows, a->tokens, groups);
-    p.r_tiles = (uint32_t)(w->gated ? blocks(p.w.part_blocks, edge / 32) : blocks(p.w.part_blocks, edge / 16));
-    p.c_tiles = token_tiles(a->tokens, groups, grouped, edge);
+    const GemmTile tile = gemm_tile(kGemmForward, w->rows, a->tokens, groups);
+    p.r_tiles = (uint32_t)(w->gated ? blocks(p.w.part_blocks, tile.r / 32) : blocks(p.w.part_blocks, tile.r / 16));
+    p.c_tiles = token_tiles(a->tokens, groups, grouped, tile.c);
     p.c_limit = (uint32_t)up(w->cols, 8);
     p.steps = p.w.col_blocks;
     p.row_blocks = p.w.row_blocks;
     p.rows = (uint32_t)w->rows;
     p.cols = (uint32_t)w->cols;
     p.lin = linear_epi(w, a);
-    return done(launch_gemm(kGemmForward, edge, p, stream));
+    return done(launch_gemm(kGemmForward, tile, p, stream));
 }
 
 // ---- backward ---------------------------------------------------------------
@@ -275,16 +275,16 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
     p.cmat = plan.make_dz ? Mat{plan.dz, plan.width} : Mat{a->dy, a->dy_stride};
     p.c_limit = (uint32_t)(plan.make_dz ? plan.width : w->rows);
     if (a->dx && a->tokens) {
-        const uint32_t edge = gemm_edge(w->cols, a->tokens, groups);
-        p.r_tiles = (uint32_t)blocks(w->cols, edge);
-        p.c_tiles = token_tiles(a->tokens, groups, grouped, edge);
+        const GemmTile tile = gemm_tile(kGemmDx, w->cols, a->tokens, groups);
+        p.r_tiles = (uint32_t)blocks(w->cols, tile.r);
+        p.c_tiles = token_tiles(a->tokens, groups, grouped, tile.c);
         p.steps = (uint32_t)blocks(v.row_blocks, 4);
         p.store = StoreEpi{};
         p.store.out = static_cast<uint16_t *>(a->dx);
         p.store.stride = a->dx_stride;
         p.store.vec = a->dx_stride % 4 == 0 && aligned(a->dx, 8);
         p.store.clear = a->clear_rest && a->offsets;
-        if (launch_gemm(kGemmDx, edge, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+        if (launch_gemm(kGemmDx, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     }
     if (a->dw) {
         p.rmat = Mat{a->x, a->x_stride};
@@ -294,15 +294,15 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
                              stream) != hipSuccess)
                 return UZIP_ERR_DEVICE;
         }
-        const uint32_t edge = gemm_edge(w->cols, w->rows * groups, 1);
+        const GemmTile tile = gemm_tile(kGemmDw, w->cols, w->rows * groups, 1);
         p.r_limit = (uint32_t)up(w->cols, 8);
-        p.r_tiles = (uint32_t)blocks(w->cols, edge);
-        p.c_tiles = (uint32_t)blocks(v.row_blocks * kTileRows, edge);
+        p.r_tiles = (uint32_t)blocks(w->cols, tile.r);
+        p.c_tiles = (uint32_t)blocks(v.row_blocks * kTileRows, tile.c);
         p.store = StoreEpi{};
         p.store.out = static_cast<uint16_t *>(a->dw);
         p.store.stride = w->cols;
         p.store.vec = w->cols % 4 == 0 && aligned(a->dw, 8);
-        if (launch_gemm(kGemmDw, edge, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+        if (launch_gemm(kGemmDw, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     }
     return UZIP_OK;
 }
@@ -327,7 +327,7 @@ struct LossPlan {
     uint16_t *dz;
     float *sum;
     uint64_t piece;  // rows of the weight in a piece
-    uint32_t edge;
+    GemmTile tile;
     bool stage;
 };
 
@@ -336,8 +336,8 @@ LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward,
     p.stage = !tiled64(a->x, a->x_stride, w->cols);
     if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 64));
     if (!backward) {
-        p.edge = gemm_edge(w->rows, a->tokens, 1);
-        p.part = c.take<float2>(a->tokens * blocks(w->rows, p.edge));
+        p.tile = gemm_tile(kGemmLossStat, w->rows, a->tokens, 1);
+        p.part = c.take<float2>(a->tokens * blocks(w->rows, p.tile.r));
         p.picked = c.take<float>(a->tokens);
         return p;
     }
@@ -475,12 +475,12 @@ uzip_status uzip_linear_cross_entropy(const uzip_weight *weight, const uzip_loss
     GemmParams p = loss_params(weight, args);
     if (stage_loss_x(weight, args, plan, p.cmat, stream) != UZIP_OK) return UZIP_ERR_DEVICE;
     p.c_limit = (uint32_t)up(weight->cols, 8);
-    p.r_tiles = (uint32_t)blocks(weight->rows, plan.edge);
-    p.c_tiles = (uint32_t)blocks(args->tokens, plan.edge);
+    p.r_tiles = (uint32_t)blocks(weight->rows, plan.tile.r);
+    p.c_tiles = (uint32_t)blocks(args->tokens, plan.tile.c);
     p.steps = p.w.col_blocks;
     p.loss.part = plan.part;
     p.loss.picked = plan.picked;
-    if (launch_gemm(kGemmLossStat, plan.edge, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+    if (launch_gemm(kGemmLossStat, plan.tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     return done(launch_loss_join(p.loss, args->loss, args->lse, p.tokens, p.r_tiles, weight->rows, stream));
 }
 
@@ -511,20 +511,20 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
         p.row_blocks = std::min(step, all - b0);
         const uint64_t rows = (uint64_t)p.row_blocks * kTileRows;
         if (args->tokens) {
-            const uint32_t edge = gemm_edge(rows, args->tokens, 1);
+            const GemmTile tile = gemm_tile(kGemmLossDz, rows, args->tokens, 1);
             p.cmat = x;
             p.c_limit = (uint32_t)up(weight->cols, 8);
-            p.r_tiles = (uint32_t)blocks(rows, edge);
-            p.c_tiles = (uint32_t)blocks(args->tokens, edge);
+            p.r_tiles = (uint32_t)blocks(rows, tile.r);
+            p.c_tiles = (uint32_t)blocks(args->tokens, tile.c);
             p.steps = p.w.col_blocks;
-            if (launch_gemm(kGemmLossDz, edge, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+            if (launch_gemm(kGemmLossDz, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
         }
         p.cmat = Mat{plan.dz, plan.piece};
         p.c_limit = (uint32_t)up(rows, 64);  // the product above wrote zeros behind the last row
         if (args->dx && args->tokens) {
-            const uint32_t edge = gemm_edge(weight->cols, args->tokens, 1);
-            p.r_tiles = (uint32_t)blocks(weight->cols, edge);
-            p.c_tiles = (uint32_t)blocks(args->tokens, edge);
+            const GemmTile tile = gemm_tile(kGemmDx, weight->cols, args->tokens, 1);
+            p.r_tiles = (uint32_t)blocks(weight->cols, tile.r);
+            p.c_tiles = (uint32_t)blocks(args->tokens, tile.c);
             p.steps = (uint32_t)blocks(p.row_blocks, 4);
             p.store = StoreEpi{};
             p.store.sum = plan.sum;
@@ -533,19 +533,19 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
             p.store.out = b0 + step >= all ? static_cast<uint16_t *>(args->dx) : nullptr;
             p.store.stride = args->dx_stride;
             p.store.vec = args->dx_stride % 4 == 0 && aligned(args->dx, 8);
-            if (launch_gemm(kGemmDx, edge, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+            if (launch_gemm(kGemmDx, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
         }
         if (args->dw) {
-            const uint32_t edge = gemm_edge(weight->cols, rows, 1);
+            const GemmTile tile = gemm_tile(kGemmDw, weight->cols, rows, 1);
             p.rmat = x;
             p.r_limit = (uint32_t)up(weight->cols, 8);
-            p.r_tiles = (uint32_t)blocks(weight->cols, edge);
-            p.c_tiles = (uint32_t)blocks(rows, edge);
+            p.r_tiles = (uint32_t)blocks(weight->cols, tile.r);
+            p.c_tiles = (uint32_t)blocks(rows, tile.c);
             p.store = StoreEpi{};
             p.store.out = static_cast<uint16_t *>(args->dw);
             p.store.stride = weight->cols;
             p.store.vec = weight->cols % 4 == 0 && aligned(args->dw, 8);
-            if (launch_gemm(kGemmDw, edge, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+            if (launch_gemm(kGemmDw, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
         }
     }
     return UZIP_OK;
