@@ -779,6 +779,52 @@ __device__ inline bool find_group(const GemmParams &p, uint32_t ct, uint32_t edg
     return false;
 }
 
+// Four results of column c, rows r .. r + 3 (of the tile's kind of rows).
+template <GemmKind KIND, bool GATED>
+__device__ inline void emit(const GemmParams &p, uint32_t g, uint32_t c, uint32_t c_end, uint32_t r,
+                            float v[GATED ? 2 : 1][4]) {
+    if constexpr (KIND == kGemmForward) {
+        if (c < c_end) linear_out<GATED>(p.lin, (uint64_t)g * p.rows, p.w.part_rows, c, r, v);
+    } else if constexpr (KIND == kGemmLossDz) {
+        // g (softmax - one at the target), rounded to bf16 for the two products that follow; zeros behind the last row
+        if (c >= c_end) return;
+        const int64_t want = p.loss.target[c];
+        const bool counts = want != p.loss.ignore && want >= 0 && want < (int64_t)p.rows;
+        const float gr = counts ? p.loss.dloss[c] : 0.0f, lse = p.loss.lse[c];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t n = p.row_block0 * 16 + r + d;
+            float e = __expf(v[0][d] - lse);
+            if ((int64_t)n == want) e -= 1.0f;
+            v[0][d] = n < p.rows && counts ? gr * e : 0.0f;
+        }
+        store4(p.loss.dz, (uint64_t)c * p.loss.dz_stride + r, false, true, 4, v[0]);
+    } else {
+        const StoreEpi &e = p.store;
+        uint64_t row = c;
+        if constexpr (KIND == kGemmDw) {
+            // padded row of the stack's part -> row of the matrix; pieces start at row_block0
+            const uint32_t n = c + p.row_block0 * 16, pad = p.w.part_blocks * 16, part = n / pad, in = n - part * pad;
+            if (in >= p.w.part_rows || part >= p.w.parts || c >= p.row_blocks * 16) return;
+            row = (uint64_t)g * p.rows + (uint64_t)part * p.w.part_rows + in;
+        } else {
+            if (c >= c_end) return;
+        }
+        if (r >= p.cols) return;
+        const uint32_t count = p.cols - r < 4 ? p.cols - r : 4;
+        if (e.sum) {
+            const bool sv = count == 4;  // the sums' stride is a multiple of four
+            if (e.add) {
+                float o[4];
+                load4(e.sum, row * e.sum_stride + r, true, sv, count, o);
+                for (int d = 0; d < 4; ++d) v[0][d] += o[d];
+            }
+            if (!e.out) store4(e.sum, row * e.sum_stride + r, true, sv, count, v[0]);
+        }
+        if (e.out) store4(e.out, row * e.stride + r, false, e.vec && count == 4, count, v[0]);
+    }
+}
+
 template <Operand RK, Operand CK, GemmKind KIND, bool GATED, int TR, int TC, int WR, int WC>
 __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     constexpr int WAVES = WR * WC;
@@ -835,7 +881,12 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
         c_end = uniform(c_end);
     }
     // stages of 32 contraction values
-    const uint32_t S_ALL = KIND == kGemmDw ? (a_end - a0 + 31) / 32 : 2 * p.steps, s0 = 0, S = S_ALL;
+    const uint32_t S_ALL = KIND == kGemmDw ? (a_end - a0 + 31) / 32 : 2 * p.steps;
+    uint32_t s0 = 0, S = S_ALL;
+    if (KIND != kGemmDw && p.splits > 1) {  // a run of the contraction
+        s0 = 2 * (uint32_t)((uint64_t)p.steps * blockIdx.y / p.splits);
+        S = 2 * (uint32_t)((uint64_t)p.steps * (blockIdx.y + 1) / p.splits) - s0;
+    }
     const uint32_t KB = p.w.col_blocks;
 
     // ---- copies from memory ----
@@ -1190,11 +1241,21 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
         for (int j = 0; j < JP; ++j)
 #pragma unroll
             for (int i = 0; i < FR; ++i) out[(j * 16 + l15) * UNITS + ((i * 4 + q) ^ (l15 & SWZ))] = acc[i][ph + j];
+        if (KIND != kGemmDw && p.splits > 1) {
+            // a run's part of the sums: [run][tile][column][row]
+            float *to = p.part + ((uint64_t)blockIdx.y * total + ct * p.r_tiles + rt) * (TR * TC) +
+                        (wc * FC + ph) * 16 * TR + wr * FR * 16;
+#pragma unroll 1
+            for (uint32_t k = lane; k < JP * 16 * UNITS; k += 64) {
+                const uint32_t cl = k / UNITS, u = k % UNITS;
+                *reinterpret_cast<f32x4 *>(to + cl * TR + u * 4) = out[cl * UNITS + (u ^ (cl & SWZ))];
+            }
+            continue;
+        }
         constexpr int OUTS = GATED ? UNITS / 2 : UNITS;  // results of a column, in units of four
 #pragma unroll 1
         for (uint32_t k = lane; k < JP * 16 * OUTS; k += 64) {
             const uint32_t cl = k / OUTS, u = k % OUTS;
-            const uint32_t c = c0 + (wc * FC + ph) * 16 + cl;  // column
             float v[GATED ? 2 : 1][4];
 #pragma unroll
             for (int h = 0; h < (GATED ? 2 : 1); ++h) {
@@ -1202,50 +1263,30 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
                 const f32x4 x = out[cl * UNITS + (from ^ (cl & SWZ))];
                 for (int d = 0; d < 4; ++d) v[h][d] = x[d];
             }
-            const uint32_t r = rt * (TR / (GATED ? 2 : 1)) + wr * OUTS * 4 + u * 4;  // first of four rows
-            if constexpr (KIND == kGemmForward) {
-                if (c < c_end) linear_out<GATED>(p.lin, (uint64_t)g * p.rows, p.w.part_rows, c, r, v);
-            } else if constexpr (KIND == kGemmLossDz) {
-                // g (softmax - one at the target), rounded to bf16 for the two products that follow; zeros behind the
-                // last row
-                if (c >= c_end) continue;
-                const int64_t want = p.loss.target[c];
-                const bool counts = want != p.loss.ignore && want >= 0 && want < (int64_t)p.rows;
-                const float gr = counts ? p.loss.dloss[c] : 0.0f, lse = p.loss.lse[c];
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const uint32_t n = p.row_block0 * 16 + r + d;
-                    float e = __expf(v[0][d] - lse);
-                    if ((int64_t)n == want) e -= 1.0f;
-                    v[0][d] = n < p.rows && counts ? gr * e : 0.0f;
-                }
-                store4(p.loss.dz, (uint64_t)c * p.loss.dz_stride + r, false, true, 4, v[0]);
-            } else {
-                const StoreEpi &e = p.store;
-                uint64_t row = c;
-                if constexpr (KIND == kGemmDw) {
-                    // padded row of the stack's part -> row of the matrix; pieces start at row_block0
-                    const uint32_t n = c + p.row_block0 * 16, pad = p.w.part_blocks * 16, part = n / pad, in = n - part * pad;
-                    if (in >= p.w.part_rows || part >= p.w.parts || c >= p.row_blocks * 16) continue;
-                    row = (uint64_t)g * p.rows + (uint64_t)part * p.w.part_rows + in;
-                } else {
-                    if (c >= c_end) continue;
-                }
-                if (r >= p.cols) continue;
-                const uint32_t count = p.cols - r < 4 ? p.cols - r : 4;
-                if (e.sum) {
-                    const bool sv = count == 4;  // the sums' stride is a multiple of four
-                    if (e.add) {
-                        float o[4];
-                        load4(e.sum, row * e.sum_stride + r, true, sv, count, o);
-                        for (int d = 0; d < 4; ++d) v[0][d] += o[d];
-                    }
-                    if (!e.out) store4(e.sum, row * e.sum_stride + r, true, sv, count, v[0]);
-                }
-                if (e.out) store4(e.out, row * e.stride + r, false, e.vec && count == 4, count, v[0]);
-            }
+            // first of four rows
+            const uint32_t r = rt * (TR / (GATED ? 2 : 1)) + wr * OUTS * 4 + u * 4;
+            emit<KIND, GATED>(p, g, c0 + (wc * FC + ph) * 16 + cl, c_end, r, v);
         }
     }
+}
+
+// The runs' parts added up in their order, a thread four rows of a column.
+template <GemmKind KIND, bool GATED>
+__global__ __launch_bounds__(256) void k_join(GemmParams p, uint32_t tr, uint32_t tc) {
+    const uint32_t outs = tr / (GATED ? 8 : 4), k = blockIdx.y * 256 + threadIdx.x;
+    const uint32_t cl = k / outs, u = k % outs, ct = blockIdx.x / p.r_tiles, rt = blockIdx.x % p.r_tiles;
+    if (cl >= tc || ct * tc + cl >= p.tokens) return;
+    float v[GATED ? 2 : 1][4];
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        const uint32_t row = GATED ? (u >> 2) * 32 + h * 16 + (u & 3) * 4 : u * 4;
+        const float *from = p.part + ((uint64_t)blockIdx.x * tc + cl) * tr + row;
+        f32x4 x = *reinterpret_cast<const f32x4 *>(from);
+        for (uint32_t i = 1; i < p.splits; ++i)
+            x += *reinterpret_cast<const f32x4 *>(from + (uint64_t)i * p.r_tiles * p.c_tiles * tr * tc);
+        for (int d = 0; d < 4; ++d) v[h][d] = x[d];
+    }
+    emit<KIND, GATED>(p, 0, ct * tc + cl, p.tokens, rt * (tr / (GATED ? 2 : 1)) + u * 4, v);
 }
 
 // ---- the loss's join -------------------------------------------------------------
@@ -1396,13 +1437,16 @@ hipError_t skinny(const SkinnyParams &p, hipStream_t s) {
 
 template <Operand RK, Operand CK, GemmKind KIND, bool GATED>
 hipError_t gemm(GemmTile tile, const GemmParams &p, hipStream_t s) {
-    const dim3 grid(p.r_tiles * p.c_tiles, KIND == kGemmDw ? p.groups : 1);
+    const dim3 grid(p.r_tiles * p.c_tiles, KIND == kGemmDw ? p.groups : p.splits);
     if (tile.r == 256 && tile.c == 256)
         k_gemm<RK, CK, KIND, GATED, 256, 256, 2, 4><<<grid, 512, 0, s>>>(p);
     else if (tile.r == 128 && tile.c == 128)
         k_gemm<RK, CK, KIND, GATED, 128, 128, 2, 4><<<grid, 512, 0, s>>>(p);
     else if constexpr (KIND != kGemmDw)
         k_gemm<RK, CK, KIND, GATED, 256, 64, 4, 2><<<grid, 512, 0, s>>>(p);
+    if constexpr (KIND == kGemmForward || KIND == kGemmDx)
+        if (p.splits > 1)
+            k_join<KIND, GATED><<<dim3(grid.x, (tile.r * tile.c / (GATED ? 8 : 4) + 255) / 256), 256, 0, s>>>(p, tile.r, tile.c);
     return hipGetLastError();
 }
 
@@ -1452,6 +1496,25 @@ GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups) {
     const uint64_t each = (c + groups - 1) / groups;
     if (kind != kGemmDw && each <= 64) return GemmTile{256, 64};
     return ((r + 255) / 256) * ((c + 255) / 256) >= 256 && each > 128 ? GemmTile{256, 256} : GemmTile{128, 128};
+}
+
+// Runs into which the contraction is cut.  With fewer tiles than workgroups
+// that fit the chip (two a CU), each run shortens the walk of `steps` blocks of
+// 64 (0.9 us each where a CU has one workgroup, 1.4 us where it has two) and
+// adds its part of the sums, written and read once at about 4 TB/s, and one
+// launch.  128 x 4096 x 4096: 57 us whole, 20 us in 8 runs; 777 x 4096 x 4096
+// (224 tiles): 62 us whole, 70 us in two.
+uint32_t gemm_splits(GemmTile tile, uint64_t r_tiles, uint64_t c_tiles, uint64_t steps) {
+    const uint64_t tiles = r_tiles * c_tiles;
+    if (tiles == 0 || tiles > 256) return 1;
+    const double part = 8.0 * tiles * tile.r * tile.c / 4e6;  // us a run
+    uint32_t best = 1;
+    double least = 0.9 * steps;
+    for (uint32_t n = 2; n <= 512 / tiles && 4 * n <= steps && n <= 64; ++n) {
+        const double t = (tiles * n <= 256 ? 0.9 : 1.4) * ((steps + n - 1) / n) + 3.0 + part * n;
+        if (t < 0.95 * least) best = n, least = t;
+    }
+    return best;
 }
 
 hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStream_t s) {

@@ -145,6 +145,8 @@ struct GemmParams {
     uint32_t r_tiles, c_tiles;
     uint32_t r_limit, c_limit;   // columns of rmat / cmat that can be read, multiples of 8; of a contraction, of 64
     uint32_t steps;         // contraction blocks of 64
+    uint32_t splits;        // runs of them, each a workgroup's (1: none)
+    float *part;            // their parts of the sums
     uint32_t row_block0;    // first row block of a piece of the weight
     uint32_t row_blocks;    // row blocks of the piece
     uint32_t rows, cols;    // N (all parts) and K of one matrix
@@ -192,6 +194,8 @@ struct GemmTile {
 };
 // The tile of a product with `r` by `c` outputs, c in all of `groups` groups.
 GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups);
+// Runs of the contraction (forward and dx, without groups).
+uint32_t gemm_splits(GemmTile tile, uint64_t r_tiles, uint64_t c_tiles, uint64_t steps);
 hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStream_t s);
 hipError_t launch_loss_join(const LossEpi &e, float *loss, float *lse, uint32_t tokens, uint32_t parts, uint64_t vocab,
                             hipStream_t s);

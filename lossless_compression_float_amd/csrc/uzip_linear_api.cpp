@@ -130,8 +130,33 @@ LinearEpi linear_epi(const uzip_weight *w, const uzip_linear_args *a) {
     return e;
 }
 
+// A tiled product's tiles and runs.
+struct Cut {
+    GemmTile tile;
+    uint32_t r_tiles, c_tiles, splits;
+    uint64_t part() const { return splits > 1 ? (uint64_t)splits * r_tiles * c_tiles * tile.r * tile.c : 0; }
+    void set(GemmParams &p, float *part) const {
+        p.r_tiles = r_tiles;
+        p.c_tiles = c_tiles;
+        p.splits = splits;
+        p.part = part;
+    }
+};
+
+// rows: of all parts together, padded to whole blocks in each.
+Cut cut(GemmKind kind, uint64_t rows, uint64_t tokens, uint64_t groups, bool grouped, uint64_t steps) {
+    Cut c{};
+    c.tile = gemm_tile(kind, rows, tokens, groups);
+    c.r_tiles = (uint32_t)blocks(rows, c.tile.r);
+    c.c_tiles = token_tiles(tokens, groups, grouped, c.tile.c);
+    c.splits = grouped ? 1 : gemm_splits(c.tile, c.r_tiles, c.c_tiles, steps);
+    return c;
+}
+
 struct LinearPlan {
     uint16_t *x;
+    float *part;
+    Cut cut;
     bool skinny, stage;
 };
 
@@ -141,6 +166,11 @@ LinearPlan plan_linear(const uzip_weight *w, const uzip_linear_args *a, Carver &
     p.skinny = skinny_fits(a->tokens, groups);
     p.stage = !(p.skinny ? tiled(a->x, a->x_stride, w->cols) : tiled64(a->x, a->x_stride, w->cols));
     if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 64));
+    if (!p.skinny) {
+        const WeightLayout l = weight_layout(w->matrices, w->rows, w->cols, w->gated);
+        p.cut = cut(kGemmForward, l.row_blocks * kTileRows, a->tokens, groups, a->offsets != nullptr, l.col_blocks);
+        if (p.cut.part()) p.part = c.take<float>(p.cut.part());
+    }
     return p;
 }
 
@@ -176,16 +206,14 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
     p.offsets = a->offsets;
     p.groups = groups;
     p.tokens = (uint32_t)a->tokens;
-    const GemmTile tile = gemm_tile(kGemmForward, w->rows, a->tokens, groups);
-    p.r_tiles = (uint32_t)(w->gated ? blocks(p.w.part_blocks, tile.r / 32) : blocks(p.w.part_blocks, tile.r / 16));
-    p.c_tiles = token_tiles(a->tokens, groups, grouped, tile.c);
+    plan.cut.set(p, plan.part);
     p.c_limit = (uint32_t)up(w->cols, 8);
     p.steps = p.w.col_blocks;
     p.row_blocks = p.w.row_blocks;
     p.rows = (uint32_t)w->rows;
     p.cols = (uint32_t)w->cols;
     p.lin = linear_epi(w, a);
-    return done(launch_gemm(kGemmForward, tile, p, stream));
+    return done(launch_gemm(kGemmForward, plan.cut.tile, p, stream));
 }
 
 // ---- backward ---------------------------------------------------------------
@@ -207,7 +235,8 @@ bool backward_ok(const uzip_weight *w, const uzip_linear_backward_args *a, bool 
 
 struct BackwardPlan {
     uint16_t *x, *dz;
-    float *colsum;
+    float *colsum, *part;
+    Cut cut;         // of dx
     uint64_t width;  // padded columns of dz
     uint32_t chunks;
     bool stage_x, make_dz;
@@ -227,6 +256,10 @@ BackwardPlan plan_backward(const uzip_weight *w, const uzip_linear_backward_args
     if (p.make_dz) p.dz = c.take<uint16_t>(a->tokens * p.width);
     if (p.stage_x) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 8));
     if (a->dbias) p.colsum = c.take<float>(groups * p.chunks * p.width);
+    if (a->dx) {
+        p.cut = cut(kGemmDx, w->cols, a->tokens, groups, a->offsets != nullptr, blocks(l.row_blocks, 4));
+        if (p.cut.part()) p.part = c.take<float>(p.cut.part());
+    }
     return p;
 }
 
@@ -275,16 +308,14 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
     p.cmat = plan.make_dz ? Mat{plan.dz, plan.width} : Mat{a->dy, a->dy_stride};
     p.c_limit = (uint32_t)(plan.make_dz ? plan.width : w->rows);
     if (a->dx && a->tokens) {
-        const GemmTile tile = gemm_tile(kGemmDx, w->cols, a->tokens, groups);
-        p.r_tiles = (uint32_t)blocks(w->cols, tile.r);
-        p.c_tiles = token_tiles(a->tokens, groups, grouped, tile.c);
+        plan.cut.set(p, plan.part);
         p.steps = (uint32_t)blocks(v.row_blocks, 4);
         p.store = StoreEpi{};
         p.store.out = static_cast<uint16_t *>(a->dx);
         p.store.stride = a->dx_stride;
         p.store.vec = a->dx_stride % 4 == 0 && aligned(a->dx, 8);
         p.store.clear = a->clear_rest && a->offsets;
-        if (launch_gemm(kGemmDx, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+        if (launch_gemm(kGemmDx, plan.cut.tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     }
     if (a->dw) {
         p.rmat = Mat{a->x, a->x_stride};
@@ -360,6 +391,7 @@ GemmParams loss_params(const uzip_weight *w, const uzip_loss_args *a) {
     GemmParams p{};
     p.w = view(w);
     p.groups = 1;
+    p.splits = 1;
     p.tokens = (uint32_t)a->tokens;
     p.row_blocks = p.w.row_blocks;
     p.rows = (uint32_t)w->rows;
