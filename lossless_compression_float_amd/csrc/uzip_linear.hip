@@ -783,7 +783,9 @@ __device__ inline bool find_group(const GemmParams &p, uint32_t ct, uint32_t edg
 template <GemmKind KIND, bool GATED>
 __device__ inline void emit(const GemmParams &p, uint32_t g, uint32_t c, uint32_t c_end, uint32_t r,
                             float v[GATED ? 2 : 1][4]) {
-    if constexpr (KIND == kGemmForward) {
+    if constexpr (KIND == kGemmLossStat) {
+        return;  // (has an epilogue of its own)
+    } else if constexpr (KIND == kGemmForward) {
         if (c < c_end) linear_out<GATED>(p.lin, (uint64_t)g * p.rows, p.w.part_rows, c, r, v);
     } else if constexpr (KIND == kGemmLossDz) {
         // g (softmax - one at the target), rounded to bf16 for the two products that follow; zeros behind the last row
@@ -890,10 +892,11 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     const uint32_t KB = p.w.col_blocks;
 
     // ---- copies from memory ----
-    // Rows: a copy takes 16 rows.  Cols: 1 KiB of the stage's rows.  What lies behind the last row or column is read
-    // as zeros.
+    // Rows: a copy takes 16 rows.  Cols: 1 KiB of the stage's rows.  What lies behind the last row or column (of Rows:
+    // of the contraction) is read as zeros.
     constexpr int PARTS = C_COPIES + (RK == kCols ? R_COPIES : 0);
     uint32_t c_off[C_COPIES], r_off[RK == kCols ? R_COPIES : 1];
+    const uint32_t c_unit = ((lane & 3) ^ rows_swizzle(lane >> 2)) * 8;  // Rows: this lane's columns of a stage
     auto c_index = [&](int i) __attribute__((always_inline)) -> uint32_t { return (wave * C_COPIES + i) % C_ALL; };
     auto r_index = [&](int i) __attribute__((always_inline)) -> uint32_t { return (wave * R_COPIES + i) % R_ALL; };
     auto cols_off = [&](uint32_t index, uint32_t wide, uint32_t x0, uint32_t limit, uint64_t stride)
@@ -905,8 +908,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
 #pragma unroll
     for (int i = 0; i < C_COPIES; ++i) {
         if constexpr (CK == kRows) {
-            const uint32_t row = c_index(i) * 16 + (lane >> 2), u = (lane & 3) ^ rows_swizzle(row);
-            c_off[i] = (row * (uint32_t)p.cmat.stride + u * 8) * 2;
+            c_off[i] = ((c_index(i) * 16 + (lane >> 2)) * (uint32_t)p.cmat.stride + c_unit) * 2;
         } else {
             c_off[i] = cols_off(c_index(i), TC, c0, p.c_limit, p.cmat.stride);
         }
@@ -920,10 +922,11 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     auto copy_part = [&](uint32_t s, int i) __attribute__((always_inline)) {
         const uint8_t *cp = static_cast<const uint8_t *>(p.cmat.p);
         if constexpr (CK == kRows) {
-            const uint32_t rows = min((uint32_t)TC, c_end - c0), bytes = ((rows - 1) * (uint32_t)p.cmat.stride + S_ALL * 32) * 2;
-            const rsrc_t c = buffer(cp + (uint64_t)c0 * p.cmat.stride * 2 + (uint64_t)(s0 + s) * 64,
-                                    s < S ? bytes - (s0 + s) * 64 : 0);
-            copy_to_lds(c, c_off[i], c_at + (s & 3) * CSTAGE + c_index(i) * 1024);
+            const uint32_t rows = min((uint32_t)TC, c_end - c0), a = (s0 + s) * 32;
+            const uint32_t left = s < S && a < p.c_limit ? p.c_limit - a : 0;  // columns from here on
+            const rsrc_t c = buffer(cp + ((uint64_t)c0 * p.cmat.stride + a) * 2,
+                                    left ? ((rows - 1) * (uint32_t)p.cmat.stride + left) * 2 : 0);
+            copy_to_lds(c, c_unit < left ? c_off[i] : kNowhere, c_at + (s & 3) * CSTAGE + c_index(i) * 1024);
         } else {
             const uint32_t a = a0 + s * 32, rows = s < S ? min(32u, a_end - a) : 0;
             const bool r = i >= C_COPIES;
@@ -1083,29 +1086,34 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
         for (int j = 0; j < FC; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
     if (S > 0) {
+        uint4 heads_first;
         if constexpr (PACKED) {
-            use_heads(0, load_heads(0));
+            heads_first = load_heads(0);
             heads_next = load_heads(64);
-            for (uint32_t d = 0; d < SLOTS; ++d) copy_tile(d);
         }
+        // the decode steps before those of step 0 take their tiles through registers, all at once
+        constexpr uint32_t BEFORE = !PACKED ? 0 : TILES == 1 ? 1 : FWD ? 3 : 2;
+        Tile first[BEFORE ? BEFORE : 1];
+#pragma unroll
+        for (uint32_t d = 0; d < BEFORE; ++d) {
+            bool live;
+            const uint8_t *from = p.w.tiles + tile_index(d, live) * kTileBytes;
+            first[d].sm = *reinterpret_cast<const uint4 *>(from + lane * 16);
+            first[d].code = *reinterpret_cast<const uint2 *>(from + kTileSm + lane * 8);
+        }
+        if constexpr (PACKED)
+            for (uint32_t d = 0; d < SLOTS; ++d) copy_tile(BEFORE + d);
         for (uint32_t s = 0; s < 3; ++s)
 #pragma unroll
             for (int i = 0; i < PARTS; ++i) copy_part(s, i);
-        if constexpr (PACKED) {
-            // the decode steps before those of step 0
-            constexpr uint32_t BEFORE = TILES == 1 ? 1 : FWD ? 3 : 2;
-#pragma unroll 1
-            for (uint32_t d = 0; d < BEFORE; ++d) {
-                wait_copies<0>();
-                Tile t;
-                uint32_t v[8];
-                read_tile(d, t);
-                tile_decode_plain(t, v);
-                store_tile(d, v);
-                mend(d, t.h.x);
-                wait_copies<0>();
-                copy_tile(d + SLOTS);
-            }
+        if constexpr (PACKED) use_heads(0, heads_first);
+#pragma unroll
+        for (uint32_t d = 0; d < BEFORE; ++d) {
+            uint32_t v[8];
+            first[d].h.x = __builtin_amdgcn_readlane(heads.x, d);
+            tile_decode_plain(first[d], v);
+            store_tile(d, v);
+            mend(d, first[d].h.x);
         }
         wait_copies<0>();
         barrier();
@@ -1183,7 +1191,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     }
 
     // ---- epilogues: acc[i][j][d] is row 16 (wr FR + i) + 4 q + d of the tile, column 16 (wc FC + j) + l15 ----
-    if constexpr (KIND == kGemmLossStat) {
+    if (KIND == kGemmLossStat && p.splits == 1) {
         // every token's largest logit in this tile, and the sum of exp(logit - that)
         f32x2 *red = reinterpret_cast<f32x2 *>(lds);  // [WR][TC]
 #pragma unroll
@@ -1223,7 +1231,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
             for (int w = 1; w < WR; ++w) ref = fmaxf(ref, red[w * TC + c][0]);
 #pragma unroll
             for (int w = 0; w < WR; ++w) sum += red[w * TC + c][1] * __expf(red[w * TC + c][0] - ref);
-            p.loss.part[(uint64_t)rt * p.tokens + c0 + c] = make_float2(ref, sum);
+            p.loss.parts[(uint64_t)(c0 + c) * p.r_tiles + rt] = make_float2(ref, sum);
         }
         return;
     }
@@ -1275,7 +1283,9 @@ template <GemmKind KIND, bool GATED>
 __global__ __launch_bounds__(256) void k_join(GemmParams p, uint32_t tr, uint32_t tc) {
     const uint32_t outs = tr / (GATED ? 8 : 4), k = blockIdx.y * 256 + threadIdx.x;
     const uint32_t cl = k / outs, u = k % outs, ct = blockIdx.x / p.r_tiles, rt = blockIdx.x % p.r_tiles;
-    if (cl >= tc || ct * tc + cl >= p.tokens) return;
+    uint32_t g, c0, c_end;
+    if (!find_group(p, ct, tc, threadIdx.x & 63, g, c0, c_end)) return;
+    if (cl >= tc || c0 + cl >= c_end) return;
     float v[GATED ? 2 : 1][4];
 #pragma unroll
     for (int h = 0; h < (GATED ? 2 : 1); ++h) {
@@ -1286,20 +1296,44 @@ __global__ __launch_bounds__(256) void k_join(GemmParams p, uint32_t tr, uint32_
             x += *reinterpret_cast<const f32x4 *>(from + (uint64_t)i * p.r_tiles * p.c_tiles * tr * tc);
         for (int d = 0; d < 4; ++d) v[h][d] = x[d];
     }
-    emit<KIND, GATED>(p, 0, ct * tc + cl, p.tokens, rt * (tr / (GATED ? 2 : 1)) + u * 4, v);
+    emit<KIND, GATED>(p, g, c0 + cl, c_end, rt * (tr / (GATED ? 2 : 1)) + u * 4, v);
+}
+
+// The same for the loss: a column's tr / 4 threads (32 or 64 lanes) find its reference and sum.
+__global__ __launch_bounds__(256) void k_join_stat(GemmParams p, uint32_t tr, uint32_t tc) {
+    const uint32_t outs = tr / 4, k = blockIdx.y * 256 + threadIdx.x;
+    const uint32_t cl = k / outs, u = k % outs, ct = blockIdx.x / p.r_tiles, rt = blockIdx.x % p.r_tiles;
+    const uint32_t m = ct * tc + cl;
+    if (cl >= tc || m >= p.tokens) return;
+    const float *from = p.part + ((uint64_t)blockIdx.x * tc + cl) * tr + u * 4;
+    f32x4 x = *reinterpret_cast<const f32x4 *>(from);
+    for (uint32_t i = 1; i < p.splits; ++i)
+        x += *reinterpret_cast<const f32x4 *>(from + (uint64_t)i * p.r_tiles * p.c_tiles * tr * tc);
+    const int64_t want = p.loss.target[m];
+    float top = -INFINITY;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t n = rt * tr + u * 4 + d;
+        if (n >= p.rows) x[d] = -INFINITY;
+        if ((int64_t)n == want && n < p.rows) p.loss.picked[m] = x[d];
+        top = fmaxf(top, x[d]);
+    }
+    for (uint32_t i = 1; i < outs; i <<= 1) top = fmaxf(top, __shfl_xor(top, i));
+    const float ref = fminf(fmaxf(top, -3.0e38f), 3.0e38f);
+    float sum = ((__expf(x[0] - ref) + __expf(x[1] - ref)) + __expf(x[2] - ref)) + __expf(x[3] - ref);
+    for (uint32_t i = 1; i < outs; i <<= 1) sum += __shfl_xor(sum, i);
+    if (u == 0) p.loss.parts[(uint64_t)m * p.r_tiles + rt] = make_float2(ref, sum);
 }
 
 // ---- the loss's join -------------------------------------------------------------
 
 // A wave per token: reference and sum over the row tiles, in a fixed order.
-__global__ __launch_bounds__(256) void k_loss_join(LossEpi e, float *loss, float *lse, uint32_t tokens, uint32_t parts,
-                                                   uint64_t vocab) {
-    const uint32_t lane = threadIdx.x & 63;
-    const uint32_t m = blockIdx.x * 4 + uniform(threadIdx.x >> 6);
-    if (m >= tokens) return;
+__global__ __launch_bounds__(64) void k_loss_join(LossEpi e, float *loss, float *lse, uint32_t parts, uint64_t vocab) {
+    const uint32_t lane = threadIdx.x, m = blockIdx.x;
     float ref = -3.0e38f, sum = 0;
+#pragma unroll 4
     for (uint32_t i = lane; i < parts; i += 64) {
-        const float2 v = e.part[(uint64_t)i * tokens + m];
+        const float2 v = e.parts[(uint64_t)m * parts + i];
         const float top = fmaxf(ref, v.x);
         sum = sum * expf(ref - top) + v.y * expf(v.x - top);
         ref = top;
@@ -1444,9 +1478,12 @@ hipError_t gemm(GemmTile tile, const GemmParams &p, hipStream_t s) {
         k_gemm<RK, CK, KIND, GATED, 128, 128, 2, 4><<<grid, 512, 0, s>>>(p);
     else if constexpr (KIND != kGemmDw)
         k_gemm<RK, CK, KIND, GATED, 256, 64, 4, 2><<<grid, 512, 0, s>>>(p);
-    if constexpr (KIND == kGemmForward || KIND == kGemmDx)
-        if (p.splits > 1)
-            k_join<KIND, GATED><<<dim3(grid.x, (tile.r * tile.c / (GATED ? 8 : 4) + 255) / 256), 256, 0, s>>>(p, tile.r, tile.c);
+    const dim3 join(grid.x, (tile.r * tile.c / (GATED ? 8 : 4) + 255) / 256);
+    if constexpr (KIND == kGemmLossStat) {
+        if (p.splits > 1) k_join_stat<<<join, 256, 0, s>>>(p, tile.r, tile.c);
+    } else if constexpr (KIND != kGemmDw) {
+        if (p.splits > 1) k_join<KIND, GATED><<<join, 256, 0, s>>>(p, tile.r, tile.c);
+    }
     return hipGetLastError();
 }
 
@@ -1533,7 +1570,7 @@ hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStr
 
 hipError_t launch_loss_join(const LossEpi &e, float *loss, float *lse, uint32_t tokens, uint32_t parts, uint64_t vocab,
                             hipStream_t s) {
-    k_loss_join<<<(tokens + 3) / 4, 256, 0, s>>>(e, loss, lse, tokens, parts, vocab);
+    k_loss_join<<<tokens, 64, 0, s>>>(e, loss, lse, parts, vocab);
     return hipGetLastError();
 }
 

@@ -64,8 +64,6 @@ uint32_t type_size(uint32_t t) { return t == UZIP_FP32 ? 4 : 2; }
 // product can: a tile's rows are addressed with 32 bits.
 bool by16(const void *p, uint64_t stride, uint64_t cols) { return aligned(p, 16) && stride % 8 == 0 && cols % 8 == 0; }
 bool tiled(const void *p, uint64_t stride, uint64_t cols) { return by16(p, stride, cols) && stride < (1u << 22); }
-// The same where its columns are the contraction, which goes in blocks of 64.
-bool tiled64(const void *p, uint64_t stride, uint64_t cols) { return tiled(p, stride, cols) && cols % 64 == 0; }
 
 // Carves a workspace; with a null base it only counts.
 struct Carver {
@@ -149,7 +147,7 @@ Cut cut(GemmKind kind, uint64_t rows, uint64_t tokens, uint64_t groups, bool gro
     c.tile = gemm_tile(kind, rows, tokens, groups);
     c.r_tiles = (uint32_t)blocks(rows, c.tile.r);
     c.c_tiles = token_tiles(tokens, groups, grouped, c.tile.c);
-    c.splits = grouped ? 1 : gemm_splits(c.tile, c.r_tiles, c.c_tiles, steps);
+    c.splits = gemm_splits(c.tile, c.r_tiles, c.c_tiles, steps);
     return c;
 }
 
@@ -164,8 +162,8 @@ LinearPlan plan_linear(const uzip_weight *w, const uzip_linear_args *a, Carver &
     LinearPlan p{};
     const uint64_t groups = a->offsets ? w->matrices : 1;
     p.skinny = skinny_fits(a->tokens, groups);
-    p.stage = !(p.skinny ? tiled(a->x, a->x_stride, w->cols) : tiled64(a->x, a->x_stride, w->cols));
-    if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 64));
+    p.stage = !tiled(a->x, a->x_stride, w->cols);
+    if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 8));
     if (!p.skinny) {
         const WeightLayout l = weight_layout(w->matrices, w->rows, w->cols, w->gated);
         p.cut = cut(kGemmForward, l.row_blocks * kTileRows, a->tokens, groups, a->offsets != nullptr, l.col_blocks);
@@ -183,7 +181,7 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
     const uint32_t groups = grouped ? (uint32_t)w->matrices : 1;
     Mat x{a->x, a->x_stride};
     if (plan.stage) {
-        x = Mat{plan.x, up(w->cols, 64)};
+        x = Mat{plan.x, up(w->cols, 8)};
         const hipError_t e = launch_stage(static_cast<const uint16_t *>(a->x), a->x_stride, plan.x, x.stride, a->tokens,
                                           w->cols, stream);
         if (e != hipSuccess) return UZIP_ERR_DEVICE;
@@ -248,7 +246,7 @@ BackwardPlan plan_backward(const uzip_weight *w, const uzip_linear_backward_args
     BackwardPlan p{};
     p.width = up(l.row_blocks * kTileRows, 64);
     p.make_dz = (a->dx || a->dw) &&
-                (a->act != UZIP_ACT_NONE || a->dy_dtype == UZIP_FP32 || !tiled64(a->dy, a->dy_stride, w->rows));
+                (a->act != UZIP_ACT_NONE || a->dy_dtype == UZIP_FP32 || !tiled(a->dy, a->dy_stride, w->rows));
     p.stage_x = a->dw && !tiled(a->x, a->x_stride, w->cols);
     // runs of rows whose column sums are taken apart: about 2,048 workgroups (of 512 columns), of at least 8 rows
     const uint64_t wide = blocks(w->gated ? l.part_blocks * kTileRows : p.width, 512) * groups;
@@ -353,29 +351,47 @@ bool loss_ok(const uzip_weight *w, const uzip_loss_args *a, bool backward) {
 
 struct LossPlan {
     uint16_t *x;
-    float2 *part;
-    float *picked;
+    float2 *parts;
+    float *picked, *part;
     uint16_t *dz;
     float *sum;
     uint64_t piece;  // rows of the weight in a piece
-    GemmTile tile;
+    Cut cut;         // of the forward product
     bool stage;
 };
 
+// The two products of a backward piece of `rows` weight rows that are cut.
+Cut cut_dz(const uzip_weight *w, const uzip_loss_args *a, uint64_t rows) {
+    return cut(kGemmLossDz, rows, a->tokens, 1, false, blocks(w->cols, kTileCols));
+}
+Cut cut_dx(const uzip_weight *w, const uzip_loss_args *a, uint64_t rows) {
+    return cut(kGemmDx, w->cols, a->tokens, 1, false, blocks(rows, 64));
+}
+
 LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward, Carver &c) {
     LossPlan p{};
-    p.stage = !tiled64(a->x, a->x_stride, w->cols);
-    if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 64));
+    p.stage = !tiled(a->x, a->x_stride, w->cols);
+    if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 8));
     if (!backward) {
-        p.tile = gemm_tile(kGemmLossStat, w->rows, a->tokens, 1);
-        p.part = c.take<float2>(a->tokens * blocks(w->rows, p.tile.r));
+        if (a->tokens == 0) return p;
+        p.cut = cut(kGemmLossStat, w->rows, a->tokens, 1, false, blocks(w->cols, kTileCols));
+        p.parts = c.take<float2>(a->tokens * p.cut.r_tiles);
         p.picked = c.take<float>(a->tokens);
+        if (p.cut.part()) p.part = c.take<float>(p.cut.part());
         return p;
     }
     // a piece's logit gradients take up to 128 MiB, half of what the last-level cache holds, but at least 4,096 rows
     const uint64_t fit = a->tokens ? (128ull << 20) / (2 * a->tokens) / 256 * 256 : 0;
     p.piece = std::min(up(w->rows, 256), std::max<uint64_t>(4096, fit));
+    if (a->tokens == 0) return p;
     p.dz = c.take<uint16_t>(a->tokens * p.piece);
+    uint64_t part = 0;
+    const uint64_t all = up(w->rows, kTileRows);
+    for (uint64_t r0 = 0; r0 < all; r0 += p.piece) {
+        const uint64_t rows = std::min(p.piece, all - r0);
+        part = std::max(part, std::max(cut_dz(w, a, rows).part(), a->dx ? cut_dx(w, a, rows).part() : 0));
+    }
+    if (part) p.part = c.take<float>(part);
     if (a->dx && p.piece < w->rows) p.sum = c.take<float>(a->tokens * up(w->cols, 4));
     return p;
 }
@@ -383,7 +399,7 @@ LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward,
 uzip_status stage_loss_x(const uzip_weight *w, const uzip_loss_args *a, const LossPlan &plan, Mat &x, hipStream_t stream) {
     x = Mat{a->x, a->x_stride};
     if (!plan.stage) return UZIP_OK;
-    x = Mat{plan.x, up(w->cols, 64)};
+    x = Mat{plan.x, up(w->cols, 8)};
     return done(launch_stage(static_cast<const uint16_t *>(a->x), a->x_stride, plan.x, x.stride, a->tokens, w->cols, stream));
 }
 
@@ -507,12 +523,11 @@ uzip_status uzip_linear_cross_entropy(const uzip_weight *weight, const uzip_loss
     GemmParams p = loss_params(weight, args);
     if (stage_loss_x(weight, args, plan, p.cmat, stream) != UZIP_OK) return UZIP_ERR_DEVICE;
     p.c_limit = (uint32_t)up(weight->cols, 8);
-    p.r_tiles = (uint32_t)blocks(weight->rows, plan.tile.r);
-    p.c_tiles = (uint32_t)blocks(args->tokens, plan.tile.c);
+    plan.cut.set(p, plan.part);
     p.steps = p.w.col_blocks;
-    p.loss.part = plan.part;
+    p.loss.parts = plan.parts;
     p.loss.picked = plan.picked;
-    if (launch_gemm(kGemmLossStat, plan.tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+    if (launch_gemm(kGemmLossStat, plan.cut.tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     return done(launch_loss_join(p.loss, args->loss, args->lse, p.tokens, p.r_tiles, weight->rows, stream));
 }
 
@@ -543,20 +558,18 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
         p.row_blocks = std::min(step, all - b0);
         const uint64_t rows = (uint64_t)p.row_blocks * kTileRows;
         if (args->tokens) {
-            const GemmTile tile = gemm_tile(kGemmLossDz, rows, args->tokens, 1);
+            const Cut dz = cut_dz(weight, args, rows);
+            dz.set(p, plan.part);
             p.cmat = x;
             p.c_limit = (uint32_t)up(weight->cols, 8);
-            p.r_tiles = (uint32_t)blocks(rows, tile.r);
-            p.c_tiles = (uint32_t)blocks(args->tokens, tile.c);
             p.steps = p.w.col_blocks;
-            if (launch_gemm(kGemmLossDz, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+            if (launch_gemm(kGemmLossDz, dz.tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
         }
         p.cmat = Mat{plan.dz, plan.piece};
         p.c_limit = (uint32_t)up(rows, 64);  // the product above wrote zeros behind the last row
         if (args->dx && args->tokens) {
-            const GemmTile tile = gemm_tile(kGemmDx, weight->cols, args->tokens, 1);
-            p.r_tiles = (uint32_t)blocks(weight->cols, tile.r);
-            p.c_tiles = (uint32_t)blocks(args->tokens, tile.c);
+            const Cut dx = cut_dx(weight, args, rows);
+            dx.set(p, plan.part);
             p.steps = (uint32_t)blocks(p.row_blocks, 4);
             p.store = StoreEpi{};
             p.store.sum = plan.sum;
@@ -565,7 +578,7 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
             p.store.out = b0 + step >= all ? static_cast<uint16_t *>(args->dx) : nullptr;
             p.store.stride = args->dx_stride;
             p.store.vec = args->dx_stride % 4 == 0 && aligned(args->dx, 8);
-            if (launch_gemm(kGemmDx, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+            if (launch_gemm(kGemmDx, dx.tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
         }
         if (args->dw) {
             const GemmTile tile = gemm_tile(kGemmDw, weight->cols, rows, 1);
