@@ -532,13 +532,17 @@ __device__ inline void clear_rest(const int32_t *offsets, uint32_t groups, uint3
 
 // ---- few rows ---------------------------------------------------------------------
 
-// y = W x for up to 16 MT rows of x at a time.  A workgroup owns RB row blocks
-// of W; its NW waves split K and add their parts in LDS in a fixed order.  The
-// weights go from memory to the matrix instructions without touching LDS, D
-// column blocks ahead.  Headers: lane l of `heads` holds that of the wave's
-// l-th block.  Blocks behind the last are read as zeros, so the loop has no
-// branch but the one for tiles with a list.
-template <int MT, int RB, bool GATED, int NW, int D>
+// y = W x for up to 16 MT rows of x at a time.  Bound by the reads of W: 28672
+// x 4096 gated, 16 rows, 35 us, 5.1 TB/s of packed bytes, as fast as a large
+// copy.  A workgroup owns RB row blocks of W; its NW waves split K and add their
+// parts in LDS in a fixed order.  The weights go from memory to the matrix
+// instructions without touching LDS; a wave has one column block on its way and
+// the bytes in flight come from the number of waves (blocks loaded two or four
+// ahead took more registers, so fewer waves, and were slower: one row of 4096 x
+// 4096 9.1 and 12.2 us against 8.3).  Headers: lane l of `heads` holds that of
+// the wave's l-th block.  What lies behind the last block, row or column is read
+// as zeros.
+template <int MT, int RB, bool GATED, int NW>
 __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
     __shared__ f32x4 part[NW][RB * MT * 64];
     const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -571,43 +575,42 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
         const uint32_t here = min(end - m0, 16u * MT);
         const rsrc_t xb = buffer(static_cast<const uint8_t *>(p.x.p) + (uint64_t)m0 * p.x.stride * 2,
                                  ((here - 1) * (uint32_t)p.x.stride + p.cols) * 2);
-        Tile t[D][RB];
-        uint4 x[D][MT][2];
-        uint4 heads[RB];
-        auto load = [&](uint32_t k, int d) __attribute__((always_inline)) {
+        Tile t[RB];
+        uint4 x[MT][2], heads[RB];
+        auto load = [&](uint32_t k) __attribute__((always_inline)) {
             const uint32_t kb = wave + k * NW;
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 const uint32_t at = kb < KB ? kb * kTileBytes : KB * kTileBytes;
-                t[d][i].sm = read16(rows[i], at + lane * 16);
-                t[d][i].code = read8(rows[i], at + kTileSm + lane * 8);
+                t[i].sm = read16(rows[i], at + lane * 16);
+                t[i].code = read8(rows[i], at + kTileSm + lane * 8);
             }
 #pragma unroll
             for (int j = 0; j < MT; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t c = kb * kTileCols + h * 32 + q * 8, m = j * 16 + r;
-                    x[d][j][h] = read16(xb, m < here && c < p.cols ? (m * (uint32_t)p.x.stride + c) * 2 : kNowhere);
+                    x[j][h] = read16(xb, m < here && c < p.cols ? (m * (uint32_t)p.x.stride + c) * 2 : kNowhere);
                 }
         };
-        auto multiply = [&](uint32_t k, int d) __attribute__((always_inline)) {
+        auto multiply = [&](uint32_t k) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 uint32_t v[8];
-                t[d][i].h.x = __builtin_amdgcn_readlane(heads[i].x, k & 63);
-                tile_decode_plain(t[d][i], v);
-                if (t[d][i].h.x & (0xFF00u | kTileZero)) {
-                    t[d][i].h.y = __builtin_amdgcn_readlane(heads[i].y, k & 63);
-                    t[d][i].h.z = __builtin_amdgcn_readlane(heads[i].z, k & 63);
-                    t[d][i].h.w = __builtin_amdgcn_readlane(heads[i].w, k & 63);
-                    tile_decode(t[d][i], p.w, lane, v);
+                t[i].h.x = __builtin_amdgcn_readlane(heads[i].x, k & 63);
+                tile_decode_plain(t[i], v);
+                if (t[i].h.x & (0xFF00u | kTileZero)) {
+                    t[i].h.y = __builtin_amdgcn_readlane(heads[i].y, k & 63);
+                    t[i].h.z = __builtin_amdgcn_readlane(heads[i].z, k & 63);
+                    t[i].h.w = __builtin_amdgcn_readlane(heads[i].w, k & 63);
+                    tile_decode(t[i], p.w, lane, v);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, x[d][j][h]),
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, x[j][h]),
                                                                             acc[i][j], 0, 0, 0);
                 }
             }
@@ -617,8 +620,7 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
             for (int i = 0; i < RB; ++i) heads[i] = p.w.head[tile0[i] + min(wave + (k0 + lane) * NW, KB - 1)];
         };
         load_heads(0);  // (first: loads come back in order)
-#pragma unroll
-        for (int d = 0; d < D; ++d) load(d, d);
+        load(0);
         for (uint32_t k0 = 0; k0 < n; k0 += 64) {
             if (k0) load_heads(k0);
 #pragma unroll
@@ -626,12 +628,9 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
                 heads[i] = head_checked(p.w, heads[i]);
                 if (wave + (k0 + lane) * NW >= KB) heads[i].x = 0;
             }
-            for (uint32_t k = k0; k < min(n, k0 + 64); k += D) {  // (64 is a multiple of D)
-#pragma unroll
-                for (int d = 0; d < D; ++d) {
-                    multiply(k + d, d);
-                    load(k + d + D, d);
-                }
+            for (uint32_t k = k0; k < min(n, k0 + 64); ++k) {
+                multiply(k);
+                load(k + 1);
             }
         }
 #pragma unroll
@@ -1461,11 +1460,11 @@ __global__ __launch_bounds__(256) void k_dbias(DzParams p) {
         static_cast<uint16_t *>(p.dbias)[o] = to_bf16(s);
 }
 
-template <int MT, int RB, bool GATED, int NW, int D>
+template <int MT, int RB, bool GATED, int NW>
 hipError_t skinny(const SkinnyParams &p, hipStream_t s) {
     const uint32_t per = GATED ? RB / 2 : RB;
     const dim3 grid((p.w.part_blocks + per - 1) / per, p.groups);
-    k_skinny<MT, RB, GATED, NW, D><<<grid, NW * 64, 0, s>>>(p);
+    k_skinny<MT, RB, GATED, NW><<<grid, NW * 64, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -1512,21 +1511,34 @@ hipError_t launch_stage(const uint16_t *in, uint64_t in_stride, uint16_t *out, u
     return hipGetLastError();
 }
 
-bool skinny_fits(uint64_t tokens, uint64_t groups) { return groups == 1 ? tokens <= 64 : tokens <= 16 * groups; }
+// Rows of x for which the skinny product is faster than the tiled one: it
+// reads all of x once a workgroup.  64 rows: 20 against 22 us on 4096 x 4096,
+// but 58 against 39 us on 4096 x 14336.
+bool skinny_fits(uint64_t tokens, uint64_t groups, uint64_t col_blocks) {
+    if (groups > 1) return tokens <= 16 * groups;
+    return tokens <= 32 || (tokens <= 64 && col_blocks <= 128);
+}
 
 // Waves and row blocks of a workgroup: with rows enough to fill the chip, few
 // waves that share their reads of x (4096 x 4096 over 13 experts: 62 us, 5.3
-// TB/s, against 84 us with one row block and 16 waves); with fewer rows, many
-// waves, for the bytes in flight (one 4096 x 4096 matrix: 8.3 against 12.0 us).
+// TB/s, against 84 us with one row block and 16 waves; 32 rows, 28672 x 4096
+// gated: 42 against 57 us); with fewer rows, many waves, for the bytes in
+// flight (one 4096 x 4096 matrix, one row: 8.3 against 12.0 us; 64 rows: 20
+// against 26 us).
 hipError_t launch_skinny(const SkinnyParams &p, hipStream_t s) {
-    const bool one = p.groups > 1 || p.tokens <= 16;
+    const uint32_t rows = p.groups > 1 ? 16 : p.tokens;
     const uint64_t blocks = (uint64_t)p.w.part_blocks * p.groups;
     if (p.lin.act == kActSwiglu) {
-        if (one) return blocks >= 512 ? skinny<1, 4, true, 4, 1>(p, s) : skinny<1, 2, true, 8, 1>(p, s);
-        return p.tokens <= 32 ? skinny<2, 2, true, 8, 2>(p, s) : skinny<4, 2, true, 8, 1>(p, s);
+        if (blocks < 512) {
+            if (rows <= 16) return skinny<1, 2, true, 8>(p, s);
+            return rows <= 32 ? skinny<2, 2, true, 8>(p, s) : skinny<4, 2, true, 8>(p, s);
+        }
+        if (rows <= 16) return skinny<1, 4, true, 4>(p, s);
+        return rows <= 32 ? skinny<2, 4, true, 4>(p, s) : skinny<4, 4, true, 4>(p, s);
     }
-    if (one) return blocks >= 1024 ? skinny<1, 2, false, 8, 1>(p, s) : skinny<1, 1, false, 16, 1>(p, s);
-    return p.tokens <= 32 ? skinny<2, 1, false, 16, 2>(p, s) : skinny<4, 2, false, 8, 1>(p, s);
+    if (rows <= 16) return blocks >= 1024 ? skinny<1, 2, false, 8>(p, s) : skinny<1, 1, false, 16>(p, s);
+    if (rows <= 32) return blocks >= 768 ? skinny<2, 2, false, 8>(p, s) : skinny<2, 1, false, 8>(p, s);
+    return blocks >= 768 ? skinny<4, 4, false, 8>(p, s) : skinny<4, 1, false, 8>(p, s);
 }
 
 GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups) {

@@ -185,8 +185,7 @@ hipError_t launch_unpack(const UnpackParams &p, hipStream_t s);
 hipError_t launch_stage(const uint16_t *in, uint64_t in_stride, uint16_t *out, uint64_t out_stride, uint64_t rows,
                         uint64_t cols, hipStream_t s);
 hipError_t launch_skinny(const SkinnyParams &p, hipStream_t s);
-// rows a call may have for the skinny kernel
-bool skinny_fits(uint64_t tokens, uint64_t groups);
+bool skinny_fits(uint64_t tokens, uint64_t groups, uint64_t col_blocks);
 enum GemmKind { kGemmForward, kGemmLossStat, kGemmLossDz, kGemmDx, kGemmDw };
 // Outputs of a workgroup: r by c.
 struct GemmTile {

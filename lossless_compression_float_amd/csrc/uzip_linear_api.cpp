@@ -161,7 +161,7 @@ struct LinearPlan {
 LinearPlan plan_linear(const uzip_weight *w, const uzip_linear_args *a, Carver &c) {
     LinearPlan p{};
     const uint64_t groups = a->offsets ? w->matrices : 1;
-    p.skinny = skinny_fits(a->tokens, groups);
+    p.skinny = skinny_fits(a->tokens, groups, blocks(w->cols, kTileCols));
     p.stage = !tiled(a->x, a->x_stride, w->cols);
     if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 8));
     if (!p.skinny) {
