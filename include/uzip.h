@@ -330,8 +330,9 @@ uzip_status uzip_decompress_batched_timed(uzip_dtype dtype, size_t num_buffers, 
  * its own workspace and outputs.  Sums are taken in fp32 in a fixed order: the
  * same call gives the same bits.  Rows of a bf16 or fp32 matrix may be any
  * stride apart (in values, at least the row's length); unaligned or odd ones
- * cost a copy.  At most 2^31 - 1 rows, columns or tokens, 65,535 matrices and
- * 2^25 tiles a stack.  No argument may overlap an output.
+ * cost a copy.  Limits: 2^31 - 1 rows or columns, 65,535 matrices and 2^25
+ * tiles a stack; 2^25 tokens a call, and 2^22 tiles of 128 by 64 outputs.  No
+ * argument may overlap an output.
  * UZIP_ERR_CAPACITY: packed capacity below uzip_weight_max_size. */
 typedef struct {
     const void *data;   /* device, 16-byte aligned, as uzip_weight_pack wrote it */

@@ -18,6 +18,10 @@ constexpr uint64_t kAlign = 256;
 constexpr uint64_t kMaxDim = 0x7FFFFFFF;
 constexpr uint64_t kMaxMatrices = 65535;
 constexpr uint64_t kMaxTiles = 1ull << 25;
+// Limits of a call: its launch grids stay within the 2^32 - 1 work-items of one
+// grid dimension (512 threads a tile of at least 128 by 64 outputs).
+constexpr uint64_t kMaxTokens = 1ull << 25;
+constexpr uint64_t kMaxOutputTiles = 1ull << 22;
 
 uint64_t up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 uint64_t blocks(uint64_t v, uint64_t a) { return (v + a - 1) / a; }
@@ -55,6 +59,12 @@ WeightView view(const uzip_weight *w) {
 bool mat_ok(const void *p, uint64_t stride, uint64_t rows, uint64_t cols, uint32_t elem) {
     if (rows == 0) return true;
     return p && aligned(p, elem) && stride >= cols && stride < (1ull << 40);
+}
+
+// Whether products of `tokens` rows with this weight, and their gradients, fit the limits.
+bool call_ok(const uzip_weight *w, uint64_t tokens) {
+    const uint64_t wide = std::max(blocks(w->rows, 128) + 1, blocks(w->cols, 128));
+    return tokens <= kMaxTokens && wide * (tokens / 64 + w->matrices + 1) <= kMaxOutputTiles;
 }
 
 bool type_ok(uint32_t t) { return t == UZIP_BF16 || t == UZIP_FP32; }
@@ -96,7 +106,7 @@ uint32_t token_tiles(uint64_t tokens, uint64_t groups, bool grouped, uint64_t ed
 bool linear_ok(const uzip_weight *w, const uzip_linear_args *a, bool grouped) {
     if (!weight_ok(w) || !a || a->clear_rest > 1 || a->reserved) return false;
     if (grouped ? !a->offsets || !aligned(a->offsets, 4) || a->residual : a->offsets || w->matrices != 1) return false;
-    if (a->tokens > kMaxDim || !type_ok(a->y_dtype) || a->act > UZIP_ACT_SWIGLU) return false;
+    if (!call_ok(w, a->tokens) || !type_ok(a->y_dtype) || a->act > UZIP_ACT_SWIGLU) return false;
     if ((a->act == UZIP_ACT_SWIGLU) != (w->gated == 1)) return false;
     const uint64_t out = w->rows / (w->gated + 1);
     if (!mat_ok(a->x, a->x_stride, a->tokens, w->cols, 2) || !mat_ok(a->y, a->y_stride, a->tokens, out, type_size(a->y_dtype)))
@@ -219,7 +229,7 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
 bool backward_ok(const uzip_weight *w, const uzip_linear_backward_args *a, bool grouped) {
     if (!weight_ok(w) || !a || a->clear_rest > 1 || a->reserved) return false;
     if (grouped ? !a->offsets || !aligned(a->offsets, 4) : a->offsets || w->matrices != 1) return false;
-    if (a->tokens > kMaxDim || !type_ok(a->dy_dtype) || a->act > UZIP_ACT_SWIGLU) return false;
+    if (!call_ok(w, a->tokens) || !type_ok(a->dy_dtype) || a->act > UZIP_ACT_SWIGLU) return false;
     if ((a->act == UZIP_ACT_SWIGLU) != (w->gated == 1)) return false;
     const uint64_t out = w->rows / (w->gated + 1);
     if (!mat_ok(a->dy, a->dy_stride, a->tokens, out, type_size(a->dy_dtype))) return false;
@@ -339,7 +349,7 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
 // ---- loss -------------------------------------------------------------------
 
 bool loss_ok(const uzip_weight *w, const uzip_loss_args *a, bool backward) {
-    if (!weight_ok(w) || !a || w->matrices != 1 || w->gated || a->tokens > kMaxDim) return false;
+    if (!weight_ok(w) || !a || w->matrices != 1 || w->gated || !call_ok(w, a->tokens)) return false;
     if (a->tokens == 0) return !(backward && a->dw) || aligned(a->dw, 2);
     if (!mat_ok(a->x, a->x_stride, a->tokens, w->cols, 2) || !a->target || !aligned(a->target, 8)) return false;
     if (!a->lse || !aligned(a->lse, 4)) return false;

@@ -107,6 +107,17 @@ def test_linear_argument_errors(grouped):
     assert fn(w, linear_args(tokens=0, x=None, y=None, **off), FAKE, need, None) == uz.UZIP_OK
 
 
+def test_calls_beyond_the_launch_grids_are_refused():
+    big = 1 << 40
+    w = weight(rows=1 << 20, cols=64)
+    for tokens in [1 << 20, (1 << 25) + 1, 1 << 63]:
+        a = linear_args(tokens=tokens, y_stride=1 << 20)
+        assert uz.uzip_linear(w, a, FAKE, big, None) == INVALID
+        assert uz.uzip_linear_backward(w, backward_args(tokens=tokens, dy_stride=1 << 20), FAKE, big, None) == INVALID
+        assert uz.uzip_linear_cross_entropy(w, loss_args(tokens=tokens), FAKE, big, None) == INVALID
+    assert uz.uzip_linear(weight(), linear_args(tokens=(1 << 25) + 1), FAKE, big, None) == INVALID
+
+
 def test_linear_workspace_holds_a_copy_of_rows_that_cannot_be_read_whole():
     small = uz.uzip_linear_workspace_size(weight(), linear_args(tokens=1000))
     for kw in [dict(x=FAKE + 2), dict(x_stride=65)]:
