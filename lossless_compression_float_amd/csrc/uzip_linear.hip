@@ -406,77 +406,100 @@ __device__ inline float activate_grad(float z, uint32_t act) {
 
 // ---- forward epilogue -----------------------------------------------------------
 
-// Four consecutive outputs n .. n + 3 of one row, of which the first `count`
-// exist.  All sums are in fp32; y and the kept pre-activation are each rounded
-// once, from the unrounded values.
-__device__ inline void load4(const void *p, uint64_t at, bool f32, bool vec, uint32_t count, float v[4]) {
+// W (1, 4 or 8) consecutive values at `at`, of which the first `count` exist;
+// those from `count` on are read as zeros.  vec: all of them in whole units.
+template <int W>
+__device__ inline void load(const void *p, uint64_t at, bool f32, bool vec, uint32_t count, float v[W]) {
     if (f32) {
         const float *s = static_cast<const float *>(p) + at;
-        if (vec) {
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(s);
-            for (int i = 0; i < 4; ++i) v[i] = x[i];
+        if (W > 1 && vec) {
+#pragma unroll
+            for (int k = 0; k + 4 <= W; k += 4) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(s + k);
+                for (int i = 0; i < 4; ++i) v[k + i] = x[i];
+            }
         } else {
-            for (uint32_t i = 0; i < 4; ++i) v[i] = i < count ? s[i] : 0.0f;
+#pragma unroll
+            for (uint32_t i = 0; i < W; ++i) v[i] = i < count ? s[i] : 0.0f;
         }
     } else {
         const uint16_t *s = static_cast<const uint16_t *>(p) + at;
-        if (vec) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(s);
-            v[0] = bf16_lo(x.x), v[1] = bf16_hi(x.x), v[2] = bf16_lo(x.y), v[3] = bf16_hi(x.y);
+        if (W > 1 && vec) {
+            uint32_t x[W / 2 + 1];
+            if constexpr (W == 8)
+                *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(s);
+            else if constexpr (W == 4)
+                *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(s);
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = i & 1 ? bf16_hi(x[i / 2]) : bf16_lo(x[i / 2]);
         } else {
-            for (uint32_t i = 0; i < 4; ++i) v[i] = i < count ? from_bf16(s[i]) : 0.0f;
+#pragma unroll
+            for (uint32_t i = 0; i < W; ++i) v[i] = i < count ? from_bf16(s[i]) : 0.0f;
         }
     }
 }
 
-__device__ inline void store4(void *p, uint64_t at, bool f32, bool vec, uint32_t count, const float v[4]) {
+template <int W>
+__device__ inline void store(void *p, uint64_t at, bool f32, bool vec, uint32_t count, const float v[W]) {
     if (f32) {
         float *d = static_cast<float *>(p) + at;
-        if (vec) {
-            *reinterpret_cast<f32x4 *>(d) = f32x4{v[0], v[1], v[2], v[3]};
+        if (W > 1 && vec) {
+#pragma unroll
+            for (int k = 0; k + 4 <= W; k += 4) *reinterpret_cast<f32x4 *>(d + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
         } else {
-            for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+            for (uint32_t i = 0; i < W; ++i)
                 if (i < count) d[i] = v[i];
         }
     } else {
         uint16_t *d = static_cast<uint16_t *>(p) + at;
-        if (vec) {
-            *reinterpret_cast<uint2 *>(d) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        if (W > 1 && vec) {
+            if constexpr (W == 8)
+                *reinterpret_cast<uint4 *>(d) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                           pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+            else if constexpr (W == 4)
+                *reinterpret_cast<uint2 *>(d) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
         } else {
-            for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+            for (uint32_t i = 0; i < W; ++i)
                 if (i < count) d[i] = to_bf16(v[i]);
         }
     }
 }
 
-// z[0]: the product's values (gate rows when gated), z[1]: the up rows.
-template <bool GATED>
+// W consecutive outputs n .. n + W - 1 of row m.  z[0]: the product's values
+// (of the gate's rows when gated), z[1]: of the up rows.  All sums are in fp32;
+// y and the kept pre-activation are each rounded once, from the unrounded
+// values.
+template <bool GATED, int W>
 __device__ inline void linear_out(const LinearEpi &e, uint64_t bias_at, uint32_t part_rows, uint64_t m, uint32_t n,
-                                  float z[GATED ? 2 : 1][4]) {
+                                  float z[GATED ? 2 : 1][W]) {
     if (n >= part_rows) return;
-    const uint32_t count = part_rows - n < 4 ? part_rows - n : 4;
-    const bool vec = e.vec && count == 4;
+    const uint32_t count = part_rows - n < W ? part_rows - n : W;
+    const bool vec = e.vec % W == 0 && count == W;
 #pragma unroll
     for (int h = 0; h < (GATED ? 2 : 1); ++h) {
         if (e.bias) {
-            float b[4];
-            load4(e.bias, bias_at + h * part_rows + n, e.bias_f32, vec, count, b);
-            for (int i = 0; i < 4; ++i) z[h][i] += b[i];
+            float b[W];
+            load<W>(e.bias, bias_at + h * part_rows + n, e.bias_f32, vec, count, b);
+            for (int i = 0; i < W; ++i) z[h][i] += b[i];
         }
-        if (e.preact) store4(e.preact, m * e.preact_stride + h * part_rows + n, e.preact_f32, vec, count, z[h]);
+        if (e.preact) store<W>(e.preact, m * e.preact_stride + h * part_rows + n, e.preact_f32, vec, count, z[h]);
     }
-    float y[4];
+    float y[W];
     if (GATED) {
-        for (int i = 0; i < 4; ++i) y[i] = z[0][i] * sigmoid(z[0][i]) * z[GATED ? 1 : 0][i];
+        for (int i = 0; i < W; ++i) y[i] = z[0][i] * sigmoid(z[0][i]) * z[GATED ? 1 : 0][i];
+    } else if (e.act == kActNone) {
+        for (int i = 0; i < W; ++i) y[i] = z[0][i];
     } else {
-        for (int i = 0; i < 4; ++i) y[i] = activate(z[0][i], e.act);
+        for (int i = 0; i < W; ++i) y[i] = activate(z[0][i], e.act);
     }
     if (e.residual) {
-        float r[4];
-        load4(e.residual, m * e.residual_stride + n, e.y_f32, vec, count, r);
-        for (int i = 0; i < 4; ++i) y[i] += r[i];
+        float r[W];
+        load<W>(e.residual, m * e.residual_stride + n, e.y_f32, vec, count, r);
+        for (int i = 0; i < W; ++i) y[i] += r[i];
     }
-    store4(e.y, m * e.y_stride + n, e.y_f32, vec, count, y);
+    store<W>(e.y, m * e.y_stride + n, e.y_f32, vec, count, y);
 }
 
 // Rows [begin, end) of group g: offsets are clamped to the rows that exist, so
@@ -651,7 +674,7 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
             const uint32_t b = GATED ? blockIdx.x * (RB / 2) + i / 2 : blockIdx.x * RB + i;
             const uint32_t m = m0 + j * 16 + (l & 15);
             if (m < end && b < p.w.part_blocks)
-                linear_out<GATED>(p.lin, (uint64_t)blockIdx.y * p.rows, p.w.part_rows, m, b * 16 + (l >> 4) * 4, z);
+                linear_out<GATED, 4>(p.lin, (uint64_t)blockIdx.y * p.rows, p.w.part_rows, m, b * 16 + (l >> 4) * 4, z);
         }
         __syncthreads();
     }
@@ -778,51 +801,51 @@ __device__ inline bool find_group(const GemmParams &p, uint32_t ct, uint32_t edg
     return false;
 }
 
-// Four results of column c, rows r .. r + 3 (of the tile's kind of rows).
-template <GemmKind KIND, bool GATED>
+// W results of column c, rows r .. r + W - 1 (of the tile's kind of rows).
+template <GemmKind KIND, bool GATED, int W>
 __device__ inline void emit(const GemmParams &p, uint32_t g, uint32_t c, uint32_t c_end, uint32_t r,
-                            float v[GATED ? 2 : 1][4]) {
+                            float v[GATED ? 2 : 1][W]) {
     if constexpr (KIND == kGemmLossStat) {
         return;  // (has an epilogue of its own)
     } else if constexpr (KIND == kGemmForward) {
-        if (c < c_end) linear_out<GATED>(p.lin, (uint64_t)g * p.rows, p.w.part_rows, c, r, v);
+        if (c < c_end) linear_out<GATED, W>(p.lin, (uint64_t)g * p.rows, p.w.part_rows, c, r, v);
     } else if constexpr (KIND == kGemmLossDz) {
         // g (softmax - one at the target), rounded to bf16 for the two products that follow; zeros behind the last row
         if (c >= c_end) return;
         const int64_t want = p.loss.target[c];
         const bool counts = want != p.loss.ignore && want >= 0 && want < (int64_t)p.rows;
         const float gr = counts ? p.loss.dloss[c] : 0.0f, lse = p.loss.lse[c];
+        const uint32_t n = p.row_block0 * 16 + r, hit = counts ? (uint32_t)want - n : W;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const uint32_t n = p.row_block0 * 16 + r + d;
+        for (int d = 0; d < W; ++d) {
             float e = __expf(v[0][d] - lse);
-            if ((int64_t)n == want) e -= 1.0f;
-            v[0][d] = n < p.rows && counts ? gr * e : 0.0f;
+            if ((uint32_t)d == hit) e -= 1.0f;
+            v[0][d] = n + d < p.rows && counts ? gr * e : 0.0f;
         }
-        store4(p.loss.dz, (uint64_t)c * p.loss.dz_stride + r, false, true, 4, v[0]);
+        store<W>(p.loss.dz, (uint64_t)c * p.loss.dz_stride + r, false, true, W, v[0]);
     } else {
         const StoreEpi &e = p.store;
         uint64_t row = c;
         if constexpr (KIND == kGemmDw) {
             // padded row of the stack's part -> row of the matrix; pieces start at row_block0
-            const uint32_t n = c + p.row_block0 * 16, pad = p.w.part_blocks * 16, part = n / pad, in = n - part * pad;
+            const uint32_t n = c + p.row_block0 * 16, pad = p.w.part_blocks * 16, part = n >= pad ? 1 : 0, in = n - part * pad;
             if (in >= p.w.part_rows || part >= p.w.parts || c >= p.row_blocks * 16) return;
             row = (uint64_t)g * p.rows + (uint64_t)part * p.w.part_rows + in;
         } else {
             if (c >= c_end) return;
         }
         if (r >= p.cols) return;
-        const uint32_t count = p.cols - r < 4 ? p.cols - r : 4;
+        const uint32_t count = p.cols - r < W ? p.cols - r : W;
         if (e.sum) {
-            const bool sv = count == 4;  // the sums' stride is a multiple of four
+            const bool sv = count == W;  // the sums' stride is a multiple of eight
             if (e.add) {
-                float o[4];
-                load4(e.sum, row * e.sum_stride + r, true, sv, count, o);
-                for (int d = 0; d < 4; ++d) v[0][d] += o[d];
+                float o[W];
+                load<W>(e.sum, row * e.sum_stride + r, true, sv, count, o);
+                for (int d = 0; d < W; ++d) v[0][d] += o[d];
             }
-            if (!e.out) store4(e.sum, row * e.sum_stride + r, true, sv, count, v[0]);
+            if (!e.out) store<W>(e.sum, row * e.sum_stride + r, true, sv, count, v[0]);
         }
-        if (e.out) store4(e.out, row * e.stride + r, false, e.vec && count == 4, count, v[0]);
+        if (e.out) store<W>(e.out, row * e.stride + r, false, e.vec % W == 0 && count == W, count, v[0]);
     }
 }
 
@@ -1193,22 +1216,33 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     if (KIND == kGemmLossStat && p.splits == 1) {
         // every token's largest logit in this tile, and the sum of exp(logit - that)
         f32x2 *red = reinterpret_cast<f32x2 *>(lds);  // [WR][TC]
+        const uint32_t n0 = rt * TR + wr * FR * 16 + q * 4;
+        if (rt * TR + TR > p.rows) {  // rows behind the last
+#pragma unroll
+            for (int i = 0; i < FR; ++i)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    if (n0 + i * 16 + d >= p.rows)
+                        for (int j = 0; j < FC; ++j) acc[i][j][d] = -INFINITY;
+        }
 #pragma unroll
         for (int j = 0; j < FC; ++j) {
             const uint32_t m = c0 + (wc * FC + j) * 16 + l15;
-            const bool live = m < c_end;
-            const int64_t want = live ? p.loss.target[m] : -1;
-            const uint32_t n0 = rt * TR + wr * FR * 16 + q * 4;
+            // the target, where it is one of this lane's rows
+            const int64_t want = m < c_end ? p.loss.target[m] : -1;
+            const uint32_t hit = want >= 0 && want < (int64_t)p.rows ? (uint32_t)want - n0 : FR * 16;
+            if (hit < FR * 16 && (hit & 15) < 4) {
+#pragma unroll
+                for (int i = 0; i < FR; ++i)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        if (hit == (uint32_t)(i * 16 + d)) p.loss.picked[m] = acc[i][j][d];
+            }
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < FR; ++i)
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const uint32_t n = n0 + i * 16 + d;
-                    if (n >= p.rows) acc[i][j][d] = -INFINITY;
-                    if (live && (int64_t)n == want && n < p.rows) p.loss.picked[m] = acc[i][j][d];
-                    top = fmaxf(top, acc[i][j][d]);
-                }
+                for (int d = 0; d < 4; ++d) top = fmaxf(top, acc[i][j][d]);
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             // a finite reference, whatever the logits: exp of -inf, +inf and NaN then say what they should
@@ -1235,44 +1269,66 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
         return;
     }
 
-    // The others go through LDS, as many fragments of columns at a time as fit, so that a column's rows leave in one
-    // run: a wave's part is [columns][16 FR] values in units of four, the unit's place xored with the column against
-    // bank conflicts.
-    constexpr int UNITS = FR * 4, BYTES = RING / WAVES / 16 * 16, FIT = BYTES / (FR * 1024);
-    constexpr int JP = FIT >= FC ? FC : FIT >= 2 && FC % 2 == 0 ? 2 : 1, SWZ = UNITS < 16 ? UNITS - 1 : 15;
-    static_assert(FIT >= 1, "a fragment of columns fits");
-    f32x4 *out = reinterpret_cast<f32x4 *>(lds + wave * BYTES);
+    // The others go through LDS, some fragments of columns at a time, so that a column's rows of the whole tile leave in
+    // one run of 16 bytes a lane (256 bytes a wave and column, from registers in two halves, took 18 us a tile of 256 x
+    // 256 instead of 7): [columns][TR] values for each wc, in units of four, the unit's place xored with the column
+    // against bank conflicts.  The WR waves of a wc share its columns.
+    constexpr int UNITS = TR / 4, FIT = RING / WC / (TR * 64);
+    constexpr int JP = FIT >= FC ? FC : FIT >= 2 && FC % 2 == 0 ? 2 : 1;  // fragments at a time
+    constexpr int COLS = JP * 16 / WR;                                    // columns of a wave
+    constexpr int ROWS = TR / (GATED ? 2 : 1), LANES = ROWS / 8;          // results of a column, lanes for them
+    static_assert(FIT >= 1 && JP * 16 % WR == 0 && COLS * LANES % 64 == 0, "whole waves");
+    f32x4 *out = reinterpret_cast<f32x4 *>(lds + wc * (JP * TR * 64));
 #pragma unroll
     for (int ph = 0; ph < FC; ph += JP) {
+        if (ph) __syncthreads();
 #pragma unroll
         for (int j = 0; j < JP; ++j)
 #pragma unroll
-            for (int i = 0; i < FR; ++i) out[(j * 16 + l15) * UNITS + ((i * 4 + q) ^ (l15 & SWZ))] = acc[i][ph + j];
+            for (int i = 0; i < FR; ++i)
+                out[(j * 16 + l15) * UNITS + ((wr * FR * 4 + i * 4 + q) ^ l15)] = acc[i][ph + j];
+        __syncthreads();
+        const uint32_t cb = (wc * FC + ph) * 16;  // the first column
         if (KIND != kGemmDw && p.splits > 1) {
             // a run's part of the sums: [run][tile][column][row]
-            float *to = p.part + ((uint64_t)blockIdx.y * total + ct * p.r_tiles + rt) * (TR * TC) +
-                        (wc * FC + ph) * 16 * TR + wr * FR * 16;
-#pragma unroll 1
-            for (uint32_t k = lane; k < JP * 16 * UNITS; k += 64) {
-                const uint32_t cl = k / UNITS, u = k % UNITS;
-                *reinterpret_cast<f32x4 *>(to + cl * TR + u * 4) = out[cl * UNITS + (u ^ (cl & SWZ))];
+            float *to = p.part + ((uint64_t)blockIdx.y * total + ct * p.r_tiles + rt) * (TR * TC);
+#pragma unroll 4
+            for (uint32_t k = lane; k < COLS * UNITS; k += 64) {
+                const uint32_t cl = wr * COLS + k / UNITS, u = k % UNITS;
+                *reinterpret_cast<f32x4 *>(to + (cb + cl) * TR + u * 4) = out[cl * UNITS + (u ^ (cl & 15))];
             }
             continue;
         }
-        constexpr int OUTS = GATED ? UNITS / 2 : UNITS;  // results of a column, in units of four
-#pragma unroll 1
-        for (uint32_t k = lane; k < JP * 16 * OUTS; k += 64) {
-            const uint32_t cl = k / OUTS, u = k % OUTS;
-            float v[GATED ? 2 : 1][4];
+        if (KIND != kGemmLossDz && (KIND == kGemmForward ? p.lin.vec : p.store.vec) != 8) {
+            // a lane a value, so that rows that no unit fits still leave in runs
+            const float *from = reinterpret_cast<const float *>(out);
+#pragma unroll 2
+            for (uint32_t k = lane; k < COLS * ROWS; k += 64) {
+                const uint32_t cl = wr * COLS + k / ROWS, r = k % ROWS;
+                float v[GATED ? 2 : 1][1];
 #pragma unroll
-            for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-                const uint32_t from = GATED ? (u >> 2) * 8 + h * 4 + (u & 3) : u;
-                const f32x4 x = out[cl * UNITS + (from ^ (cl & SWZ))];
-                for (int d = 0; d < 4; ++d) v[h][d] = x[d];
+                for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+                    const uint32_t u = GATED ? (r >> 4) * 8 + h * 4 + (r >> 2 & 3) : r >> 2;
+                    v[h][0] = from[(cl * UNITS + (u ^ (cl & 15))) * 4 + (r & 3)];
+                }
+                emit<KIND, GATED, 1>(p, g, c0 + cb + cl, c_end, rt * ROWS + r, v);
             }
-            // first of four rows
-            const uint32_t r = rt * (TR / (GATED ? 2 : 1)) + wr * OUTS * 4 + u * 4;
-            emit<KIND, GATED>(p, g, c0 + (wc * FC + ph) * 16 + cl, c_end, r, v);
+            continue;
+        }
+#pragma unroll 2
+        for (uint32_t k = lane; k < COLS * LANES; k += 64) {
+            const uint32_t cl = wr * COLS + k / LANES, l = k % LANES;
+            float v[GATED ? 2 : 1][8];
+#pragma unroll
+            for (int h = 0; h < (GATED ? 2 : 1); ++h)
+#pragma unroll
+                for (int d = 0; d < 8; d += 4) {
+                    // gated: eight results come from half a block of the gate and half of the block behind it
+                    const uint32_t u = GATED ? (l >> 1) * 8 + h * 4 + (l & 1) * 2 + d / 4 : l * 2 + d / 4;
+                    const f32x4 x = out[cl * UNITS + (u ^ (cl & 15))];
+                    for (int e = 0; e < 4; ++e) v[h][d + e] = x[e];
+                }
+            emit<KIND, GATED, 8>(p, g, c0 + cb + cl, c_end, rt * ROWS + l * 8, v);
         }
     }
 }
@@ -1295,7 +1351,7 @@ __global__ __launch_bounds__(256) void k_join(GemmParams p, uint32_t tr, uint32_
             x += *reinterpret_cast<const f32x4 *>(from + (uint64_t)i * p.r_tiles * p.c_tiles * tr * tc);
         for (int d = 0; d < 4; ++d) v[h][d] = x[d];
     }
-    emit<KIND, GATED>(p, g, c0 + cl, c_end, rt * (tr / (GATED ? 2 : 1)) + u * 4, v);
+    emit<KIND, GATED, 4>(p, g, c0 + cl, c_end, rt * (tr / (GATED ? 2 : 1)) + u * 4, v);
 }
 
 // The same for the loss: a column's tr / 4 threads (32 or 64 lanes) find its reference and sum.
@@ -1355,26 +1411,6 @@ __global__ __launch_bounds__(64) void k_loss_join(LossEpi e, float *loss, float 
 
 // ---- the pre-activation's gradient --------------------------------------------------
 
-// Eight consecutive values, those from `count` on as zeros.
-__device__ inline void read8v(const void *p, uint64_t at, bool f32, bool vec, uint32_t count, float v[8]) {
-    if (vec && count == 8) {
-        if (f32) {
-            const f32x4 *s = reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + at);
-            const f32x4 a = s[0], b = s[1];
-            for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
-            v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
-            v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
-        }
-        return;
-    }
-    for (uint32_t i = 0; i < 8; ++i)
-        v[i] = i >= count ? 0.0f
-               : f32      ? static_cast<const float *>(p)[at + i]
-                          : from_bf16(static_cast<const uint16_t *>(p)[at + i]);
-}
-
 // dz = dy act'(z) in the padded column order of the packed rows, and the sums
 // of its columns over a run of the group's rows, from the unrounded values.
 // A thread takes eight columns (of both halves when gated).  Bound by memory.
@@ -1400,11 +1436,11 @@ __global__ __launch_bounds__(256) void k_dz(DzParams p) {
 #pragma unroll 2
         for (uint32_t m = m0 + wave; m < m1; m += 4) {
             float v[H][8], z[H][8], dy[8];
-            read8v(p.dy, m * p.dy_stride + c, p.dy_f32, p.vec, count, dy);
+            load<8>(p.dy, m * p.dy_stride + c, p.dy_f32, p.vec && count == 8, count, dy);
             if (GATED || p.act != kActNone)
 #pragma unroll
                 for (int h = 0; h < H; ++h)
-                    read8v(p.z, m * p.z_stride + (uint64_t)h * p.part_rows + c, p.z_f32, p.vec, count, z[h]);
+                    load<8>(p.z, m * p.z_stride + (uint64_t)h * p.part_rows + c, p.z_f32, p.vec && count == 8, count, z[h]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (GATED) {

@@ -110,7 +110,7 @@ struct LinearEpi {
     void *preact;           // or null
     uint64_t residual_stride, y_stride, preact_stride;
     uint32_t bias_f32, y_f32, preact_f32, act;
-    uint32_t vec;           // four consecutive values can be moved as one
+    uint32_t vec;           // consecutive values that can be moved as one: 8, 4 or 1
     uint32_t clear;         // zeros in the rows of no group
 };
 
@@ -132,7 +132,7 @@ struct StoreEpi {
     float *sum;          // fp32 running sums, or null
     uint64_t stride, sum_stride, matrix_stride;
     uint32_t add;        // read the running sums first
-    uint32_t vec;
+    uint32_t vec;        // as above
     uint32_t clear;      // zeros in the rows of no group
 };
 
