@@ -120,6 +120,14 @@ __device__ inline uint32_t tile_entry(const WeightView &w, uint4 h, uint32_t lan
     return reinterpret_cast<const uint32_t *>(w.extra + (uint64_t)h.y * 16)[min(lane, n - 1)];
 }
 
+// Puts one entry (uniform) into its place in registers.
+__device__ inline void tile_patch(uint32_t e, uint32_t lane, uint32_t v[8]) {
+    const uint32_t at = lane == (e >> 4 & 63) ? e >> 1 & 7 : 8;
+    const uint32_t keep = e & 1 ? 0x0000FFFFu : 0xFFFF0000u, put = e >> 16 << (e & 1 ? 16 : 0);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) v[p] = at == (uint32_t)p ? (v[p] & keep) | put : v[p];
+}
+
 // All of it, in registers.
 __device__ inline void tile_decode(const Tile &t, const WeightView &w, uint32_t lane, uint32_t v[8]) {
     tile_decode_plain(t, v);
@@ -129,15 +137,7 @@ __device__ inline void tile_decode(const Tile &t, const WeightView &w, uint32_t 
     const uint32_t n = tile_listed(t.h.x);
     if (n == 0) return;
     const uint32_t ent = tile_entry(w, t.h, lane);
-    for (uint32_t i = 0; i < n; ++i) {
-        const uint32_t e = __builtin_amdgcn_readlane(ent, i);
-        const uint32_t idx = e & 15, val = e >> 16;
-        const bool mine = lane == (e >> 4 & 63);
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-            if ((idx >> 1) == (uint32_t)p)
-                v[p] = !mine ? v[p] : idx & 1 ? (v[p] & 0xFFFFu) | (val << 16) : (v[p] & 0xFFFF0000u) | val;
-    }
+    for (uint32_t i = 0; i < n; ++i) tile_patch(__builtin_amdgcn_readlane(ent, i), lane, v);
 }
 
 // ---- packing ------------------------------------------------------------------
@@ -693,6 +693,16 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
 // its share of the weights of the stages after next; one barrier ends the step.
 // Two waves a SIMD: a wave alone issues an instruction every four cycles, and a
 // step has too many of them for the matrix instructions' time.
+//
+// With 64 or 128 columns a tile (and packed rows) the traffic of LDS and a
+// step's latencies weigh more than the matrix instructions: there a wave takes
+// two row blocks and all columns, so that its weights go from memory through
+// the decoder to the matrix instructions in registers, and only the tokens'
+// values go through LDS.  128 x 128: two times four waves, each half of the
+// contraction, added up at the end (one wave a SIMD: 67 us for 1024 x 4096 x
+// 4096 instead of 55; decoded tiles through the ring: 70); 256 x 64: eight
+// waves (128256 x 4096, 64 tokens: 158 us, 5 TB/s of packed bytes; through the
+// ring 212).
 
 enum Operand { kPacked, kPackedT, kRows, kCols };
 
@@ -849,22 +859,26 @@ __device__ inline void emit(const GemmParams &p, uint32_t g, uint32_t c, uint32_
     }
 }
 
-template <Operand RK, Operand CK, GemmKind KIND, bool GATED, int TR, int TC, int WR, int WC>
-__global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
-    constexpr int WAVES = WR * WC;
-    static_assert(WAVES == 8, "eight waves");
+// WR by WC waves share a tile's outputs; WK 2: twice, each half of the contraction.
+template <Operand RK, Operand CK, GemmKind KIND, bool GATED, int TR, int TC, int WR, int WC, int WK = 1>
+__global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
+    constexpr int WAVES = WR * WC, ALL = WAVES * WK;
+    constexpr bool DIRECT = RK == kPacked && WC == 1;      // every wave decodes its own rows, in registers
+    static_assert(ALL == 8 && (DIRECT || WK == 1), "eight waves");
     constexpr int FR = TR / WR / 16, FC = TC / WC / 16;    // fragments of a wave
-    constexpr int RSTAGE = TR * 64, CSTAGE = TC * 64;      // bytes of an operand's stage
-    constexpr int C_ALL = CSTAGE / 1024, R_ALL = RSTAGE / 1024;      // copies that fill one
+    constexpr int RSTAGE = DIRECT ? 0 : TR * 64, CSTAGE = TC * 64;  // bytes of an operand's stage
+    constexpr int STAGES = DIRECT ? 8 : 4;
+    constexpr int C_ALL = CSTAGE / 1024, R_ALL = TR / 16;      // copies that fill one
     constexpr int C_COPIES = C_ALL > WAVES ? C_ALL / WAVES : 1;      // a wave's (with fewer than waves, some twice)
     constexpr int R_COPIES = R_ALL > WAVES ? R_ALL / WAVES : 1;
     constexpr bool PACKED = RK == kPacked || RK == kPackedT;
-    constexpr int TILES = TR / 16 / WAVES;  // packed tiles a wave decodes in two steps: 2 or 1
+    constexpr int TILES = DIRECT ? 1 : TR / 16 / WAVES;  // packed tiles a wave decodes in two steps: 2 or 1
     constexpr int SLOT = 2048;              // a packed tile on its way to the decoder
-    // four stages of R, four of C, the packed tiles
-    constexpr int RING = 4 * (RSTAGE + CSTAGE);
-    __shared__ __align__(16) uint8_t lds[RING + (PACKED ? TILES * WAVES * SLOT : 0)];
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    // the stages of R and of C, the packed tiles
+    constexpr int RING = WK * STAGES * (RSTAGE + CSTAGE);
+    __shared__ __align__(16) uint8_t lds[RING + (PACKED && !DIRECT ? TILES * WAVES * SLOT : 0)];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave_all = uniform(tid >> 6);
+    const uint32_t wave = wave_all % WAVES, wk = wave_all / WAVES;
     const uint32_t q = lane >> 4, l15 = lane & 15;
     const uint32_t wr = wave % WR, wc = wave / WR;
 
@@ -896,7 +910,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
             if (F ? p.lin.clear : p.store.clear) {
                 const uint32_t wide = GATED ? TR / 2 : TR, limit = F ? p.w.part_rows : p.cols, c = min(rt * wide, limit);
                 clear_rest(p.offsets, p.groups, p.tokens, F ? p.lin.y : p.store.out, F ? p.lin.y_stride : p.store.stride,
-                           F && p.lin.y_f32 ? 4 : 2, c, min(c + wide, limit), WAVES * 64);
+                           F && p.lin.y_f32 ? 4 : 2, c, min(c + wide, limit), ALL * 64);
             }
         }
         if (!find_group(p, ct, TC, lane, g, c0, c_end)) return;
@@ -938,8 +952,8 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     if constexpr (RK == kCols)
 #pragma unroll
         for (int i = 0; i < R_COPIES; ++i) r_off[i] = cols_off(r_index(i), TR, rt * TR, p.r_limit, p.rmat.stride);
-    uint8_t *const r_lds = lds, *const c_lds = lds + 4 * RSTAGE;
-    const uint32_t r_at = lds_address(lds), c_at = r_at + 4 * RSTAGE;
+    uint8_t *const r_lds = lds, *const c_lds = lds + STAGES * RSTAGE + (WK > 1 ? wk * (STAGES * CSTAGE) : 0);
+    const uint32_t r_at = lds_address(lds), c_at = r_at + STAGES * RSTAGE;
     // The i-th of a wave's copies of stage s.  Stages behind the last are zeros.
     auto copy_part = [&](uint32_t s, int i) __attribute__((always_inline)) {
         const uint8_t *cp = static_cast<const uint8_t *>(p.cmat.p);
@@ -948,7 +962,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
             const uint32_t left = s < S && a < p.c_limit ? p.c_limit - a : 0;  // columns from here on
             const rsrc_t c = buffer(cp + ((uint64_t)c0 * p.cmat.stride + a) * 2,
                                     left ? ((rows - 1) * (uint32_t)p.cmat.stride + left) * 2 : 0);
-            copy_to_lds(c, c_unit < left ? c_off[i] : kNowhere, c_at + (s & 3) * CSTAGE + c_index(i) * 1024);
+            copy_to_lds(c, c_unit < left ? c_off[i] : kNowhere, c_at + s % STAGES * CSTAGE + c_index(i) * 1024);
         } else {
             const uint32_t a = a0 + s * 32, rows = s < S ? min(32u, a_end - a) : 0;
             const bool r = i >= C_COPIES;
@@ -957,7 +971,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
             if (r)
                 copy_to_lds(x, r_off[i - C_COPIES], r_at + (s & 3) * RSTAGE + r_index(i - C_COPIES) * 1024);
             else
-                copy_to_lds(x, c_off[i], c_at + (s & 3) * CSTAGE + c_index(i) * 1024);
+                copy_to_lds(x, c_off[i], c_at + s % STAGES * CSTAGE + c_index(i) * 1024);
         }
     };
 
@@ -965,18 +979,18 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     // A block of 64 contraction values (two stages) is TR / 16 tiles; a wave decodes TILES of them.
     // TILES 2: one in each step.  Forward: decode step d fills half of stages d & ~1 and (d & ~1) + 1; in step s,
     // d = s + 3 (stage s + 2 is whole after step s, when s is odd with the one after it).  dx: d fills stage d, d = s + 2.
-    // TILES 1: one in every other step, d = s / 2 + 1.  Forward: in even steps, into stages 2 d and 2 d + 1.  dx: half of
-    // the waves in even steps into stage 2 d, half in odd ones into 2 d + 1.
+    // TILES 1 (dx): one in every other step, d = s / 2 + 1, half of the waves in even steps into stage 2 d, half in odd
+    // ones into 2 d + 1.
     // A tile is copied to LDS two steps before.
     constexpr bool FWD = RK == kPacked;
-    const uint32_t half = TILES == 2 || FWD ? 0 : wave / (WAVES / 2);
+    const uint32_t half = TILES == 2 ? 0 : wave / (WAVES / 2);
     const uint32_t decodes = TILES == 2 ? S : (S + 1) / 2;
     auto tile_index = [&](uint32_t d, bool &live) __attribute__((always_inline)) -> uint64_t {
         uint32_t rb, kb;
         d = min(d, decodes - 1);
         if (FWD) {
-            const uint32_t j = TILES == 2 ? wave * 2 + (d & 1) : wave;
-            kb = (s0 >> 1) + (TILES == 2 ? d >> 1 : d);
+            const uint32_t j = wave * 2 + (d & 1);
+            kb = (s0 >> 1) + (d >> 1);
             if (GATED) {
                 rb = rt * (TR / 32) + (j >> 1);
                 live = rb < p.w.part_blocks;
@@ -1027,8 +1041,8 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     // Places in LDS of the two halves of a lane's 16 values; dx: both in one stage.
     auto tile_place = [&](uint32_t d, uint32_t l, uint32_t &at0, uint32_t &at1) __attribute__((always_inline)) {
         if (FWD) {
-            const uint32_t j = TILES == 2 ? wave * 2 + (d & 1) : wave, at = j * 1024 + l * 16;
-            at0 = (TILES == 2 ? d & 2 : d * 2 & 2) * RSTAGE + at;
+            const uint32_t j = wave * 2 + (d & 1), at = j * 1024 + l * 16;
+            at0 = (d & 2) * RSTAGE + at;
             at1 = at0 + RSTAGE;
         } else {
             const uint32_t j = TILES == 2 ? wave : wave % (WAVES / 2), row = (j & 1) * 16 + (l & 15), lq = l >> 4;
@@ -1095,7 +1109,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
             rf[at] = cols_frag<TR>(rl, rr, lane);
     };
     auto read_c = [&](uint32_t s, int b, int i) __attribute__((always_inline)) {
-        const uint8_t *cl = c_lds + (s & 3) * CSTAGE;
+        const uint8_t *cl = c_lds + s % STAGES * CSTAGE;
         const uint32_t cc = (wc * FC + i) * 16;
         if constexpr (CK == kCols)
             cf[b][i] = cols_frag<TC>(cl, cc, lane);
@@ -1107,7 +1121,166 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     for (int i = 0; i < FR; ++i)
         for (int j = 0; j < FC; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    if (S > 0) {
+    if constexpr (DIRECT) {
+        // Blocks of 64 contraction values, two stages each.  In block k a wave multiplies with its rows' tiles k, decodes
+        // its tiles k + 1 between the products, copies block k + 3 of C and loads its tiles k + 3.
+        const uint32_t each = (S / 2 + WK - 1) / WK, kb0 = s0 / 2 + wk * each, n = wk ? S / 2 - each : each;
+        uint64_t tile0[FR];
+        rsrc_t rows[FR];
+#pragma unroll
+        for (int i = 0; i < FR; ++i) {
+            uint32_t rb;
+            if (GATED) {
+                rb = rt * (TR / 32) + wave * (FR / 2) + i / 2;
+                rb = rb < p.w.part_blocks ? rb + (i & 1 ? p.w.part_blocks : 0) : 0;
+            } else {
+                rb = rt * (TR / 16) + wave * FR + i;
+                rb = rb < p.row_blocks ? rb + p.row_block0 : 0;
+            }
+            tile0[i] = ((uint64_t)g * p.w.row_blocks + rb) * KB;
+            rows[i] = buffer(p.w.tiles + tile0[i] * kTileBytes, KB * kTileBytes);
+        }
+        uint4 hd[FR], hd_next[FR];  // lane l: the header of block 64 j + l
+        auto first_heads = [&](uint32_t k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < FR; ++i) hd_next[i] = p.w.head[tile0[i] + min(kb0 + k + lane, KB - 1)];
+        };
+        auto turn_heads = [&](uint32_t k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < FR; ++i) {
+                hd[i] = head_checked(p.w, hd_next[i]);
+                if (k + lane >= n) hd[i].x = 0;
+            }
+            first_heads(k + 64);
+        };
+        Tile t[2][FR];
+        uint32_t v[2][FR][8];
+        auto load_tiles = [&](uint32_t k, Tile (&to)[FR]) __attribute__((always_inline)) {
+            const uint32_t at = (k < n ? kb0 + k : KB) * kTileBytes;  // (behind the last block: zeros)
+#pragma unroll
+            for (int i = 0; i < FR; ++i) {
+                to[i].sm = read16(rows[i], at + lane * 16);
+                to[i].code = read8(rows[i], at + kTileSm + lane * 8);
+            }
+        };
+        auto begin_tiles = [&](uint32_t k, Tile (&from)[FR]) __attribute__((always_inline)) {
+            if ((k & 63) == 0 && k) turn_heads(k);
+#pragma unroll
+            for (int i = 0; i < FR; ++i) from[i].h.x = __builtin_amdgcn_readlane(hd[i].x, k & 63);
+        };
+        auto decode_pair = [&](const Tile (&from)[FR], uint32_t (&to)[FR][8], int u) __attribute__((always_inline)) {
+            const int i = u / 8, k = u % 8;
+            to[i][k] = tile_signs(from[i], k) | ((from[i].h.x & 0xFF) * 0x00800080u - tile_codes(from[i], k));
+        };
+        auto end_tiles = [&](uint32_t k, Tile (&from)[FR], uint32_t (&to)[FR][8]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < FR; ++i)
+                if (const uint32_t odd = from[i].h.x & (0xFF00u | kTileZero)) {
+                    from[i].h.z = __builtin_amdgcn_readlane(hd[i].z, k & 63);
+                    from[i].h.w = __builtin_amdgcn_readlane(hd[i].w, k & 63);
+                    if (odd <= kInline << 8) {
+                        tile_patch(from[i].h.z, lane, to[i]);
+                        if (odd == kInline << 8) tile_patch(from[i].h.w, lane, to[i]);
+                    } else {
+                        from[i].h.y = __builtin_amdgcn_readlane(hd[i].y, k & 63);
+                        tile_decode(from[i], p.w, lane, to[i]);
+                        __builtin_amdgcn_s_waitcnt(0x0F70);  // (so that no wait for what was loaded here stays in the loop)
+                    }
+                }
+        };
+        // A block's values of C: the i-th KiB of this wave.
+        constexpr int BC = 2 * C_ALL / WAVES;
+        static_assert(2 * C_ALL % WAVES == 0 && BC >= 1, "whole copies");
+        uint4 cs[2][BC];
+        uint32_t cs_off[BC], cs_col[BC];
+#pragma unroll
+        for (int i = 0; i < BC; ++i) {
+            const uint32_t index = wave * BC + i;
+            cs_col[i] = index / C_ALL * 32 + c_unit;
+            cs_off[i] = ((index % C_ALL * 16 + (lane >> 2)) * (uint32_t)p.cmat.stride + cs_col[i]) * 2;
+        }
+        auto load_c = [&](uint32_t k, uint4 (&to)[BC]) __attribute__((always_inline)) {
+            const uint32_t wide = min((uint32_t)TC, c_end - c0), a = (kb0 + k) * 64;
+            const uint32_t left = k < n && a < p.c_limit ? p.c_limit - a : 0;
+            const rsrc_t c = buffer(static_cast<const uint8_t *>(p.cmat.p) + ((uint64_t)c0 * p.cmat.stride + a) * 2,
+                                    left ? ((wide - 1) * (uint32_t)p.cmat.stride + left) * 2 : 0);
+#pragma unroll
+            for (int i = 0; i < BC; ++i) to[i] = read16(c, cs_col[i] < left ? cs_off[i] : kNowhere);
+        };
+        auto store_c = [&](uint32_t k, const uint4 (&from)[BC]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < BC; ++i)
+                *reinterpret_cast<uint4 *>(c_lds + k % 4 * (2 * CSTAGE) + (wave * BC + i) * 1024 + lane * 16) = from[i];
+        };
+        first_heads(0);
+        load_tiles(0, t[0]);
+        load_c(0, cs[0]);
+        load_c(1, cs[1]);
+        load_tiles(1, t[1]);
+        turn_heads(0);
+        begin_tiles(0, t[0]);
+#pragma unroll
+        for (int u = 0; u < FR * 8; ++u) decode_pair(t[0], v[0], u);
+        end_tiles(0, t[0], v[0]);
+        store_c(0, cs[0]);
+        load_c(2, cs[0]);
+        store_c(1, cs[1]);
+        load_c(3, cs[1]);
+        load_tiles(2, t[0]);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        barrier();
+#pragma unroll
+        for (int j = 0; j < FC; ++j) read_c(0, 0, j);
+        auto block = [&](uint32_t k, auto parity) __attribute__((always_inline)) {
+            constexpr int b = decltype(parity)::value;
+            begin_tiles(k + 1, t[b ^ 1]);
+            store_c(k + 2, cs[b]);  // (over block k - 2, which no wave reads any more)
+            load_c(k + 4, cs[b]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < FC; ++j) {
+                    read_c(2 * k + h + 1, h ^ 1, j);
+#pragma unroll
+                    for (int i = 0; i < FR; ++i) {
+                        const bf16x8 a = __builtin_bit_cast(
+                            bf16x8, u32x4{v[b][i][4 * h], v[b][i][4 * h + 1], v[b][i][4 * h + 2], v[b][i][4 * h + 3]});
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, cf[h][j], acc[i][j], 0, 0, 0);
+                    }
+                    if (h == 0)
+#pragma unroll
+                        for (int u = j * FR * 8 / FC; u < (j + 1) * FR * 8 / FC; ++u) decode_pair(t[b ^ 1], v[b ^ 1], u);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (h == 0) {
+                    end_tiles(k + 1, t[b ^ 1], v[b ^ 1]);
+                    load_tiles(k + 3, t[b ^ 1]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            // block k + 2's values of C are in LDS; only the last reads may be on their way
+            asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(FC) : "memory");
+            barrier();
+        };
+        for (uint32_t k = 0; k < each; k += 2) {  // (blocks behind the last add zeros)
+            block(k, std::integral_constant<int, 0>{});
+            block(k + 1, std::integral_constant<int, 1>{});
+        }
+        __syncthreads();
+        if constexpr (WK > 1) {  // the halves' sums
+            f32x4 *half = reinterpret_cast<f32x4 *>(lds) + wave * (FR * FC * 64) + lane;
+            static_assert(WAVES * FR * FC * 1024 <= RING, "fits");
+            if (wk)
+#pragma unroll
+                for (int i = 0; i < FR * FC; ++i) half[i * 64] = acc[i / FC][i % FC];
+            __syncthreads();
+            if (!wk)
+#pragma unroll
+                for (int i = 0; i < FR * FC; ++i) acc[i / FC][i % FC] += half[i * 64];
+            __syncthreads();
+        }
+    } else if (S > 0) {
         uint4 heads_first;
         if constexpr (PACKED) {
             heads_first = load_heads(0);
@@ -1147,8 +1320,8 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
         auto step = [&](uint32_t s, auto parity) __attribute__((always_inline)) {
             constexpr int b = decltype(parity)::value;
             const uint32_t d = TILES == 1 ? s / 2 + 1 : FWD ? s + 3 : s + 2;
-            // whether this wave decodes in this step (TILES 1, dx: a uniform branch, else known)
-            const bool mine = PACKED && (TILES == 2 || (FWD ? b == 0 : half == b));
+            // whether this wave decodes in this step (TILES 1: a uniform branch, else known)
+            const bool mine = PACKED && (TILES == 2 || half == b);
             Tile t;
             uint32_t v[8];
             if constexpr (PACKED) {
@@ -1171,10 +1344,6 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
                     read_r(s + 1, i, place(i, b ^ 1));
                     if constexpr (PACKED) {
                         if (mine) {
-                            if constexpr (FR <= 2) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) v[k] = tile_signs(t, k) | (base - tile_codes(t, k));
-                            }
                             store_tile(d, v);  // behind the last stage: into stages that nothing reads any more
                             mend(d, t.h.x);
                             copy_tile(d + SLOTS);
@@ -1185,7 +1354,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
 #pragma unroll
                 for (int j = 0; j < FC; ++j) mfma(acc[i][j], rf[place(i, b)], cf[b][j]);
                 if (i < FR - 1) read_r(s + 1, i, i);
-                if constexpr (PACKED && FR > 2) {
+                if constexpr (PACKED) {
                     // eight pairs, between the first and the last group of products
                     constexpr int GROUPS = FR - 2;
                     if (i > 0 && i <= GROUPS)
@@ -1231,7 +1400,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
             // the target, where it is one of this lane's rows
             const int64_t want = m < c_end ? p.loss.target[m] : -1;
             const uint32_t hit = want >= 0 && want < (int64_t)p.rows ? (uint32_t)want - n0 : FR * 16;
-            if (hit < FR * 16 && (hit & 15) < 4) {
+            if (hit < FR * 16 && (hit & 15) < 4 && wk == 0) {
 #pragma unroll
                 for (int i = 0; i < FR; ++i)
 #pragma unroll
@@ -1254,10 +1423,10 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
                 for (int d = 0; d < 4; ++d) sum += __expf(acc[i][j][d] - ref);
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (q == 0) red[wr * TC + (wc * FC + j) * 16 + l15] = f32x2{ref, sum};
+            if (q == 0 && wk == 0) red[wr * TC + (wc * FC + j) * 16 + l15] = f32x2{ref, sum};
         }
         __syncthreads();
-        for (uint32_t c = tid; c < TC; c += WAVES * 64) {
+        for (uint32_t c = tid; c < TC; c += ALL * 64) {
             if (c0 + c >= c_end) continue;
             float ref = red[c][0], sum = 0;
 #pragma unroll
@@ -1275,15 +1444,17 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
     // against bank conflicts.  The WR waves of a wc share its columns.
     constexpr int UNITS = TR / 4, FIT = RING / WC / (TR * 64);
     constexpr int JP = FIT >= FC ? FC : FIT >= 2 && FC % 2 == 0 ? 2 : 1;  // fragments at a time
-    constexpr int COLS = JP * 16 / WR;                                    // columns of a wave
+    constexpr int SHARE = WR * WK, COLS = JP * 16 / SHARE;                // waves of a column, columns of a wave
     constexpr int ROWS = TR / (GATED ? 2 : 1), LANES = ROWS / 8;          // results of a column, lanes for them
-    static_assert(FIT >= 1 && JP * 16 % WR == 0 && COLS * LANES % 64 == 0, "whole waves");
+    static_assert(FIT >= 1 && JP * 16 % SHARE == 0 && COLS * LANES % 64 == 0, "whole waves");
     f32x4 *out = reinterpret_cast<f32x4 *>(lds + wc * (JP * TR * 64));
+    const uint32_t share = WK > 1 ? wave_all : wr;
 #pragma unroll
     for (int ph = 0; ph < FC; ph += JP) {
         if (ph) __syncthreads();
+        if (wk == 0)
 #pragma unroll
-        for (int j = 0; j < JP; ++j)
+            for (int j = 0; j < JP; ++j)
 #pragma unroll
             for (int i = 0; i < FR; ++i)
                 out[(j * 16 + l15) * UNITS + ((wr * FR * 4 + i * 4 + q) ^ l15)] = acc[i][ph + j];
@@ -1294,7 +1465,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
             float *to = p.part + ((uint64_t)blockIdx.y * total + ct * p.r_tiles + rt) * (TR * TC);
 #pragma unroll 4
             for (uint32_t k = lane; k < COLS * UNITS; k += 64) {
-                const uint32_t cl = wr * COLS + k / UNITS, u = k % UNITS;
+                const uint32_t cl = share * COLS + k / UNITS, u = k % UNITS;
                 *reinterpret_cast<f32x4 *>(to + (cb + cl) * TR + u * 4) = out[cl * UNITS + (u ^ (cl & 15))];
             }
             continue;
@@ -1304,7 +1475,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
             const float *from = reinterpret_cast<const float *>(out);
 #pragma unroll 2
             for (uint32_t k = lane; k < COLS * ROWS; k += 64) {
-                const uint32_t cl = wr * COLS + k / ROWS, r = k % ROWS;
+                const uint32_t cl = share * COLS + k / ROWS, r = k % ROWS;
                 float v[GATED ? 2 : 1][1];
 #pragma unroll
                 for (int h = 0; h < (GATED ? 2 : 1); ++h) {
@@ -1317,7 +1488,7 @@ __global__ __launch_bounds__(WR *WC * 64, 2) void k_gemm(GemmParams p) {
         }
 #pragma unroll 2
         for (uint32_t k = lane; k < COLS * LANES; k += 64) {
-            const uint32_t cl = wr * COLS + k / LANES, l = k % LANES;
+            const uint32_t cl = share * COLS + k / LANES, l = k % LANES;
             float v[GATED ? 2 : 1][8];
 #pragma unroll
             for (int h = 0; h < (GATED ? 2 : 1); ++h)
@@ -1509,8 +1680,13 @@ hipError_t gemm(GemmTile tile, const GemmParams &p, hipStream_t s) {
     const dim3 grid(p.r_tiles * p.c_tiles, KIND == kGemmDw ? p.groups : p.splits);
     if (tile.r == 256 && tile.c == 256)
         k_gemm<RK, CK, KIND, GATED, 256, 256, 2, 4><<<grid, 512, 0, s>>>(p);
-    else if (tile.r == 128 && tile.c == 128)
-        k_gemm<RK, CK, KIND, GATED, 128, 128, 2, 4><<<grid, 512, 0, s>>>(p);
+    else if (tile.r == 128 && tile.c == 128) {
+        if constexpr (RK == kPacked)
+            k_gemm<RK, CK, KIND, GATED, 128, 128, 4, 1, 2><<<grid, 512, 0, s>>>(p);
+        else
+            k_gemm<RK, CK, KIND, GATED, 128, 128, 2, 4><<<grid, 512, 0, s>>>(p);
+    } else if constexpr (RK == kPacked)
+        k_gemm<RK, CK, KIND, GATED, 256, 64, 8, 1><<<grid, 512, 0, s>>>(p);
     else if constexpr (KIND != kGemmDw)
         k_gemm<RK, CK, KIND, GATED, 256, 64, 4, 2><<<grid, 512, 0, s>>>(p);
     const dim3 join(grid.x, (tile.r * tile.c / (GATED ? 8 : 4) + 255) / 256);
@@ -1548,11 +1724,14 @@ hipError_t launch_stage(const uint16_t *in, uint64_t in_stride, uint16_t *out, u
 }
 
 // Rows of x for which the skinny product is faster than the tiled one: it
-// reads all of x once a workgroup.  64 rows: 20 against 22 us on 4096 x 4096,
-// but 58 against 39 us on 4096 x 14336.
+// reads all of x once a workgroup, so that the width of x counts.  Skinny and
+// tiled in us: 4096 x 4096 with 32 rows 11 and 17, with 64 rows 19 and 17;
+// 4096 x 14336 with 17 rows 23 and 27, with 32 rows 31 and 27; 2048 x 2048 with
+// 48 rows 9 and 11; 8 experts of 4096 x 4096 with 16 rows each 34 and 59, with
+// 20 rows (two rounds of 16) 60 and 59, with 48 rows 92 and 61.
 bool skinny_fits(uint64_t tokens, uint64_t groups, uint64_t col_blocks) {
     if (groups > 1) return tokens <= 16 * groups;
-    return tokens <= 32 || (tokens <= 64 && col_blocks <= 128);
+    return tokens <= 24 || (tokens <= 64 && tokens * col_blocks <= 2048);
 }
 
 // Waves and row blocks of a workgroup: with rows enough to fill the chip, few
@@ -1584,19 +1763,20 @@ GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups) {
 }
 
 // Runs into which the contraction is cut.  With fewer tiles than workgroups
-// that fit the chip (two a CU), each run shortens the walk of `steps` blocks of
-// 64 (0.9 us each where a CU has one workgroup, 1.4 us where it has two) and
+// that fit the chip, each run shortens the walk of `steps` blocks of 64 and
 // adds its part of the sums, written and read once at about 4 TB/s, and one
-// launch.  128 x 4096 x 4096: 57 us whole, 20 us in 8 runs; 777 x 4096 x 4096
-// (224 tiles): 62 us whole, 70 us in two.
-uint32_t gemm_splits(GemmTile tile, uint64_t r_tiles, uint64_t c_tiles, uint64_t steps) {
-    const uint64_t tiles = r_tiles * c_tiles;
+// launch.  A block takes 0.6 us with tiles of 128 x 128, 0.8 with 256 x 64, one
+// workgroup a CU (more do not fit: 128 x 4096 x 4096 20 us in 8 runs, 44 whole,
+// 32 in 16); dx 0.9 us where a CU has one workgroup, 1.4 where it has two.
+uint32_t gemm_splits(GemmKind kind, GemmTile tile, uint64_t r_tiles, uint64_t c_tiles, uint64_t steps) {
+    const uint64_t tiles = r_tiles * c_tiles, most = kind == kGemmDx ? 512 : 256;
     if (tiles == 0 || tiles > 256) return 1;
+    const double one = kind == kGemmDx ? 0.9 : tile.c == 64 ? 0.8 : 0.6;
     const double part = 8.0 * tiles * tile.r * tile.c / 4e6;  // us a run
     uint32_t best = 1;
-    double least = 0.9 * steps;
-    for (uint32_t n = 2; n <= 512 / tiles && 4 * n <= steps && n <= 64; ++n) {
-        const double t = (tiles * n <= 256 ? 0.9 : 1.4) * ((steps + n - 1) / n) + 3.0 + part * n;
+    double least = one * steps;
+    for (uint32_t n = 2; n <= most / tiles && 4 * n <= steps && n <= 64; ++n) {
+        const double t = (tiles * n <= 256 ? one : 1.4) * ((steps + n - 1) / n) + 3.0 + part * n;
         if (t < 0.95 * least) best = n, least = t;
     }
     return best;

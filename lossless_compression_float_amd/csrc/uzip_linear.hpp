@@ -194,7 +194,7 @@ struct GemmTile {
 // The tile of a product with `r` by `c` outputs, c in all of `groups` groups.
 GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups);
 // Runs of the contraction (all but dw).
-uint32_t gemm_splits(GemmTile tile, uint64_t r_tiles, uint64_t c_tiles, uint64_t steps);
+uint32_t gemm_splits(GemmKind kind, GemmTile tile, uint64_t r_tiles, uint64_t c_tiles, uint64_t steps);
 hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStream_t s);
 hipError_t launch_loss_join(const LossEpi &e, float *loss, float *lse, uint32_t tokens, uint32_t parts, uint64_t vocab,
                             hipStream_t s);

@@ -165,7 +165,7 @@ Cut cut(GemmKind kind, uint64_t rows, uint64_t tokens, uint64_t groups, bool gro
     c.tile = gemm_tile(kind, rows, tokens, groups);
     c.r_tiles = (uint32_t)blocks(rows, c.tile.r);
     c.c_tiles = token_tiles(tokens, groups, grouped, c.tile.c);
-    c.splits = gemm_splits(c.tile, c.r_tiles, c.c_tiles, steps);
+    c.splits = gemm_splits(kind, c.tile, c.r_tiles, c.c_tiles, steps);
     return c;
 }
 

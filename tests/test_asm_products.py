@@ -30,18 +30,21 @@ def regs(text, kind):
 
 
 def kernels(text):
-    """(name, its instruction lines; None for a label) of every tiled product."""
-    name, lines = None, []
+    """(name, its instruction lines; None for a label) of every tiled product whose matrix instructions come from asm."""
+    name, lines, asm, inline = None, [], False, False
     for raw in text.splitlines():
         m = re.match(r"^(_ZN\S*k_gemm\S*):", raw)
         if m:
-            name, lines = m.group(1), []
+            name, lines, asm, inline = m.group(1), [], False, False
         elif name:
+            asm = "#ASMSTART" in raw or (asm and "#ASMEND" not in raw)
+            inline = inline or (asm and "v_mfma" in raw)
             s = raw.split(";")[0].strip()
             if re.match(r"^\.LBB\S*:", s):
                 lines.append(None)
             elif s.startswith("s_endpgm"):
-                yield name, lines
+                if inline:
+                    yield name, lines
                 name = None
             elif s and not s.startswith("."):
                 lines.append(s)
@@ -87,7 +90,7 @@ def test_asm_products_have_room():
         assert not bad, (name, bad[:5])
         assert products >= 16, name
         seen += 1
-    assert seen >= 16
+    assert seen >= 9
     # (the check itself: a planted write right before a product is found)
     assert check(["v_mov_b32_e32 v5, 0", "v_mfma_f32_16x16x32_bf16 a[0:3], v[4:7], v[8:11], a[0:3]", "s_nop 0",
                   "v_mfma_f32_16x16x32_bf16 a[0:3], v[4:7], v[8:11], a[0:3]"])[0]
