@@ -820,11 +820,15 @@ __device__ inline void emit(const GemmParams &p, uint32_t g, uint32_t c, uint32_
     } else if constexpr (KIND == kGemmForward) {
         if (c < c_end) linear_out<GATED, W>(p.lin, (uint64_t)g * p.rows, p.w.part_rows, c, r, v);
     } else if constexpr (KIND == kGemmLossDz) {
-        // g (softmax - one at the target), rounded to bf16 for the two products that follow; zeros behind the last row
+        // g (softmax - one at the target), rounded to bf16 for the two products that follow; zeros behind the last row.
+        // In units of the largest g, which the products' results are multiplied with in fp32: with one g for all tokens,
+        // as a mean has, g (p - 1) would be off by the same part of itself, up to 2^-8, at nearly every target, and the
+        // gradients' errors would add up instead of averaging out.  p - 1 itself is near -1, which is exact.  (A g under
+        // 2^-126 of the largest is lost.)
         if (c >= c_end) return;
         const int64_t want = p.loss.target[c];
         const bool counts = want != p.loss.ignore && want >= 0 && want < (int64_t)p.rows;
-        const float gr = counts ? p.loss.dloss[c] : 0.0f, lse = p.loss.lse[c];
+        const float gr = counts ? p.loss.dloss[c] / *p.loss.unit : 0.0f, lse = p.loss.lse[c];
         const uint32_t n = p.row_block0 * 16 + r, hit = counts ? (uint32_t)want - n : W;
 #pragma unroll
         for (int d = 0; d < W; ++d) {
@@ -854,6 +858,10 @@ __device__ inline void emit(const GemmParams &p, uint32_t g, uint32_t c, uint32_
                 for (int d = 0; d < W; ++d) v[0][d] += o[d];
             }
             if (!e.out) store<W>(e.sum, row * e.sum_stride + r, true, sv, count, v[0]);
+        }
+        if (e.out && e.unit) {
+            const float unit = *e.unit;
+            for (int d = 0; d < W; ++d) v[0][d] *= unit;
         }
         if (e.out) store<W>(e.out, row * e.stride + r, false, e.vec % W == 0 && count == W, count, v[0]);
     }
@@ -1580,6 +1588,23 @@ __global__ __launch_bounds__(64) void k_loss_join(LossEpi e, float *loss, float 
     }
 }
 
+__global__ __launch_bounds__(1024) void k_loss_unit(LossEpi e, float *unit, uint32_t tokens, uint64_t vocab) {
+    __shared__ float red[16];
+    float top = 0;
+#pragma unroll 4
+    for (uint32_t m = threadIdx.x; m < tokens; m += 1024) {
+        const int64_t t = e.target[m];
+        const float a = fabsf(e.dloss[m]);
+        if (t != e.ignore && t >= 0 && t < (int64_t)vocab && a < INFINITY) top = fmaxf(top, a);
+    }
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int w = 1; w < 16; ++w) top = fmaxf(top, red[w]);
+    *unit = top > 0 ? top : 1.0f;
+}
+
 // ---- the pre-activation's gradient --------------------------------------------------
 
 // dz = dy act'(z) in the padded column order of the packed rows, and the sums
@@ -1799,6 +1824,11 @@ hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStr
 hipError_t launch_loss_join(const LossEpi &e, float *loss, float *lse, uint32_t tokens, uint32_t parts, uint64_t vocab,
                             hipStream_t s) {
     k_loss_join<<<tokens, 64, 0, s>>>(e, loss, lse, parts, vocab);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_unit(const LossEpi &e, float *unit, uint32_t tokens, uint64_t vocab, hipStream_t s) {
+    k_loss_unit<<<1, 1024, 0, s>>>(e, unit, tokens, vocab);
     return hipGetLastError();
 }
 

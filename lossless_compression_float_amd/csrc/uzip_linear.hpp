@@ -122,6 +122,7 @@ struct LossEpi {
     float *picked;       // the target's logit
     const float *lse;    // backward
     const float *dloss;
+    const float *unit;   // backward: the largest dloss, by which dz is divided
     uint16_t *dz;        // backward: one piece's gradient of the logits
     uint64_t dz_stride;
 };
@@ -130,6 +131,7 @@ struct LossEpi {
 struct StoreEpi {
     uint16_t *out;       // null while pieces remain
     float *sum;          // fp32 running sums, or null
+    const float *unit;   // the results' factor, or null
     uint64_t stride, sum_stride, matrix_stride;
     uint32_t add;        // read the running sums first
     uint32_t vec;        // as above
@@ -198,6 +200,8 @@ uint32_t gemm_splits(GemmKind kind, GemmTile tile, uint64_t r_tiles, uint64_t c_
 hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStream_t s);
 hipError_t launch_loss_join(const LossEpi &e, float *loss, float *lse, uint32_t tokens, uint32_t parts, uint64_t vocab,
                             hipStream_t s);
+// The largest finite |dloss| of the tokens that count (1 where all are 0).
+hipError_t launch_loss_unit(const LossEpi &e, float *unit, uint32_t tokens, uint64_t vocab, hipStream_t s);
 hipError_t launch_dz(const DzParams &p, hipStream_t s);
 
 }  // namespace uzip

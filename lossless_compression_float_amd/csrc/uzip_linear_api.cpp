@@ -372,7 +372,7 @@ struct LossPlan {
     float2 *parts;
     float *picked, *part;
     uint16_t *dz;
-    float *sum;
+    float *unit, *sum;
     uint64_t piece;  // rows of the weight in a piece
     Cut cut;         // of the forward product
     bool stage;
@@ -403,6 +403,7 @@ LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward,
     p.piece = std::min(up(w->rows, 256), std::max<uint64_t>(4096, fit));
     if (a->tokens == 0) return p;
     p.dz = c.take<uint16_t>(a->tokens * p.piece);
+    p.unit = c.take<float>(1);
     uint64_t part = 0;
     const uint64_t all = up(w->rows, kTileRows);
     for (uint64_t r0 = 0; r0 < all; r0 += p.piece) {
@@ -410,7 +411,7 @@ LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward,
         part = std::max(part, std::max(cut_dz(w, a, rows).part(), a->dx ? cut_dx(w, a, rows).part() : 0));
     }
     if (part) p.part = c.take<float>(part);
-    if (a->dx && p.piece < w->rows) p.sum = c.take<float>(a->tokens * up(w->cols, 4));
+    if (a->dx && p.piece < w->rows) p.sum = c.take<float>(a->tokens * up(w->cols, 8));
     return p;
 }
 
@@ -570,6 +571,10 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
     p.loss.dloss = args->dloss;
     p.loss.dz = plan.dz;
     p.loss.dz_stride = plan.piece;
+    if (args->tokens) {
+        p.loss.unit = plan.unit;
+        if (launch_loss_unit(p.loss, plan.unit, args->tokens, weight->rows, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+    }
     const uint32_t all = p.w.row_blocks, step = (uint32_t)(plan.piece / kTileRows);
     for (uint32_t b0 = 0; b0 < all; b0 += step) {
         p.row_block0 = b0;
@@ -592,6 +597,7 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
             p.store = StoreEpi{};
             p.store.sum = plan.sum;
             p.store.sum_stride = up(weight->cols, 8);
+            p.store.unit = plan.unit;
             p.store.add = b0 > 0;
             p.store.out = b0 + step >= all ? static_cast<uint16_t *>(args->dx) : nullptr;
             p.store.stride = args->dx_stride;
@@ -606,6 +612,7 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
             p.c_tiles = (uint32_t)blocks(rows, tile.c);
             p.store = StoreEpi{};
             p.store.out = static_cast<uint16_t *>(args->dw);
+            p.store.unit = args->tokens ? plan.unit : nullptr;
             p.store.stride = weight->cols;
             p.store.vec = units(args->dw, weight->cols, UZIP_BF16);
             if (launch_gemm(kGemmDw, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;

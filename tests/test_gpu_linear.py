@@ -384,6 +384,45 @@ def test_loss_pieces():
     check_loss(17000, 5000, 16, backward=True)  # two pieces of 4,096 rows
 
 
+def test_loss_gradient_of_a_mean():
+    """One dloss for all tokens, halfway between two bf16 values, 2^-8 of itself away from both: rounded with the logit
+    gradients it would be missing from, or added to, every target's alike.  The gradients' errors are those of two
+    roundings that know nothing of each other, each uniform over up to +-2^-8 of a value: 2^-8 sqrt(2 / 3) = 0.0032 of the
+    whole, 0.0039 and more with the other.  The unit's reduction also meets NaN and infinity where no token counts."""
+    g = gen(48)
+    m, v, k = 500, 3001, 136
+    x, w = normal(g, m, k), normal(g, v, k, scale=0.02)
+    t = torch.randint(0, v, (m,), generator=g).to(DEV)
+    t[3:9] = -100
+    t[11] = v
+    dl = torch.full((m,), (1 + 2.0 ** -8) / 512, device=DEV)
+    p = uz.pack_weight(w)
+    _, lse = uz.linear_cross_entropy(x, p, t)
+    dl[3], dl[4], dl[11] = float("nan"), float("inf"), 3e38
+    dx, dw = uz.linear_cross_entropy_backward(dl, x, p, t, lse)
+    dl[3], dl[4], dl[11] = 0, 0, 0
+    t[11] = -100
+    (wx, _), (ww, _) = loss_backward64(dl, x, w, t, -100)
+    for got, want in ((dx, wx), (dw, ww)):
+        off = (got.double().cpu() - want).norm() / want.norm()
+        assert off < 2.0 ** -8 * (2 / 3) ** 0.5, off
+
+
+def test_loss_gradients_of_any_size():
+    """dloss over twenty decades; tiny; none at all."""
+    g = gen(49)
+    m, v, k = 40, 300, 64
+    x, w = normal(g, m, k), normal(g, v, k, scale=0.1)
+    t = torch.randint(0, v, (m,), generator=g).to(DEV)
+    p = uz.pack_weight(w)
+    _, lse = uz.linear_cross_entropy(x, p, t)
+    for dl in (torch.logspace(-10, 10, m, device=DEV), torch.full((m,), 1e-30, device=DEV), torch.zeros(m, device=DEV)):
+        dx, dw = uz.linear_cross_entropy_backward(dl, x, p, t, lse)
+        (wx, ex), (ww, ew) = loss_backward64(dl, x, w, t, -100)
+        close(dx, wx, ex, "dx")
+        close(dw, ww, ew, "dw")
+
+
 def test_loss_large_logits():
     check_loss(40, 600, 64, scale=20.0)
 

@@ -269,3 +269,36 @@ def test_rows_far_apart(m):
     xs = x.contiguous()
     uz.linear(xs, p, out=out)
     assert torch.equal(out, want)
+
+
+def test_nothing_is_written_behind_a_workspace(monkeypatch):
+    """Every workspace is exactly as large as its size function says, with a guard behind it."""
+    import lossless_compression_float_amd.weights as ws
+    held = []
+
+    def guarded(need, device):
+        t = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device=device)
+        held.append((t, need))
+        return t[:need]
+
+    monkeypatch.setattr(ws, "workspace", guarded)
+    x = normal(1, 17000, 20)
+    p = uz.pack_weight(normal(2, 5000, 20, scale=0.1))
+    t = torch.arange(17000, device=DEV) % 5000
+    loss, lse = uz.linear_cross_entropy(x, p, t)
+    uz.linear_cross_entropy_backward(torch.ones_like(loss), x, p, t, lse)  # two pieces, sums over them
+    for m, n, k in ((100, 300, 1027), (70, 130, 4100), (777, 515, 330)):
+        x = normal(3, m, k)
+        p = uz.pack_weight(normal(4, n, k, scale=0.1))
+        y, z = uz.linear(x, p, act="silu", return_preact=True)
+        uz.linear_backward(y, x, p, preact=z, act="silu", need_bias=True)
+        loss, lse = uz.linear_cross_entropy(x, p, torch.zeros(m, dtype=torch.int64, device=DEV))
+        uz.linear_cross_entropy_backward(torch.ones_like(loss), x, p, torch.zeros(m, dtype=torch.int64, device=DEV), lse)
+        p = uz.pack_weight(normal(5, 3, n // 2 * 2, k, scale=0.1), gated=True)
+        off = torch.tensor([0, m // 3, m // 3, m], dtype=torch.int32, device=DEV)
+        y, z = uz.grouped_linear(x, off, p, act="swiglu", return_preact=True)
+        uz.grouped_linear_backward(y, x, off, p, preact=z, act="swiglu", need_bias=True)
+    torch.cuda.synchronize()
+    assert len(held) > 20
+    for t, need in held:
+        assert bool((t[need:] == 0xA5).all()), need
