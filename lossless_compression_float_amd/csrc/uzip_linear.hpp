@@ -110,7 +110,6 @@ struct LinearEpi {
     void *preact;           // or null
     uint64_t residual_stride, y_stride, preact_stride;
     uint32_t bias_f32, y_f32, preact_f32, act;
-    uint32_t vec;           // consecutive values that can be moved as one: 8, 4 or 1
     uint32_t clear;         // zeros in the rows of no group
 };
 
@@ -134,7 +133,6 @@ struct StoreEpi {
     const float *unit;   // the results' factor, or null
     uint64_t stride, sum_stride, matrix_stride;
     uint32_t add;        // read the running sums first
-    uint32_t vec;        // as above
     uint32_t clear;      // zeros in the rows of no group
 };
 
@@ -177,7 +175,6 @@ struct DzParams {
     uint32_t groups, tokens;
     uint32_t part_rows, part_pad, parts, width;  // width: padded columns of dz
     uint32_t dy_f32, z_f32, act, chunks;
-    uint32_t vec;  // eight consecutive values can be read as one
     void *dbias;
     uint32_t dbias_f32;
 };

@@ -75,12 +75,6 @@ uint32_t type_size(uint32_t t) { return t == UZIP_FP32 ? 4 : 2; }
 bool by16(const void *p, uint64_t stride, uint64_t cols) { return aligned(p, 16) && stride % 8 == 0 && cols % 8 == 0; }
 bool tiled(const void *p, uint64_t stride, uint64_t cols) { return by16(p, stride, cols) && stride < (1u << 22); }
 
-// Consecutive values of a row that can be moved as one: 8 (bf16 in 16 bytes, fp32 in twice 16), 4 or 1.
-uint32_t units(const void *p, uint64_t stride, uint32_t type) {
-    if (stride % 8 == 0 && aligned(p, 16)) return 8;
-    return stride % 4 == 0 && aligned(p, 4 * type_size(type)) ? 4 : 1;
-}
-
 // Carves a workspace; with a null base it only counts.
 struct Carver {
     uint8_t *base;
@@ -136,13 +130,6 @@ LinearEpi linear_epi(const uzip_weight *w, const uzip_linear_args *a) {
     e.y_f32 = a->y_dtype == UZIP_FP32;
     e.act = a->act;
     e.clear = a->clear_rest && a->offsets;
-    const uint64_t part = w->rows / (w->gated + 1);
-    e.vec = units(a->y, a->y_stride, a->y_dtype);
-    if (a->bias) e.vec = std::min(e.vec, units(a->bias, part, a->bias_dtype));
-    if (a->residual) e.vec = std::min(e.vec, units(a->residual, a->residual_stride, a->y_dtype));
-    // (the up rows' part of preact starts part values in)
-    if (a->preact)
-        e.vec = std::min(e.vec, std::min(units(a->preact, a->preact_stride, a->preact_dtype), units(nullptr, part, UZIP_BF16)));
     return e;
 }
 
@@ -307,8 +294,6 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
         p.dy_f32 = a->dy_dtype == UZIP_FP32;
         p.act = a->act;
         p.chunks = plan.chunks;
-        p.vec = a->dy_stride % 8 == 0 && aligned(a->dy, 16) &&
-                (a->act == UZIP_ACT_NONE || (a->preact_stride % 8 == 0 && aligned(a->preact, 16) && v.part_rows % 8 == 0));
         p.dbias = a->dbias;
         p.dbias_f32 = a->dbias_dtype == UZIP_FP32;
         if (launch_dz(p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
@@ -329,7 +314,6 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
         p.store = StoreEpi{};
         p.store.out = static_cast<uint16_t *>(a->dx);
         p.store.stride = a->dx_stride;
-        p.store.vec = units(a->dx, a->dx_stride, UZIP_BF16);
         p.store.clear = a->clear_rest && a->offsets;
         if (launch_gemm(kGemmDx, plan.cut.tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     }
@@ -348,7 +332,6 @@ uzip_status backward_run(const uzip_weight *w, const uzip_linear_backward_args *
         p.store = StoreEpi{};
         p.store.out = static_cast<uint16_t *>(a->dw);
         p.store.stride = w->cols;
-        p.store.vec = units(a->dw, w->cols, UZIP_BF16);
         if (launch_gemm(kGemmDw, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     }
     return UZIP_OK;
@@ -601,7 +584,6 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
             p.store.add = b0 > 0;
             p.store.out = b0 + step >= all ? static_cast<uint16_t *>(args->dx) : nullptr;
             p.store.stride = args->dx_stride;
-            p.store.vec = units(args->dx, args->dx_stride, UZIP_BF16);
             if (launch_gemm(kGemmDx, dx.tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
         }
         if (args->dw) {
@@ -614,7 +596,6 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
             p.store.out = static_cast<uint16_t *>(args->dw);
             p.store.unit = args->tokens ? plan.unit : nullptr;
             p.store.stride = weight->cols;
-            p.store.vec = units(args->dw, weight->cols, UZIP_BF16);
             if (launch_gemm(kGemmDw, tile, p, stream) != hipSuccess) return UZIP_ERR_DEVICE;
         }
     }
