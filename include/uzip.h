@@ -313,7 +313,7 @@ uzip_status uzip_decompress_batched_timed(uzip_dtype dtype, size_t num_buffers, 
  * resident form: the same split of each bf16 value into its exponent and its
  * sign+mantissa byte, the exponent as a 4-bit code within the window of a
  * 16 x 64 tile, so that a product can decode it while it reads it, at the
- * speed of memory.  Near-Gaussian weights take about 12.1 bits a value; any
+ * speed of memory.  Near-Gaussian weights take about 12.2 bits a value; any
  * bit pattern comes back as it was (values outside a tile's window are listed
  * beside it, and a tile with more than 64 of them keeps its exponents as
  * bytes, at most 20.2 bits a value).  Only bf16 weights are packed.
@@ -331,8 +331,9 @@ uzip_status uzip_decompress_batched_timed(uzip_dtype dtype, size_t num_buffers, 
  * same call gives the same bits.  Rows of a bf16 or fp32 matrix may be any
  * stride apart (in values, at least the row's length); unaligned or odd ones
  * cost a copy.  Limits: 2^31 - 1 rows or columns, 65,535 matrices and 2^25
- * tiles a stack; 2^25 tokens a call, and 2^22 tiles of 128 by 64 outputs.  No
- * argument may overlap an output.
+ * tiles a stack; products take 2^22 - 512 rows and columns a matrix,
+ * 2^25 tokens a call, and 2^22 tiles of 128 by 64 outputs.  No argument may
+ * overlap an output (y may be the residual itself).
  * UZIP_ERR_CAPACITY: packed capacity below uzip_weight_max_size. */
 typedef struct {
     const void *data;   /* device, 16-byte aligned, as uzip_weight_pack wrote it */

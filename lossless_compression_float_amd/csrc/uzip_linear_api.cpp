@@ -22,6 +22,8 @@ constexpr uint64_t kMaxTiles = 1ull << 25;
 // grid dimension (512 threads a tile of at least 128 by 64 outputs).
 constexpr uint64_t kMaxTokens = 1ull << 25;
 constexpr uint64_t kMaxOutputTiles = 1ull << 22;
+// and a tile's rows, up to 256 of these, are addressed with 32 bits.
+constexpr uint64_t kMaxWide = (1ull << 22) - 512;
 
 uint64_t up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 uint64_t blocks(uint64_t v, uint64_t a) { return (v + a - 1) / a; }
@@ -64,7 +66,7 @@ bool mat_ok(const void *p, uint64_t stride, uint64_t rows, uint64_t cols, uint32
 // Whether products of `tokens` rows with this weight, and their gradients, fit the limits.
 bool call_ok(const uzip_weight *w, uint64_t tokens) {
     const uint64_t wide = std::max(blocks(w->rows, 128) + 1, blocks(w->cols, 128));
-    return tokens <= kMaxTokens && wide * (tokens / 64 + w->matrices + 1) <= kMaxOutputTiles;
+    return w->rows <= kMaxWide && w->cols <= kMaxWide && tokens <= kMaxTokens && wide * (tokens / 64 + w->matrices + 1) <= kMaxOutputTiles;
 }
 
 bool type_ok(uint32_t t) { return t == UZIP_BF16 || t == UZIP_FP32; }

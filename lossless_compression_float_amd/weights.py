@@ -228,6 +228,22 @@ def _offsets(offsets, w: PackedWeight):
     return offsets.data_ptr()
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two matrices with contiguous rows share memory."""
+    if 0 in (a.numel(), b.numel()) or a.device != b.device:
+        return False
+    wide = [t.shape[1] * t.element_size() for t in (a, b)]
+    step = [t.stride(0) * t.element_size() if t.shape[0] > 1 else w for t, w in zip((a, b), wide)]
+    first = [t.data_ptr() for t in (a, b)]
+    end = [f + (t.shape[0] - 1) * s + w for f, t, s, w in zip(first, (a, b), step, wide)]
+    if first[0] >= end[1] or first[1] >= end[0]:
+        return False
+    if step[0] == step[1] and a.shape[0] > 1 and b.shape[0] > 1:  # two slices of columns
+        at = (first[0] - first[1]) % step[0]
+        return not (at >= wide[1] and at + wide[0] <= step[0])
+    return True
+
+
 def _tokens(x, what: str) -> int:
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a tensor, not %s" % (what, type(x).__name__))
@@ -328,13 +344,18 @@ def _forward(what, w, x, offsets, bias, act, residual, out_dtype, return_preact,
         r_stride = _matrix(residual, "residual", tokens, width, device, out_dtype)
         r = residual.data_ptr()
     z_code = _code(preact_dtype, "preact_dtype") if return_preact else 0
+    clear = int(grouped and out is None)
+    if out is not None:
+        y_stride = _matrix(out, "out", tokens, width, device, out_dtype)
+        if _overlap(out, x):
+            raise ValueError("out must not overlap x")
+        if residual is not None and _overlap(out, residual) and (
+                out.data_ptr() != residual.data_ptr() or y_stride != r_stride):
+            raise ValueError("out must be the residual itself or not overlap it")
     with _on(device):
-        clear = int(grouped and out is None)
         if out is None:
             out = torch.empty((tokens, width), dtype=out_dtype, device=device)
             y_stride = width
-        else:
-            y_stride = _matrix(out, "out", tokens, width, device, out_dtype)
         z = torch.empty((tokens, rows), dtype=preact_dtype, device=device) if return_preact else None
         if tokens:
             a = uzip_linear_args(x.data_ptr(), x_stride, tokens, off, b, r, r_stride, out.data_ptr(), y_stride,
@@ -348,7 +369,8 @@ def linear(x, weight: PackedWeight, bias=None, act: str = "none", residual=None,
            return_preact: bool = False, preact_dtype=torch.float32, out=None, ws=None, stream=None):
     """act(x W^T + bias) + residual for x [tokens, cols] bf16 and a packed
     weight [rows, cols]; the result [tokens, rows] ([tokens, rows / 2] for
-    swiglu) is bf16, or out_dtype.  residual has the result's shape and type.
+    swiglu) is bf16, or out_dtype.  residual has the result's shape and type;
+    out (the result's place) may be the residual, and must not overlap x.
     return_preact=True also returns x W^T + bias [tokens, rows], which
     linear_backward takes, in preact_dtype (in bf16 it takes half the memory and
     the gradients lose about as much as dz's own rounding costs them)."""

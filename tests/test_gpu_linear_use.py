@@ -302,3 +302,16 @@ def test_nothing_is_written_behind_a_workspace(monkeypatch):
     assert len(held) > 20
     for t, need in held:
         assert bool((t[need:] == 0xA5).all()), need
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 512, 256), (50, 4096, 2048), (100, 515, 4096), (300, 1030, 200), (2100, 8200, 64)])
+def test_the_result_may_replace_its_residual(m, n, k):
+    x, p = normal(1, m, k), uz.pack_weight(normal(2, n, k, scale=0.05))
+    r = normal(3, m, n)
+    want = uz.linear(x, p, residual=r)
+    assert same(uz.linear(x, p, residual=r, out=r), want) and same(r, want)
+    # and columns beside x in one buffer
+    both = torch.zeros(m, n + k, dtype=BF, device=DEV)
+    both[:, n:] = x
+    uz.linear(both[:, n:], p, out=both[:, :n])
+    assert same(both[:, :n], uz.linear(x, p)) and same(both[:, n:], x)

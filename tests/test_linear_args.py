@@ -118,6 +118,24 @@ def test_calls_beyond_the_launch_grids_are_refused():
     assert uz.uzip_linear(weight(), linear_args(tokens=(1 << 25) + 1), FAKE, big, None) == INVALID
 
 
+def test_matrices_too_wide_for_a_product_are_refused():
+    """A tile's rows are addressed with 32 bits; such weights can be packed all the same."""
+    big, most = 1 << 45, (1 << 22) - 512
+    for kw in (dict(rows=64, cols=most + 1), dict(rows=most + 1, cols=64)):
+        w = weight(**kw)
+        assert uz.uzip_weight_max_size(1, kw["rows"], kw["cols"]) > 0
+        rows, cols = kw["rows"], kw["cols"]
+        a = linear_args(x_stride=cols, y_stride=rows)
+        assert uz.uzip_linear(w, a, FAKE, big, None) == INVALID
+        b = backward_args(dy_stride=rows, x_stride=cols, dx_stride=cols)
+        assert uz.uzip_linear_backward(w, b, FAKE, big, None) == INVALID
+        l = loss_args(x_stride=cols, dx_stride=cols)
+        assert uz.uzip_linear_cross_entropy(w, l, FAKE, big, None) == INVALID
+        assert uz.uzip_linear_cross_entropy_backward(w, l, FAKE, big, None) == INVALID
+    w = weight(rows=64, cols=most)
+    assert uz.uzip_linear_workspace_size(w, linear_args(x_stride=most + 1, y_stride=64)) > 2 * most
+
+
 def test_linear_workspace_holds_a_copy_of_rows_that_cannot_be_read_whole():
     small = uz.uzip_linear_workspace_size(weight(), linear_args(tokens=1000))
     for kw in [dict(x=FAKE + 2), dict(x_stride=65)]:
@@ -199,6 +217,18 @@ OFF = torch.zeros(4, dtype=torch.int32)
 def test_linear_refusals(kw, error):
     with pytest.raises(error):
         uz.linear(**{**dict(x=X, weight=packed()), **kw})
+
+
+def test_linear_refuses_an_output_over_its_inputs():
+    square = packed((64, 64))
+    both = torch.zeros(5, 128, dtype=BF)
+    for out, x, residual in [(X, X, None), (both[:, :64], both[:, 63:127], None), (both[:, :64], X, both[:, 1:65]),
+                             (both[1:5, :64], X[:4], both[:4, :64])]:
+        with pytest.raises(ValueError, match="overlap"):
+            uz.linear(x, square, out=out, residual=residual)
+    from lossless_compression_float_amd.weights import _overlap
+    assert not _overlap(both[:, :64], both[:, 64:]) and not _overlap(both[:2], both[2:]) and not _overlap(X[:0], X)
+    assert _overlap(both[:, 60:70], both[:, :61]) and _overlap(both[1:2, :3], both[:, 2:])
 
 
 @pytest.mark.parametrize("kw,error", [
