@@ -73,22 +73,32 @@ __device__ inline void tile_load(Tile &t, const WeightView &w, uint64_t tile, ui
     t.h = make_uint4(uniform(head.x), uniform(head.y), uniform(head.z), uniform(head.w));
 }
 
-// Eight pairs of bf16 values from a lane's tile registers: five operations a
-// pair, no branches.  The byte of sign and mantissa is spread over a half word
-// and masked, the code shifted to the exponent's place and taken from the base.
-__device__ inline uint32_t tile_signs(const Tile &t, int p) {
+// Eight pairs of bf16 values from a lane's tile registers, no branches, 4 1/4
+// operations a pair: the byte of sign and mantissa is spread over a half word;
+// the code is masked out where it is and one packed multiplication brings it to
+// the exponent's place, negative, and adds the base (two of four codes need a
+// shift by 8 first, one for both); a bit select joins the two.  (Shifted to
+// their place, masked, subtracted and joined: six.)
+__device__ inline uint32_t tile_signs(const Tile &t, int p) {  // with the mantissa's top bits where the exponent goes
     const uint32_t sm[4] = {t.sm.x, t.sm.y, t.sm.z, t.sm.w};
-    return __builtin_amdgcn_perm(0, sm[p >> 1], p & 1 ? 0x03030202u : 0x01010000u) & 0x807F807Fu;
+    return __builtin_amdgcn_perm(0, sm[p >> 1], p & 1 ? 0x03030202u : 0x01010000u);
 }
-__device__ inline uint32_t tile_codes(const Tile &t, int p) {
-    const uint32_t c = p < 4 ? t.code.x : t.code.y;
-    const int k = p & 3;
-    return (k == 0 ? c << 7 : k == 1 ? c << 3 : k == 2 ? c >> 1 : c >> 5) & 0x07800780u;
+constexpr uint32_t kNotExponent = 0x807F807Fu;
+__device__ inline uint32_t tile_join(uint32_t signs, uint32_t exponents) {
+    return (signs & kNotExponent) | (exponents & ~kNotExponent);
+}
+__device__ inline uint32_t tile_pair(const Tile &t, int p, uint32_t base) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t by = p & 1 ? 0xFFF8FFF8u : 0xFF80FF80u;  // -8, -128
+    asm("" : "+s"(by));                                // (a constant would become a shift and a subtraction)
+    const uint32_t c = (p < 4 ? t.code.x : t.code.y) >> (p & 2 ? 8 : 0) & (p & 1 ? 0x00F000F0u : 0x000F000Fu);
+    const u16x2 e = __builtin_bit_cast(u16x2, c) * __builtin_bit_cast(u16x2, by) + __builtin_bit_cast(u16x2, base);
+    return tile_join(tile_signs(t, p), __builtin_bit_cast(uint32_t, e));
 }
 __device__ inline void tile_decode_plain(const Tile &t, uint32_t v[8]) {
     const uint32_t base = (t.h.x & 0xFF) * 0x00800080u;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) v[p] = tile_signs(t, p) | (base - tile_codes(t, p));
+    for (int p = 0; p < 8; ++p) v[p] = tile_pair(t, p, base);
 }
 
 // The two kinds of tile for which that is not enough: exponent bytes, and
@@ -101,17 +111,19 @@ __device__ inline void tile_decode_raw(const Tile &t, const WeightView &w, uint3
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const uint32_t x = e[p >> 1] >> (p & 1 ? 16 : 0);
-        v[p] = tile_signs(t, p) | ((x & 0xFF) << 7) | ((x & 0xFF00) << 15);
+        v[p] = tile_join(tile_signs(t, p), ((x & 0xFF) << 7) | ((x & 0xFF00) << 15));
     }
 }
 __device__ inline void tile_decode_zero(const Tile &t, uint32_t v[8]) {
     const uint32_t base = (t.h.x & 0xFF) * 0x00800080u;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        const uint32_t x = tile_codes(t, p);
+        const uint32_t c = p < 4 ? t.code.x : t.code.y;
+        const int k = p & 3;
+        const uint32_t x = (k == 0 ? c << 7 : k == 1 ? c << 3 : k == 2 ? c >> 1 : c >> 5) & 0x07800780u;
         const uint32_t z = (x + 0x00800080u) & 0x08000800u;  // bit 11 of the halves whose code is 15
         const uint32_t m = (z << 4) - (z >> 4);              // 0x7F80 there
-        v[p] = tile_signs(t, p) | ((base - (x & ~m)) & ~m);
+        v[p] = tile_join(tile_signs(t, p), (base - (x & ~m)) & ~m);
     }
 }
 
@@ -1223,7 +1235,7 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
         };
         auto decode_pair = [&](const Tile (&from)[FR], uint32_t (&to)[FR][8], int u) __attribute__((always_inline)) {
             const int i = u / 8, k = u % 8;
-            to[i][k] = tile_signs(from[i], k) | ((from[i].h.x & 0xFF) * 0x00800080u - tile_codes(from[i], k));
+            to[i][k] = tile_pair(from[i], k, (from[i].h.x & 0xFF) * 0x00800080u);
         };
         auto end_tiles = [&](uint32_t k, Tile (&from)[FR], uint32_t (&to)[FR][8]) __attribute__((always_inline)) {
 #pragma unroll
@@ -1413,7 +1425,7 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
                     if (i > 0 && i <= GROUPS)
 #pragma unroll
                         for (int k = (i - 1) * 8 / GROUPS; k < i * 8 / GROUPS; ++k)
-                            v[k] = tile_signs(t, k) | (base - tile_codes(t, k));
+                            v[k] = tile_pair(t, k, base);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
