@@ -315,3 +315,76 @@ def test_the_result_may_replace_its_residual(m, n, k):
     both[:, n:] = x
     uz.linear(both[:, n:], p, out=both[:, :n])
     assert same(both[:, :n], uz.linear(x, p)) and same(both[:, n:], x)
+
+
+def small(seed, *shape):
+    """-1, 0 and 1: sums of their products are exact."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=g, device=DEV).to(BF)
+
+
+WIDEST = (1 << 22) - 512
+
+
+@pytest.mark.parametrize("m", [5, 300])
+def test_the_most_rows_of_a_weight(m):
+    w, x = small(1, WIDEST, 64), small(2, m, 64)
+    p = uz.pack_weight(w)
+    y, z = uz.linear(x, p, return_preact=True)
+    for c in range(0, WIDEST, 1 << 20):
+        assert torch.equal(y[:, c:c + (1 << 20)].float(), x.float() @ w[c:c + (1 << 20)].float().t())
+    at = (torch.arange(m, device=DEV) * 13981) % WIDEST
+    at[-1] = WIDEST - 1
+    dy = torch.zeros(m, WIDEST, dtype=BF, device=DEV)
+    dy[torch.arange(m), at] = 1
+    del y
+    for act in ("none", "relu"):  # dy as it is, and its product with the activation's gradient
+        on = (z[torch.arange(m), at] > 0)[:, None] if act == "relu" else torch.ones(m, 1, dtype=torch.bool, device=DEV)
+        dx, dw, _ = uz.linear_backward(dy, x, p, preact=z, act=act)
+        assert torch.equal(dx, torch.where(on, w[at], 0))
+        assert torch.equal(dw[at], torch.where(on, x, 0))
+        assert int((dw != 0).sum()) == int((dw[at] != 0).sum())
+
+
+@pytest.mark.parametrize("m", [5, 300])
+def test_the_most_columns_of_a_weight(m):
+    w, x = small(3, 16, WIDEST), small(4, m, WIDEST)
+    p = uz.pack_weight(w)
+    y = uz.linear(x, p, out_dtype=F32)
+    want = torch.zeros(m, 16, dtype=torch.float64, device=DEV)
+    for c in range(0, WIDEST, 1 << 20):
+        s = slice(c, c + (1 << 20))
+        want += (x[:, s].float() @ w[:, s].float().t()).double()  # (each exact: below 2^24)
+    assert torch.equal(y.double(), want)
+    dy = torch.zeros(m, 16, dtype=BF, device=DEV)
+    dy[torch.arange(m), torch.arange(m) % 16] = 1
+    dx, dw, _ = uz.linear_backward(dy, x, p)
+    assert torch.equal(dx, w[torch.arange(m, device=DEV) % 16])
+    for n in range(16):
+        assert torch.equal(dw[n].float(), x[n::16].float().sum(0))
+
+
+def test_the_largest_vocabulary():
+    """Logits are exact here.  A token's sum passes through at most 32 additions in a lane, 10 in a tile and 262 over the
+    16,382 tiles, each 2^-24 of it, and exponentials good to 2^-20: 1.9e-5 of the sum, and lse is rounded at 15."""
+    m = 70
+    w, x = small(5, WIDEST, 64), small(6, m, 64)
+    t = (torch.arange(m, device=DEV) * 59999) % WIDEST
+    p = uz.pack_weight(w)
+    loss, lse = uz.linear_cross_entropy(x, p, t)
+    total = torch.zeros(m, dtype=torch.float64, device=DEV)
+    for c in range(0, WIDEST, 1 << 20):
+        total += torch.exp((x.float() @ w[c:c + (1 << 20)].float().t()).double()).sum(1)
+    want = torch.log(total)
+    bound = 304 * 2.0 ** -24 + 2.0 ** -20 + 15 * 2.0 ** -23
+    assert float((lse.double() - want).abs().max()) < bound
+    picked = (x.float() * w[t].float()).sum(1).double()
+    assert float((loss.double() - (want - picked)).abs().max()) < bound + 40 * 2.0 ** -24
+    # with a dloss for one token only, dw's rows are multiples of its x: that of its target, and those of the softmax
+    g = torch.zeros(m, device=DEV)
+    g[9] = 1
+    dx, dw = uz.linear_cross_entropy_backward(g, x, p, t, lse)
+    soft = torch.exp(picked[9] - want[9]) - 1
+    assert torch.allclose(dw[t[9]].double(), soft * x[9].double(), rtol=2.0 ** -7, atol=0)
+    assert not bool(dx[:9].any()) and not bool(dx[10:].any()) and bool(dx[9].any())
