@@ -757,9 +757,9 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
 // two row blocks and all columns, so that its weights go from memory through
 // the decoder to the matrix instructions in registers, and only the tokens'
 // values go through LDS.  128 x 128: two times four waves, each half of the
-// contraction, added up at the end (one wave a SIMD: 67 us for 1024 x 4096 x
-// 4096 instead of 55; decoded tiles through the ring: 70); 256 x 64: eight
-// waves (128256 x 4096, 64 tokens: 158 us, 5 TB/s of packed bytes; through the
+// contraction, added up at the end (1024 x 4096 x 4096 in 51 us; with one wave a
+// SIMD 67 where this took 55, decoded tiles through the ring 70); 256 x 64: eight
+// waves (128256 x 4096, 64 tokens: 148 us, 5.3 TB/s of packed bytes; through the
 // ring 212).
 
 enum Operand { kPacked, kPackedT, kRows, kCols };
@@ -1188,7 +1188,7 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
 
     if constexpr (DIRECT) {
         // Blocks of 64 contraction values, two stages each.  In block k a wave multiplies with its rows' tiles k, decodes
-        // its tiles k + 1 between the products, copies block k + 3 of C and loads its tiles k + 3.
+        // its tiles k + 1 between the products, stores its share of block k + 2 of C and loads its tiles k + 3.
         const uint32_t each = (S / 2 + WK - 1) / WK, kb0 = s0 / 2 + wk * each, n = wk ? S / 2 - each : each;
         uint64_t tile0[FR];
         rsrc_t rows[FR];
@@ -1256,6 +1256,10 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
         // A block's values of C: the i-th KiB of this wave.
         constexpr int BC = 2 * C_ALL / WAVES;
         static_assert(2 * C_ALL % WAVES == 0 && BC >= 1, "whole copies");
+        // Blocks of C on their way in registers: two where that is a KiB each (64 rows by 32768 x 4096 41.6 us, with one
+        // 43); with 128 columns one, since two spill unless they are stored and loaded at a block's start, in front of its
+        // products (777 x 4096 x 1024 18.6 us instead of 17.5).
+        constexpr int AHEAD = TC == 64 ? 2 : 1;
         uint4 cs[2][BC];
         uint32_t cs_off[BC], cs_col[BC];
 #pragma unroll
@@ -1264,33 +1268,33 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
             cs_col[i] = index / C_ALL * 32 + c_unit;
             cs_off[i] = ((index % C_ALL * 16 + (lane >> 2)) * (uint32_t)p.cmat.stride + cs_col[i]) * 2;
         }
-        auto load_c = [&](uint32_t k, uint4 (&to)[BC]) __attribute__((always_inline)) {
+        auto load_c = [&](uint32_t k, uint4 (&to)[BC], int i0, int i1) __attribute__((always_inline)) {
             const uint32_t wide = min((uint32_t)TC, c_end - c0), a = (kb0 + k) * 64;
             const uint32_t left = k < n && a < p.c_limit ? p.c_limit - a : 0;
             const rsrc_t c = buffer(static_cast<const uint8_t *>(p.cmat.p) + ((uint64_t)c0 * p.cmat.stride + a) * 2,
                                     left ? ((wide - 1) * (uint32_t)p.cmat.stride + left) * 2 : 0);
 #pragma unroll
-            for (int i = 0; i < BC; ++i) to[i] = read16(c, cs_col[i] < left ? cs_off[i] : kNowhere);
+            for (int i = i0; i < i1; ++i) to[i] = read16(c, cs_col[i] < left ? cs_off[i] : kNowhere);
         };
-        auto store_c = [&](uint32_t k, const uint4 (&from)[BC]) __attribute__((always_inline)) {
+        auto store_c = [&](uint32_t k, const uint4 (&from)[BC], int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < BC; ++i)
+            for (int i = i0; i < i1; ++i)
                 *reinterpret_cast<uint4 *>(c_lds + k % 4 * (2 * CSTAGE) + (wave * BC + i) * 1024 + lane * 16) = from[i];
         };
         first_heads(0);
         load_tiles(0, t[0]);
-        load_c(0, cs[0]);
-        load_c(1, cs[1]);
+        load_c(0, cs[0], 0, BC);
+        load_c(1, cs[1], 0, BC);
         load_tiles(1, t[1]);
         turn_heads(0);
         begin_tiles(0, t[0]);
 #pragma unroll
         for (int u = 0; u < FR * 8; ++u) decode_pair(t[0], v[0], u);
         end_tiles(0, t[0], v[0]);
-        store_c(0, cs[0]);
-        load_c(2, cs[0]);
-        store_c(1, cs[1]);
-        load_c(3, cs[1]);
+        store_c(0, cs[0], 0, BC);
+        load_c(2, cs[0], 0, BC);
+        store_c(1, cs[1], 0, BC);
+        if (AHEAD == 2) load_c(3, cs[1], 0, BC);
         load_tiles(2, t[0]);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         barrier();
@@ -1299,14 +1303,16 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
         auto block = [&](uint32_t k, auto parity) __attribute__((always_inline)) {
             constexpr int b = decltype(parity)::value;
             begin_tiles(k + 1, t[b ^ 1]);
-            store_c(k + 2, cs[b]);  // (over block k - 2, which no wave reads any more)
-            load_c(k + 4, cs[b]);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int j = 0; j < FC; ++j) {
                     read_c(2 * k + h + 1, h ^ 1, j);
+                    // block k + 2 over block k - 2, which no wave reads any more; all before this block's last FC reads
+                    constexpr int EACH = (BC + FC - 1) / FC;
+                    if (h == 0 && j * EACH < BC) store_c(k + 2, cs[AHEAD == 2 ? b : 0], j * EACH, (j + 1) * EACH);
+                    if (h == 1 && j * EACH < BC) load_c(k + 2 + AHEAD, cs[AHEAD == 2 ? b : 0], j * EACH, (j + 1) * EACH);
 #pragma unroll
                     for (int i = 0; i < FR; ++i) {
                         const bf16x8 a = __builtin_bit_cast(
