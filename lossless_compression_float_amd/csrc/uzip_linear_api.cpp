@@ -118,7 +118,7 @@ bool linear_ok(const uzip_weight *w, const uzip_linear_args *a, bool grouped) {
     return !a->preact || (type_ok(a->preact_dtype) && mat_ok(a->preact, a->preact_stride, a->tokens, w->rows, type_size(a->preact_dtype)));
 }
 
-LinearEpi linear_epi(const uzip_weight *w, const uzip_linear_args *a) {
+LinearEpi linear_epi(const uzip_linear_args *a) {
     LinearEpi e{};
     e.bias = a->bias;
     e.residual = a->residual;
@@ -202,7 +202,7 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
         p.tokens = (uint32_t)a->tokens;
         p.rows = (uint32_t)w->rows;
         p.cols = (uint32_t)up(w->cols, 8);
-        p.lin = linear_epi(w, a);
+        p.lin = linear_epi(a);
         return done(launch_skinny(p, stream));
     }
     GemmParams p{};
@@ -217,7 +217,7 @@ uzip_status linear_run(const uzip_weight *w, const uzip_linear_args *a, void *ws
     p.row_blocks = p.w.row_blocks;
     p.rows = (uint32_t)w->rows;
     p.cols = (uint32_t)w->cols;
-    p.lin = linear_epi(w, a);
+    p.lin = linear_epi(a);
     return done(launch_gemm(kGemmForward, plan.cut.tile, p, stream));
 }
 
