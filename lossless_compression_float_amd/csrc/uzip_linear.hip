@@ -588,22 +588,42 @@ __device__ inline uint2 read8(rsrc_t r, uint32_t off) {
 }
 constexpr uint32_t kNowhere = 0xFFFFFF00u;  // an offset that is behind every buffer
 
-// Zeros in columns [c0, c1) of the rows before the first group and behind the
-// last (all of a workgroup's threads together).
-__device__ inline void clear_rest(const int32_t *offsets, uint32_t groups, uint32_t tokens, void *out, uint64_t stride,
+// Zeros in columns [c0, c1) of the rows that no group holds (all of a
+// workgroup's threads together).  Where the offsets ascend these are the rows
+// before the first and behind the last.  A descending pair is an empty group, and the
+// groups around it may lie anywhere: then each row is looked for in all of
+// them.  Rows of a group are other workgroups' results and never touched here.
+// A call, since inlined it takes registers from the products' main loops.
+__device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups, uint32_t tokens, void *out, uint64_t stride,
                                   uint32_t elem, uint32_t c0, uint32_t c1, uint32_t threads) {
-    uint32_t first, last, unused;
-    group_rows(offsets, 0, tokens, first, unused);
-    const int32_t e = offsets[groups];
-    last = max(first, e < 0 ? 0u : min((uint32_t)e, tokens));
-    const uint32_t rest = first + (tokens - last), wide = c1 - c0;
-    for (uint64_t i = threadIdx.x; i < (uint64_t)rest * wide; i += threads) {
-        const uint32_t r = (uint32_t)(i / wide), row = r < first ? r : last + (r - first);
-        const uint64_t at = (uint64_t)row * stride + c0 + (uint32_t)(i % wide);
+    const uint32_t lane = threadIdx.x & 63, wide = c1 - c0;
+    auto clear = [&](uint32_t row, uint32_t c) {
+        const uint64_t at = (uint64_t)row * stride + c0 + c;
         if (elem == 4)
             static_cast<uint32_t *>(out)[at] = 0;
         else
             static_cast<uint16_t *>(out)[at] = 0;
+    };
+    auto clamped = [&](uint32_t i) { return (uint32_t)min(max(offsets[i], 0), (int32_t)tokens); };
+    const uint32_t first = clamped(0), last = clamped(groups);
+    bool down = false;
+#pragma unroll 1
+    for (uint32_t g = lane; g < groups; g += 64) down |= clamped(g + 1) < clamped(g);
+    if (!__any(down)) {
+        const uint32_t rest = first + (tokens - last);
+        for (uint64_t i = threadIdx.x; i < (uint64_t)rest * wide; i += threads) {
+            const uint32_t r = (uint32_t)(i / wide);
+            clear(r < first ? r : last + (r - first), (uint32_t)(i % wide));
+        }
+        return;
+    }
+    for (uint32_t row = threadIdx.x >> 6; row < tokens; row += threads / 64) {  // a wave a row
+        bool held = false;
+#pragma unroll 1
+        for (uint32_t g = lane; g < groups; g += 64) held |= row >= clamped(g) && row < clamped(g + 1);
+        if (__any(held)) continue;
+#pragma unroll 1
+        for (uint32_t c = lane; c < wide; c += 64) clear(row, c);
     }
 }
 
@@ -950,6 +970,17 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
     // Workgroups go to the 8 XCDs in turn: give each XCD a run of neighbouring
     // tiles, four column tiles wide, so that its L2 holds what they share.
     const uint32_t total = p.r_tiles * p.c_tiles;
+    if constexpr (KIND == kGemmForward || KIND == kGemmDx) {
+        if (blockIdx.x >= total) {  // behind the tiles, one a strip of columns: the rows of no group
+            if (blockIdx.y) return;
+            constexpr bool F = KIND == kGemmForward;
+            const uint32_t wide = GATED ? TR / 2 : TR, limit = F ? p.w.part_rows : p.cols;
+            const uint32_t c = (blockIdx.x - total) * wide;
+            clear_rest(p.offsets, p.groups, p.tokens, F ? p.lin.y : p.store.out, F ? p.lin.y_stride : p.store.stride,
+                       F && p.lin.y_f32 ? 4 : 2, min(c, limit), min(c + wide, limit), ALL * 64);
+            return;
+        }
+    }
     uint32_t id = blockIdx.x;
     {
         const uint32_t x = id & 7, i = id >> 3, full = total >> 3, rest = total & 7;
@@ -970,14 +1001,6 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
         c0 = ct * TC;
         c_end = p.c_limit;
     } else {
-        if ((KIND == kGemmForward || KIND == kGemmDx) && ct == 0) {
-            constexpr bool F = KIND == kGemmForward;
-            if (F ? p.lin.clear : p.store.clear) {
-                const uint32_t wide = GATED ? TR / 2 : TR, limit = F ? p.w.part_rows : p.cols, c = min(rt * wide, limit);
-                clear_rest(p.offsets, p.groups, p.tokens, F ? p.lin.y : p.store.out, F ? p.lin.y_stride : p.store.stride,
-                           F && p.lin.y_f32 ? 4 : 2, c, min(c + wide, limit), ALL * 64);
-            }
-        }
         if (!find_group(p, ct, TC, lane, g, c0, c_end)) return;
         g = uniform(g);
         c0 = uniform(c0);
@@ -1754,7 +1777,9 @@ hipError_t skinny(const SkinnyParams &p, hipStream_t s) {
 
 template <Operand RK, Operand CK, GemmKind KIND, bool GATED>
 hipError_t gemm(GemmTile tile, const GemmParams &p, hipStream_t s) {
-    const dim3 grid(p.r_tiles * p.c_tiles, KIND == kGemmDw ? p.groups : p.splits);
+    const uint32_t tiles = p.r_tiles * p.c_tiles;
+    const bool clear = KIND == kGemmForward ? p.lin.clear : KIND == kGemmDx && p.store.clear;
+    const dim3 grid(tiles + (clear ? p.r_tiles : 0), KIND == kGemmDw ? p.groups : p.splits);
     if (tile.r == 256 && tile.c == 256)
         k_gemm<RK, CK, KIND, GATED, 256, 256, 2, 4><<<grid, 512, 0, s>>>(p);
     else if (tile.r == 128 && tile.c == 128) {
@@ -1766,7 +1791,7 @@ hipError_t gemm(GemmTile tile, const GemmParams &p, hipStream_t s) {
         k_gemm<RK, CK, KIND, GATED, 256, 64, 8, 1><<<grid, 512, 0, s>>>(p);
     else if constexpr (KIND != kGemmDw)
         k_gemm<RK, CK, KIND, GATED, 256, 64, 4, 2><<<grid, 512, 0, s>>>(p);
-    const dim3 join(grid.x, (tile.r * tile.c / (GATED ? 8 : 4) + 255) / 256);
+    const dim3 join(tiles, (tile.r * tile.c / (GATED ? 8 : 4) + 255) / 256);
     if constexpr (KIND == kGemmLossStat) {
         if (p.splits > 1) k_join_stat<<<join, 256, 0, s>>>(p, tile.r, tile.c);
     } else if constexpr (KIND != kGemmDw) {
