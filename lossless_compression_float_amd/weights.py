@@ -8,6 +8,11 @@ and ``linear_cross_entropy`` (the loss over a large vocabulary, the logits
 never stored), each with its gradients.  Shapes, types and the rounding of
 each result are those the header states; argument errors raise ValueError or
 TypeError before anything is launched.
+
+A call with ``stream=`` runs there, and what it allocates is that stream's
+memory.  The caller orders the streams: the arguments have to be ready for
+``stream``, and be kept until its work is done, and the results are not ready
+for the current stream until that waits for it.
 """
 from __future__ import annotations
 
@@ -16,7 +21,7 @@ import ctypes
 
 import torch
 
-from . import (UZIP_BF16, UZIP_FP32, UZIP_OK, _check, _keep_for, _stream, lib, workspace)
+from . import (UZIP_BF16, UZIP_FP32, UZIP_OK, _check, lib, workspace)
 
 _vp, _sz, _u32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int64
 
@@ -167,9 +172,33 @@ class PackedWeight:
 _here = contextlib.nullcontext()
 
 
-def _on(device):
-    """Makes `device` current for a launch when it is not already."""
+def _on(device, stream=None):
+    """Makes `device` current for a launch when it is not already, and `stream`
+    if there is one: what is allocated meanwhile comes from that stream's
+    memory, so that no work of another stream can still be using it."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream is on %s, the weight on %s" % (stream.device, device))
+        return torch.cuda.stream(stream)
     return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _caller(device, stream):
+    """The stream that results made on `stream` are handed to."""
+    return None if stream is None else torch.cuda.current_stream(device)
+
+
+def _share(stream, caller, new=(), given=()):
+    """Tells the allocator of tensors that two streams use: `new` ones of
+    `stream` that the caller gets, and `given` ones that `stream` works on."""
+    if stream is None or stream == caller:
+        return
+    for t in new:
+        if t is not None:
+            t.record_stream(caller)
+    for t in given:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _stream_of(stream, device) -> int:
@@ -252,9 +281,9 @@ def _tokens(x, what: str) -> int:
     return x.shape[0]
 
 
-def _call(name: str, fn, size, w, a, ws, stream, *outputs):
-    """Calls `fn` with the caller's workspace or a new one: nothing is shared
-    between calls."""
+def _call(name: str, fn, size, w, a, ws, stream):
+    """Calls `fn` with the caller's workspace or a new one (made under
+    `_on(device, stream)`): nothing is shared between calls."""
     ref, device = ctypes.byref(a), w.device
     if ws is None:
         need = size(w._ref, ref)
@@ -265,8 +294,6 @@ def _call(name: str, fn, size, w, a, ws, stream, *outputs):
             _stream_of(stream, device))
     if st != UZIP_OK:
         _check(st, "uzip_" + name)
-    if stream is not None:
-        _keep_for(stream, *[t for t in (ws, *outputs) if t is not None])
 
 
 def pack_weight(w: torch.Tensor, gated: bool = False, trim: bool = True, stream=None) -> PackedWeight:
@@ -286,21 +313,19 @@ def pack_weight(w: torch.Tensor, gated: bool = False, trim: bool = True, stream=
     cap = uzip_weight_max_size(matrices, rows, cols, int(gated))
     if cap == 0:
         raise ValueError("a weight of shape %s%s cannot be packed" % (list(w.shape), " (gated)" if gated else ""))
-    with _on(w.device):
+    caller = _caller(w.device, stream)
+    with _on(w.device, stream):
         out = torch.empty(cap, dtype=torch.uint8, device=w.device)
         size = torch.empty(1, dtype=torch.int64, device=w.device)
         ws = workspace(uzip_weight_workspace_size(matrices, rows, cols, int(gated)), w.device)
         st = uzip_weight_pack(w.data_ptr(), matrices, rows, cols, max(w.stride(-2), cols), w.stride(0) if w.dim() == 3 else 0,
-                              int(gated), out.data_ptr(), cap, size.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+                              int(gated), out.data_ptr(), cap, size.data_ptr(), ws.data_ptr(), ws.numel(), _stream_of(stream, w.device))
         _check(st, "uzip_weight_pack")
-        _keep_for(stream, out, size, ws)
         if trim:
-            if stream is not None:
-                torch.cuda.current_stream().wait_stream(stream)
             out = out[:int(size.item())].clone()
-            if stream is not None:
-                stream.wait_stream(torch.cuda.current_stream())
-                _keep_for(stream, out)
+    if trim and stream is not None:
+        caller.wait_stream(stream)
+    _share(stream, caller, new=(out,))
     return PackedWeight(out, w.shape, gated)
 
 
@@ -308,14 +333,15 @@ def unpack_weight(w: PackedWeight, out: torch.Tensor | None = None, stream=None)
     """The bf16 weight back, bit for bit."""
     if not isinstance(w, PackedWeight):
         raise TypeError("unpack_weight takes a PackedWeight, not %s" % type(w).__name__)
-    with _on(w.device):
+    caller, given = _caller(w.device, stream), out
+    with _on(w.device, stream):
         if out is None:
             out = torch.empty(tuple(w.shape), dtype=torch.bfloat16, device=w.device)
         elif out.dtype is not torch.bfloat16 or out.shape != w.shape or out.device != w.device or not out.is_contiguous():
             raise ValueError("out must be a contiguous bfloat16 tensor of shape %s on %s" % (tuple(w.shape), w.device))
-        st = uzip_weight_unpack(w._c, out.data_ptr(), w.shape[-1], w.shape[-2] * w.shape[-1], _stream(stream))
+        st = uzip_weight_unpack(w._c, out.data_ptr(), w.shape[-1], w.shape[-2] * w.shape[-1], _stream_of(stream, w.device))
         _check(st, "uzip_weight_unpack")
-        _keep_for(stream, out)
+    _share(stream, caller, new=(out,) if given is None else (), given=(given,))
     return out
 
 
@@ -352,7 +378,8 @@ def _forward(what, w, x, offsets, bias, act, residual, out_dtype, return_preact,
         if residual is not None and _overlap(out, residual) and (
                 out.data_ptr() != residual.data_ptr() or y_stride != r_stride):
             raise ValueError("out must be the residual itself or not overlap it")
-    with _on(device):
+    caller, given = _caller(device, stream), out
+    with _on(device, stream):
         if out is None:
             out = torch.empty((tokens, width), dtype=out_dtype, device=device)
             y_stride = width
@@ -360,8 +387,8 @@ def _forward(what, w, x, offsets, bias, act, residual, out_dtype, return_preact,
         if tokens:
             a = uzip_linear_args(x.data_ptr(), x_stride, tokens, off, b, r, r_stride, out.data_ptr(), y_stride,
                                  z.data_ptr() if return_preact else 0, rows, b_code, y_code, act, z_code, clear)
-            _call(what, L.uzip_grouped_linear if grouped else L.uzip_linear, L.uzip_linear_workspace_size, w, a, ws, stream,
-                  out, z)
+            _call(what, L.uzip_grouped_linear if grouped else L.uzip_linear, L.uzip_linear_workspace_size, w, a, ws, stream)
+    _share(stream, caller, new=(out if given is None else None, z), given=(given, ws))
     return (out, z) if return_preact else out
 
 
@@ -408,7 +435,8 @@ def _backward(what, w, dy, x, offsets, preact, act, need_x, need_weight, need_bi
     if grouped:
         a.offsets = _offsets(offsets, w)
     code = _code(bias_dtype, "bias_dtype")
-    with _on(device):
+    caller = _caller(device, stream)
+    with _on(device, stream):
         dx = dw = db = None
         if need_x:
             dx = torch.empty((tokens, cols), dtype=torch.bfloat16, device=device)
@@ -420,7 +448,8 @@ def _backward(what, w, dy, x, offsets, preact, act, need_x, need_weight, need_bi
             db = torch.empty((w.shape[0], rows) if grouped else (rows,), dtype=bias_dtype, device=device)
             a.dbias, a.dbias_dtype = db.data_ptr(), code
         _call(what, L.uzip_grouped_linear_backward if grouped else L.uzip_linear_backward,
-              L.uzip_linear_backward_workspace_size, w, a, ws, stream, dx, dw, db)
+              L.uzip_linear_backward_workspace_size, w, a, ws, stream)
+    _share(stream, caller, new=(dx, dw, db), given=(ws,))
     return dx, dw, db
 
 
@@ -468,13 +497,15 @@ def linear_cross_entropy(x, weight: PackedWeight, target, ignore_index: int = -1
     loss 0; a target outside the vocabulary gives NaN."""
     w, tokens, a = _loss_args("linear_cross_entropy", x, weight, target, ignore_index)
     L, device = _lib(), w.device
-    with _on(device):
+    caller = _caller(device, stream)
+    with _on(device, stream):
         loss = torch.empty(tokens, dtype=torch.float32, device=device)
         lse = torch.empty(tokens, dtype=torch.float32, device=device)
         if tokens:
             a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
             _call("linear_cross_entropy", L.uzip_linear_cross_entropy, L.uzip_linear_cross_entropy_workspace_size, w, a, ws,
-                  stream, loss, lse)
+                  stream)
+    _share(stream, caller, new=(loss, lse), given=(ws,))
     return loss, lse
 
 
@@ -486,7 +517,8 @@ def linear_cross_entropy_backward(dloss, x, weight: PackedWeight, target, lse, i
     L, device = _lib(), w.device
     a.dloss = _vector(dloss, "dloss", tokens, device, torch.float32)
     a.lse = _vector(lse, "lse", tokens, device, torch.float32)
-    with _on(device):
+    caller = _caller(device, stream)
+    with _on(device, stream):
         dx = dw = None
         if need_x:
             dx = torch.empty((tokens, w.shape[1]), dtype=torch.bfloat16, device=device)
@@ -495,5 +527,6 @@ def linear_cross_entropy_backward(dloss, x, weight: PackedWeight, target, lse, i
             dw = torch.empty(w.shape, dtype=torch.bfloat16, device=device)
             a.dw = dw.data_ptr()
         _call("linear_cross_entropy_backward", L.uzip_linear_cross_entropy_backward,
-              L.uzip_linear_cross_entropy_backward_workspace_size, w, a, ws, stream, dx, dw)
+              L.uzip_linear_cross_entropy_backward_workspace_size, w, a, ws, stream)
+    _share(stream, caller, new=(dx, dw), given=(ws,))
     return dx, dw

@@ -62,3 +62,38 @@ def test_groups_out_of_order_keep_their_rows(name, n, k, act, out):
             close(dx[s], *want["dx"], "dx of group %d" % i)
             close(dw[i], *want["dw"], "dw of group %d" % i)
         assert (y[rest] == 0).all() and (dx[rest] == 0).all()
+
+
+# ---- a stream of the call's own ----------------------------------------------------
+
+def test_memory_of_a_call_on_another_stream_is_that_streams_own():
+    """Blocks that the current stream's pending work still uses are not handed to a call on another stream."""
+    m, n, k, act = 300, 320, 4096, "silu"
+    g = gen(2)
+    x, dy, wt = normal(g, m, k), normal(g, m, n), normal(g, n, k, scale=0.05)
+    w, t, dl = uz.pack_weight(wt), torch.randint(0, n, (m,), generator=g).to(DEV), torch.ones(m, device=DEV)
+
+    def calls(**kw):
+        p = uz.pack_weight(wt, **kw)
+        y, z = uz.linear(x, w, act=act, return_preact=True, **kw)
+        dx, dw, db = uz.linear_backward(dy, x, w, preact=z, act=act, need_bias=True, **kw)
+        loss, lse = uz.linear_cross_entropy(x, w, t, **kw)
+        lx, lw = uz.linear_cross_entropy_backward(dl, x, w, t, lse, **kw)
+        return [p.data, uz.unpack_weight(w, **kw), y, z, dx, dw, db, loss, lse, lx, lw]
+
+    want = calls()
+    main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = [torch.empty(s, dtype=torch.uint8, device=DEV) for s in (512, m * n * 2, m * n * 4, 1 << 21, 1 << 25, 1 << 25)]
+    for b in busy:
+        b.zero_()
+    del b, busy  # free for the current stream's next work, and only for that
+    side.wait_stream(main)
+    got = calls(stream=side)
+    blocks = [(s["address"], s["address"] + s["total_size"]) for s in torch.cuda.memory_snapshot()
+              if s["stream"] == side.cuda_stream]
+    for r in got:
+        assert any(a <= r.data_ptr() < e for a, e in blocks), (r.shape, r.dtype)
+    main.wait_stream(side)
+    for a, b in zip(want, got):
+        assert torch.equal(a.reshape(-1).view(torch.uint8), b.reshape(-1).view(torch.uint8))
