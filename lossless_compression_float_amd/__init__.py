@@ -14,6 +14,7 @@ fails loudly when the library is missing.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import os
 
@@ -290,6 +291,26 @@ def _keep_for(stream, *tensors):
                 u.record_stream(stream)
 
 
+def _memory_of(stream):
+    """What is allocated under this comes from `stream`'s memory: a block of
+    the current stream's could still be in use by its pending work when
+    `stream` writes it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *tensors):
+    """Tensors allocated under `_memory_of(stream)` that the caller gets: the
+    current stream will use them too."""
+    if stream is None:
+        return
+    caller = torch.cuda.current_stream(stream.device)
+    if stream == caller:
+        return
+    for t in tensors:
+        for u in [t] if isinstance(t, torch.Tensor) else t:
+            u.record_stream(caller)
+
+
 def _check(st: int, what: str):
     if st != UZIP_OK:
         raise UzipError(st, what)
@@ -313,18 +334,20 @@ def compress(t: torch.Tensor, chunk_bytes: int = 0, out: torch.Tensor | None = N
     cap = uzip_max_compressed_size(code, n, chunk_bytes)
     if cap == 0:
         raise ValueError("invalid chunk_bytes %d, or %d values beyond the limits of one call" % (chunk_bytes, n))
-    if out is None:
-        out = torch.empty(cap, dtype=torch.uint8, device=t.device)
-    if out_size is None:
-        out_size = torch.empty(1, dtype=torch.int64, device=t.device)
-    wsz = uzip_workspace_size(code, n, chunk_bytes)
-    if ws is None:
-        ws = workspace(wsz, t.device)
+    with _memory_of(stream):
+        if out is None:
+            out = torch.empty(cap, dtype=torch.uint8, device=t.device)
+        if out_size is None:
+            out_size = torch.empty(1, dtype=torch.int64, device=t.device)
+        wsz = uzip_workspace_size(code, n, chunk_bytes)
+        if ws is None:
+            ws = workspace(wsz, t.device)
     fn = uzip_compress_sampled if sampled else uzip_compress
     st = fn(code, t.data_ptr() if n else None, n, chunk_bytes, out.data_ptr(), out.numel(),
             out_size.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(st, fn.__name__)
     _keep_for(stream, out, out_size, ws)
+    _hand_over(stream, out, out_size)
     return out, out_size
 
 
@@ -335,17 +358,19 @@ def decompress(buf: torch.Tensor, dtype: torch.dtype, n: int, in_bytes: int | No
     (values, status) where status is a one-element int32 device tensor
     (0 = valid, 3 = corrupt input)."""
     code = dtype_code(dtype)
-    if out is None:
-        out = torch.empty(n, dtype=dtype, device=buf.device)
-    if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=buf.device)
-    if ws is None:
-        ws = workspace(uzip_workspace_size(code, 0, 0), buf.device)
+    with _memory_of(stream):
+        if out is None:
+            out = torch.empty(n, dtype=dtype, device=buf.device)
+        if status is None:
+            status = torch.empty(1, dtype=torch.int32, device=buf.device)
+        if ws is None:
+            ws = workspace(uzip_workspace_size(code, 0, 0), buf.device)
     nb = buf.numel() if in_bytes is None else in_bytes
     st = uzip_decompress(buf.data_ptr() if nb else None, nb, code, n, out.data_ptr() if n else None,
                          status.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(st, "uzip_decompress")
     _keep_for(stream, out, status, ws)
+    _hand_over(stream, out, status)
     return out, status
 
 
@@ -357,36 +382,40 @@ def compress_batched(tensors, chunk_bytes: int = 0, outs=None, ws=None, out_size
     code = dtype_code(tensors[0].dtype)
     dev = tensors[0].device
     ns = [t.numel() for t in tensors]
-    if outs is None:
-        outs = [torch.empty(uzip_max_compressed_size(code, n, chunk_bytes), dtype=torch.uint8, device=dev) for n in ns]
-    if out_sizes is None:
-        out_sizes = torch.empty(len(tensors), dtype=torch.int64, device=dev)
-    if ws is None:
-        ws = workspace(uzip_workspace_size_batched(code, ns, chunk_bytes), dev)
+    with _memory_of(stream):
+        if outs is None:
+            outs = [torch.empty(uzip_max_compressed_size(code, n, chunk_bytes), dtype=torch.uint8, device=dev) for n in ns]
+        if out_sizes is None:
+            out_sizes = torch.empty(len(tensors), dtype=torch.int64, device=dev)
+        if ws is None:
+            ws = workspace(uzip_workspace_size_batched(code, ns, chunk_bytes), dev)
     fn = uzip_compress_batched_sampled if sampled else uzip_compress_batched
     st = fn(code, [t.data_ptr() if t.numel() else 0 for t in tensors], ns, chunk_bytes,
             [o.data_ptr() for o in outs], [o.numel() for o in outs], out_sizes.data_ptr(),
             ws.data_ptr(), ws.numel(), _stream(stream))
     _check(st, fn.__name__)
     _keep_for(stream, outs, out_sizes, ws)
+    _hand_over(stream, outs, out_sizes)
     return outs, out_sizes
 
 
 def decompress_batched(bufs, dtype: torch.dtype, ns, in_bytes=None, outs=None, status=None, ws=None, stream=None):
     code = dtype_code(dtype)
     dev = bufs[0].device
-    if outs is None:
-        outs = [torch.empty(n, dtype=dtype, device=dev) for n in ns]
-    if status is None:
-        status = torch.empty(len(bufs), dtype=torch.int32, device=dev)
-    if ws is None:
-        ws = workspace(uzip_workspace_size_batched(code, list(ns), 0), dev)
+    with _memory_of(stream):
+        if outs is None:
+            outs = [torch.empty(n, dtype=dtype, device=dev) for n in ns]
+        if status is None:
+            status = torch.empty(len(bufs), dtype=torch.int32, device=dev)
+        if ws is None:
+            ws = workspace(uzip_workspace_size_batched(code, list(ns), 0), dev)
     nbs = [b.numel() for b in bufs] if in_bytes is None else list(in_bytes)
     st = uzip_decompress_batched(code, [b.data_ptr() for b in bufs], nbs, list(ns),
                                  [o.data_ptr() if o.numel() else 0 for o in outs], status.data_ptr(), ws.data_ptr(),
                                  ws.numel(), _stream(stream))
     _check(st, "uzip_decompress_batched")
     _keep_for(stream, outs, status, ws)
+    _hand_over(stream, outs, status)
     return outs, status
 
 
@@ -413,18 +442,20 @@ def compress_arbitrated(t: torch.Tensor, pol: uzip_policy, chunk_bytes: int = 0,
     cap = uzip_max_compressed_size(code, n, chunk_bytes)
     if cap == 0:
         raise ValueError("invalid chunk_bytes %d, or %d values beyond the limits of one call" % (chunk_bytes, n))
-    if out is None:
-        out = torch.empty(cap, dtype=torch.uint8, device=t.device)
-    if out_size is None:
-        out_size = torch.empty(1, dtype=torch.int64, device=t.device)
-    if plan is None:
-        plan = torch.empty(4, dtype=torch.int64, device=t.device)
-    if ws is None:
-        ws = workspace(uzip_workspace_size(code, n, chunk_bytes), t.device)
+    with _memory_of(stream):
+        if out is None:
+            out = torch.empty(cap, dtype=torch.uint8, device=t.device)
+        if out_size is None:
+            out_size = torch.empty(1, dtype=torch.int64, device=t.device)
+        if plan is None:
+            plan = torch.empty(4, dtype=torch.int64, device=t.device)
+        if ws is None:
+            ws = workspace(uzip_workspace_size(code, n, chunk_bytes), t.device)
     st = uzip_compress_arbitrated(code, t.data_ptr() if n else None, n, chunk_bytes, pol, out.data_ptr(), out.numel(),
                                   out_size.data_ptr(), plan.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(st, "uzip_compress_arbitrated")
     _keep_for(stream, out, out_size, plan, ws)
+    _hand_over(stream, out, out_size, plan)
     return out, out_size, plan
 
 
@@ -434,20 +465,22 @@ def compress_batched_arbitrated(tensors, pol: uzip_policy, chunk_bytes: int = 0,
     code = dtype_code(tensors[0].dtype)
     dev = tensors[0].device
     ns = [t.numel() for t in tensors]
-    if outs is None:
-        outs = [torch.empty(uzip_max_compressed_size(code, n, chunk_bytes), dtype=torch.uint8, device=dev) for n in ns]
-    if out_sizes is None:
-        out_sizes = torch.empty(len(tensors), dtype=torch.int64, device=dev)
-    if plans is None:
-        plans = torch.empty(4 * len(tensors), dtype=torch.int64, device=dev)
-    if ws is None:
-        ws = workspace(uzip_workspace_size_batched(code, ns, chunk_bytes), dev)
+    with _memory_of(stream):
+        if outs is None:
+            outs = [torch.empty(uzip_max_compressed_size(code, n, chunk_bytes), dtype=torch.uint8, device=dev) for n in ns]
+        if out_sizes is None:
+            out_sizes = torch.empty(len(tensors), dtype=torch.int64, device=dev)
+        if plans is None:
+            plans = torch.empty(4 * len(tensors), dtype=torch.int64, device=dev)
+        if ws is None:
+            ws = workspace(uzip_workspace_size_batched(code, ns, chunk_bytes), dev)
     st = uzip_compress_batched_arbitrated(code, [t.data_ptr() if t.numel() else 0 for t in tensors], ns, chunk_bytes,
                                           pol, [o.data_ptr() for o in outs], [o.numel() for o in outs],
                                           out_sizes.data_ptr(), plans.data_ptr(), ws.data_ptr(), ws.numel(),
                                           _stream(stream))
     _check(st, "uzip_compress_batched_arbitrated")
     _keep_for(stream, outs, out_sizes, plans, ws)
+    _hand_over(stream, outs, out_sizes, plans)
     return outs, out_sizes, plans
 
 
