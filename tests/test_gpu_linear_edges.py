@@ -2,6 +2,8 @@
 out of order, rows of no group, the activations' tails, masked tokens, runs of
 the contraction joined behind every epilogue.  The bounds are derived in
 linear_testlib or beside the test."""
+import math
+
 import pytest
 import torch
 
@@ -97,3 +99,57 @@ def test_memory_of_a_call_on_another_stream_is_that_streams_own():
     main.wait_stream(side)
     for a, b in zip(want, got):
         assert torch.equal(a.reshape(-1).view(torch.uint8), b.reshape(-1).view(torch.uint8))
+
+
+# ---- tails of the activations --------------------------------------------------------
+
+STEP = 2.0 ** -24
+K0, K1 = math.sqrt(2 / math.pi), 0.044715
+
+
+def scalar64(z, act):
+    """(act(z), act'(z), how far fp32 may be off relative to each of its terms, act's two terms) in 64 bits.  The
+    function's argument passes through up to 2 (gelu: a rounded constant and a product) or 8 roundings (tanh form: 2 u);
+    erfc(t) then moves by at most t (2 t + 1.2) = z^2 + 0.9 |z| times the argument's relative error, exp(-2 u) by 2 |u| times it,
+    exp(-z^2 / 2) by z^2 / 2 times two roundings.  2^-20 covers the functions themselves and the products around them."""
+    if act == "gelu":
+        cdf = 0.5 * torch.special.erfc(-z / math.sqrt(2))
+        slope = z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+        rel = 2 * STEP * (z * z + 0.9 * z.abs()) + 2.0 ** -20
+        return z * cdf, cdf + slope, rel, (cdf, slope)
+    u2 = 2 * K0 * (z + K1 * z ** 3)
+    s, r = torch.sigmoid(u2), torch.sigmoid(-u2)
+    slope = z * s * r * 2 * K0 * (1 + 3 * K1 * z * z)
+    return z * s, s + slope, 2 * 8 * STEP * u2.abs() + 2.0 ** -20, (s, slope)
+
+
+TINY = 2.0 ** -120  # results that have run out of exponents: exp(2 u) passes fp32's range at 2 u = 88
+
+
+@pytest.mark.parametrize("m", [1, 200])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh"])
+def test_gelu_keeps_its_bits_in_the_negative_tail(m, act):
+    z = torch.cat((torch.linspace(-12, 12, 1531), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 100.0, -13.0]))).to(BF)
+    n = z.numel()
+    w = torch.zeros(n, 8, dtype=BF, device=DEV)
+    w[:, 0] = z.to(DEV)
+    x = torch.zeros(m, 8, dtype=BF, device=DEV)
+    x[:, 0] = 1
+    p = uz.pack_weight(w)
+    y, pre = uz.linear(x, p, act=act, out_dtype=F32, return_preact=True)
+    z = z.double()
+    assert torch.equal(pre.cpu().double(), z.expand(m, n))
+    y64, _, rel, _ = scalar64(z, act)
+    close(y, y64.expand(m, n), ((rel + STEP) * y64.abs() + TINY).expand(m, n), "y")
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh"])
+def test_gelus_gradient_keeps_its_bits_in_the_negative_tail(act):
+    """One row of dy, whose bias gradient is the unrounded gradient of the pre-activation."""
+    z = torch.cat((torch.linspace(-12, 12, 4000), torch.tensor([0.0, 1e-30, 100.0, -13.0])))
+    n = z.numel()
+    p = uz.pack_weight(torch.zeros(n, 8, dtype=BF, device=DEV))
+    _, _, db = uz.linear_backward(torch.ones(1, n, device=DEV), None, p, preact=z[None].to(DEV), act=act, need_x=False,
+                                  need_weight=False, need_bias=True, bias_dtype=F32)
+    _, d64, rel, (a, b) = scalar64(z.double(), act)
+    close(db, d64, (rel + STEP) * (a.abs() + b.abs()) + TINY, "gradient")
