@@ -471,7 +471,8 @@ __device__ inline float activate_grad(float z, uint32_t act) {
     case kActGelu: return normal_cdf(z) + z * 0.3989422804014327f * expf(-0.5f * z * z);
     case kActGeluTanh: {
         const float u2 = gelu_tanh_2u(z), s = sigmoid(u2), r = sigmoid(-u2);  // r = 1 - s
-        return s + z * (s * r) * (2.0f * kGeluC * (1.0f + 0.134145f * z * z));
+        // (s r is 0 from |z| = 12 on: there z^2 must only not be infinite)
+        return s + z * (s * r) * (2.0f * kGeluC * (1.0f + 0.134145f * fminf(z * z, 1e6f)));
     }
     case kActSilu: {
         const float s = sigmoid(z);

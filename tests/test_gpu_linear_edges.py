@@ -153,3 +153,19 @@ def test_gelus_gradient_keeps_its_bits_in_the_negative_tail(act):
                                   need_weight=False, need_bias=True, bias_dtype=F32)
     _, d64, rel, (a, b) = scalar64(z.double(), act)
     close(db, d64, (rel + STEP) * (a.abs() + b.abs()) + TINY, "gradient")
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+def test_huge_values_have_the_gradient_of_the_limit(act):
+    """0 to the left, 1 to the right (swiglu: times the other half, 1 here), past where z^2 and z^3 leave fp32."""
+    big = torch.tensor([1e3, 1e10, 1e13, 2e19, 1e25, 3e38])
+    z = torch.cat((big, -big))
+    n = z.numel()
+    gated = act == "swiglu"
+    pre = torch.cat((z, torch.ones(n)))[None] if gated else z[None]
+    p = uz.pack_weight(torch.zeros(pre.shape[1], 8, dtype=BF, device=DEV), gated=gated)
+    _, _, db = uz.linear_backward(torch.ones(1, n, device=DEV), None, p, preact=pre.to(DEV), act=act, need_x=False,
+                                  need_weight=False, need_bias=True, bias_dtype=F32)
+    assert torch.equal(db.cpu()[:n], (z > 0).float()), db
+    if gated:
+        assert torch.equal(db.cpu()[n:], z.clamp(min=0))
