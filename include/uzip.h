@@ -396,7 +396,7 @@ typedef struct {
     uint32_t y_dtype;
     uint32_t act;        /* uzip_act */
     uint32_t preact_dtype;
-    uint32_t clear_rest; /* grouped: 1 writes zeros to y in the rows of no group */
+    uint32_t clear_rest; /* grouped: 1 writes zeros to y and preact in the rows of no group */
     uint32_t reserved;   /* 0 */
 } uzip_linear_args;
 

@@ -650,6 +650,16 @@ __device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups,
     }
 }
 
+// The same for columns [c0, c1) of a part in y and in the pre-activation.
+template <class P>
+__device__ inline void clear_rest_linear(const P &p, uint32_t c0, uint32_t c1, uint32_t threads) {
+    const LinearEpi &e = p.lin;
+    clear_rest(p.offsets, p.groups, p.tokens, e.y, e.y_stride, e.y_f32 ? 4 : 2, c0, c1, threads);
+    if (!e.preact) return;
+    for (uint32_t n = 0; n < p.w.parts * p.w.part_rows; n += p.w.part_rows)
+        clear_rest(p.offsets, p.groups, p.tokens, e.preact, e.preact_stride, e.preact_f32 ? 4 : 2, n + c0, n + c1, threads);
+}
+
 // ---- few rows ---------------------------------------------------------------------
 
 // y = W x for up to 16 MT rows of x at a time.  Bound by the reads of W: 28672
@@ -672,8 +682,7 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
     if (p.lin.clear && blockIdx.y == 0) {
         constexpr uint32_t WIDE = (GATED ? RB / 2 : RB) * 16;
         const uint32_t c = min(blockIdx.x * WIDE, p.w.part_rows);
-        clear_rest(p.offsets, p.groups, p.tokens, p.lin.y, p.lin.y_stride, p.lin.y_f32 ? 4 : 2, c,
-                   min(c + WIDE, p.w.part_rows), NW * 64);
+        clear_rest_linear(p, c, min(c + WIDE, p.w.part_rows), NW * 64);
     }
     if (begin == end) return;
     const uint32_t KB = p.w.col_blocks, n = (KB + NW - 1 - wave) / NW;  // blocks of this wave
@@ -998,9 +1007,11 @@ __global__ __launch_bounds__(WR *WC *WK * 64, 2) void k_gemm(GemmParams p) {
             if (blockIdx.y) return;
             constexpr bool F = KIND == kGemmForward;
             const uint32_t wide = GATED ? TR / 2 : TR, limit = F ? p.w.part_rows : p.cols;
-            const uint32_t c = (blockIdx.x - total) * wide;
-            clear_rest(p.offsets, p.groups, p.tokens, F ? p.lin.y : p.store.out, F ? p.lin.y_stride : p.store.stride,
-                       F && p.lin.y_f32 ? 4 : 2, min(c, limit), min(c + wide, limit), ALL * 64);
+            const uint32_t c = min((blockIdx.x - total) * wide, limit), end = min(c + wide, limit);
+            if constexpr (F)
+                clear_rest_linear(p, c, end, ALL * 64);
+            else
+                clear_rest(p.offsets, p.groups, p.tokens, p.store.out, p.store.stride, 2, c, end, ALL * 64);
             return;
         }
     }

@@ -110,7 +110,7 @@ struct LinearEpi {
     void *preact;           // or null
     uint64_t residual_stride, y_stride, preact_stride;
     uint32_t bias_f32, y_f32, preact_f32, act;
-    uint32_t clear;         // zeros in the rows of no group
+    uint32_t clear;         // zeros in y's and the pre-activation's rows of no group
 };
 
 // The loss's epilogues.

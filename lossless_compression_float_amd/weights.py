@@ -383,7 +383,9 @@ def _forward(what, w, x, offsets, bias, act, residual, out_dtype, return_preact,
         if out is None:
             out = torch.empty((tokens, width), dtype=out_dtype, device=device)
             y_stride = width
-        z = torch.empty((tokens, rows), dtype=preact_dtype, device=device) if return_preact else None
+        z = None
+        if return_preact:  # (rows of no group: zero; the call itself clears them only together with a new output's)
+            z = (torch.zeros if grouped and not clear else torch.empty)((tokens, rows), dtype=preact_dtype, device=device)
         if tokens:
             a = uzip_linear_args(x.data_ptr(), x_stride, tokens, off, b, r, r_stride, out.data_ptr(), y_stride,
                                  z.data_ptr() if return_preact else 0, rows, b_code, y_code, act, z_code, clear)
@@ -411,7 +413,7 @@ def grouped_linear(x, offsets, weight: PackedWeight, bias=None, act: str = "none
     of x [tokens, cols] are multiplied with matrix g of a packed stack
     [matrices, rows, cols].  offsets: matrices + 1 ascending int32 values on
     the device.  bias: [matrices, rows].  Rows of no group are not written:
-    zero in a new output, unchanged in `out`."""
+    zero in a new output and in the pre-activation, unchanged in `out`."""
     return _forward("grouped_linear", weight, x, offsets, bias, act, None, out_dtype, return_preact, preact_dtype, out, ws,
                     stream)
 

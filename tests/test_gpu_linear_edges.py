@@ -66,6 +66,32 @@ def test_groups_out_of_order_keep_their_rows(name, n, k, act, out):
         assert (y[rest] == 0).all() and (dx[rest] == 0).all()
 
 
+@pytest.mark.parametrize("keep", [F32, BF])
+@pytest.mark.parametrize("own_out", [False, True])
+@pytest.mark.parametrize("offsets,t", [([3, 5, 5, 9], 20), ([100, 180, 181, 400], 450), ([0, 0, 0, 0], 40), ([7, 9, 2, 6], 12)])
+@pytest.mark.parametrize("n,k,act", [(40, 64, "silu"), (134, 72, "swiglu"), (256, 2048, "gelu")])
+def test_the_pre_activation_of_rows_of_no_group_is_zero(offsets, t, n, k, act, own_out, keep):
+    g = gen(3)
+    w, x = normal(g, 3, n, k, scale=0.1), normal(g, t, k)
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    p = uz.pack_weight(w, gated=act == "swiglu")
+    width = n // 2 if act == "swiglu" else n
+    out = torch.full((t, width), 5.0, dtype=BF, device=DEV) if own_out else None
+    junk = [torch.full((t, n), float("nan"), dtype=keep, device=DEV) for _ in range(4)]  # what new memory may hold
+    torch.cuda.synchronize()
+    del junk
+    y, z = uz.grouped_linear(x, off, p, act=act, return_preact=True, preact_dtype=keep, out=out)
+    rest = torch.ones(t, dtype=torch.bool, device=DEV)
+    for i in range(3):
+        s = slice(offsets[i], offsets[i + 1])
+        if offsets[i + 1] > offsets[i]:
+            rest[s] = False
+            z64, ez, y64, ey = linear64(x[s], w[i], None, act, None, BF, keep)
+            close(z[s], z64, ez, "preact")
+            close(y[s], y64, ey, "y")
+    assert (z[rest] == 0).all() and (y[rest] == (5 if own_out else 0)).all()
+
+
 # ---- a stream of the call's own ----------------------------------------------------
 
 def test_memory_of_a_call_on_another_stream_is_that_streams_own():
