@@ -404,6 +404,19 @@ __global__ __launch_bounds__(256) void k_unpack(UnpackParams p) {
     }
 }
 
+// Columns c .. c + 7 of a row, zeros behind the last column.
+__device__ inline u32x4 stage_unit(const uint16_t *row, uint64_t c, uint64_t cols) {
+    u32x4 v = {0, 0, 0, 0};
+    if (c + 8 <= cols) {
+        v = *reinterpret_cast<const u32x4_any *>(row + c);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < cols) v[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
+    }
+    return v;
+}
+
 // Rows copied to a stride of whole 16-byte units, zeros behind the last column:
 // the tiled products read x 16 bytes at a time, and what lies behind a row must
 // not meet the zeros of a packed weight as a NaN.  1999 x 2050 in 6.2 us, 2.6
@@ -413,16 +426,7 @@ __global__ __launch_bounds__(256) void k_stage(const uint16_t *in, uint64_t in_s
     const uint64_t units = out_stride / 8, n = rows * units;
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (uint64_t)gridDim.x * 256) {
         const uint64_t row = i / units, c = i % units * 8;
-        const uint16_t *from = in + row * in_stride + c;
-        u32x4 v = {0, 0, 0, 0};
-        if (c + 8 <= cols) {
-            v = *reinterpret_cast<const u32x4_any *>(from);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < cols) v[j >> 1] |= (uint32_t)from[j] << (16 * (j & 1));
-        }
-        *reinterpret_cast<u32x4 *>(out + row * out_stride + c) = v;
+        *reinterpret_cast<u32x4 *>(out + row * out_stride + c) = stage_unit(in + row * in_stride, c, cols);
     }
 }
 
@@ -1695,15 +1699,31 @@ __global__ __launch_bounds__(64) void k_loss_join(LossEpi e, float *loss, float 
     }
 }
 
-// One workgroup: 5 us for 4096 tokens.
-__global__ __launch_bounds__(1024) void k_loss_unit(LossEpi e, float *unit, uint32_t tokens, uint64_t vocab) {
+// What the gradients need first, in one launch.  Workgroup 0: the largest dloss
+// (5 us for 4096 tokens).  The others, if `out` is given: x in rows of whole 16-byte
+// units, with zeros for the tokens that do not count: their dlogits are 0, but in
+// dw 0 times an infinity or a NaN, as the rows of padding may hold, would not be.
+__global__ __launch_bounds__(1024) void k_loss_begin(LossEpi e, float *unit, uint32_t tokens, uint64_t vocab,
+                                                     const uint16_t *in, uint64_t in_stride, uint16_t *out,
+                                                     uint64_t out_stride, uint64_t cols) {
     __shared__ float red[16];
+    auto counts = [&](int64_t t) { return t != e.ignore && t >= 0 && t < (int64_t)vocab; };
+    if (blockIdx.x) {
+        const uint64_t units = out_stride / 8, n = tokens * units, step = (uint64_t)(gridDim.x - 1) * 1024;
+        for (uint64_t i = (uint64_t)(blockIdx.x - 1) * 1024 + threadIdx.x; i < n; i += step) {
+            const uint64_t row = n >> 32 ? i / units : (uint32_t)i / (uint32_t)units, c = (i - row * units) * 8;
+            const int64_t t = e.target[row];  // (both loads together)
+            u32x4 v = stage_unit(in + row * in_stride, c, cols);
+            if (!counts(t)) v = u32x4{0, 0, 0, 0};
+            *reinterpret_cast<u32x4 *>(out + row * out_stride + c) = v;
+        }
+        return;
+    }
     float top = 0;
 #pragma unroll 4
     for (uint32_t m = threadIdx.x; m < tokens; m += 1024) {
-        const int64_t t = e.target[m];
         const float a = fabsf(e.dloss[m]);
-        if (t != e.ignore && t >= 0 && t < (int64_t)vocab && a < INFINITY) top = fmaxf(top, a);
+        if (counts(e.target[m]) && a < INFINITY) top = fmaxf(top, a);
     }
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
@@ -1938,8 +1958,11 @@ hipError_t launch_loss_join(const LossEpi &e, float *loss, float *lse, uint32_t 
     return hipGetLastError();
 }
 
-hipError_t launch_loss_unit(const LossEpi &e, float *unit, uint32_t tokens, uint64_t vocab, hipStream_t s) {
-    k_loss_unit<<<1, 1024, 0, s>>>(e, unit, tokens, vocab);
+hipError_t launch_loss_begin(const LossEpi &e, float *unit, uint32_t tokens, uint64_t vocab, const uint16_t *in,
+                             uint64_t in_stride, uint16_t *out, uint64_t out_stride, uint64_t cols, hipStream_t s) {
+    const uint64_t wgs = out ? (tokens * (out_stride / 8) + 1023) / 1024 : 0;
+    k_loss_begin<<<1 + (uint32_t)(wgs < 2048 ? wgs : 2048), 1024, 0, s>>>(e, unit, tokens, vocab, in, in_stride, out,
+                                                                          out_stride, cols);
     return hipGetLastError();
 }
 

@@ -197,8 +197,10 @@ uint32_t gemm_splits(GemmKind kind, GemmTile tile, uint64_t r_tiles, uint64_t c_
 hipError_t launch_gemm(GemmKind kind, GemmTile tile, const GemmParams &p, hipStream_t s);
 hipError_t launch_loss_join(const LossEpi &e, float *loss, float *lse, uint32_t tokens, uint32_t parts, uint64_t vocab,
                             hipStream_t s);
-// The largest finite |dloss| of the tokens that count (1 where all are 0).
-hipError_t launch_loss_unit(const LossEpi &e, float *unit, uint32_t tokens, uint64_t vocab, hipStream_t s);
+// The largest finite |dloss| of the tokens that count (1 where all are 0); with `out`, x is staged there with zeros for
+// those that do not.
+hipError_t launch_loss_begin(const LossEpi &e, float *unit, uint32_t tokens, uint64_t vocab, const uint16_t *in,
+                             uint64_t in_stride, uint16_t *out, uint64_t out_stride, uint64_t cols, hipStream_t s);
 hipError_t launch_dz(const DzParams &p, hipStream_t s);
 
 }  // namespace uzip

@@ -373,7 +373,7 @@ Cut cut_dx(const uzip_weight *w, const uzip_loss_args *a, uint64_t rows) {
 
 LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward, Carver &c) {
     LossPlan p{};
-    p.stage = !tiled(a->x, a->x_stride, w->cols);
+    p.stage = !tiled(a->x, a->x_stride, w->cols) || (backward && a->dw);  // (dw: with zeros for tokens that do not count)
     if (p.stage) p.x = c.take<uint16_t>(a->tokens * up(w->cols, 8));
     if (!backward) {
         if (a->tokens == 0) return p;
@@ -400,11 +400,9 @@ LossPlan plan_loss(const uzip_weight *w, const uzip_loss_args *a, bool backward,
     return p;
 }
 
-uzip_status stage_loss_x(const uzip_weight *w, const uzip_loss_args *a, const LossPlan &plan, Mat &x, hipStream_t stream) {
-    x = Mat{a->x, a->x_stride};
-    if (!plan.stage) return UZIP_OK;
-    x = Mat{plan.x, up(w->cols, 8)};
-    return done(launch_stage(static_cast<const uint16_t *>(a->x), a->x_stride, plan.x, x.stride, a->tokens, w->cols, stream));
+// x as the products read it.
+Mat loss_x(const uzip_weight *w, const uzip_loss_args *a, const LossPlan &plan) {
+    return plan.stage ? Mat{plan.x, up(w->cols, 8)} : Mat{a->x, a->x_stride};
 }
 
 GemmParams loss_params(const uzip_weight *w, const uzip_loss_args *a) {
@@ -525,7 +523,10 @@ uzip_status uzip_linear_cross_entropy(const uzip_weight *weight, const uzip_loss
     if (!workspace_ok(d_workspace, workspace_bytes, c.bytes())) return UZIP_ERR_INVALID_ARGUMENT;
     if (args->tokens == 0) return UZIP_OK;
     GemmParams p = loss_params(weight, args);
-    if (stage_loss_x(weight, args, plan, p.cmat, stream) != UZIP_OK) return UZIP_ERR_DEVICE;
+    p.cmat = loss_x(weight, args, plan);
+    if (plan.stage && launch_stage(static_cast<const uint16_t *>(args->x), args->x_stride, plan.x, p.cmat.stride, args->tokens,
+                                   weight->cols, stream) != hipSuccess)
+        return UZIP_ERR_DEVICE;
     p.c_limit = (uint32_t)up(weight->cols, 8);
     plan.cut.set(p, plan.part);
     p.steps = p.w.col_blocks;
@@ -550,15 +551,16 @@ uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const 
     if (!workspace_ok(d_workspace, workspace_bytes, c.bytes())) return UZIP_ERR_INVALID_ARGUMENT;
     if (!args->dx && !args->dw) return UZIP_OK;
     GemmParams p = loss_params(weight, args);
-    Mat x{};
-    if (args->tokens && stage_loss_x(weight, args, plan, x, stream) != UZIP_OK) return UZIP_ERR_DEVICE;
+    const Mat x = loss_x(weight, args, plan);
     p.loss.lse = args->lse;
     p.loss.dloss = args->dloss;
     p.loss.dz = plan.dz;
     p.loss.dz_stride = plan.piece;
     if (args->tokens) {
         p.loss.unit = plan.unit;
-        if (launch_loss_unit(p.loss, plan.unit, args->tokens, weight->rows, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+        if (launch_loss_begin(p.loss, plan.unit, args->tokens, weight->rows, static_cast<const uint16_t *>(args->x),
+                              args->x_stride, plan.x, x.stride, weight->cols, stream) != hipSuccess)
+            return UZIP_ERR_DEVICE;
     }
     const uint32_t all = p.w.row_blocks, step = (uint32_t)(plan.piece / kTileRows);
     for (uint32_t b0 = 0; b0 < all; b0 += step) {

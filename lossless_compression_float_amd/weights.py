@@ -514,7 +514,8 @@ def linear_cross_entropy(x, weight: PackedWeight, target, ignore_index: int = -1
 def linear_cross_entropy_backward(dloss, x, weight: PackedWeight, target, lse, ignore_index: int = -100,
                                   need_x: bool = True, need_weight: bool = True, ws=None, stream=None):
     """(dx, dw) of `linear_cross_entropy`, bf16, None for one not needed, given
-    the losses' gradients dloss (fp32 [tokens]) and its lse."""
+    the losses' gradients dloss (fp32 [tokens]) and its lse.  Tokens that are
+    ignored or have no such target leave no trace, whatever their x holds."""
     w, tokens, a = _loss_args("linear_cross_entropy_backward", x, weight, target, ignore_index)
     L, device = _lib(), w.device
     a.dloss = _vector(dloss, "dloss", tokens, device, torch.float32)

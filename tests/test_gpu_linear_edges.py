@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import lossless_compression_float_amd as uz
-from linear_testlib import backward64, close, linear64
+from linear_testlib import backward64, close, linear64, loss64, loss_backward64
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -195,3 +195,43 @@ def test_huge_values_have_the_gradient_of_the_limit(act):
     assert torch.equal(db.cpu()[:n], (z > 0).float()), db
     if gated:
         assert torch.equal(db.cpu()[n:], z.clamp(min=0))
+
+
+# ---- masked tokens of the loss ----------------------------------------------------------
+
+@pytest.mark.parametrize("m,v,k", [(5, 50, 64), (70, 1000, 65), (300, 515, 1024), (1030, 4200, 72)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_masked_tokens_may_hold_anything(m, v, k, pad):
+    """Rows of padding hold infinities and NaNs: tokens that do not count leave no trace in the gradients."""
+    g = gen(4)
+    x = torch.zeros(m, k + pad, dtype=BF, device=DEV)[:, :k]
+    x.copy_(normal(g, m, k))
+    w = normal(g, v, k, scale=0.1)
+    t = torch.randint(0, v, (m,), generator=g).to(DEV)
+    off = torch.randperm(m, generator=g)[:max(3, m // 4)].to(DEV)
+    t[off[0::3]], t[off[1::3]], t[off[2::3]] = -100, v, -1
+    p = uz.pack_weight(w)
+    clean = x.clone()
+    clean[off] = 0
+    x[off[0::2]], x[off[1::2]] = float("nan"), float("inf")
+    before = x.clone()
+    loss, lse = uz.linear_cross_entropy(x, p, t)
+    dl = torch.randn(m, generator=g).to(DEV)
+    dl[off[0]] = float("nan")
+    dx, dw = uz.linear_cross_entropy_backward(dl, x, p, t, lse)
+    kept = torch.where((t >= 0) & (t < v), t, -100)
+    l64, s64, el, es, _, _ = loss64(clean, w, kept, -100)
+    on = torch.ones(m, dtype=torch.bool, device=DEV)
+    on[off] = False
+    close(loss[on], l64[on.cpu()], el[on.cpu()], "loss")
+    close(lse[on], s64[on.cpu()], es[on.cpu()], "lse")
+    assert (loss[t == -100] == 0).all() and torch.isnan(loss[(t == -1) | (t == v)]).all()
+    dl[off[0]] = 0
+    wx, ww = loss_backward64(dl, clean, w, kept, -100)
+    close(dx, *wx, "dx")
+    close(dw, *ww, "dw")
+    assert (dx[off] == 0).all()
+    one = uz.linear_cross_entropy_backward(dl, x, p, t, lse, need_x=False)[1]
+    assert torch.equal(one, dw)
+    assert torch.equal(uz.linear_cross_entropy_backward(dl, x, p, t, lse, need_weight=False)[0], dx)
+    assert torch.equal(x.view(torch.int16), before.view(torch.int16))
