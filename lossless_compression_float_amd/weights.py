@@ -13,6 +13,11 @@ A call with ``stream=`` runs there, and what it allocates is that stream's
 memory.  The caller orders the streams: the arguments have to be ready for
 ``stream``, and be kept until its work is done, and the results are not ready
 for the current stream until that waits for it.
+
+Nothing is recorded for autograd.  Where it would be expected to be (an
+argument requires grad and gradients are enabled) the forward calls raise
+ValueError: wrap the pair of calls in a ``torch.autograd.Function``, or call
+them under ``torch.no_grad()``.
 """
 from __future__ import annotations
 
@@ -281,6 +286,15 @@ def _tokens(x, what: str) -> int:
     return x.shape[0]
 
 
+def _no_history(what: str, *tensors):
+    """Refuses arguments whose gradient autograd is to record: the result would
+    have no history, and the gradient would be missing without a word."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("%s records nothing for autograd, and an argument requires grad: call it under torch.no_grad() "
+                             "or from a torch.autograd.Function, and take the gradients from %s_backward" % (what, what))
+
+
 def _call(name: str, fn, size, w, a, ws, stream):
     """Calls `fn` with the caller's workspace or a new one (made under
     `_on(device, stream)`): nothing is shared between calls."""
@@ -378,6 +392,7 @@ def _forward(what, w, x, offsets, bias, act, residual, out_dtype, return_preact,
         if residual is not None and _overlap(out, residual) and (
                 out.data_ptr() != residual.data_ptr() or y_stride != r_stride):
             raise ValueError("out must be the residual itself or not overlap it")
+    _no_history(what, x, bias, residual, out)
     caller, given = _caller(device, stream), out
     with _on(device, stream):
         if out is None:
@@ -498,6 +513,7 @@ def linear_cross_entropy(x, weight: PackedWeight, target, ignore_index: int = -1
     gradient takes.  The logits are not stored.  A token with ignore_index has
     loss 0; a target outside the vocabulary gives NaN."""
     w, tokens, a = _loss_args("linear_cross_entropy", x, weight, target, ignore_index)
+    _no_history("linear_cross_entropy", x)
     L, device = _lib(), w.device
     caller = _caller(device, stream)
     with _on(device, stream):
