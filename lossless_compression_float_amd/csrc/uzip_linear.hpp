@@ -131,7 +131,7 @@ struct StoreEpi {
     uint16_t *out;       // null while pieces remain
     float *sum;          // fp32 running sums, or null
     const float *unit;   // the results' factor, or null
-    uint64_t stride, sum_stride, matrix_stride;
+    uint64_t stride, sum_stride;
     uint32_t add;        // read the running sums first
     uint32_t clear;      // zeros in the rows of no group
 };
