@@ -235,3 +235,113 @@ def test_masked_tokens_may_hold_anything(m, v, k, pad):
     assert torch.equal(one, dw)
     assert torch.equal(uz.linear_cross_entropy_backward(dl, x, p, t, lse, need_weight=False)[0], dx)
     assert torch.equal(x.view(torch.int16), before.view(torch.int16))
+
+
+# ---- runs of the contraction, joined behind every epilogue --------------------------------
+
+def cut(w, x, **kw):
+    """Whether a forward call with these rows of x (aligned, so not staged) has its contraction cut: only then does it need
+    a workspace."""
+    a = uz.uzip_linear_args(x=x.data_ptr(), x_stride=x.stride(0), tokens=x.shape[0], y=x.data_ptr(), y_stride=1 << 20,
+                            y_dtype=uz.UZIP_BF16, **kw)
+    return uz.uzip_linear_workspace_size(w._c, a) > 0
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("bias", [BF, F32, None])
+@pytest.mark.parametrize("m,n,k,act", [(100, 256, 2048, "swiglu"), (40, 516, 4096, "swiglu"), (100, 300, 2048, "gelu"),
+                                       (130, 515, 1096, "silu")])
+def test_joined_runs_of_linear(m, n, k, act, bias, out):
+    g = gen(5)
+    gated = act == "swiglu"
+    x, w = normal(g, m, k), normal(g, n, k, scale=0.02)
+    b = None if bias is None else normal(g, n, dtype=bias)
+    r = normal(g, m, n // 2 if gated else n, dtype=out)
+    p = uz.pack_weight(w, gated=gated)
+    assert cut(p, x, act=uz.ACTIVATIONS[act])
+    for keep in (F32, BF):
+        y, z = uz.linear(x, p, bias=b, act=act, residual=r, out_dtype=out, return_preact=True, preact_dtype=keep)
+        z64, ez, y64, ey = linear64(x, w, b, act, r, out, keep)
+        close(z, z64, ez, "preact")
+        close(y, y64, ey, "y")
+
+
+@pytest.mark.parametrize("out,keep,grad", [(BF, F32, BF), (F32, BF, F32), (F32, F32, BF)])
+@pytest.mark.parametrize("act,bias", [("silu", BF), ("swiglu", F32), ("none", None)])
+@pytest.mark.parametrize("counts,n,k,runs", [([40, 0, 60], 256, 4096, True), ([100, 300, 7], 130, 1096, True),
+                                             ([3, 0, 9], 256, 520, False), ([400, 500, 300], 1100, 136, False)])
+def test_grouped_types_and_joined_runs(counts, n, k, runs, act, bias, out, keep, grad):
+    """fp32 results, pre-activations in bf16 and dy in fp32, whole and in runs of the contraction."""
+    g = gen(6)
+    e, first, t = len(counts), 2, sum(counts) + 5
+    gated = act == "swiglu"
+    width = n // 2 if gated else n
+    w, x = normal(g, e, n, k, scale=0.05), normal(g, t, k)
+    b = None if bias is None else normal(g, e, n, dtype=bias)
+    off = torch.tensor([first] + counts).cumsum(0).to(torch.int32).to(DEV)
+    p = uz.pack_weight(w, gated=gated)
+    assert cut(p, x, offsets=off.data_ptr(), act=uz.ACTIVATIONS[act]) == runs
+    y, z = uz.grouped_linear(x, off, p, bias=b, act=act, out_dtype=out, return_preact=True, preact_dtype=keep)
+    dy = normal(g, t, width, dtype=grad)
+    dx, dw, db = uz.grouped_linear_backward(dy, x, off, p, preact=z, act=act, need_bias=True, bias_dtype=F32)
+    assert y.dtype is out and z.dtype is keep
+    at = first
+    for i, c in enumerate(counts):
+        s = slice(at, at + c)
+        at += c
+        if not c:
+            assert (dw[i] == 0).all() and (db[i] == 0).all()
+            continue
+        z64, ez, y64, ey = linear64(x[s], w[i], None if b is None else b[i], act, None, out, keep)
+        close(z[s], z64, ez, "preact")
+        close(y[s], y64, ey, "y")
+        want = backward64(dy[s], x[s], w[i], z[s], act, F32)
+        close(dx[s], *want["dx"], "dx")
+        close(dw[i], *want["dw"], "dw")
+        close(db[i], *want["dbias"], "dbias")
+    for v in (y, z, dx):
+        assert (v[:first] == 0).all() and (v[at:] == 0).all()
+
+
+@pytest.mark.parametrize("m,v,k,runs", [(100, 300, 1024, True), (33, 4097, 2048, True), (200, 129, 4096, True),
+                                        (64, 5000, 1000, True), (129, 1, 512, False)])
+def test_joined_runs_of_the_loss(m, v, k, runs):
+    """The loss's own join and that of the logit gradients: odd vocabularies, targets at both ends, masked tokens."""
+    g = gen(7)
+    x, w = normal(g, m, k), normal(g, v, k, scale=0.05)
+    t = torch.randint(0, v, (m,), generator=g).to(DEV)
+    t[0], t[1], t[2] = v - 1, 0, -100
+    p = uz.pack_weight(w)
+    a = uz.uzip_loss_args(x=x.data_ptr(), x_stride=k, tokens=m, target=t.data_ptr(), ignore_index=-100, loss=x.data_ptr(),
+                          lse=x.data_ptr())
+    tiles = 8 * m * -(-v // 128) + 4 * m + 3 * 256
+    # (more than the tokens' references, sums and picked logits, with their alignment)
+    assert (uz.uzip_linear_cross_entropy_workspace_size(p._c, a) > tiles) == runs
+    loss, lse = uz.linear_cross_entropy(x, p, t)
+    l64, s64, el, es, _, _ = loss64(x, w, t, -100)
+    close(loss, l64, el, "loss")
+    close(lse, s64, es, "lse")
+    dl = torch.randn(m, generator=g).to(DEV)
+    dx, dw = uz.linear_cross_entropy_backward(dl, x, p, t, lse)
+    wx, ww = loss_backward64(dl, x, w, t, -100)
+    close(dx, *wx, "dx")
+    close(dw, *ww, "dw")
+
+
+def test_joined_runs_of_the_loss_with_infinite_logits():
+    g = gen(8)
+    m, v, k = 70, 300, 1024
+    x, w = normal(g, m, k).abs(), normal(g, v, k).abs()
+    w[40, 3], x[1, 5] = float("inf"), float("nan")
+    t = torch.randint(0, v, (m,), generator=g).to(DEV)
+    t[0] = 40
+    loss, lse = uz.linear_cross_entropy(x, uz.pack_weight(w), t)
+    z = x.double().cpu() @ w.double().cpu().T
+    want = torch.logsumexp(z, 1)
+    assert torch.equal(torch.isnan(lse.cpu()), torch.isnan(want)) and bool((lse.cpu()[~torch.isnan(want)] == float("inf")).all())
+    lw = want - z.gather(1, t.cpu()[:, None])[:, 0]
+    assert torch.equal(torch.isnan(loss.cpu()), torch.isnan(lw))
+    w = normal(g, v, k).abs()
+    w[:, 0] = float("-inf")
+    loss, lse = uz.linear_cross_entropy(x[:2] + 0.5, uz.pack_weight(w), t[:2])
+    assert lse[0] == float("-inf") and torch.isnan(lse[1]) and torch.isnan(loss).all()
