@@ -345,3 +345,139 @@ def test_joined_runs_of_the_loss_with_infinite_logits():
     w[:, 0] = float("-inf")
     loss, lse = uz.linear_cross_entropy(x[:2] + 0.5, uz.pack_weight(w), t[:2])
     assert lse[0] == float("-inf") and torch.isnan(lse[1]) and torch.isnan(loss).all()
+
+
+# ---- the largest calls, and captured ones on other streams ----------------------------------
+
+def small(seed, *shape):
+    """-1, 0 and 1: sums of their products are exact."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=g, device=DEV, dtype=torch.int8).to(BF)
+
+
+MOST = 1 << 25  # tokens of a call
+
+
+def test_the_most_tokens_of_a_product():
+    n, k = 16, 64
+    w, x = small(1, n, k), small(2, MOST, k)
+    p = uz.pack_weight(w)
+    y = uz.linear(x, p)
+    for c in range(0, MOST, 1 << 22):
+        s = slice(c, c + (1 << 22))
+        assert torch.equal(y[s].float(), x[s].float() @ w.float().t())
+    at = torch.tensor([0, 1, 255, 256, MOST // 2 + 77, MOST - 257, MOST - 1], device=DEV)
+    dy = torch.zeros(MOST, n, dtype=BF, device=DEV)
+    dy[at] = small(3, at.numel(), n)
+    dx, dw, db = uz.linear_backward(dy, x, p, need_bias=True, bias_dtype=F32)
+    assert torch.equal(dx[at].float(), dy[at].float() @ w.float())
+    dx[at] = 0
+    assert not bool(dx.any())
+    assert torch.equal(dw.float(), dy[at].float().t() @ x[at].float()) and torch.equal(db, dy[at].float().sum(0))
+
+
+def test_the_most_tokens_of_a_loss():
+    """Logits are exact.  A sum of 16 exponentials good to 2^-20, its logarithm and lse each rounded once, below 2^7."""
+    v, k = 16, 64
+    w, x = small(4, v, k), small(5, MOST, k)
+    t = torch.arange(MOST, device=DEV) % (v + 1) - 1  # (every 17th target is no row of w)
+    p = uz.pack_weight(w)
+    loss, lse = uz.linear_cross_entropy(x, p, t, ignore_index=-1)
+    bound = 16 * STEP + 2.0 ** -20 + 2 * 2.0 ** 7 * STEP
+    for c in range(0, MOST, 1 << 22):
+        s = slice(c, c + (1 << 22))
+        z = (x[s].float() @ w.float().t()).double()
+        want = torch.logsumexp(z, 1)
+        assert float((lse[s].double() - want).abs().max()) < bound
+        picked = z.gather(1, t[s].clamp(min=0)[:, None])[:, 0]
+        off = (loss[s].double() - torch.where(t[s] < 0, 0.0, want - picked)).abs()
+        assert float(off.max()) < bound + 2.0 ** 7 * STEP
+    at = torch.tensor([1, 300, MOST // 2 + 78, MOST - 1], device=DEV)
+    assert bool((t[at] >= 0).all())
+    g = torch.zeros(MOST, device=DEV)
+    g[at] = 1.0
+    dx, dw = uz.linear_cross_entropy_backward(g, x, p, t, lse, ignore_index=-1)
+    wx, ww = loss_backward64(g[at], x[at], w, t[at], -1)
+    close(dx[at], *wx, "dx")
+    close(dw, *ww, "dw")
+    dx[at] = 0
+    assert not bool(dx.any())
+
+
+def test_the_most_matrices_of_a_stack():
+    e, n, k = 65535, 16, 64
+    w = small(6, e, n, k)
+    p = uz.pack_weight(w)
+    assert torch.equal(uz.unpack_weight(p), w)
+    for rows in ({0: 3, 777: 1, 65534: 5}, {0: 30, 64: 700, 40000: 1, 65533: 2, 65534: 300}):
+        counts = torch.zeros(e, dtype=torch.int64)
+        for i, c in rows.items():
+            counts[i] = c
+        off = torch.cat((torch.tensor([2]), 2 + counts.cumsum(0))).to(torch.int32).to(DEV)
+        t = int(off[-1]) + 3
+        x, dy = small(7, t, k), small(8, t, n)
+        of = torch.repeat_interleave(torch.arange(e), counts).to(DEV)
+        y = uz.grouped_linear(x, off, p)
+        dx, dw, db = uz.grouped_linear_backward(dy, x, off, p, need_bias=True, bias_dtype=F32)
+        s = slice(2, t - 3)
+        assert torch.equal(y[s].float(), (w[of].float() @ x[s].float()[:, :, None])[:, :, 0])
+        assert torch.equal(dx[s].float(), (dy[s].float()[:, None] @ w[of].float())[:, 0])
+        for i in rows:
+            r = s.start + int(counts[:i].sum())
+            r = slice(r, r + rows[i])
+            assert torch.equal(dw[i].float(), (dy[r].float().t() @ x[r].float()).to(BF).float())
+            assert torch.equal(db[i], dy[r].float().sum(0))
+        hit = torch.tensor(sorted(rows), device=DEV)
+        dw[hit], db[hit] = 0, 0
+        assert not bool(dw.any()) and not bool(db.any())
+        for v in (y, dx):
+            assert not bool(v[:2].any()) and not bool(v[t - 3:].any())
+
+
+def test_captured_on_another_stream_and_from_packing_on():
+    """Packing without a wait, products on a second stream of the capture, their memory the graph's; replayed with new
+    values between eager calls."""
+    g = gen(9)
+    m, n, k = 100, 256, 4096
+    wt, x, dy = normal(g, n, k, scale=0.02), normal(g, m, k), normal(g, m, n)
+    t, dl = torch.randint(0, n, (m,), generator=g).to(DEV), torch.ones(m, device=DEV)
+    off = torch.tensor([60, 90, 10, 40], dtype=torch.int32, device=DEV)
+    stack = normal(g, 3, n, k, scale=0.02)
+    side = torch.cuda.Stream()
+
+    def calls(stream):
+        main = torch.cuda.current_stream()
+        kw = {}
+        if stream is not None:
+            stream.wait_stream(main)
+            kw["stream"] = stream
+        w, ws = uz.pack_weight(wt, trim=False, **kw), uz.pack_weight(stack, trim=False, **kw)
+        y, z = uz.linear(x, w, act="gelu", return_preact=True, **kw)
+        dx, dw, db = uz.linear_backward(dy, x, w, preact=z, act="gelu", need_bias=True, **kw)
+        gy, gz = uz.grouped_linear(x, off, ws, act="silu", return_preact=True, **kw)
+        gdx, gdw, _ = uz.grouped_linear_backward(dy, x, off, ws, preact=gz, act="silu", **kw)
+        loss, lse = uz.linear_cross_entropy(x, w, t, **kw)
+        lx, lw = uz.linear_cross_entropy_backward(dl, x, w, t, lse, **kw)
+        back = uz.unpack_weight(w, **kw)
+        if stream is not None:
+            main.wait_stream(stream)
+        return [y, z, dx, dw, db, gy, gz, gdx, gdw, loss, lse, lx, lw, back]
+
+    calls(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = calls(side)
+    for i in range(4):
+        for v, s in ((wt, 0.02), (x, 1.0), (dy, 1.0), (stack, 0.02)):
+            v.copy_(normal(g, *v.shape, scale=s))
+        want = [o.clone() for o in calls(None)]
+        graph.replay()
+        if i & 1:
+            torch.cuda.synchronize()
+        eager = calls(side)
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, outs, eager):
+            for o in (b, c):
+                assert torch.equal(a.reshape(-1).view(torch.uint8), o.reshape(-1).view(torch.uint8))
