@@ -620,16 +620,18 @@ constexpr uint32_t kNowhere = 0xFFFFFF00u;  // an offset that is behind every bu
 // before the first and behind the last.  A descending pair is an empty group, and the
 // groups around it may lie anywhere: then each row is looked for in all of
 // them.  Rows of a group are other workgroups' results and never touched here.
-// A call, since inlined it takes registers from the products' main loops.
+// A call, since inlined it takes registers from the products' main loops.  At
+// most 1,024 bytes a row, a lane for each 16.
 __device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups, uint32_t tokens, void *out, uint64_t stride,
                                   uint32_t elem, uint32_t c0, uint32_t c1, uint32_t threads) {
-    const uint32_t lane = threadIdx.x & 63, wide = c1 - c0;
-    auto clear = [&](uint32_t row, uint32_t c) {
-        const uint64_t at = (uint64_t)row * stride + c0 + c;
-        if (elem == 4)
-            static_cast<uint32_t *>(out)[at] = 0;
-        else
-            static_cast<uint16_t *>(out)[at] = 0;
+    const uint32_t lane = threadIdx.x & 63, wide = c1 - c0, each = 16 / elem, units = (wide + each - 1) / each;
+    auto clear = [&](uint32_t row, uint32_t u) {  // 16 bytes, at any value's address
+        uint8_t *const at = static_cast<uint8_t *>(out) + ((uint64_t)row * stride + c0 + u * each) * elem;
+        if ((u + 1) * each <= wide) {
+            *reinterpret_cast<u32x4_any *>(at) = u32x4{0, 0, 0, 0};
+            return;
+        }
+        for (uint32_t b = 0; b < (wide - u * each) * elem; b += 2) *reinterpret_cast<uint16_t *>(at + b) = 0;
     };
     auto clamped = [&](uint32_t i) { return (uint32_t)min(max(offsets[i], 0), (int32_t)tokens); };
     const uint32_t first = clamped(0), last = clamped(groups);
@@ -637,11 +639,11 @@ __device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups,
 #pragma unroll 1
     for (uint32_t g = lane; g < groups; g += 64) down |= clamped(g + 1) < clamped(g);
     if (!__any(down)) {
-        const uint32_t rest = first + (tokens - last);
-        for (uint64_t i = threadIdx.x; i < (uint64_t)rest * wide; i += threads) {
-            const uint32_t r = (uint32_t)(i / wide);
-            clear(r < first ? r : last + (r - first), (uint32_t)(i % wide));
-        }
+        uint32_t per = 1;  // lanes a row
+        while (per < units) per *= 2;
+        const uint32_t rest = first + (tokens - last), u = threadIdx.x & (per - 1);
+        if (u < units)
+            for (uint32_t i = threadIdx.x / per; i < rest; i += threads / per) clear(i < first ? i : last + (i - first), u);
         return;
     }
     for (uint32_t row = threadIdx.x >> 6; row < tokens; row += threads / 64) {  // a wave a row
@@ -650,7 +652,7 @@ __device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups,
         for (uint32_t g = lane; g < groups; g += 64) held |= row >= clamped(g) && row < clamped(g + 1);
         if (__any(held)) continue;
 #pragma unroll 1
-        for (uint32_t c = lane; c < wide; c += 64) clear(row, c);
+        for (uint32_t u = lane; u < units; u += 64) clear(row, u);
     }
 }
 
