@@ -1892,26 +1892,27 @@ bool skinny_fits(uint64_t tokens, uint64_t groups, uint64_t col_blocks) {
     return tokens <= 24 || (tokens <= 64 && tokens * col_blocks <= 2048);
 }
 
-// Waves and row blocks of a workgroup: with rows enough to fill the chip, few
-// waves that share their reads of x (4096 x 4096 over 13 experts: 62 us, 5.3
-// TB/s, against 84 us with one row block and 16 waves; 32 rows, 28672 x 4096
-// gated: 42 against 57 us); with fewer rows, many waves, for the bytes in
-// flight (one 4096 x 4096 matrix, one row: 8.3 against 12.0 us; 64 rows: 20
-// against 26 us).
+// Waves and row blocks of a workgroup.  While each CU has at most one row block,
+// many waves on it, for the bytes in flight (4096 x 4096, 256 blocks, one row: 5.8
+// us against 8.7 with few waves; 64 rows: 18.6 against 23.5).  From there on few waves
+// that share their reads of x: a second round of many costs more (5120 x 4096, 320
+// blocks, 16 rows: 9.9 us against 14.1, 32 rows: 12.9 against 19.7; 8192 x 4096, 64
+// rows: 24 against 34; 4096 x 4096 over 13 experts: 61, 5.3 TB/s, against 80).  Gated:
+// two row blocks, each with its up rows, and four waves where x's reads weigh
+// (24576 x 4096, 768 blocks: 16 rows 25.7 us with one block and eight waves, 26.9 so,
+// 32 rows 32.7 and 29.0; 896 blocks, 16 rows: 31.5 and 29.1; 256 blocks, 64 rows: 20.8
+// and 26.6, 384 blocks: 38.5 and 27.1).
 hipError_t launch_skinny(const SkinnyParams &p, hipStream_t s) {
     const uint32_t rows = p.groups > 1 ? 16 : p.tokens;
     const uint64_t blocks = (uint64_t)p.w.part_blocks * p.groups;
     if (p.lin.act == kActSwiglu) {
-        if (blocks < 512) {
-            if (rows <= 16) return skinny<1, 2, true, 8>(p, s);
-            return rows <= 32 ? skinny<2, 2, true, 8>(p, s) : skinny<4, 2, true, 8>(p, s);
-        }
-        if (rows <= 16) return skinny<1, 4, true, 4>(p, s);
-        return rows <= 32 ? skinny<2, 4, true, 4>(p, s) : skinny<4, 4, true, 4>(p, s);
+        if (rows <= 16) return blocks <= 768 ? skinny<1, 2, true, 8>(p, s) : skinny<1, 4, true, 4>(p, s);
+        if (rows <= 32) return blocks <= 256 ? skinny<2, 2, true, 8>(p, s) : skinny<2, 4, true, 4>(p, s);
+        return blocks <= 256 ? skinny<4, 2, true, 8>(p, s) : skinny<4, 4, true, 4>(p, s);
     }
-    if (rows <= 16) return blocks >= 1024 ? skinny<1, 2, false, 8>(p, s) : skinny<1, 1, false, 16>(p, s);
-    if (rows <= 32) return blocks >= 768 ? skinny<2, 2, false, 8>(p, s) : skinny<2, 1, false, 8>(p, s);
-    return blocks >= 768 ? skinny<4, 4, false, 8>(p, s) : skinny<4, 1, false, 8>(p, s);
+    if (rows <= 16) return blocks <= 256 ? skinny<1, 1, false, 16>(p, s) : skinny<1, 2, false, 8>(p, s);
+    if (rows <= 32) return blocks <= 256 ? skinny<2, 1, false, 8>(p, s) : skinny<2, 2, false, 8>(p, s);
+    return blocks <= 256 ? skinny<4, 1, false, 8>(p, s) : skinny<4, 4, false, 8>(p, s);
 }
 
 GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups) {

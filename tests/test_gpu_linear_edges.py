@@ -347,6 +347,40 @@ def test_joined_runs_of_the_loss_with_infinite_logits():
     assert lse[0] == float("-inf") and torch.isnan(lse[1]) and torch.isnan(loss).all()
 
 
+# ---- every shape of workgroup of the product for few rows ---------------------------------
+
+@pytest.mark.parametrize("m", [1, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("n,k,act", [(4096, 200, "none"), (4097, 72, "silu"), (8192, 136, "swiglu"), (8194, 65, "swiglu"),
+                                     (24576, 64, "swiglu"), (24578, 72, "swiglu")])
+def test_few_rows_on_both_sides_of_each_rule(m, n, k, act):
+    """256 and 257 row blocks; gated 256, 257, 768 and 769 of each half."""
+    g = gen(10)
+    gated = act == "swiglu"
+    x, w, b = normal(g, m, k), normal(g, n, k, scale=0.05), normal(g, n)
+    r = normal(g, m, n // 2 if gated else n)
+    y, z = uz.linear(x, uz.pack_weight(w, gated=gated), bias=b, act=act, residual=r, return_preact=True)
+    z64, ez, y64, ey = linear64(x, w, b, act, r, BF)
+    close(z, z64, ez, "preact")
+    close(y, y64, ey, "y")
+
+
+@pytest.mark.parametrize("counts", [[16, 0, 3, 13], [40, 0, 0, 24]])
+@pytest.mark.parametrize("n,act", [(1024, "silu"), (1040, "silu"), (6144, "swiglu"), (6176, "swiglu")])
+def test_few_grouped_rows_on_both_sides_of_each_rule(counts, n, act):
+    g = gen(11)
+    k, e, t = 136, len(counts), sum(counts)
+    gated = act == "swiglu"
+    x, w = normal(g, t, k), normal(g, e, n, k, scale=0.05)
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32).to(DEV)
+    y = uz.grouped_linear(x, off, uz.pack_weight(w, gated=gated), act=act)
+    at = 0
+    for i, c in enumerate(counts):
+        if c:
+            _, _, y64, ey = linear64(x[at:at + c], w[i], None, act, None, BF)
+            close(y[at:at + c], y64, ey, "y of group %d" % i)
+        at += c
+
+
 # ---- the largest calls, and captured ones on other streams ----------------------------------
 
 def small(seed, *shape):
