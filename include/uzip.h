@@ -449,8 +449,8 @@ uzip_status uzip_grouped_linear_backward(const uzip_weight *weight, const uzip_l
  * loss is lse - logit[target] with lse = log(sum(exp(logits))).  target:
  * int64 [tokens]; a token whose target is ignore_index has loss 0 and no
  * gradient; one whose target is neither that nor a row of W has loss NaN and
- * no gradient.  Without a gradient: dx's row is 0, and dw does not see the
- * token's row of x, which may hold anything.  loss and lse: fp32 [tokens].
+ * no gradient.  Without a gradient: dx's row is 0 (if W is finite), and dw does
+ * not see the token's row of x, which may hold anything.  loss and lse: fp32 [tokens].
  * One matrix, not gated. */
 typedef struct {
     const void *x;

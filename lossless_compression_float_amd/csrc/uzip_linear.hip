@@ -376,7 +376,7 @@ __global__ __launch_bounds__(256) void k_pack_extra(PackParams p) {
 }
 
 // A wave decodes a tile and writes its rows.  Bound by memory: 28672 x 4096 in
-// 65 us, 411 MB read and written (part of it from the last-level cache).
+// 67 us, 411 MB read and written (part of it from the last-level cache).
 __global__ __launch_bounds__(256) void k_unpack(UnpackParams p) {
     const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint64_t tile = (uint64_t)blockIdx.x * 4 + wave;
@@ -419,7 +419,7 @@ __device__ inline u32x4 stage_unit(const uint16_t *row, uint64_t c, uint64_t col
 
 // Rows copied to a stride of whole 16-byte units, zeros behind the last column:
 // the tiled products read x 16 bytes at a time, and what lies behind a row must
-// not meet the zeros of a packed weight as a NaN.  1999 x 2050 in 6.2 us, 2.6
+// not meet the zeros of a packed weight as a NaN.  1999 x 2050 in 6.5 us, 2.5
 // TB/s: latency and the launch.
 __global__ __launch_bounds__(256) void k_stage(const uint16_t *in, uint64_t in_stride, uint16_t *out, uint64_t out_stride,
                                                uint64_t rows, uint64_t cols) {
@@ -622,8 +622,8 @@ constexpr uint32_t kNowhere = 0xFFFFFF00u;  // an offset that is behind every bu
 // them.  Rows of a group are other workgroups' results and never touched here.
 // A call, since inlined it takes registers from the products' main loops.  At
 // most 1,024 bytes a row, a lane for each 16.
-__device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups, uint32_t tokens, void *out, uint64_t stride,
-                                  uint32_t elem, uint32_t c0, uint32_t c1, uint32_t threads) {
+__device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups, uint32_t tokens, void *out,
+                                        uint64_t stride, uint32_t elem, uint32_t c0, uint32_t c1, uint32_t threads) {
     const uint32_t lane = threadIdx.x & 63, wide = c1 - c0, each = 16 / elem, units = (wide + each - 1) / each;
     auto clear = [&](uint32_t row, uint32_t u) {  // 16 bytes, at any value's address
         uint8_t *const at = static_cast<uint8_t *>(out) + ((uint64_t)row * stride + c0 + u * each) * elem;
@@ -669,13 +669,13 @@ __device__ inline void clear_rest_linear(const P &p, uint32_t c0, uint32_t c1, u
 // ---- few rows ---------------------------------------------------------------------
 
 // y = W x for up to 16 MT rows of x at a time.  Bound by the reads of W: 28672
-// x 4096 gated, 16 rows, 35 us, 5.1 TB/s of packed bytes, as fast as a large
-// copy.  A workgroup owns RB row blocks of W; its NW waves split K and add their
+// x 4096 gated, 16 rows, 37 us from memory, 4.9 TB/s of packed bytes, about as fast as
+// a large copy (29.5 us when half of them are in the last-level cache).  A workgroup owns RB row blocks of W; its NW waves split K and add their
 // parts in LDS in a fixed order.  The weights go from memory to the matrix
 // instructions without touching LDS; a wave has one column block on its way and
 // the bytes in flight come from the number of waves (blocks loaded two or four
 // ahead took more registers, so fewer waves, and were slower: one row of 4096 x
-// 4096 9.1 and 12.2 us against 8.3).  Headers: lane l of `heads` holds that of
+// 4096 in 1.1 and 1.5 times the time, which is 5.8 us now, 8.4 with weights from memory).  Headers: lane l of `heads` holds that of
 // the wave's l-th block.  What lies behind the last block, row or column is read
 // as zeros.
 template <int MT, int RB, bool GATED, int NW>
@@ -805,9 +805,9 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
 // its share of the weights of the stages after next; one barrier ends the step.
 // Two waves a SIMD: a wave alone issues an instruction every four cycles, and a
 // step has too many of them for the matrix instructions' time.  256 x 256: 8192
-// x 4096 x 14336 in 960 us, 1000 TFLOP/s; dx 1040, dw (nothing to decode) 1340,
-// the loss's logits 1070, their gradient 1000; a large library product reaches
-// 1310 here.  Forward and dx are bound by the instructions of the decoder, which
+// x 4096 x 14336 in 880 to 970 us, 990 to 1090 TFLOP/s as the clock allows; dx 1000, dw
+// (nothing to decode) 1270 to 1320, the loss's logits 1040, their gradient 1000; a large
+// library product reaches 1310 here.  Forward and dx are bound by the instructions of the decoder, which
 // share the SIMD with the matrix instructions' issue and its power.
 //
 // With 64 or 128 columns a tile (and packed rows) the traffic of LDS and a
@@ -815,9 +815,9 @@ __global__ __launch_bounds__(NW * 64) void k_skinny(SkinnyParams p) {
 // two row blocks and all columns, so that its weights go from memory through
 // the decoder to the matrix instructions in registers, and only the tokens'
 // values go through LDS.  128 x 128: two times four waves, each half of the
-// contraction, added up at the end (1024 x 4096 x 4096 in 51 us; with one wave a
+// contraction, added up at the end (1024 x 4096 x 4096 in 49 us; with one wave a
 // SIMD 67 where this took 55, decoded tiles through the ring 70); 256 x 64: eight
-// waves (128256 x 4096, 64 tokens: 148 us, 5.3 TB/s of packed bytes; through the
+// waves (128256 x 4096, 64 tokens: 151 us, 5.3 TB/s of packed bytes; through the
 // ring 212).
 
 enum Operand { kPacked, kPackedT, kRows, kCols };
@@ -1702,7 +1702,7 @@ __global__ __launch_bounds__(64) void k_loss_join(LossEpi e, float *loss, float 
 }
 
 // What the gradients need first, in one launch.  Workgroup 0: the largest dloss
-// (5 us for 4096 tokens).  The others, if `out` is given: x in rows of whole 16-byte
+// (5 us for 4096 tokens; with the copy of 4096 x 4096 the launch takes 12).  The others, if `out` is given: x in rows of whole 16-byte
 // units, with zeros for the tokens that do not count: their dlogits are 0, but in
 // dw 0 times an infinity or a NaN, as the rows of padding may hold, would not be.
 __global__ __launch_bounds__(1024) void k_loss_begin(LossEpi e, float *unit, uint32_t tokens, uint64_t vocab,
@@ -1883,10 +1883,14 @@ hipError_t launch_stage(const uint16_t *in, uint64_t in_stride, uint16_t *out, u
 
 // Rows of x for which the skinny product is faster than the tiled one: it
 // reads all of x once a workgroup, so that the width of x counts.  Skinny and
-// tiled in us: 4096 x 4096 with 32 rows 11 and 17, with 64 rows 19 and 17;
-// 4096 x 14336 with 17 rows 23 and 27, with 32 rows 31 and 27; 2048 x 2048 with
-// 48 rows 9 and 11; 8 experts of 4096 x 4096 with 16 rows each 34 and 59, with
-// 20 rows (two rounds of 16) 60 and 59, with 48 rows 92 and 61.
+// tiled in us: 4096 x 4096 with 32 rows 11 and 16, with 48 rows 16 and 16, with 64 rows
+// 19 and 16; 4096 x 14336 with 17 rows 23 and 25, with 24 rows 27 and 25, with 32 rows
+// 31 and 26; 2048 x 2048 with 48 rows 9 and 11; only for much wider results does the
+// tiled one gain before that (28672 x 4096 with 32 rows 42 and 35).  8 experts of 4096 x
+// 4096 with 16 rows each 34 and 53, with 20 rows (two rounds of 16) 59 and 53, with 48
+// rows 91 and 55.  The host knows only the experts' mean, not the offsets: 128
+// experts of 2048 x 2048 with 15 rows each take 164 and 166, but 1,939 rows by a power
+// law 274 and 171, and 2,000 rows all to one 561 and 144.
 bool skinny_fits(uint64_t tokens, uint64_t groups, uint64_t col_blocks) {
     if (groups > 1) return tokens <= 16 * groups;
     return tokens <= 24 || (tokens <= 64 && tokens * col_blocks <= 2048);
@@ -1925,8 +1929,9 @@ GemmTile gemm_tile(GemmKind kind, uint64_t r, uint64_t c, uint64_t groups) {
 // that fit the chip, each run shortens the walk of `steps` blocks of 64 and
 // adds its part of the sums, written and read once at about 4 TB/s, and one
 // launch.  A block takes 0.6 us with tiles of 128 x 128, 0.8 with 256 x 64, one
-// workgroup a CU (more do not fit: 128 x 4096 x 4096 20 us in 8 runs, 44 whole,
-// 32 in 16); dx 0.9 us where a CU has one workgroup, 1.4 where it has two.
+// workgroup a CU (more do not fit: 128 x 4096 x 4096 20 us in 8 runs, 39 whole,
+// 31 in 16); dx 0.9 us where a CU has one workgroup, 1.4 where it has two (the same
+// size: 22 us in 8 runs, 77 whole, 31 in 16; 300 rows 47 in 2, 78 whole, 50 in 4 or 8).
 uint32_t gemm_splits(GemmKind kind, GemmTile tile, uint64_t r_tiles, uint64_t c_tiles, uint64_t steps) {
     const uint64_t tiles = r_tiles * c_tiles, most = kind == kGemmDx ? 512 : 256;
     if (tiles == 0 || tiles > 256) return 1;
