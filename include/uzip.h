@@ -400,7 +400,8 @@ typedef struct {
     uint32_t reserved;   /* 0 */
 } uzip_linear_args;
 
-/* The workspace depends on sizes, strides, pointers' alignment and types only.
+/* The workspace depends on sizes, strides, pointers' alignment, types and the
+ * results asked for only.
  * 0: the call needs none (d_workspace may be null), or its arguments are
  * invalid, which the call itself reports. */
 size_t uzip_linear_workspace_size(const uzip_weight *weight, const uzip_linear_args *args);

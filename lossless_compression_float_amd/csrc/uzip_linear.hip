@@ -618,8 +618,9 @@ constexpr uint32_t kNowhere = 0xFFFFFF00u;  // an offset that is behind every bu
 // Zeros in columns [c0, c1) of the rows that no group holds (all of a
 // workgroup's threads together).  Where the offsets ascend these are the rows
 // before the first and behind the last.  A descending pair is an empty group, and the
-// groups around it may lie anywhere: then each row is looked for in all of
-// them.  Rows of a group are other workgroups' results and never touched here.
+// groups around it may lie anywhere: then a run of such rows begins at 0 or at a group's
+// end and goes to the next group's begin.  Rows of a group are other workgroups'
+// results and never touched here.
 // A call, since inlined it takes registers from the products' main loops.  At
 // most 1,024 bytes a row, a lane for each 16.
 __device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups, uint32_t tokens, void *out,
@@ -638,21 +639,32 @@ __device__ __noinline__ void clear_rest(const int32_t *offsets, uint32_t groups,
     bool down = false;
 #pragma unroll 1
     for (uint32_t g = lane; g < groups; g += 64) down |= clamped(g + 1) < clamped(g);
+    uint32_t per = 1;  // lanes a row
+    while (per < units) per *= 2;
     if (!__any(down)) {
-        uint32_t per = 1;  // lanes a row
-        while (per < units) per *= 2;
         const uint32_t rest = first + (tokens - last), u = threadIdx.x & (per - 1);
         if (u < units)
             for (uint32_t i = threadIdx.x / per; i < rest; i += threads / per) clear(i < first ? i : last + (i - first), u);
         return;
     }
-    for (uint32_t row = threadIdx.x >> 6; row < tokens; row += threads / 64) {  // a wave a row
+    for (uint32_t i = threadIdx.x >> 6; i <= groups; i += threads / 64) {  // a wave a group's end; row 0 behind the last
+        uint32_t end = 0;
+        if (i < groups) {
+            end = clamped(i + 1);
+            if (end <= clamped(i)) continue;
+        }
         bool held = false;
+        uint32_t next = tokens;  // where the next group begins
 #pragma unroll 1
-        for (uint32_t g = lane; g < groups; g += 64) held |= row >= clamped(g) && row < clamped(g + 1);
+        for (uint32_t g = lane; g < groups; g += 64) {
+            const uint32_t b = clamped(g), e = clamped(g + 1);
+            held |= b <= end && end < e;
+            if (b < e && b >= end) next = min(next, b);
+        }
         if (__any(held)) continue;
-#pragma unroll 1
-        for (uint32_t u = lane; u < units; u += 64) clear(row, u);
+        for (int d = 1; d < 64; d <<= 1) next = min(next, (uint32_t)__shfl_xor((int)next, d));
+        if (const uint32_t u = lane & (per - 1); u < units)
+            for (uint32_t row = end + lane / per; row < next; row += 64 / per) clear(row, u);
     }
 }
 

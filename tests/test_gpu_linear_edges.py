@@ -66,6 +66,37 @@ def test_groups_out_of_order_keep_their_rows(name, n, k, act, out):
         assert (y[rest] == 0).all() and (dx[rest] == 0).all()
 
 
+@pytest.mark.parametrize("n,k,rows", [(40, 64, 9), (300, 136, 40)])
+def test_many_groups_in_descending_order(n, k, rows):
+    """A hundred groups from the last rows to the first, every third right below the one before, the others with gaps."""
+    g = gen(12)
+    offsets, at = [], 110 * rows
+    for i in range(100):
+        begin = at - 1 - int(torch.randint(0, rows, (1,), generator=g))
+        offsets += [begin, at]
+        at = begin if i % 3 == 0 else begin - int(torch.randint(0, 4, (1,), generator=g))
+    t, e = 110 * rows + 3, len(offsets) - 1
+    assert offsets[-2] >= 0
+    x, w = normal(g, t, k), normal(g, e, n, k, scale=0.1)
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    p = uz.pack_weight(w)
+    junk = [torch.full((t, c), float("nan"), device=DEV) for c in (n, n, k)]
+    torch.cuda.synchronize()
+    del junk
+    y, z = uz.grouped_linear(x, off, p, act="relu", return_preact=True)
+    dx, _, _ = uz.grouped_linear_backward(y, x, off, p, preact=z, act="relu", need_weight=False)
+    rest = torch.ones(t, dtype=torch.bool, device=DEV)
+    for i in range(0, e, 2):
+        s = slice(offsets[i], offsets[i + 1])
+        rest[s] = False
+        z64, ez, y64, ey = linear64(x[s], w[i], None, "relu", None, BF)
+        close(z[s], z64, ez, "preact of group %d" % i)
+        close(y[s], y64, ey, "y of group %d" % i)
+        close(dx[s], *backward64(y[s], x[s], w[i], z[s], "relu", BF)["dx"], "dx of group %d" % i)
+    for v in (y, z, dx):
+        assert (v[rest] == 0).all()
+
+
 @pytest.mark.parametrize("keep", [F32, BF])
 @pytest.mark.parametrize("own_out", [False, True])
 @pytest.mark.parametrize("offsets,t", [([3, 5, 5, 9], 20), ([100, 180, 181, 400], 450), ([0, 0, 0, 0], 40), ([7, 9, 2, 6], 12)])
