@@ -477,6 +477,86 @@ size_t uzip_linear_cross_entropy_backward_workspace_size(const uzip_weight *weig
 uzip_status uzip_linear_cross_entropy_backward(const uzip_weight *weight, const uzip_loss_args *args,
                                                void *d_workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- experts ---------------------------------------------------------------
+ * A mixture of experts around the products above: the router turns logits into
+ * experts, weights and rows grouped by expert, as uzip_grouped_linear takes
+ * them; uzip_moe is the whole layer.  Conventions as above.  Limits: 1,024
+ * experts, 64 of them a token, 2^25 pairs of token and expert. */
+typedef enum {
+    UZIP_SCORES_SOFTMAX = 0, /* of all of a token's logits */
+    UZIP_SCORES_SIGMOID = 1
+} uzip_scores;
+
+/* Per token the k best experts, best first, of equal ones the lowest, and
+ * their weights: scale times the score, with renormalize over the chosen
+ * scores' sum.  bias (sigmoid only): added to the scores for the choice, not
+ * for the weights.  An expert whose logit is -inf is never chosen; a place for
+ * which none is left holds expert -1 and weight 0.  A NaN is not chosen
+ * either, and makes the token's weights NaN.  An infinite logit gives the
+ * limit.
+ * order: the pairs token * k + place, grouped by expert, ascending within;
+ * offsets: where each expert's begin (pairs of no expert are behind the last).
+ * logits null: experts and weights are given and only grouped; there an expert
+ * outside [0, num_experts) becomes -1 with weight 0, and one that a token
+ * names again too, its weight added to the first.
+ * Backward: dlogits from dweights, the choice held fixed, with the experts of
+ * the forward call. */
+typedef struct {
+    const void *logits;     /* [tokens, num_experts] bf16 or fp32 */
+    size_t logits_stride;
+    size_t tokens;
+    const float *bias;      /* [num_experts], or null */
+    int32_t *experts;       /* [tokens, k] */
+    float *weights;         /* [tokens, k] */
+    int32_t *order;         /* [tokens * k] */
+    int32_t *offsets;       /* [num_experts + 1] */
+    const float *dweights;  /* backward: [tokens, k] */
+    void *dlogits;          /* backward: the logits' shape and type */
+    size_t dlogits_stride;
+    uint32_t num_experts;
+    uint32_t k;
+    uint32_t logits_dtype;
+    uint32_t scores;        /* uzip_scores */
+    uint32_t renormalize;   /* 0 or 1 */
+    float scale;
+} uzip_moe_route_args;
+
+size_t uzip_moe_route_workspace_size(const uzip_moe_route_args *args);
+uzip_status uzip_moe_route(const uzip_moe_route_args *args, void *d_workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+/* Needs no workspace. */
+uzip_status uzip_moe_route_backward(const uzip_moe_route_args *args, hipStream_t stream);
+
+/* y_t = sum over j of weights[t, j] (D_e act(U_e x_t + up_bias_e) + down_bias_e),
+ * e = experts[t, j], + residual_t.  up: a packed stack of U, gated for
+ * UZIP_ACT_SWIGLU; down: one of D with as many columns as up has outputs.
+ * x: [tokens, up cols] bf16; y, residual: [tokens, down rows] bf16 or fp32.
+ * weights, order and offsets are uzip_moe_route's.  The activations between
+ * the products are rounded to bf16.  Entries of order and offsets out of
+ * range are left out.  y may be the residual itself. */
+typedef struct {
+    const void *x;
+    size_t x_stride;
+    size_t tokens;
+    const float *weights;
+    const int32_t *order;
+    const int32_t *offsets;
+    const void *up_bias;    /* [matrices, up rows], or null */
+    const void *down_bias;  /* [matrices, down rows], or null */
+    const void *residual;   /* or null */
+    size_t residual_stride;
+    void *y;
+    size_t y_stride;
+    uint32_t k;
+    uint32_t act;           /* uzip_act */
+    uint32_t bias_dtype;    /* of both biases */
+    uint32_t y_dtype;
+} uzip_moe_args;
+
+size_t uzip_moe_workspace_size(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *args);
+uzip_status uzip_moe(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *args, void *d_workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+
 /* Static English name of a status code. */
 const char *uzip_status_string(uzip_status s);
 

@@ -85,6 +85,11 @@ EXPORTED = (
     "uzip_linear_cross_entropy",
     "uzip_linear_cross_entropy_backward_workspace_size",
     "uzip_linear_cross_entropy_backward",
+    "uzip_moe_route_workspace_size",
+    "uzip_moe_route",
+    "uzip_moe_route_backward",
+    "uzip_moe_workspace_size",
+    "uzip_moe",
 )
 
 _lib = None
@@ -493,3 +498,7 @@ from .weights import (ACTIVATIONS, PackedWeight, grouped_linear, grouped_linear_
                       uzip_linear_cross_entropy_backward_workspace_size, uzip_linear_cross_entropy_workspace_size,
                       uzip_linear_workspace_size, uzip_loss_args, uzip_weight, uzip_weight_max_size, uzip_weight_pack,
                       uzip_weight_unpack, uzip_weight_workspace_size)
+# ---- experts --------------------------------------------------------------------
+from .experts import (Routing, moe, moe_group, moe_route, moe_route_backward, uzip_moe, uzip_moe_args,  # noqa: E402
+                  uzip_moe_route, uzip_moe_route_args, uzip_moe_route_backward, uzip_moe_route_workspace_size,
+                  uzip_moe_workspace_size)

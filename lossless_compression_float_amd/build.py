@@ -9,7 +9,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libuzip.so")
-SOURCES = ["uzip_kernels.hip", "uzip_api.cpp", "uzip_linear.hip", "uzip_linear_api.cpp"]
+SOURCES = ["uzip_kernels.hip", "uzip_api.cpp", "uzip_linear.hip", "uzip_linear_api.cpp", "uzip_moe.hip",
+           "uzip_moe_api.cpp"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -1,0 +1,70 @@
+// uzip_moe.hpp -- kernel parameter blocks and launchers of the router and the
+// expert layer (internal).
+#pragma once
+
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+#include "uzip_linear.hpp"
+
+namespace uzip {
+
+constexpr uint32_t kMaxExperts = 1024;  // a wave holds a token's scores, 16 a lane
+constexpr uint32_t kMaxChosen = 64;     // and its choice, one a lane
+constexpr uint32_t kRouteChunks = 256;
+
+struct RouteParams {
+    const void *logits;  // null: experts and weights are given, and only grouped
+    uint64_t stride;
+    const float *bias;
+    int32_t *experts;
+    float *weights;
+    int32_t *order, *offsets;
+    int32_t *counts;  // [chunks][num + 1]: pairs of each expert, then those of none
+    float scale;
+    uint32_t tokens, num, k, f32, sigmoid, renorm;
+    uint32_t chunk, chunks;  // tokens of a workgroup
+};
+
+struct RouteBackwardParams {
+    const void *logits;
+    uint64_t stride;
+    const int32_t *experts;
+    const float *dweights;
+    void *dlogits;
+    uint64_t d_stride;
+    float scale;
+    uint32_t tokens, num, k, f32, sigmoid, renorm;
+};
+
+// The layer with rows gathered by expert.
+struct GatherParams {
+    Mat x;
+    uint16_t *out;         // [pairs][out_stride]
+    uint64_t out_stride;
+    uint32_t cols, tokens, k;
+    const int32_t *order, *ends;  // ends: one past the last pair that has an expert
+    uint32_t *place;       // of each pair in the order
+};
+
+struct CombineParams {
+    const float *o;        // [pairs][stride]
+    uint64_t stride;
+    const uint32_t *place;
+    const int32_t *ends;
+    const float *weights;
+    const void *residual;
+    uint64_t residual_stride;
+    void *y;
+    uint64_t y_stride;
+    uint32_t y_f32, tokens, k, cols;
+};
+
+hipError_t launch_route(const RouteParams &p, hipStream_t s);
+uint32_t route_chunks(uint64_t tokens, uint64_t k);
+hipError_t launch_route_backward(const RouteBackwardParams &p, hipStream_t s);
+hipError_t launch_gather(const GatherParams &p, hipStream_t s);
+hipError_t launch_combine(const CombineParams &p, hipStream_t s);
+
+}  // namespace uzip
