@@ -557,6 +557,46 @@ size_t uzip_moe_workspace_size(const uzip_weight *up, const uzip_weight *down, c
 uzip_status uzip_moe(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *args, void *d_workspace,
                      size_t workspace_bytes, hipStream_t stream);
 
+/* ---- sampling --------------------------------------------------------------
+ * A token a row from logits [rows, vocab] bf16 or fp32, which uzip_linear
+ * makes of a packed output head.  With e_i = exp((z_i - max) / temperature) and
+ * the tokens ordered by (z descending, index ascending) these are kept: of the
+ * first top_k (0 or less, or vocab and more: of all), in that order, each
+ * before which less than top_p of their sum has passed, and always the first
+ * (top_p of 1 and more: all); of those, the ones with e >= min_p.  The token is
+ * the first kept one, by index, at which the running sum of e exceeds u times
+ * the kept ones' sum, u in [0, 1).  Temperature 0: the first of the order.
+ * logprob: the logarithm of the token's softmax over all of the row's logits,
+ * divided by the temperature (by 1 where that is 0), whatever the filters.
+ * -inf is never drawn.  A row that holds a NaN, or nothing above -inf, or whose
+ * temperature is negative or a parameter NaN, gets token -1 and logprob NaN.
+ * Infinite logits give the limit.  Each parameter is a device array of one
+ * value a row, or, where that is null, the value beside it.  e and its sums are
+ * taken in 64 bits.  Limits: 2^21 rows, 2^22 tokens. */
+typedef struct {
+    const void *logits;
+    size_t logits_stride;
+    size_t rows;
+    size_t vocab;
+    const void *u;             /* [rows] fp32, or fp64 (u_double) */
+    const float *temperature;  /* [rows], or null */
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+    int64_t *token;            /* [rows] */
+    float *logprob;            /* [rows], or null */
+    float temperature_all;
+    int32_t top_k_all;
+    float top_p_all;
+    float min_p_all;
+    uint32_t logits_dtype;
+    uint32_t u_double;         /* 0 or 1 */
+} uzip_sample_args;
+
+/* 0: the call needs none, or its arguments are invalid. */
+size_t uzip_sample_workspace_size(const uzip_sample_args *args);
+uzip_status uzip_sample(const uzip_sample_args *args, void *d_workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Static English name of a status code. */
 const char *uzip_status_string(uzip_status s);
 

@@ -90,6 +90,8 @@ EXPORTED = (
     "uzip_moe_route_backward",
     "uzip_moe_workspace_size",
     "uzip_moe",
+    "uzip_sample_workspace_size",
+    "uzip_sample",
 )
 
 _lib = None
@@ -502,3 +504,5 @@ from .weights import (ACTIVATIONS, PackedWeight, grouped_linear, grouped_linear_
 from .experts import (Routing, moe, moe_group, moe_route, moe_route_backward, uzip_moe, uzip_moe_args,  # noqa: E402
                   uzip_moe_route, uzip_moe_route_args, uzip_moe_route_backward, uzip_moe_route_workspace_size,
                   uzip_moe_workspace_size)
+# ---- sampling -------------------------------------------------------------------
+from .sampling import sample, uzip_sample, uzip_sample_args, uzip_sample_workspace_size  # noqa: E402

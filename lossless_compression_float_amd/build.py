@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libuzip.so")
 SOURCES = ["uzip_kernels.hip", "uzip_api.cpp", "uzip_linear.hip", "uzip_linear_api.cpp", "uzip_moe.hip",
-           "uzip_moe_api.cpp"]
+           "uzip_moe_api.cpp", "uzip_sample.hip", "uzip_sample_api.cpp"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
