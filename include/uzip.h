@@ -572,7 +572,8 @@ uzip_status uzip_moe(const uzip_weight *up, const uzip_weight *down, const uzip_
  * temperature is negative or a parameter NaN, gets token -1 and logprob NaN.
  * Infinite logits give the limit.  Each parameter is a device array of one
  * value a row, or, where that is null, the value beside it.  e and its sums are
- * taken in 64 bits.  Limits: 2^21 rows, 2^22 tokens. */
+ * taken in 64 bits.  Limits: 2^21 rows, 2^22 tokens, 2^24 runs of 2,048 tokens a
+ * call. */
 typedef struct {
     const void *logits;
     size_t logits_stride;

@@ -21,6 +21,11 @@
 namespace uzip {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
 constexpr uint32_t kThreads = 1024, kWaves = kThreads / 64;
 
 // Unsigned keys in the order of the values; both zeros are one value.
@@ -35,21 +40,21 @@ __device__ inline float value(const void *p, uint64_t at, bool f32) {
     return f32 ? static_cast<const float *>(p)[at] : __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[at] << 16);
 }
 
-// 2^x for x <= 0, off by 3e-13 of itself: x = n + f, |f| <= 1/2, Taylor's
-// series of 2^f up to f^10.
-__device__ inline double exp2_below(double x) {
-    if (!(x > -1000.0)) return 0.0;
+// 2^x for x <= 0, off by 1.5e-14 of itself and exact at 0: x = n + f, |f| <= 1/2,
+// and 1 + f q(f) with q the polynomial of degree 8 whose largest relative error
+// is smallest there (least squares, weighted until it stops falling).  Below -1000 anything tiny.
+__device__ inline double exp2_low(double x) {
+    x = fmax(x, -1000.0);
     const double n = rint(x), f = x - n;
-    double p = 7.054911620801121e-9;
-    p = p * f + 1.01780860092396960e-7;
-    p = p * f + 1.32154867901443094e-6;
-    p = p * f + 1.52527338040598402e-5;
-    p = p * f + 1.54035303933816099e-4;
-    p = p * f + 1.33335581464284434e-3;
-    p = p * f + 9.61812910762847716e-3;
-    p = p * f + 5.55041086648215800e-2;
-    p = p * f + 2.40226506959100712e-1;
-    p = p * f + 6.93147180559945309e-1;
+    double p = 1.01483365409060702e-07;
+    p = p * f + 1.32583358083804669e-06;
+    p = p * f + 1.52529900401267599e-05;
+    p = p * f + 1.54034408823874327e-04;
+    p = p * f + 1.33335576254202024e-03;
+    p = p * f + 9.61812918116721968e-03;
+    p = p * f + 5.55041086684161314e-02;
+    p = p * f + 2.40226506957228025e-01;
+    p = p * f + 6.93147180559885112e-01;
     p = p * f + 1.0;
     return ldexp(p, (int)n);
 }
@@ -79,7 +84,8 @@ __device__ inline Row row_of(const SampleParams &p, uint32_t r) {
 
 // e of a value; the limit where the largest is infinite.
 __device__ inline double weight(float z, float top, double scale) {
-    return z == top ? 1.0 : exp2_below(((double)z - (double)top) * scale);
+    const double x = ((double)z - (double)top) * scale;
+    return z == top ? 1.0 : x > -1000.0 ? exp2_low(x) : 0.0;
 }
 
 template <class T>
@@ -92,14 +98,29 @@ __device__ inline uint32_t wave_max(uint32_t v) {
     return v;
 }
 
+constexpr uint32_t kMaxHot = 2048;         // groups that are read again
+constexpr uint32_t kMaxCandidates = 4096;  // tokens that are sorted
+constexpr uint32_t kBins = 256;
+
 struct Shared {
-    double mass[kWaves];
-    uint32_t count[kWaves];
-    uint64_t bin_mass[256];
-    uint32_t bin_count[256];
+    double mass[kWaves], sums[kWaves];
+    uint32_t count[kWaves], other[kWaves];
+    double total;
+    uint64_t border;
     uint32_t pick, pick_count;
-    double pick_mass;
     uint64_t found;
+    uint32_t bin_count[kBins];
+    union {
+        struct {
+            uint16_t hot[2 * kMaxVocab / kSegment];  // hot groups of each half segment, then those before
+            uint64_t tokens[kMaxCandidates];         // key << 32 | ~index, by index
+            union {
+                uint32_t reads[kMaxHot * (kGroup / 4)];  // first tokens of the hot groups' reads, by index
+                uint64_t sorted[kMaxCandidates];
+            };
+        };
+        uint64_t bin_mass[kBins];
+    };
 };
 
 // The sum of a value over the workgroup, the same for all, in a fixed order.
@@ -177,36 +198,69 @@ __device__ inline Border find_border(const SampleParams &p, uint64_t at, float t
     return out;
 }
 
-// A row by one workgroup, any filters.
-__global__ __launch_bounds__(kThreads) void k_sample(SampleParams p) {
-    __shared__ Shared s;
-    const uint32_t r = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Sums over the threads before this one, in a fixed order, and over all.
+__device__ inline double block_scan(double v, double *lds, double &total) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double x = v;
+    for (int d = 1; d < 64; d <<= 1) {
+        const double y = __shfl_up(x, d);
+        if (lane >= (uint32_t)d) x += y;
+    }
+    const double upto = __shfl_up(x, 1);
+    __syncthreads();
+    if (lane == 63) lds[wave] = x;
+    __syncthreads();
+    double before = 0;
+    total = 0;
+    for (uint32_t i = 0; i < kWaves; ++i) {
+        if (i < wave) before += lds[i];
+        total += lds[i];
+    }
+    return before + (lane ? upto : 0.0);
+}
+__device__ inline uint32_t block_scan(uint32_t v, uint32_t *lds, uint32_t &total) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t x = v;
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t y = __shfl_up(x, d);
+        if (lane >= (uint32_t)d) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) lds[wave] = x;
+    __syncthreads();
+    uint32_t before = 0;
+    total = 0;
+    for (uint32_t i = 0; i < kWaves; ++i) {
+        if (i < wave) before += lds[i];
+        total += lds[i];
+    }
+    return before + x - v;
+}
+__device__ inline uint32_t block_max(uint32_t v, uint32_t *lds) {
+    v = wave_max(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    for (uint32_t i = 0; i < kWaves; ++i) v = max(v, lds[i]);
+    return v;
+}
+
+__device__ inline void finish(const SampleParams &p, uint32_t r, uint32_t token, float top, double heat, double all) {
+    p.token[r] = token;
+    if (!p.logprob) return;
+    const float z = value(p.logits, (uint64_t)r * p.stride + token, p.f32);
+    p.logprob[r] = (float)((z == top ? 0.0 : ((double)z - (double)top) / heat) - log(all));
+}
+__device__ inline double uniform_of(const SampleParams &p, uint32_t r) {
+    return p.u_f64 ? static_cast<const double *>(p.u)[r] : (double)static_cast<const float *>(p.u)[r];
+}
+
+// Any row by passes over all of it: where the survey's groups are no help, for
+// many tokens alike in weight.
+__device__ inline void by_histograms(const SampleParams &p, uint32_t r, const Row &row, float top, double all,
+                                           Shared &s) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t at = (uint64_t)r * p.stride;
-    const Row row = row_of(p, r);
-    // the largest, and whether there is a NaN
-    uint32_t best = 0, nan = 0;
-    for (uint32_t i = threadIdx.x; i < p.vocab; i += kThreads) {
-        const float z = value(p.logits, at + i, p.f32);
-        nan |= z != z;
-        if (z == z) best = max(best, ordered(z));
-    }
-    best = wave_max(best);
-    nan = __any(nan);
-    if (lane == 0) s.count[wave] = best, s.bin_count[wave] = nan;
-    __syncthreads();
-    for (uint32_t i = 0; i < kWaves; ++i) best = max(best, s.count[i]), nan |= s.bin_count[i];
-    __syncthreads();
-    if (nan || best <= kKeyMinusInf || row.bad) {
-        if (threadIdx.x == 0) {
-            p.token[r] = -1;
-            if (p.logprob) p.logprob[r] = __builtin_nanf("");
-        }
-        return;
-    }
-    const float top = unordered(best);
-    double all = 0;
-    for (uint32_t i = threadIdx.x; i < p.vocab; i += kThreads) all += weight(value(p.logits, at + i, p.f32), top, row.scale);
-    all = block_sum(all, s.mass);
     // fixed point: sums of `vocab` values of at most 1 stay below 2^63
     uint32_t bits = 1;
     while (p.vocab >> bits) ++bits;
@@ -240,29 +294,33 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleParams p) {
     equals = wave_sum(equals);
     if (lane == 0) s.mass[wave] = mine, s.count[wave] = equals;
     __syncthreads();
-    const bool keep_equal = each >= row.min_p || border.key == best;
-    double sums[kWaves], total = 0;
-    uint32_t rest = border.equal;
-    uint32_t before_mine = 0;
-    for (uint32_t i = 0; i < kWaves; ++i) {
-        const uint32_t n = min(rest, s.count[i]);
-        if (i == wave) before_mine = border.equal - rest;
-        rest -= n;
-        sums[i] = s.mass[i] + (keep_equal ? n * each : 0.0);
-        total += sums[i];
+    const bool keep_equal = each >= row.min_p || unordered(border.key) == top;
+    if (threadIdx.x == 0) {
+        double total = 0;
+        uint32_t rest = border.equal;
+        for (uint32_t i = 0; i < kWaves; ++i) {
+            const uint32_t n = min(rest, s.count[i]);
+            s.other[i] = border.equal - rest;  // equals before this run
+            rest -= n;
+            s.sums[i] = s.mass[i] + (keep_equal ? n * each : 0.0);
+            total += s.sums[i];
+        }
+        s.total = uniform_of(p, r) * total;
+        // the run that holds the draw: the first whose running sum exceeds it; the last with any, if rounding leaves none
+        double before = 0, base = 0;
+        uint32_t hit = kWaves;
+        for (uint32_t i = 0; i < kWaves; ++i) {
+            if (s.sums[i] > 0 && (hit == kWaves || !(base + s.sums[hit] > s.total))) hit = i, base = before;
+            before += s.sums[i];
+        }
+        s.pick = hit;
+        s.mass[0] = base;
     }
-    const double want = (p.u_f64 ? static_cast<const double *>(p.u)[r] : (double)static_cast<const float *>(p.u)[r]) * total;
-    // the run that holds the draw: the first whose running sum exceeds it; the last with any, if rounding leaves none
-    double before = 0, base = 0;
-    uint32_t hit = kWaves;
-    for (uint32_t i = 0; i < kWaves; ++i) {
-        if (sums[i] > 0 && (hit == kWaves || !(base + sums[hit] > want))) hit = i, base = before;
-        before += sums[i];
-    }
-    if (wave != hit) return;
-    uint32_t token = 0;
-    double running = base;
-    uint32_t seen = before_mine;
+    __syncthreads();
+    if (wave != s.pick) return;
+    const double want = s.total;
+    uint32_t token = 0, seen = s.other[wave];
+    double running = s.mass[0];
     bool done = false;
     for (uint32_t i0 = begin; i0 < end && !done; i0 += 64) {
         const uint32_t i = i0 + lane;
@@ -292,19 +350,382 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleParams p) {
         }
         running += __shfl(x, 63);
     }
-    if (lane == 0) {
-        p.token[r] = token;
-        if (p.logprob) {
-            const float z = value(p.logits, at + token, p.f32);
-            p.logprob[r] = (float)((z == top ? 0.0 : ((double)z - (double)top) / row.heat) - log(all));
+    if (lane == 0) finish(p, r, token, top, row.heat, all);
+}
+
+// ---- the survey ---------------------------------------------------------------------
+
+// W consecutive values from token i on, -inf behind the last.
+template <bool F32, int W = F32 ? 4 : 8>
+__device__ inline void read_values(const SampleParams &p, uint64_t at, uint32_t i, float v[W]) {
+    if (i + W <= p.vocab) {
+        if constexpr (F32) {
+            const f32x4 x = *reinterpret_cast<const f32x4_any *>(static_cast<const float *>(p.logits) + at + i);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = x[c];
+        } else {
+            const u32x4 x = *reinterpret_cast<const u32x4_any *>(static_cast<const uint16_t *>(p.logits) + at + i);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = __uint_as_float(c & 1 ? x[c / 2] & 0xFFFF0000u : x[c / 2] << 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < W; ++c) v[c] = i + c < p.vocab ? value(p.logits, at + i + c, F32) : -INFINITY;
+}
+
+// A wave a segment of 2,048 tokens: its largest value, the sum of its weights
+// relative to that, and the largest of each group of 16 tokens (a lane's reads
+// of half a segment), so that the second kernel reads little of the row again.
+template <bool F32>
+__global__ __launch_bounds__(256) void k_survey(SampleParams p) {
+    constexpr int W = F32 ? 4 : 8, READS = kSegment / 64 / W, HALF = READS / 2;
+    const uint32_t lane = threadIdx.x & 63;
+    const uint64_t n = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (n >= (uint64_t)p.rows * p.segments) return;
+    const uint32_t r = (uint32_t)(n / p.segments), seg = (uint32_t)(n % p.segments);
+    const uint64_t at = (uint64_t)r * p.stride;
+    float v[READS][W];
+#pragma unroll
+    for (int i = 0; i < READS; ++i) read_values<F32>(p, at, seg * kSegment + (i * 64 + lane) * W, v[i]);
+    bool nan = false;
+    float group[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        group[h] = -INFINITY;
+#pragma unroll
+        for (int i = h * HALF; i < (h + 1) * HALF; ++i)
+#pragma unroll
+            for (int c = 0; c < W; ++c) {
+                nan |= v[i][c] != v[i][c];
+                group[h] = fmaxf(group[h], v[i][c]);
+            }
+        p.groups[(n * 2 + h) * 64 + lane] = group[h];
+    }
+    float top = fmaxf(group[0], group[1]);
+    float low = fminf(group[0] > -INFINITY ? group[0] : INFINITY, group[1] > -INFINITY ? group[1] : INFINITY);
+    for (int d = 1; d < 64; d <<= 1) {
+        top = fmaxf(top, __shfl_xor(top, d));
+        low = fminf(low, __shfl_xor(low, d));
+    }
+    const double scale = row_of(p, r).scale;
+    double sum = 0;
+    if (top > -INFINITY) {
+        double part[W];
+#pragma unroll
+        for (int c = 0; c < W; ++c) part[c] = 0;
+#pragma unroll
+        for (int i = 0; i < READS; ++i)
+#pragma unroll
+            for (int c = 0; c < W; ++c) part[c] += exp2_low(((double)v[i][c] - (double)top) * scale);
+#pragma unroll
+        for (int c = 0; c < W; ++c) sum += part[c];
+        sum = wave_sum(sum);
+    }
+    if (top == INFINITY) sum = 1;
+    if (__any(nan)) sum = __builtin_nan("");
+    if (lane == 0) p.segment[n] = Segment{sum, top, low};
+}
+
+// ---- the draw -----------------------------------------------------------------------
+
+// Bins of the values from the largest (0) to `low` (254), in even steps, and of
+// those from there to `floor` (255); beyond that 256.
+struct Bins {
+    float top, low, floor, inv;
+};
+__device__ inline uint32_t bin_of(const Bins &b, float z) {
+    return z >= b.low ? min((uint32_t)((b.top - z) * b.inv), kBins - 2) : z >= b.floor ? kBins - 1 : kBins;
+}
+
+// The kept tokens of a row with filters among its largest ones: those in the
+// first bins of the groups' largest values.  False if they do not decide it.
+template <bool F32>
+__device__ inline bool by_candidates(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all,
+                                     uint32_t want_groups, Shared &s) {
+    constexpr uint32_t W = F32 ? 4 : 8, READS = kGroup / W;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t at = (uint64_t)r * p.stride;
+    const float *groups = p.groups + (uint64_t)r * p.segments * 128;
+    const uint32_t halves = p.segments * 2;
+    const float top = bins.top;
+    // the bins that are taken: with enough groups, and none whose tokens all fall to min_p (but top-p of the first k
+    // needs the sum of those too)
+    uint32_t least = kBins - 1;
+    if (row.min_p > 0 && !(row.k && row.top_p < 1)) {
+        const double z = (double)top + log(row.min_p) * row.heat * 1.000001 - fabs((double)top) * 1e-6;
+        least = min(bin_of(bins, (float)z) + 1, kBins - 1);
+    }
+    if (threadIdx.x == 0) {
+        uint32_t c = 0, b = 0;
+        for (; b < kBins; ++b) {
+            c += s.bin_count[b];
+            if (b >= least || (c >= want_groups && (row.k || row.top_p < 1))) break;
+        }
+        s.pick = min(b, kBins - 1);
+        s.pick_count = c;
+    }
+    __syncthreads();
+    const uint32_t last = s.pick;
+    if (s.pick_count > kMaxHot) return false;
+    // their reads, by index
+    for (uint32_t h = wave; h < halves; h += kWaves) {
+        const uint64_t m = __ballot(bin_of(bins, groups[h * 64 + lane]) <= last);
+        if (lane == 0) s.hot[h] = (uint16_t)__popcll(m);
+    }
+    __syncthreads();
+    constexpr uint32_t EACH = 4;  // halves, and candidates, of a thread
+    const uint32_t mine0 = threadIdx.x * EACH;
+    uint32_t mine[EACH], sum = 0, total;
+#pragma unroll
+    for (uint32_t c = 0; c < EACH; ++c) {
+        mine[c] = mine0 + c < halves ? s.hot[mine0 + c] : 0;
+        sum += mine[c];
+    }
+    uint32_t before = block_scan(sum, s.count, total);
+#pragma unroll
+    for (uint32_t c = 0; c < EACH; ++c) {
+        if (mine0 + c < halves) s.hot[mine0 + c] = (uint16_t)before;
+        before += mine[c];
+    }
+    __syncthreads();
+    for (uint32_t h = wave; h < halves; h += kWaves) {
+        const bool on = bin_of(bins, groups[h * 64 + lane]) <= last;
+        const uint64_t m = __ballot(on);
+        const uint32_t count = __popcll(m), rank = __popcll(m & ((1ull << lane) - 1));
+        if (on)
+#pragma unroll
+            for (uint32_t q = 0; q < READS; ++q)
+                s.reads[s.hot[h] * READS + q * count + rank] = h * (kSegment / 2) + (q * 64 + lane) * W;
+    }
+    __syncthreads();
+    // their tokens in the bins, by index
+    const uint32_t reads = total * READS;
+    uint32_t n = 0;
+    for (uint32_t j0 = 0; j0 < reads; j0 += kThreads) {
+        const uint32_t j = j0 + threadIdx.x;
+        const uint32_t i = j < reads ? s.reads[j] : p.vocab;
+        float v[W];
+        uint32_t have = 0;
+        if (j < reads) {
+            read_values<F32>(p, at, i, v);
+#pragma unroll
+            for (uint32_t c = 0; c < W; ++c) have += v[c] > -INFINITY && bin_of(bins, v[c]) <= last;
+        }
+        uint32_t found, place = n + block_scan(have, s.count, found);
+        n += found;
+        if (n > kMaxCandidates) return false;
+        if (have)
+#pragma unroll
+            for (uint32_t c = 0; c < W; ++c)
+                if (v[c] > -INFINITY && bin_of(bins, v[c]) <= last)
+                    s.tokens[place++] = (uint64_t)ordered(v[c]) << 32 | (0xFFFFFFFFu - (i + c));
+    }
+    __syncthreads();
+    const bool closed = last >= least;  // nothing outside is kept
+    if (row.k && n < row.k && !closed) return false;
+    // in their order (s.reads is done with)
+    uint32_t n2 = 64;
+    while (n2 < n) n2 *= 2;
+    for (uint32_t i = threadIdx.x; i < n2; i += kThreads) s.sorted[i] = i < n ? s.tokens[i] : 0;
+    __syncthreads();
+    for (uint32_t k = 2; k <= n2; k *= 2)
+        for (uint32_t j = k / 2; j; j /= 2) {
+            for (uint32_t t = threadIdx.x; t < n2 / 2; t += kThreads) {
+                const uint32_t i = 2 * t - (t & (j - 1));
+                const uint64_t a = s.sorted[i], b = s.sorted[i + j];
+                if ((a < b) == ((i & k) == 0)) s.sorted[i] = b, s.sorted[i + j] = a;
+            }
+            __syncthreads();
+        }
+    // the sums before each, and how many are kept
+    double e[EACH], part = 0, whole;
+#pragma unroll
+    for (uint32_t c = 0; c < EACH; ++c) {
+        const uint32_t i = mine0 + c;
+        e[c] = i < n ? weight(unordered((uint32_t)(s.sorted[i] >> 32)), top, row.scale) : 0.0;
+        part += e[c];
+    }
+    double run = block_scan(part, s.mass, whole);
+    const uint32_t limit = row.k ? min(row.k, n) : n;
+    if (row.k) {
+        double x = run;
+#pragma unroll
+        for (uint32_t c = 0; c < EACH; ++c) {
+            x += e[c];
+            if (mine0 + c == limit - 1) s.total = x;
+        }
+        __syncthreads();
+    }
+    const double reach = row.top_p * (row.k ? s.total : all);
+    uint32_t kept = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < EACH; ++c) {
+        const uint32_t i = mine0 + c;
+        kept += i < limit && (i == 0 || ((row.top_p >= 1 || run < reach) && e[c] >= row.min_p));
+        run += e[c];
+    }
+    uint32_t keep;
+    block_scan(kept, s.count, keep);
+    if (keep == n && !closed && !(row.k && n >= row.k)) return false;
+    const uint64_t border = s.sorted[keep - 1];
+    // the draw, by index
+    part = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < EACH; ++c) {
+        const uint32_t i = mine0 + c;
+        const uint64_t x = i < n ? s.tokens[i] : 0;
+        e[c] = x >= border ? weight(unordered((uint32_t)(x >> 32)), top, row.scale) : 0.0;
+        part += e[c];
+    }
+    run = block_scan(part, s.mass, whole);
+    const double want = uniform_of(p, r) * whole;
+    // the first whose running sum exceeds it, as a maximum of complements; of the last with any, if rounding leaves none
+    uint32_t first = 0, any = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < EACH; ++c) {
+        const uint32_t i = mine0 + c;
+        run += e[c];
+        if (e[c] > 0) {
+            any = i + 1;
+            if (run > want && !first) first = 0xFFFFFFFFu - i;
         }
     }
+    first = block_max(first, s.count);
+    any = block_max(any, s.other);
+    if (threadIdx.x == 0) {
+        const uint32_t i = first ? 0xFFFFFFFFu - first : any - 1;
+        finish(p, r, 0xFFFFFFFFu - (uint32_t)s.tokens[i], top, row.heat, all);
+    }
+    return true;
+}
+
+// A workgroup a row, after the survey.
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
+    __shared__ Shared s;
+    const uint32_t r = blockIdx.x;
+    const uint64_t at = (uint64_t)r * p.stride;
+    const Row row = row_of(p, r);
+    const Segment *segs = p.segment + (uint64_t)r * p.segments;
+    uint32_t best = 0, nan = 0, lowest = 0;
+    for (uint32_t i = threadIdx.x; i < p.segments; i += kThreads) {
+        const Segment g = segs[i];
+        best = max(best, ordered(g.top));
+        lowest = max(lowest, ~ordered(g.low));
+        nan |= g.sum != g.sum;
+    }
+    best = block_max(best, s.count);
+    lowest = ~block_max(lowest, s.other);
+    nan = block_max(nan, s.count);
+    if (nan || best <= kKeyMinusInf || row.bad) {
+        if (threadIdx.x == 0) {
+            p.token[r] = -1;
+            if (p.logprob) p.logprob[r] = __builtin_nanf("");
+        }
+        return;
+    }
+    const float top = unordered(best);
+    constexpr uint32_t PER = kMaxVocab / kSegment / kThreads;  // segments of a thread, in their order
+    double share[PER], part = 0, all;
+#pragma unroll
+    for (uint32_t c = 0; c < PER; ++c) {
+        const uint32_t i = threadIdx.x * PER + c;
+        share[c] = i < p.segments ? segs[i].sum * weight(segs[i].top, top, row.scale) : 0.0;
+        part += share[c];
+    }
+    double run = block_scan(part, s.mass, all);
+    if (top < INFINITY && row.k == 1) {
+        // the first of the largest
+        uint32_t first = 0;
+        for (uint32_t i = threadIdx.x; i < p.segments; i += kThreads)
+            if (segs[i].top == top) first = max(first, 0xFFFFFFFFu - i);
+        const uint32_t seg = 0xFFFFFFFFu - block_max(first, s.count);
+        first = 0;
+        for (uint32_t i = seg * kSegment + threadIdx.x; i < min((seg + 1) * kSegment, p.vocab); i += kThreads)
+            if (value(p.logits, at + i, F32) == top) first = max(first, 0xFFFFFFFFu - i);
+        first = block_max(first, s.other);
+        if (threadIdx.x == 0) finish(p, r, 0xFFFFFFFFu - first, top, row.heat, all);
+        return;
+    }
+    if (top < INFINITY && !row.k && row.top_p >= 1 && row.min_p <= 0) {
+        // the segment, then the token, at which the running sum exceeds the draw
+        const double want = uniform_of(p, r) * all;
+        uint32_t first = 0, any = 0;
+        double first_at = 0, any_at = 0;  // the sums before them
+#pragma unroll
+        for (uint32_t c = 0; c < PER; ++c) {
+            const uint32_t i = threadIdx.x * PER + c;
+            if (share[c] > 0) {
+                any = i + 1, any_at = run;
+                if (run + share[c] > want && !first) first = 0xFFFFFFFFu - i, first_at = run;
+            }
+            run += share[c];
+        }
+        const uint32_t hit = block_max(first, s.count), last = block_max(any, s.other);
+        if (hit ? first == hit : any == last) s.total = hit ? first_at : any_at;
+        __syncthreads();
+        const uint32_t seg = hit ? 0xFFFFFFFFu - hit : last - 1;
+        const uint32_t i0 = seg * kSegment + threadIdx.x * 2;
+        double e[2];
+#pragma unroll
+        for (uint32_t c = 0; c < 2; ++c)
+            e[c] = i0 + c < p.vocab ? weight(value(p.logits, at + i0 + c, F32), top, row.scale) : 0.0;
+        double whole;
+        run = block_scan(e[0] + e[1], s.mass, whole) + s.total;
+        first = any = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < 2; ++c) {
+            run += e[c];
+            if (e[c] > 0) {
+                any = i0 + c + 1;
+                if (run > want && !first) first = 0xFFFFFFFFu - (i0 + c);
+            }
+        }
+        first = block_max(first, s.count);
+        any = block_max(any, s.other);
+        if (threadIdx.x == 0) finish(p, r, first ? 0xFFFFFFFFu - first : any - 1, top, row.heat, all);
+        return;
+    }
+    if (top < INFINITY) {
+        // The groups' largest values in bins.  Tokens that weigh less than 2^-80 of
+        // the largest change no sum in 64 bits and are left out.
+        Bins bins;
+        bins.top = top;
+        bins.floor = (float)((double)top - 80.0 / row.scale);
+        bins.low = fmaxf(unordered(lowest), bins.floor);
+        const float range = top - bins.low;
+        bins.inv = range > 0 ? (kBins - 1.01f) / range : 0.0f;
+        for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.bin_count[i] = 0;
+        __syncthreads();
+        const float *groups = p.groups + (uint64_t)r * p.segments * 128;
+        for (uint32_t i = threadIdx.x; i < p.segments * 128; i += kThreads) {
+            const uint32_t b = bin_of(bins, groups[i]);
+            if (b < kBins) atomicAdd(&s.bin_count[b], 1u);
+        }
+        __syncthreads();
+        if (by_candidates<F32>(p, r, row, bins, all, row.k ? row.k : 512, s)) return;
+        __syncthreads();
+    } else {  // the infinite ones share alike
+        double n = 0;
+        for (uint32_t i = threadIdx.x; i < p.vocab; i += kThreads) n += value(p.logits, at + i, F32) == INFINITY;
+        all = block_sum(n, s.mass);
+        __syncthreads();
+    }
+    by_histograms(p, r, row, top, all, s);
 }
 
 }  // namespace
 
 hipError_t launch_sample(const SampleParams &p, hipStream_t s) {
-    k_sample<<<p.rows, kThreads, 0, s>>>(p);
+    const uint32_t wgs = (uint32_t)(((uint64_t)p.rows * p.segments + 3) / 4);
+    if (p.f32) {
+        k_survey<true><<<wgs, 256, 0, s>>>(p);
+        k_draw<true><<<p.rows, kThreads, 0, s>>>(p);
+    } else {
+        k_survey<false><<<wgs, 256, 0, s>>>(p);
+        k_draw<false><<<p.rows, kThreads, 0, s>>>(p);
+    }
     return hipGetLastError();
 }
 

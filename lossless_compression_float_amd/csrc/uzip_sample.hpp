@@ -8,6 +8,16 @@
 namespace uzip {
 
 constexpr uint64_t kMaxVocab = 1ull << 22;
+constexpr uint32_t kSegment = 2048;  // tokens that a wave surveys
+constexpr uint32_t kGroup = 16;      // tokens of a lane in half a segment
+
+// Of a segment: the sum of its weights relative to its largest value (NaN if
+// it holds one), that value, and the smallest of its groups' largest values
+// above -inf.
+struct Segment {
+    double sum;
+    float top, low;
+};
 
 struct SampleParams {
     const void *logits;
@@ -19,7 +29,9 @@ struct SampleParams {
     int32_t top_k_all;
     int64_t *token;
     float *logprob;  // or null
-    uint32_t rows, vocab, f32, u_f64;
+    Segment *segment;    // workspace: [rows][segments]
+    float *groups;       // workspace: the largest value of each group, [rows][segments][2][64]
+    uint32_t rows, vocab, segments, f32, u_f64;
 };
 
 hipError_t launch_sample(const SampleParams &p, hipStream_t s);

@@ -14,10 +14,12 @@ using namespace uzip;
 namespace {
 
 constexpr uint64_t kMaxRows = 1ull << 21;
+constexpr uint64_t kMaxSegments = 1ull << 24;  // of a call
 
 bool sample_ok(const uzip_sample_args *a) {
     if (!a || a->rows > kMaxRows || a->vocab == 0 || a->vocab > kMaxVocab || !type_ok(a->logits_dtype) || a->u_double > 1)
         return false;
+    if (a->rows * blocks(a->vocab, kSegment) > kMaxSegments) return false;
     if (!a->temperature && !(a->temperature_all >= 0)) return false;
     if ((!a->top_p && a->top_p_all != a->top_p_all) || (!a->min_p && a->min_p_all != a->min_p_all)) return false;
     for (const void *p : {(const void *)a->temperature, (const void *)a->top_k, (const void *)a->top_p, (const void *)a->min_p,
@@ -28,7 +30,7 @@ bool sample_ok(const uzip_sample_args *a) {
            aligned(a->u, a->u_double ? 8 : 4) && a->token && aligned(a->token, 8);
 }
 
-SampleParams params(const uzip_sample_args *a) {
+SampleParams plan(const uzip_sample_args *a, Carver &c) {
     SampleParams p{};
     p.logits = a->logits;
     p.stride = a->logits_stride;
@@ -47,6 +49,9 @@ SampleParams params(const uzip_sample_args *a) {
     p.vocab = (uint32_t)a->vocab;
     p.f32 = a->logits_dtype == UZIP_FP32;
     p.u_f64 = a->u_double;
+    p.segments = (uint32_t)blocks(a->vocab, kSegment);
+    p.segment = c.take<Segment>(a->rows * p.segments);
+    p.groups = c.take<float>(a->rows * p.segments * (kSegment / kGroup));
     return p;
 }
 
@@ -55,15 +60,19 @@ SampleParams params(const uzip_sample_args *a) {
 extern "C" {
 
 size_t uzip_sample_workspace_size(const uzip_sample_args *args) {
-    (void)args;
-    return 0;
+    if (!sample_ok(args) || args->rows == 0) return 0;
+    Carver c(nullptr);
+    plan(args, c);
+    return (size_t)c.bytes();
 }
 
 uzip_status uzip_sample(const uzip_sample_args *args, void *d_workspace, size_t workspace_bytes, hipStream_t stream) {
     if (!sample_ok(args)) return UZIP_ERR_INVALID_ARGUMENT;
-    if (!workspace_ok(d_workspace, workspace_bytes, uzip_sample_workspace_size(args))) return UZIP_ERR_INVALID_ARGUMENT;
     if (args->rows == 0) return UZIP_OK;
-    return done(launch_sample(params(args), stream));
+    Carver c(d_workspace);
+    const SampleParams p = plan(args, c);
+    if (!workspace_ok(d_workspace, workspace_bytes, c.bytes())) return UZIP_ERR_INVALID_ARGUMENT;
+    return done(launch_sample(p, stream));
 }
 
 }  // extern "C"

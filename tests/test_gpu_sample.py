@@ -50,8 +50,8 @@ def check(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, rows=None):
     f32 = lambda v, i: float(v[i]) if isinstance(v, torch.Tensor) else float(torch.tensor(v, dtype=F32))
     for i in range(logits.shape[0]) if rows is None else rows:
         want, lp, room = row64(logits[i], float(u[i]), f32(temperature, i), int(f32(top_k, i)), f32(top_p, i), f32(min_p, i))
-        # e is off by 3e-13 of itself, and its sums by as much: only a draw closer than that to a border may fall on
-        # the other side of it
+        # e is off by 1.5e-14 of itself, sums of 2^17 of them by 2^17 2^-53 more at most: only a draw closer than that to a
+        # border may fall on the other side of it
         if room > 1e-12:
             assert int(token[i]) == want, (i, int(token[i]), want, room)
         if int(token[i]) == want:
