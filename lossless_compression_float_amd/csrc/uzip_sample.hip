@@ -98,41 +98,69 @@ __device__ inline uint32_t wave_max(uint32_t v) {
     return v;
 }
 
-constexpr uint32_t kMaxHot = 2048;         // groups that are read again
+constexpr uint32_t kMaxHot = 2048;         // groups that are read again apart from the others
 constexpr uint32_t kMaxCandidates = 4096;  // tokens that are sorted
-constexpr uint32_t kBins = 256;
+constexpr uint32_t kMaxCells = kThreads;   // runs of 64 reads
+constexpr uint32_t kBins = 1024, kCoarse = kBins / 4;
 
 struct Shared {
-    double mass[kWaves], sums[kWaves];
+    double mass[kWaves], total;
+    uint64_t large[kWaves];
     uint32_t count[kWaves], other[kWaves];
-    double total;
-    uint64_t border;
     uint32_t pick, pick_count;
-    uint64_t found;
+    uint64_t pick_mass;
     uint32_t bin_count[kBins];
+    uint64_t bin_mass[kBins];
     union {
-        struct {
-            uint16_t hot[2 * kMaxVocab / kSegment];  // hot groups of each half segment, then those before
-            uint64_t tokens[kMaxCandidates];         // key << 32 | ~index, by index
-            union {
-                uint32_t reads[kMaxHot * (kGroup / 4)];  // first tokens of the hot groups' reads, by index
-                uint64_t sorted[kMaxCandidates];
-            };
-        };
-        uint64_t bin_mass[kBins];
+        uint64_t hot[2 * kMaxVocab / kSegment];          // the hot lanes of each half segment
+        uint32_t reads[kMaxHot * (kGroup / 4)];          // first tokens of the hot groups' reads, by index
     };
+    union {
+        uint64_t tokens[kMaxCandidates];                 // key << 32 | ~index, by index
+        double cell[kMaxCells];
+    };
+    uint64_t sorted[kMaxCandidates];
 };
 
-// The sum of a value over the workgroup, the same for all, in a fixed order.
-__device__ inline double block_sum(double v, double *lds) {
-    v = wave_sum(v);
+template <class T>
+__device__ inline T shuffle_up(T v, int d) {
+    if constexpr (sizeof(T) == 8 && !__is_same(T, double)) return (T)__shfl_up((unsigned long long)v, d);
+    else return __shfl_up(v, d);
+}
+// The sum over the threads before this one, in a fixed order, and over all.
+template <class T>
+__device__ inline T block_scan(T v, T *lds, T &total) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    T x = v;
+    for (int d = 1; d < 64; d <<= 1) {
+        const T y = shuffle_up(x, d);
+        if (lane >= (uint32_t)d) x += y;
+    }
+    const T upto = shuffle_up(x, 1);
+    __syncthreads();
+    if (lane == 63) lds[wave] = x;
+    __syncthreads();
+    T before = 0;
+    total = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kWaves; ++i) {
+        if (i < wave) before += lds[i];
+        total += lds[i];
+    }
+    return before + (lane ? upto : T(0));
+}
+__device__ inline uint32_t block_max(uint32_t v, uint32_t *lds) {
+    v = wave_max(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    double s = 0;
-    for (uint32_t i = 0; i < kWaves; ++i) s += lds[i];
-    return s;
+#pragma unroll
+    for (uint32_t i = 0; i < kWaves; ++i) v = max(v, lds[i]);
+    return v;
 }
+
+// Fixed point for sums of at most `all`: 61 to 62 bits of it.
+__device__ inline double unit_of(double all) { return ldexp(1.0, 61 - ilogb(all)); }
 
 // Where a prefix of the order ends: all keys above `key`, and the first `equal`
 // of those equal to it.
@@ -151,7 +179,7 @@ __device__ inline Border find_border(const SampleParams &p, uint64_t at, float t
     uint64_t have_mass = 0;
     uint32_t equal = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
-        for (uint32_t i = threadIdx.x; i < 256; i += kThreads) s.bin_mass[i] = 0, s.bin_count[i] = 0;
+        if (threadIdx.x < 256) s.bin_mass[threadIdx.x] = 0, s.bin_count[threadIdx.x] = 0;
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < p.vocab; i += kThreads) {
             const float z = value(p.logits, at + i, p.f32);
@@ -163,26 +191,21 @@ __device__ inline Border find_border(const SampleParams &p, uint64_t at, float t
             atomicAdd((unsigned long long *)&s.bin_mass[b], (unsigned long long)(weight(z, top, scale) * unit + 0.5));
         }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            // (keys equal to `in`'s count as often as it admits)
-            int b = 255;
-            uint32_t c = have_count;
-            uint64_t m = have_mass;
-            for (; b > 0; --b) {
-                if (by_count ? c + s.bin_count[b] >= count : (double)(m + s.bin_mass[b]) >= mass * unit) {
-                    if (s.bin_count[b]) break;
-                }
-                c += s.bin_count[b];
-                m += s.bin_mass[b];
-            }
-            s.pick = prefix | (uint32_t)b << shift;
-            s.pick_count = c;
-            s.found = m;
-        }
+        // from the highest bin down: the first at which the prefix is long enough; else the lowest
+        const uint32_t b = 255 - min(threadIdx.x, 255u);
+        const uint32_t c = threadIdx.x < 256 ? s.bin_count[b] : 0;
+        const uint64_t m = threadIdx.x < 256 ? s.bin_mass[b] : 0;
+        uint32_t counts;
+        uint64_t masses;
+        const uint32_t c0 = have_count + block_scan(c, s.count, counts);
+        const uint64_t m0 = have_mass + block_scan(m, s.large, masses);
+        const bool enough = c && (by_count ? c0 + c >= count : (double)(m0 + m) >= mass * unit);
+        const uint32_t first = 0xFFFFFFFFu - block_max(enough ? 0xFFFFFFFFu - threadIdx.x : 0, s.other);
+        if (threadIdx.x == min(first, 255u)) s.pick = prefix | b << shift, s.pick_count = c0, s.pick_mass = m0;
         __syncthreads();
         prefix = s.pick;
         have_count = s.pick_count;
-        have_mass = s.found;
+        have_mass = s.pick_mass;
         equal = s.bin_count[prefix >> shift & 255];
         __syncthreads();
     }
@@ -196,53 +219,6 @@ __device__ inline Border find_border(const SampleParams &p, uint64_t at, float t
         out.equal = n < 1 ? 1 : n < (double)equal ? (uint32_t)n : equal;
     }
     return out;
-}
-
-// Sums over the threads before this one, in a fixed order, and over all.
-__device__ inline double block_scan(double v, double *lds, double &total) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double x = v;
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(x, d);
-        if (lane >= (uint32_t)d) x += y;
-    }
-    const double upto = __shfl_up(x, 1);
-    __syncthreads();
-    if (lane == 63) lds[wave] = x;
-    __syncthreads();
-    double before = 0;
-    total = 0;
-    for (uint32_t i = 0; i < kWaves; ++i) {
-        if (i < wave) before += lds[i];
-        total += lds[i];
-    }
-    return before + (lane ? upto : 0.0);
-}
-__device__ inline uint32_t block_scan(uint32_t v, uint32_t *lds, uint32_t &total) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t x = v;
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t y = __shfl_up(x, d);
-        if (lane >= (uint32_t)d) x += y;
-    }
-    __syncthreads();
-    if (lane == 63) lds[wave] = x;
-    __syncthreads();
-    uint32_t before = 0;
-    total = 0;
-    for (uint32_t i = 0; i < kWaves; ++i) {
-        if (i < wave) before += lds[i];
-        total += lds[i];
-    }
-    return before + x - v;
-}
-__device__ inline uint32_t block_max(uint32_t v, uint32_t *lds) {
-    v = wave_max(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    for (uint32_t i = 0; i < kWaves; ++i) v = max(v, lds[i]);
-    return v;
 }
 
 __device__ inline void finish(const SampleParams &p, uint32_t r, uint32_t token, float top, double heat, double all) {
@@ -261,10 +237,7 @@ __device__ inline void by_histograms(const SampleParams &p, uint32_t r, const Ro
                                            Shared &s) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t at = (uint64_t)r * p.stride;
-    // fixed point: sums of `vocab` values of at most 1 stay below 2^63
-    uint32_t bits = 1;
-    while (p.vocab >> bits) ++bits;
-    const double unit = ldexp(1.0, 62 - (int)bits);
+    const double unit = unit_of(all);
     Border border{kKeyMinusInf + 1, p.vocab};
     double left = all, above;
     if (row.k) {
@@ -302,16 +275,16 @@ __device__ inline void by_histograms(const SampleParams &p, uint32_t r, const Ro
             const uint32_t n = min(rest, s.count[i]);
             s.other[i] = border.equal - rest;  // equals before this run
             rest -= n;
-            s.sums[i] = s.mass[i] + (keep_equal ? n * each : 0.0);
-            total += s.sums[i];
+            s.mass[i] += keep_equal ? n * each : 0.0;
+            total += s.mass[i];
         }
         s.total = uniform_of(p, r) * total;
         // the run that holds the draw: the first whose running sum exceeds it; the last with any, if rounding leaves none
         double before = 0, base = 0;
         uint32_t hit = kWaves;
         for (uint32_t i = 0; i < kWaves; ++i) {
-            if (s.sums[i] > 0 && (hit == kWaves || !(base + s.sums[hit] > s.total))) hit = i, base = before;
-            before += s.sums[i];
+            if (s.mass[i] > 0 && (hit == kWaves || !(base + s.mass[hit] > s.total))) hit = i, base = before;
+            before += s.mass[i];
         }
         s.pick = hit;
         s.mass[0] = base;
@@ -429,8 +402,8 @@ __global__ __launch_bounds__(256) void k_survey(SampleParams p) {
 
 // ---- the draw -----------------------------------------------------------------------
 
-// Bins of the values from the largest (0) to `low` (254), in even steps, and of
-// those from there to `floor` (255); beyond that 256.
+// Bins of the values from the largest (0) to `low` (kBins - 2), in even steps,
+// and of those from there to `floor`; beyond that kBins.  Four make a coarse bin.
 struct Bins {
     float top, low, floor, inv;
 };
@@ -438,93 +411,130 @@ __device__ inline uint32_t bin_of(const Bins &b, float z) {
     return z >= b.low ? min((uint32_t)((b.top - z) * b.inv), kBins - 2) : z >= b.floor ? kBins - 1 : kBins;
 }
 
-// The kept tokens of a row with filters among its largest ones: those in the
-// first bins of the groups' largest values.  False if they do not decide it.
+// The reads that hold every token of the first `last` + 1 coarse bins, by
+// index: of the hot groups, or all of the row's.
+struct Reads {
+    uint32_t count;
+    bool all;
+};
 template <bool F32>
-__device__ inline bool by_candidates(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all,
-                                     uint32_t want_groups, Shared &s) {
+__device__ inline uint32_t read_at(const Shared &s, const Reads &q, uint32_t j) {
+    return q.all ? j * (F32 ? 4 : 8) : s.reads[j];
+}
+
+// The first bins whose groups (by their largest values) hold k tokens, or
+// weigh enough for top-p, none beyond `least`, and the reads of those groups.
+template <bool F32>
+__device__ inline Reads choose_reads(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all,
+                                     uint32_t least, uint32_t &last, Shared &s) {
     constexpr uint32_t W = F32 ? 4 : 8, READS = kGroup / W;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint64_t at = (uint64_t)r * p.stride;
     const float *groups = p.groups + (uint64_t)r * p.segments * 128;
     const uint32_t halves = p.segments * 2;
-    const float top = bins.top;
-    // the bins that are taken: with enough groups, and none whose tokens all fall to min_p (but top-p of the first k
-    // needs the sum of those too)
-    uint32_t least = kBins - 1;
-    if (row.min_p > 0 && !(row.k && row.top_p < 1)) {
-        const double z = (double)top + log(row.min_p) * row.heat * 1.000001 - fabs((double)top) * 1e-6;
-        least = min(bin_of(bins, (float)z) + 1, kBins - 1);
-    }
-    if (threadIdx.x == 0) {
-        uint32_t c = 0, b = 0;
-        for (; b < kBins; ++b) {
-            c += s.bin_count[b];
-            if (b >= least || (c >= want_groups && (row.k || row.top_p < 1))) break;
+    for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.bin_count[i] = 0, s.bin_mass[i] = 0;
+    __syncthreads();
+    const bool by_mass = !row.k && row.top_p < 1;
+    const double unit = unit_of(all);
+    constexpr uint32_t AHEAD = 8;  // loads on their way
+    for (uint32_t i0 = threadIdx.x; i0 < halves * 64; i0 += AHEAD * kThreads) {
+        float z[AHEAD];
+#pragma unroll
+        for (uint32_t c = 0; c < AHEAD; ++c) z[c] = i0 + c * kThreads < halves * 64 ? groups[i0 + c * kThreads] : -INFINITY;
+#pragma unroll
+        for (uint32_t c = 0; c < AHEAD; ++c) {
+            const uint32_t b = bin_of(bins, z[c]) / 4;
+            if (b >= kCoarse) continue;
+            atomicAdd(&s.bin_count[b], 1u);
+            if (by_mass)  // (a lower bound of what the bins hold: fp32 will do, a little less of it)
+                atomicAdd((unsigned long long *)&s.bin_mass[b],
+                          (unsigned long long)(exp2f((float)(((double)z[c] - (double)bins.top) * row.scale)) * (float)(unit * 0.9999)));
         }
-        s.pick = min(b, kBins - 1);
-        s.pick_count = c;
     }
     __syncthreads();
-    const uint32_t last = s.pick;
-    if (s.pick_count > kMaxHot) return false;
-    // their reads, by index
-    for (uint32_t h = wave; h < halves; h += kWaves) {
-        const uint64_t m = __ballot(bin_of(bins, groups[h * 64 + lane]) <= last);
-        if (lane == 0) s.hot[h] = (uint16_t)__popcll(m);
-    }
+    // the first bin with groups for k, or weights for p, but none beyond `least`
+    const uint32_t c = threadIdx.x < kCoarse ? s.bin_count[threadIdx.x] : 0;
+    const uint64_t m = threadIdx.x < kCoarse ? s.bin_mass[threadIdx.x] : 0;
+    uint32_t counts;
+    uint64_t masses;
+    const uint32_t c0 = block_scan(c, s.count, counts);
+    const uint64_t m0 = by_mass ? block_scan(m, s.large, masses) : 0;
+    const bool enough = threadIdx.x >= least || (row.k ? c0 + c >= row.k : by_mass && (double)(m0 + m) >= row.top_p * all * unit);
+    last = min(0xFFFFFFFFu - block_max(enough ? 0xFFFFFFFFu - threadIdx.x : 0, s.other), kCoarse - 1);
+    if (threadIdx.x == last) s.pick_count = c0 + c;
     __syncthreads();
-    constexpr uint32_t EACH = 4;  // halves, and candidates, of a thread
-    const uint32_t mine0 = threadIdx.x * EACH;
-    uint32_t mine[EACH], sum = 0, total;
+    const uint32_t hot = s.pick_count;
+    if (hot > kMaxHot) return Reads{(p.vocab + W - 1) / W, true};
+    for (uint32_t h0 = wave; h0 < halves; h0 += AHEAD * kWaves) {
+        float z[AHEAD];
 #pragma unroll
-    for (uint32_t c = 0; c < EACH; ++c) {
-        mine[c] = mine0 + c < halves ? s.hot[mine0 + c] : 0;
-        sum += mine[c];
-    }
-    uint32_t before = block_scan(sum, s.count, total);
+        for (uint32_t c = 0; c < AHEAD; ++c) z[c] = h0 + c * kWaves < halves ? groups[(h0 + c * kWaves) * 64 + lane] : -INFINITY;
 #pragma unroll
-    for (uint32_t c = 0; c < EACH; ++c) {
-        if (mine0 + c < halves) s.hot[mine0 + c] = (uint16_t)before;
-        before += mine[c];
+        for (uint32_t c = 0; c < AHEAD; ++c) {
+            const uint64_t on = __ballot(bin_of(bins, z[c]) / 4 <= last);
+            if (lane == 0 && h0 + c * kWaves < halves) s.hot[h0 + c * kWaves] = on;
+        }
     }
     __syncthreads();
-    for (uint32_t h = wave; h < halves; h += kWaves) {
-        const bool on = bin_of(bins, groups[h * 64 + lane]) <= last;
-        const uint64_t m = __ballot(on);
-        const uint32_t count = __popcll(m), rank = __popcll(m & ((1ull << lane) - 1));
-        if (on)
+    constexpr uint32_t EACH = 2 * kMaxVocab / kSegment / kThreads;
+    uint64_t mine[EACH];
+    uint32_t sum = 0, total;
 #pragma unroll
-            for (uint32_t q = 0; q < READS; ++q)
-                s.reads[s.hot[h] * READS + q * count + rank] = h * (kSegment / 2) + (q * 64 + lane) * W;
+    for (uint32_t i = 0; i < EACH; ++i) {
+        const uint32_t h = threadIdx.x * EACH + i;
+        mine[i] = h < halves ? s.hot[h] : 0;
+        sum += __popcll(mine[i]);
+    }
+    uint32_t at = block_scan(sum, s.count, total);
+    __syncthreads();  // (s.reads takes the place of s.hot)
+    // a thread writes the reads of its own half segments: few of them hold any
+#pragma unroll
+    for (uint32_t i = 0; i < EACH; ++i) {
+        const uint32_t h = threadIdx.x * EACH + i, n = __popcll(mine[i]);
+        uint32_t rank = 0;
+        for (uint64_t m64 = mine[i]; m64; m64 &= m64 - 1, ++rank) {
+            const uint32_t l = (uint32_t)__ffsll((unsigned long long)m64) - 1;
+#pragma unroll
+            for (uint32_t q = 0; q < READS; ++q) s.reads[at * READS + q * n + rank] = h * (kSegment / 2) + (q * 64 + l) * W;
+        }
+        at += n;
     }
     __syncthreads();
-    // their tokens in the bins, by index
-    const uint32_t reads = total * READS;
-    uint32_t n = 0;
-    for (uint32_t j0 = 0; j0 < reads; j0 += kThreads) {
-        const uint32_t j = j0 + threadIdx.x;
-        const uint32_t i = j < reads ? s.reads[j] : p.vocab;
+    return Reads{total * READS, false};
+}
+
+// Tokens of the bins [from, to] into s.tokens, by index; false if there are too many.
+template <bool F32>
+__device__ inline bool collect(const SampleParams &p, uint64_t at, const Bins &bins, const Reads &q, uint32_t from, uint32_t to,
+                               uint32_t &n, Shared &s) {
+    constexpr uint32_t W = F32 ? 4 : 8;
+    n = 0;
+    for (uint32_t j0 = 0; j0 < q.count; j0 += kThreads) {
+        const uint32_t j = j0 + threadIdx.x, i = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
         float v[W];
+        read_values<F32>(p, at, i, v);
         uint32_t have = 0;
-        if (j < reads) {
-            read_values<F32>(p, at, i, v);
 #pragma unroll
-            for (uint32_t c = 0; c < W; ++c) have += v[c] > -INFINITY && bin_of(bins, v[c]) <= last;
+        for (uint32_t c = 0; c < W; ++c) {
+            const uint32_t b = bin_of(bins, v[c]);
+            have += v[c] > -INFINITY && b >= from && b <= to;
         }
         uint32_t found, place = n + block_scan(have, s.count, found);
         n += found;
         if (n > kMaxCandidates) return false;
         if (have)
 #pragma unroll
-            for (uint32_t c = 0; c < W; ++c)
-                if (v[c] > -INFINITY && bin_of(bins, v[c]) <= last)
+            for (uint32_t c = 0; c < W; ++c) {
+                const uint32_t b = bin_of(bins, v[c]);
+                if (v[c] > -INFINITY && b >= from && b <= to)
                     s.tokens[place++] = (uint64_t)ordered(v[c]) << 32 | (0xFFFFFFFFu - (i + c));
+            }
     }
     __syncthreads();
-    const bool closed = last >= least;  // nothing outside is kept
-    if (row.k && n < row.k && !closed) return false;
-    // in their order (s.reads is done with)
+    return true;
+}
+
+// s.tokens into s.sorted, the order of the filters.
+__device__ inline void sort_tokens(uint32_t n, Shared &s) {
     uint32_t n2 = 64;
     while (n2 < n) n2 *= 2;
     for (uint32_t i = threadIdx.x; i < n2; i += kThreads) s.sorted[i] = i < n ? s.tokens[i] : 0;
@@ -538,53 +548,21 @@ __device__ inline bool by_candidates(const SampleParams &p, uint32_t r, const Ro
             }
             __syncthreads();
         }
-    // the sums before each, and how many are kept
-    double e[EACH], part = 0, whole;
-#pragma unroll
-    for (uint32_t c = 0; c < EACH; ++c) {
-        const uint32_t i = mine0 + c;
-        e[c] = i < n ? weight(unordered((uint32_t)(s.sorted[i] >> 32)), top, row.scale) : 0.0;
-        part += e[c];
-    }
-    double run = block_scan(part, s.mass, whole);
-    const uint32_t limit = row.k ? min(row.k, n) : n;
-    if (row.k) {
-        double x = run;
-#pragma unroll
-        for (uint32_t c = 0; c < EACH; ++c) {
-            x += e[c];
-            if (mine0 + c == limit - 1) s.total = x;
-        }
-        __syncthreads();
-    }
-    const double reach = row.top_p * (row.k ? s.total : all);
-    uint32_t kept = 0;
-#pragma unroll
-    for (uint32_t c = 0; c < EACH; ++c) {
-        const uint32_t i = mine0 + c;
-        kept += i < limit && (i == 0 || ((row.top_p >= 1 || run < reach) && e[c] >= row.min_p));
-        run += e[c];
-    }
-    uint32_t keep;
-    block_scan(kept, s.count, keep);
-    if (keep == n && !closed && !(row.k && n >= row.k)) return false;
-    const uint64_t border = s.sorted[keep - 1];
-    // the draw, by index
-    part = 0;
-#pragma unroll
-    for (uint32_t c = 0; c < EACH; ++c) {
-        const uint32_t i = mine0 + c;
-        const uint64_t x = i < n ? s.tokens[i] : 0;
-        e[c] = x >= border ? weight(unordered((uint32_t)(x >> 32)), top, row.scale) : 0.0;
-        part += e[c];
-    }
-    run = block_scan(part, s.mass, whole);
-    const double want = uniform_of(p, r) * whole;
-    // the first whose running sum exceeds it, as a maximum of complements; of the last with any, if rounding leaves none
+}
+__device__ inline double sorted_weight(uint64_t x, float top, double scale) {
+    return weight(unordered((uint32_t)(x >> 32)), top, scale);
+}
+
+constexpr uint32_t kOwn = kMaxCandidates / kThreads;  // tokens of a thread, one after another
+
+// The first place, by index, at which the running sum of e[] over threads and their N values exceeds the draw; of the
+// last with any, if rounding leaves none.
+template <uint32_t N>
+__device__ inline uint32_t first_over(const double (&e)[N], double run, double want, Shared &s) {
     uint32_t first = 0, any = 0;
 #pragma unroll
-    for (uint32_t c = 0; c < EACH; ++c) {
-        const uint32_t i = mine0 + c;
+    for (uint32_t c = 0; c < N; ++c) {
+        const uint32_t i = threadIdx.x * N + c;
         run += e[c];
         if (e[c] > 0) {
             any = i + 1;
@@ -593,10 +571,154 @@ __device__ inline bool by_candidates(const SampleParams &p, uint32_t r, const Ro
     }
     first = block_max(first, s.count);
     any = block_max(any, s.other);
-    if (threadIdx.x == 0) {
-        const uint32_t i = first ? 0xFFFFFFFFu - first : any - 1;
-        finish(p, r, 0xFFFFFFFFu - (uint32_t)s.tokens[i], top, row.heat, all);
+    return first ? 0xFFFFFFFFu - first : any - 1;
+}
+
+// Rows with top-k: the tokens of the first bins that hold k, sorted.
+template <bool F32>
+__device__ inline bool by_sorting(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all,
+                                  uint32_t least, Shared &s) {
+    uint32_t last, n;
+    const float top = bins.top;
+    const Reads q = choose_reads<F32>(p, r, row, bins, all, least, last, s);
+    if (q.all || !collect<F32>(p, (uint64_t)r * p.stride, bins, q, 0, last * 4 + 3, n, s)) return false;
+    sort_tokens(n, s);
+    // the sums before each, and how many are kept
+    double e[kOwn], part = 0, whole;
+#pragma unroll
+    for (uint32_t c = 0; c < kOwn; ++c) {
+        const uint32_t i = threadIdx.x * kOwn + c;
+        e[c] = i < n ? sorted_weight(s.sorted[i], top, row.scale) : 0.0;
+        part += e[c];
     }
+    double run = block_scan(part, s.mass, whole);
+    const uint32_t limit = min(row.k, n);
+    double x = run;
+#pragma unroll
+    for (uint32_t c = 0; c < kOwn; ++c) {
+        x += e[c];
+        if (threadIdx.x * kOwn + c == limit - 1) s.total = x;
+    }
+    __syncthreads();
+    const double reach = row.top_p * s.total;
+    uint32_t kept = 0, keep;
+#pragma unroll
+    for (uint32_t c = 0; c < kOwn; ++c) {
+        const uint32_t i = threadIdx.x * kOwn + c;
+        kept += i < limit && (i == 0 || ((row.top_p >= 1 || run < reach) && e[c] >= row.min_p));
+        run += e[c];
+    }
+    block_scan(kept, s.count, keep);
+    const uint64_t border = s.sorted[keep - 1];
+    part = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < kOwn; ++c) {
+        const uint32_t i = threadIdx.x * kOwn + c;
+        const uint64_t t = i < n ? s.tokens[i] : 0;
+        e[c] = t >= border ? sorted_weight(t, top, row.scale) : 0.0;
+        part += e[c];
+    }
+    run = block_scan(part, s.mass, whole);
+    const uint32_t i = first_over(e, run, uniform_of(p, r) * whole, s);
+    if (threadIdx.x == 0) finish(p, r, 0xFFFFFFFFu - (uint32_t)s.tokens[i], top, row.heat, all);
+    return true;
+}
+
+// Rows with top-p or min-p alone: the bin in which top-p ends, from a histogram
+// of sums, the tokens of that one bin sorted, then the kept ones' sums by runs.
+template <bool F32>
+__device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all, uint32_t least,
+                               Shared &s) {
+    constexpr uint32_t W = F32 ? 4 : 8;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t at = (uint64_t)r * p.stride;
+    const float top = bins.top;
+    uint32_t last;
+    Reads q = choose_reads<F32>(p, r, row, bins, all, least, last, s);
+    if ((q.count + 63) / 64 > kMaxCells) return false;
+    const uint32_t end = (q.all ? least : last) * 4 + 3;  // bins that the reads hold whole
+    const double unit = unit_of(all);
+    uint64_t border = 0;
+    if (row.top_p < 1) {
+        for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.bin_mass[i] = 0;
+        __syncthreads();
+        uint32_t tops = 0;
+        for (uint32_t j = threadIdx.x; j < q.count; j += kThreads) {
+            float v[W];
+            read_values<F32>(p, at, read_at<F32>(s, q, j), v);
+#pragma unroll
+            for (uint32_t c = 0; c < W; ++c) {
+                const uint32_t b = bin_of(bins, v[c]);
+                if (v[c] == top) ++tops;  // (equal ones would meet at one address)
+                else if (b <= end)
+                    atomicAdd((unsigned long long *)&s.bin_mass[b], (unsigned long long)(weight(v[c], top, row.scale) * unit + 0.5));
+            }
+        }
+        uint32_t all_tops;
+        block_scan(tops, s.count, all_tops);
+        const uint64_t m = s.bin_mass[threadIdx.x] + (threadIdx.x == 0 ? (uint64_t)(all_tops * unit) : 0);
+        uint64_t masses;
+        const uint64_t m0 = block_scan(m, s.large, masses);
+        const double reach = row.top_p * all;
+        const uint32_t bin = 0xFFFFFFFFu - block_max(m && (double)(m0 + m) >= reach * unit ? 0xFFFFFFFFu - threadIdx.x : 0, s.other);
+        if (bin < kBins) {
+            if (threadIdx.x == bin) s.pick_mass = m0;
+            uint32_t n;
+            if (!collect<F32>(p, at, bins, q, bin, bin, n, s)) return false;
+            sort_tokens(n, s);
+            double e[kOwn], part = 0, whole;
+#pragma unroll
+            for (uint32_t c = 0; c < kOwn; ++c) {
+                const uint32_t i = threadIdx.x * kOwn + c;
+                e[c] = i < n ? sorted_weight(s.sorted[i], top, row.scale) : 0.0;
+                part += e[c];
+            }
+            double run = (double)s.pick_mass / unit + block_scan(part, s.mass, whole);
+            uint32_t kept = 0, keep;
+#pragma unroll
+            for (uint32_t c = 0; c < kOwn; ++c) {
+                kept += threadIdx.x * kOwn + c < n && run < reach;
+                run += e[c];
+            }
+            block_scan(kept, s.count, keep);
+            border = s.sorted[max(keep, 1u) - 1];
+        } else if (!q.all && last < least) {
+            return false;
+        }
+        __syncthreads();  // (s.cell takes the place of s.tokens)
+    }
+    // the kept ones' sums by runs of 64 reads
+    auto kept = [&](uint32_t j, double e[W]) __attribute__((always_inline)) {
+        const uint32_t i = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
+        float v[W];
+        read_values<F32>(p, at, i, v);
+        double sum = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < W; ++c) {
+            const uint64_t t = (uint64_t)ordered(v[c]) << 32 | (0xFFFFFFFFu - (i + c));
+            const double x = t >= border ? weight(v[c], top, row.scale) : 0.0;
+            e[c] = x >= row.min_p || v[c] == top ? x : 0.0;
+            sum += e[c];
+        }
+        return sum;
+    };
+    double e[W];
+    for (uint32_t j0 = 0; j0 < q.count; j0 += kThreads) {
+        const double sum = wave_sum(kept(j0 + threadIdx.x, e));
+        if (lane == 0) s.cell[j0 / 64 + wave] = sum;
+    }
+    __syncthreads();
+    const double mine[1] = {threadIdx.x < (q.count + 63) / 64 ? s.cell[threadIdx.x] : 0.0};
+    double whole;
+    double run = block_scan(mine[0], s.mass, whole);
+    const double want = uniform_of(p, r) * whole;
+    const uint32_t cell = first_over(mine, run, want, s);
+    if (threadIdx.x == cell) s.total = run;
+    const uint32_t j = cell * 64 + lane;
+    const double sum = kept(threadIdx.x < 64 ? j : q.count, e);
+    run = block_scan(sum, s.mass, whole) + s.total;
+    const uint32_t place = first_over(e, run, want, s);
+    if (threadIdx.x == 0) finish(p, r, read_at<F32>(s, q, cell * 64 + place / W) + place % W, top, row.heat, all);
     return true;
 }
 
@@ -688,28 +810,25 @@ __global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
         return;
     }
     if (top < INFINITY) {
-        // The groups' largest values in bins.  Tokens that weigh less than 2^-80 of
-        // the largest change no sum in 64 bits and are left out.
+        // Tokens that weigh less than 2^-80 of the largest change no sum in 64 bits and are left out.
         Bins bins;
         bins.top = top;
         bins.floor = (float)((double)top - 80.0 / row.scale);
         bins.low = fmaxf(unordered(lowest), bins.floor);
         const float range = top - bins.low;
         bins.inv = range > 0 ? (kBins - 1.01f) / range : 0.0f;
-        for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.bin_count[i] = 0;
-        __syncthreads();
-        const float *groups = p.groups + (uint64_t)r * p.segments * 128;
-        for (uint32_t i = threadIdx.x; i < p.segments * 128; i += kThreads) {
-            const uint32_t b = bin_of(bins, groups[i]);
-            if (b < kBins) atomicAdd(&s.bin_count[b], 1u);
+        // the last coarse bin with tokens that min_p keeps (top-p of the first k needs the sum of the others too)
+        uint32_t least = kCoarse - 1;
+        if (row.min_p > 0 && !(row.k && row.top_p < 1)) {
+            const double z = (double)top + log(row.min_p) * row.heat * 1.000001 - fabs((double)top) * 1e-6;
+            least = min(bin_of(bins, (float)z) / 4 + 1, kCoarse - 1);
         }
-        __syncthreads();
-        if (by_candidates<F32>(p, r, row, bins, all, row.k ? row.k : 512, s)) return;
+        if (row.k ? by_sorting<F32>(p, r, row, bins, all, least, s) : by_sums<F32>(p, r, row, bins, all, least, s)) return;
         __syncthreads();
     } else {  // the infinite ones share alike
         double n = 0;
         for (uint32_t i = threadIdx.x; i < p.vocab; i += kThreads) n += value(p.logits, at + i, F32) == INFINITY;
-        all = block_sum(n, s.mass);
+        block_scan(n, s.mass, all);
         __syncthreads();
     }
     by_histograms(p, r, row, top, all, s);
