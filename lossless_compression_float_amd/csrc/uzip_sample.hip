@@ -88,15 +88,54 @@ __device__ inline double weight(float z, float top, double scale) {
     return z == top ? 1.0 : x > -1000.0 ? exp2_low(x) : 0.0;
 }
 
+// A value of another lane by DPP, zero where there is none.
+template <int CTRL, int ROWS = 15, class T>
+__device__ inline T moved(T v) {
+    if constexpr (sizeof(T) == 8) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint64_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 15, false);
+        const uint64_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 15, false);
+        return __builtin_bit_cast(T, hi << 32 | lo);
+    } else {
+        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 15, false));
+    }
+}
+constexpr int kRowShift = 0x110, kWaveShift1 = 0x138, kRowLast = 0x142, kHalfLast = 0x143;
 template <class T>
-__device__ inline T wave_sum(T v) {
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
+__device__ inline T lane_of(T v, uint32_t lane) {  // (lane uniform)
+    if constexpr (sizeof(T) == 8) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)u, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+        return __builtin_bit_cast(T, hi << 32 | lo);
+    } else {
+        return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+    }
 }
-__device__ inline uint32_t wave_max(uint32_t v) {
-    for (int d = 1; d < 64; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
-    return v;
+struct Sum {
+    template <class T>
+    __device__ static T of(T a, T b) { return a + b; }
+};
+struct Max {
+    template <class T>
+    __device__ static T of(T a, T b) { return a > b ? a : b; }
+};
+// Of the lanes up to this one (zero is the operation's neutral value).
+template <class OP, class T>
+__device__ inline T row_scan(T v) {  // within 16 lanes
+    v = OP::of(moved<kRowShift + 1>(v), v);
+    v = OP::of(moved<kRowShift + 2>(v), v);
+    v = OP::of(moved<kRowShift + 4>(v), v);
+    return OP::of(moved<kRowShift + 8>(v), v);
 }
+template <class OP, class T>
+__device__ inline T wave_scan(T v) {
+    v = row_scan<OP>(v);
+    v = OP::of(moved<kRowLast, 10>(v), v);
+    return OP::of(moved<kHalfLast, 12>(v), v);
+}
+template <class T>
+__device__ inline T wave_sum(T v) { return lane_of(wave_scan<Sum>(v), 63); }
+__device__ inline uint32_t wave_max(uint32_t v) { return lane_of(wave_scan<Max>(v), 63); }
 
 constexpr uint32_t kMaxHot = 2048;         // groups that are read again apart from the others
 constexpr uint32_t kMaxCandidates = 4096;  // tokens that are sorted
@@ -122,41 +161,25 @@ struct Shared {
     uint64_t sorted[kMaxCandidates];
 };
 
-template <class T>
-__device__ inline T shuffle_up(T v, int d) {
-    if constexpr (sizeof(T) == 8 && !__is_same(T, double)) return (T)__shfl_up((unsigned long long)v, d);
-    else return __shfl_up(v, d);
-}
 // The sum over the threads before this one, in a fixed order, and over all.
 template <class T>
 __device__ inline T block_scan(T v, T *lds, T &total) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    T x = v;
-    for (int d = 1; d < 64; d <<= 1) {
-        const T y = shuffle_up(x, d);
-        if (lane >= (uint32_t)d) x += y;
-    }
-    const T upto = shuffle_up(x, 1);
+    const T x = wave_scan<Sum>(v), upto = moved<kWaveShift1>(x);
     __syncthreads();
     if (lane == 63) lds[wave] = x;
     __syncthreads();
-    T before = 0;
-    total = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < kWaves; ++i) {
-        if (i < wave) before += lds[i];
-        total += lds[i];
-    }
-    return before + (lane ? upto : T(0));
+    const T waves = row_scan<Sum>(lds[lane & (kWaves - 1)]);
+    total = lane_of(waves, kWaves - 1);
+    const uint32_t w = __builtin_amdgcn_readfirstlane(wave);
+    return w ? lane_of(waves, w - 1) + upto : upto;
 }
 __device__ inline uint32_t block_max(uint32_t v, uint32_t *lds) {
     v = wave_max(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-#pragma unroll
-    for (uint32_t i = 0; i < kWaves; ++i) v = max(v, lds[i]);
-    return v;
+    return lane_of(row_scan<Max>(lds[threadIdx.x & (kWaves - 1)]), kWaves - 1);
 }
 
 // Fixed point for sums of at most `all`: 61 to 62 bits of it.
@@ -200,7 +223,7 @@ __device__ inline Border find_border(const SampleParams &p, uint64_t at, float t
         const uint32_t c0 = have_count + block_scan(c, s.count, counts);
         const uint64_t m0 = have_mass + block_scan(m, s.large, masses);
         const bool enough = c && (by_count ? c0 + c >= count : (double)(m0 + m) >= mass * unit);
-        const uint32_t first = 0xFFFFFFFFu - block_max(enough ? 0xFFFFFFFFu - threadIdx.x : 0, s.other);
+        const uint32_t first = ~0u - block_max(enough ? 0xFFFFFFFFu - threadIdx.x : 0, s.other);
         if (threadIdx.x == min(first, 255u)) s.pick = prefix | b << shift, s.pick_count = c0, s.pick_mass = m0;
         __syncthreads();
         prefix = s.pick;
@@ -221,11 +244,9 @@ __device__ inline Border find_border(const SampleParams &p, uint64_t at, float t
     return out;
 }
 
-__device__ inline void finish(const SampleParams &p, uint32_t r, uint32_t token, float top, double heat, double all) {
+__device__ inline void finish(const SampleParams &p, uint32_t r, uint32_t token, float z, float top, double heat, double all) {
     p.token[r] = token;
-    if (!p.logprob) return;
-    const float z = value(p.logits, (uint64_t)r * p.stride + token, p.f32);
-    p.logprob[r] = (float)((z == top ? 0.0 : ((double)z - (double)top) / heat) - log(all));
+    if (p.logprob) p.logprob[r] = (float)((z == top ? 0.0 : ((double)z - (double)top) / heat) - log(all));
 }
 __device__ inline double uniform_of(const SampleParams &p, uint32_t r) {
     return p.u_f64 ? static_cast<const double *>(p.u)[r] : (double)static_cast<const float *>(p.u)[r];
@@ -309,11 +330,7 @@ __device__ inline void by_histograms(const SampleParams &p, uint32_t r, const Ro
             e = each;
         }
         seen += __popcll(m);
-        double x = e;
-        for (int d = 1; d < 64; d <<= 1) {
-            const double y = __shfl_up(x, d);
-            if (lane >= (uint32_t)d) x += y;
-        }
+        const double x = wave_scan<Sum>(e);
         const uint64_t some = __ballot(e > 0), over = __ballot(e > 0 && running + x > want);
         if (over) {
             token = i0 + (uint32_t)__ffsll((unsigned long long)over) - 1;
@@ -321,9 +338,9 @@ __device__ inline void by_histograms(const SampleParams &p, uint32_t r, const Ro
         } else if (some) {
             token = i0 + 63 - (uint32_t)__clzll((long long)some);  // the last so far
         }
-        running += __shfl(x, 63);
+        running += lane_of(x, 63);
     }
-    if (lane == 0) finish(p, r, token, top, row.heat, all);
+    if (lane == 0) finish(p, r, token, value(p.logits, at + token, p.f32), top, row.heat, all);
 }
 
 // ---- the survey ---------------------------------------------------------------------
@@ -377,10 +394,8 @@ __global__ __launch_bounds__(256) void k_survey(SampleParams p) {
     }
     float top = fmaxf(group[0], group[1]);
     float low = fminf(group[0] > -INFINITY ? group[0] : INFINITY, group[1] > -INFINITY ? group[1] : INFINITY);
-    for (int d = 1; d < 64; d <<= 1) {
-        top = fmaxf(top, __shfl_xor(top, d));
-        low = fminf(low, __shfl_xor(low, d));
-    }
+    top = unordered(wave_max(ordered(top)));
+    low = unordered(~wave_max(~ordered(low)));
     const double scale = row_of(p, r).scale;
     double sum = 0;
     if (top > -INFINITY) {
@@ -424,30 +439,40 @@ __device__ inline uint32_t read_at(const Shared &s, const Reads &q, uint32_t j) 
 
 // The first bins whose groups (by their largest values) hold k tokens, or
 // weigh enough for top-p, none beyond `least`, and the reads of those groups.
+constexpr uint32_t kAhead = 8;  // loads on their way
+struct Groups {  // this lane's of the first 128 half segments: of kAhead times a wave each
+    float z[kAhead];
+};
+__device__ inline void load_groups(Groups &g, const float *groups, uint32_t halves, uint32_t h0) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (uint32_t c = 0; c < kAhead; ++c) {
+        const uint32_t h = h0 + c * kWaves + wave;
+        g.z[c] = h < halves ? groups[h * 64 + lane] : -INFINITY;
+    }
+}
 template <bool F32>
 __device__ inline Reads choose_reads(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all,
-                                     uint32_t least, uint32_t &last, Shared &s) {
+                                     uint32_t least, Groups &g, uint32_t &last, Shared &s) {
     constexpr uint32_t W = F32 ? 4 : 8, READS = kGroup / W;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float *groups = p.groups + (uint64_t)r * p.segments * 128;
     const uint32_t halves = p.segments * 2;
-    for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.bin_count[i] = 0, s.bin_mass[i] = 0;
-    __syncthreads();
     const bool by_mass = !row.k && row.top_p < 1;
     const double unit = unit_of(all);
-    constexpr uint32_t AHEAD = 8;  // loads on their way
-    for (uint32_t i0 = threadIdx.x; i0 < halves * 64; i0 += AHEAD * kThreads) {
-        float z[AHEAD];
+    s.bin_count[threadIdx.x] = 0;
+    s.bin_mass[threadIdx.x] = 0;
+    __syncthreads();
+    for (uint32_t h0 = 0; h0 < halves; h0 += kAhead * kWaves) {
+        if (h0) load_groups(g, groups, halves, h0);
 #pragma unroll
-        for (uint32_t c = 0; c < AHEAD; ++c) z[c] = i0 + c * kThreads < halves * 64 ? groups[i0 + c * kThreads] : -INFINITY;
-#pragma unroll
-        for (uint32_t c = 0; c < AHEAD; ++c) {
-            const uint32_t b = bin_of(bins, z[c]) / 4;
+        for (uint32_t c = 0; c < kAhead; ++c) {
+            const uint32_t b = bin_of(bins, g.z[c]) / 4;
             if (b >= kCoarse) continue;
             atomicAdd(&s.bin_count[b], 1u);
             if (by_mass)  // (a lower bound of what the bins hold: fp32 will do, a little less of it)
                 atomicAdd((unsigned long long *)&s.bin_mass[b],
-                          (unsigned long long)(exp2f((float)(((double)z[c] - (double)bins.top) * row.scale)) * (float)(unit * 0.9999)));
+                          (unsigned long long)(exp2f((float)(((double)g.z[c] - (double)bins.top) * row.scale)) * (float)(unit * 0.9999)));
         }
     }
     __syncthreads();
@@ -464,32 +489,32 @@ __device__ inline Reads choose_reads(const SampleParams &p, uint32_t r, const Ro
     __syncthreads();
     const uint32_t hot = s.pick_count;
     if (hot > kMaxHot) return Reads{(p.vocab + W - 1) / W, true};
-    for (uint32_t h0 = wave; h0 < halves; h0 += AHEAD * kWaves) {
-        float z[AHEAD];
+    for (uint32_t h0 = 0; h0 < halves; h0 += kAhead * kWaves) {
+        if (halves > kAhead * kWaves) load_groups(g, groups, halves, h0);
 #pragma unroll
-        for (uint32_t c = 0; c < AHEAD; ++c) z[c] = h0 + c * kWaves < halves ? groups[(h0 + c * kWaves) * 64 + lane] : -INFINITY;
-#pragma unroll
-        for (uint32_t c = 0; c < AHEAD; ++c) {
-            const uint64_t on = __ballot(bin_of(bins, z[c]) / 4 <= last);
-            if (lane == 0 && h0 + c * kWaves < halves) s.hot[h0 + c * kWaves] = on;
+        for (uint32_t c = 0; c < kAhead; ++c) {
+            const uint64_t on = __ballot(bin_of(bins, g.z[c]) / 4 <= last);
+            const uint32_t h = h0 + c * kWaves + wave;
+            if (lane == 0 && h < halves) s.hot[h] = on;
         }
     }
     __syncthreads();
     constexpr uint32_t EACH = 2 * kMaxVocab / kSegment / kThreads;
     uint64_t mine[EACH];
     uint32_t sum = 0, total;
+    // (a half a thread where there are no more, so that they share the work)
+    auto half_of = [&](uint32_t i) { return halves > kThreads ? threadIdx.x * EACH + i : threadIdx.x + i * kThreads; };
 #pragma unroll
     for (uint32_t i = 0; i < EACH; ++i) {
-        const uint32_t h = threadIdx.x * EACH + i;
+        const uint32_t h = half_of(i);
         mine[i] = h < halves ? s.hot[h] : 0;
         sum += __popcll(mine[i]);
     }
     uint32_t at = block_scan(sum, s.count, total);
     __syncthreads();  // (s.reads takes the place of s.hot)
-    // a thread writes the reads of its own half segments: few of them hold any
 #pragma unroll
     for (uint32_t i = 0; i < EACH; ++i) {
-        const uint32_t h = threadIdx.x * EACH + i, n = __popcll(mine[i]);
+        const uint32_t h = half_of(i), n = __popcll(mine[i]);
         uint32_t rank = 0;
         for (uint64_t m64 = mine[i]; m64; m64 &= m64 - 1, ++rank) {
             const uint32_t l = (uint32_t)__ffsll((unsigned long long)m64) - 1;
@@ -533,9 +558,54 @@ __device__ inline bool collect(const SampleParams &p, uint64_t at, const Bins &b
     return true;
 }
 
-// s.tokens into s.sorted, the order of the filters.
+// The same of one bin, in any order.
+template <bool F32>
+__device__ inline bool collect_bin(const SampleParams &p, uint64_t at, const Bins &bins, const Reads &q, uint32_t bin, uint32_t &n,
+                                   Shared &s) {
+    constexpr uint32_t W = F32 ? 4 : 8;
+    if (threadIdx.x == 0) s.pick_count = 0;
+    __syncthreads();
+    for (uint32_t j0 = 0; j0 < q.count; j0 += 4 * kThreads) {
+        float v[4][W];
+        uint32_t first[4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) {
+            const uint32_t j = j0 + u * kThreads + threadIdx.x;
+            first[u] = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
+            read_values<F32>(p, at, first[u], v[u]);
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u)
+#pragma unroll
+            for (uint32_t c = 0; c < W; ++c)
+                if (v[u][c] > -INFINITY && bin_of(bins, v[u][c]) == bin) {
+                    const uint32_t place = atomicAdd(&s.pick_count, 1u);
+                    if (place < kMaxCandidates) s.tokens[place] = (uint64_t)ordered(v[u][c]) << 32 | (0xFFFFFFFFu - (first[u] + c));
+                }
+    }
+    __syncthreads();
+    n = s.pick_count;
+    return n <= kMaxCandidates;
+}
+
+// s.tokens into s.sorted, the order of the filters.  Few are ranked by counting.
 __device__ inline void sort_tokens(uint32_t n, Shared &s) {
-    uint32_t n2 = 64;
+    if (n <= 256) {
+        uint32_t wide = 64;
+        while (wide < n) wide *= 2;
+        s.bin_count[threadIdx.x] = 0;
+        __syncthreads();
+        const uint32_t i = threadIdx.x & (wide - 1), parts = kThreads / wide;
+        const uint64_t mine = i < n ? s.tokens[i] : 0;
+        uint32_t above = 0;
+        for (uint32_t j = threadIdx.x / wide; j < n; j += parts) above += s.tokens[j] > mine;
+        if (i < n) atomicAdd(&s.bin_count[i], above);
+        __syncthreads();
+        if (threadIdx.x < n) s.sorted[s.bin_count[threadIdx.x]] = mine;
+        __syncthreads();
+        return;
+    }
+    uint32_t n2 = 512;
     while (n2 < n) n2 *= 2;
     for (uint32_t i = threadIdx.x; i < n2; i += kThreads) s.sorted[i] = i < n ? s.tokens[i] : 0;
     __syncthreads();
@@ -555,32 +625,44 @@ __device__ inline double sorted_weight(uint64_t x, float top, double scale) {
 
 constexpr uint32_t kOwn = kMaxCandidates / kThreads;  // tokens of a thread, one after another
 
-// The first place, by index, at which the running sum of e[] over threads and their N values exceeds the draw; of the
-// last with any, if rounding leaves none.
+// The first place, by index, at which the running sum of e[] over threads and
+// their N values exceeds the draw; of the last with any, if rounding leaves
+// none.  s.pick: set to kNone before the scan that gave `run`.
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 template <uint32_t N>
 __device__ inline uint32_t first_over(const double (&e)[N], double run, double want, Shared &s) {
-    uint32_t first = 0, any = 0;
+    double sum = run;
+#pragma unroll
+    for (uint32_t c = 0; c < N; ++c) {
+        const double before = sum;
+        sum += e[c];
+        if (sum > want && before <= want) atomicMin(&s.pick, threadIdx.x * N + c);
+    }
+    __syncthreads();
+    const uint32_t first = s.pick;
+    if (first != kNone) return first;
+    // (the sums of neighbouring threads need not meet exactly)
+    uint32_t over = 0, any = 0;
+    sum = run;
 #pragma unroll
     for (uint32_t c = 0; c < N; ++c) {
         const uint32_t i = threadIdx.x * N + c;
-        run += e[c];
-        if (e[c] > 0) {
-            any = i + 1;
-            if (run > want && !first) first = 0xFFFFFFFFu - i;
-        }
+        sum += e[c];
+        if (e[c] > 0) any = i + 1;
+        if (e[c] > 0 && sum > want && !over) over = kNone - i;
     }
-    first = block_max(first, s.count);
+    over = block_max(over, s.count);
     any = block_max(any, s.other);
-    return first ? 0xFFFFFFFFu - first : any - 1;
+    return over ? kNone - over : any - 1;
 }
 
 // Rows with top-k: the tokens of the first bins that hold k, sorted.
 template <bool F32>
 __device__ inline bool by_sorting(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all,
-                                  uint32_t least, Shared &s) {
+                                  uint32_t least, Groups &g, Shared &s) {
     uint32_t last, n;
     const float top = bins.top;
-    const Reads q = choose_reads<F32>(p, r, row, bins, all, least, last, s);
+    const Reads q = choose_reads<F32>(p, r, row, bins, all, least, g, last, s);
     if (q.all || !collect<F32>(p, (uint64_t)r * p.stride, bins, q, 0, last * 4 + 3, n, s)) return false;
     sort_tokens(n, s);
     // the sums before each, and how many are kept
@@ -618,9 +700,11 @@ __device__ inline bool by_sorting(const SampleParams &p, uint32_t r, const Row &
         e[c] = t >= border ? sorted_weight(t, top, row.scale) : 0.0;
         part += e[c];
     }
+    if (threadIdx.x == 0) s.pick = kNone;
     run = block_scan(part, s.mass, whole);
     const uint32_t i = first_over(e, run, uniform_of(p, r) * whole, s);
-    if (threadIdx.x == 0) finish(p, r, 0xFFFFFFFFu - (uint32_t)s.tokens[i], top, row.heat, all);
+    if (threadIdx.x == 0)
+        finish(p, r, kNone - (uint32_t)s.tokens[i], unordered((uint32_t)(s.tokens[i] >> 32)), top, row.heat, all);
     return true;
 }
 
@@ -628,13 +712,13 @@ __device__ inline bool by_sorting(const SampleParams &p, uint32_t r, const Row &
 // of sums, the tokens of that one bin sorted, then the kept ones' sums by runs.
 template <bool F32>
 __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all, uint32_t least,
-                               Shared &s) {
+                               Groups &g, Shared &s) {
     constexpr uint32_t W = F32 ? 4 : 8;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t at = (uint64_t)r * p.stride;
     const float top = bins.top;
     uint32_t last;
-    Reads q = choose_reads<F32>(p, r, row, bins, all, least, last, s);
+    Reads q = choose_reads<F32>(p, r, row, bins, all, least, g, last, s);
     if ((q.count + 63) / 64 > kMaxCells) return false;
     const uint32_t end = (q.all ? least : last) * 4 + 3;  // bins that the reads hold whole
     const double unit = unit_of(all);
@@ -643,16 +727,23 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
         for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.bin_mass[i] = 0;
         __syncthreads();
         uint32_t tops = 0;
-        for (uint32_t j = threadIdx.x; j < q.count; j += kThreads) {
-            float v[W];
-            read_values<F32>(p, at, read_at<F32>(s, q, j), v);
+        for (uint32_t j0 = threadIdx.x; j0 < q.count; j0 += 4 * kThreads) {
+            float v[4][W];
 #pragma unroll
-            for (uint32_t c = 0; c < W; ++c) {
-                const uint32_t b = bin_of(bins, v[c]);
-                if (v[c] == top) ++tops;  // (equal ones would meet at one address)
-                else if (b <= end)
-                    atomicAdd((unsigned long long *)&s.bin_mass[b], (unsigned long long)(weight(v[c], top, row.scale) * unit + 0.5));
+            for (uint32_t u = 0; u < 4; ++u) {
+                const uint32_t j = j0 + u * kThreads;
+                read_values<F32>(p, at, j < q.count ? read_at<F32>(s, q, j) : p.vocab, v[u]);
             }
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u)
+#pragma unroll
+                for (uint32_t c = 0; c < W; ++c) {
+                    const uint32_t b = bin_of(bins, v[u][c]);
+                    if (v[u][c] == top) ++tops;  // (equal ones would meet at one address)
+                    else if (b <= end)
+                        atomicAdd((unsigned long long *)&s.bin_mass[b],
+                                  (unsigned long long)(weight(v[u][c], top, row.scale) * unit + 0.5));
+                }
         }
         uint32_t all_tops;
         block_scan(tops, s.count, all_tops);
@@ -664,7 +755,7 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
         if (bin < kBins) {
             if (threadIdx.x == bin) s.pick_mass = m0;
             uint32_t n;
-            if (!collect<F32>(p, at, bins, q, bin, bin, n, s)) return false;
+            if (!collect_bin<F32>(p, at, bins, q, bin, n, s)) return false;
             sort_tokens(n, s);
             double e[kOwn], part = 0, whole;
 #pragma unroll
@@ -688,14 +779,11 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
         __syncthreads();  // (s.cell takes the place of s.tokens)
     }
     // the kept ones' sums by runs of 64 reads
-    auto kept = [&](uint32_t j, double e[W]) __attribute__((always_inline)) {
-        const uint32_t i = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
-        float v[W];
-        read_values<F32>(p, at, i, v);
+    auto kept = [&](uint32_t i, const float (&v)[W], double (&e)[W]) __attribute__((always_inline)) {
         double sum = 0;
 #pragma unroll
         for (uint32_t c = 0; c < W; ++c) {
-            const uint64_t t = (uint64_t)ordered(v[c]) << 32 | (0xFFFFFFFFu - (i + c));
+            const uint64_t t = (uint64_t)ordered(v[c]) << 32 | (kNone - (i + c));
             const double x = t >= border ? weight(v[c], top, row.scale) : 0.0;
             e[c] = x >= row.min_p || v[c] == top ? x : 0.0;
             sum += e[c];
@@ -703,10 +791,23 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
         return sum;
     };
     double e[W];
-    for (uint32_t j0 = 0; j0 < q.count; j0 += kThreads) {
-        const double sum = wave_sum(kept(j0 + threadIdx.x, e));
-        if (lane == 0) s.cell[j0 / 64 + wave] = sum;
+    for (uint32_t j0 = 0; j0 < q.count; j0 += 4 * kThreads) {
+        float v[4][W];
+        uint32_t first[4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) {
+            const uint32_t j = j0 + u * kThreads + threadIdx.x;
+            first[u] = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
+            read_values<F32>(p, at, first[u], v[u]);
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) {
+            const double sum = wave_sum(kept(first[u], v[u], e));
+            const uint32_t cell = (j0 + u * kThreads) / 64 + wave;
+            if (lane == 0 && cell < kMaxCells) s.cell[cell] = sum;
+        }
     }
+    if (threadIdx.x == 0) s.pick = kNone;
     __syncthreads();
     const double mine[1] = {threadIdx.x < (q.count + 63) / 64 ? s.cell[threadIdx.x] : 0.0};
     double whole;
@@ -714,11 +815,17 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
     const double want = uniform_of(p, r) * whole;
     const uint32_t cell = first_over(mine, run, want, s);
     if (threadIdx.x == cell) s.total = run;
-    const uint32_t j = cell * 64 + lane;
-    const double sum = kept(threadIdx.x < 64 ? j : q.count, e);
+    const uint32_t j = cell * 64 + lane, i = threadIdx.x < 64 && j < q.count ? read_at<F32>(s, q, j) : p.vocab;
+    float v[W];
+    read_values<F32>(p, at, i, v);
+    const double sum = kept(i, v, e);
+    __syncthreads();
+    if (threadIdx.x == 0) s.pick = kNone;
     run = block_scan(sum, s.mass, whole) + s.total;
     const uint32_t place = first_over(e, run, want, s);
-    if (threadIdx.x == 0) finish(p, r, read_at<F32>(s, q, cell * 64 + place / W) + place % W, top, row.heat, all);
+#pragma unroll
+    for (uint32_t c = 0; c < W; ++c)
+        if (threadIdx.x * W + c == place) finish(p, r, i + c, v[c], top, row.heat, all);
     return true;
 }
 
@@ -730,17 +837,28 @@ __global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
     const uint64_t at = (uint64_t)r * p.stride;
     const Row row = row_of(p, r);
     const Segment *segs = p.segment + (uint64_t)r * p.segments;
+    // thread i has segments PER i .. , so that sums over the threads before it are those of the tokens before
+    constexpr uint32_t PER = kMaxVocab / kSegment / kThreads;
     uint32_t best = 0, nan = 0, lowest = 0;
-    for (uint32_t i = threadIdx.x; i < p.segments; i += kThreads) {
-        const Segment g = segs[i];
-        best = max(best, ordered(g.top));
-        lowest = max(lowest, ~ordered(g.low));
-        nan |= g.sum != g.sum;
+    Segment mine[PER];
+#pragma unroll
+    for (uint32_t c = 0; c < PER; ++c) {
+        const uint32_t i = threadIdx.x * PER + c;
+        mine[c] = i < p.segments ? segs[i] : Segment{0.0, -INFINITY, INFINITY};
+        best = max(best, ordered(mine[c].top));
+        lowest = max(lowest, ~ordered(mine[c].low));
+        nan |= mine[c].sum != mine[c].sum;
     }
-    best = block_max(best, s.count);
-    lowest = ~block_max(lowest, s.other);
-    nan = block_max(nan, s.count);
-    if (nan || best <= kKeyMinusInf || row.bad) {
+    Groups g;
+    load_groups(g, p.groups + (uint64_t)r * p.segments * 128, p.segments * 2, 0);
+    best = wave_max(best);
+    lowest = wave_max(lowest);
+    nan = __any(nan);
+    if ((threadIdx.x & 63) == 0) s.count[threadIdx.x >> 6] = nan ? kNone : best, s.other[threadIdx.x >> 6] = lowest;
+    __syncthreads();
+    best = lane_of(row_scan<Max>(s.count[threadIdx.x & (kWaves - 1)]), kWaves - 1);
+    lowest = ~lane_of(row_scan<Max>(s.other[threadIdx.x & (kWaves - 1)]), kWaves - 1);
+    if (best == kNone || best <= kKeyMinusInf || row.bad) {
         if (threadIdx.x == 0) {
             p.token[r] = -1;
             if (p.logprob) p.logprob[r] = __builtin_nanf("");
@@ -748,65 +866,58 @@ __global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
         return;
     }
     const float top = unordered(best);
-    constexpr uint32_t PER = kMaxVocab / kSegment / kThreads;  // segments of a thread, in their order
     double share[PER], part = 0, all;
 #pragma unroll
     for (uint32_t c = 0; c < PER; ++c) {
-        const uint32_t i = threadIdx.x * PER + c;
-        share[c] = i < p.segments ? segs[i].sum * weight(segs[i].top, top, row.scale) : 0.0;
+        share[c] = mine[c].sum * weight(mine[c].top, top, row.scale);
         part += share[c];
     }
     double run = block_scan(part, s.mass, all);
     if (top < INFINITY && row.k == 1) {
         // the first of the largest
         uint32_t first = 0;
-        for (uint32_t i = threadIdx.x; i < p.segments; i += kThreads)
-            if (segs[i].top == top) first = max(first, 0xFFFFFFFFu - i);
-        const uint32_t seg = 0xFFFFFFFFu - block_max(first, s.count);
+#pragma unroll
+        for (uint32_t c = PER; c-- > 0;)
+            if (mine[c].top == top) first = kNone - (threadIdx.x * PER + c);
+        const uint32_t seg = kNone - block_max(first, s.count);
         first = 0;
-        for (uint32_t i = seg * kSegment + threadIdx.x; i < min((seg + 1) * kSegment, p.vocab); i += kThreads)
-            if (value(p.logits, at + i, F32) == top) first = max(first, 0xFFFFFFFFu - i);
+#pragma unroll
+        for (uint32_t c = 0; c < kSegment / kThreads; ++c) {
+            const uint32_t i = seg * kSegment + c * kThreads + threadIdx.x;
+            if (i < p.vocab && value(p.logits, at + i, F32) == top) first = max(first, kNone - i);
+        }
         first = block_max(first, s.other);
-        if (threadIdx.x == 0) finish(p, r, 0xFFFFFFFFu - first, top, row.heat, all);
+        if (threadIdx.x == 0) finish(p, r, kNone - first, top, top, row.heat, all);
         return;
     }
     if (top < INFINITY && !row.k && row.top_p >= 1 && row.min_p <= 0) {
         // the segment, then the token, at which the running sum exceeds the draw
         const double want = uniform_of(p, r) * all;
-        uint32_t first = 0, any = 0;
-        double first_at = 0, any_at = 0;  // the sums before them
+        if (threadIdx.x == 0) s.pick = kNone;
+        __syncthreads();
+        const uint32_t seg = first_over(share, run, want, s);
 #pragma unroll
         for (uint32_t c = 0; c < PER; ++c) {
-            const uint32_t i = threadIdx.x * PER + c;
-            if (share[c] > 0) {
-                any = i + 1, any_at = run;
-                if (run + share[c] > want && !first) first = 0xFFFFFFFFu - i, first_at = run;
-            }
+            if (threadIdx.x * PER + c == seg) s.total = run;
             run += share[c];
         }
-        const uint32_t hit = block_max(first, s.count), last = block_max(any, s.other);
-        if (hit ? first == hit : any == last) s.total = hit ? first_at : any_at;
-        __syncthreads();
-        const uint32_t seg = hit ? 0xFFFFFFFFu - hit : last - 1;
-        const uint32_t i0 = seg * kSegment + threadIdx.x * 2;
-        double e[2];
+        constexpr uint32_t OWN = kSegment / kThreads;
+        const uint32_t i0 = seg * kSegment + threadIdx.x * OWN;
+        float z[OWN];
+        double e[OWN], sum = 0, whole;
 #pragma unroll
-        for (uint32_t c = 0; c < 2; ++c)
-            e[c] = i0 + c < p.vocab ? weight(value(p.logits, at + i0 + c, F32), top, row.scale) : 0.0;
-        double whole;
-        run = block_scan(e[0] + e[1], s.mass, whole) + s.total;
-        first = any = 0;
-#pragma unroll
-        for (uint32_t c = 0; c < 2; ++c) {
-            run += e[c];
-            if (e[c] > 0) {
-                any = i0 + c + 1;
-                if (run > want && !first) first = 0xFFFFFFFFu - (i0 + c);
-            }
+        for (uint32_t c = 0; c < OWN; ++c) {
+            z[c] = i0 + c < p.vocab ? value(p.logits, at + i0 + c, F32) : -INFINITY;
+            e[c] = weight(z[c], top, row.scale);
+            sum += e[c];
         }
-        first = block_max(first, s.count);
-        any = block_max(any, s.other);
-        if (threadIdx.x == 0) finish(p, r, first ? 0xFFFFFFFFu - first : any - 1, top, row.heat, all);
+        __syncthreads();
+        if (threadIdx.x == 0) s.pick = kNone;
+        run = block_scan(sum, s.mass, whole) + s.total;
+        const uint32_t place = first_over(e, run, want, s);
+#pragma unroll
+        for (uint32_t c = 0; c < OWN; ++c)
+            if (threadIdx.x * OWN + c == place) finish(p, r, i0 + c, z[c], top, row.heat, all);
         return;
     }
     if (top < INFINITY) {
@@ -823,7 +934,7 @@ __global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
             const double z = (double)top + log(row.min_p) * row.heat * 1.000001 - fabs((double)top) * 1e-6;
             least = min(bin_of(bins, (float)z) / 4 + 1, kCoarse - 1);
         }
-        if (row.k ? by_sorting<F32>(p, r, row, bins, all, least, s) : by_sums<F32>(p, r, row, bins, all, least, s)) return;
+        if (row.k ? by_sorting<F32>(p, r, row, bins, all, least, g, s) : by_sums<F32>(p, r, row, bins, all, least, g, s)) return;
         __syncthreads();
     } else {  // the infinite ones share alike
         double n = 0;
