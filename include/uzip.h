@@ -569,7 +569,8 @@ uzip_status uzip_moe(const uzip_weight *up, const uzip_weight *down, const uzip_
  * logprob: the logarithm of the token's softmax over all of the row's logits,
  * divided by the temperature (by 1 where that is 0), whatever the filters.
  * -inf is never drawn.  A row that holds a NaN, or nothing above -inf, or whose
- * temperature is negative or a parameter NaN, gets token -1 and logprob NaN.
+ * temperature is negative or infinite or a parameter NaN, gets token -1 and
+ * logprob NaN.
  * Infinite logits give the limit.  Each parameter is a device array of one
  * value a row, or, where that is null, the value beside it.  e and its sums are
  * taken in 64 bits.  Limits: 2^21 rows, 2^22 tokens, 2^24 runs of 2,048 tokens a

@@ -73,7 +73,7 @@ __device__ inline Row row_of(const SampleParams &p, uint32_t r) {
     const float t = p.temperature ? p.temperature[r] : p.temperature_all;
     const float tp = p.top_p ? p.top_p[r] : p.top_p_all, mp = p.min_p ? p.min_p[r] : p.min_p_all;
     const int32_t k = p.top_k ? p.top_k[r] : p.top_k_all;
-    o.bad = !(t >= 0) || tp != tp || mp != mp;
+    o.bad = !(t >= 0 && t < INFINITY) || tp != tp || mp != mp;
     o.heat = t > 0 ? (double)t : 1.0;
     o.scale = 1.4426950408889634 / o.heat;
     o.top_p = tp;
@@ -87,6 +87,9 @@ __device__ inline double weight(float z, float top, double scale) {
     const double x = ((double)z - (double)top) * scale;
     return z == top ? 1.0 : x > -1000.0 ? exp2_low(x) : 0.0;
 }
+
+// The same where the largest is finite and z not below 2^-1000 of it (there not 0).
+__device__ inline double weight_near(float z, float top, double scale) { return exp2_low(((double)z - (double)top) * scale); }
 
 // A value of another lane by DPP, zero where there is none.
 template <int CTRL, int ROWS = 15, class T>
@@ -154,10 +157,8 @@ struct Shared {
         uint64_t hot[2 * kMaxVocab / kSegment];          // the hot lanes of each half segment
         uint32_t reads[kMaxHot * (kGroup / 4)];          // first tokens of the hot groups' reads, by index
     };
-    union {
-        uint64_t tokens[kMaxCandidates];                 // key << 32 | ~index, by index
-        double cell[kMaxCells];
-    };
+    double cell[kMaxCells];
+    uint64_t tokens[kMaxCandidates];                     // key << 32 | ~index
     uint64_t sorted[kMaxCandidates];
 };
 
@@ -365,8 +366,9 @@ __device__ inline void read_values(const SampleParams &p, uint64_t at, uint32_t 
 }
 
 // A wave a segment of 2,048 tokens: its largest value, the sum of its weights
-// relative to that, and the largest of each group of 16 tokens (a lane's reads
-// of half a segment), so that the second kernel reads little of the row again.
+// relative to that, its smallest value, and the largest of each group of 16
+// tokens (a lane's reads of half a segment), so that the second kernel reads
+// little of the row again.
 template <bool F32>
 __global__ __launch_bounds__(256) void k_survey(SampleParams p) {
     constexpr int W = F32 ? 4 : 8, READS = kSegment / 64 / W, HALF = READS / 2;
@@ -392,8 +394,18 @@ __global__ __launch_bounds__(256) void k_survey(SampleParams p) {
             }
         p.groups[(n * 2 + h) * 64 + lane] = group[h];
     }
-    float top = fmaxf(group[0], group[1]);
-    float low = fminf(group[0] > -INFINITY ? group[0] : INFINITY, group[1] > -INFINITY ? group[1] : INFINITY);
+    float top = fmaxf(group[0], group[1]), low = INFINITY;
+    if ((seg + 1) * kSegment <= p.vocab) {
+#pragma unroll
+        for (int i = 0; i < READS; ++i)
+#pragma unroll
+            for (int c = 0; c < W; ++c) low = fminf(low, v[i][c]);
+    } else {  // (what is behind the last token does not count)
+#pragma unroll
+        for (int i = 0; i < READS; ++i)
+#pragma unroll
+            for (int c = 0; c < W; ++c) low = fminf(low, v[i][c] > -INFINITY ? v[i][c] : INFINITY);
+    }
     top = unordered(wave_max(ordered(top)));
     low = unordered(~wave_max(~ordered(low)));
     const double scale = row_of(p, r).scale;
@@ -417,13 +429,13 @@ __global__ __launch_bounds__(256) void k_survey(SampleParams p) {
 
 // ---- the draw -----------------------------------------------------------------------
 
-// Bins of the values from the largest (0) to `low` (kBins - 2), in even steps,
-// and of those from there to `floor`; beyond that kBins.  Four make a coarse bin.
+// Bins of the values from the largest (0) to `floor` in even steps; beyond that
+// kBins.  Four make a coarse bin.
 struct Bins {
-    float top, low, floor, inv;
+    float top, floor, inv;
 };
 __device__ inline uint32_t bin_of(const Bins &b, float z) {
-    return z >= b.low ? min((uint32_t)((b.top - z) * b.inv), kBins - 2) : z >= b.floor ? kBins - 1 : kBins;
+    return z >= b.floor ? min((uint32_t)((b.top - z) * b.inv), kBins - 1) : kBins;
 }
 
 // The reads that hold every token of the first `last` + 1 coarse bins, by
@@ -558,36 +570,6 @@ __device__ inline bool collect(const SampleParams &p, uint64_t at, const Bins &b
     return true;
 }
 
-// The same of one bin, in any order.
-template <bool F32>
-__device__ inline bool collect_bin(const SampleParams &p, uint64_t at, const Bins &bins, const Reads &q, uint32_t bin, uint32_t &n,
-                                   Shared &s) {
-    constexpr uint32_t W = F32 ? 4 : 8;
-    if (threadIdx.x == 0) s.pick_count = 0;
-    __syncthreads();
-    for (uint32_t j0 = 0; j0 < q.count; j0 += 4 * kThreads) {
-        float v[4][W];
-        uint32_t first[4];
-#pragma unroll
-        for (uint32_t u = 0; u < 4; ++u) {
-            const uint32_t j = j0 + u * kThreads + threadIdx.x;
-            first[u] = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
-            read_values<F32>(p, at, first[u], v[u]);
-        }
-#pragma unroll
-        for (uint32_t u = 0; u < 4; ++u)
-#pragma unroll
-            for (uint32_t c = 0; c < W; ++c)
-                if (v[u][c] > -INFINITY && bin_of(bins, v[u][c]) == bin) {
-                    const uint32_t place = atomicAdd(&s.pick_count, 1u);
-                    if (place < kMaxCandidates) s.tokens[place] = (uint64_t)ordered(v[u][c]) << 32 | (0xFFFFFFFFu - (first[u] + c));
-                }
-    }
-    __syncthreads();
-    n = s.pick_count;
-    return n <= kMaxCandidates;
-}
-
 // s.tokens into s.sorted, the order of the filters.  Few are ranked by counting.
 __device__ inline void sort_tokens(uint32_t n, Shared &s) {
     if (n <= 256) {
@@ -708,8 +690,22 @@ __device__ inline bool by_sorting(const SampleParams &p, uint32_t r, const Row &
     return true;
 }
 
-// Rows with top-p or min-p alone: the bin in which top-p ends, from a histogram
-// of sums, the tokens of that one bin sorted, then the kept ones' sums by runs.
+// Four reads of a thread, 1,024 apart.
+template <bool F32, uint32_t W = F32 ? 4 : 8>
+__device__ inline void four_reads(const SampleParams &p, uint64_t at, const Shared &s, const Reads &q, uint32_t j0, float (&v)[4][W],
+                                  uint32_t (&first)[4]) {
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u) {
+        const uint32_t j = j0 + u * kThreads + threadIdx.x;
+        first[u] = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
+        read_values<F32>(p, at, first[u], v[u]);
+    }
+}
+
+// Rows with top-p or min-p alone.  A histogram of the weights, in fp32, tells
+// the bin in which top-p ends; then the sums before that bin in 64 bits, by
+// runs of 64 reads, beside the list of the bin's tokens, whose order gives the
+// border.  False if the histogram missed the bin, or holds too many there.
 template <bool F32>
 __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all, uint32_t least,
                                Groups &g, Shared &s) {
@@ -718,22 +714,20 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
     const uint64_t at = (uint64_t)r * p.stride;
     const float top = bins.top;
     uint32_t last;
-    Reads q = choose_reads<F32>(p, r, row, bins, all, least, g, last, s);
+    const Reads q = choose_reads<F32>(p, r, row, bins, all, least, g, last, s);
     if ((q.count + 63) / 64 > kMaxCells) return false;
     const uint32_t end = (q.all ? least : last) * 4 + 3;  // bins that the reads hold whole
-    const double unit = unit_of(all);
-    uint64_t border = 0;
+    const double unit = unit_of(all), reach = fmax(row.top_p * all, 1e-300);
+    uint32_t bin = kBins;
     if (row.top_p < 1) {
-        for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.bin_mass[i] = 0;
+        s.bin_mass[threadIdx.x] = 0;
         __syncthreads();
+        const float scale = (float)row.scale, funit = (float)unit;
         uint32_t tops = 0;
-        for (uint32_t j0 = threadIdx.x; j0 < q.count; j0 += 4 * kThreads) {
+        for (uint32_t j0 = 0; j0 < q.count; j0 += 4 * kThreads) {
             float v[4][W];
-#pragma unroll
-            for (uint32_t u = 0; u < 4; ++u) {
-                const uint32_t j = j0 + u * kThreads;
-                read_values<F32>(p, at, j < q.count ? read_at<F32>(s, q, j) : p.vocab, v[u]);
-            }
+            uint32_t first[4];
+            four_reads<F32>(p, at, s, q, j0, v, first);
 #pragma unroll
             for (uint32_t u = 0; u < 4; ++u)
 #pragma unroll
@@ -742,7 +736,7 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
                     if (v[u][c] == top) ++tops;  // (equal ones would meet at one address)
                     else if (b <= end)
                         atomicAdd((unsigned long long *)&s.bin_mass[b],
-                                  (unsigned long long)(weight(v[u][c], top, row.scale) * unit + 0.5));
+                                  (unsigned long long)(__builtin_amdgcn_exp2f((v[u][c] - top) * scale) * funit));
                 }
         }
         uint32_t all_tops;
@@ -750,75 +744,102 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
         const uint64_t m = s.bin_mass[threadIdx.x] + (threadIdx.x == 0 ? (uint64_t)(all_tops * unit) : 0);
         uint64_t masses;
         const uint64_t m0 = block_scan(m, s.large, masses);
-        const double reach = row.top_p * all;
-        const uint32_t bin = 0xFFFFFFFFu - block_max(m && (double)(m0 + m) >= reach * unit ? 0xFFFFFFFFu - threadIdx.x : 0, s.other);
-        if (bin < kBins) {
-            if (threadIdx.x == bin) s.pick_mass = m0;
-            uint32_t n;
-            if (!collect_bin<F32>(p, at, bins, q, bin, n, s)) return false;
-            sort_tokens(n, s);
-            double e[kOwn], part = 0, whole;
-#pragma unroll
-            for (uint32_t c = 0; c < kOwn; ++c) {
-                const uint32_t i = threadIdx.x * kOwn + c;
-                e[c] = i < n ? sorted_weight(s.sorted[i], top, row.scale) : 0.0;
-                part += e[c];
-            }
-            double run = (double)s.pick_mass / unit + block_scan(part, s.mass, whole);
-            uint32_t kept = 0, keep;
-#pragma unroll
-            for (uint32_t c = 0; c < kOwn; ++c) {
-                kept += threadIdx.x * kOwn + c < n && run < reach;
-                run += e[c];
-            }
-            block_scan(kept, s.count, keep);
-            border = s.sorted[max(keep, 1u) - 1];
-        } else if (!q.all && last < least) {
-            return false;
+        bin = kNone - block_max(m && (double)(m0 + m) >= reach * unit ? kNone - threadIdx.x : 0, s.other);
+        if (bin >= kBins) {
+            // min_p ends all, or everything counts
+            if (!q.all && last < least) return false;
+            bin = kBins;
         }
-        __syncthreads();  // (s.cell takes the place of s.tokens)
     }
-    // the kept ones' sums by runs of 64 reads
-    auto kept = [&](uint32_t i, const float (&v)[W], double (&e)[W]) __attribute__((always_inline)) {
-        double sum = 0;
-#pragma unroll
-        for (uint32_t c = 0; c < W; ++c) {
-            const uint64_t t = (uint64_t)ordered(v[c]) << 32 | (kNone - (i + c));
-            const double x = t >= border ? weight(v[c], top, row.scale) : 0.0;
-            e[c] = x >= row.min_p || v[c] == top ? x : 0.0;
-            sum += e[c];
-        }
-        return sum;
-    };
-    double e[W];
+    if (threadIdx.x == 0) s.pick_count = 0;
+    __syncthreads();
+    double above = 0;
     for (uint32_t j0 = 0; j0 < q.count; j0 += 4 * kThreads) {
         float v[4][W];
         uint32_t first[4];
+        four_reads<F32>(p, at, s, q, j0, v, first);
 #pragma unroll
         for (uint32_t u = 0; u < 4; ++u) {
-            const uint32_t j = j0 + u * kThreads + threadIdx.x;
-            first[u] = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
-            read_values<F32>(p, at, first[u], v[u]);
-        }
+            double sum = 0;
 #pragma unroll
-        for (uint32_t u = 0; u < 4; ++u) {
-            const double sum = wave_sum(kept(first[u], v[u], e));
+            for (uint32_t c = 0; c < W; ++c) {
+                const uint32_t b = bin_of(bins, v[u][c]);
+                if (b < bin) {
+                    const double e = weight_near(v[u][c], top, row.scale);
+                    above += e;
+                    sum += e >= row.min_p ? e : 0.0;
+                } else if (b == bin && b < kBins) {
+                    const uint32_t place = atomicAdd(&s.pick_count, 1u);
+                    if (place < kMaxCandidates) s.tokens[place] = (uint64_t)ordered(v[u][c]) << 32 | (kNone - (first[u] + c));
+                }
+            }
+            sum = wave_sum(sum);
             const uint32_t cell = (j0 + u * kThreads) / 64 + wave;
             if (lane == 0 && cell < kMaxCells) s.cell[cell] = sum;
         }
     }
+    __syncthreads();
+    uint64_t border = 0;
+    s.bin_mass[threadIdx.x] = 0;  // of the bin's kept tokens, by runs
+    if (bin < kBins) {
+        const uint32_t n = s.pick_count;
+        if (n > kMaxCandidates) return false;
+        sort_tokens(n, s);
+        double e[kOwn], part = 0, whole, before;
+#pragma unroll
+        for (uint32_t c = 0; c < kOwn; ++c) {
+            const uint32_t i = threadIdx.x * kOwn + c;
+            e[c] = i < n ? weight_near(unordered((uint32_t)(s.sorted[i] >> 32)), top, row.scale) : 0.0;
+            part += e[c];
+        }
+        block_scan(above, s.mass, before);
+        double run = block_scan(part, s.mass, whole) + before;
+        uint32_t kept = 0, keep;
+#pragma unroll
+        for (uint32_t c = 0; c < kOwn; ++c) {
+            const uint32_t i = threadIdx.x * kOwn + c;
+            if (i < n && run < reach) {
+                ++kept;
+                const uint32_t token = kNone - (uint32_t)s.sorted[i];
+                uint32_t j = token / W;
+                if (!q.all) {  // the last read that begins at or before it
+                    uint32_t lo = 0, hi = q.count;
+                    while (hi - lo > 1) {
+                        const uint32_t mid = (lo + hi) / 2;
+                        if (s.reads[mid] <= token) lo = mid;
+                        else hi = mid;
+                    }
+                    j = lo;
+                }
+                if (e[c] >= row.min_p)
+                    atomicAdd((unsigned long long *)&s.bin_mass[j / 64], (unsigned long long)(e[c] * unit + 0.5));
+            }
+            run += e[c];
+        }
+        block_scan(kept, s.count, keep);
+        if (keep == 0 || (keep == n && before + whole < reach)) return false;
+        border = s.sorted[keep - 1];
+    }
     if (threadIdx.x == 0) s.pick = kNone;
     __syncthreads();
-    const double mine[1] = {threadIdx.x < (q.count + 63) / 64 ? s.cell[threadIdx.x] : 0.0};
+    const double mine[1] = {threadIdx.x < (q.count + 63) / 64 ? s.cell[threadIdx.x] + (double)s.bin_mass[threadIdx.x] / unit : 0.0};
     double whole;
     double run = block_scan(mine[0], s.mass, whole);
     const double want = uniform_of(p, r) * whole;
     const uint32_t cell = first_over(mine, run, want, s);
     if (threadIdx.x == cell) s.total = run;
+    // the run again, a read a lane
     const uint32_t j = cell * 64 + lane, i = threadIdx.x < 64 && j < q.count ? read_at<F32>(s, q, j) : p.vocab;
     float v[W];
+    double e[W], sum = 0;
     read_values<F32>(p, at, i, v);
-    const double sum = kept(i, v, e);
+#pragma unroll
+    for (uint32_t c = 0; c < W; ++c) {
+        const bool in = v[c] >= bins.floor && ((uint64_t)ordered(v[c]) << 32 | (kNone - (i + c))) >= border;
+        const double x = in ? weight_near(v[c], top, row.scale) : 0.0;
+        e[c] = x >= row.min_p ? x : 0.0;
+        sum += e[c];
+    }
     __syncthreads();
     if (threadIdx.x == 0) s.pick = kNone;
     run = block_scan(sum, s.mass, whole) + s.total;
@@ -924,10 +945,9 @@ __global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
         // Tokens that weigh less than 2^-80 of the largest change no sum in 64 bits and are left out.
         Bins bins;
         bins.top = top;
-        bins.floor = (float)((double)top - 80.0 / row.scale);
-        bins.low = fmaxf(unordered(lowest), bins.floor);
-        const float range = top - bins.low;
-        bins.inv = range > 0 ? (kBins - 1.01f) / range : 0.0f;
+        bins.floor = fmaxf(unordered(lowest), (float)((double)top - 80.0 / row.scale));
+        const float range = top - bins.floor;
+        bins.inv = range > 0 ? (kBins - 0.01f) / range : 0.0f;
         // the last coarse bin with tokens that min_p keeps (top-p of the first k needs the sum of the others too)
         uint32_t least = kCoarse - 1;
         if (row.min_p > 0 && !(row.k && row.top_p < 1)) {

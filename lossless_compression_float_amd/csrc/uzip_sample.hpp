@@ -12,8 +12,7 @@ constexpr uint32_t kSegment = 2048;  // tokens that a wave surveys
 constexpr uint32_t kGroup = 16;      // tokens of a lane in half a segment
 
 // Of a segment: the sum of its weights relative to its largest value (NaN if
-// it holds one), that value, and the smallest of its groups' largest values
-// above -inf.
+// it holds one), that value, and its smallest.
 struct Segment {
     double sum;
     float top, low;

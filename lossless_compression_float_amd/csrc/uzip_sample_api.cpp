@@ -1,6 +1,7 @@
 // uzip_sample_api.cpp -- the C ABI of the sampler (include/uzip.h): argument
 // checks and launches on the caller's stream.  Nothing here allocates or
 // synchronises.
+#include <math.h>
 #include <stdint.h>
 
 #include <hip/hip_runtime.h>
@@ -20,7 +21,7 @@ bool sample_ok(const uzip_sample_args *a) {
     if (!a || a->rows > kMaxRows || a->vocab == 0 || a->vocab > kMaxVocab || !type_ok(a->logits_dtype) || a->u_double > 1)
         return false;
     if (a->rows * blocks(a->vocab, kSegment) > kMaxSegments) return false;
-    if (!a->temperature && !(a->temperature_all >= 0)) return false;
+    if (!a->temperature && !(a->temperature_all >= 0 && a->temperature_all < INFINITY)) return false;
     if ((!a->top_p && a->top_p_all != a->top_p_all) || (!a->min_p && a->min_p_all != a->min_p_all)) return false;
     for (const void *p : {(const void *)a->temperature, (const void *)a->top_k, (const void *)a->top_p, (const void *)a->min_p,
                           (const void *)a->logprob})

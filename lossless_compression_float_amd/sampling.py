@@ -76,8 +76,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ws=None, s
     fp32) or a tensor with one value a row: fp32, top_k int32.
 
     -inf is never drawn; a row with a NaN or with nothing above -inf, or with a
-    negative temperature or a NaN among its parameters, gives token -1 and
-    logprob NaN."""
+    negative or infinite temperature or a NaN among its parameters, gives token
+    -1 and logprob NaN."""
     if not isinstance(logits, torch.Tensor) or not isinstance(u, torch.Tensor):
         raise TypeError("logits and u must be tensors")
     code = _code(logits.dtype, "logits")
