@@ -378,6 +378,330 @@ __global__ __launch_bounds__(256) void k_combine(CombineParams p) {
     }
 }
 
+// ---- the layer for few tokens ---------------------------------------------------------
+
+// Pairs [begin, end) of an expert; offsets are clamped to the pairs that exist.
+__device__ inline uint32_t clamped(int32_t v, uint32_t pairs) { return v < 0 ? 0u : min((uint32_t)v, pairs); }
+
+// The n-th expert that has pairs and those; their number with n = kAllExperts.
+constexpr uint32_t kAllExperts = 0xFFFFFFFFu;
+struct Found {
+    uint32_t expert, begin, end, count;
+};
+__device__ inline Found find_expert(const MoeParams &p, uint32_t n) {
+    constexpr uint32_t AHEAD = 4;
+    const uint32_t lane = threadIdx.x & 63, pairs = p.tokens * p.k;
+    Found f{0, 0, 0, 0};
+    for (uint32_t e0 = 0; e0 < p.num; e0 += 64 * AHEAD) {
+        uint32_t b[AHEAD], t[AHEAD];
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) {
+            const uint32_t e = e0 + i * 64 + lane;
+            b[i] = e < p.num ? clamped(p.offsets[e], pairs) : 0;
+            t[i] = e < p.num ? clamped(p.offsets[e + 1], pairs) : 0;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) {
+            const uint64_t m = __ballot(t[i] > b[i]);
+            const uint32_t c = __popcll(m);
+            if (n >= f.count && n < f.count + c) {
+                const uint64_t at = __ballot((m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == n - f.count);
+                const uint32_t l = (uint32_t)__ffsll((unsigned long long)at) - 1;
+                f.expert = e0 + i * 64 + l;
+                f.begin = __builtin_amdgcn_readlane(b[i], l);
+                f.end = __builtin_amdgcn_readlane(t[i], l);
+                f.count = n + 1;
+                return f;
+            }
+            f.count += c;
+        }
+    }
+    return f;
+}
+
+// A wave's tiles of one row block, kb = first, first + step, ..: from memory
+// through the decoder into the matrix instructions with `columns`, one block on
+// its way.  `load` reads the second operand's values of a block, `multiply`
+// takes the weights'.
+template <int RB>
+struct TileRows {
+    rsrc_t rows[RB];
+    uint64_t tile0[RB];
+};
+template <int RB, class L, class M>
+__device__ inline void stream_tiles(const WeightView &w, const TileRows<RB> &t, uint32_t first, uint32_t step, uint32_t count,
+                                    uint32_t lane, L load_columns, M multiply) {
+    const uint32_t KB = w.col_blocks;
+    Tile tile[RB];
+    uint4 heads[RB];
+    auto load = [&](uint32_t i) __attribute__((always_inline)) {
+        const uint32_t kb = i < count ? first + i * step : KB;  // (behind the last block: zeros)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            tile[b].sm = read16(t.rows[b], kb * kTileBytes + lane * 16);
+            tile[b].code = read8(t.rows[b], kb * kTileBytes + kTileSm + lane * 8);
+        }
+        load_columns(kb);
+    };
+    for (uint32_t i0 = 0; i0 < count; i0 += 64) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) heads[b] = w.head[t.tile0[b] + min(first + (i0 + lane) * step, KB - 1)];
+        if (i0 == 0) load(0);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) heads[b] = head_checked(w, heads[b]);
+        for (uint32_t i = i0; i < min(count, i0 + 64); ++i) {
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
+                uint32_t v[8];
+                tile[b].h.x = __builtin_amdgcn_readlane(heads[b].x, i & 63);
+                tile_decode_plain(tile[b], v);
+                if (tile[b].h.x & (0xFF00u | kTileZero)) {
+                    tile[b].h.y = __builtin_amdgcn_readlane(heads[b].y, i & 63);
+                    tile[b].h.z = __builtin_amdgcn_readlane(heads[b].z, i & 63);
+                    tile[b].h.w = __builtin_amdgcn_readlane(heads[b].w, i & 63);
+                    tile_decode(tile[b], w, lane, v);
+                }
+                multiply(b, v);
+            }
+            load(i + 1);
+        }
+    }
+}
+
+// h = weight * act(U x + bias) for the pairs of one expert: RB row blocks of U
+// (gated: RB / 2, each with its up rows), NW waves that split its columns, 16 CT
+// pairs at a time, whose rows of x are read where they are.
+template <int CT, int RB, bool GATED, int NW>
+__global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
+    __shared__ f32x4 part[NW][RB * CT * 64];
+    const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const uint32_t q = lane >> 4, r = lane & 15, pairs = p.tokens * p.k;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && p.splits > 1)
+        for (uint32_t i = threadIdx.x; i < p.down.row_blocks; i += NW * 64) p.arrived[i] = 0;
+    const Found f = find_expert(p, blockIdx.y);
+    if (f.begin == f.end) return;
+    const uint32_t KB = p.up.col_blocks, n = KB > wave ? (KB + NW - 1 - wave) / NW : 0;
+    TileRows<RB> t;
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        uint32_t b = GATED ? blockIdx.x * (RB / 2) + i / 2 : blockIdx.x * RB + i;
+        if (b >= p.up.part_blocks) b = p.up.part_blocks - 1;  // computed and dropped
+        if (GATED && (i & 1)) b += p.up.part_blocks;
+        t.tile0[i] = ((uint64_t)f.expert * p.up.row_blocks + b) * KB;
+        t.rows[i] = buffer(p.up.tiles + t.tile0[i] * kTileBytes, KB * kTileBytes);
+    }
+    const rsrc_t xb = buffer(static_cast<const uint8_t *>(p.x.p), ((p.tokens - 1) * (uint32_t)p.x.stride + p.up_cols) * 2);
+    for (uint32_t s0 = f.begin; s0 < f.end; s0 += 16 * CT) {
+        const uint32_t here = min(f.end - s0, 16u * CT);
+        uint32_t row[CT];
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const uint32_t pair = j * 16 + r < here ? (uint32_t)p.order[s0 + j * 16 + r] : pairs;
+            row[j] = pair < pairs ? pair / p.k * (uint32_t)p.x.stride * 2 : kNowhere;
+        }
+        f32x4 acc[RB][CT];
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+            for (int j = 0; j < CT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        uint4 x[CT][2];
+        stream_tiles<RB>(
+            p.up, t, wave, NW, n, lane,
+            [&](uint32_t kb) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t c = kb * kTileCols + h * 32 + q * 8;
+                        if (j == 0 || (uint32_t)j * 16 < here) x[j][h] = read16(xb, row[j] != kNowhere && c < p.up_cols ? row[j] + c * 2 : kNowhere);
+                    }
+            },
+            [&](int i, const uint32_t (&v)[8]) __attribute__((always_inline)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
+#pragma unroll
+                    for (int j = 0; j < CT; ++j)
+                        if (j == 0 || (uint32_t)j * 16 < here)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, x[j][h]), acc[i][j], 0, 0, 0);
+                }
+            });
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+            for (int j = 0; j < CT; ++j) part[wave][(i * CT + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+        constexpr int STEP = GATED ? 2 : 1;
+        for (uint32_t u = threadIdx.x; u < RB / STEP * CT * 64; u += NW * 64) {
+            const uint32_t l = u & 63, j = (u >> 6) % CT, i = (u >> 6) / CT * STEP;
+            const uint32_t slot = j * 16 + (l & 15);
+            const uint32_t b = GATED ? blockIdx.x * (RB / 2) + i / 2 : blockIdx.x * RB + i;
+            if (slot >= here || b >= p.up.part_blocks) continue;
+            const uint32_t m = b * 16 + (l >> 4) * 4, count = m < p.h_cols ? min(p.h_cols - m, 4u) : 0;
+            const uint32_t pair = (uint32_t)p.order[s0 + slot];
+            const float w = pair < pairs ? p.weights[pair] : 0.0f;
+            float z[STEP][4];
+#pragma unroll
+            for (int h = 0; h < STEP; ++h) {
+                f32x4 s = part[0][((i + h) * CT + j) * 64 + l];
+                for (int g = 1; g < NW; ++g) s += part[g][((i + h) * CT + j) * 64 + l];
+                float bias[4] = {0, 0, 0, 0};
+                if (p.up_bias && count) load<4>(p.up_bias, (uint64_t)f.expert * p.up_rows + h * p.up.part_rows + m, p.bias_f32, count, bias);
+                for (int d = 0; d < 4; ++d) z[h][d] = s[d] + bias[d];
+            }
+            // weight times activation as the sum of two bf16 values, off by 2^-17 of it: the second product then adds
+            // less than its own result's rounding (with one value the layer's error is 1.4 times that)
+            float hi[4], lo[4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const float a = GATED ? z[0][d] * sigmoid(z[0][d]) * z[GATED ? 1 : 0][d] : activate(z[0][d], p.act);
+                const float y = d < (int)count && pair < pairs ? w * a : 0.0f;
+                hi[d] = from_bf16(to_bf16(y));
+                lo[d] = isfinite(hi[d]) ? y - hi[d] : 0.0f;
+            }
+            uint16_t *out = p.h + (uint64_t)(s0 + slot) * 2 * p.h_stride + m;
+            *reinterpret_cast<u32x2 *>(out) = u32x2{pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3])};
+            *reinterpret_cast<u32x2 *>(out + p.h_stride) = u32x2{pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3])};
+        }
+        __syncthreads();
+    }
+}
+
+// y = the sum over the experts of D_e h_e, as one long contraction: the blocks
+// of all experts that have pairs, in a row, are dealt out in runs to the waves
+// of the workgroups that share a row block.  Columns 2 i and 2 i + 1 of the
+// matrix instruction are the two values of pair i of an expert; when a wave
+// leaves an expert, it adds them to its sums of the pairs' tokens in LDS.  The
+// waves' sums are added in a fixed order, and the splits' by the workgroup that
+// comes last.
+template <int CT, int NW>
+__global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
+    extern __shared__ float sums[];  // [NW][tokens][16]
+    __shared__ uint32_t last;
+    const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const uint32_t q = lane >> 4, r = lane & 15, pairs = p.tokens * p.k, block = blockIdx.x;
+    const uint32_t KB = p.down.col_blocks, size = p.tokens * 16;
+    float *mine = sums + wave * size;
+    for (uint32_t i = lane; i < size / 4; i += 64) reinterpret_cast<f32x4 *>(mine)[i] = f32x4{0, 0, 0, 0};
+    const uint32_t waves = NW * p.splits, w = blockIdx.y * NW + wave;
+    const uint64_t items = (uint64_t)find_expert(p, kAllExperts).count * KB;
+    uint64_t at = items * w / waves;
+    const uint64_t stop = items * (w + 1) / waves;
+    const rsrc_t hb = buffer(reinterpret_cast<const uint8_t *>(p.h), pairs * 4 * p.h_stride);
+    const uint32_t wide = (p.h_cols + 15) / 16 * 16;  // columns of h that are written
+    while (at < stop) {
+        const Found f = find_expert(p, (uint32_t)(at / KB));
+        const uint32_t kb0 = (uint32_t)(at % KB), n = (uint32_t)min<uint64_t>(KB - kb0, stop - at);
+        at += n;
+        TileRows<1> t;
+        t.tile0[0] = ((uint64_t)f.expert * p.down.row_blocks + block) * KB;
+        t.rows[0] = buffer(p.down.tiles + t.tile0[0] * kTileBytes, KB * kTileBytes);
+        for (uint32_t s0 = f.begin; s0 < f.end; s0 += 8 * CT) {
+            const uint32_t here = min(f.end - s0, 8u * CT);
+            f32x4 acc[CT];
+            uint32_t row[CT], pair[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const uint32_t slot = j * 8 + r / 2;
+                acc[j] = f32x4{0, 0, 0, 0};
+                row[j] = slot < here ? ((s0 + slot) * 2 + (r & 1)) * p.h_stride * 2 : kNowhere;
+                pair[j] = slot < here ? (uint32_t)p.order[s0 + slot] : pairs;
+            }
+            uint4 x[CT][2];
+            stream_tiles<1>(
+                p.down, t, kb0, 1, n, lane,
+                [&](uint32_t kb) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int j = 0; j < CT; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t c = kb * kTileCols + h * 32 + q * 8;
+                            if (j == 0 || (uint32_t)j * 8 < here) x[j][h] = read16(hb, row[j] != kNowhere && c < wide ? row[j] + c * 2 : kNowhere);
+                        }
+                },
+                [&](int, const uint32_t (&v)[8]) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
+#pragma unroll
+                        for (int j = 0; j < CT; ++j)
+                            if (j == 0 || (uint32_t)j * 8 < here)
+                                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, x[j][h]), acc[j], 0, 0, 0);
+                    }
+                });
+            // both values together, then to the token's sums; the wave that has an expert's first block adds its bias
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                if (j && (uint32_t)j * 8 >= here) continue;
+                f32x4 s = acc[j];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) s[d] += __shfl_xor(s[d], 1);
+                if (pair[j] >= pairs) continue;
+                const uint32_t m = block * 16 + q * 4;
+                if (p.down_bias && kb0 == 0 && m < p.down_rows) {
+                    float b[4];
+                    load<4>(p.down_bias, (uint64_t)f.expert * p.down_rows + m, p.bias_f32, min(p.down_rows - m, 4u), b);
+                    const float g = p.weights[pair[j]];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) s[d] += g * b[d];
+                }
+                if (r & 1) continue;
+                f32x4 *to = reinterpret_cast<f32x4 *>(mine + pair[j] / p.k * 16 + q * 4);
+                *to = *to + s;
+            }
+        }
+    }
+    __syncthreads();
+    const uint32_t rows4 = p.tokens * 4;
+    auto finish = [&](uint32_t u, f32x4 s) {
+        const uint32_t t = u / 4, m = block * 16 + u % 4 * 4;
+        if (m >= p.down_rows) return;
+        const uint32_t count = min(p.down_rows - m, 4u);
+        float y[4] = {s[0], s[1], s[2], s[3]};
+        if (p.residual) {
+            float res[4];
+            load<4>(p.residual, (uint64_t)t * p.residual_stride + m, p.y_f32, count, res);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) y[d] += res[d];
+        }
+        store<4>(p.y, (uint64_t)t * p.y_stride + m, p.y_f32, count, y);
+    };
+    for (uint32_t u = threadIdx.x; u < rows4; u += NW * 64) {
+        f32x4 s = reinterpret_cast<const f32x4 *>(sums)[u];
+        for (uint32_t g = 1; g < NW; ++g) s += reinterpret_cast<const f32x4 *>(sums + g * size)[u];
+        if (p.splits == 1) {
+            finish(u, s);
+            continue;
+        }
+        // Past the L2, which the other workgroup's XCD does not share.  (With fences around plain stores, which write that
+        // cache back from every wave, the kernel took 90 us more.)
+        float *to = p.part + (((uint64_t)blockIdx.y * p.down.row_blocks + block) * rows4 + u) * 4;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) __hip_atomic_store(to + d, s[d], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (p.splits == 1) return;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // they are there
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(&p.arrived[block], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
+    __syncthreads();
+    if (!last) return;
+    for (uint32_t u = threadIdx.x; u < rows4; u += NW * 64) {
+        f32x4 s = f32x4{0, 0, 0, 0};
+        for (uint32_t g = 0; g < p.splits; ++g) {
+            const float *from = p.part + (((uint64_t)g * p.down.row_blocks + block) * rows4 + u) * 4;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) s[d] += __hip_atomic_load(from + d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        finish(u, s);
+    }
+}
+
+template <int CT, int RB, bool GATED, int NW>
+hipError_t moe_up(const MoeParams &p, hipStream_t s) {
+    const uint32_t per = GATED ? RB / 2 : RB, experts = p.num < p.tokens * p.k ? p.num : p.tokens * p.k;
+    k_moe_up<CT, RB, GATED, NW><<<dim3((p.up.part_blocks + per - 1) / per, experts), NW * 64, 0, s>>>(p);
+    return hipGetLastError();
+}
+
 template <int V>
 hipError_t route(const RouteParams &p, hipStream_t s) {
     if (p.chunks == 1) {
@@ -412,6 +736,30 @@ hipError_t launch_route_backward(const RouteBackwardParams &p, hipStream_t s) {
     else if (p.num <= 128) k_route_backward<2><<<wgs, 256, 0, s>>>(p);
     else if (p.num <= 256) k_route_backward<4><<<wgs, 256, 0, s>>>(p);
     else k_route_backward<16><<<wgs, 256, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+uint32_t moe_splits(uint64_t down_blocks, uint64_t items) {
+    const uint64_t n = (256 + down_blocks - 1) / down_blocks, most = items / 16;
+    return (uint32_t)(n < most ? n : most ? most : 1);
+}
+
+hipError_t launch_moe_few(const MoeParams &p, hipStream_t s) {
+    hipError_t e;
+    const uint64_t pairs = (uint64_t)p.tokens * p.k, experts = p.num < pairs ? p.num : pairs, blocks = p.up.part_blocks * experts;
+    const bool one = p.tokens <= 16 || pairs <= 8 * experts;
+    if (p.act == kActSwiglu) {
+        if (one) e = blocks <= 768 ? moe_up<1, 2, true, 8>(p, s) : moe_up<1, 4, true, 4>(p, s);
+        else e = blocks <= 768 ? moe_up<2, 2, true, 8>(p, s) : moe_up<2, 4, true, 4>(p, s);
+    } else {
+        e = one ? moe_up<1, 2, false, 8>(p, s) : moe_up<2, 2, false, 8>(p, s);
+    }
+    if (e != hipSuccess) return e;
+    const dim3 grid(p.down.row_blocks, p.splits);
+    const uint32_t lds = 16 * p.tokens * 16 * 4;
+    if (p.tokens <= 8) k_moe_down<1, 16><<<grid, 1024, lds, s>>>(p);
+    else if (p.tokens <= 16) k_moe_down<2, 16><<<grid, 1024, lds, s>>>(p);
+    else k_moe_down<4, 16><<<grid, 1024, lds, s>>>(p);
     return hipGetLastError();
 }
 

@@ -61,6 +61,28 @@ struct CombineParams {
     uint32_t y_f32, tokens, k, cols;
 };
 
+// The layer for few tokens, in two kernels.
+struct MoeParams {
+    WeightView up, down;
+    Mat x;
+    const int32_t *order, *offsets;
+    const float *weights;
+    const void *up_bias, *down_bias, *residual;
+    uint64_t residual_stride;
+    uint16_t *h;          // [pairs][2][h_stride]: activation times weight as the sum of two bf16 values
+    float *part;          // [splits][row blocks of down][tokens][16], with more than one split
+    uint32_t *arrived;    // [row blocks of down]
+    void *y;
+    uint64_t y_stride;
+    uint32_t tokens, k, num;
+    uint32_t up_rows, up_cols, down_rows, h_cols, h_stride;
+    uint32_t bias_f32, y_f32, act, splits;
+};
+constexpr uint32_t kFewTokens = 64;
+
+hipError_t launch_moe_few(const MoeParams &p, hipStream_t s);
+// Workgroups that share a row block of down.
+uint32_t moe_splits(uint64_t down_blocks, uint64_t items);
 hipError_t launch_route(const RouteParams &p, hipStream_t s);
 uint32_t route_chunks(uint64_t tokens, uint64_t k);
 hipError_t launch_route_backward(const RouteBackwardParams &p, hipStream_t s);

@@ -85,8 +85,53 @@ bool moe_ok(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args 
     return mat_ok(a->x, a->x_stride, a->tokens, up->cols, 2) && mat_ok(a->y, a->y_stride, a->tokens, down->rows, size);
 }
 
-// Rows gathered by expert, the two grouped products, the results joined.
-struct MoePlan {
+// Few tokens: two kernels.
+bool few(const uzip_weight *down, const uzip_moe_args *a) {
+    // (the pairs' activations, two bf16 values each, are addressed with 32 bits)
+    return a->tokens <= kFewTokens && a->tokens * a->k * 4 * uzip::up(down->cols, 64) < (1ull << 32) - 4096;
+}
+
+MoeParams plan_few(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *a, Carver &c) {
+    MoeParams p{};
+    p.up = view(up);
+    p.down = view(down);
+    p.x = Mat{a->x, a->x_stride};
+    if (!tiled(a->x, a->x_stride, up->cols)) {
+        p.x.stride = uzip::up(up->cols, 8);
+        p.x.p = c.take<uint16_t>(a->tokens * p.x.stride);
+    }
+    p.order = a->order;
+    p.offsets = a->offsets;
+    p.weights = a->weights;
+    p.up_bias = a->up_bias;
+    p.down_bias = a->down_bias;
+    p.residual = a->residual;
+    p.residual_stride = a->residual_stride;
+    p.y = a->y;
+    p.y_stride = a->y_stride;
+    p.tokens = (uint32_t)a->tokens;
+    p.k = a->k;
+    p.num = (uint32_t)up->matrices;
+    p.up_rows = (uint32_t)up->rows;
+    p.up_cols = (uint32_t)uzip::up(up->cols, 8);
+    p.down_rows = (uint32_t)down->rows;
+    p.h_cols = (uint32_t)down->cols;
+    p.h_stride = (uint32_t)uzip::up(down->cols, 64);
+    p.bias_f32 = a->bias_dtype == UZIP_FP32;
+    p.y_f32 = a->y_dtype == UZIP_FP32;
+    p.act = a->act;
+    const uint64_t pairs = a->tokens * a->k;
+    p.splits = moe_splits(p.down.row_blocks, std::min<uint64_t>(up->matrices, pairs) * p.down.col_blocks);
+    p.h = c.take<uint16_t>(pairs * 2 * p.h_stride);
+    if (p.splits > 1) {
+        p.part = c.take<float>((uint64_t)p.splits * p.down.row_blocks * a->tokens * 16);
+        p.arrived = c.take<uint32_t>(p.down.row_blocks);
+    }
+    return p;
+}
+
+// Many: rows gathered by expert, the two grouped products, the results joined.
+struct ManyPlan {
     uint16_t *x, *h;
     float *o;
     uint32_t *place;
@@ -95,43 +140,72 @@ struct MoePlan {
     uint8_t *ws;
 };
 
-MoePlan plan_moe(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *a, Carver &c) {
-    MoePlan p{};
-    const uint64_t pairs = a->tokens * a->k, xs = uzip::up(up->cols, 8), hs = uzip::up(down->cols, 8);
-    p.x = c.take<uint16_t>(pairs * xs);
-    p.h = c.take<uint16_t>(pairs * hs);
-    p.o = c.take<float>(pairs * down->rows);
-    p.place = c.take<uint32_t>(pairs);
+ManyPlan plan_many(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *a, Carver &c) {
+    ManyPlan p{};
+    const uint64_t pairs = a->tokens * a->k;
     uzip_linear_args f{};
     f.tokens = pairs;
     f.offsets = a->offsets;
     f.bias_dtype = a->bias_dtype;
-    f.x = p.x;
-    f.x_stride = xs;
-    f.bias = a->up_bias;
-    f.y = p.h;
-    f.y_stride = hs;
-    f.y_dtype = UZIP_BF16;
-    f.act = a->act;
-    p.first = f;
-    f.x = p.h;
-    f.x_stride = hs;
-    f.bias = a->down_bias;
-    f.y = p.o;
-    f.y_stride = down->rows;
-    f.y_dtype = UZIP_FP32;
-    f.act = UZIP_ACT_NONE;
-    p.second = f;
-    // (sizes do not depend on where the buffers are, only on their alignment)
-    uint8_t *const some = reinterpret_cast<uint8_t *>(kAlign);
-    for (uzip_linear_args *l : {&f, &p.first}) {
-        uzip_linear_args probe = *l;
-        if (!probe.x) probe.x = some;
-        if (!probe.y) probe.y = some;
-        p.ws_bytes = std::max(p.ws_bytes, uzip_linear_workspace_size(l == &f ? down : up, &probe));
-    }
+    p.first = p.second = f;
+    p.first.x_stride = uzip::up(up->cols, 8);
+    p.first.bias = a->up_bias;
+    p.first.y_stride = p.second.x_stride = uzip::up(down->cols, 8);
+    p.first.y_dtype = UZIP_BF16;
+    p.first.act = a->act;
+    p.second.bias = a->down_bias;
+    p.second.y_stride = down->rows;
+    p.second.y_dtype = UZIP_FP32;
+    p.x = c.take<uint16_t>(pairs * p.first.x_stride);
+    p.h = c.take<uint16_t>(pairs * p.first.y_stride);
+    p.o = c.take<float>(pairs * p.second.y_stride);
+    p.place = c.take<uint32_t>(pairs);
+    p.first.x = p.x;
+    p.first.y = p.h;
+    p.second.x = p.h;
+    p.second.y = p.o;
+    // the products' workspace: it does not depend on where the buffers are, which are all aligned
+    uzip_linear_args one = p.first, two = p.second;
+    void *const some = reinterpret_cast<void *>(kAlign);
+    one.x = two.x = some;
+    one.y = two.y = some;
+    p.ws_bytes = std::max(uzip_linear_workspace_size(up, &one), uzip_linear_workspace_size(down, &two));
     if (p.ws_bytes) p.ws = c.take<uint8_t>(p.ws_bytes);
     return p;
+}
+
+uzip_status run_many(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *a, const ManyPlan &plan,
+                     hipStream_t stream) {
+    GatherParams g{};
+    g.x = Mat{a->x, a->x_stride};
+    g.out = plan.x;
+    g.out_stride = plan.first.x_stride;
+    g.cols = (uint32_t)up->cols;
+    g.tokens = (uint32_t)a->tokens;
+    g.k = a->k;
+    g.order = a->order;
+    g.ends = a->offsets + up->matrices;
+    g.place = plan.place;
+    if (launch_gather(g, stream) != hipSuccess) return UZIP_ERR_DEVICE;
+    uzip_status st = uzip_grouped_linear(up, &plan.first, plan.ws, plan.ws_bytes, stream);
+    if (st != UZIP_OK) return st;
+    st = uzip_grouped_linear(down, &plan.second, plan.ws, plan.ws_bytes, stream);
+    if (st != UZIP_OK) return st;
+    CombineParams p{};
+    p.o = plan.o;
+    p.stride = plan.second.y_stride;
+    p.place = plan.place;
+    p.ends = g.ends;
+    p.weights = a->weights;
+    p.residual = a->residual;
+    p.residual_stride = a->residual_stride;
+    p.y = a->y;
+    p.y_stride = a->y_stride;
+    p.y_f32 = a->y_dtype == UZIP_FP32;
+    p.tokens = g.tokens;
+    p.k = a->k;
+    p.cols = (uint32_t)down->rows;
+    return done(launch_combine(p, stream));
 }
 
 }  // namespace
@@ -176,7 +250,8 @@ uzip_status uzip_moe_route_backward(const uzip_moe_route_args *args, hipStream_t
 size_t uzip_moe_workspace_size(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *args) {
     if (!moe_ok(up, down, args) || args->tokens == 0) return 0;
     Carver c(nullptr);
-    plan_moe(up, down, args, c);
+    if (few(down, args)) plan_few(up, down, args, c);
+    else plan_many(up, down, args, c);
     return (size_t)c.bytes();
 }
 
@@ -185,38 +260,18 @@ uzip_status uzip_moe(const uzip_weight *up, const uzip_weight *down, const uzip_
     if (!moe_ok(up, down, args)) return UZIP_ERR_INVALID_ARGUMENT;
     if (args->tokens == 0) return UZIP_OK;
     Carver c(d_workspace);
-    const MoePlan plan = plan_moe(up, down, args, c);
+    if (!few(down, args)) {
+        const ManyPlan plan = plan_many(up, down, args, c);
+        if (!workspace_ok(d_workspace, workspace_bytes, c.bytes())) return UZIP_ERR_INVALID_ARGUMENT;
+        return run_many(up, down, args, plan, stream);
+    }
+    const MoeParams p = plan_few(up, down, args, c);
     if (!workspace_ok(d_workspace, workspace_bytes, c.bytes())) return UZIP_ERR_INVALID_ARGUMENT;
-    GatherParams g{};
-    g.x = Mat{args->x, args->x_stride};
-    g.out = plan.x;
-    g.out_stride = plan.first.x_stride;
-    g.cols = (uint32_t)up->cols;
-    g.tokens = (uint32_t)args->tokens;
-    g.k = args->k;
-    g.order = args->order;
-    g.ends = args->offsets + up->matrices;
-    g.place = plan.place;
-    if (launch_gather(g, stream) != hipSuccess) return UZIP_ERR_DEVICE;
-    uzip_status st = uzip_grouped_linear(up, &plan.first, plan.ws, plan.ws_bytes, stream);
-    if (st != UZIP_OK) return st;
-    st = uzip_grouped_linear(down, &plan.second, plan.ws, plan.ws_bytes, stream);
-    if (st != UZIP_OK) return st;
-    CombineParams p{};
-    p.o = plan.o;
-    p.stride = plan.second.y_stride;
-    p.place = plan.place;
-    p.ends = g.ends;
-    p.weights = args->weights;
-    p.residual = args->residual;
-    p.residual_stride = args->residual_stride;
-    p.y = args->y;
-    p.y_stride = args->y_stride;
-    p.y_f32 = args->y_dtype == UZIP_FP32;
-    p.tokens = g.tokens;
-    p.k = args->k;
-    p.cols = (uint32_t)down->rows;
-    return done(launch_combine(p, stream));
+    if (p.x.p != args->x && launch_stage(static_cast<const uint16_t *>(args->x), args->x_stride,
+                                         static_cast<uint16_t *>(const_cast<void *>(p.x.p)), p.x.stride, args->tokens, up->cols,
+                                         stream) != hipSuccess)
+        return UZIP_ERR_DEVICE;
+    return done(launch_moe_few(p, stream));
 }
 
 }  // extern "C"
