@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "uzip_lanes.hpp"
 #include "uzip_moe.hpp"
 #include "uzip_tiles.hpp"
 
@@ -28,22 +29,7 @@ __device__ inline uint64_t ordered(double v) {
     return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-__device__ inline uint64_t wave_max(uint64_t v) {
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t o = __shfl_xor((unsigned long long)v, d);
-        v = o > v ? o : v;
-    }
-    return v;
-}
-__device__ inline uint32_t wave_min(uint32_t v) {
-    for (int d = 1; d < 64; d <<= 1) v = min(v, (uint32_t)__shfl_xor((int)v, d));
-    return v;
-}
-template <class T>
-__device__ inline T wave_sum(T v) {
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
-}
+__device__ inline uint32_t wave_min(uint32_t v) { return ~wave_max(~v); }
 
 // The limit where the maximum is infinite: all of it shares alike.
 __device__ inline float exp_below(float z, float top) { return z == top ? 1.0f : expf(z - top); }
@@ -108,7 +94,7 @@ __device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, i
         float top = z[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) top = fmaxf(top, z[i]);
-        for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+        top = unordered(wave_max(ordered(top)));
         const float s = on ? exp_below(mine, top) : 0.0f;
         float all = s;
         if (!p.renorm) {
@@ -383,15 +369,15 @@ __global__ __launch_bounds__(256) void k_combine(CombineParams p) {
 // Pairs [begin, end) of an expert; offsets are clamped to the pairs that exist.
 __device__ inline uint32_t clamped(int32_t v, uint32_t pairs) { return v < 0 ? 0u : min((uint32_t)v, pairs); }
 
-// The n-th expert that has pairs and those; their number with n = kAllExperts.
-constexpr uint32_t kAllExperts = 0xFFFFFFFFu;
+// The n-th expert that has pairs, and those; none: no pairs.
 struct Found {
-    uint32_t expert, begin, end, count;
+    uint32_t expert, begin, end;
 };
 __device__ inline Found find_expert(const MoeParams &p, uint32_t n) {
     constexpr uint32_t AHEAD = 4;
     const uint32_t lane = threadIdx.x & 63, pairs = p.tokens * p.k;
-    Found f{0, 0, 0, 0};
+    Found f{0, 0, 0};
+    uint32_t seen = 0;
     for (uint32_t e0 = 0; e0 < p.num; e0 += 64 * AHEAD) {
         uint32_t b[AHEAD], t[AHEAD];
 #pragma unroll
@@ -404,19 +390,30 @@ __device__ inline Found find_expert(const MoeParams &p, uint32_t n) {
         for (uint32_t i = 0; i < AHEAD; ++i) {
             const uint64_t m = __ballot(t[i] > b[i]);
             const uint32_t c = __popcll(m);
-            if (n >= f.count && n < f.count + c) {
-                const uint64_t at = __ballot((m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == n - f.count);
+            if (n >= seen && n < seen + c) {
+                const uint64_t at = __ballot((m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == n - seen);
                 const uint32_t l = (uint32_t)__ffsll((unsigned long long)at) - 1;
                 f.expert = e0 + i * 64 + l;
                 f.begin = __builtin_amdgcn_readlane(b[i], l);
                 f.end = __builtin_amdgcn_readlane(t[i], l);
-                f.count = n + 1;
                 return f;
             }
-            f.count += c;
+            seen += c;
         }
     }
     return f;
+}
+
+// Reads at a lane's offset plus a uniform one, which costs no vector operation.
+// Lanes that are to read zeros have an offset behind every buffer used here.
+constexpr uint32_t kBehind = 1u << 31;
+__device__ inline uint4 read16(rsrc_t r, uint32_t lane_off, uint32_t off) {
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane_off, (int)off, 0);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ inline uint2 read8(rsrc_t r, uint32_t lane_off, uint32_t off) {
+    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane_off, (int)off, 0);
+    return make_uint2(v[0], v[1]);
 }
 
 // A wave's tiles of one row block, kb = first, first + step, ..: from memory
@@ -431,15 +428,16 @@ struct TileRows {
 template <int RB, class L, class M>
 __device__ inline void stream_tiles(const WeightView &w, const TileRows<RB> &t, uint32_t first, uint32_t step, uint32_t count,
                                     uint32_t lane, L load_columns, M multiply) {
+    if (count == 0) return;
     const uint32_t KB = w.col_blocks;
     Tile tile[RB];
     uint4 heads[RB];
     auto load = [&](uint32_t i) __attribute__((always_inline)) {
-        const uint32_t kb = i < count ? first + i * step : KB;  // (behind the last block: zeros)
+        const uint32_t kb = first + min(i, count - 1) * step;  // (behind the last block: that again, for nothing)
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            tile[b].sm = read16(t.rows[b], kb * kTileBytes + lane * 16);
-            tile[b].code = read8(t.rows[b], kb * kTileBytes + kTileSm + lane * 8);
+            tile[b].sm = read16(t.rows[b], lane * 16, kb * kTileBytes);
+            tile[b].code = read8(t.rows[b], kTileSm + lane * 8, kb * kTileBytes);
         }
         load_columns(kb);
     };
@@ -491,13 +489,14 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
         t.rows[i] = buffer(p.up.tiles + t.tile0[i] * kTileBytes, KB * kTileBytes);
     }
     const rsrc_t xb = buffer(static_cast<const uint8_t *>(p.x.p), ((p.tokens - 1) * (uint32_t)p.x.stride + p.up_cols) * 2);
+    const uint32_t part_block = p.up_cols % kTileCols ? KB - 1 : KB;  // the block whose last columns x does not have
     for (uint32_t s0 = f.begin; s0 < f.end; s0 += 16 * CT) {
         const uint32_t here = min(f.end - s0, 16u * CT);
         uint32_t row[CT];
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const uint32_t pair = j * 16 + r < here ? (uint32_t)p.order[s0 + j * 16 + r] : pairs;
-            row[j] = pair < pairs ? pair / p.k * (uint32_t)p.x.stride * 2 : kNowhere;
+            row[j] = pair < pairs ? pair / p.k * (uint32_t)p.x.stride * 2 + q * 16 : kBehind;
         }
         f32x4 acc[RB][CT];
 #pragma unroll
@@ -511,8 +510,8 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
                 for (int j = 0; j < CT; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t c = kb * kTileCols + h * 32 + q * 8;
-                        if (j == 0 || (uint32_t)j * 16 < here) x[j][h] = read16(xb, row[j] != kNowhere && c < p.up_cols ? row[j] + c * 2 : kNowhere);
+                        const bool in = kb != part_block || part_block * kTileCols + h * 32 + q * 8 < p.up_cols;
+                        if (j == 0 || (uint32_t)j * 16 < here) x[j][h] = read16(xb, in ? row[j] : kBehind, (kb * kTileCols + h * 32) * 2);
                     }
             },
             [&](int i, const uint32_t (&v)[8]) __attribute__((always_inline)) {
@@ -560,6 +559,9 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
             uint16_t *out = p.h + (uint64_t)(s0 + slot) * 2 * p.h_stride + m;
             *reinterpret_cast<u32x2 *>(out) = u32x2{pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3])};
             *reinterpret_cast<u32x2 *>(out + p.h_stride) = u32x2{pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3])};
+            if (b + 1 == p.up.part_blocks)  // zeros up to a whole block of columns
+                for (uint32_t c = 16; b * 16 + c < p.h_stride; c += 16)
+                    *reinterpret_cast<u32x2 *>(out + c) = *reinterpret_cast<u32x2 *>(out + p.h_stride + c) = u32x2{0, 0};
         }
         __syncthreads();
     }
@@ -567,113 +569,206 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
 
 // y = the sum over the experts of D_e h_e, as one long contraction: the blocks
 // of all experts that have pairs, in a row, are dealt out in runs to the waves
-// of the workgroups that share a row block.  Columns 2 i and 2 i + 1 of the
-// matrix instruction are the two values of pair i of an expert; when a wave
-// leaves an expert, it adds them to its sums of the pairs' tokens in LDS.  The
-// waves' sums are added in a fixed order, and the splits' by the workgroup that
-// comes last.
-template <int CT, int NW>
+// of the workgroups that share RB row blocks.  Columns 2 i and 2 i + 1 of the
+// matrix instruction are the two values of pair i; an expert with more than 8 CT
+// pairs comes several times.  A wave's blocks follow one another without a
+// pause over the experts, one on its way (with two the registers cost as much as
+// they gain); when it leaves an expert, it adds its results to its own sums of the pairs' tokens in LDS.  The waves' sums are
+// added in a fixed order, and the splits' by the workgroup that comes last.
+constexpr uint32_t kMaxVisits = kMaxExperts + kFewPairs / 8;
+template <int CT, int RB, int NW>
 __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
-    extern __shared__ float sums[];  // [NW][tokens][16]
-    __shared__ uint32_t last;
+    extern __shared__ float sums[];                 // [NW][RB][tokens][16]
+    __shared__ uint32_t visits[kMaxVisits];         // expert, first pair << 10, pairs - 1 << 23
+    __shared__ uint16_t token_of[kFewPairs];
+    __shared__ uint32_t before[NW], last;
+    constexpr uint32_t PAIRS = 8 * CT, EXPERTS = (kMaxExperts + NW * 64 - 1) / (NW * 64);
     const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const uint32_t q = lane >> 4, r = lane & 15, pairs = p.tokens * p.k, block = blockIdx.x;
-    const uint32_t KB = p.down.col_blocks, size = p.tokens * 16;
-    float *mine = sums + wave * size;
-    for (uint32_t i = lane; i < size / 4; i += 64) reinterpret_cast<f32x4 *>(mine)[i] = f32x4{0, 0, 0, 0};
+    const uint32_t q = lane >> 4, r = lane & 15, pairs = p.tokens * p.k, block = blockIdx.x * RB;
+    const uint32_t KB = p.down.col_blocks, rows4 = RB * p.tokens * 4;
+    f32x4 *const all = reinterpret_cast<f32x4 *>(sums), *const mine = all + wave * rows4;
+    uint32_t first[EXPERTS], count[EXPERTS], own = 0, entries;
+#pragma unroll
+    for (uint32_t i = 0; i < EXPERTS; ++i) {
+        const uint32_t e = threadIdx.x * EXPERTS + i;
+        first[i] = e < p.num ? clamped(p.offsets[e], pairs) : 0;
+        const uint32_t end = e < p.num ? clamped(p.offsets[e + 1], pairs) : 0;
+        count[i] = end > first[i] ? end - first[i] : 0;
+        own += (count[i] + PAIRS - 1) / PAIRS;
+    }
+    for (uint32_t s = threadIdx.x; s < pairs; s += NW * 64) {
+        const uint32_t pair = (uint32_t)p.order[s];
+        token_of[s] = (uint16_t)(pair < pairs ? pair / p.k : 0xFFFF);
+    }
+    for (uint32_t i = lane; i < rows4; i += 64) mine[i] = f32x4{0, 0, 0, 0};
+    uint32_t at = scan_before<NW>(own, before, entries);
+#pragma unroll
+    for (uint32_t i = 0; i < EXPERTS; ++i)
+        for (uint32_t c = 0; c < count[i]; c += PAIRS, ++at)  // (groups that overlap could be more than there is room for)
+            if (at < kMaxVisits) visits[at] = (threadIdx.x * EXPERTS + i) | (first[i] + c) << 10 | (min(count[i] - c, PAIRS) - 1) << 23;
+    entries = min(entries, kMaxVisits);
+    __syncthreads();
     const uint32_t waves = NW * p.splits, w = blockIdx.y * NW + wave;
-    const uint64_t items = (uint64_t)find_expert(p, kAllExperts).count * KB;
-    uint64_t at = items * w / waves;
-    const uint64_t stop = items * (w + 1) / waves;
+    const uint64_t items = (uint64_t)entries * KB;
+    const uint32_t begin = uniform((uint32_t)(items * w / waves)), n = uniform((uint32_t)(items * (w + 1) / waves)) - begin;
     const rsrc_t hb = buffer(reinterpret_cast<const uint8_t *>(p.h), pairs * 4 * p.h_stride);
-    const uint32_t wide = (p.h_cols + 15) / 16 * 16;  // columns of h that are written
-    while (at < stop) {
-        const Found f = find_expert(p, (uint32_t)(at / KB));
-        const uint32_t kb0 = (uint32_t)(at % KB), n = (uint32_t)min<uint64_t>(KB - kb0, stop - at);
-        at += n;
-        TileRows<1> t;
-        t.tile0[0] = ((uint64_t)f.expert * p.down.row_blocks + block) * KB;
-        t.rows[0] = buffer(p.down.tiles + t.tile0[0] * kTileBytes, KB * kTileBytes);
-        for (uint32_t s0 = f.begin; s0 < f.end; s0 += 8 * CT) {
-            const uint32_t here = min(f.end - s0, 8u * CT);
-            f32x4 acc[CT];
-            uint32_t row[CT], pair[CT];
+    uint64_t row_tile[RB];  // of expert 0 (a block behind the last: the last, computed and dropped)
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                const uint32_t slot = j * 8 + r / 2;
-                acc[j] = f32x4{0, 0, 0, 0};
-                row[j] = slot < here ? ((s0 + slot) * 2 + (r & 1)) * p.h_stride * 2 : kNowhere;
-                pair[j] = slot < here ? (uint32_t)p.order[s0 + slot] : pairs;
-            }
-            uint4 x[CT][2];
-            stream_tiles<1>(
-                p.down, t, kb0, 1, n, lane,
-                [&](uint32_t kb) __attribute__((always_inline)) {
+    for (int i = 0; i < RB; ++i) row_tile[i] = (uint64_t)min(block + i, p.down.row_blocks - 1) * KB;
+    const uint64_t expert_tiles = (uint64_t)p.down.row_blocks * KB;
+    // what is loaded: an entry and its next block
+    uint32_t visit = begin / KB, kb = begin % KB, coming = 0, row[CT];
+    rsrc_t rows[RB];
+    auto enter = [&]() __attribute__((always_inline)) {
+        const uint32_t v = uniform(visits[min(visit, entries - 1)]), s0 = v >> 10 & 0x1FFF;
+        coming = (v >> 23) + 1;
 #pragma unroll
-                    for (int j = 0; j < CT; ++j)
+        for (int i = 0; i < RB; ++i)
+            rows[i] = buffer(p.down.tiles + ((v & 1023) * expert_tiles + row_tile[i]) * kTileBytes, KB * kTileBytes);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t c = kb * kTileCols + h * 32 + q * 8;
-                            if (j == 0 || (uint32_t)j * 8 < here) x[j][h] = read16(hb, row[j] != kNowhere && c < wide ? row[j] + c * 2 : kNowhere);
-                        }
-                },
-                [&](int, const uint32_t (&v)[8]) __attribute__((always_inline)) {
+        for (int j = 0; j < CT; ++j) {
+            const uint32_t slot = j * 8 + r / 2;
+            row[j] = slot < coming ? ((s0 + slot) * 2 + (r & 1)) * p.h_stride * 2 + q * 16 : kBehind;
+        }
+    };
+    struct Stage {
+        Tile tile[RB];
+        uint4 x[CT][2];
+    } stage;
+    auto load = [&](Stage &s, uint32_t i) __attribute__((always_inline)) {
+        if (kb == KB) {
+            kb = 0;
+            ++visit;
+            enter();
+        }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
+        for (int d = 0; d < RB; ++d) {
+            s.tile[d].sm = read16(rows[d], lane * 16, kb * kTileBytes);
+            s.tile[d].code = read8(rows[d], kTileSm + lane * 8, kb * kTileBytes);
+        }
 #pragma unroll
-                        for (int j = 0; j < CT; ++j)
-                            if (j == 0 || (uint32_t)j * 8 < here)
-                                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, x[j][h]), acc[j], 0, 0, 0);
-                    }
-                });
-            // both values together, then to the token's sums; the wave that has an expert's first block adds its bias
+        for (int j = 0; j < CT; ++j)
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                if (j && (uint32_t)j * 8 >= here) continue;
-                f32x4 s = acc[j];
+            for (int h = 0; h < 2; ++h)
+                if (j == 0 || (uint32_t)j * 8 < coming) s.x[j][h] = read16(hb, row[j], (kb * kTileCols + h * 32) * 2);
+        kb += i + 1 < n;  // (behind the last block: that again, for nothing)
+    };
+    // what is multiplied
+    uint32_t done_visit = visit, done_kb = kb, entered = kb, have = 0, s0 = 0, expert = 0;
+    f32x4 acc[RB][CT];
+    auto start = [&]() __attribute__((always_inline)) {
+        const uint32_t v = uniform(visits[min(done_visit, entries - 1)]);
+        expert = v & 1023, s0 = v >> 10 & 0x1FFF, have = (v >> 23) + 1;
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+            for (int j = 0; j < CT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    };
+    auto leave = [&]() __attribute__((always_inline)) {  // both values together, to the tokens' sums
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            if (j && (uint32_t)j * 8 >= have) continue;
+            const uint32_t slot = j * 8 + r / 2, token = slot < have ? token_of[s0 + slot] : 0xFFFF;
+            const bool on = token < p.tokens;
+            // the wave that has an expert's first block adds its bias
+            const bool biased = p.down_bias && entered == 0;
+            const float g = biased && on ? p.weights[p.order[s0 + slot]] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                f32x4 s = acc[i][j];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) s[d] += __shfl_xor(s[d], 1);
-                if (pair[j] >= pairs) continue;
-                const uint32_t m = block * 16 + q * 4;
-                if (p.down_bias && kb0 == 0 && m < p.down_rows) {
+                if (!on || (r & 1)) continue;
+                const uint32_t m = (block + i) * 16 + q * 4;
+                if (biased && m < p.down_rows) {
                     float b[4];
-                    load<4>(p.down_bias, (uint64_t)f.expert * p.down_rows + m, p.bias_f32, min(p.down_rows - m, 4u), b);
-                    const float g = p.weights[pair[j]];
+                    uzip::load<4>(p.down_bias, (uint64_t)expert * p.down_rows + m, p.bias_f32, min(p.down_rows - m, 4u), b);
 #pragma unroll
                     for (int d = 0; d < 4; ++d) s[d] += g * b[d];
                 }
-                if (r & 1) continue;
-                f32x4 *to = reinterpret_cast<f32x4 *>(mine + pair[j] / p.k * 16 + q * 4);
+                f32x4 *to = mine + (i * p.tokens + token) * 4 + q;
                 *to = *to + s;
             }
         }
+    };
+    uint4 heads[RB];
+    auto multiply = [&](Stage &s, uint32_t i) __attribute__((always_inline)) {
+        if (done_kb == KB) {
+            leave();
+            done_kb = entered = 0;
+            ++done_visit;
+            start();
+        }
+        ++done_kb;
+#pragma unroll
+        for (int d = 0; d < RB; ++d) {
+            uint32_t v[8];
+            Tile &t = s.tile[d];
+            t.h.x = __builtin_amdgcn_readlane(heads[d].x, i & 63);
+            tile_decode_plain(t, v);
+            if (t.h.x & (0xFF00u | kTileZero)) {
+                t.h.y = __builtin_amdgcn_readlane(heads[d].y, i & 63);
+                t.h.z = __builtin_amdgcn_readlane(heads[d].z, i & 63);
+                t.h.w = __builtin_amdgcn_readlane(heads[d].w, i & 63);
+                tile_decode(t, p.down, lane, v);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bf16x8 a = __builtin_bit_cast(bf16x8, u32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+                    if (j == 0 || (uint32_t)j * 8 < have)
+                        acc[d][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, s.x[j][h]), acc[d][j], 0, 0, 0);
+            }
+        }
+    };
+    auto load_heads = [&](uint32_t i0) __attribute__((always_inline)) {
+        const uint32_t item = begin + min(i0 + lane, n - 1), v = visits[item / KB];
+#pragma unroll
+        for (int d = 0; d < RB; ++d) heads[d] = p.down.head[(v & 1023) * expert_tiles + row_tile[d] + item % KB];
+    };
+    if (n) {
+        start();
+        enter();
+        load_heads(0);  // (first: loads come back in order)
+        load(stage, 0);
+        for (uint32_t i0 = 0; i0 < n; i0 += 64) {
+            if (i0) load_heads(i0);
+#pragma unroll
+            for (int d = 0; d < RB; ++d) heads[d] = head_checked(p.down, heads[d]);
+            const uint32_t end = min(n, i0 + 64);
+            for (uint32_t i = i0; i < end; ++i) {
+                multiply(stage, i);
+                load(stage, i + 1);
+            }
+        }
+        leave();
     }
     __syncthreads();
-    const uint32_t rows4 = p.tokens * 4;
     auto finish = [&](uint32_t u, f32x4 s) {
-        const uint32_t t = u / 4, m = block * 16 + u % 4 * 4;
+        const uint32_t t = u / 4 % p.tokens, m = (block + u / 4 / p.tokens) * 16 + u % 4 * 4;
         if (m >= p.down_rows) return;
         const uint32_t count = min(p.down_rows - m, 4u);
         float y[4] = {s[0], s[1], s[2], s[3]};
         if (p.residual) {
             float res[4];
-            load<4>(p.residual, (uint64_t)t * p.residual_stride + m, p.y_f32, count, res);
+            uzip::load<4>(p.residual, (uint64_t)t * p.residual_stride + m, p.y_f32, count, res);
 #pragma unroll
             for (int d = 0; d < 4; ++d) y[d] += res[d];
         }
         store<4>(p.y, (uint64_t)t * p.y_stride + m, p.y_f32, count, y);
     };
+    float *const part = p.part + (uint64_t)blockIdx.x * rows4 * 4;  // this block's of the first split
+    const uint64_t split = (uint64_t)gridDim.x * rows4 * 4;
     for (uint32_t u = threadIdx.x; u < rows4; u += NW * 64) {
-        f32x4 s = reinterpret_cast<const f32x4 *>(sums)[u];
-        for (uint32_t g = 1; g < NW; ++g) s += reinterpret_cast<const f32x4 *>(sums + g * size)[u];
+        f32x4 s = all[u];
+        for (uint32_t g = 1; g < NW; ++g) s += all[g * rows4 + u];
         if (p.splits == 1) {
             finish(u, s);
             continue;
         }
         // Past the L2, which the other workgroup's XCD does not share.  (With fences around plain stores, which write that
         // cache back from every wave, the kernel took 90 us more.)
-        float *to = p.part + (((uint64_t)blockIdx.y * p.down.row_blocks + block) * rows4 + u) * 4;
+        float *to = part + blockIdx.y * split + u * 4;
 #pragma unroll
         for (int d = 0; d < 4; ++d) __hip_atomic_store(to + d, s[d], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
@@ -681,18 +776,24 @@ __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // they are there
     __syncthreads();
     if (threadIdx.x == 0)
-        last = __hip_atomic_fetch_add(&p.arrived[block], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
+        last = __hip_atomic_fetch_add(&p.arrived[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
     __syncthreads();
     if (!last) return;
     for (uint32_t u = threadIdx.x; u < rows4; u += NW * 64) {
         f32x4 s = f32x4{0, 0, 0, 0};
-        for (uint32_t g = 0; g < p.splits; ++g) {
-            const float *from = p.part + (((uint64_t)g * p.down.row_blocks + block) * rows4 + u) * 4;
+        for (uint32_t g = 0; g < p.splits; ++g)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) s[d] += __hip_atomic_load(from + d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
+            for (int d = 0; d < 4; ++d)
+                s[d] += __hip_atomic_load(part + g * split + u * 4 + d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         finish(u, s);
     }
+}
+
+template <int CT, int RB, int NW>
+hipError_t moe_down(const MoeParams &p, hipStream_t s) {
+    const dim3 grid((p.down.row_blocks + RB - 1) / RB, p.splits);
+    k_moe_down<CT, RB, NW><<<grid, NW * 64, NW * RB * p.tokens * 64, s>>>(p);
+    return hipGetLastError();
 }
 
 template <int CT, int RB, bool GATED, int NW>
@@ -739,28 +840,43 @@ hipError_t launch_route_backward(const RouteBackwardParams &p, hipStream_t s) {
     return hipGetLastError();
 }
 
-uint32_t moe_splits(uint64_t down_blocks, uint64_t items) {
-    const uint64_t n = (256 + down_blocks - 1) / down_blocks, most = items / 16;
-    return (uint32_t)(n < most ? n : most ? most : 1);
+// How many workgroups, of how many waves and row blocks, the second product
+// takes.  Row blocks: one with 16 waves; two with 8, which read h once for both,
+// where an expert has many pairs (in us, one and two: 64 tokens, 64 experts of 2048 x
+// 1024, 8 pairs each, 58 and 56; 8 experts of 4096 x 2048, 16 each, 50 and 41; but
+// 64 of 1024 x 512, 3 each, 16.5 and 19; 8 of 4096 x 14336, 4 each, 128 and 133); 8 waves
+// where the tokens' sums fill LDS.  Splits: until there are about 16 waves a CU,
+// each with 4 blocks or more (65 row blocks of 147 blocks: 18, 14 and 18 us with 1, 2 and 4).
+MoeShape moe_shape(uint64_t tokens, uint64_t pairs, uint64_t experts, uint64_t row_blocks, uint64_t col_blocks) {
+    MoeShape m;
+    experts = experts < pairs ? experts : pairs;
+    m.rows = tokens <= 64 && pairs >= 6 * experts ? 2 : 1;
+    m.waves = m.rows == 2 || tokens > 64 ? 8 : 16;
+    const uint64_t n = 4096 / (m.waves * ((row_blocks + m.rows - 1) / m.rows)), most = experts * col_blocks / (4 * m.waves);
+    m.splits = (uint32_t)(n < most ? n : most);
+    if (m.splits == 0) m.splits = 1;
+    return m;
+}
+
+// The first product: with few row blocks one pair of them a workgroup and eight
+// waves (384 of them, one token: 13 us against 16.5), else two and four, so that x is read
+// once for both (2048 of them, 64 tokens: 77 and 95); with more than 16 pairs of an
+// expert in sight two columns of tiles (16 each: 58 us against 72).
+template <bool GATED>
+hipError_t moe_up_any(const MoeParams &p, hipStream_t s) {
+    const uint64_t pairs = (uint64_t)p.tokens * p.k, experts = p.num < pairs ? p.num : pairs;
+    const bool wide = p.tokens > 16 && pairs > 4 * experts;
+    if (p.up.part_blocks * experts <= 768) return wide ? moe_up<2, 2, GATED, 8>(p, s) : moe_up<1, 2, GATED, 8>(p, s);
+    return wide ? moe_up<2, 4, GATED, 4>(p, s) : moe_up<1, 4, GATED, 4>(p, s);
 }
 
 hipError_t launch_moe_few(const MoeParams &p, hipStream_t s) {
-    hipError_t e;
-    const uint64_t pairs = (uint64_t)p.tokens * p.k, experts = p.num < pairs ? p.num : pairs, blocks = p.up.part_blocks * experts;
-    const bool one = p.tokens <= 16 || pairs <= 8 * experts;
-    if (p.act == kActSwiglu) {
-        if (one) e = blocks <= 768 ? moe_up<1, 2, true, 8>(p, s) : moe_up<1, 4, true, 4>(p, s);
-        else e = blocks <= 768 ? moe_up<2, 2, true, 8>(p, s) : moe_up<2, 4, true, 4>(p, s);
-    } else {
-        e = one ? moe_up<1, 2, false, 8>(p, s) : moe_up<2, 2, false, 8>(p, s);
-    }
+    const hipError_t e = p.act == kActSwiglu ? moe_up_any<true>(p, s) : moe_up_any<false>(p, s);
     if (e != hipSuccess) return e;
-    const dim3 grid(p.down.row_blocks, p.splits);
-    const uint32_t lds = 16 * p.tokens * 16 * 4;
-    if (p.tokens <= 8) k_moe_down<1, 16><<<grid, 1024, lds, s>>>(p);
-    else if (p.tokens <= 16) k_moe_down<2, 16><<<grid, 1024, lds, s>>>(p);
-    else k_moe_down<4, 16><<<grid, 1024, lds, s>>>(p);
-    return hipGetLastError();
+    const MoeShape m = moe_shape(p.tokens, (uint64_t)p.tokens * p.k, p.num, p.down.row_blocks, p.down.col_blocks);
+    if (m.rows == 2) return moe_down<2, 2, 8>(p, s);
+    if (m.waves == 8) return moe_down<2, 1, 8>(p, s);
+    return p.tokens <= 8 ? moe_down<1, 1, 16>(p, s) : moe_down<2, 1, 16>(p, s);
 }
 
 hipError_t launch_gather(const GatherParams &p, hipStream_t s) {

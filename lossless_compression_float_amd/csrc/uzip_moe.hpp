@@ -78,11 +78,13 @@ struct MoeParams {
     uint32_t up_rows, up_cols, down_rows, h_cols, h_stride;
     uint32_t bias_f32, y_f32, act, splits;
 };
-constexpr uint32_t kFewTokens = 64;
+constexpr uint32_t kFewTokens = 256, kFewPairs = 4096;
 
 hipError_t launch_moe_few(const MoeParams &p, hipStream_t s);
-// Workgroups that share a row block of down.
-uint32_t moe_splits(uint64_t down_blocks, uint64_t items);
+struct MoeShape {
+    uint32_t rows, waves, splits;  // row blocks and waves of a workgroup, workgroups that share them
+};
+MoeShape moe_shape(uint64_t tokens, uint64_t pairs, uint64_t experts, uint64_t row_blocks, uint64_t col_blocks);
 hipError_t launch_route(const RouteParams &p, hipStream_t s);
 uint32_t route_chunks(uint64_t tokens, uint64_t k);
 hipError_t launch_route_backward(const RouteBackwardParams &p, hipStream_t s);

@@ -85,10 +85,12 @@ bool moe_ok(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args 
     return mat_ok(a->x, a->x_stride, a->tokens, up->cols, 2) && mat_ok(a->y, a->y_stride, a->tokens, down->rows, size);
 }
 
-// Few tokens: two kernels.
-bool few(const uzip_weight *down, const uzip_moe_args *a) {
-    // (the pairs' activations, two bf16 values each, are addressed with 32 bits)
-    return a->tokens <= kFewTokens && a->tokens * a->k * 4 * uzip::up(down->cols, 64) < (1ull << 32) - 4096;
+// Few tokens: two kernels.  As for the products alone, up to 16 pairs an expert on average.
+bool few(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *a) {
+    const uint64_t pairs = a->tokens * a->k;
+    // (the pairs' activations, two bf16 values each, are addressed with 31 bits)
+    return a->tokens <= kFewTokens && pairs <= kFewPairs && pairs <= 16 * up->matrices &&
+           pairs * 4 * uzip::up(down->cols, 64) < 1ull << 31;
 }
 
 MoeParams plan_few(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *a, Carver &c) {
@@ -121,10 +123,11 @@ MoeParams plan_few(const uzip_weight *up, const uzip_weight *down, const uzip_mo
     p.y_f32 = a->y_dtype == UZIP_FP32;
     p.act = a->act;
     const uint64_t pairs = a->tokens * a->k;
-    p.splits = moe_splits(p.down.row_blocks, std::min<uint64_t>(up->matrices, pairs) * p.down.col_blocks);
+    const MoeShape m = moe_shape(a->tokens, pairs, up->matrices, p.down.row_blocks, p.down.col_blocks);
+    p.splits = m.splits;
     p.h = c.take<uint16_t>(pairs * 2 * p.h_stride);
     if (p.splits > 1) {
-        p.part = c.take<float>((uint64_t)p.splits * p.down.row_blocks * a->tokens * 16);
+        p.part = c.take<float>((uint64_t)p.splits * uzip::up(p.down.row_blocks, m.rows) * a->tokens * 16);
         p.arrived = c.take<uint32_t>(p.down.row_blocks);
     }
     return p;
@@ -250,7 +253,7 @@ uzip_status uzip_moe_route_backward(const uzip_moe_route_args *args, hipStream_t
 size_t uzip_moe_workspace_size(const uzip_weight *up, const uzip_weight *down, const uzip_moe_args *args) {
     if (!moe_ok(up, down, args) || args->tokens == 0) return 0;
     Carver c(nullptr);
-    if (few(down, args)) plan_few(up, down, args, c);
+    if (few(up, down, args)) plan_few(up, down, args, c);
     else plan_many(up, down, args, c);
     return (size_t)c.bytes();
 }
@@ -260,7 +263,7 @@ uzip_status uzip_moe(const uzip_weight *up, const uzip_weight *down, const uzip_
     if (!moe_ok(up, down, args)) return UZIP_ERR_INVALID_ARGUMENT;
     if (args->tokens == 0) return UZIP_OK;
     Carver c(d_workspace);
-    if (!few(down, args)) {
+    if (!few(up, down, args)) {
         const ManyPlan plan = plan_many(up, down, args, c);
         if (!workspace_ok(d_workspace, workspace_bytes, c.bytes())) return UZIP_ERR_INVALID_ARGUMENT;
         return run_many(up, down, args, plan, stream);

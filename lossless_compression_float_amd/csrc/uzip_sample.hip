@@ -16,6 +16,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "uzip_lanes.hpp"
 #include "uzip_sample.hpp"
 
 namespace uzip {
@@ -91,55 +92,6 @@ __device__ inline double weight(float z, float top, double scale) {
 // The same where the largest is finite and z not below 2^-1000 of it (there not 0).
 __device__ inline double weight_near(float z, float top, double scale) { return exp2_low(((double)z - (double)top) * scale); }
 
-// A value of another lane by DPP, zero where there is none.
-template <int CTRL, int ROWS = 15, class T>
-__device__ inline T moved(T v) {
-    if constexpr (sizeof(T) == 8) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        const uint64_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 15, false);
-        const uint64_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 15, false);
-        return __builtin_bit_cast(T, hi << 32 | lo);
-    } else {
-        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 15, false));
-    }
-}
-constexpr int kRowShift = 0x110, kWaveShift1 = 0x138, kRowLast = 0x142, kHalfLast = 0x143;
-template <class T>
-__device__ inline T lane_of(T v, uint32_t lane) {  // (lane uniform)
-    if constexpr (sizeof(T) == 8) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)u, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
-        return __builtin_bit_cast(T, hi << 32 | lo);
-    } else {
-        return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-    }
-}
-struct Sum {
-    template <class T>
-    __device__ static T of(T a, T b) { return a + b; }
-};
-struct Max {
-    template <class T>
-    __device__ static T of(T a, T b) { return a > b ? a : b; }
-};
-// Of the lanes up to this one (zero is the operation's neutral value).
-template <class OP, class T>
-__device__ inline T row_scan(T v) {  // within 16 lanes
-    v = OP::of(moved<kRowShift + 1>(v), v);
-    v = OP::of(moved<kRowShift + 2>(v), v);
-    v = OP::of(moved<kRowShift + 4>(v), v);
-    return OP::of(moved<kRowShift + 8>(v), v);
-}
-template <class OP, class T>
-__device__ inline T wave_scan(T v) {
-    v = row_scan<OP>(v);
-    v = OP::of(moved<kRowLast, 10>(v), v);
-    return OP::of(moved<kHalfLast, 12>(v), v);
-}
-template <class T>
-__device__ inline T wave_sum(T v) { return lane_of(wave_scan<Sum>(v), 63); }
-__device__ inline uint32_t wave_max(uint32_t v) { return lane_of(wave_scan<Max>(v), 63); }
-
 constexpr uint32_t kMaxHot = 2048;         // groups that are read again apart from the others
 constexpr uint32_t kMaxCandidates = 4096;  // tokens that are sorted
 constexpr uint32_t kMaxCells = kThreads;   // runs of 64 reads
@@ -162,19 +114,8 @@ struct Shared {
     uint64_t sorted[kMaxCandidates];
 };
 
-// The sum over the threads before this one, in a fixed order, and over all.
 template <class T>
-__device__ inline T block_scan(T v, T *lds, T &total) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const T x = wave_scan<Sum>(v), upto = moved<kWaveShift1>(x);
-    __syncthreads();
-    if (lane == 63) lds[wave] = x;
-    __syncthreads();
-    const T waves = row_scan<Sum>(lds[lane & (kWaves - 1)]);
-    total = lane_of(waves, kWaves - 1);
-    const uint32_t w = __builtin_amdgcn_readfirstlane(wave);
-    return w ? lane_of(waves, w - 1) + upto : upto;
-}
+__device__ inline T block_scan(T v, T *lds, T &total) { return scan_before<kWaves>(v, lds, total); }
 __device__ inline uint32_t block_max(uint32_t v, uint32_t *lds) {
     v = wave_max(v);
     __syncthreads();
