@@ -21,6 +21,7 @@ __device__ inline T moved(T v) {
         return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 15, false));
     }
 }
+constexpr int kNeighbour = 0xB1;  // lanes 0 and 1, 2 and 3, .. change places
 constexpr int kRowShift = 0x110, kWaveShift1 = 0x138, kRowLast = 0x142, kHalfLast = 0x143;
 template <class T>
 __device__ inline T lane_of(T v, uint32_t lane) {  // (lane uniform)

@@ -3,6 +3,8 @@
 // gradient, and of the expert layer around the grouped products.
 #include <stdint.h>
 
+#include <type_traits>
+
 #include <hip/hip_runtime.h>
 
 #include "uzip_lanes.hpp"
@@ -18,9 +20,9 @@ __device__ inline float logit(const void *p, uint64_t at, bool f32) {
     return f32 ? static_cast<const float *>(p)[at] : from_bf16(static_cast<const uint16_t *>(p)[at]);
 }
 
-// Unsigned keys in the order of the values.
+// Unsigned keys in the order of the values; both zeros are one value.
 __device__ inline uint32_t ordered(float v) {
-    const uint32_t u = __float_as_uint(v);
+    const uint32_t u = __float_as_uint(v + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ inline float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
@@ -28,8 +30,6 @@ __device__ inline uint64_t ordered(double v) {
     const uint64_t u = (uint64_t)__double_as_longlong(v);
     return u >> 63 ? ~u : u | 1ull << 63;
 }
-
-__device__ inline uint32_t wave_min(uint32_t v) { return ~wave_max(~v); }
 
 // The limit where the maximum is infinite: all of it shares alike.
 __device__ inline float exp_below(float z, float top) { return z == top ? 1.0f : expf(z - top); }
@@ -41,49 +41,50 @@ __device__ inline double sigmoid64(double z) { return 1.0 / (1.0 + exp(-z)); }
 // in 64 bits, since there neighbours could change places.
 template <int V, bool BIAS>
 __device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, int32_t &expert, float &weight) {
+    typedef std::conditional_t<BIAS, uint64_t, uint32_t> Key;
     float z[V];
     bool nan = false;
-    uint64_t key[V];
+    Key key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t e = i * 64 + lane;
         z[i] = e < p.num ? logit(p.logits, (uint64_t)t * p.stride + e, p.f32) : -INFINITY;
         nan |= z[i] != z[i];
-        const bool out = !(z[i] > -INFINITY);
+        key[i] = 0;
         if constexpr (BIAS) {
-            const double s = out ? -INFINITY : sigmoid64(z[i]) + (double)p.bias[e];
-            key[i] = s > -INFINITY ? ordered(s) : 0;
-        } else {
-            key[i] = out ? 0 : (uint64_t)ordered(z[i]) << 32 | (0xFFFFFFFFu - e);
+            if (z[i] > -INFINITY) {
+                const double s = sigmoid64(z[i]) + (double)p.bias[e];
+                key[i] = s > -INFINITY ? ordered(s) : 0;
+            }
+        } else if (z[i] > -INFINITY) {
+            key[i] = ordered(z[i]);
         }
     }
     nan = __any(nan);
     expert = -1;
     float mine = 0;
     for (uint32_t j = 0; j < p.k; ++j) {
-        uint64_t best = 0;
-        uint32_t at = 0;
+        Key best = key[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > best) best = key[i], at = i * 64 + lane;
-        const uint64_t top = wave_max(best);
+        for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
+        const Key top = wave_max(best);
         if (top == 0) break;
-        uint32_t e;
-        if constexpr (BIAS)
-            e = wave_min(best == top ? at : 0xFFFFFFFFu);
-        else
-            e = 0xFFFFFFFFu - (uint32_t)top;
+        uint32_t e = 0xFFFFFFFFu;  // the first that has it
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint64_t m = __ballot(key[i] == top);
+            if (m && e == 0xFFFFFFFFu) e = i * 64 + (uint32_t)__ffsll((unsigned long long)m) - 1;
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (e == i * 64 + lane) key[i] = 0;
         if (lane == j) {
             expert = (int32_t)e;
-            if constexpr (BIAS)
-                mine = logit(p.logits, (uint64_t)t * p.stride + e, p.f32);
-            else
-                mine = unordered((uint32_t)(top >> 32));
+            if constexpr (!BIAS) mine = unordered(top);
         }
     }
+    if constexpr (BIAS)
+        if (expert >= 0) mine = logit(p.logits, (uint64_t)t * p.stride + expert, p.f32);
     const bool on = expert >= 0;
     if (p.sigmoid) {
         // (64 bits: scores of very negative logits keep their ratio)
@@ -118,8 +119,8 @@ __device__ inline void given(const RouteParams &p, uint32_t t, uint32_t lane, in
     const int32_t was = expert;
     const float w = weight;
     for (uint32_t j = 0; j < p.k; ++j) {
-        const int32_t e = __shfl(was, j);
-        const float x = __shfl(w, j);
+        const int32_t e = lane_of(was, j);
+        const float x = lane_of(w, j);
         if (e != was || was < 0 || j == lane) continue;
         if (j < lane) again = true;
         else weight += x;
@@ -135,32 +136,17 @@ __device__ inline void choose_any(const RouteParams &p, uint32_t t, uint32_t lan
     else choose<V, false>(p, t, lane, expert, weight);
 }
 
-// Exclusive prefix of a workgroup's 1,024 values.
-__device__ inline uint32_t scan1024(uint32_t v, uint32_t *lds) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t x = v;
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t y = __shfl_up(x, d);
-        if (lane >= (uint32_t)d) x += y;
-    }
-    if (lane == 63) lds[wave] = x;
-    __syncthreads();
-    uint32_t before = 0;
-    for (uint32_t i = 0; i < wave; ++i) before += lds[i];
-    return before + x - v;
-}
-
 // Pairs [p0, p1) to their places: base[e] is the next one of expert e.  Waves
 // take turns, 64 pairs each, so that an expert's pairs keep their order.
-template <class E>
-__device__ inline void place(const RouteParams &p, E expert_of, uint32_t p0, uint32_t p1, uint32_t *base) {
+template <uint32_t NT>
+__device__ inline void place(const RouteParams &p, uint32_t p0, uint32_t p1, uint32_t *base) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t bits = 1;
     while (p.num >> bits) ++bits;
-    for (uint32_t r = p0; r < p1; r += 1024) {
+    for (uint32_t r = p0; r < p1; r += NT) {
         const uint32_t pair = r + wave * 64 + lane;
         const bool on = pair < p1;
-        const int32_t x = on ? expert_of(pair) : -1;
+        const int32_t x = on ? p.experts[pair] : -1;
         const uint32_t e = x < 0 ? p.num : (uint32_t)x;
         uint64_t same = __ballot(on);
         for (uint32_t b = 0; b < bits; ++b) {
@@ -168,7 +154,7 @@ __device__ inline void place(const RouteParams &p, E expert_of, uint32_t p0, uin
             same &= e >> b & 1 ? m : ~m;
         }
         const uint32_t before = __popcll(same & ((1ull << lane) - 1));
-        const uint32_t turns = min((p1 - r + 63) / 64, 16u);
+        const uint32_t turns = min((p1 - r + 63) / 64, NT / 64);
         for (uint32_t turn = 0; turn < turns; ++turn) {
             if (turn == wave && on) {
                 const uint32_t at = base[e];
@@ -182,15 +168,15 @@ __device__ inline void place(const RouteParams &p, E expert_of, uint32_t p0, uin
 
 // Few pairs, or one chunk of many: choice and counts (CHOOSE), then the places
 // (PLACE), which need the counts of the chunks before.
-template <int V, bool CHOOSE, bool PLACE>
-__global__ __launch_bounds__(1024) void k_route(RouteParams p) {
-    __shared__ uint32_t count[kMaxExperts + 1], base[kMaxExperts + 1], lds[16];
+template <int V, bool CHOOSE, bool PLACE, uint32_t NT>
+__global__ __launch_bounds__(NT) void k_route(RouteParams p) {
+    __shared__ uint32_t count[kMaxExperts + 1], base[kMaxExperts + 1], waves[NT / 64];
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t t0 = min(blockIdx.x * p.chunk, p.tokens), t1 = min(t0 + p.chunk, p.tokens);
-    for (uint32_t e = threadIdx.x; e <= p.num; e += 1024) count[e] = base[e] = 0;
+    for (uint32_t e = threadIdx.x; e <= p.num; e += NT) count[e] = base[e] = 0;
     __syncthreads();
     if constexpr (CHOOSE) {
-        for (uint32_t t = t0 + wave; t < t1; t += 16) {
+        for (uint32_t t = t0 + wave; t < t1; t += NT / 64) {
             int32_t e;
             float w;
             choose_any<V>(p, t, lane, e, w);
@@ -202,15 +188,15 @@ __global__ __launch_bounds__(1024) void k_route(RouteParams p) {
         }
         __syncthreads();
         if constexpr (!PLACE)
-            for (uint32_t e = threadIdx.x; e <= p.num; e += 1024) p.counts[(uint64_t)blockIdx.x * (p.num + 1) + e] = (int32_t)count[e];
+            for (uint32_t e = threadIdx.x; e <= p.num; e += NT) p.counts[(uint64_t)blockIdx.x * (p.num + 1) + e] = (int32_t)count[e];
     } else {
         // count: pairs of all chunks, base: of those before this one
         uint32_t wide = 1;
         while (wide < p.num + 1) wide *= 2;
-        const uint32_t runs = wide < 1024 ? 1024 / wide : 1;
-        for (uint32_t e = threadIdx.x & (wide - 1); e <= p.num; e += 1024) {
+        const uint32_t runs = wide < NT ? NT / wide : 1;
+        for (uint32_t e = threadIdx.x & (wide - 1); e <= p.num; e += NT) {
             uint32_t all = 0, before = 0;
-            for (uint32_t c = wide < 1024 ? threadIdx.x / wide : 0; c < p.chunks; c += runs) {
+            for (uint32_t c = wide < NT ? threadIdx.x / wide : 0; c < p.chunks; c += runs) {
                 const uint32_t n = (uint32_t)p.counts[(uint64_t)c * (p.num + 1) + e];
                 all += n;
                 before += c < blockIdx.x ? n : 0;
@@ -221,19 +207,19 @@ __global__ __launch_bounds__(1024) void k_route(RouteParams p) {
         __syncthreads();
     }
     if constexpr (PLACE) {
-        const uint32_t start = scan1024(threadIdx.x < p.num ? count[threadIdx.x] : 0, lds);
+        // (a thread an expert: a small workgroup has no more)
+        uint32_t with;
+        const uint32_t start = scan_before<NT / 64>(threadIdx.x < p.num ? count[threadIdx.x] : 0u, waves, with);
         if (threadIdx.x < p.num) {
             base[threadIdx.x] += start;
             if (blockIdx.x == 0) p.offsets[threadIdx.x] = (int32_t)start;
         }
-        const uint32_t none = p.tokens * p.k - count[p.num];
         if (threadIdx.x == 0) {
-            base[p.num] += none;
-            if (blockIdx.x == 0) p.offsets[p.num] = (int32_t)none;
+            base[p.num] += with;
+            if (blockIdx.x == 0) p.offsets[p.num] = (int32_t)with;
         }
         __syncthreads();
-        const int32_t *experts = p.experts;
-        place(p, [=](uint32_t pair) { return experts[pair]; }, t0 * p.k, t1 * p.k, base);
+        place<NT>(p, t0 * p.k, t1 * p.k, base);
     }
 }
 
@@ -254,7 +240,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
         top = fmaxf(top, z[i]);
     }
     nan = __any(nan);
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    top = unordered(wave_max(ordered(top)));
     int32_t expert = lane < p.k ? p.experts[(uint64_t)t * p.k + lane] : -1;
     if (expert >= (int32_t)p.num) expert = -1;
     const bool on = expert >= 0;
@@ -291,8 +277,8 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
         for (int i = 0; i < V; ++i) out[i] = 0;
     }
     for (uint32_t j = 0; j < p.k; ++j) {
-        const int32_t e = __shfl(expert, j);
-        const float d = __shfl(dz, j);
+        const int32_t e = lane_of(expert, j);
+        const float d = lane_of(dz, j);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (e == (int32_t)(i * 64 + lane)) out[i] = d;
@@ -572,11 +558,15 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
 // of the workgroups that share RB row blocks.  Columns 2 i and 2 i + 1 of the
 // matrix instruction are the two values of pair i; an expert with more than 8 CT
 // pairs comes several times.  A wave's blocks follow one another without a
-// pause over the experts, one on its way (with two the registers cost as much as
-// they gain); when it leaves an expert, it adds its results to its own sums of the pairs' tokens in LDS.  The waves' sums are
+// pause over the experts, DEPTH on their way (two with 8 waves, where they gain
+// 2 to 5%; with 16 the registers cost as much); when it leaves an expert, it adds
+// its results to its own sums of the pairs' tokens in LDS.  The waves' sums are
 // added in a fixed order, and the splits' by the workgroup that comes last.
+// Bound by the reads of D where experts are large (8 of 4096 x 14336, 16 tokens:
+// 128 us, 5.6 TB/s of packed bytes), by the turns of the waves where they are small (64 of
+// 2048 x 1024, 64 tokens: 53 us, 3.9 TB/s).
 constexpr uint32_t kMaxVisits = kMaxExperts + kFewPairs / 8;
-template <int CT, int RB, int NW>
+template <int CT, int RB, int NW, int DEPTH>
 __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
     extern __shared__ float sums[];                 // [NW][RB][tokens][16]
     __shared__ uint32_t visits[kMaxVisits];         // expert, first pair << 10, pairs - 1 << 23
@@ -634,7 +624,7 @@ __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
     struct Stage {
         Tile tile[RB];
         uint4 x[CT][2];
-    } stage;
+    } stage[DEPTH];
     auto load = [&](Stage &s, uint32_t i) __attribute__((always_inline)) {
         if (kb == KB) {
             kb = 0;
@@ -654,11 +644,11 @@ __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
         kb += i + 1 < n;  // (behind the last block: that again, for nothing)
     };
     // what is multiplied
-    uint32_t done_visit = visit, done_kb = kb, entered = kb, have = 0, s0 = 0, expert = 0;
+    uint32_t done_visit = visit, done_kb = kb, have = 0, s0 = 0;
     f32x4 acc[RB][CT];
     auto start = [&]() __attribute__((always_inline)) {
         const uint32_t v = uniform(visits[min(done_visit, entries - 1)]);
-        expert = v & 1023, s0 = v >> 10 & 0x1FFF, have = (v >> 23) + 1;
+        s0 = v >> 10 & 0x1FFF, have = (v >> 23) + 1;
 #pragma unroll
         for (int i = 0; i < RB; ++i)
             for (int j = 0; j < CT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
@@ -668,23 +658,12 @@ __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
         for (int j = 0; j < CT; ++j) {
             if (j && (uint32_t)j * 8 >= have) continue;
             const uint32_t slot = j * 8 + r / 2, token = slot < have ? token_of[s0 + slot] : 0xFFFF;
-            const bool on = token < p.tokens;
-            // the wave that has an expert's first block adds its bias
-            const bool biased = p.down_bias && entered == 0;
-            const float g = biased && on ? p.weights[p.order[s0 + slot]] : 0.0f;
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 f32x4 s = acc[i][j];
 #pragma unroll
-                for (int d = 0; d < 4; ++d) s[d] += __shfl_xor(s[d], 1);
-                if (!on || (r & 1)) continue;
-                const uint32_t m = (block + i) * 16 + q * 4;
-                if (biased && m < p.down_rows) {
-                    float b[4];
-                    uzip::load<4>(p.down_bias, (uint64_t)expert * p.down_rows + m, p.bias_f32, min(p.down_rows - m, 4u), b);
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) s[d] += g * b[d];
-                }
+                for (int d = 0; d < 4; ++d) s[d] += moved<kNeighbour>(s[d]);
+                if (token >= p.tokens || (r & 1)) continue;
                 f32x4 *to = mine + (i * p.tokens + token) * 4 + q;
                 *to = *to + s;
             }
@@ -694,7 +673,7 @@ __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
     auto multiply = [&](Stage &s, uint32_t i) __attribute__((always_inline)) {
         if (done_kb == KB) {
             leave();
-            done_kb = entered = 0;
+            done_kb = 0;
             ++done_visit;
             start();
         }
@@ -730,18 +709,39 @@ __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
         start();
         enter();
         load_heads(0);  // (first: loads come back in order)
-        load(stage, 0);
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u) load(stage[u], u);
         for (uint32_t i0 = 0; i0 < n; i0 += 64) {
             if (i0) load_heads(i0);
 #pragma unroll
             for (int d = 0; d < RB; ++d) heads[d] = head_checked(p.down, heads[d]);
             const uint32_t end = min(n, i0 + 64);
-            for (uint32_t i = i0; i < end; ++i) {
-                multiply(stage, i);
-                load(stage, i + 1);
+            for (uint32_t i = i0; i < end; i += DEPTH) {
+#pragma unroll
+                for (int u = 0; u < DEPTH; ++u) {
+                    if (u == 0 || i + u < end) multiply(stage[u], i + u);
+                    load(stage[u], i + u + DEPTH);
+                }
             }
         }
         leave();
+    }
+    if (p.down_bias && blockIdx.y == 0) {  // each pair's by its weight
+        for (uint32_t v = wave; v < entries; v += NW) {
+            const uint32_t x = visits[v], first_pair = x >> 10 & 0x1FFF, pairs_here = (x >> 23) + 1;
+            for (uint32_t c = 0; c < pairs_here; ++c) {
+                const uint32_t token = token_of[first_pair + c];
+                if (token >= p.tokens) continue;
+                const float g = p.weights[p.order[first_pair + c]];
+                for (uint32_t u = lane; u < RB * 16; u += 64) {
+                    const uint32_t m = block * 16 + u;
+                    if (m >= p.down_rows) continue;
+                    const uint64_t from = (uint64_t)(x & 1023) * p.down_rows + m;
+                    const float b = p.bias_f32 ? static_cast<const float *>(p.down_bias)[from] : from_bf16(static_cast<const uint16_t *>(p.down_bias)[from]);
+                    reinterpret_cast<float *>(mine)[((u / 16) * p.tokens + token) * 16 + u % 16] += g * b;
+                }
+            }
+        }
     }
     __syncthreads();
     auto finish = [&](uint32_t u, f32x4 s) {
@@ -789,10 +789,10 @@ __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
     }
 }
 
-template <int CT, int RB, int NW>
+template <int CT, int RB, int NW, int DEPTH = 1>
 hipError_t moe_down(const MoeParams &p, hipStream_t s) {
     const dim3 grid((p.down.row_blocks + RB - 1) / RB, p.splits);
-    k_moe_down<CT, RB, NW><<<grid, NW * 64, NW * RB * p.tokens * 64, s>>>(p);
+    k_moe_down<CT, RB, NW, DEPTH><<<grid, NW * 64, NW * RB * p.tokens * 64, s>>>(p);
     return hipGetLastError();
 }
 
@@ -805,20 +805,21 @@ hipError_t moe_up(const MoeParams &p, hipStream_t s) {
 
 template <int V>
 hipError_t route(const RouteParams &p, hipStream_t s) {
-    if (p.chunks == 1) {
-        k_route<V, true, true><<<1, 1024, 0, s>>>(p);
-        return hipGetLastError();
+    if (p.chunks > 1) {
+        k_route<V, true, false, 1024><<<p.chunks, 1024, 0, s>>>(p);
+        k_route<V, false, true, 1024><<<p.chunks, 1024, 0, s>>>(p);
+    } else if (p.tokens <= 4 && p.num <= 256) {
+        k_route<V, true, true, 256><<<1, 256, 0, s>>>(p);
+    } else {
+        k_route<V, true, true, 1024><<<1, 1024, 0, s>>>(p);
     }
-    k_route<V, true, false><<<p.chunks, 1024, 0, s>>>(p);
-    k_route<V, false, true><<<p.chunks, 1024, 0, s>>>(p);
     return hipGetLastError();
 }
 
 }  // namespace
 
-uint32_t route_chunks(uint64_t tokens, uint64_t k) {
-    (void)k;
-    if (tokens <= 64) return 1;
+uint32_t route_chunks(uint64_t tokens) {
+    if (tokens <= kRouteOnce) return 1;
     const uint64_t n = (tokens + 15) / 16;  // a token a wave
     return (uint32_t)(n < kRouteChunks ? n : kRouteChunks);
 }
@@ -843,16 +844,17 @@ hipError_t launch_route_backward(const RouteBackwardParams &p, hipStream_t s) {
 // How many workgroups, of how many waves and row blocks, the second product
 // takes.  Row blocks: one with 16 waves; two with 8, which read h once for both,
 // where an expert has many pairs (in us, one and two: 64 tokens, 64 experts of 2048 x
-// 1024, 8 pairs each, 58 and 56; 8 experts of 4096 x 2048, 16 each, 50 and 41; but
-// 64 of 1024 x 512, 3 each, 16.5 and 19; 8 of 4096 x 14336, 4 each, 128 and 133); 8 waves
-// where the tokens' sums fill LDS.  Splits: until there are about 16 waves a CU,
-// each with 4 blocks or more (65 row blocks of 147 blocks: 18, 14 and 18 us with 1, 2 and 4).
+// 1024, 8 pairs each, 58 and 53; 128 tokens, 16 of 4096 x 4096, 16 each, 159 and 116; but
+// 64 of 1024 x 512, 3 each, 16.5 and 19; 8 of 4096 x 14336, 4 each, 128 and 134); 8 waves
+// too where the tokens' sums fill LDS.  Splits: until there are 16 waves a CU (8
+// of the others), each with 4 blocks or more (65 row blocks of 147 blocks:
+// 18, 14 and 18 us with 1, 2 and 4 splits).
 MoeShape moe_shape(uint64_t tokens, uint64_t pairs, uint64_t experts, uint64_t row_blocks, uint64_t col_blocks) {
     MoeShape m;
     experts = experts < pairs ? experts : pairs;
-    m.rows = tokens <= 64 && pairs >= 6 * experts ? 2 : 1;
+    m.rows = tokens <= 128 && pairs >= 6 * experts ? 2 : 1;
     m.waves = m.rows == 2 || tokens > 64 ? 8 : 16;
-    const uint64_t n = 4096 / (m.waves * ((row_blocks + m.rows - 1) / m.rows)), most = experts * col_blocks / (4 * m.waves);
+    const uint64_t n = (m.waves == 8 ? 2048 : 4096) / (m.waves * ((row_blocks + m.rows - 1) / m.rows)), most = experts * col_blocks / (4 * m.waves);
     m.splits = (uint32_t)(n < most ? n : most);
     if (m.splits == 0) m.splits = 1;
     return m;
@@ -874,8 +876,8 @@ hipError_t launch_moe_few(const MoeParams &p, hipStream_t s) {
     const hipError_t e = p.act == kActSwiglu ? moe_up_any<true>(p, s) : moe_up_any<false>(p, s);
     if (e != hipSuccess) return e;
     const MoeShape m = moe_shape(p.tokens, (uint64_t)p.tokens * p.k, p.num, p.down.row_blocks, p.down.col_blocks);
-    if (m.rows == 2) return moe_down<2, 2, 8>(p, s);
-    if (m.waves == 8) return moe_down<2, 1, 8>(p, s);
+    if (m.rows == 2) return moe_down<2, 2, 8, 2>(p, s);
+    if (m.waves == 8) return moe_down<2, 1, 8, 2>(p, s);
     return p.tokens <= 8 ? moe_down<1, 1, 16>(p, s) : moe_down<2, 1, 16>(p, s);
 }
 

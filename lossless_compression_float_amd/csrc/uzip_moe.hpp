@@ -13,6 +13,7 @@ namespace uzip {
 constexpr uint32_t kMaxExperts = 1024;  // a wave holds a token's scores, 16 a lane
 constexpr uint32_t kMaxChosen = 64;     // and its choice, one a lane
 constexpr uint32_t kRouteChunks = 256;
+constexpr uint32_t kRouteOnce = 32;  // tokens that one workgroup routes
 
 struct RouteParams {
     const void *logits;  // null: experts and weights are given, and only grouped
@@ -86,7 +87,7 @@ struct MoeShape {
 };
 MoeShape moe_shape(uint64_t tokens, uint64_t pairs, uint64_t experts, uint64_t row_blocks, uint64_t col_blocks);
 hipError_t launch_route(const RouteParams &p, hipStream_t s);
-uint32_t route_chunks(uint64_t tokens, uint64_t k);
+uint32_t route_chunks(uint64_t tokens);
 hipError_t launch_route_backward(const RouteBackwardParams &p, hipStream_t s);
 hipError_t launch_gather(const GatherParams &p, hipStream_t s);
 hipError_t launch_combine(const CombineParams &p, hipStream_t s);

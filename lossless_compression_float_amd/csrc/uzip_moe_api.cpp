@@ -60,7 +60,7 @@ RouteParams plan_route(const uzip_moe_route_args *a, Carver &c) {
     p.f32 = a->logits_dtype == UZIP_FP32;
     p.sigmoid = a->scores == UZIP_SCORES_SIGMOID;
     p.renorm = a->renormalize;
-    p.chunks = route_chunks(a->tokens, a->k);
+    p.chunks = route_chunks(a->tokens);
     p.chunk = (uint32_t)blocks(a->tokens, p.chunks);
     if (p.chunks > 1) p.counts = c.take<int32_t>((uint64_t)p.chunks * (p.num + 1));
     return p;

@@ -247,8 +247,12 @@ def moe(x, routing: Routing, up: PackedWeight, down: PackedWeight, act: str = "s
     with gated=True for swiglu; down: packed stack of D, [experts, out_cols,
     rows], for swiglu [experts, out_cols, rows / 2].  The result is bf16, or
     out_dtype; residual has its shape and type; out may be the residual, and
-    must not overlap x.  The activations between the products are bf16.  The
-    biases have one type, bf16 or fp32."""
+    must not overlap x.  The biases have one type, bf16 or fp32.
+
+    Up to 256 tokens (4,096 pairs, 16 an expert on average) take two kernels
+    and keep the activations between the products to 2^-17 of themselves; more
+    go through gathered rows and ``grouped_linear``, with activations in
+    bf16."""
     r = _routing(routing, "moe")
     _weight(up, "moe", 3)
     _weight(down, "moe", 3)
@@ -287,7 +291,9 @@ def moe(x, routing: Routing, up: PackedWeight, down: PackedWeight, act: str = "s
         if residual is not None and _overlap(out, residual) and (
                 out.data_ptr() != residual.data_ptr() or a.y_stride != a.residual_stride):
             raise ValueError("out must be the residual itself or not overlap it")
-    _no_history("moe", x, r.weights, up_bias, down_bias, residual, out)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, r.weights, up_bias, down_bias, residual, out)):
+        raise ValueError("moe records nothing for autograd, and an argument requires grad: call it under torch.no_grad(); for "
+                         "training multiply by grouped_linear, which has its gradients, in a torch.autograd.Function")
     caller, given = _caller(device, stream), out
     with _on(device, stream):
         if out is None:

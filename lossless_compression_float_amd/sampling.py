@@ -54,6 +54,12 @@ def _row(v, what: str, rows: int, device, dtype) -> int:
     return v.data_ptr()
 
 
+def _device(t):
+    if not t.is_cuda:
+        raise ValueError("sample needs device tensors")
+    return t.device
+
+
 def _number(v, what: str) -> float:
     if isinstance(v, bool) or not isinstance(v, (int, float)) or v != v:
         raise TypeError("%s must be a number or a tensor, not %r" % (what, v))
@@ -83,9 +89,7 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ws=None, s
     code = _code(logits.dtype, "logits")
     if logits.dim() != 2 or logits.shape[1] == 0:
         raise ValueError("logits must have shape [rows, vocab], not %s" % list(logits.shape))
-    if not logits.is_cuda:
-        raise ValueError("sample needs device tensors")
-    device, (rows, vocab) = logits.device, logits.shape
+    device, (rows, vocab) = _device(logits), logits.shape
     if u.dtype not in (torch.float32, torch.float64):
         raise TypeError("u must be float32 or float64, not %s" % u.dtype)
     if u.shape != (rows,) or u.device != device or not u.is_contiguous():
@@ -112,6 +116,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ws=None, s
             if not 0 <= v <= 1:
                 raise ValueError("%s must be from 0 to 1, not %r" % (name, v))
             setattr(a, name + "_all", v)
+    if logits.requires_grad and torch.is_grad_enabled():
+        raise ValueError("sample records nothing for autograd, and logits requires grad: call it under torch.no_grad()")
     caller = _caller(device, stream)
     with _on(device, stream):
         token = torch.empty(rows, dtype=torch.int64, device=device)
