@@ -35,7 +35,7 @@ __device__ inline uint32_t ordered(float v) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ inline float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
-constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;  // of -inf; NaNs have keys below it or above that of +inf
+constexpr uint32_t kKeyMinusInf = 0x007FFFFFu, kKeyInf = 0xFF800000u;  // NaNs have keys beyond them
 
 __device__ inline float value(const void *p, uint64_t at, bool f32) {
     return f32 ? static_cast<const float *>(p)[at] : __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[at] << 16);
@@ -45,8 +45,9 @@ __device__ inline float value(const void *p, uint64_t at, bool f32) {
 // and 1 + f q(f) with q the polynomial of degree 8 whose largest relative error
 // is smallest there (least squares, weighted until it stops falling).  Below -1000 anything tiny.
 __device__ inline double exp2_low(double x) {
+    constexpr double ROUND = 6755399441055744.0;  // 1.5 2^52: added, it leaves n in the low bits
     x = fmax(x, -1000.0);
-    const double n = rint(x), f = x - n;
+    const double n = x + ROUND, f = x - (n - ROUND);
     double p = 1.01483365409060702e-07;
     p = p * f + 1.32583358083804669e-06;
     p = p * f + 1.52529900401267599e-05;
@@ -57,7 +58,7 @@ __device__ inline double exp2_low(double x) {
     p = p * f + 2.40226506957228025e-01;
     p = p * f + 6.93147180559885112e-01;
     p = p * f + 1.0;
-    return ldexp(p, (int)n);
+    return __longlong_as_double(__double_as_longlong(p) + (int64_t)((uint64_t)__double_as_longlong(n) << 52));
 }
 
 // What a row asks for, read once.
@@ -94,7 +95,8 @@ __device__ inline double weight_near(float z, float top, double scale) { return 
 
 constexpr uint32_t kMaxHot = 2048;         // groups that are read again apart from the others
 constexpr uint32_t kMaxCandidates = 4096;  // tokens that are sorted
-constexpr uint32_t kMaxCells = kThreads;   // runs of 64 reads
+constexpr uint32_t kReads = 4, kCell = 64 * kReads;  // of a lane at a time, of a wave: a run
+constexpr uint32_t kMaxCells = kThreads;             // runs
 constexpr uint32_t kBins = 1024, kCoarse = kBins / 4;
 
 struct Shared {
@@ -287,23 +289,35 @@ __device__ inline void by_histograms(const SampleParams &p, uint32_t r, const Ro
 
 // ---- the survey ---------------------------------------------------------------------
 
-// W consecutive values from token i on, -inf behind the last.
+// 16 bytes of values from token i on, -inf behind the last.
+template <bool F32>
+__device__ inline u32x4 read_raw(const SampleParams &p, uint64_t at, uint32_t i) {
+    constexpr uint32_t W = F32 ? 4 : 8;
+    if (i + W <= p.vocab)
+        return F32 ? __builtin_bit_cast(u32x4, *reinterpret_cast<const f32x4_any *>(static_cast<const float *>(p.logits) + at + i))
+                   : (u32x4) * reinterpret_cast<const u32x4_any *>(static_cast<const uint16_t *>(p.logits) + at + i);
+    u32x4 x;
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c) {
+        if constexpr (F32) {
+            x[c] = i + c < p.vocab ? static_cast<const uint32_t *>(p.logits)[at + i + c] : 0xFF800000u;
+        } else {
+            const uint16_t *s = static_cast<const uint16_t *>(p.logits) + at + i + 2 * c;
+            const uint32_t lo = i + 2 * c < p.vocab ? s[0] : 0xFF80u, hi = i + 2 * c + 1 < p.vocab ? s[1] : 0xFF80u;
+            x[c] = lo | hi << 16;
+        }
+    }
+    return x;
+}
+template <bool F32, int W = F32 ? 4 : 8>
+__device__ inline void unpack(u32x4 x, float v[W]) {
+#pragma unroll
+    for (int c = 0; c < W; ++c)
+        v[c] = F32 ? __uint_as_float(x[c & 3]) : __uint_as_float(c & 1 ? x[c / 2 & 3] & 0xFFFF0000u : x[c / 2 & 3] << 16);
+}
 template <bool F32, int W = F32 ? 4 : 8>
 __device__ inline void read_values(const SampleParams &p, uint64_t at, uint32_t i, float v[W]) {
-    if (i + W <= p.vocab) {
-        if constexpr (F32) {
-            const f32x4 x = *reinterpret_cast<const f32x4_any *>(static_cast<const float *>(p.logits) + at + i);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = x[c];
-        } else {
-            const u32x4 x = *reinterpret_cast<const u32x4_any *>(static_cast<const uint16_t *>(p.logits) + at + i);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = __uint_as_float(c & 1 ? x[c / 2] & 0xFFFF0000u : x[c / 2] << 16);
-        }
-        return;
-    }
-#pragma unroll
-    for (int c = 0; c < W; ++c) v[c] = i + c < p.vocab ? value(p.logits, at + i + c, F32) : -INFINITY;
+    unpack<F32>(read_raw<F32>(p, at, i), v);
 }
 
 // A wave a segment of 2,048 tokens: its largest value, the sum of its weights
@@ -329,9 +343,9 @@ __global__ __launch_bounds__(256) void k_survey(SampleParams p) {
 #pragma unroll
         for (int i = h * HALF; i < (h + 1) * HALF; ++i)
 #pragma unroll
-            for (int c = 0; c < W; ++c) {
-                nan |= v[i][c] != v[i][c];
-                group[h] = fmaxf(group[h], v[i][c]);
+            for (int c = 0; c < W; c += 2) {
+                nan |= __builtin_isunordered(v[i][c], v[i][c + 1]);
+                group[h] = fmaxf(group[h], fmaxf(v[i][c], v[i][c + 1]));
             }
         p.groups[(n * 2 + h) * 64 + lane] = group[h];
     }
@@ -377,6 +391,21 @@ struct Bins {
 };
 __device__ inline uint32_t bin_of(const Bins &b, float z) {
     return z >= b.floor ? min((uint32_t)((b.top - z) * b.inv), kBins - 1) : kBins;
+}
+
+// The least value whose bin is at most `bin` (above infinity: none has it), by a
+// wave that tries 64 keys at a time.
+__device__ inline float least_of_bin(const Bins &b, uint32_t bin) {
+    const uint32_t lane = threadIdx.x & 63;
+    uint64_t lo = kKeyMinusInf;  // too low
+    for (int shift = 26; shift > -6; shift -= 6) {
+        const uint64_t step = shift > 0 ? 1ull << shift : 1;
+        const uint64_t k = lo + (lane + 1) * step;
+        const float z = k <= kKeyInf ? unordered((uint32_t)k) : INFINITY;
+        const uint64_t low = __ballot(k < kKeyInf && !(z <= b.top && bin_of(b, z) <= bin) && z < b.top);
+        lo += (uint64_t)__popcll(low) * step;
+    }
+    return lo + 1 >= kKeyInf ? INFINITY : unordered((uint32_t)(lo + 1));
 }
 
 // The reads that hold every token of the first `last` + 1 coarse bins, by
@@ -631,98 +660,128 @@ __device__ inline bool by_sorting(const SampleParams &p, uint32_t r, const Row &
     return true;
 }
 
-// Four reads of a thread, 1,024 apart.
-template <bool F32, uint32_t W = F32 ? 4 : 8>
-__device__ inline void four_reads(const SampleParams &p, uint64_t at, const Shared &s, const Reads &q, uint32_t j0, float (&v)[4][W],
-                                  uint32_t (&first)[4]) {
+// A lane's reads of its wave's run, all on their way at once.
+template <bool F32>
+__device__ inline void run_reads(const SampleParams &p, uint64_t at, const Shared &s, const Reads &q, uint32_t run, u32x4 (&x)[kReads]) {
 #pragma unroll
-    for (uint32_t u = 0; u < 4; ++u) {
-        const uint32_t j = j0 + u * kThreads + threadIdx.x;
-        first[u] = j < q.count ? read_at<F32>(s, q, j) : p.vocab;
-        read_values<F32>(p, at, first[u], v[u]);
+    for (uint32_t u = 0; u < kReads; ++u) {
+        const uint32_t j = run * kCell + u * 64 + (threadIdx.x & 63);
+        x[u] = read_raw<F32>(p, at, j < q.count ? read_at<F32>(s, q, j) : p.vocab);
     }
+}
+
+// The sums of the tokens from z1 on by runs of reads (of those that min_p
+// keeps), this thread's part of all of them, and the tokens from z0 to below z1
+// as a list.
+template <bool F32, bool MIN_P>
+__device__ inline double sum_runs(const SampleParams &p, uint64_t at, const Reads &q, float top, const Row &row, float z0, float z1,
+                                  Shared &s) {
+    constexpr uint32_t W = F32 ? 4 : 8;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (threadIdx.x == 0) s.pick_count = 0;
+    __syncthreads();
+    double above = 0;
+    for (uint32_t run = wave; run * kCell < q.count; run += kWaves) {
+        u32x4 x[kReads];
+        run_reads<F32>(p, at, s, q, run, x);
+        double sum = 0;
+#pragma unroll
+        for (uint32_t u = 0; u < kReads; ++u) {
+            float v[W];
+            unpack<F32>(x[u], v);
+            float most = v[0];
+#pragma unroll
+            for (uint32_t c = 1; c < W; ++c) most = fmaxf(most, v[c]);
+            if (__any(most >= z1)) {
+#pragma unroll
+                for (uint32_t c = 0; c < W; ++c) {
+                    const double w = weight_near(v[c], top, row.scale), e = v[c] >= z1 ? w : 0.0;
+                    if constexpr (MIN_P) {
+                        above += e;
+                        sum += e >= row.min_p ? e : 0.0;
+                    } else {
+                        sum += e;
+                    }
+                }
+            }
+            if (__any(most >= z0)) {
+#pragma unroll
+                for (uint32_t c = 0; c < W; ++c)
+                    if (v[c] >= z0 && v[c] < z1) {
+                        const uint32_t place = atomicAdd(&s.pick_count, 1u), first = read_at<F32>(s, q, run * kCell + u * 64 + lane);
+                        if (place < kMaxCandidates) s.tokens[place] = (uint64_t)ordered(v[c]) << 32 | (kNone - (first + c));
+                    }
+            }
+        }
+        if constexpr (!MIN_P) above += sum;
+        sum = wave_sum(sum);
+        if (lane == 0) s.cell[run] = sum;
+    }
+    __syncthreads();
+    return above;
 }
 
 // Rows with top-p or min-p alone.  A histogram of the weights, in fp32, tells
 // the bin in which top-p ends; then the sums before that bin in 64 bits, by
-// runs of 64 reads, beside the list of the bin's tokens, whose order gives the
-// border.  False if the histogram missed the bin, or holds too many there.
+// runs of reads, beside the list of the bin's tokens, whose order gives the
+// border.  Should the histogram's rounding have missed the bin, it is the next
+// one.  False if that holds too many tokens.
 template <bool F32>
 __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all, uint32_t least,
                                Groups &g, Shared &s) {
     constexpr uint32_t W = F32 ? 4 : 8;
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t wave = threadIdx.x >> 6;
     const uint64_t at = (uint64_t)r * p.stride;
     const float top = bins.top;
     uint32_t last;
     const Reads q = choose_reads<F32>(p, r, row, bins, all, least, g, last, s);
-    if ((q.count + 63) / 64 > kMaxCells) return false;
+    const uint32_t runs = (q.count + kCell - 1) / kCell;
+    if (runs > kMaxCells) return false;
     const uint32_t end = (q.all ? least : last) * 4 + 3;  // bins that the reads hold whole
     const double unit = unit_of(all), reach = fmax(row.top_p * all, 1e-300);
     uint32_t bin = kBins;
     if (row.top_p < 1) {
-        s.bin_mass[threadIdx.x] = 0;
+        // fixed point with 30 to 31 bits for all
+        s.bin_count[threadIdx.x] = 0;
         __syncthreads();
-        const float scale = (float)row.scale, funit = (float)unit;
+        const float scale = (float)row.scale, unit31 = (float)(unit * 0x1p-31);
         uint32_t tops = 0;
-        for (uint32_t j0 = 0; j0 < q.count; j0 += 4 * kThreads) {
-            float v[4][W];
-            uint32_t first[4];
-            four_reads<F32>(p, at, s, q, j0, v, first);
+        for (uint32_t i = wave; i * kCell < q.count; i += kWaves) {
+            u32x4 x[kReads];
+            run_reads<F32>(p, at, s, q, i, x);
 #pragma unroll
-            for (uint32_t u = 0; u < 4; ++u)
+            for (uint32_t u = 0; u < kReads; ++u) {
+                float v[W];
+                unpack<F32>(x[u], v);
 #pragma unroll
                 for (uint32_t c = 0; c < W; ++c) {
-                    const uint32_t b = bin_of(bins, v[u][c]);
-                    if (v[u][c] == top) ++tops;  // (equal ones would meet at one address)
-                    else if (b <= end)
-                        atomicAdd((unsigned long long *)&s.bin_mass[b],
-                                  (unsigned long long)(__builtin_amdgcn_exp2f((v[u][c] - top) * scale) * funit));
+                    const uint32_t b = bin_of(bins, v[c]);
+                    const uint32_t e = (uint32_t)(__builtin_amdgcn_exp2f((v[c] - top) * scale) * unit31 + 0.5f);
+                    tops += v[c] == top;
+                    if (v[c] != top && b <= end) atomicAdd(&s.bin_count[b], e);  // (equal ones would meet at one address)
                 }
+            }
         }
         uint32_t all_tops;
         block_scan(tops, s.count, all_tops);
-        const uint64_t m = s.bin_mass[threadIdx.x] + (threadIdx.x == 0 ? (uint64_t)(all_tops * unit) : 0);
+        const uint64_t m = s.bin_count[threadIdx.x] + (threadIdx.x == 0 ? (uint64_t)(all_tops * unit * 0x1p-31) : 0);
         uint64_t masses;
         const uint64_t m0 = block_scan(m, s.large, masses);
-        bin = kNone - block_max(m && (double)(m0 + m) >= reach * unit ? kNone - threadIdx.x : 0, s.other);
+        bin = kNone - block_max(m && (double)(m0 + m) >= reach * unit * 0x1p-31 ? kNone - threadIdx.x : 0, s.other);
         if (bin >= kBins) {
             // min_p ends all, or everything counts
             if (!q.all && last < least) return false;
             bin = kBins;
         }
     }
-    if (threadIdx.x == 0) s.pick_count = 0;
-    __syncthreads();
-    double above = 0;
-    for (uint32_t j0 = 0; j0 < q.count; j0 += 4 * kThreads) {
-        float v[4][W];
-        uint32_t first[4];
-        four_reads<F32>(p, at, s, q, j0, v, first);
-#pragma unroll
-        for (uint32_t u = 0; u < 4; ++u) {
-            double sum = 0;
-#pragma unroll
-            for (uint32_t c = 0; c < W; ++c) {
-                const uint32_t b = bin_of(bins, v[u][c]);
-                if (b < bin) {
-                    const double e = weight_near(v[u][c], top, row.scale);
-                    above += e;
-                    sum += e >= row.min_p ? e : 0.0;
-                } else if (b == bin && b < kBins) {
-                    const uint32_t place = atomicAdd(&s.pick_count, 1u);
-                    if (place < kMaxCandidates) s.tokens[place] = (uint64_t)ordered(v[u][c]) << 32 | (kNone - (first[u] + c));
-                }
-            }
-            sum = wave_sum(sum);
-            const uint32_t cell = (j0 + u * kThreads) / 64 + wave;
-            if (lane == 0 && cell < kMaxCells) s.cell[cell] = sum;
-        }
-    }
-    __syncthreads();
     uint64_t border = 0;
-    s.bin_mass[threadIdx.x] = 0;  // of the bin's kept tokens, by runs
-    if (bin < kBins) {
+    for (uint32_t attempt = 0;; ++attempt) {
+        const float z0 = bin < kBins ? least_of_bin(bins, bin) : INFINITY;
+        const float z1 = bin == kBins ? bins.floor : bin ? least_of_bin(bins, bin - 1) : INFINITY;
+        const double above = row.min_p > 0 ? sum_runs<F32, true>(p, at, q, top, row, z0, z1, s)
+                                           : sum_runs<F32, false>(p, at, q, top, row, z0, z1, s);
+        s.bin_mass[threadIdx.x] = 0;  // of the bin's kept tokens, by runs
+        if (bin == kBins) break;
         const uint32_t n = s.pick_count;
         if (n > kMaxCandidates) return false;
         sort_tokens(n, s);
@@ -753,24 +812,30 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
                     j = lo;
                 }
                 if (e[c] >= row.min_p)
-                    atomicAdd((unsigned long long *)&s.bin_mass[j / 64], (unsigned long long)(e[c] * unit + 0.5));
+                    atomicAdd((unsigned long long *)&s.bin_mass[j / kCell], (unsigned long long)(e[c] * unit + 0.5));
             }
             run += e[c];
         }
         block_scan(kept, s.count, keep);
-        if (keep == 0 || (keep == n && before + whole < reach)) return false;
-        border = s.sorted[keep - 1];
+        if (keep && !(keep == n && before + whole < reach)) {
+            border = s.sorted[keep - 1];
+            break;
+        }
+        const bool up = keep == 0;
+        if (attempt == 2 || (up && bin == 0) || (!up && bin >= end)) return false;
+        bin += up ? ~0u : 1u;
+        __syncthreads();
     }
     if (threadIdx.x == 0) s.pick = kNone;
     __syncthreads();
-    const double mine[1] = {threadIdx.x < (q.count + 63) / 64 ? s.cell[threadIdx.x] + (double)s.bin_mass[threadIdx.x] / unit : 0.0};
+    const double mine[1] = {threadIdx.x < runs ? s.cell[threadIdx.x] + (double)s.bin_mass[threadIdx.x] / unit : 0.0};
     double whole;
     double run = block_scan(mine[0], s.mass, whole);
     const double want = uniform_of(p, r) * whole;
     const uint32_t cell = first_over(mine, run, want, s);
     if (threadIdx.x == cell) s.total = run;
     // the run again, a read a lane
-    const uint32_t j = cell * 64 + lane, i = threadIdx.x < 64 && j < q.count ? read_at<F32>(s, q, j) : p.vocab;
+    const uint32_t j = cell * kCell + threadIdx.x, i = threadIdx.x < kCell && j < q.count ? read_at<F32>(s, q, j) : p.vocab;
     float v[W];
     double e[W], sum = 0;
     read_values<F32>(p, at, i, v);
