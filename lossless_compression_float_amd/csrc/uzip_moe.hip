@@ -45,6 +45,7 @@ __device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, i
     float z[V];
     bool nan = false;
     Key key[V];
+    double score[BIAS ? V : 1];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t e = i * 64 + lane;
@@ -52,8 +53,9 @@ __device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, i
         nan |= z[i] != z[i];
         key[i] = 0;
         if constexpr (BIAS) {
+            score[i] = sigmoid64(z[i]);
             if (z[i] > -INFINITY) {
-                const double s = sigmoid64(z[i]) + (double)p.bias[e];
+                const double s = score[i] + (double)p.bias[e];
                 key[i] = s > -INFINITY ? ordered(s) : 0;
             }
         } else if (z[i] > -INFINITY) {
@@ -62,33 +64,44 @@ __device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, i
     }
     nan = __any(nan);
     expert = -1;
-    float mine = 0;
+    float mine = 0;         // the chosen logit
+    double mine_score = 0;  // its score, where it is known
     for (uint32_t j = 0; j < p.k; ++j) {
         Key best = key[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
-        const Key top = wave_max(best);
+        Key top;
+        if constexpr (BIAS) {  // the upper halves first: two short searches
+            const uint32_t hi = wave_max((uint32_t)(best >> 32));
+            top = (uint64_t)hi << 32 | wave_max((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+        } else {
+            top = wave_max(best);
+        }
         if (top == 0) break;
         uint32_t e = 0xFFFFFFFFu;  // the first that has it
+        double its = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint64_t m = __ballot(key[i] == top);
-            if (m && e == 0xFFFFFFFFu) e = i * 64 + (uint32_t)__ffsll((unsigned long long)m) - 1;
+            if (m && e == 0xFFFFFFFFu) {
+                const uint32_t l = (uint32_t)__ffsll((unsigned long long)m) - 1;
+                e = i * 64 + l;
+                if constexpr (BIAS) its = lane_of(score[i], l);
+            }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (e == i * 64 + lane) key[i] = 0;
         if (lane == j) {
             expert = (int32_t)e;
-            if constexpr (!BIAS) mine = unordered(top);
+            if constexpr (BIAS) mine_score = its;
+            else mine = unordered(top);
         }
     }
-    if constexpr (BIAS)
-        if (expert >= 0) mine = logit(p.logits, (uint64_t)t * p.stride + expert, p.f32);
     const bool on = expert >= 0;
     if (p.sigmoid) {
         // (64 bits: scores of very negative logits keep their ratio)
-        const double s = on ? sigmoid64(mine) : 0.0;
+        const double s = BIAS ? mine_score : on ? sigmoid64(mine) : 0.0;
         const double all = p.renorm ? wave_sum(s) : 1.0;
         weight = on ? (float)(s / all * p.scale) : 0.0f;
     } else {
@@ -196,10 +209,18 @@ __global__ __launch_bounds__(NT) void k_route(RouteParams p) {
         const uint32_t runs = wide < NT ? NT / wide : 1;
         for (uint32_t e = threadIdx.x & (wide - 1); e <= p.num; e += NT) {
             uint32_t all = 0, before = 0;
-            for (uint32_t c = wide < NT ? threadIdx.x / wide : 0; c < p.chunks; c += runs) {
-                const uint32_t n = (uint32_t)p.counts[(uint64_t)c * (p.num + 1) + e];
-                all += n;
-                before += c < blockIdx.x ? n : 0;
+            for (uint32_t c0 = wide < NT ? threadIdx.x / wide : 0; c0 < p.chunks; c0 += 8 * runs) {
+                uint32_t n[8];  // on their way at once
+#pragma unroll
+                for (uint32_t u = 0; u < 8; ++u) {
+                    const uint32_t c = c0 + u * runs;
+                    n[u] = c < p.chunks ? (uint32_t)p.counts[(uint64_t)c * (p.num + 1) + e] : 0;
+                }
+#pragma unroll
+                for (uint32_t u = 0; u < 8; ++u) {
+                    all += n[u];
+                    before += c0 + u * runs < blockIdx.x ? n[u] : 0;
+                }
             }
             atomicAdd(&count[e], all);
             atomicAdd(&base[e], before);
@@ -245,10 +266,15 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
     if (expert >= (int32_t)p.num) expert = -1;
     const bool on = expert >= 0;
     const float g = on ? p.dweights[(uint64_t)t * p.k + lane] * p.scale : 0.0f;
-    const float zj = on ? logit(p.logits, (uint64_t)t * p.stride + expert, p.f32) : -INFINITY;
+    float zj = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float x = __shfl(z[i], expert & 63);
+        if (on && expert / 64 == i) zj = x;
+    }
     float out[V], dz;  // of the experts that are not chosen, of this lane's chosen one
     if (p.sigmoid) {
-        const double s = on ? sigmoid64(zj) : 0.0, rest = on ? sigmoid64(-zj) : 0.0;
+        const double t = exp(fmin(-(double)zj, 700.0)), s = on ? 1.0 / (1.0 + t) : 0.0, rest = t * s;  // s and 1 - s
         double d = g;
         if (p.renorm) {
             const double all = wave_sum(s);

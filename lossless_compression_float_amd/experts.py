@@ -87,6 +87,15 @@ class Routing:
     [num_experts + 1], where each expert's begin."""
 
     def __init__(self, experts, weights, order, offsets, scores="softmax", renormalize=True, scale=1.0):
+        if experts.dim() != 2 or not 1 <= experts.shape[1] <= MAX_CHOSEN or not 2 <= offsets.numel() <= MAX_EXPERTS + 1:
+            raise ValueError("a Routing is of up to %d experts, of which each token has 1 to %d, not of %s and %s" % (
+                MAX_EXPERTS, MAX_CHOSEN, list(experts.shape), list(offsets.shape)))
+        for what, t, shape, dtype in (("experts", experts, experts.shape, torch.int32), ("weights", weights, experts.shape, torch.float32),
+                                      ("order", order, (experts.numel(),), torch.int32), ("offsets", offsets, (offsets.numel(),), torch.int32)):
+            if t.dtype is not dtype:
+                raise TypeError("a Routing's %s must be %s, not %s" % (what, dtype, t.dtype))
+            if t.shape != shape or t.device != experts.device or not t.is_contiguous():
+                raise ValueError("a Routing's %s must be contiguous of shape %s on %s" % (what, list(shape), experts.device))
         self.experts, self.weights, self.order, self.offsets = experts, weights, order, offsets
         self.scores, self.renormalize, self.scale = scores, renormalize, scale
         self.tokens, self.k = experts.shape
@@ -125,18 +134,20 @@ def _device(t, what: str):
     return t.device
 
 
-def _route(a, k, num_experts, device, ws, stream, given=None):
+def _route(a, k, num_experts, device, ws, stream, how=("softmax", True, 1.0), given=None):
     tokens = a.tokens
+    pairs = tokens * k
     caller = _caller(device, stream)
     with _on(device, stream):
-        if given is None:
-            experts = torch.empty((tokens, k), dtype=torch.int32, device=device)
-            weights = torch.empty((tokens, k), dtype=torch.float32, device=device)
-        else:
-            experts, weights = (t.clone(memory_format=torch.contiguous_format) for t in given)
-        order = torch.empty(tokens * k, dtype=torch.int32, device=device)
-        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=device)
-        a.experts, a.weights, a.order, a.offsets = (t.data_ptr() for t in (experts, weights, order, offsets))
+        # one allocation for the four results
+        room = torch.empty(3 * pairs + num_experts + 1, dtype=torch.int32, device=device)
+        weights, experts, order, offsets = room.split_with_sizes((pairs, pairs, pairs, num_experts + 1))
+        weights, experts = weights.view(torch.float32).view(tokens, k), experts.view(tokens, k)
+        if given is not None:
+            experts.copy_(given[0])
+            weights.copy_(given[1])
+        at, step = room.data_ptr(), 4 * pairs
+        a.weights, a.experts, a.order, a.offsets = at, at + step, at + 2 * step, at + 3 * step
         a.num_experts, a.k = num_experts, k
         L, ref = _lib(), ctypes.byref(a)
         ws = _workspace(L.uzip_moe_route_workspace_size(ref), ws, device)
@@ -144,7 +155,11 @@ def _route(a, k, num_experts, device, ws, stream, given=None):
         if st != UZIP_OK:
             _check(st, "uzip_moe_route")
     _share(stream, caller, new=(experts, weights, order, offsets), given=(ws,))
-    return experts, weights, order, offsets
+    r = Routing.__new__(Routing)
+    r.experts, r.weights, r.order, r.offsets = experts, weights, order, offsets
+    r.scores, r.renormalize, r.scale = how
+    r.tokens, r.k, r.num_experts, r.device = tokens, k, num_experts, device
+    return r
 
 
 def moe_route(logits, k: int, scores: str = "softmax", bias=None, renormalize: bool = True, scale: float = 1.0, ws=None,
@@ -174,7 +189,7 @@ def moe_route(logits, k: int, scores: str = "softmax", bias=None, renormalize: b
             raise ValueError("bias must be %d contiguous values on %s" % (num, device))
         a.bias = bias.data_ptr()
     _no_history("moe_route", logits)
-    return Routing(*_route(a, k, num, device, ws, stream), scores, bool(renormalize), float(scale))
+    return _route(a, k, num, device, ws, stream, (scores, bool(renormalize), float(scale)))
 
 
 def moe_group(experts, weights, num_experts: int, ws=None, stream=None) -> Routing:
@@ -196,7 +211,7 @@ def moe_group(experts, weights, num_experts: int, ws=None, stream=None) -> Routi
     device = _device(experts, "moe_group")
     _no_history("moe_group", weights)
     a = uzip_moe_route_args(tokens=experts.shape[0], scale=1.0)
-    return Routing(*_route(a, experts.shape[1], num_experts, device, ws, stream, given=(experts, weights)))
+    return _route(a, experts.shape[1], num_experts, device, ws, stream, given=(experts, weights))
 
 
 def _routing(r, what: str) -> Routing:

@@ -203,7 +203,7 @@ def test_a_stack_past_4_gib():
         r = uz.moe_route(z, 3)
         assert (r.experts == torch.tensor([num - 1, 0, num - 2], device=DEV, dtype=torch.int32)).all()
         pick = [0, num - 2, num - 1]
-        few = uz.Routing(torch.tensor([2, 0, 1], dtype=torch.int32).repeat(tokens, 1), r.weights.cpu(), r.order.cpu(), torch.zeros(4))
+        few = uz.Routing(torch.tensor([2, 0, 1], dtype=torch.int32).repeat(tokens, 1), r.weights.cpu(), r.order.cpu(), torch.zeros(4, dtype=torch.int32))
         want, bound = layer64(x, few, up[pick], down[pick], "swiglu", None, None, None, BF)
         close(uz.moe(x, r, pu, pd), want, bound, "y")
 

@@ -214,6 +214,22 @@ def test_group_refusals(device, error, match, args):
         uz.moe_group(*args)
 
 
+@pytest.mark.parametrize("error,match,kw", [
+    (TypeError, "experts", dict(experts=torch.zeros(T, K))), (ValueError, "up to", dict(experts=torch.zeros(T, dtype=I32))),
+    (ValueError, "up to", dict(experts=torch.zeros(T, 65, dtype=I32))), (ValueError, "up to", dict(offsets=torch.zeros(1026, dtype=I32))),
+    (ValueError, "experts", dict(experts=torch.zeros(K, T, dtype=I32).t())), (TypeError, "weights", dict(weights=torch.zeros(T, K, dtype=BF))),
+    (ValueError, "weights", dict(weights=torch.zeros(T, K + 1))), (TypeError, "order", dict(order=torch.zeros(T * K, dtype=torch.int64))),
+    (ValueError, "order", dict(order=torch.zeros(T * K - 1, dtype=I32))), (TypeError, "offsets", dict(offsets=torch.zeros(E + 1))),
+    (ValueError, "offsets", dict(offsets=torch.zeros(2, E + 1, dtype=I32)[:, ::2])),
+])
+def test_a_routing_of_other_tensors_is_checked(error, match, kw):
+    base = dict(experts=torch.zeros(T, K, dtype=I32), weights=torch.zeros(T, K), order=torch.zeros(T * K, dtype=I32),
+                offsets=torch.zeros(E + 1, dtype=I32))
+    with pytest.raises(error, match=match):
+        uz.Routing(**{**base, **kw})
+    assert uz.Routing(**base).num_experts == E
+
+
 @pytest.mark.parametrize("error,match,args", [
     (TypeError, "Routing", (torch.zeros(T, K), LOGITS, None)), (ValueError, "shape", (torch.zeros(T, K), LOGITS[:, :-1].contiguous(), routing())),
     (TypeError, "dweights", (torch.zeros(T, K, dtype=BF), LOGITS, routing())), (ValueError, "dweights", (torch.zeros(K, T).t(), LOGITS, routing())),
