@@ -480,7 +480,10 @@ __device__ inline void stream_tiles(const WeightView &w, const TileRows<RB> &t, 
 
 // h = weight * act(U x + bias) for the pairs of one expert: RB row blocks of U
 // (gated: RB / 2, each with its up rows), NW waves that split its columns, 16 CT
-// pairs at a time, whose rows of x are read where they are.
+// pairs at a time, whose rows of x are read where they are.  Bound by the reads
+// of U (8 experts of 28672 x 4096, 16 tokens: 234 us, 6.1 TB/s of packed bytes, part of
+// them from the last-level cache; 64 of 2048 x 2048: 75 us, 5.5), for a token by latency
+// (8 of 1536 x 2048: 12.5 us, 3.1 TB/s).
 template <int CT, int RB, bool GATED, int NW>
 __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
     __shared__ f32x4 part[NW][RB * CT * 64];

@@ -148,14 +148,25 @@ __device__ inline Border find_border(const SampleParams &p, uint64_t at, float t
     for (int shift = 24; shift >= 0; shift -= 8) {
         if (threadIdx.x < 256) s.bin_mass[threadIdx.x] = 0, s.bin_count[threadIdx.x] = 0;
         __syncthreads();
-        for (uint32_t i = threadIdx.x; i < p.vocab; i += kThreads) {
-            const float z = value(p.logits, at + i, p.f32);
-            const uint32_t k = ordered(z);
-            if (k < in.key || k <= kKeyMinusInf) continue;
-            if (shift < 24 && (k >> (shift + 8)) != (prefix >> (shift + 8))) continue;
-            const uint32_t b = k >> shift & 255;
-            atomicAdd(&s.bin_count[b], 1u);
-            atomicAdd((unsigned long long *)&s.bin_mass[b], (unsigned long long)(weight(z, top, scale) * unit + 0.5));
+        for (uint32_t i0 = 0; i0 < p.vocab; i0 += kThreads) {
+            const uint32_t i = i0 + threadIdx.x;
+            const float z = i < p.vocab ? value(p.logits, at + i, p.f32) : -INFINITY;
+            const uint32_t k = ordered(z), b = k >> shift & 255;
+            const bool on = k >= in.key && k > kKeyMinusInf && (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)));
+            const uint64_t some = __ballot(on);
+            if (!some) continue;
+            const uint64_t w = on ? (uint64_t)(weight(z, top, scale) * unit + 0.5) : 0;
+            const uint32_t lane = (uint32_t)__ffsll((unsigned long long)some) - 1, b0 = lane_of(b, lane);
+            if (__ballot(on && b == b0) == some) {  // (a wave's equal ones together: 64 at one address take 64 turns)
+                const uint64_t sum = wave_sum(w);
+                if ((threadIdx.x & 63) == lane) {
+                    atomicAdd(&s.bin_count[b], (uint32_t)__popcll(some));
+                    atomicAdd((unsigned long long *)&s.bin_mass[b], (unsigned long long)sum);
+                }
+            } else if (on) {
+                atomicAdd(&s.bin_count[b], 1u);
+                atomicAdd((unsigned long long *)&s.bin_mass[b], (unsigned long long)w);
+            }
         }
         __syncthreads();
         // from the highest bin down: the first at which the prefix is long enough; else the lowest
@@ -323,7 +334,8 @@ __device__ inline void read_values(const SampleParams &p, uint64_t at, uint32_t 
 // A wave a segment of 2,048 tokens: its largest value, the sum of its weights
 // relative to that, its smallest value, and the largest of each group of 16
 // tokens (a lane's reads of half a segment), so that the second kernel reads
-// little of the row again.
+// little of the row again.  About 24 operations a token: 256 rows of 128,256 in
+// fp32 36 us, 3.7 TB/s, half of the issue slots; 64 in bf16 12 us.
 template <bool F32>
 __global__ __launch_bounds__(256) void k_survey(SampleParams p) {
     constexpr int W = F32 ? 4 : 8, READS = kSegment / 64 / W, HALF = READS / 2;
@@ -608,14 +620,60 @@ __device__ inline uint32_t first_over(const double (&e)[N], double run, double w
     return over ? kNone - over : any - 1;
 }
 
-// Rows with top-k: the tokens of the first bins that hold k, sorted.
+// A lane's reads of its wave's run, all on their way at once.
+template <bool F32>
+__device__ inline void run_reads(const SampleParams &p, uint64_t at, const Shared &s, const Reads &q, uint32_t run, u32x4 (&x)[kReads]) {
+#pragma unroll
+    for (uint32_t u = 0; u < kReads; ++u) {
+        const uint32_t j = run * kCell + u * 64 + (threadIdx.x & 63);
+        x[u] = read_raw<F32>(p, at, j < q.count ? read_at<F32>(s, q, j) : p.vocab);
+    }
+}
+
+// The first bin up to which all reads hold k tokens.
+template <bool F32>
+__device__ inline uint32_t bin_of_count(const SampleParams &p, uint64_t at, const Bins &bins, const Reads &q, uint32_t k, Shared &s) {
+    constexpr uint32_t W = F32 ? 4 : 8;
+    s.bin_count[threadIdx.x] = 0;
+    __syncthreads();
+    uint32_t tops = 0;
+    for (uint32_t i = threadIdx.x >> 6; i * kCell < q.count; i += kWaves) {
+        u32x4 x[kReads];
+        run_reads<F32>(p, at, s, q, i, x);
+#pragma unroll
+        for (uint32_t u = 0; u < kReads; ++u) {
+            float v[W];
+            unpack<F32>(x[u], v);
+#pragma unroll
+            for (uint32_t c = 0; c < W; ++c) {
+                const uint32_t b = bin_of(bins, v[c]);
+                tops += v[c] == bins.top;
+                if (v[c] != bins.top && v[c] > -INFINITY && b < kBins) atomicAdd(&s.bin_count[b], 1u);
+            }
+        }
+    }
+    uint32_t all_tops, all;
+    block_scan(tops, s.count, all_tops);
+    const uint32_t c = s.bin_count[threadIdx.x] + (threadIdx.x == 0 ? all_tops : 0), c0 = block_scan(c, s.count, all);
+    return min(kNone - block_max(c0 + c >= k ? kNone - threadIdx.x : 0, s.other), kBins - 1);
+}
+
+// Rows with top-k: the tokens of the first bins that hold k, sorted.  Where the
+// row has fewer groups than k, or too many of them are hot, the tokens
+// themselves are counted.
 template <bool F32>
 __device__ inline bool by_sorting(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all,
                                   uint32_t least, Groups &g, Shared &s) {
     uint32_t last, n;
     const float top = bins.top;
-    const Reads q = choose_reads<F32>(p, r, row, bins, all, least, g, last, s);
-    if (q.all || !collect<F32>(p, (uint64_t)r * p.stride, bins, q, 0, last * 4 + 3, n, s)) return false;
+    const uint64_t at = (uint64_t)r * p.stride;
+    Reads q = choose_reads<F32>(p, r, row, bins, all, least, g, last, s);
+    uint32_t to = last * 4 + 3;
+    if (q.all || (last == least && s.pick_count < row.k)) {
+        q = Reads{(p.vocab + (F32 ? 3 : 7)) / (F32 ? 4 : 8), true};
+        to = min(bin_of_count<F32>(p, at, bins, q, row.k, s), least * 4 + 3);
+    }
+    if (!collect<F32>(p, at, bins, q, 0, to, n, s)) return false;
     sort_tokens(n, s);
     // the sums before each, and how many are kept
     double e[kOwn], part = 0, whole;
@@ -658,16 +716,6 @@ __device__ inline bool by_sorting(const SampleParams &p, uint32_t r, const Row &
     if (threadIdx.x == 0)
         finish(p, r, kNone - (uint32_t)s.tokens[i], unordered((uint32_t)(s.tokens[i] >> 32)), top, row.heat, all);
     return true;
-}
-
-// A lane's reads of its wave's run, all on their way at once.
-template <bool F32>
-__device__ inline void run_reads(const SampleParams &p, uint64_t at, const Shared &s, const Reads &q, uint32_t run, u32x4 (&x)[kReads]) {
-#pragma unroll
-    for (uint32_t u = 0; u < kReads; ++u) {
-        const uint32_t j = run * kCell + u * 64 + (threadIdx.x & 63);
-        x[u] = read_raw<F32>(p, at, j < q.count ? read_at<F32>(s, q, j) : p.vocab);
-    }
 }
 
 // The sums of the tokens from z1 on by runs of reads (of those that min_p
@@ -856,7 +904,9 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
     return true;
 }
 
-// A workgroup a row, after the survey.
+// A workgroup a row, after the survey.  Latency, in steps of 0.5 to 2 us: one
+// row with top-k 12 us, 64 without filters 7; a row with top-p that has to be
+// read whole 70 us, bound by its operations.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
     __shared__ Shared s;

@@ -81,6 +81,18 @@ def test_filters(vocab, dtype):
         check(z, torch.rand(6, generator=g, device=DEV), **f)
 
 
+@pytest.mark.parametrize("vocab", [2000, 4097, 9001, 20000, 128256])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_large_top_k(vocab, dtype):
+    """More than the row has groups of tokens, more than are sorted, among many equal ones (bf16)."""
+    g = gen(vocab + 1)
+    for k in (700, 1000, 3000, 5000, vocab - 1):
+        for f in (dict(), dict(top_p=0.9), dict(min_p=0.01), dict(top_p=0.99, min_p=0.001, temperature=2.0)):
+            z = peaked(g, 3, vocab, spread=1.0, dtype=dtype)
+            z[1, ::5] = -INF
+            check(z, torch.rand(3, generator=g, device=DEV), top_k=k, **f)
+
+
 @pytest.mark.parametrize("rows", [1, 3, 300])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_large_vocabulary(rows, dtype):
