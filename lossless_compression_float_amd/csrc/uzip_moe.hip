@@ -35,6 +35,15 @@ __device__ inline uint64_t ordered(double v) {
 __device__ inline float exp_below(float z, float top) { return z == top ? 1.0f : expf(z - top); }
 __device__ inline double sigmoid64(double z) { return 1.0 / (1.0 + exp(-z)); }
 
+// Scores that are all below this are exp(z) in 64 bits, or less than that can
+// tell; relative to the largest they are whatever the logits are (masked by
+// their type's lowest value, say).
+constexpr double kFaint = 1e-290;
+__device__ inline double faint(bool on, float z) {
+    const float top = unordered(wave_max(on ? ordered(z) : 0u));
+    return on ? exp((double)z - (double)top) : 0.0;
+}
+
 // A token's choice by one wave: lane j < k gets the j-th best expert and its
 // weight.  Lane l holds the scores of experts 64 i + l.  Keys are the logits,
 // since softmax and sigmoid keep their order; with a bias the biased scores,
@@ -101,8 +110,13 @@ __device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, i
     const bool on = expert >= 0;
     if (p.sigmoid) {
         // (64 bits: scores of very negative logits keep their ratio)
-        const double s = BIAS ? mine_score : on ? sigmoid64(mine) : 0.0;
-        const double all = p.renorm ? wave_sum(s) : 1.0;
+        double s = BIAS ? mine_score : on ? sigmoid64(mine) : 0.0;
+        double all = p.renorm ? wave_sum(s) : 1.0;
+        if (all < kFaint) {
+            if (BIAS && on) mine = logit(p.logits, (uint64_t)t * p.stride + (uint32_t)expert, p.f32);
+            s = faint(on, mine);
+            all = wave_sum(s);
+        }
         weight = on ? (float)(s / all * p.scale) : 0.0f;
     } else {
         float top = z[0];
@@ -274,10 +288,14 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
     }
     float out[V], dz;  // of the experts that are not chosen, of this lane's chosen one
     if (p.sigmoid) {
-        const double t = exp(fmin(-(double)zj, 700.0)), s = on ? 1.0 / (1.0 + t) : 0.0, rest = t * s;  // s and 1 - s
-        double d = g;
+        const double t = exp(fmin(-(double)zj, 700.0));
+        double s = on ? 1.0 / (1.0 + t) : 0.0, rest = t * s, d = g;  // rest: 1 - s
         if (p.renorm) {
-            const double all = wave_sum(s);
+            double all = wave_sum(s);
+            if (all < kFaint) {
+                s = faint(on, zj), rest = 1.0;
+                all = wave_sum(s);
+            }
             d = (d - wave_sum(d * s) / all) / all;
         }
         dz = (float)(d * s * rest);

@@ -12,6 +12,7 @@
 // that fp32's error moves (128,256 even tokens, off by 1e-7 of the whole each,
 // would change one draw in a hundred); histograms are summed in fixed point, so
 // that the order of their atomics is no matter.
+#include <float.h>
 #include <stdint.h>
 
 #include <hip/hip_runtime.h>
@@ -998,10 +999,10 @@ __global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
         return;
     }
     if (top < INFINITY) {
-        // Tokens that weigh less than 2^-80 of the largest change no sum in 64 bits and are left out.
+        // Tokens that weigh less than 2^-80 of the largest change no sum in 64 bits and are left out, as -inf is.
         Bins bins;
         bins.top = top;
-        bins.floor = fmaxf(unordered(lowest), (float)((double)top - 80.0 / row.scale));
+        bins.floor = fmaxf(fmaxf(unordered(lowest), (float)((double)top - 80.0 / row.scale)), -FLT_MAX);
         const float range = top - bins.floor;
         bins.inv = range > 0 ? (kBins - 0.01f) / range : 0.0f;
         // the last coarse bin with tokens that min_p keeps (top-p of the first k needs the sum of the others too)

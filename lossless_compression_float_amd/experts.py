@@ -90,6 +90,8 @@ class Routing:
         if experts.dim() != 2 or not 1 <= experts.shape[1] <= MAX_CHOSEN or not 2 <= offsets.numel() <= MAX_EXPERTS + 1:
             raise ValueError("a Routing is of up to %d experts, of which each token has 1 to %d, not of %s and %s" % (
                 MAX_EXPERTS, MAX_CHOSEN, list(experts.shape), list(offsets.shape)))
+        if scores not in SCORES:
+            raise ValueError("scores must be softmax or sigmoid, not %r" % (scores,))
         for what, t, shape, dtype in (("experts", experts, experts.shape, torch.int32), ("weights", weights, experts.shape, torch.float32),
                                       ("order", order, (experts.numel(),), torch.int32), ("offsets", offsets, (offsets.numel(),), torch.int32)):
             if t.dtype is not dtype:

@@ -106,6 +106,31 @@ def test_sigmoid_scores_of_very_negative_logits_keep_their_ratio():
     assert torch.allclose(r.weights.cpu(), torch.softmax(torch.tensor([[-200.0, -201.0]]), 1), rtol=1e-6)
 
 
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_sigmoid_scores_that_all_vanish_keep_their_ratio(dtype, bias):
+    """Below e^-745, masked by the type's lowest value among them."""
+    low = torch.finfo(dtype).min
+    rows = [[low] * 4, [-720.0, -721, low, low], [-1e5, -1e5, -1.5e5, low], [-800, -801, -802, -math.inf], [-660, -670, -672, -1000],
+            [low, 0.5, low, low]]
+    logits = torch.tensor(rows, device=DEV).to(dtype)
+    b = torch.zeros(4, device=DEV) if bias else None
+    for n in (1, 20):
+        z = logits.repeat(n, 1)
+        r = uz.moe_route(z, 3, scores="sigmoid", bias=b)
+        # scores of exactly 0 are equal to the biased choice, which then takes the lowest index
+        s = torch.nn.functional.logsigmoid(z.double()).cpu().gather(1, r.experts.cpu().long())
+        want = torch.softmax(s, 1)
+        # one rounding to 24 bits, exponents of less than 1,000 in 64 bits
+        close(r.weights, want, want * (2.0 ** -24 + 1e-12) + 2.0 ** -126, "weights")
+        dw = normal(gen(n), z.shape[0], 3, dtype=F32)
+        d = dw.double().cpu()
+        rest = torch.sigmoid(-z.double()).cpu().gather(1, r.experts.cpu().long())
+        dz = torch.zeros(z.shape, dtype=torch.float64).scatter(1, r.experts.cpu().long(), want * rest * (d - (d * want).sum(1, keepdim=True)))
+        got = uz.moe_route_backward(dw, z, r)
+        close(got, dz, dz.abs() * (HALF[dtype] + 2.0 ** -24) + d.abs().max() * 1e-12, "dlogits")
+
+
 def test_a_bias_decides_and_does_not_weigh():
     z = torch.zeros((70, 8), device=DEV)
     bias = torch.tensor([0, 3, 0, 2.0, -1, 0, 1, 0], device=DEV)

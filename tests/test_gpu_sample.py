@@ -203,6 +203,19 @@ def test_wide_spread_at_low_temperature():
         check(z, torch.rand(8, generator=g, device=DEV), temperature=t, top_p=0.99)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_masked_tokens_are_not_drawn_at_the_highest_temperatures(dtype):
+    z = torch.randn((3, 3001), generator=gen(7), device=DEV).to(dtype)
+    z[:, :40] = -INF
+    z[1, 50::2] = -INF
+    z[2, 41:] = torch.finfo(dtype).min
+    for t in (1e20, 1e37, 3e38):
+        for u in (0.0, 0.6):
+            for f in (dict(), dict(top_p=1 - 2.0 ** -24), dict(top_p=0.3), dict(min_p=1e-30), dict(top_k=2999, top_p=0.9), dict(top_k=50)):
+                token, _ = check(z, torch.full((3,), u, device=DEV), temperature=t, **f)
+                assert (token >= 40).all()
+
+
 def test_no_rows():
     token, logprob = uz.sample(torch.empty((0, 10), device=DEV), torch.empty(0, device=DEV))
     assert token.shape == logprob.shape == (0,)

@@ -221,6 +221,7 @@ def test_group_refusals(device, error, match, args):
     (ValueError, "weights", dict(weights=torch.zeros(T, K + 1))), (TypeError, "order", dict(order=torch.zeros(T * K, dtype=torch.int64))),
     (ValueError, "order", dict(order=torch.zeros(T * K - 1, dtype=I32))), (TypeError, "offsets", dict(offsets=torch.zeros(E + 1))),
     (ValueError, "offsets", dict(offsets=torch.zeros(2, E + 1, dtype=I32)[:, ::2])),
+    (ValueError, "scores", dict(scores="linear")),
 ])
 def test_a_routing_of_other_tensors_is_checked(error, match, kw):
     base = dict(experts=torch.zeros(T, K, dtype=I32), weights=torch.zeros(T, K), order=torch.zeros(T * K, dtype=I32),
