@@ -446,6 +446,16 @@ __device__ inline uint2 read8(rsrc_t r, uint32_t lane_off, uint32_t off) {
     return make_uint2(v[0], v[1]);
 }
 
+// 8 values of which `left` exist, zeros for the others.
+__device__ inline uint4 read_tail(const uint16_t *from, int left) {
+    if (left >= 8) return __builtin_bit_cast(uint4, *reinterpret_cast<const u32x4_any *>(from));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (c < left) w[c / 2] |= (uint32_t)from[c] << (16 * (c & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A wave's tiles of one row block, kb = first, first + step, ..: from memory
 // through the decoder into the matrix instructions with `columns`, one block on
 // its way.  `load` reads the second operand's values of a block, `multiply`
@@ -502,7 +512,7 @@ __device__ inline void stream_tiles(const WeightView &w, const TileRows<RB> &t, 
 // of U (8 experts of 28672 x 4096, 16 tokens: 234 us, 6.1 TB/s of packed bytes, part of
 // them from the last-level cache; 64 of 2048 x 2048: 75 us, 5.5), for a token by latency
 // (8 of 1536 x 2048: 12.5 us, 3.1 TB/s).
-template <int CT, int RB, bool GATED, int NW>
+template <int CT, int RB, bool GATED, int NW, bool ANY>
 __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
     __shared__ f32x4 part[NW][RB * CT * 64];
     const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -526,10 +536,13 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
     for (uint32_t s0 = f.begin; s0 < f.end; s0 += 16 * CT) {
         const uint32_t here = min(f.end - s0, 16u * CT);
         uint32_t row[CT];
+        const uint16_t *from[CT];
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const uint32_t pair = j * 16 + r < here ? (uint32_t)p.order[s0 + j * 16 + r] : pairs;
             row[j] = pair < pairs ? pair / p.k * (uint32_t)p.x.stride * 2 + q * 16 : kBehind;
+            // (the first row where there is no pair: its column is computed and dropped)
+            from[j] = static_cast<const uint16_t *>(p.x.p) + (pair < pairs ? pair / p.k * p.x.stride : 0) + q * 8;
         }
         f32x4 acc[RB][CT];
 #pragma unroll
@@ -543,6 +556,13 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
                 for (int j = 0; j < CT; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        if constexpr (ANY) {
+                            if (j && (uint32_t)j * 16 >= here) continue;
+                            const uint32_t c = kb * kTileCols + h * 32;
+                            if (kb != part_block) x[j][h] = __builtin_bit_cast(uint4, *reinterpret_cast<const u32x4_any *>(from[j] + c));
+                            else x[j][h] = read_tail(from[j] + c, (int)p.up_cols - (int)(c + q * 8));
+                            continue;
+                        }
                         const bool in = kb != part_block || part_block * kTileCols + h * 32 + q * 8 < p.up_cols;
                         if (j == 0 || (uint32_t)j * 16 < here) x[j][h] = read16(xb, in ? row[j] : kBehind, (kb * kTileCols + h * 32) * 2);
                     }
@@ -846,7 +866,9 @@ hipError_t moe_down(const MoeParams &p, hipStream_t s) {
 template <int CT, int RB, bool GATED, int NW>
 hipError_t moe_up(const MoeParams &p, hipStream_t s) {
     const uint32_t per = GATED ? RB / 2 : RB, experts = p.num < p.tokens * p.k ? p.num : p.tokens * p.k;
-    k_moe_up<CT, RB, GATED, NW><<<dim3((p.up.part_blocks + per - 1) / per, experts), NW * 64, 0, s>>>(p);
+    const dim3 grid((p.up.part_blocks + per - 1) / per, experts);
+    if (p.x_any) k_moe_up<CT, RB, GATED, NW, true><<<grid, NW * 64, 0, s>>>(p);
+    else k_moe_up<CT, RB, GATED, NW, false><<<grid, NW * 64, 0, s>>>(p);
     return hipGetLastError();
 }
 

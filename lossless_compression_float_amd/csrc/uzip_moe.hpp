@@ -78,6 +78,7 @@ struct MoeParams {
     uint32_t tokens, k, num;
     uint32_t up_rows, up_cols, down_rows, h_cols, h_stride;
     uint32_t bias_f32, y_f32, act, splits;
+    uint32_t x_any;       // x's rows are not 16 bytes apart, or too far for 32 bits
 };
 constexpr uint32_t kFewTokens = 256, kFewPairs = 4096;
 

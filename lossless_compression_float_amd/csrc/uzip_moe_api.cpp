@@ -98,10 +98,7 @@ MoeParams plan_few(const uzip_weight *up, const uzip_weight *down, const uzip_mo
     p.up = view(up);
     p.down = view(down);
     p.x = Mat{a->x, a->x_stride};
-    if (!tiled(a->x, a->x_stride, up->cols)) {
-        p.x.stride = uzip::up(up->cols, 8);
-        p.x.p = c.take<uint16_t>(a->tokens * p.x.stride);
-    }
+    p.x_any = !tiled(a->x, a->x_stride, up->cols);
     p.order = a->order;
     p.offsets = a->offsets;
     p.weights = a->weights;
@@ -115,7 +112,7 @@ MoeParams plan_few(const uzip_weight *up, const uzip_weight *down, const uzip_mo
     p.k = a->k;
     p.num = (uint32_t)up->matrices;
     p.up_rows = (uint32_t)up->rows;
-    p.up_cols = (uint32_t)uzip::up(up->cols, 8);
+    p.up_cols = (uint32_t)up->cols;
     p.down_rows = (uint32_t)down->rows;
     p.h_cols = (uint32_t)down->cols;
     p.h_stride = (uint32_t)uzip::up(down->cols, 64);
@@ -270,10 +267,6 @@ uzip_status uzip_moe(const uzip_weight *up, const uzip_weight *down, const uzip_
     }
     const MoeParams p = plan_few(up, down, args, c);
     if (!workspace_ok(d_workspace, workspace_bytes, c.bytes())) return UZIP_ERR_INVALID_ARGUMENT;
-    if (p.x.p != args->x && launch_stage(static_cast<const uint16_t *>(args->x), args->x_stride,
-                                         static_cast<uint16_t *>(const_cast<void *>(p.x.p)), p.x.stride, args->tokens, up->cols,
-                                         stream) != hipSuccess)
-        return UZIP_ERR_DEVICE;
     return done(launch_moe_few(p, stream));
 }
 
