@@ -48,23 +48,21 @@ __device__ inline double faint(bool on, float z) {
 // weight.  Lane l holds the scores of experts 64 i + l.  Keys are the logits,
 // since softmax and sigmoid keep their order; with a bias the biased scores,
 // in 64 bits, since there neighbours could change places.
-template <int V, bool BIAS>
-__device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, int32_t &expert, float &weight) {
+template <int V, bool BIAS, class B>
+__device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, const float (&z)[V], B bias, int32_t &expert,
+                              float &weight) {
     typedef std::conditional_t<BIAS, uint64_t, uint32_t> Key;
-    float z[V];
     bool nan = false;
     Key key[V];
     double score[BIAS ? V : 1];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const uint32_t e = i * 64 + lane;
-        z[i] = e < p.num ? logit(p.logits, (uint64_t)t * p.stride + e, p.f32) : -INFINITY;
         nan |= z[i] != z[i];
         key[i] = 0;
         if constexpr (BIAS) {
             score[i] = sigmoid64(z[i]);
             if (z[i] > -INFINITY) {
-                const double s = score[i] + (double)p.bias[e];
+                const double s = score[i] + (double)bias(i);
                 key[i] = s > -INFINITY ? ordered(s) : 0;
             }
         } else if (z[i] > -INFINITY) {
@@ -80,9 +78,12 @@ __device__ inline void choose(const RouteParams &p, uint32_t t, uint32_t lane, i
 #pragma unroll
         for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
         Key top;
-        if constexpr (BIAS) {  // the upper halves first: two short searches
+        if constexpr (BIAS) {  // the upper halves, and the lower ones where more than one lane has it
             const uint32_t hi = wave_max((uint32_t)(best >> 32));
-            top = (uint64_t)hi << 32 | wave_max((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+            const uint64_t m = __ballot((uint32_t)(best >> 32) == hi);
+            const uint32_t lo = m & (m - 1) ? wave_max((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u)
+                                            : lane_of((uint32_t)best, (uint32_t)__ffsll((unsigned long long)m) - 1);
+            top = (uint64_t)hi << 32 | lo;
         } else {
             top = wave_max(best);
         }
@@ -156,11 +157,42 @@ __device__ inline void given(const RouteParams &p, uint32_t t, uint32_t lane, in
     if (expert < 0) weight = 0;
 }
 
-template <int V>
-__device__ inline void choose_any(const RouteParams &p, uint32_t t, uint32_t lane, int32_t &expert, float &weight) {
-    if (!p.logits) given(p, t, lane, expert, weight);
-    else if (p.bias) choose<V, true>(p, t, lane, expert, weight);
-    else choose<V, false>(p, t, lane, expert, weight);
+// The tokens t0, t0 + step, .. before t1, the next one's logits on their way
+// (up to 256 experts: more have no registers left for it).
+template <int V, class F>
+__device__ inline void choose_all(const RouteParams &p, uint32_t t0, uint32_t t1, uint32_t step, uint32_t lane, F keep) {
+    int32_t expert;
+    float weight;
+    if (!p.logits) {
+        for (uint32_t t = t0; t < t1; t += step) {
+            given(p, t, lane, expert, weight);
+            keep(t, expert, weight);
+        }
+        return;
+    }
+    constexpr bool AHEAD = V <= 4;
+    float first[V], next[V];
+    auto bias = [&](int i) { return AHEAD ? first[i] : p.bias[i * 64 + lane]; };  // of one that has a logit
+    auto load = [&](uint32_t t) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t e = i * 64 + lane;
+            next[i] = e < p.num ? logit(p.logits, (uint64_t)t * p.stride + e, p.f32) : -INFINITY;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < V; ++i) first[i] = AHEAD && p.bias && i * 64 + lane < p.num ? p.bias[i * 64 + lane] : 0.0f;
+    if (AHEAD && t0 < t1) load(t0);
+    for (uint32_t t = t0; t < t1; t += step) {
+        float z[V];
+        if (!AHEAD) load(t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = next[i];
+        if (AHEAD && t + step < t1) load(t + step);
+        if (p.bias) choose<V, true>(p, t, lane, z, bias, expert, weight);
+        else choose<V, false>(p, t, lane, z, bias, expert, weight);
+        keep(t, expert, weight);
+    }
 }
 
 // Pairs [p0, p1) to their places: base[e] is the next one of expert e.  Waves
@@ -203,16 +235,13 @@ __global__ __launch_bounds__(NT) void k_route(RouteParams p) {
     for (uint32_t e = threadIdx.x; e <= p.num; e += NT) count[e] = base[e] = 0;
     __syncthreads();
     if constexpr (CHOOSE) {
-        for (uint32_t t = t0 + wave; t < t1; t += NT / 64) {
-            int32_t e;
-            float w;
-            choose_any<V>(p, t, lane, e, w);
+        choose_all<V>(p, t0 + wave, t1, NT / 64, lane, [&](uint32_t t, int32_t e, float w) {
             if (lane < p.k) {
                 p.experts[(uint64_t)t * p.k + lane] = e;
                 p.weights[(uint64_t)t * p.k + lane] = w;
                 atomicAdd(&count[e < 0 ? p.num : (uint32_t)e], 1u);
             }
-        }
+        });
         __syncthreads();
         if constexpr (!PLACE)
             for (uint32_t e = threadIdx.x; e <= p.num; e += NT) p.counts[(uint64_t)blockIdx.x * (p.num + 1) + e] = (int32_t)count[e];
@@ -635,6 +664,7 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
 constexpr uint32_t kMaxVisits = kMaxExperts + kFewPairs / 8;
 template <int CT, int RB, int NW, int DEPTH>
 __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
+    static_assert(64 % DEPTH == 0, "stages keep their turns over batches of headers");
     extern __shared__ float sums[];                 // [NW][RB][tokens][16]
     __shared__ uint32_t visits[kMaxVisits];         // expert, first pair << 10, pairs - 1 << 23
     __shared__ uint16_t token_of[kFewPairs];
@@ -877,11 +907,15 @@ hipError_t route(const RouteParams &p, hipStream_t s) {
     if (p.chunks > 1) {
         k_route<V, true, false, 1024><<<p.chunks, 1024, 0, s>>>(p);
         k_route<V, false, true, 1024><<<p.chunks, 1024, 0, s>>>(p);
-    } else if (p.tokens <= 4 && p.num <= 256) {
-        k_route<V, true, true, 256><<<1, 256, 0, s>>>(p);
-    } else {
-        k_route<V, true, true, 1024><<<1, 1024, 0, s>>>(p);
+        return hipGetLastError();
     }
+    if constexpr (V <= 4) {
+        if (p.tokens <= 4 && p.num <= 256) {  // (any number may be grouped by V = 1)
+            k_route<V, true, true, 256><<<1, 256, 0, s>>>(p);
+            return hipGetLastError();
+        }
+    }
+    k_route<V, true, true, 1024><<<1, 1024, 0, s>>>(p);
     return hipGetLastError();
 }
 
