@@ -328,6 +328,36 @@ def test_strides_and_places(tokens):
         assert torch.equal(room, before)
 
 
+@pytest.mark.parametrize("tokens", [3, 30, 80])
+@pytest.mark.parametrize("d", [1, 7, 8, 9, 60, 63, 64, 65, 120, 129, 200])
+def test_nothing_beside_the_rows_of_x_is_used(tokens, d):
+    """Rows of every width among NaNs, 16 bytes apart and not."""
+    g = gen(d)
+    num, k, f = 4, 2, 40
+    up, down = normal(g, num, f, d, scale=0.2), normal(g, num, 33, f, scale=0.2)
+    pu, pd = uz.pack_weight(up), uz.pack_weight(down)
+    r = uz.moe_route(normal(g, tokens, num, dtype=F32), k)
+    for lead, wide in ((8, (d + 23) // 8 * 8), (3, d + 7)):
+        room = torch.full((tokens, wide), math.nan, dtype=BF, device=DEV)
+        x = room[:, lead:lead + d]
+        x.copy_(normal(g, tokens, d))
+        want, bound = layer64(x, r, up, down, "silu", None, None, None, F32)
+        close(uz.moe(x, r, pu, pd, act="silu", out_dtype=F32), want, bound, "y")
+
+
+def test_rows_of_x_far_apart():
+    g = gen(9)
+    num, k, d, f = 4, 2, 72, 40
+    up, down = normal(g, num, f, d, scale=0.2), normal(g, num, 33, f, scale=0.2)
+    pu, pd = uz.pack_weight(up), uz.pack_weight(down)
+    r = uz.moe_route(normal(g, 3, num, dtype=F32), k)
+    for stride in ((1 << 22) + 8, (1 << 31) + 8):
+        x = torch.empty(2 * stride + d, dtype=BF, device=DEV).as_strided((3, d), (stride, 1))
+        x.copy_(normal(g, 3, d))
+        want, bound = layer64(x, r, up, down, "silu", None, None, None, F32)
+        close(uz.moe(x, r, pu, pd, act="silu", out_dtype=F32), want, bound, "y")
+
+
 def test_a_call_gives_the_same_bits_again_and_in_a_larger_batch_the_same_values():
     g = gen(9)
     num, k, d, f = 16, 4, 256, 128
