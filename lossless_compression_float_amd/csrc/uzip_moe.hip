@@ -226,7 +226,11 @@ __device__ inline void place(const RouteParams &p, uint32_t p0, uint32_t p1, uin
 }
 
 // Few pairs, or one chunk of many: choice and counts (CHOOSE), then the places
-// (PLACE), which need the counts of the chunks before.
+// (PLACE), which need the counts of the chunks before.  The same pairs have the
+// same places whatever the order of the workgroups.  Bound by latency where
+// tokens are few (4 of 128 experts, 8 each: 5 us, a launch 2.5 of them; 777 of
+// 60, 4 each: 4.5 and 4.5), by the steps of a search where they are many (16384
+// of 64, 6 each, biased: 14 and 7 us, half of the issue slots; 4.2 MB of logits).
 template <int V, bool CHOOSE, bool PLACE, uint32_t NT>
 __global__ __launch_bounds__(NT) void k_route(RouteParams p) {
     __shared__ uint32_t count[kMaxExperts + 1], base[kMaxExperts + 1], waves[NT / 64];
@@ -288,7 +292,8 @@ __global__ __launch_bounds__(NT) void k_route(RouteParams p) {
 }
 
 // The gradient of the logits, a wave a token: dp of the chosen experts, then
-// through the scores.  The choice itself has none.
+// through the scores.  The choice itself has none.  Bound by latency, a token's
+// reads and then its sums over a wave (16384 tokens of 64, 6 each: 10 us, 8.4 MB).
 template <int V>
 __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
     const uint32_t lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -368,7 +373,8 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
 
 // ---- the layer around grouped products ----------------------------------------------
 
-// Rows of x in the order of their experts, zeros behind the last column, and the place of each pair.
+// Rows of x in the order of their experts, zeros behind the last column, and the place of each pair.  Bound by the writes
+// (4096 tokens of 2048, 6 of 64 experts each: 101 MB, 31 us, where the two products take 820).
 __global__ __launch_bounds__(256) void k_gather(GatherParams p) {
     const uint32_t pairs = p.tokens * p.k, units = (uint32_t)(p.out_stride / 8);
     const uint32_t end = (uint32_t)min(max(*p.ends, 0), (int32_t)pairs);
@@ -395,7 +401,8 @@ __global__ __launch_bounds__(256) void k_gather(GatherParams p) {
     }
 }
 
-// y of a token: its experts' results by their weights, in the order of the choice, and the residual.
+// y of a token: its experts' results by their weights, in the order of the choice, and the residual.  Bound by the reads
+// (of the above 201 MB of fp32, 36 us, 6.0 TB/s).
 __global__ __launch_bounds__(256) void k_combine(CombineParams p) {
     const uint32_t pairs = p.tokens * p.k, units = (p.cols + 7) / 8;
     const uint32_t end = (uint32_t)min(max(*p.ends, 0), (int32_t)pairs);
@@ -540,7 +547,9 @@ __device__ inline void stream_tiles(const WeightView &w, const TileRows<RB> &t, 
 // pairs at a time, whose rows of x are read where they are.  Bound by the reads
 // of U (8 experts of 28672 x 4096, 16 tokens: 234 us, 6.1 TB/s of packed bytes, part of
 // them from the last-level cache; 64 of 2048 x 2048: 75 us, 5.5), for a token by latency
-// (8 of 1536 x 2048: 12.5 us, 3.1 TB/s).
+// (8 of 1536 x 2048: 12.5 us, 3.1 TB/s).  ANY: rows of x that are not 16 bytes
+// apart, or too far for 32 bits, by 64-bit addresses (13 tokens, 7 experts of 1333 x
+// 1027: 12.3 us, where a copy of x before took 4.1 and the kernel 9.8).
 template <int CT, int RB, bool GATED, int NW, bool ANY>
 __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
     __shared__ f32x4 part[NW][RB * CT * 64];
