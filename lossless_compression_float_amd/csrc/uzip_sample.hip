@@ -483,7 +483,10 @@ __device__ inline Reads choose_reads(const SampleParams &p, uint32_t r, const Ro
     if (threadIdx.x == last) s.pick_count = c0 + c;
     __syncthreads();
     const uint32_t hot = s.pick_count;
-    if (hot > kMaxHot) return Reads{(p.vocab + W - 1) / W, true};
+    if (hot > kMaxHot) {
+        __syncthreads();  // (all have read the count before sum_runs counts there anew)
+        return Reads{(p.vocab + W - 1) / W, true};
+    }
     for (uint32_t h0 = 0; h0 < halves; h0 += kAhead * kWaves) {
         if (halves > kAhead * kWaves) load_groups(g, groups, halves, h0);
 #pragma unroll
