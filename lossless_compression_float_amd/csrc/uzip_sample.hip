@@ -773,11 +773,37 @@ __device__ inline double sum_runs(const SampleParams &p, uint64_t at, const Read
     return above;
 }
 
+// The first bin, up to `end`, up to which all reads weigh `reach`, in 64 bits;
+// beyond the last if they do not.
+template <bool F32>
+__device__ inline uint32_t bin_of_mass(const SampleParams &p, uint64_t at, const Bins &bins, const Reads &q, uint32_t end, double scale,
+                                       uint32_t tops, double unit, double reach, Shared &s) {
+    constexpr uint32_t W = F32 ? 4 : 8;
+    s.bin_mass[threadIdx.x] = 0;
+    __syncthreads();
+    for (uint32_t j = threadIdx.x; j < q.count; j += kThreads) {
+        float v[W];
+        read_values<F32>(p, at, read_at<F32>(s, q, j), v);
+#pragma unroll
+        for (uint32_t c = 0; c < W; ++c) {
+            const uint32_t b = bin_of(bins, v[c]);
+            if (v[c] != bins.top && b <= end)
+                atomicAdd((unsigned long long *)&s.bin_mass[b], (unsigned long long)(weight_near(v[c], bins.top, scale) * unit + 0.5));
+        }
+    }
+    __syncthreads();
+    const uint64_t m = s.bin_mass[threadIdx.x] + (threadIdx.x == 0 ? (uint64_t)(tops * unit) : 0);
+    uint64_t all;
+    const uint64_t m0 = block_scan(m, s.large, all);
+    return kNone - block_max(m && (double)(m0 + m) >= reach * unit ? kNone - threadIdx.x : 0, s.other);
+}
+
 // Rows with top-p or min-p alone.  A histogram of the weights, in fp32, tells
-// the bin in which top-p ends; then the sums before that bin in 64 bits, by
-// runs of reads, beside the list of the bin's tokens, whose order gives the
-// border.  Should the histogram's rounding have missed the bin, it is the next
-// one.  False if that holds too many tokens.
+// the bin in which top-p ends, unless it ends among tokens too faint for it;
+// then the sums before that bin in 64 bits, by runs of reads, beside the list of
+// the bin's tokens, whose order gives the border.  Should the histogram's
+// rounding have missed the bin, it is the next one.  False if that holds too
+// many tokens.
 template <bool F32>
 __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row, const Bins &bins, double all, uint32_t least,
                                Groups &g, Shared &s) {
@@ -820,8 +846,12 @@ __device__ inline bool by_sums(const SampleParams &p, uint32_t r, const Row &row
         uint64_t masses;
         const uint64_t m0 = block_scan(m, s.large, masses);
         bin = kNone - block_max(m && (double)(m0 + m) >= reach * unit * 0x1p-31 ? kNone - threadIdx.x : 0, s.other);
+        // Below the reach in all bins: min_p ends all if they are below it by more than the histogram's error (half a unit a token;
+        // 80 2^-22 of a weight's logarithm; anything where differences of logits overflow), else 64 bits tell.
+        const double most = (double)masses + 0.5 * W * q.count + 0x1p-12 * all * unit * 0x1p-31;
+        if (bin >= kBins && !(bins.inv > 0 && most < reach * unit * 0x1p-31))
+            bin = bin_of_mass<F32>(p, at, bins, q, end, row.scale, all_tops, unit, reach, s);
         if (bin >= kBins) {
-            // min_p ends all, or everything counts
             if (!q.all && last < least) return false;
             bin = kBins;
         }
@@ -1007,7 +1037,7 @@ __global__ __launch_bounds__(kThreads) void k_draw(SampleParams p) {
         bins.top = top;
         bins.floor = fmaxf(fmaxf(unordered(lowest), (float)((double)top - 80.0 / row.scale)), -FLT_MAX);
         const float range = top - bins.floor;
-        bins.inv = range > 0 ? (kBins - 0.01f) / range : 0.0f;
+        bins.inv = range > 0 ? (kBins - 0.01f) / range : 0.0f;  // (0 where the range overflows: all in the first bin, NaN converts to 0)
         // the last coarse bin with tokens that min_p keeps (top-p of the first k needs the sum of the others too)
         uint32_t least = kCoarse - 1;
         if (row.min_p > 0 && !(row.k && row.top_p < 1)) {
