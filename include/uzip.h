@@ -531,7 +531,9 @@ uzip_status uzip_moe_route_backward(const uzip_moe_route_args *args, hipStream_t
  * e = experts[t, j], + residual_t.  up: a packed stack of U, gated for
  * UZIP_ACT_SWIGLU; down: one of D with as many columns as up has outputs.
  * x: [tokens, up cols] bf16; y, residual: [tokens, down rows] bf16 or fp32.
- * weights, order and offsets are uzip_moe_route's.  Up to 256 tokens, 4,096
+ * weights, order and offsets are uzip_moe_route's, or a program's own (order:
+ * each pair at most once, in any order within its expert; a token may name an
+ * expert again, and gets both).  Up to 256 tokens, 4,096
  * pairs and 16 pairs an expert on average take two kernels; there the
  * activations between the products, times their weights, are kept to 2^-17 of
  * themselves (as two bf16 values), else they are rounded to bf16.  Entries of

@@ -22,6 +22,7 @@ __device__ inline T moved(T v) {
     }
 }
 constexpr int kNeighbour = 0xB1;  // lanes 0 and 1, 2 and 3, .. change places
+constexpr int kRowBack = 0x100;   // + n: from the lane n above, within 16
 constexpr int kRowShift = 0x110, kWaveShift1 = 0x138, kRowLast = 0x142, kHalfLast = 0x143;
 template <class T>
 __device__ inline T lane_of(T v, uint32_t lane) {  // (lane uniform)

@@ -764,15 +764,28 @@ __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
         for (int j = 0; j < CT; ++j) {
             if (j && (uint32_t)j * 8 >= have) continue;
             const uint32_t slot = j * 8 + r / 2, token = slot < have ? token_of[s0 + slot] : 0xFFFF;
+            // Where the tokens ascend no two lanes add to one sum; in a program's own order, which may name an expert twice for
+            // a token, pair after pair.
+            const uint32_t after = moved<kRowBack + 2>(token);
+            const bool ascend = __all(r >= 14 || after > min(token, 0xFFFEu));
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 f32x4 s = acc[i][j];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) s[d] += moved<kNeighbour>(s[d]);
-                if (token >= p.tokens || (r & 1)) continue;
-                f32x4 *to = mine + (i * p.tokens + token) * 4 + q;
-                *to = *to + s;
+                const bool on = token < p.tokens && !(r & 1);
+                f32x4 *to = mine + (i * p.tokens + (on ? token : 0)) * 4 + q;
+                if (ascend) {
+                    if (on) *to = *to + s;
+                    continue;
+                }
+#pragma unroll 1
+                for (uint32_t c = 0; c < 16; c += 2) {
+                    if (on && r == c) *to = *to + s;
+                    asm volatile("" ::: "memory");
+                }
             }
+            asm volatile("" ::: "memory");  // (what one lane has added here another may add to next)
         }
     };
     uint4 heads[RB];

@@ -83,8 +83,10 @@ def uzip_moe(up, down, args, d_workspace, workspace_bytes, stream) -> int:
 class Routing:
     """What a router decided for [tokens] of `num_experts` experts: ``experts``
     int32 and ``weights`` fp32 [tokens, k]; ``order`` int32 [tokens * k], the
-    pairs token * k + place grouped by expert; ``offsets`` int32
-    [num_experts + 1], where each expert's begin."""
+    pairs token * k + place grouped by expert, each at most once; ``offsets``
+    int32 [num_experts + 1], where each expert's begin.  A program may make one
+    of its own tensors; where a token names an expert again ``moe`` adds both
+    (``moe_route_backward`` is for routings of ``moe_route``)."""
 
     def __init__(self, experts, weights, order, offsets, scores="softmax", renormalize=True, scale=1.0):
         if experts.dim() != 2 or not 1 <= experts.shape[1] <= MAX_CHOSEN or not 2 <= offsets.numel() <= MAX_EXPERTS + 1:
