@@ -533,11 +533,12 @@ uzip_status uzip_moe_route_backward(const uzip_moe_route_args *args, hipStream_t
  * x: [tokens, up cols] bf16; y, residual: [tokens, down rows] bf16 or fp32.
  * weights, order and offsets are uzip_moe_route's, or a program's own (order:
  * each pair at most once, in any order within its expert; a token may name an
- * expert again, and gets both).  Up to 256 tokens, 4,096
- * pairs and 16 pairs an expert on average take two kernels; there the
- * activations between the products, times their weights, are kept to 2^-17 of
- * themselves (as two bf16 values), else they are rounded to bf16.  Entries of
- * order and offsets out of range are left out.  y may be the residual itself. */
+ * expert again, and gets both).  Offsets are taken as for uzip_grouped_linear;
+ * entries of order out of range, pairs that it does not name and pairs of no
+ * group are left out.  Up to 256 tokens, 4,096 pairs and 16 pairs an expert on
+ * average take two kernels; there the activations between the products, times
+ * their weights, are kept to 2^-17 of themselves (as two bf16 values), else they
+ * are rounded to bf16.  y may be the residual itself. */
 typedef struct {
     const void *x;
     size_t x_stride;

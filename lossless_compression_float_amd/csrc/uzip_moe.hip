@@ -373,19 +373,42 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
 
 // ---- the layer around grouped products ----------------------------------------------
 
-// Rows of x in the order of their experts, zeros behind the last column, and the place of each pair.  Bound by the writes
+// Pairs [begin, end) of an expert; offsets are clamped to the pairs that exist.
+__device__ inline uint32_t clamped(int32_t v, uint32_t pairs) { return v < 0 ? 0u : min((uint32_t)v, pairs); }
+
+// Whether a group holds row s, by a thread: where the offsets ascend (a wave
+// finds out at once) the first and the last tell.
+struct Held {
+    const int32_t *offsets;
+    uint32_t num, pairs, first, last;
+    bool down;
+};
+__device__ inline Held held_rows(const int32_t *offsets, uint32_t num, uint32_t pairs) {
+    Held h{offsets, num, pairs, clamped(offsets[0], pairs), clamped(offsets[num], pairs), false};
+    for (uint32_t e = threadIdx.x & 63; e < num; e += 64) h.down |= clamped(offsets[e + 1], pairs) < clamped(offsets[e], pairs);
+    h.down = __any(h.down);
+    return h;
+}
+__device__ inline bool is_held(const Held &h, uint32_t s) {
+    if (!h.down) return s >= h.first && s < h.last;
+    bool in = false;
+#pragma unroll 1
+    for (uint32_t e = 0; e < h.num; ++e) in |= clamped(h.offsets[e], h.pairs) <= s && s < clamped(h.offsets[e + 1], h.pairs);
+    return in;
+}
+
+// Rows of x in the order of their experts, zeros behind the last column, and the place of each pair that the order names (one
+// that lies in no group has none).  Bound by the writes
 // (4096 tokens of 2048, 6 of 64 experts each: 101 MB, 31 us, where the two products take 820).
 __global__ __launch_bounds__(256) void k_gather(GatherParams p) {
     const uint32_t pairs = p.tokens * p.k, units = (uint32_t)(p.out_stride / 8);
-    const uint32_t end = (uint32_t)min(max(*p.ends, 0), (int32_t)pairs);
+    const Held held = held_rows(p.offsets, p.num, pairs);
     const uint64_t n = (uint64_t)pairs * units;
     const uint16_t *x = static_cast<const uint16_t *>(p.x.p);
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (uint64_t)gridDim.x * 256) {
         const uint32_t s = (uint32_t)(i / units), u = (uint32_t)(i % units);
         const uint32_t pair = (uint32_t)p.order[s];
         if (pair >= pairs) continue;
-        if (u == 0) p.place[pair] = s;
-        if (s >= end) continue;
         const uint16_t *row = x + (uint64_t)(pair / p.k) * p.x.stride;
         u32x4 v;
         if ((u + 1) * 8 <= p.cols) {
@@ -397,28 +420,30 @@ __global__ __launch_bounds__(256) void k_gather(GatherParams p) {
                 if (u * 8 + c < p.cols) w[c / 2] |= (uint32_t)row[u * 8 + c] << (16 * (c & 1));
             v = u32x4{w[0], w[1], w[2], w[3]};
         }
-        *reinterpret_cast<u32x4 *>(p.out + (uint64_t)s * p.out_stride + u * 8) = v;
+        if (is_held(held, s)) *reinterpret_cast<u32x4 *>(p.out + (uint64_t)s * p.out_stride + u * 8) = v;
+        if (u == 0) p.place[pair] = is_held(held, s) ? s : pairs;
     }
 }
 
-// y of a token: its experts' results by their weights, in the order of the choice, and the residual.  Bound by the reads
-// (of the above 201 MB of fp32, 36 us, 6.0 TB/s).
+// y of a token: its experts' results by their weights, in the order of the choice, and the residual.  For a pair that the
+// order does not name nothing was written: whatever stands there, the order has another pair at that place.  Bound by the
+// reads (of the above 201 MB of fp32, 36 us, 6.0 TB/s).
 __global__ __launch_bounds__(256) void k_combine(CombineParams p) {
     const uint32_t pairs = p.tokens * p.k, units = (p.cols + 7) / 8;
-    const uint32_t end = (uint32_t)min(max(*p.ends, 0), (int32_t)pairs);
     const uint64_t n = (uint64_t)p.tokens * units;
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (uint64_t)gridDim.x * 256) {
         const uint32_t t = (uint32_t)(i / units), c = (uint32_t)(i % units) * 8;
         const uint32_t count = min(8u, p.cols - c);
         float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (uint32_t j = 0; j < p.k; ++j) {
-            const uint32_t s = p.place[(uint64_t)t * p.k + j];
-            if (s >= end) continue;
-            const float w = p.weights[(uint64_t)t * p.k + j];
+            const uint32_t pair = t * p.k + j, s = p.place[pair];
+            if (s >= pairs) continue;
+            const bool its = (uint32_t)p.order[s] == pair;  // (on its way beside o)
+            const float w = p.weights[pair];
             float o[8];
             load<8>(p.o, (uint64_t)s * p.stride + c, true, count, o);
 #pragma unroll
-            for (int d = 0; d < 8; ++d) y[d] += w * o[d];
+            for (int d = 0; d < 8; ++d) y[d] += its ? w * o[d] : 0.0f;
         }
         if (p.residual) {
             float r[8];
@@ -431,9 +456,6 @@ __global__ __launch_bounds__(256) void k_combine(CombineParams p) {
 }
 
 // ---- the layer for few tokens ---------------------------------------------------------
-
-// Pairs [begin, end) of an expert; offsets are clamped to the pairs that exist.
-__device__ inline uint32_t clamped(int32_t v, uint32_t pairs) { return v < 0 ? 0u : min((uint32_t)v, pairs); }
 
 // The n-th expert that has pairs, and those; none: no pairs.
 struct Found {

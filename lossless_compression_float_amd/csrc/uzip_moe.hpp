@@ -44,16 +44,16 @@ struct GatherParams {
     Mat x;
     uint16_t *out;         // [pairs][out_stride]
     uint64_t out_stride;
-    uint32_t cols, tokens, k;
-    const int32_t *order, *ends;  // ends: one past the last pair that has an expert
-    uint32_t *place;       // of each pair in the order
+    uint32_t cols, tokens, k, num;
+    const int32_t *order, *offsets;
+    uint32_t *place;       // of each pair that the order names
 };
 
 struct CombineParams {
     const float *o;        // [pairs][stride]
     uint64_t stride;
     const uint32_t *place;
-    const int32_t *ends;
+    const int32_t *order;
     const float *weights;
     const void *residual;
     uint64_t residual_stride;

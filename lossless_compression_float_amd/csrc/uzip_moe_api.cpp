@@ -183,8 +183,9 @@ uzip_status run_many(const uzip_weight *up, const uzip_weight *down, const uzip_
     g.cols = (uint32_t)up->cols;
     g.tokens = (uint32_t)a->tokens;
     g.k = a->k;
+    g.num = (uint32_t)up->matrices;
     g.order = a->order;
-    g.ends = a->offsets + up->matrices;
+    g.offsets = a->offsets;
     g.place = plan.place;
     if (launch_gather(g, stream) != hipSuccess) return UZIP_ERR_DEVICE;
     uzip_status st = uzip_grouped_linear(up, &plan.first, plan.ws, plan.ws_bytes, stream);
@@ -195,7 +196,7 @@ uzip_status run_many(const uzip_weight *up, const uzip_weight *down, const uzip_
     p.o = plan.o;
     p.stride = plan.second.y_stride;
     p.place = plan.place;
-    p.ends = g.ends;
+    p.order = a->order;
     p.weights = a->weights;
     p.residual = a->residual;
     p.residual_stride = a->residual_stride;

@@ -43,3 +43,45 @@ def test_a_token_that_names_an_expert_twice_gets_both(tokens, num, k, act):
             for s in (r, uz.Routing(r.experts, r.weights, order, r.offsets)):
                 want, bound = layer64(x, s, up, down, act, None, bias, None, F32)
                 close(uz.moe(x, s, pu, pd, act=act, down_bias=bias, out_dtype=F32), want, bound, "y")
+
+
+def meant(r):
+    """The experts of each token as order and offsets have them: a pair that order does not name within a group has none."""
+    pairs = r.tokens * r.k
+    experts = torch.full((pairs,), -1, dtype=I32)
+    at = [min(max(v, 0), pairs) for v in r.offsets.tolist()]
+    order = r.order.tolist()
+    for e in range(r.num_experts):
+        for s in range(at[e], at[e + 1]):
+            if 0 <= order[s] < pairs:
+                experts[order[s]] = e
+    return uz.Routing(experts.view(r.tokens, r.k), r.weights.cpu(), r.order.cpu(), r.offsets.cpu())
+
+
+@pytest.mark.parametrize("tokens", [4, 40, 100, 300])
+def test_entries_out_of_range_and_rows_of_no_group_are_left_out(tokens):
+    """Both ways of the layer (the last two gather rows), over workspaces that hold other numbers."""
+    g = gen(tokens)
+    num, k, d, f = 6, 2, 72, 48
+    pairs = tokens * k
+    up, down = normal(g, num, 2 * f, d, scale=0.2), normal(g, num, d, f, scale=0.2)
+    pu, pd = uz.pack_weight(up, gated=True), uz.pack_weight(down)
+    x, r = normal(g, tokens, d), uz.moe_route(normal(g, tokens, num, dtype=F32), k)
+    bias = normal(g, num, d, dtype=F32)
+    orders, offsets = [r.order], [r.offsets]
+    for bad in (-1, -1 << 31, pairs, 1 << 30):
+        o = r.order.clone()
+        o[::3] = bad
+        orders.append(o)
+    h, q = pairs // 2, pairs // 3
+    rows = r.offsets.tolist()
+    for o in ([q] + [max(q, v) for v in rows[1:]], rows[:-1] + [rows[-2]], [-5] + rows[1:-1] + [1 << 30], [0] * (num + 1), [pairs] * (num + 1),
+              [h, pairs, 0, q, h, h, h], [h, pairs, 0, q, q, q, q], [pairs, 0, 0, q, q, h, h], [1 << 30, -7, q, h, h, h, pairs - 1]):
+        offsets.append(torch.tensor(o, dtype=I32, device=DEV))
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=DEV)
+    for order in orders:
+        for o in offsets:
+            s = uz.Routing(r.experts, r.weights, order, o)
+            want, bound = layer64(x, meant(s), up, down, "swiglu", None, bias, x.float(), F32)
+            got = uz.moe(x, s, pu, pd, down_bias=bias, residual=x.float(), out_dtype=F32, ws=ws)
+            close(got, want, bound, "y of offsets %s" % o.tolist())
