@@ -313,41 +313,53 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
     int32_t expert = lane < p.k ? p.experts[(uint64_t)t * p.k + lane] : -1;
     if (expert >= (int32_t)p.num) expert = -1;
     const bool on = expert >= 0;
-    const float g = on ? p.dweights[(uint64_t)t * p.k + lane] * p.scale : 0.0f;
+    const float g = on ? p.dweights[(uint64_t)t * p.k + lane] : 0.0f;
     float zj = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const float x = __shfl(z[i], expert & 63);
         if (on && expert / 64 == i) zj = x;
     }
+    // The share p_j times (g_j - the sum of p_i g_i).  Where p_j is nearly 1 that cancels; for the largest, the leading one, it
+    // is p_j (g_j Q - R) with Q and R the sums of p_i and p_i g_i over the others.
     float out[V], dz;  // of the experts that are not chosen, of this lane's chosen one
     if (p.sigmoid) {
         const double t = exp(fmin(-(double)zj, 700.0));
         double s = on ? 1.0 / (1.0 + t) : 0.0, rest = t * s, d = g;  // rest: 1 - s
         if (p.renorm) {
-            double all = wave_sum(s);
+            const uint32_t key = on ? ordered(zj) : 0;
+            const uint32_t lead = (uint32_t)__ffsll((unsigned long long)__ballot(key == wave_max(key))) - 1;
+            const bool leads = lane == lead;
+            double q = wave_sum(leads ? 0.0 : s), all = q + lane_of(s, lead);
             if (all < kFaint) {
                 s = faint(on, zj), rest = 1.0;
-                all = wave_sum(s);
+                q = wave_sum(leads ? 0.0 : s), all = q + lane_of(s, lead);
             }
-            d = (d - wave_sum(d * s) / all) / all;
+            const double r = wave_sum(leads ? 0.0 : d * s), dot = r + lane_of(d * s, lead), inv = 1.0 / all;
+            d = (leads ? (d * q - r) * inv : d - dot * inv) * inv;
         }
-        dz = (float)(d * s * rest);
+        dz = (float)(d * s * rest * p.scale);
 #pragma unroll
         for (int i = 0; i < V; ++i) out[i] = 0;
     } else {
         const float s = on ? exp_below(zj, top) : 0.0f;
-        float all = s;
+        // (of a routing of moe_route's there is one; of another perhaps none, and nothing to lead)
+        const uint64_t tops = __ballot(on && zj == top);
+        const uint32_t lead = tops ? (uint32_t)__ffsll((unsigned long long)tops) - 1 : 64;
+        const bool leads = lane == lead;
+        const uint32_t first = tops ? (uint32_t)lane_of(expert, lead) : 0xFFFFFFFFu;
+        const float its = tops ? 1.0f : 0.0f, g0 = tops ? lane_of(g, lead) : 0.0f;
+        float q = leads ? 0.0f : s;
         if (!p.renorm) {
-            all = 0;
+            q = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) all += z[i] > -INFINITY ? exp_below(z[i], top) : 0.0f;
+            for (int i = 0; i < V; ++i) q += z[i] > -INFINITY && i * 64 + lane != first ? exp_below(z[i], top) : 0.0f;
         }
-        all = wave_sum(all);
-        const float dot = wave_sum(g * s) / all;
-        dz = s / all * (g - dot);
+        q = wave_sum(q);
+        const float inv = 1.0f / (q + its), r = wave_sum(leads ? 0.0f : g * s), dot = (r + its * g0) * inv;
+        dz = (leads ? (g0 * q - r) * inv : s * (g - dot)) * inv * p.scale;
 #pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = p.renorm || !(z[i] > -INFINITY) ? 0.0f : -exp_below(z[i], top) / all * dot;
+        for (int i = 0; i < V; ++i) out[i] = p.renorm || !(z[i] > -INFINITY) ? 0.0f : -exp_below(z[i], top) * inv * dot * p.scale;
     }
     if (!__any(on)) {
         dz = 0;
