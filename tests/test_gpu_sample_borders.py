@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import lossless_compression_float_amd as uz
-from test_gpu_sample import check, gen, row64
+from test_gpu_sample import FILTERS, check, gen, row64
 
 pytestmark = pytest.mark.gpu
 DEV, BF, F32 = "cuda", torch.bfloat16, torch.float32
@@ -72,3 +72,75 @@ def test_top_p_over_the_whole_range_of_fp32(vocab):
         for top_p in (0.3, 0.9, 0.999):
             for u in (0.123456, 0.55555, 0.98765):
                 compared(z, torch.full((2,), u, dtype=torch.float64, device=DEV), temperature=heat, top_p=top_p)
+
+
+def kept64(z, temperature, top_k, top_p, min_p):
+    """(e where it is kept, else 0; the log-probabilities; how far top-p is from keeping one more or less, relative to the sum)
+    of one row on the CPU in 64 bits.  A product by which min_p decides is exact in the rows used here, or far from it."""
+    z = z.double().cpu()
+    top, n = z.max(), z.numel()
+    y = torch.where(z == top, torch.zeros_like(z), (z - top) / (temperature if temperature > 0 else 1.0))
+    e = torch.exp(y)
+    order = torch.sort(z, descending=True, stable=True).indices
+    es = e[order]
+    count = 1 if temperature == 0 else n if top_k <= 0 or top_k >= n else top_k
+    run, room = es[:count].cumsum(0), 1.0
+    if top_p < 1 and count > 1:
+        before = run - es[:count]
+        room = float((before / run[-1] - top_p).abs()[1:].min())
+        count = max(1, int((before < top_p * run[-1]).sum()))
+    count = max(1, int((es[:count] >= min(min_p, 1.0)).sum()))
+    kept = torch.zeros(n, dtype=torch.float64)
+    kept[order[:count]] = es[:count]
+    return kept, y - e.sum().log(), room
+
+
+def drawn(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """Every token is one that is kept, and the running sum passes u there to 1e-12 of the whole; at u = 0 it is the first."""
+    token, logprob = uz.sample(logits, u, temperature, top_k, top_p, min_p)
+    f32 = lambda v: float(torch.tensor(v, dtype=F32))
+    for i in range(logits.shape[0]):
+        kept, logp, room = kept64(logits[i], f32(temperature), top_k, f32(top_p), f32(min_p))
+        assert room > 1e-12
+        run, t = kept.cumsum(0), int(token[i])
+        total, at = float(run[-1]), float(u[i])
+        what = (i, t, at, temperature, top_k, top_p, min_p)
+        assert kept[t] > 0, what
+        assert float(run[t]) >= (at - 1e-12) * total and float(run[t] - kept[t]) <= (at + 1e-12) * total, what
+        if at == 0:
+            assert t == int((kept > 0).nonzero()[0]), what
+        assert abs(float(logprob[i]) - float(logp[t])) <= 2.0 ** -24 * abs(float(logp[t])) + 1e-12, what
+
+
+ENDS = [0.0, 2.0 ** -70, 0.37, 1 - 2.0 ** -24, 1 - 2.0 ** -53]
+
+
+def at(u, rows):
+    return torch.full((rows,), u, dtype=torch.float64, device=DEV)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("u", ENDS)
+def test_draws_at_the_ends_of_u(u, dtype):
+    g = torch.Generator().manual_seed(2)
+    for vocab in (7, 3001, 40000):
+        z = torch.randn((4, vocab), generator=g) * 3
+        z = z.scatter_add(1, torch.randint(0, vocab, (4, 4), generator=g), torch.rand((4, 4), generator=g) * 10).to(DEV, dtype)
+        z[1:, ::7] = -INF
+        z[2:, -1] = -INF
+        z[3, 0:3] = -INF
+        for f in FILTERS:
+            drawn(z, at(u, 4), **f)
+
+
+@pytest.mark.parametrize("u", ENDS)
+def test_draws_at_the_ends_of_u_among_equal_logits_and_masks(u):
+    for vocab in (5, 700, 70001):
+        z = torch.zeros((5, vocab), device=DEV)
+        z[1] = -7.5
+        z[2] = (torch.arange(vocab, device=DEV) % 3).float()
+        z[3, ::2] = -INF
+        z[4, :-1] = -INF
+        for f in (dict(), dict(top_k=3), dict(top_p=0.5003), dict(top_k=vocab // 2 + 1, top_p=0.7703), dict(temperature=0.0), dict(min_p=0.9),
+                  dict(temperature=1e30, top_p=0.3301), dict(temperature=1e30), dict(min_p=1.0, top_k=2)):
+            drawn(z, at(u, 5), **f)
