@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import lossless_compression_float_amd as uz
-from linear_testlib import close
+from linear_testlib import ACC, HALF, close, linear64
 from test_gpu_moe import gen, layer64, normal
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +85,60 @@ def test_entries_out_of_range_and_rows_of_no_group_are_left_out(tokens):
             want, bound = layer64(x, meant(s), up, down, "swiglu", None, bias, x.float(), F32)
             got = uz.moe(x, s, pu, pd, down_bias=bias, residual=x.float(), out_dtype=F32, ws=ws)
             close(got, want, bound, "y of offsets %s" % o.tolist())
+
+
+def two_value64(x, r, up, down, act, up_bias, keep):
+    """(y, its bound) of a call that takes two kernels: the weight times the activation as two bf16 values (off by 2^-17 of
+    itself: half a step of the second, which is at most half a step of the first), fp32 else.  keep: what becomes of it here."""
+    experts, weights = r.experts.cpu(), r.weights.double().cpu()
+    y = torch.zeros((x.shape[0], down.shape[1]), dtype=torch.float64)
+    err = torch.zeros_like(y)
+    for e in range(up.shape[0]):
+        t, j = torch.nonzero(experts == e, as_tuple=True)
+        if t.numel() == 0:
+            continue
+        _, _, h, eh = linear64(x[t], up[e], None if up_bias is None else up_bias[e], act, None, F32)
+        w, d = weights[t, j][:, None], down[e].double().cpu()
+        h, eh = w * h, w.abs() * (eh + (2.0 ** -17 + 2.0 ** -23) * (h.abs() + eh))
+        y.index_add_(0, t, keep(h) @ d.T)
+        err.index_add_(0, t, eh @ d.abs().T + (d.shape[1] * r.k + 24) * ACC * ((h.abs() + eh) @ d.abs().T))
+    return y, err + HALF[F32] * (y.abs() + err)
+
+
+# each shape of the two kernels' workgroups: 1, 2 and 4 row blocks, one and two columns of tiles, 4, 8 and 16 waves, splits
+FEW = [(1, 8, 2, 64, 40, 72), (1, 300, 1, 32, 16, 17), (7, 7, 1, 64, 64, 100), (16, 4, 1, 64, 48, 2000), (33, 16, 2, 40, 32, 64), (64, 8, 2, 64, 64, 130),
+       (100, 8, 1, 56, 24, 600), (128, 16, 2, 64, 32, 64), (200, 64, 2, 24, 48, 80), (256, 32, 2, 64, 40, 64), (60, 100, 2, 64, 64, 1000),
+       (64, 128, 2, 24, 112, 64), (256, 128, 3, 24, 112, 40)]
+
+
+@pytest.mark.parametrize("act", ["swiglu", "none", "gelu"])
+@pytest.mark.parametrize("tokens,num,k,d,f,out", FEW)
+def test_activations_between_the_two_kernels_keep_17_bits(tokens, num, k, d, f, out, act):
+    assert tokens <= 256 and tokens * k <= 16 * num
+    g = gen(tokens + f)
+    rows = 2 * f if act == "swiglu" else f
+    up, down = normal(g, num, rows, d, scale=0.2), normal(g, num, out, f, scale=0.2)
+    x, bias = normal(g, tokens, d), normal(g, num, rows, dtype=F32)
+    r = uz.moe_route(normal(g, tokens, num, dtype=F32), k)
+    want, bound = two_value64(x, r, up, down, act, bias, lambda h: h)
+    one, _ = two_value64(x, r, up, down, act, bias, lambda h: h.bfloat16().double())
+    assert ((one - want).abs() > 2 * bound).any()  # with one bf16 value it would show
+    got = uz.moe(x, r, uz.pack_weight(up, gated=act == "swiglu"), uz.pack_weight(down), act=act, up_bias=bias, out_dtype=F32)
+    close(got, want, bound, "y")
+
+
+def test_a_token_alone_and_in_batches_is_within_what_each_way_promises():
+    g = gen(12)
+    num, k, d, f = 16, 2, 64, 48
+    up, down = normal(g, num, 2 * f, d, scale=0.2), normal(g, num, d, f, scale=0.2)
+    pu, pd = uz.pack_weight(up, gated=True), uz.pack_weight(down)
+    x, z = normal(g, 600, d), normal(g, 600, num, dtype=F32)
+    whole = uz.moe_route(z, k)
+    want, bound = two_value64(x, whole, up, down, "swiglu", None, lambda h: h)
+    rough, wide = layer64(x, whole, up, down, "swiglu", None, None, None, F32)
+    for tokens in (1, 2, 9, 40, 128, 600):
+        r = uz.moe_route(z[:tokens], k)
+        assert torch.equal(r.experts, whole.experts[:tokens]) and torch.equal(r.weights, whole.weights[:tokens])
+        got = [uz.moe(x[:tokens], r, pu, pd, out_dtype=F32) for _ in range(2)]
+        assert torch.equal(*got)
+        close(got[0], want[:tokens] if tokens <= 128 else rough, bound[:tokens] if tokens <= 128 else wide, "y")
