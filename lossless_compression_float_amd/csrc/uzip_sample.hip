@@ -363,19 +363,20 @@ __global__ __launch_bounds__(256) void k_survey(SampleParams p) {
         p.groups[(n * 2 + h) * 64 + lane] = group[h];
     }
     float top = fmaxf(group[0], group[1]), low = INFINITY;
-    if ((seg + 1) * kSegment <= p.vocab) {
 #pragma unroll
-        for (int i = 0; i < READS; ++i)
+    for (int i = 0; i < READS; ++i)
 #pragma unroll
-            for (int c = 0; c < W; ++c) low = fminf(low, v[i][c]);
-    } else {  // (what is behind the last token does not count)
+        for (int c = 0; c < W; ++c) low = fminf(low, v[i][c]);
+    top = unordered(wave_max(ordered(top)));
+    low = unordered(~wave_max(~ordered(low)));
+    if (low == -INFINITY) {  // (masked tokens, and what is behind the last one, do not count)
+        low = INFINITY;
 #pragma unroll
         for (int i = 0; i < READS; ++i)
 #pragma unroll
             for (int c = 0; c < W; ++c) low = fminf(low, v[i][c] > -INFINITY ? v[i][c] : INFINITY);
+        low = unordered(~wave_max(~ordered(low)));
     }
-    top = unordered(wave_max(ordered(top)));
-    low = unordered(~wave_max(~ordered(low)));
     const double scale = row_of(p, r).scale;
     double sum = 0;
     if (top > -INFINITY) {

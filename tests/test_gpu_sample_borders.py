@@ -144,3 +144,24 @@ def test_draws_at_the_ends_of_u_among_equal_logits_and_masks(u):
         for f in (dict(), dict(top_k=3), dict(top_p=0.5003), dict(top_k=vocab // 2 + 1, top_p=0.7703), dict(temperature=0.0), dict(min_p=0.9),
                   dict(temperature=1e30, top_p=0.3301), dict(temperature=1e30), dict(min_p=1.0, top_k=2)):
             drawn(z, at(u, 5), **f)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_masked_tokens_are_not_a_segments_smallest(dtype):
+    """What the draw takes from the survey of 2,048 tokens, in the workspace: were -inf the smallest value of a segment, a row's
+    bins would reach down to 2^-80 of the largest, and ordinary masked rows would go the way of rows of equal logits."""
+    vocab = 2 * 2048 + 700
+    z = torch.randn((3, vocab), generator=torch.Generator().manual_seed(3)).to(DEV, dtype)
+    z[1, 5] = z[1, 3000:3100] = z[1, -2:] = -INF
+    z[2, :2048] = -INF
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    u = torch.full((3,), 0.4, device=DEV)
+    token, _ = uz.sample(z, u, top_p=0.9, ws=ws)
+    begin = -ws.data_ptr() % 256
+    room = ws[begin:begin + 3 * 3 * 16].view(torch.float32).view(3, 3, 4).cpu()  # sum (64 bits), largest, smallest
+    for r in range(3):
+        for seg in range(3):
+            part = z[r, seg * 2048:(seg + 1) * 2048].float().cpu()
+            part = part[part > -INF]
+            assert room[r, seg, 2] == (part.max() if len(part) else -INF) and room[r, seg, 3] == (part.min() if len(part) else INF)
+    check(z, u, top_p=0.9)
