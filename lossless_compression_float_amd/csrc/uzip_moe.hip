@@ -1006,8 +1006,10 @@ hipError_t launch_route_backward(const RouteBackwardParams &p, hipStream_t s) {
 // 1024, 8 pairs each, 58 and 53; 128 tokens, 16 of 4096 x 4096, 16 each, 159 and 116; but
 // 64 of 1024 x 512, 3 each, 16.5 and 19; 8 of 4096 x 14336, 4 each, 128 and 134); 8 waves
 // too where the tokens' sums fill LDS.  Splits: until there are 16 waves a CU (8
-// of the others), each with 4 blocks or more (65 row blocks of 147 blocks:
-// 18, 14 and 18 us with 1, 2 and 4 splits).
+// of the others), each with 4 blocks or more (the layer with 8, 4 and 2 blocks or
+// more: 64 row blocks of 192 blocks 25.7, 23.1 and 23.3 us, of 147 27.7, 25.1 and 24.0; 128
+// of 192 35.7, 33.3 and 33.2, of 147 33.8, 31.4 and 31.4; 64 of 64 12.5, 12.5 and 13.3; 256 row
+// blocks need none).
 MoeShape moe_shape(uint64_t tokens, uint64_t pairs, uint64_t experts, uint64_t row_blocks, uint64_t col_blocks) {
     MoeShape m;
     experts = experts < pairs ? experts : pairs;
@@ -1019,15 +1021,23 @@ MoeShape moe_shape(uint64_t tokens, uint64_t pairs, uint64_t experts, uint64_t r
     return m;
 }
 
-// The first product: with few row blocks one pair of them a workgroup and eight
-// waves (384 of them, one token: 13 us against 16.5), else two and four, so that x is read
-// once for both (2048 of them, 64 tokens: 77 and 95); with more than 16 pairs of an
-// expert in sight two columns of tiles (16 each: 58 us against 72).
+// The first product.  Two row blocks a workgroup and eight waves where such
+// workgroups about fill the chip, which holds two on each of 256 CUs; else four and
+// four, so that x is read once for more of them.  Experts without a pair are counted
+// too, and odd numbers of blocks leave a part of four idle.  The layer in us, two and
+// four, every expert with pairs: gated, one token, 384 workgroups of two 20.0 and 22.7,
+// 512 23.1 and 25.4, 768 32.7 and 30.9, 1024 39.7 and 37.2; 64 tokens, 512 31.9 and 33.1,
+// 768 40.5 and 38.3, 2048 82.7 and 77.8; plain, one token, 512 26.1 and 28.2, 640 33.4 and 32.5.
+// Sizes drawn over the whole range, some experts without: gated, 20 of 512 to 768, two
+// from 7% slower to 22% faster; plain, 24 of 384 to 640, from 3% slower to 12% faster, 12
+// of 640 to 768 from 7% slower to 10% faster.  With more than 16 pairs of an expert in
+// sight two columns of tiles (16 each: 58 us against 72).
 template <bool GATED>
 hipError_t moe_up_any(const MoeParams &p, hipStream_t s) {
     const uint64_t pairs = (uint64_t)p.tokens * p.k, experts = p.num < pairs ? p.num : pairs;
     const bool wide = p.tokens > 16 && pairs > 4 * experts;
-    if (p.up.part_blocks * experts <= 768) return wide ? moe_up<2, 2, GATED, 8>(p, s) : moe_up<1, 2, GATED, 8>(p, s);
+    if (GATED ? p.up.part_blocks * experts <= 768 : (p.up.part_blocks + 1) / 2 * experts <= 640)
+        return wide ? moe_up<2, 2, GATED, 8>(p, s) : moe_up<1, 2, GATED, 8>(p, s);
     return wide ? moe_up<2, 4, GATED, 4>(p, s) : moe_up<1, 4, GATED, 4>(p, s);
 }
 

@@ -108,7 +108,7 @@ def two_value64(x, r, up, down, act, up_bias, keep):
 # each shape of the two kernels' workgroups: 1, 2 and 4 row blocks, one and two columns of tiles, 4, 8 and 16 waves, splits
 FEW = [(1, 8, 2, 64, 40, 72), (1, 300, 1, 32, 16, 17), (7, 7, 1, 64, 64, 100), (16, 4, 1, 64, 48, 2000), (33, 16, 2, 40, 32, 64), (64, 8, 2, 64, 64, 130),
        (100, 8, 1, 56, 24, 600), (128, 16, 2, 64, 32, 64), (200, 64, 2, 24, 48, 80), (256, 32, 2, 64, 40, 64), (60, 100, 2, 64, 64, 1000),
-       (64, 128, 2, 24, 112, 64), (256, 128, 3, 24, 112, 40)]
+       (64, 128, 2, 24, 112, 64), (256, 128, 3, 24, 112, 40), (64, 128, 2, 24, 200, 64), (256, 128, 3, 24, 200, 40)]
 
 
 @pytest.mark.parametrize("act", ["swiglu", "none", "gelu"])
