@@ -230,7 +230,8 @@ __device__ inline void place(const RouteParams &p, uint32_t p0, uint32_t p1, uin
 // same places whatever the order of the workgroups.  Bound by latency where
 // tokens are few (4 of 128 experts, 8 each: 5 us, a launch 2.5 of them; 777 of
 // 60, 4 each: 4.5 and 4.5), by the steps of a search where they are many (16384
-// of 64, 6 each, biased: 14 and 7 us, half of the issue slots; 4.2 MB of logits).
+// of 64, 6 each, biased: 14 and 7 us, a third of the issue slots; 4.2 MB of logits).
+// More than 256 experts take all 128 registers of a lane and 14 to 16 more in scratch.
 template <int V, bool CHOOSE, bool PLACE, uint32_t NT>
 __global__ __launch_bounds__(NT) void k_route(RouteParams p) {
     __shared__ uint32_t count[kMaxExperts + 1], base[kMaxExperts + 1], waves[NT / 64];
@@ -292,8 +293,9 @@ __global__ __launch_bounds__(NT) void k_route(RouteParams p) {
 }
 
 // The gradient of the logits, a wave a token: dp of the chosen experts, then
-// through the scores.  The choice itself has none.  Bound by latency, a token's
-// reads and then its sums over a wave (16384 tokens of 64, 6 each: 10 us, 8.4 MB).
+// through the scores.  The choice itself has none.  Half of the issue slots are
+// busy: all lanes take the exponentials and divisions of at most k experts, for
+// sigmoid scores in 64 bits (16384 tokens of 64, 6 each: 10 us, softmax 8; 8.4 MB).
 template <int V>
 __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardParams p) {
     const uint32_t lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -411,7 +413,7 @@ __device__ inline bool is_held(const Held &h, uint32_t s) {
 
 // Rows of x in the order of their experts, zeros behind the last column, and the place of each pair that the order names (one
 // that lies in no group has none).  Bound by the writes
-// (4096 tokens of 2048, 6 of 64 experts each: 101 MB, 31 us, where the two products take 820).
+// (4096 tokens of 2048, 6 of 64 experts each: 101 MB, 31 us, where the two products take 740).
 __global__ __launch_bounds__(256) void k_gather(GatherParams p) {
     const uint32_t pairs = p.tokens * p.k, units = (uint32_t)(p.out_stride / 8);
     const Held held = held_rows(p.offsets, p.num, pairs);
@@ -580,7 +582,8 @@ __device__ inline void stream_tiles(const WeightView &w, const TileRows<RB> &t, 
 // (gated: RB / 2, each with its up rows), NW waves that split its columns, 16 CT
 // pairs at a time, whose rows of x are read where they are.  Bound by the reads
 // of U (8 experts of 28672 x 4096, 16 tokens: 234 us, 6.1 TB/s of packed bytes, part of
-// them from the last-level cache; 64 of 2048 x 2048: 75 us, 5.5), for a token by latency
+// them from the last-level cache; 64 of 2048 x 2048: 75 us, 5.5), for a token by the
+// chain from offsets to pairs to a wave's four blocks, one on its way at a time
 // (8 of 1536 x 2048: 12.5 us, 3.1 TB/s).  ANY: rows of x that are not 16 bytes
 // apart, or too far for 32 bits, by 64-bit addresses (13 tokens, 7 experts of 1333 x
 // 1027: 12.3 us, where a copy of x before took 4.1 and the kernel 9.8).
@@ -703,7 +706,8 @@ __global__ __launch_bounds__(NW * 64) void k_moe_up(MoeParams p) {
 // added in a fixed order, and the splits' by the workgroup that comes last.
 // Bound by the reads of D where experts are large (8 of 4096 x 14336, 16 tokens:
 // 128 us, 5.6 TB/s of packed bytes), by the turns of the waves where they are small (64 of
-// 2048 x 1024, 64 tokens: 53 us, 3.9 TB/s).
+// 2048 x 1024, 64 tokens: 53 us, 3.9 TB/s), for a token by a chain as above on half of the
+// CUs (8 of 2048 x 768: 128 workgroups, 10.5 us).
 constexpr uint32_t kMaxVisits = kMaxExperts + kFewPairs / 8;
 template <int CT, int RB, int NW, int DEPTH>
 __global__ __launch_bounds__(NW * 64) void k_moe_down(MoeParams p) {
@@ -1028,7 +1032,7 @@ MoeShape moe_shape(uint64_t tokens, uint64_t pairs, uint64_t experts, uint64_t r
 // four, every expert with pairs: gated, one token, 384 workgroups of two 20.0 and 22.7,
 // 512 23.1 and 25.4, 768 32.7 and 30.9, 1024 39.7 and 37.2; 64 tokens, 512 31.9 and 33.1,
 // 768 40.5 and 38.3, 2048 82.7 and 77.8; plain, one token, 512 26.1 and 28.2, 640 33.4 and 32.5.
-// Sizes drawn over the whole range, some experts without: gated, 20 of 512 to 768, two
+// Sizes drawn over the whole range, some experts without: gated, 18 of 512 to 768, two
 // from 7% slower to 22% faster; plain, 24 of 384 to 640, from 3% slower to 12% faster, 12
 // of 640 to 768 from 7% slower to 10% faster.  With more than 16 pairs of an expert in
 // sight two columns of tiles (16 each: 58 us against 72).

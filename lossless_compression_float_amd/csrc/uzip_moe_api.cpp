@@ -131,6 +131,10 @@ MoeParams plan_few(const uzip_weight *up, const uzip_weight *down, const uzip_mo
 }
 
 // Many: rows gathered by expert, the two grouped products, the results joined.
+// The activations between them are rounded to bf16 once: as two values they would
+// double the second product, which is a third of the work, and their memory.  The
+// layer's error is then 0.0023 of the whole with a bf16 result (two values 0.0017,
+// the result's own rounding), 0.0017 with an fp32 one (2e-6).
 struct ManyPlan {
     uint16_t *x, *h;
     float *o;

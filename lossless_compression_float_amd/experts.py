@@ -270,8 +270,8 @@ def moe(x, routing: Routing, up: PackedWeight, down: PackedWeight, act: str = "s
 
     Up to 256 tokens (4,096 pairs, 16 an expert on average) take two kernels
     and keep the activations between the products to 2^-17 of themselves; more
-    go through gathered rows and ``grouped_linear``, with activations in
-    bf16."""
+    go through gathered rows and ``grouped_linear``, with activations in bf16
+    (a result off by 0.0023 of the whole instead of 0.0017, its own rounding)."""
     r = _routing(routing, "moe")
     _weight(up, "moe", 3)
     _weight(down, "moe", 3)

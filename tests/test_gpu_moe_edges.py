@@ -142,3 +142,33 @@ def test_a_token_alone_and_in_batches_is_within_what_each_way_promises():
         got = [uz.moe(x[:tokens], r, pu, pd, out_dtype=F32) for _ in range(2)]
         assert torch.equal(*got)
         close(got[0], want[:tokens] if tokens <= 128 else rough, bound[:tokens] if tokens <= 128 else wide, "y")
+
+
+def test_the_weights_gradients_of_a_training_step():
+    """From grouped_linear's rows to the router's logits, as a program that trains the layer takes them, against autograd in 64
+    bits over the same rows."""
+    g = gen(13)
+    tokens, num, k, d, f = 50, 6, 2, 72, 40
+    up, down = uz.pack_weight(normal(g, num, 2 * f, d, scale=0.2), gated=True), uz.pack_weight(normal(g, num, d, f, scale=0.2))
+    x, scores, dy = normal(g, tokens, d), normal(g, tokens, num, dtype=F32), normal(g, tokens, d, dtype=F32)
+    scores[3] = -float("inf")
+    scores[4, 1:] = -float("inf")
+    r = uz.moe_route(scores, k)
+    h = uz.grouped_linear(x[r.order // k], r.offsets, up, act="swiglu")
+    o = uz.grouped_linear(h, r.offsets, down, out_dtype=F32)
+    dweights = torch.empty_like(r.weights)
+    dweights.view(-1)[r.order] = (dy[r.order // k] * o).sum(-1)
+    got = uz.moe_route_backward(dweights, scores, r)
+    z = scores.double().cpu().requires_grad_(True)
+    chosen = r.experts.cpu().long()
+    p = torch.where(chosen >= 0, torch.exp(z.gather(1, chosen.clamp(min=0))), 0.0)
+    s = p.sum(1, keepdim=True)
+    w = torch.where(s > 0, p / torch.where(s > 0, s, 1.0), 0.0)
+    rows = torch.empty((tokens * k, d), dtype=torch.float64)
+    rows[r.order.cpu().long()] = o.double().cpu()
+    rows = rows.view(tokens, k, d)
+    y = (w[:, :, None] * rows).sum(1)
+    want, = torch.autograd.grad(y, z, dy.double().cpu())
+    # dweights: a sum of d products in fp32; its gradient then by at most the share times that, twice, and the share's own error
+    size = (dy.double().cpu().abs()[:, None, :] * rows.abs()).sum(2).max(1, keepdim=True).values
+    close(got, want, 4 * (d + 8 + 40 + num + 16) * ACC * size * torch.ones_like(want), "dlogits")
