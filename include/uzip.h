@@ -579,8 +579,8 @@ uzip_status uzip_moe(const uzip_weight *up, const uzip_weight *down, const uzip_
  * Infinite logits give the limit.  Each parameter is a device array of one
  * value a row, or, where that is null, the value beside it.  e and its sums are
  * taken in 64 bits: a draw or a border of top-p within about 1e-12 of the sum from a
- * token's edge may fall on either side of it (behind a filter tokens of e below
- * 2^-80 are never drawn).  Limits: 2^21 rows, 2^22 tokens, 2^24 runs of 2,048
+ * token's edge may fall on either side of it, and e within 1e-12 of min_p (behind a
+ * filter tokens of e below 2^-80 are never drawn).  Limits: 2^21 rows, 2^22 tokens, 2^24 runs of 2,048
  * tokens a call. */
 typedef struct {
     const void *logits;
